@@ -508,7 +508,7 @@ struct LocateSmem {
 // which case the last positive mass is taken.  Returns k (-1 if R <= 0), its
 // exclusive prefix in *base_out and t in *t_out; every thread gets them.
 // Float32 pipes only (two-float sums): this part's float64 rate is low.
-__device__ int block_locate(const F2* masses, int NT, float u, F2* R_out, F2* base_out, F2* t_out,
+static __device__ int block_locate(const F2* masses, int NT, float u, F2* R_out, F2* base_out, F2* t_out,
                             LocateSmem& ls, bool from_global) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int nw = blockDim.x >> 5, nt = blockDim.x;
@@ -573,7 +573,7 @@ __device__ int block_locate(const F2* masses, int NT, float u, F2* R_out, F2* ba
 // The same search done by warp 0 alone (no block barriers during the scan;
 // one __syncthreads publishes the result).  Same summation order for the
 // total and the prefixes: 32-wide chunks, two-float inclusive scans, carry.
-__device__ int warp_locate(const F2* masses, int NT, float u, F2* R_out, F2* base_out, F2* t_out,
+static __device__ int warp_locate(const F2* masses, int NT, float u, F2* R_out, F2* base_out, F2* t_out,
                            LocateSmem& ls, bool from_global) {
   const int tid = threadIdx.x;
   if (tid < 32) {
@@ -850,7 +850,7 @@ __device__ __forceinline__ int count_greater(const unsigned long long* X, int n,
 // Top-k row finisher: merge the S per-slice lists of row rr into the row's
 // top-k, apply softmax(./T) over it, cut by top-p, renormalise, store the kept
 // (index, probability) list and the acceptance probability of the row's draft.
-__device__ void finish_row_topk(const Params& p, int b, int i, int rr, RowsSmem& sm) {
+static __device__ void finish_row_topk(const Params& p, int b, int i, int rr, RowsSmem& sm) {
   const int tid = threadIdx.x;
   const int k = p.top_k, G = p.gamma, V = p.V;
   const int gb = seq_gamma(p, b);
@@ -962,7 +962,7 @@ __device__ void finish_row_topk(const Params& p, int b, int i, int rr, RowsSmem&
 
 // Top-k sequence finisher: scan, then the final draw from the kept list of
 // row n (residual against q gathered at the kept indices) or row gamma.
-__device__ void finish_sequence_topk(const Params& p, int b, RowsSmem& sm) {
+static __device__ void finish_sequence_topk(const Params& p, int b, RowsSmem& sm) {
   const int tid = threadIdx.x;
   const int k = p.top_k, G = p.gamma, G1 = G + 1, V = p.V;
   const int gb = seq_gamma(p, b);

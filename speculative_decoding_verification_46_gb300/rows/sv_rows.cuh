@@ -1,0 +1,185 @@
+// Shared device code of the operators on logits rows (include/specverify_rows.h).
+//
+// A row of V elements at element offset r * V of a 16-byte aligned tensor
+// starts at any element of a 16-byte vector when V is not a multiple of the
+// vector width VW.  Every kernel here therefore walks a row through its
+// window of aligned vectors: vector v of the window holds the row's elements
+// v * VW - a0 .. v * VW - a0 + VW - 1, a0 = (r * V) % VW.  Whole vectors move
+// as one 16-byte access; the first and the last, where they reach outside the
+// row, element by element, so nothing outside the row is read or written.
+#pragma once
+
+#include "../csrc/sv_device.cuh"
+
+namespace sv {
+namespace rows {
+
+// Bits of an element type's own lowest value: -inf.
+template <typename T> struct Elem;
+template <> struct Elem<float> {
+  __device__ static __forceinline__ float load(const float* p) { return *p; }
+  __device__ static __forceinline__ void store(float* p, float x) { *p = x; }
+  __device__ static __forceinline__ uint32_t raw(const float* p) { return *reinterpret_cast<const uint32_t*>(p); }
+  __device__ static __forceinline__ void store_raw(float* p, uint32_t x) { *reinterpret_cast<uint32_t*>(p) = x; }
+  static constexpr uint32_t kNegInf = 0xff800000u;
+  // VW rounded values packed into a vector
+  __device__ static __forceinline__ uint4 pack(const float* x) {
+    return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+  }
+};
+template <> struct Elem<__nv_bfloat16> {
+  __device__ static __forceinline__ float load(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+  __device__ static __forceinline__ void store(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+  __device__ static __forceinline__ uint32_t raw(const __nv_bfloat16* p) {
+    return *reinterpret_cast<const unsigned short*>(p);
+  }
+  __device__ static __forceinline__ void store_raw(__nv_bfloat16* p, uint32_t x) {
+    *reinterpret_cast<unsigned short*>(p) = (unsigned short)x;
+  }
+  static constexpr uint32_t kNegInf = 0xff80u;
+  __device__ static __forceinline__ uint4 pack(const float* x) {
+    uint4 v;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * w], x[2 * w + 1]);
+      set_word(v, w, *reinterpret_cast<const uint32_t*>(&h));
+    }
+    return v;
+  }
+};
+template <> struct Elem<__half> {
+  __device__ static __forceinline__ float load(const __half* p) { return __half2float(*p); }
+  __device__ static __forceinline__ void store(__half* p, float x) { *p = __float2half_rn(x); }
+  __device__ static __forceinline__ uint32_t raw(const __half* p) { return *reinterpret_cast<const unsigned short*>(p); }
+  __device__ static __forceinline__ void store_raw(__half* p, uint32_t x) {
+    *reinterpret_cast<unsigned short*>(p) = (unsigned short)x;
+  }
+  static constexpr uint32_t kNegInf = 0xfc00u;
+  __device__ static __forceinline__ uint4 pack(const float* x) {
+    uint4 v;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const __half2 h = __floats2half2_rn(x[2 * w], x[2 * w + 1]);
+      set_word(v, w, *reinterpret_cast<const uint32_t*>(&h));
+    }
+    return v;
+  }
+};
+
+// Element t (a compile-time index after unrolling) of a vector in float32.
+template <typename T>
+__device__ __forceinline__ uint32_t raw_of(const uint4& v, int t) {
+  if (sizeof(T) == 4) return word_of(v, t);
+  const uint32_t w = word_of(v, t >> 1);
+  return (t & 1) ? (w >> 16) : (w & 0xffffu);
+}
+
+// A row's window of aligned vectors (P: T or const T).
+template <typename T, typename P = T>
+struct Window {
+  P* base;   // first element of the window's first vector (16-byte aligned)
+  int a0;    // elements of the window before the row
+  int V;     // elements of the row
+  __device__ __forceinline__ Window(P* tensor, size_t r, int V_) : V(V_) {
+    const size_t e0 = r * (size_t)V_;
+    a0 = (int)(e0 % Tr<T>::VW);
+    base = tensor + (e0 - a0);
+  }
+  __device__ __forceinline__ int vectors() const { return (int)(((long long)a0 + V + Tr<T>::VW - 1) / Tr<T>::VW); }
+  // whether vector v lies inside the row
+  __device__ __forceinline__ bool whole(int v) const {
+    const int t = v * Tr<T>::VW - a0;
+    return t >= 0 && t + Tr<T>::VW <= V;
+  }
+  // vector v (0 <= v < vectors()); elements outside the row read as -inf.
+  // Read once: the line is first in line to leave the caches.
+  __device__ __forceinline__ uint4 load(int v) const {
+    const T* p = base + (size_t)v * Tr<T>::VW;
+    if (whole(v)) return __ldcs(reinterpret_cast<const uint4*>(p));
+    uint4 x = make_uint4(Tr<T>::kPadWord, Tr<T>::kPadWord, Tr<T>::kPadWord, Tr<T>::kPadWord);
+#pragma unroll
+    for (int t = 0; t < Tr<T>::VW; ++t) {
+      const int e = v * Tr<T>::VW - a0 + t;
+      if (e >= 0 && e < V) Tr<T>::put(x, t, Elem<T>::raw(p + t));
+    }
+    return x;
+  }
+  __device__ __forceinline__ void store(int v, const uint4& x) const {
+    T* p = base + (size_t)v * Tr<T>::VW;
+    if (whole(v)) {
+      __stcs(reinterpret_cast<uint4*>(p), x);
+      return;
+    }
+#pragma unroll
+    for (int t = 0; t < Tr<T>::VW; ++t) {
+      const int e = v * Tr<T>::VW - a0 + t;
+      if (e >= 0 && e < V) Elem<T>::store_raw(p + t, raw_of<T>(x, t));
+    }
+  }
+};
+
+// ------------------------------------------------------------ block reductions
+
+template <int NW>
+__device__ __forceinline__ float block_max_n(float v, float* sm) {
+#pragma unroll
+  for (int m = 16; m >= 1; m >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, m));
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = v;
+  __syncthreads();
+  float t = sm[0];
+#pragma unroll
+  for (int w = 1; w < NW; ++w) t = fmaxf(t, sm[w]);
+  return t;
+}
+
+__device__ __forceinline__ F2 warp_sum_f2(F2 v) {
+#pragma unroll
+  for (int m = 16; m >= 1; m >>= 1) v = f2_add(v, f2_shfl_xor(v, m));
+  return v;
+}
+
+template <int NW>
+__device__ __forceinline__ F2 block_sum_f2_n(F2 v, F2* sm) {
+  v = warp_sum_f2(v);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = v;
+  __syncthreads();
+  F2 t = sm[0];
+#pragma unroll
+  for (int w = 1; w < NW; ++w) t = f2_add(t, sm[w]);
+  return t;
+}
+
+template <int NW>
+__device__ __forceinline__ int block_sum_int_w(int v, int* sm) {
+#pragma unroll
+  for (int m = 16; m >= 1; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = v;
+  __syncthreads();
+  int t = sm[0];
+#pragma unroll
+  for (int w = 1; w < NW; ++w) t += sm[w];
+  return t;
+}
+
+// 2^((x - m) c) to about 44 bits, c = c.hi + c.lo; x <= m, either may be
+// -inf (0 then).  The difference keeps its rounding error.
+__device__ __forceinline__ F2 weight_f2(float x, float m, F2 c, const float* tab) {
+  if (x == -INFINITY) return F2{0.f, 0.f};
+  const float d = x - m;
+  const float bb = d - x;
+  const float de = (x - (d - bb)) + (-m - bb);
+  const F2 y = exp2_f2(f2_mul(F2{d, de}, c), tab);
+  return f2_norm(y.hi, y.lo);   // so that .hi alone is the rounded weight
+}
+
+__device__ __forceinline__ double f2_double(F2 a) { return (double)a.hi + (double)a.lo; }
+__device__ __forceinline__ F2 f2_from(double d) {
+  const float h = (float)d;
+  return F2{h, (float)(d - (double)h)};
+}
+
+}  // namespace rows
+}  // namespace sv

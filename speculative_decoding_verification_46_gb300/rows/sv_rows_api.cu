@@ -1,0 +1,354 @@
+// Host side of the operators on logits rows: argument validation and launches
+// for the C ABI declared in include/specverify_rows.h.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstddef>
+#include <cstdint>
+
+#include "specverify_rows.h"
+#include "sv_adjust.cuh"
+#include "sv_distill.cuh"
+#include "sv_toplogits.cuh"
+
+namespace {
+
+constexpr size_t kAlign = 256;
+size_t up(size_t x) { return (x + kAlign - 1) & ~(kAlign - 1); }
+long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool dtype_ok(sv_dtype dt) { return dt == SV_DTYPE_F32 || dt == SV_DTYPE_BF16 || dt == SV_DTYPE_F16; }
+int vec_width(sv_dtype dt) { return dt == SV_DTYPE_F32 ? 4 : 8; }
+size_t elem_size(sv_dtype dt) { return dt == SV_DTYPE_F32 ? 4 : 2; }
+bool rows_ok(long long R, int V) { return R >= 0 && R <= SV_MAX_ROWS && V >= 1 && V <= SV_MAX_VOCAB; }
+bool temperature_ok(float t) { return t > 0.f && std::isfinite(t) && std::isfinite((float)(1.4426950408889634 / (double)t)); }
+
+// a is b, or the n bytes at a and at b have nothing in common
+bool same_or_apart(const void* a, const void* b, size_t n) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x == y || x + n <= y || y + n <= x;
+}
+
+int sm_count() {
+  static int cached[64] = {0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 152;
+  if (dev >= 0 && dev < 64 && cached[dev] > 0) return cached[dev];
+  int n = 0;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 152;
+  if (dev >= 0 && dev < 64) cached[dev] = n;
+  return n;
+}
+
+sv_status launched() {
+  return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+}
+
+// log2(e) / temperature as a float pair
+void exponent_scale(float temperature, float* hi, float* lo) {
+  const double c = 1.4426950408889634 / (double)temperature;
+  *hi = (float)c;
+  *lo = (float)(c - (double)*hi);
+}
+
+// ---------------------------------------------------------------- adjust
+
+template <typename T>
+sv_status launch_adjust(const sv::rows::AdjustParams& p, cudaStream_t stream) {
+  auto kern = sv::rows::adjust_kernel<T>;
+  const bool sparse = p.count || p.NB;
+  const size_t smem = sparse ? (size_t)p.tile * 6 + (size_t)p.NB * 8 : 0;
+  // (the kernel's static shared memory counts toward the 48 KB that need no opt-in)
+  if (smem > 32 * 1024 &&
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
+    cudaGetLastError();
+    return SV_ERR_CUDA;
+  }
+  const long long grid = (long long)p.B * p.tiles;
+  kern<<<(unsigned)grid, sv::rows::kAdThreads, smem, stream>>>(p);
+  return launched();
+}
+
+// Tokens per tile: 8192 where that still gives every SM four CTAs, fewer for
+// small calls, down to 256; the tiles of a row are then made equal.
+void choose_tile(sv::rows::AdjustParams& p) {
+  const long long want = 4ll * sm_count();
+  long long tile = ceil_div((long long)p.B * p.V, want);
+  tile = std::min<long long>(std::max<long long>(tile, 256), sv::rows::kAdMaxTile);
+  p.tiles = (int)ceil_div(p.V, tile);
+  p.tile = (int)(ceil_div(ceil_div(p.V, p.tiles), 64) * 64);
+  p.tiles = (int)ceil_div(p.V, p.tile);
+}
+
+// ---------------------------------------------------------------- top logits
+
+struct TopLayout {
+  size_t ticket, part, lists, total;
+  int H, SV;
+};
+
+// Slices of at most 2048 vectors of 8 elements; more, smaller ones where the
+// rows alone would leave SMs without work, as long as a slice holds 8 k
+// elements (its candidates are then a small part of it).
+TopLayout top_layout(long long R, int V, int k, int VW, int sms) {
+  TopLayout L{};
+  const long long nv = ceil_div((long long)V + (V % VW ? VW - 1 : 0), VW);
+  long long H = ceil_div(nv, sv::rows::kTlThreads * 8);
+  const long long most = std::max<long long>(H, nv / std::max(sv::rows::kTlThreads, 8 * k / VW));
+  if (R > 0) H = std::max(H, std::min(most, (2ll * sms) / R));
+  L.SV = (int)ceil_div(nv, H);
+  L.H = (int)ceil_div(nv, L.SV);
+  size_t o = 0;
+  L.ticket = o; o += up(sizeof(int) * (size_t)R);
+  L.part = o;   o += up(sizeof(float4) * (size_t)R * L.H);
+  L.lists = o;  o += up(sizeof(unsigned long long) * (size_t)R * L.H * k);
+  L.total = o;
+  return L;
+}
+
+template <typename T, int U>
+sv_status launch_top_u(const sv::rows::TopParams& p, cudaStream_t stream) {
+  sv::rows::top_slice_kernel<T, U><<<(unsigned)((long long)p.R * p.H), sv::rows::kTlThreads, 0, stream>>>(p);
+  return launched();
+}
+template <typename T>
+sv_status launch_top(const sv::rows::TopParams& p, cudaStream_t stream) {
+  const int u = (int)ceil_div(p.SV, sv::rows::kTlThreads);
+  if (u <= 1) return launch_top_u<T, 1>(p, stream);
+  if (u <= 2) return launch_top_u<T, 2>(p, stream);
+  if (u <= 4) return launch_top_u<T, 4>(p, stream);
+  return launch_top_u<T, 8>(p, stream);
+}
+
+// ---------------------------------------------------------------- distill
+
+template <typename T, int U, bool GRAD>
+sv_status launch_distill_u(sv::rows::DistillParams p, cudaStream_t stream) {
+  p.NCK = (int)ceil_div(p.SV, sv::rows::kDiThreads * U);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((long long)p.R * p.C));
+  cfg.blockDim = dim3(sv::rows::kDiThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)p.C;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, sv::rows::distill_kernel<T, U, GRAD>, p) != cudaSuccess) {
+    cudaGetLastError();
+    return SV_ERR_CUDA;
+  }
+  return launched();
+}
+
+// CTAs per row: as few as hold the row in registers (8 vectors per thread),
+// more where the rows alone would leave SMs without work, at most 8.
+template <typename T, bool GRAD>
+sv_status launch_distill(sv::rows::DistillParams p, cudaStream_t stream) {
+  constexpr int VW = sv::Tr<T>::VW;
+  const long long nv = ceil_div((long long)p.V + (p.V % VW ? VW - 1 : 0), VW);
+  int C = (int)std::min<long long>(sv::rows::kDiMaxC, ceil_div(nv, sv::rows::kDiThreads * 8));
+  while (C < sv::rows::kDiMaxC && (long long)p.R * C < sm_count() && ceil_div(nv, C) > sv::rows::kDiThreads) ++C;
+  p.C = C;
+  p.SV = (int)ceil_div(nv, C);
+  const int u = (int)ceil_div(p.SV, sv::rows::kDiThreads);
+  if (u <= 1) return launch_distill_u<T, 1, GRAD>(p, stream);
+  if (u <= 2) return launch_distill_u<T, 2, GRAD>(p, stream);
+  if (u <= 4) return launch_distill_u<T, 4, GRAD>(p, stream);
+  return launch_distill_u<T, 8, GRAD>(p, stream);
+}
+
+template <typename T>
+sv_status launch_distill_backward(sv::rows::DistillParams p, cudaStream_t stream) {
+  constexpr int VW = sv::Tr<T>::VW;
+  const long long nv = ceil_div((long long)p.V + (p.V % VW ? VW - 1 : 0), VW);
+  p.C = (int)ceil_div(nv, sv::rows::kDiBwThreads * sv::rows::kDiBwU);
+  p.SV = sv::rows::kDiBwThreads * sv::rows::kDiBwU;
+  const long long grid = (long long)p.R * p.C;
+  if (grid > 0x7fffffffll) return SV_ERR_UNSUPPORTED;
+  sv::rows::distill_backward_kernel<T><<<(unsigned)grid, sv::rows::kDiBwThreads, 0, stream>>>(p);
+  return launched();
+}
+
+// What the three distillation calls check alike.
+sv_status check_distill(int R, int V, const void* student, sv_dtype dtype, const int32_t* indices,
+                        const float* logprobs, int k, float temperature) {
+  if (!rows_ok(R, V) || !dtype_ok(dtype) || k < 1 || k > SV_MAX_TOP_K || !temperature_ok(temperature))
+    return SV_ERR_INVALID_ARG;
+  if (R == 0) return SV_OK;
+  if (!student || !indices || !logprobs || !aligned16(student)) return SV_ERR_INVALID_ARG;
+  return SV_OK;
+}
+
+sv::rows::DistillParams distill_params(int R, int V, const void* student, const int32_t* indices,
+                                       const float* logprobs, const float* tail, int k, float temperature,
+                                       const float* weight) {
+  sv::rows::DistillParams p{};
+  p.R = R;
+  p.V = V;
+  p.k = k;
+  exponent_scale(temperature, &p.c, &p.c_lo);
+  p.inv_t = 1.0 / (double)temperature;
+  p.student = student;
+  p.indices = indices;
+  p.logprobs = logprobs;
+  p.tail = tail;
+  p.weight = weight;
+  return p;
+}
+
+}  // namespace
+
+extern "C" sv_status sv_adjust_logits(int B, int gamma, int V, const void* logits, sv_dtype dtype, void* out,
+                                      const int32_t* draft_tokens, const int32_t* gamma_b, const int32_t* history,
+                                      int H, const int32_t* history_len, const int32_t* prompt_len,
+                                      const float* repetition, const float* frequency, const float* presence,
+                                      const int32_t* bias_tokens, const float* bias_values, int NB,
+                                      const uint32_t* mask, int M, const int32_t* mask_index, sv_stream_t stream) {
+  if (B < 0 || gamma < 0 || gamma > SV_MAX_GAMMA || !rows_ok((long long)B * (gamma + 1), V) || !dtype_ok(dtype) ||
+      H < 0 || H > SV_MAX_HISTORY || NB < 0 || NB > SV_MAX_BIAS || M < 0 || M > SV_MAX_MASKS)
+    return SV_ERR_INVALID_ARG;
+  if (B == 0) return SV_OK;
+  const size_t bytes = (size_t)B * (gamma + 1) * (size_t)V * elem_size(dtype);
+  if (!logits || !out || !aligned16(logits) || !aligned16(out) || !same_or_apart(logits, out, bytes))
+    return SV_ERR_INVALID_ARG;
+  if (history && H > 0 && !history_len) return SV_ERR_INVALID_ARG;
+  if (NB > 0 && (!bias_tokens || !bias_values)) return SV_ERR_INVALID_ARG;
+  if (mask && !mask_index && (long long)M != (long long)B * (gamma + 1)) return SV_ERR_INVALID_ARG;
+  sv::rows::AdjustParams p{};
+  p.B = B;
+  p.G1 = gamma + 1;
+  p.V = V;
+  p.logits = logits;
+  p.out = out;
+  p.copy = out != logits;
+  p.draft = gamma > 0 ? draft_tokens : nullptr;
+  p.gamma_b = gamma_b;
+  p.history = H > 0 ? history : nullptr;
+  p.H = H;
+  p.history_len = history_len;
+  p.prompt_len = prompt_len;
+  p.repetition = repetition;
+  p.frequency = frequency;
+  p.presence = presence;
+  p.count = (repetition || frequency || presence) && (p.history || p.draft);
+  p.bias_tokens = bias_tokens;
+  p.bias_values = bias_values;
+  p.NB = NB;
+  p.mask = mask;
+  p.M = M;
+  p.W = (V + 31) / 32;
+  p.mask_index = mask_index;
+  if (!p.copy && !p.count && !p.NB && !p.mask) return SV_OK;   // nothing to do in place
+  choose_tile(p);
+  if ((long long)p.B * p.tiles > 0x7fffffffll) return SV_ERR_UNSUPPORTED;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  switch (dtype) {
+    case SV_DTYPE_F32: return launch_adjust<float>(p, s);
+    case SV_DTYPE_BF16: return launch_adjust<__nv_bfloat16>(p, s);
+    default: return launch_adjust<__half>(p, s);
+  }
+}
+
+extern "C" size_t sv_top_logits_workspace_bytes(int R, int V, int k) {
+  if (!rows_ok(R, V) || k < 1 || k > SV_MAX_TOP_K) return 0;
+  // one size for every type: a float32 row has the most slices
+  const size_t a = top_layout(R, V, k, 4, sm_count()).total, b = top_layout(R, V, k, 8, sm_count()).total;
+  return std::max<size_t>(std::max(a, b), kAlign);
+}
+
+extern "C" sv_status sv_top_logits(int R, int V, const void* logits, sv_dtype dtype, int k, float temperature,
+                                   int32_t* indices, float* logprobs, float* tail, void* workspace,
+                                   size_t workspace_bytes, sv_stream_t stream) {
+  if (!rows_ok(R, V) || !dtype_ok(dtype) || k < 1 || k > SV_MAX_TOP_K || !temperature_ok(temperature))
+    return SV_ERR_INVALID_ARG;
+  if (R == 0) return SV_OK;
+  if (!logits || !aligned16(logits) || !indices || !logprobs || !tail) return SV_ERR_INVALID_ARG;
+  const TopLayout L = top_layout(R, V, k, vec_width(dtype), sm_count());
+  if (!workspace || !aligned16(workspace) || workspace_bytes < sv_top_logits_workspace_bytes(R, V, k))
+    return SV_ERR_WORKSPACE;
+  if ((long long)R * L.H > 0x7fffffffll) return SV_ERR_UNSUPPORTED;
+  sv::rows::TopParams p{};
+  p.R = R;
+  p.V = V;
+  p.k = k;
+  p.H = L.H;
+  p.SV = L.SV;
+  // tau from one maximum per thread, or from more where k is near the number
+  // of threads (a slice then lists about 1.4 k elements)
+  p.KP = 1;
+  while (p.KP < 8 && sv::rows::kTlThreads * p.KP < 2 * k) p.KP *= 2;
+  exponent_scale(temperature, &p.c, &p.c_lo);
+  p.inv_t = 1.0 / (double)temperature;
+  p.logits = logits;
+  p.indices = indices;
+  p.logprobs = logprobs;
+  p.tail = tail;
+  unsigned char* w = static_cast<unsigned char*>(workspace);
+  p.ticket = reinterpret_cast<int*>(w + L.ticket);
+  p.part = reinterpret_cast<float4*>(w + L.part);
+  p.lists = reinterpret_cast<unsigned long long*>(w + L.lists);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  switch (dtype) {
+    case SV_DTYPE_F32: return launch_top<float>(p, s);
+    case SV_DTYPE_BF16: return launch_top<__nv_bfloat16>(p, s);
+    default: return launch_top<__half>(p, s);
+  }
+}
+
+extern "C" sv_status sv_distill_forward(int R, int V, const void* student, sv_dtype dtype, const int32_t* indices,
+                                        const float* logprobs, const float* tail, int k, float temperature,
+                                        const float* weight, float* loss, float* stats, sv_stream_t stream) {
+  const sv_status st = check_distill(R, V, student, dtype, indices, logprobs, k, temperature);
+  if (st != SV_OK || R == 0) return st;
+  if (!loss || (stats && !aligned16(stats))) return SV_ERR_INVALID_ARG;
+  sv::rows::DistillParams p = distill_params(R, V, student, indices, logprobs, tail, k, temperature, weight);
+  p.loss = loss;
+  p.stats = stats;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  switch (dtype) {
+    case SV_DTYPE_F32: return launch_distill<float, false>(p, s);
+    case SV_DTYPE_BF16: return launch_distill<__nv_bfloat16, false>(p, s);
+    default: return launch_distill<__half, false>(p, s);
+  }
+}
+
+extern "C" sv_status sv_distill_backward(int R, int V, const void* student, sv_dtype dtype, const int32_t* indices,
+                                         const float* logprobs, int k, float temperature, const float* weight,
+                                         const float* stats, const float* grad_loss, void* grad, sv_stream_t stream) {
+  const sv_status st = check_distill(R, V, student, dtype, indices, logprobs, k, temperature);
+  if (st != SV_OK || R == 0) return st;
+  if (!stats || !aligned16(stats) || !grad_loss || !grad || !aligned16(grad) ||
+      !same_or_apart(student, grad, (size_t)R * V * elem_size(dtype)))
+    return SV_ERR_INVALID_ARG;
+  sv::rows::DistillParams p = distill_params(R, V, student, indices, logprobs, nullptr, k, temperature, weight);
+  p.stats = const_cast<float*>(stats);
+  p.grad_loss = grad_loss;
+  p.grad = grad;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  switch (dtype) {
+    case SV_DTYPE_F32: return launch_distill_backward<float>(p, s);
+    case SV_DTYPE_BF16: return launch_distill_backward<__nv_bfloat16>(p, s);
+    default: return launch_distill_backward<__half>(p, s);
+  }
+}
+
+extern "C" sv_status sv_distill_loss_grad(int R, int V, const void* student, sv_dtype dtype, const int32_t* indices,
+                                          const float* logprobs, const float* tail, int k, float temperature,
+                                          const float* weight, float* loss, void* grad, sv_stream_t stream) {
+  const sv_status st = check_distill(R, V, student, dtype, indices, logprobs, k, temperature);
+  if (st != SV_OK || R == 0) return st;
+  if (!loss || !grad || !aligned16(grad) || !same_or_apart(student, grad, (size_t)R * V * elem_size(dtype)))
+    return SV_ERR_INVALID_ARG;
+  sv::rows::DistillParams p = distill_params(R, V, student, indices, logprobs, tail, k, temperature, weight);
+  p.loss = loss;
+  p.grad = grad;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  switch (dtype) {
+    case SV_DTYPE_F32: return launch_distill<float, true>(p, s);
+    case SV_DTYPE_BF16: return launch_distill<__nv_bfloat16, true>(p, s);
+    default: return launch_distill<__half, true>(p, s);
+  }
+}
