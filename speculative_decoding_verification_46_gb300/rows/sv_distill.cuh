@@ -54,9 +54,11 @@ struct DistillParams {
 
 constexpr float kLog2eHi = 1.442695022e+00f, kLog2eLo = 1.925963033e-08f;
 
-// 2^x of the sum of a product's parts, one correction step: the weight of a
-// value d below its reference.
-__device__ __forceinline__ float weight_fast(float d, float c, float c_lo) { return q_weight(d, 0.f, c, c_lo); }
+// 2^(d (c + c_lo)), one correction step: the weight of a value that lies d
+// below its reference.
+__device__ __forceinline__ float weight_fast(float d, float c, float c_lo) {
+  return d * c < -150.f ? 0.f : q_weight(d, 0.f, c, c_lo);
+}
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }

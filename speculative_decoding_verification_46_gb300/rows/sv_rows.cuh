@@ -169,6 +169,7 @@ __device__ __forceinline__ int block_sum_int_w(int v, int* sm) {
 __device__ __forceinline__ F2 weight_f2(float x, float m, F2 c, const float* tab) {
   if (x == -INFINITY) return F2{0.f, 0.f};
   const float d = x - m;
+  if (d * c.hi < -150.f) return F2{0.f, 0.f};   // also where the product leaves float32's range
   const float bb = d - x;
   const float de = (x - (d - bb)) + (-m - bb);
   const F2 y = exp2_f2(f2_mul(F2{d, de}, c), tab);

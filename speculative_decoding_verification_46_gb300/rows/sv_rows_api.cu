@@ -6,6 +6,8 @@
 #include <cmath>
 #include <cstddef>
 #include <cstdint>
+#include <cstdlib>
+#include <cstring>
 
 #include "specverify_rows.h"
 #include "sv_adjust.cuh"
@@ -113,7 +115,28 @@ sv_status launch_top_u(const sv::rows::TopParams& p, cudaStream_t stream) {
   return launched();
 }
 template <typename T>
+sv_status launch_top_rows(const sv::rows::TopParams& p, cudaStream_t stream) {
+  auto kern = sv::rows::top_row_kernel<T>;
+  const int cap = std::max(512, p.k) + sv::rows::kTrStep;
+  const size_t smem = (size_t)sv::rows::kTrStages * sv::rows::kTrStep * sizeof(uint4) + (size_t)cap * (sizeof(uint4) + sizeof(int));
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
+    cudaGetLastError();
+    return SV_ERR_CUDA;
+  }
+  kern<<<(unsigned)p.R, sv::rows::kTlThreads, smem, stream>>>(p);
+  return launched();
+}
+
+// SPECVERIFY_PATH=toprow / =topslice overrides the choice below (tests cover both).
+int top_override() {
+  const char* e = std::getenv("SPECVERIFY_PATH");
+  return !e ? 0 : std::strcmp(e, "toprow") == 0 ? 1 : std::strcmp(e, "topslice") == 0 ? 2 : 0;
+}
+
+template <typename T>
 sv_status launch_top(const sv::rows::TopParams& p, cudaStream_t stream) {
+  const int o = top_override();
+  if (o == 1 || (o == 0 && p.R >= sm_count())) return launch_top_rows<T>(p, stream);
   const int u = (int)ceil_div(p.SV, sv::rows::kTlThreads);
   if (u <= 1) return launch_top_u<T, 1>(p, stream);
   if (u <= 2) return launch_top_u<T, 2>(p, stream);

@@ -4,8 +4,9 @@
 // A row is cut into H slices of at most 256 * U vectors, one CTA each, held
 // in registers from one read of HBM.  A CTA finds a lower bound tau of its
 // slice's k-th largest value (the k-th largest of some of its group maxima),
-// lists the elements >= tau, ranks them exactly by (value descending, index
-// ascending), and sums 2^((x - m) c) over everything it did not list, m the
+// sets the few vectors that hold an element >= tau aside in shared memory,
+// ranks their elements >= tau exactly by (value descending, index ascending),
+// and sums 2^((x - m) c) over everything it did not list, m the
 // largest of those.  So the mass outside is a sum of its own terms and not a
 // difference, and stays accurate however small it is.  The slices' lists and
 // sums go to the workspace; the last CTA of a row to arrive (an atomic
@@ -25,6 +26,7 @@ namespace rows {
 constexpr int kTlThreads = 256;
 constexpr int kTlWarps = kTlThreads / 32;
 constexpr int kTlCap = 2048;      // candidates of a slice; more are selected exactly
+constexpr int kTlVecs = 1280;     // vectors of a slice set aside
 constexpr int kTlStage = 4096;    // list entries of a row staged in shared memory
 
 struct TopParams {
@@ -42,24 +44,38 @@ struct TopParams {
   unsigned long long* lists;      // [R][H][k] sorted keys; 0 = none
 };
 
-struct TopSmem {
-  unsigned long long buf[kTlStage];   // a slice's candidates; a row's list entries
-  unsigned long long sel[kMaxK];
+struct PickSmem {
   int hist[256];
+  int digit, rank, count;
+};
+
+struct TopSmem {
+  union {
+    struct {                            // a slice's selection
+      unsigned long long cand[kTlCap];
+      uint4 vec[kTlVecs];               // the vectors that hold an element >= tau
+      int vid[kTlVecs];                 // and their numbers in the window
+    };
+    struct {                            // a row's selection
+      unsigned long long buf[kTlStage];
+      unsigned long long sel[kMaxK];
+    };
+  };
+  PickSmem pick;
   float tab[128];
   float fred[kTlWarps];
   F2 f2red[kTlWarps];
   int ired[kTlWarps];
   double lns;
   unsigned long long kth;
-  unsigned lmax;                      // okey of the largest candidate beyond the k best
-  int count, flag, pick_digit, pick_rank, pick_count;
+  unsigned lmax;                        // okey of the largest candidate beyond the k best
+  int count, nvec, flag;
 };
 
 // One digit of a radix select: with hist[] complete, the digit (0..255, from
 // the top) that holds the rank-th largest, the rank inside it and its count.
 // digit -1: fewer than rank keys.  Every thread returns the same values.
-__device__ __forceinline__ int pick_digit(TopSmem& sm, int rank, int* rank_in, int* count) {
+__device__ __forceinline__ int pick_digit(PickSmem& sm, int rank, int* rank_in, int* count) {
   __syncthreads();
   const int lane = threadIdx.x & 31;
   if (threadIdx.x < 32) {
@@ -87,22 +103,22 @@ __device__ __forceinline__ int pick_digit(TopSmem& sm, int rank, int* rank_in, i
         }
         if (dg < 0) run += c[e];
       }
-      sm.pick_digit = dg;
-      sm.pick_rank = rank - run;
-      sm.pick_count = cc;
+      sm.digit = dg;
+      sm.rank = rank - run;
+      sm.count = cc;
     }
-    if (__ballot_sync(0xffffffffu, mine) == 0u && lane == 0) sm.pick_digit = -1;
+    if (__ballot_sync(0xffffffffu, mine) == 0u && lane == 0) sm.digit = -1;
   }
   __syncthreads();
-  *rank_in = sm.pick_rank;
-  *count = sm.pick_count;
-  return sm.pick_digit;
+  *rank_in = sm.rank;
+  *count = sm.count;
+  return sm.digit;
 }
 
 // The largest K, bits below LOW zero, such that at least k of the block's
 // keys (U per thread, 0 = none) are >= K; 0 if there are fewer than k.
 template <int LOW, int U>
-__device__ __forceinline__ uint32_t kth_key(const uint32_t (&key)[U], int k, TopSmem& sm) {
+__device__ __forceinline__ uint32_t kth_key(const uint32_t (&key)[U], int k, PickSmem& sm) {
   uint32_t prefix = 0u;
   int rank = k;
 #pragma unroll
@@ -123,6 +139,90 @@ __device__ __forceinline__ uint32_t kth_key(const uint32_t (&key)[U], int k, Top
     if (cnt == rank) break;   // everything in the digit is wanted: the rest of the bits may stay 0
   }
   return prefix;
+}
+
+// The k-th largest of more than k distinct keys (value, ~index) that
+// each(f) passes to f, every thread its own: a radix select from the top, up
+// to the digit whose keys are all wanted (then the bits below stay 0).
+template <typename T, typename Each>
+__device__ __forceinline__ unsigned long long select_kth64(int k, int V, PickSmem& sm, Each each) {
+  constexpr int LOW = Tr<T>::KEY_LOW_BIT;
+  const int nidx = V > 1 ? 32 - __clz(V - 1) : 1;          // index bits that differ
+  unsigned long long prefix = 0ull, known = 0ull;
+  int rank = k, hi = 63;
+#pragma unroll 1
+  while (true) {
+    const int lo = max(hi - 7, hi >= 32 ? 32 + LOW : 0);
+    const unsigned dmask = (1u << (hi - lo + 1)) - 1u;
+    __syncthreads();
+    sm.hist[threadIdx.x] = 0;
+    __syncthreads();
+    each([&](unsigned long long key) {
+      if ((key & known) == prefix) atomicAdd(&sm.hist[(unsigned)(key >> lo) & dmask], 1);
+    });
+    int in, cnt;
+    const int dg = pick_digit(sm, rank, &in, &cnt);
+    prefix |= (unsigned long long)(unsigned)dg << lo;
+    known |= (unsigned long long)dmask << lo;
+    rank = in;
+    if (cnt == rank || lo == 0) return prefix;
+    hi = lo - 1;
+    if (lo == 32 + LOW) {
+      // value bits below LOW copy the sign (all ones in a negative's key);
+      // index bits above those that differ are ones (the index is complemented)
+      const unsigned long long skip = ((1ull << (32 + LOW)) - 1ull) & ~((1ull << 32) - 1ull);
+      if (!(prefix >> 63)) prefix |= skip;
+      const unsigned long long ones = nidx >= 32 ? 0ull : ((1ull << 32) - 1ull) & ~((1ull << nidx) - 1ull);
+      prefix |= ones;
+      known |= skip | ones;
+      hi = nidx - 1;
+    }
+  }
+}
+
+// The record of a row from its k best (keys sel[0 .. kk), any order) and the
+// rest's mass st relative to mt (0: none).  Ends with the outputs written.
+template <int NW>
+__device__ __forceinline__ void top_write(const TopParams& p, int r, const unsigned long long* sel, int kk, float mt,
+                                          F2 st, const float* tab, float* fred, F2* f2red, double* s_lns) {
+  const int tid = threadIdx.x, k = p.k;
+  const F2 c{p.c, p.c_lo};
+  float M = -INFINITY;
+  for (int j = tid; j < kk; j += NW * 32) M = fmaxf(M, comp_val(sel[j]));
+  M = block_max_n<NW>(M, fred);
+  F2 sk{0.f, 0.f};
+  for (int j = tid; j < kk; j += NW * 32) sk = f2_add(sk, weight_f2(comp_val(sel[j]), M, c, tab));
+  sk = block_sum_f2_n<NW>(sk, f2red);
+  if (tid == 0) {
+    const bool some = st.hi > 0.f;
+    const F2 tail_m = some ? f2_mul(st, weight_f2(mt, M, c, tab)) : F2{0.f, 0.f};
+    const double lns = log(f2_double(f2_add(sk, tail_m)));
+    *s_lns = lns;
+    p.tail[r] = some ? (float)(((double)mt - (double)M) * p.inv_t + log(f2_double(st)) - lns) : -INFINITY;
+  }
+  __syncthreads();
+  const double lns = *s_lns;
+  for (int e = tid; e < kk; e += NW * 32) {
+    const unsigned long long me = sel[e];
+    int rank = 0;
+    for (int j = 0; j < kk; ++j) rank += sel[j] > me;
+    p.indices[(size_t)r * k + rank] = comp_idx(me);
+    p.logprobs[(size_t)r * k + rank] = (float)(((double)comp_val(me) - (double)M) * p.inv_t - lns);
+  }
+  for (int j = kk + tid; j < k; j += NW * 32) {
+    p.indices[(size_t)r * k + j] = -1;
+    p.logprobs[(size_t)r * k + j] = -INFINITY;
+  }
+}
+
+// The record of a row that defines no distribution.
+__device__ __forceinline__ void top_write_bad(const TopParams& p, int r) {
+  const float nan = __uint_as_float(0x7fffffffu);
+  if (threadIdx.x == 0) p.tail[r] = nan;
+  for (int j = threadIdx.x; j < p.k; j += blockDim.x) {
+    p.indices[(size_t)r * p.k + j] = -1;
+    p.logprobs[(size_t)r * p.k + j] = nan;
+  }
 }
 
 // The row's lists are in: select, rank and write the record.
@@ -150,65 +250,29 @@ __device__ void top_finish_row(const TopParams& p, int r, TopSmem& sm) {
   const bool ok = have > 0 && !bad;
   const int kk = min(k, have);
   if (ok) {
-    // ---- K64: exactly kk keys are >= it (the keys are distinct)
-    unsigned long long K64 = 1ull;
-    if (have > k) {
-      constexpr int LOW = Tr<T>::KEY_LOW_BIT;
-      const int nidx = p.V > 1 ? 32 - __clz(p.V - 1) : 1;        // index bits that differ
-      unsigned long long prefix = 0ull, known = 0ull;
-      int rank = k;
-      int hi = 63;
-      while (true) {
-        const int stop = hi >= 32 ? 32 + LOW : 0;
-        const int lo = max(hi - 7, stop);
-        const unsigned dmask = (1u << (hi - lo + 1)) - 1u;
-        sm.hist[tid] = 0;
-        __syncthreads();
-        for (int e = tid; e < slots; e += kTlThreads) {
-          const unsigned long long key = staged ? sm.buf[e] : __ldcg(lists + e);
-          if (key != 0ull && (key & known) == prefix) atomicAdd(&sm.hist[(unsigned)(key >> lo) & dmask], 1);
-        }
-        int in, cnt;
-        const int dg = pick_digit(sm, rank, &in, &cnt);
-        prefix |= (unsigned long long)(unsigned)dg << lo;
-        known |= (unsigned long long)dmask << lo;
-        rank = in;
-        if (cnt == rank || lo == 0) break;
-        hi = lo - 1;
-        if (lo == 32 + LOW) {
-          // value bits below LOW copy the sign (all ones in a negative's key);
-          // index bits above those that differ are ones (the index is complemented)
-          const unsigned long long skip = ((1ull << (32 + LOW)) - 1ull) & ~((1ull << 32) - 1ull);
-          if (!(prefix >> 63)) prefix |= skip;
-          known |= skip;
-          const unsigned long long ones = nidx >= 32 ? 0ull : ((1ull << 32) - 1ull) & ~((1ull << nidx) - 1ull);
-          prefix |= ones;
-          known |= ones;
-          hi = nidx - 1;
-        }
+    // ---- K64: exactly kk keys are >= it
+    const unsigned long long K64 = have > k ? select_kth64<T>(k, p.V, sm.pick, [&](auto f) {
+      for (int e = tid; e < slots; e += kTlThreads) {
+        const unsigned long long key = staged ? sm.buf[e] : __ldcg(lists + e);
+        if (key != 0ull) f(key);
       }
-      K64 = prefix;
-    }
+    }) : 1ull;
     // ---- the k best, in any order, then ranked
     if (tid == 0) sm.count = 0;
     __syncthreads();
-    float lm = -INFINITY, M = -INFINITY;
+    float lm = -INFINITY;
     for (int e = tid; e < slots; e += kTlThreads) {
       const unsigned long long key = staged ? sm.buf[e] : __ldcg(lists + e);
       if (key >= K64) {
         const int pos = atomicAdd(&sm.count, 1);
         if (pos < kMaxK) sm.sel[pos] = key;
-        M = fmaxf(M, comp_val(key));
       } else if (key != 0ull) {
         lm = fmaxf(lm, comp_val(key));
       }
     }
     mt = block_max_n<kTlWarps>(fmaxf(mt, lm), sm.fred);
-    M = block_max_n<kTlWarps>(M, sm.fred);
     const F2 c{p.c, p.c_lo};
-    // ---- the masses: of K relative to M, of the rest relative to mt
-    F2 sk{0.f, 0.f}, st{0.f, 0.f};
-    for (int j = tid; j < kk; j += kTlThreads) sk = f2_add(sk, weight_f2(comp_val(sm.sel[j]), M, c, sm.tab));
+    F2 st{0.f, 0.f};
     for (int h = tid; h < p.H; h += kTlThreads) {
       const float4 v = __ldcg(part + h);
       if (v.x > -INFINITY) st = f2_add(st, f2_mul(F2{v.y, v.z}, weight_f2(v.x, mt, c, sm.tab)));
@@ -217,30 +281,10 @@ __device__ void top_finish_row(const TopParams& p, int r, TopSmem& sm) {
       const unsigned long long key = staged ? sm.buf[e] : __ldcg(lists + e);
       if (key < K64 && key != 0ull) st = f2_add(st, weight_f2(comp_val(key), mt, c, sm.tab));
     }
-    sk = block_sum_f2_n<kTlWarps>(sk, sm.f2red);
     st = block_sum_f2_n<kTlWarps>(st, sm.f2red);
-    if (tid == 0) {
-      const bool some = st.hi > 0.f;
-      const F2 tail_m = some ? f2_mul(st, weight_f2(mt, M, c, sm.tab)) : F2{0.f, 0.f};
-      const double lns = log(f2_double(f2_add(sk, tail_m)));
-      sm.lns = lns;
-      p.tail[r] = some ? (float)(((double)mt - (double)M) * p.inv_t + log(f2_double(st)) - lns) : -INFINITY;
-    }
-    __syncthreads();
-    const double lns = sm.lns;
-    for (int e = tid; e < kk; e += kTlThreads) {
-      const unsigned long long me = sm.sel[e];
-      int rank = 0;
-      for (int j = 0; j < kk; ++j) rank += sm.sel[j] > me;
-      p.indices[(size_t)r * k + rank] = comp_idx(me);
-      p.logprobs[(size_t)r * k + rank] = (float)(((double)comp_val(me) - (double)M) * p.inv_t - lns);
-    }
-  } else if (tid == 0) {
-    p.tail[r] = __uint_as_float(0x7fffffffu);
-  }
-  for (int j = (ok ? kk : 0) + tid; j < k; j += kTlThreads) {
-    p.indices[(size_t)r * k + j] = -1;
-    p.logprobs[(size_t)r * k + j] = ok ? -INFINITY : __uint_as_float(0x7fffffffu);
+    top_write<kTlWarps>(p, r, sm.sel, kk, mt, st, sm.tab, sm.fred, sm.f2red, &sm.lns);
+  } else {
+    top_write_bad(p, r);
   }
   // leave the workspace zero-filled
   __syncthreads();
@@ -249,11 +293,73 @@ __device__ void top_finish_row(const TopParams& p, int r, TopSmem& sm) {
   for (int h = tid; h < p.H; h += kTlThreads) part[h] = make_float4(0.f, 0.f, 0.f, 0.f);
 }
 
+// Too many elements reach the bound (ties, or fewer groups than k): the exact
+// k-th largest value of the slice by bisection over its key, of its ties the
+// first ones.  Fills cand[0 .. k) and returns the largest and the sum of the
+// rest.  Rare, so it reads the slice again (L2) in small loops instead of
+// keeping a second unrolled copy of the work in the instruction cache.
+template <typename T>
+__device__ __noinline__ F2 top_slice_exact(const Window<T, const T>& win, int v0, int v1, int k, float c, TopSmem& sm,
+                                           float* rest_max) {
+  using TR = Tr<T>;
+  constexpr int VW = TR::VW;
+  const int tid = threadIdx.x;
+  auto each = [&](auto f) {
+    for (int v = v0 + tid; v < v1; v += kTlThreads) {
+      const uint4 x = win.load(v);
+#pragma unroll
+      for (int t = 0; t < VW; ++t) f(TR::get(x, t), v * VW - win.a0 + t);
+    }
+  };
+  uint32_t KV = 0u;
+#pragma unroll 1
+  for (int bit = 31; bit >= TR::KEY_LOW_BIT; --bit) {
+    const uint32_t Kt = KV | (1u << bit);
+    int mine = 0;
+    each([&](float x, int) { mine += x > -INFINITY && okey(x) >= Kt; });
+    if (block_sum_int_w<kTlWarps>(mine, sm.ired) >= k) KV = Kt;
+  }
+  // the value itself: bits below KEY_LOW_BIT are ones in a negative's key
+  const float tau = key_to_float((KV & 0x80000000u) ? KV : KV | ((1u << TR::KEY_LOW_BIT) - 1u));
+  int above = 0;
+  each([&](float x, int) { above += x > tau; });
+  const int need = k - block_sum_int_w<kTlWarps>(above, sm.ired);
+  int lo = v0 * VW - win.a0, hi = v1 * VW - win.a0 - 1;   // the smallest index with `need` ties up to it
+#pragma unroll 1
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    int mine = 0;
+    each([&](float x, int i) { mine += x == tau && i <= mid; });
+    if (block_sum_int_w<kTlWarps>(mine, sm.ired) >= need) hi = mid; else lo = mid + 1;
+  }
+  __syncthreads();
+  if (tid == 0) sm.count = 0;
+  __syncthreads();
+  float mr = -INFINITY;
+  each([&](float x, int i) {
+    if (x > tau || (x == tau && i <= lo)) {
+      const int pos = atomicAdd(&sm.count, 1);
+      if (pos < kTlCap) sm.cand[pos] = comp_key(x, i);
+    } else {
+      mr = fmaxf(mr, x);
+    }
+  });
+  mr = block_max_n<kTlWarps>(mr, sm.fred);
+  *rest_max = mr;
+  F2 s{0.f, 0.f};
+  if (mr > -INFINITY) {
+    each([&](float x, int i) {
+      if (!(x > tau || (x == tau && i <= lo))) s = f2_add(s, F2{ex2_approx((x - mr) * c), 0.f});
+    });
+  }
+  return s;
+}
+
 template <typename T, int U>
 __global__ void __launch_bounds__(kTlThreads, 4) top_slice_kernel(const TopParams p) {
   using TR = Tr<T>;
   constexpr int VW = TR::VW;
-  __shared__ TopSmem sm;
+  __shared__ __align__(16) TopSmem sm;
   const int tid = threadIdx.x, k = p.k;
   const int r = blockIdx.x / p.H;
   const int h = blockIdx.x - r * p.H;
@@ -268,7 +374,7 @@ __global__ void __launch_bounds__(kTlThreads, 4) top_slice_kernel(const TopParam
   }
   load_exp2_table(sm.tab);
   if (tid == 0) {
-    sm.count = 0;
+    sm.count = sm.nvec = 0;
     sm.lmax = 0u;
     sm.kth = 0ull;
   }
@@ -283,135 +389,330 @@ __global__ void __launch_bounds__(kTlThreads, 4) top_slice_kernel(const TopParam
     for (int u = 0; u < U; ++u) {
       vm[u] = TR::template vmax<true>(x[u]);
       bad |= !(vm[u] < INFINITY);                      // NaN or +inf
-      g = (u % gs) == 0 ? vm[u] : fmaxf(g, vm[u]);
-      key[u] = (u % gs) == gs - 1 && g > -INFINITY ? okey(g) : 0u;
+      g = (u & (gs - 1)) == 0 ? vm[u] : fmaxf(g, vm[u]);
+      key[u] = (u & (gs - 1)) == gs - 1 && g > -INFINITY ? okey(g) : 0u;
     }
   }
   bad = __syncthreads_or(bad);
   F2 s{0.f, 0.f};
   float mr = -INFINITY;
   if (!bad) {
-    const uint32_t K = kth_key<TR::KEY_LOW_BIT, U>(key, k, sm);
-    float tau = K == 0u ? -INFINITY : key_to_float(K);
-    const int i0 = v0 * VW - win.a0;                   // row index of the slice's first element
+    const uint32_t K = kth_key<TR::KEY_LOW_BIT, U>(key, k, sm.pick);
+    const float tau = K == 0u ? -INFINITY : key_to_float(K);
+    // ---- the few vectors that reach tau go to shared memory and out of the registers
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (vm[u] > -INFINITY && vm[u] >= tau) {
-#pragma unroll
-        for (int t = 0; t < VW; ++t) {
-          const float xv = TR::get(x[u], t);
-          if (xv > -INFINITY && xv >= tau) {
-            const int pos = atomicAdd(&sm.count, 1);
-            if (pos < kTlCap) sm.buf[pos] = comp_key(xv, i0 + (u * kTlThreads + tid) * VW + t);
-          }
+      if (vm[u] >= tau && vm[u] > -INFINITY) {
+        const int pos = atomicAdd(&sm.nvec, 1);
+        if (pos < kTlVecs) {
+          sm.vec[pos] = x[u];
+          sm.vid[pos] = v0 + u * kTlThreads + tid;
         }
+        x[u] = make_uint4(TR::kPadWord, TR::kPadWord, TR::kPadWord, TR::kPadWord);
+        vm[u] = -INFINITY;
       }
+      mr = fmaxf(mr, vm[u]);
     }
     __syncthreads();
-    int N = sm.count;
-    int tie_idx = 0x7fffffff;                          // of the elements equal to tau, those up to this index are listed
-    if (N > kTlCap) {
-      // Too many (ties at tau, or fewer groups than k): the exact k-th
-      // largest value by bisection over its key, then of its ties the first.
-      uint32_t KV = 0u;
-      for (int bit = 31; bit >= TR::KEY_LOW_BIT; --bit) {
-        const uint32_t Kt = KV | (1u << bit);
-        int mine = 0;
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-          for (int t = 0; t < VW; ++t) {
-            const float xv = TR::get(x[u], t);
-            mine += xv > -INFINITY && okey(xv) >= Kt;
-          }
-        if (block_sum_int_w<kTlWarps>(mine, sm.ired) >= k) KV = Kt;
-      }
-      // the value itself: bits below KEY_LOW_BIT are ones in a negative's key
-      tau = key_to_float((KV & 0x80000000u) ? KV : KV | ((1u << TR::KEY_LOW_BIT) - 1u));
-      int above = 0;
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int t = 0; t < VW; ++t) above += TR::get(x[u], t) > tau;
-      const int need = k - block_sum_int_w<kTlWarps>(above, sm.ired);
-      int lo = i0, hi = i0 + p.SV * VW - 1;            // the smallest index with `need` ties up to it
-      while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        int mine = 0;
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-          for (int t = 0; t < VW; ++t)
-            mine += TR::get(x[u], t) == tau && i0 + (u * kTlThreads + tid) * VW + t <= mid;
-        if (block_sum_int_w<kTlWarps>(mine, sm.ired) >= need) hi = mid; else lo = mid + 1;
-      }
-      tie_idx = lo;
-      __syncthreads();
-      if (tid == 0) sm.count = 0;
-      __syncthreads();
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int t = 0; t < VW; ++t) {
-          const float xv = TR::get(x[u], t);
-          const int idx = i0 + (u * kTlThreads + tid) * VW + t;
-          if (xv > tau || (xv == tau && idx <= tie_idx)) {
-            const int pos = atomicAdd(&sm.count, 1);
-            if (pos < kTlCap) sm.buf[pos] = comp_key(xv, idx);
-          }
+    const int NE = sm.nvec * VW;
+    bool exact = NE > kTlVecs * VW;
+    // ---- their elements, one thread each: candidates, or rest
+    if (!exact) {
+      for (int e = tid; e < NE; e += kTlThreads) {
+        const float xv = Elem<T>::load(reinterpret_cast<const T*>(sm.vec) + e);
+        if (xv >= tau && xv > -INFINITY) {
+          const int pos = atomicAdd(&sm.count, 1);
+          if (pos < kTlCap) sm.cand[pos] = comp_key(xv, sm.vid[e / VW] * VW - win.a0 + e % VW);
+        } else {
+          mr = fmaxf(mr, xv);
         }
+      }
       __syncthreads();
-      N = min(sm.count, kTlCap);
+      exact = sm.count > kTlCap;
     }
+    if (exact) {
+      __syncthreads();                                 // everyone has read the counts
+      s = top_slice_exact(win, v0, v1, k, p.c, sm, &mr);
+      __syncthreads();
+    }
+    const int N = min(sm.count, kTlCap);
     // ---- exact ranks: the k best to the row's list, the others to the rest
     unsigned long long* list = p.lists + ((size_t)r * p.H + h) * k;
     for (int e = tid; e < N; e += kTlThreads) {
-      const unsigned long long me = sm.buf[e];
+      const unsigned long long me = sm.cand[e];
       int rank = 0;
-      for (int j = 0; j < N; ++j) rank += sm.buf[j] > me;
+      for (int j = 0; j < N; ++j) rank += sm.cand[j] > me;
       if (rank < k) list[rank] = me;
       if (rank == k - 1) sm.kth = me;
       if (rank == k) sm.lmax = okey(comp_val(me));     // the largest beyond the list
     }
-    // ---- the mass of everything not listed
+    // ---- the mass of everything not listed, relative to its largest
+    if (!exact) {
+      mr = block_max_n<kTlWarps>(mr, sm.fred);         // its barriers publish kth and lmax too
+      if (sm.lmax != 0u) mr = fmaxf(mr, key_to_float(sm.lmax));
+      if (mr > -INFINITY) {
+        float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (vm[u] < tau) {
-        mr = fmaxf(mr, vm[u]);
-      } else {
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int t = 0; t < VW; ++t) {
-          const float xv = TR::get(x[u], t);
-          if (xv < tau || (xv == tau && i0 + (u * kTlThreads + tid) * VW + t > tie_idx)) mr = fmaxf(mr, xv);
+          for (int t = 0; t < VW; t += 2) {
+            s0 += ex2_approx((TR::get(x[u], t) - mr) * p.c);
+            s1 += ex2_approx((TR::get(x[u], t + 1) - mr) * p.c);
+          }
+        for (int e = tid; e < NE; e += kTlThreads) {
+          const float xv = Elem<T>::load(reinterpret_cast<const T*>(sm.vec) + e);
+          if (xv < tau) s0 += ex2_approx((xv - mr) * p.c);
+        }
+        s = f2_add(F2{s0, 0.f}, F2{s1, 0.f});
+        const unsigned long long kth = sm.kth;         // 0: the list holds all candidates
+        for (int e = tid; e < N; e += kTlThreads) {
+          const unsigned long long me = sm.cand[e];
+          if (me < kth) s = f2_add(s, weight_f2(comp_val(me), mr, F2{p.c, p.c_lo}, sm.tab));
         }
       }
     }
-    mr = block_max_n<kTlWarps>(mr, sm.fred);           // its barriers publish kth and lmax too
-    if (sm.lmax != 0u) mr = fmaxf(mr, key_to_float(sm.lmax));
-    if (mr > -INFINITY) {
-      float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int t = 0; t < VW; t += 2) {
-          const float xa = TR::get(x[u], t), xb = TR::get(x[u], t + 1);
-          const int ia = i0 + (u * kTlThreads + tid) * VW + t;
-          const bool ra = xa < tau || (xa == tau && ia > tie_idx);
-          const bool rb = xb < tau || (xb == tau && ia + 1 > tie_idx);
-          s0 += ra ? ex2_approx((xa - mr) * p.c) : 0.f;
-          s1 += rb ? ex2_approx((xb - mr) * p.c) : 0.f;
-        }
-      s = f2_add(F2{s0, 0.f}, F2{s1, 0.f});
-      const unsigned long long kth = sm.kth;           // 0: the list holds all candidates
-      for (int e = tid; e < N; e += kTlThreads) {
-        const unsigned long long me = sm.buf[e];
-        if (me < kth) s = f2_add(s, weight_f2(comp_val(me), mr, F2{p.c, p.c_lo}, sm.tab));
-      }
-      s = block_sum_f2_n<kTlWarps>(s, sm.f2red);
-    }
+    s = block_sum_f2_n<kTlWarps>(s, sm.f2red);
   }
   if (tid == 0) p.part[(size_t)r * p.H + h] = make_float4(mr, s.hi, s.lo, bad ? 1.f : 0.f);
   if (arrive_last(p.ticket + r, p.H, &sm.flag)) top_finish_row<T>(p, r, sm);
+}
+
+// ---- one CTA per row
+//
+// For many rows the slices' selections are most of the work: ten per row of
+// 150 thousand tokens.  Here a CTA streams a whole row through a ring of
+// cp.async stages private to each thread and selects once.  `thr` is a lower
+// bound of the row's k-th largest value at any time: from the first step's
+// vector maxima, later from the elements set aside so far.  Vectors that reach
+// it are set aside in shared memory; everything else goes into the thread's
+// running (maximum, sum) at once.  When the vectors set aside exceed `trig`
+// (>= k) they are cut back to those that hold one of the k best so far - an
+// element equal to the k-th that comes later in the row loses the tie, so the
+// bound is strict from then on, and rows of ties or of rising values cost more
+// cuts but need no other path.
+constexpr int kTrU = 4;                         // vectors per thread per step
+constexpr int kTrStages = 2;                    // steps in flight
+constexpr int kTrStep = kTrU * kTlThreads;      // vectors per step
+
+struct TopRowSmem {
+  PickSmem pick;
+  float tab[128];
+  float fred[kTlWarps];
+  F2 f2red[kTlWarps];
+  int ired[kTlWarps];
+  double lns;
+  int nvec, count;
+};
+
+// A thread's running (maximum, sum) of the elements that are not set aside.
+// The sum is relative to rho = round(m c) in units of log2, so that a term
+// costs one multiply-add and one exponential; the rounding of rho leaves with
+// scale().  Terms gather in short float32 chains that take() adds to the
+// two-float total, so a row of 2^24 tokens is summed as exactly as a short
+// one.  rho that leaves the range of exact multiply-adds (enormous logits or
+// tiny temperatures) takes the difference first.
+struct RunningSum {
+  float m = -INFINITY, rho = 0.f;
+  F2 s{0.f, 0.f};
+  bool far = false;
+  __device__ __forceinline__ float scale(float c) const { return far || m == -INFINITY ? 1.f : ex2_approx(-fmaf(m, c, -rho)); }
+  __device__ __forceinline__ void raise(float to, float c) {
+    if (to > m) {
+      const float f = m == -INFINITY ? 0.f : ex2_approx((m - to) * c) * scale(c);
+      s.hi *= f;
+      s.lo *= f;
+      m = to;
+      rho = m * c;
+      far = !(fabsf(rho) < 1.0e30f);
+    }
+  }
+  // 2^((x - m) c), x <= m
+  __device__ __forceinline__ float term(float x, float c) const { return ex2_approx(fmaf(x, c, -rho)); }
+  __device__ __forceinline__ float term_far(float x, float c) const { return ex2_approx((x - m) * c); }
+  __device__ __forceinline__ void take(float t) { s = f2_add(s, F2{t, 0.f}); }
+  __device__ __forceinline__ void add(float x, float c) {
+    if (x == -INFINITY) return;
+    raise(x, c);
+    take(far ? term_far(x, c) : term(x, c));
+  }
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kTlThreads, 3) top_row_kernel(const TopParams p) {
+  using TR = Tr<T>;
+  constexpr int VW = TR::VW;
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  __shared__ TopRowSmem sm;
+  const int tid = threadIdx.x, k = p.k, r = blockIdx.x;
+  const int trig = max(512, k);                                      // cap - kTrStep
+  uint4* ring = reinterpret_cast<uint4*>(smem_raw);                  // [kTrStages][kTrU][kTlThreads]
+  uint4* vec = ring + kTrStages * kTrStep;                           // [trig + kTrStep] set aside
+  int* vid = reinterpret_cast<int*>(vec + trig + kTrStep);           // their numbers in the window
+  const Window<T, const T> win(static_cast<const T*>(p.logits), (size_t)r, p.V);
+  const int NV = win.vectors();
+  const int steps = (NV + kTrStep - 1) / kTrStep;
+  const uint4 pad = make_uint4(TR::kPadWord, TR::kPadWord, TR::kPadWord, TR::kPadWord);
+
+  auto issue = [&](int step) {
+    uint4* slot = ring + (step % kTrStages) * kTrStep + tid;
+#pragma unroll
+    for (int u = 0; u < kTrU; ++u) {
+      const int v = step * kTrStep + u * kTlThreads + tid;
+      if (v < NV) {
+        if (win.whole(v)) {
+          const unsigned sa = (unsigned)__cvta_generic_to_shared(slot + u * kTlThreads);
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(sa), "l"(win.base + (size_t)v * VW) : "memory");
+        } else {
+          slot[u * kTlThreads] = win.load(v);
+        }
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int s = 0; s < kTrStages; ++s) issue(s);
+  load_exp2_table(sm.tab);
+  if (tid == 0) sm.nvec = 0;
+
+  float thr = -INFINITY;                                             // what is set aside from here on
+  float low = -INFINITY;                                             // what is among the best of those set aside
+  int bad = 0;
+  RunningSum acc;
+  const float c = p.c;
+  // every element set aside that may be among the k best
+  auto candidates = [&](int n, auto f) {
+    for (int e = tid; e < n * VW; e += kTlThreads) {
+      const float xv = Elem<T>::load(reinterpret_cast<const T*>(vec) + e);
+      if (xv >= low && xv > -INFINITY) f(comp_key(xv, vid[e / VW] * VW - win.a0 + e % VW));
+    }
+  };
+#pragma unroll 1
+  for (int step = 0; step < steps; ++step) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kTrStages - 1) : "memory");
+    uint4 x[kTrU];
+    float vm[kTrU];
+    const uint4* slot = ring + (step % kTrStages) * kTrStep + tid;
+#pragma unroll
+    for (int u = 0; u < kTrU; ++u) {
+      x[u] = step * kTrStep + u * kTlThreads + tid < NV ? slot[u * kTlThreads] : pad;
+      vm[u] = TR::template vmax<true>(x[u]);
+      bad |= !(vm[u] < INFINITY);                                    // NaN or +inf
+    }
+    issue(step + kTrStages);
+    if (step == 0) {
+      uint32_t key[kTrU];
+#pragma unroll
+      for (int u = 0; u < kTrU; ++u) key[u] = vm[u] > -INFINITY ? okey(vm[u]) : 0u;
+      const uint32_t K = kth_key<TR::KEY_LOW_BIT, kTrU>(key, k, sm.pick);
+      if (K != 0u) thr = low = key_to_float(K);
+    }
+    int over = 0;
+    float mc = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < kTrU; ++u) {
+      if (vm[u] >= thr && vm[u] > -INFINITY) {
+        const int pos = atomicAdd(&sm.nvec, 1);
+        vec[pos] = x[u];
+        vid[pos] = step * kTrStep + u * kTlThreads + tid;
+        over |= pos >= trig;
+        x[u] = pad;
+      } else {
+        mc = fmaxf(mc, vm[u]);
+      }
+    }
+    acc.raise(mc, c);
+    if (acc.m > -INFINITY) {
+      float s0 = 0.f, s1 = 0.f;
+      if (!acc.far) {
+#pragma unroll
+        for (int u = 0; u < kTrU; ++u)
+#pragma unroll
+          for (int t = 0; t < VW; t += 2) {
+            s0 += acc.term(TR::get(x[u], t), c);
+            s1 += acc.term(TR::get(x[u], t + 1), c);
+          }
+      } else {
+#pragma unroll
+        for (int u = 0; u < kTrU; ++u) {
+#pragma unroll 1
+          for (int t = 0; t < VW; ++t) s0 += acc.term_far(TR::get(x[u], t), c);
+        }
+      }
+      acc.take(s0 + s1);
+    }
+    if (__syncthreads_or(over)) {
+      // cut back to the vectors that hold one of the k best so far
+      const int n = sm.nvec;
+      const unsigned long long K64 = select_kth64<T>(k, p.V, sm.pick, [&](auto f) { candidates(n, f); });
+      __syncthreads();
+      if (tid == 0) sm.nvec = 0;
+#pragma unroll 1
+      for (int e0 = 0; e0 < n; e0 += kTlThreads) {
+        const int e = e0 + tid;
+        uint4 y = pad;
+        int id = 0;
+        if (e < n) {
+          y = vec[e];
+          id = vid[e];
+        }
+        bool keep = false;
+#pragma unroll
+        for (int t = 0; t < VW; ++t) {
+          const float xv = TR::get(y, t);
+          keep |= xv > -INFINITY && comp_key(xv, id * VW - win.a0 + t) >= K64;
+        }
+        __syncthreads();                                             // this round's vectors are in registers
+        if (keep) {
+          const int pos = atomicAdd(&sm.nvec, 1);
+          vec[pos] = y;
+          vid[pos] = id;
+        } else {
+#pragma unroll
+          for (int t = 0; t < VW; ++t) acc.add(TR::get(y, t), c);
+        }
+      }
+      // K64 may have stopped early, with zeros below the digits that it
+      // needed: a smaller bound then.  Keys of finite values start at 0x00800000.
+      const uint32_t kv = max((uint32_t)(K64 >> 32), 0x007fffffu);
+      thr = key_to_float(kv + 1u);
+      low = key_to_float(max(kv, 0x00800000u));
+      __syncthreads();
+    }
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+
+  // ---- the record
+  bad = __syncthreads_or(bad);
+  const int n = sm.nvec;
+  unsigned long long* sel = reinterpret_cast<unsigned long long*>(ring);
+  int have = 0;
+  if (!bad) {
+    for (int e = tid; e < n * VW; e += kTlThreads) have += Elem<T>::load(reinterpret_cast<const T*>(vec) + e) > -INFINITY;
+    have = block_sum_int_w<kTlWarps>(have, sm.ired);
+  }
+  if (bad || have == 0) {
+    top_write_bad(p, r);
+    return;
+  }
+  low = -INFINITY;                                                   // the record may reach any element set aside
+  const unsigned long long K64 = have > k ? select_kth64<T>(k, p.V, sm.pick, [&](auto f) { candidates(n, f); }) : 1ull;
+  __syncthreads();
+  if (tid == 0) sm.count = 0;
+  __syncthreads();
+  candidates(n, [&](unsigned long long key) {
+    if (key >= K64) {
+      const int pos = atomicAdd(&sm.count, 1);
+      if (pos < kMaxK) sel[pos] = key;
+    } else {
+      acc.add(comp_val(key), c);
+    }
+  });
+  const float mt = block_max_n<kTlWarps>(acc.m, sm.fred);
+  F2 st{0.f, 0.f};
+  if (acc.m > -INFINITY)
+    st = f2_mul(f2_mul(acc.s, F2{acc.scale(c), 0.f}), weight_f2(acc.m, mt, F2{p.c, p.c_lo}, sm.tab));
+  st = block_sum_f2_n<kTlWarps>(st, sm.f2red);
+  top_write<kTlWarps>(p, r, sel, min(k, have), mt, st, sm.tab, sm.fred, sm.f2red, &sm.lns);
 }
 
 }  // namespace rows

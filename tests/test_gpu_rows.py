@@ -225,6 +225,13 @@ def _check_top(sv, L, k, T, dtype, **kw):
     _assert_close(tail.reshape(-1), want_t, 2 * s + U * np.abs(np.where(np.isfinite(want_t), want_t, 0)), "tail")
 
 
+@pytest.fixture(params=["toprow", "topslice"])
+def top_path(request, monkeypatch):
+    """Both kernels at every size: one CTA per row, and slices of rows."""
+    monkeypatch.setenv("SPECVERIFY_PATH", request.param)
+    return request.param
+
+
 def _top_rows(seed, R, V, dtype, ties=False):
     g = torch.Generator().manual_seed(seed)
     x = torch.randn(R, V, generator=g) * 2.5
@@ -236,14 +243,14 @@ def _top_rows(seed, R, V, dtype, ties=False):
 @pytest.mark.parametrize("dtype", list(DTYPES))
 @pytest.mark.parametrize("V", [1, 2, 7, 8, 9, 100, 255, 1024, 5003, 40000])
 @pytest.mark.parametrize("k", [1, 8, 63])
-def test_top_sizes(sv, dtype, V, k):
+def test_top_sizes(sv, top_path, dtype, V, k):
     _check_top(sv, _top_rows(V + k, 3, V, dtype), k, 0.8, dtype)
 
 
 @pytest.mark.parametrize("dtype", list(DTYPES))
 @pytest.mark.parametrize("k", [128, 129, 256, 300, 513, 1000, 1024])
 @pytest.mark.parametrize("V", [1500, 33000])
-def test_top_wide_records(sv, dtype, k, V):
+def test_top_wide_records(sv, top_path, dtype, k, V):
     _check_top(sv, _top_rows(k, 2, V, dtype), k, 1.0, dtype)
 
 
@@ -251,7 +258,7 @@ def test_top_wide_records(sv, dtype, k, V):
 @pytest.mark.parametrize("kind", ["ties", "constant", "two_values", "negative_ties", "zeros"])
 @pytest.mark.parametrize("V", [60, 5000, 70000])
 @pytest.mark.parametrize("k", [5, 200])
-def test_top_ties(sv, dtype, kind, V, k):
+def test_top_ties(sv, top_path, dtype, kind, V, k):
     """Ties at the k-th value, up to rows with more ties than a slice's buffer."""
     x = _top_rows(V, 2, V, dtype, ties=True)
     if kind == "constant":
@@ -267,7 +274,7 @@ def test_top_ties(sv, dtype, kind, V, k):
 
 @pytest.mark.parametrize("dtype", list(DTYPES))
 @pytest.mark.parametrize("V", [50, 4000, 40001])
-def test_top_masked_and_bad_rows(sv, dtype, V):
+def test_top_masked_and_bad_rows(sv, top_path, dtype, V):
     x = _top_rows(4, 8, V, dtype)
     x[1, 3:] = -math.inf                                     # fewer than k tokens
     x[2] = -math.inf
@@ -282,11 +289,46 @@ def test_top_masked_and_bad_rows(sv, dtype, V):
 
 
 @pytest.mark.parametrize("T", [0.05, 1.0, 20.0])
-def test_top_temperatures_and_small_tails(sv, T):
+def test_top_temperatures_and_small_tails(sv, top_path, T):
     """A tail of 1e-30 keeps its relative accuracy."""
     x = _top_rows(6, 4, 3000, "f32")
     x[:, 7] += 60 * T
     _check_top(sv, x, 3, T, "f32")
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("k", [3, 64, 700])
+@pytest.mark.parametrize("kind", ["rising", "falling", "late", "steps"])
+def test_top_ordered_rows(sv, top_path, dtype, k, kind):
+    """Rows whose order makes every step bring better tokens than the last."""
+    V = 60001
+    x = torch.sort(_top_rows(k, 2, V, "f32"), -1).values
+    if kind == "falling":
+        x = x.flip(-1)
+    if kind == "late":
+        x = torch.cat([x[:, : V // 2].flip(-1), x[:, V // 2:]], -1)
+    if kind == "steps":
+        x = torch.floor(x * 2) / 2                           # rising, in runs of ties
+    _check_top(sv, x.to(DTYPES[dtype]), k, 1.0, dtype)
+
+
+@pytest.mark.parametrize("T", [1e-6, 1e-30, 1e30])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_top_extreme_temperatures(sv, top_path, dtype, T):
+    x = _top_rows(12, 3, 9000, dtype)
+    x[1] *= 1e20
+    x[2] = torch.finfo(x.dtype).min
+    idx, lp, tail = (_np(t) for t in sv.top_logits(x.to(DEV), 6, T))
+    want_i, want_lp, want_t = rowsref.top(_np(x), 6, T)
+    assert np.array_equal(idx, want_i)
+    # logits / T reach 1e50: float32 results beyond its range are -inf, the
+    # others are off by half a step; exponents that small weigh nothing
+    big = np.abs(want_lp) > 3.4e38
+    assert np.array_equal(np.isneginf(lp), big | np.isneginf(want_lp))
+    ok = ~np.isneginf(lp)
+    D = np.minimum(_spread(_np(x) / T), 120)[:, None]        # terms below e^-120 of the sum do not count
+    np.testing.assert_array_less(np.abs(lp - want_lp)[ok], np.broadcast_to((40 + D) * U, lp.shape)[ok] + U * np.abs(want_lp[ok]) + 1e-30)
+    assert not np.isnan(tail).any()
 
 
 def test_top_shapes_workspace_and_outputs(sv):
@@ -304,7 +346,7 @@ def test_top_shapes_workspace_and_outputs(sv):
     assert empty[0].shape == (0, 5)
 
 
-def test_top_large_rows(sv):
+def test_top_large_rows(sv, top_path):
     _check_top(sv, _top_rows(8, 1, (1 << 24) - 3, "bf16"), 50, 1.0, "bf16")
     _check_top(sv, _top_rows(9, 2, 152064, "f32"), 64, 1.0, "f32")
     _check_top(sv, _top_rows(10, 700, 9001, "bf16"), 17, 1.0, "bf16")
