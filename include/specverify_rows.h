@@ -130,8 +130,8 @@ sv_status sv_top_logits(int R, int V, const void* logits, sv_dtype dtype, int k,
  *               whose index is outside [0, V) are ignored; a token listed
  *               twice counts with both values, and once in q
  *   tail        [R] float32, or NULL: no such outcome
- *   weight      [R] float32, or NULL: 1.  A row whose weight is 0 is not read:
- *               loss 0, gradient 0.
+ *   weight      [R] float32, or NULL: 1.  A row whose weight is 0 costs no pass
+ *               over its logits and may hold anything: loss 0, gradient 0.
  *   loss        [R] float32
  *   stats       [R][SV_DISTILL_STAT_WORDS] float32 written by the forward
  *               pass for the backward pass of the same inputs

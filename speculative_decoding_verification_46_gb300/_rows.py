@@ -298,7 +298,7 @@ def distill_loss(student, indices, logprobs, tail=None, temperature=1.0, *, weig
     logprobs [..., k] float32 as top_logits returns them (indices outside the
     vocabulary are ignored); tail [...] float32 adds the outcome "any token not
     listed", None renormalises the teacher over the listed tokens; weight [...]
-    float32 scales each row's loss, and a row of weight 0 is not read.  Returns
+    float32 scales each row's loss, and a row of weight 0 may hold anything.  Returns
     the rows' losses [...] float32: weight * KL(teacher || student), both at
     `temperature`.  The gradient has the student's type.  Runs on the current
     stream.

@@ -89,8 +89,12 @@ struct DistillSmem {
 };
 
 template <typename T>
+__device__ __forceinline__ void zero_slice_of(const Window<T>& g, int v0, int v1, int first, int step) {
+  for (int v = v0 + first; v < v1; v += step) g.store(v, make_uint4(0u, 0u, 0u, 0u));
+}
+template <typename T>
 __device__ __forceinline__ void zero_slice(const Window<T>& g, int v0, int v1) {
-  for (int v = v0 + (int)threadIdx.x; v < v1; v += (int)blockDim.x) g.store(v, make_uint4(0u, 0u, 0u, 0u));
+  zero_slice_of(g, v0, v1, (int)threadIdx.x, (int)blockDim.x);
 }
 
 template <typename T, int U, bool GRAD>

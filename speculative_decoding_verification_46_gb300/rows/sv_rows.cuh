@@ -164,6 +164,12 @@ __device__ __forceinline__ int block_sum_int_w(int v, int* sm) {
   return t;
 }
 
+// 2^((x - m) c) is formed as 2^(x c - rho), rho = round(m c), one multiply-add
+// and one exponential, where |rho| stays below this: rho is then off by at
+// most half, which a factor common to all terms takes back.  Beyond it
+// (enormous logits or tiny temperatures) the difference is taken first.
+constexpr float kNear = 8.0e6f;
+
 // 2^((x - m) c) to about 44 bits, c = c.hi + c.lo; x <= m, either may be
 // -inf (0 then).  The difference keeps its rounding error.
 __device__ __forceinline__ F2 weight_f2(float x, float m, F2 c, const float* tab) {

@@ -3,6 +3,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstddef>
 #include <cstdint>
@@ -12,6 +13,7 @@
 #include "specverify_rows.h"
 #include "sv_adjust.cuh"
 #include "sv_distill.cuh"
+#include "sv_distill_pipe.cuh"
 #include "sv_toplogits.cuh"
 
 namespace {
@@ -166,11 +168,68 @@ sv_status launch_distill_u(sv::rows::DistillParams p, cudaStream_t stream) {
   return launched();
 }
 
+// The persistent form (sv_distill_pipe.cuh): as many clusters as fit at once.
+// Returns SV_ERR_UNSUPPORTED where it does not apply.
+template <typename T, bool GRAD>
+sv_status launch_distill_pipe(sv::rows::DistillParams p, cudaStream_t stream) {
+  constexpr int VW = sv::Tr<T>::VW;
+  const long long nv = ceil_div((long long)p.V + (p.V % VW ? VW - 1 : 0), VW);
+  const long long C = ceil_div(nv, sv::rows::kDpSlice);
+  if (C > sv::rows::kDiMaxC || p.k > sv::rows::kDpLi) return SV_ERR_UNSUPPORTED;
+  p.C = (int)C;
+  p.SV = (int)ceil_div(nv, C);
+  auto kern = sv::rows::distill_pipe_kernel<T, GRAD>;
+  const size_t smem = sizeof(sv::rows::DpSmem<T>);
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
+    cudaGetLastError();
+    return SV_ERR_CUDA;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)p.C);
+  cfg.blockDim = dim3(sv::rows::kDpThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)p.C;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  static std::atomic<int> fit[64][sv::rows::kDiMaxC + 1];   // clusters at once, by device and size
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SV_ERR_CUDA;
+  int clusters = fit[dev][p.C].load(std::memory_order_relaxed);
+  if (clusters == 0) {
+    if (cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg) != cudaSuccess || clusters < 1) {
+      cudaGetLastError();
+      return SV_ERR_CUDA;
+    }
+    fit[dev][p.C].store(clusters, std::memory_order_relaxed);
+  }
+  cfg.gridDim = dim3((unsigned)(std::min<long long>(clusters, p.R) * p.C));
+  if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) {
+    cudaGetLastError();
+    return SV_ERR_CUDA;
+  }
+  return launched();
+}
+
+// SPECVERIFY_PATH=distillpipe / =distillrow overrides the choice below (tests cover both).
+int distill_override() {
+  const char* e = std::getenv("SPECVERIFY_PATH");
+  return !e ? 0 : std::strcmp(e, "distillpipe") == 0 ? 1 : std::strcmp(e, "distillrow") == 0 ? 2 : 0;
+}
+
 // CTAs per row: as few as hold the row in registers (8 vectors per thread),
 // more where the rows alone would leave SMs without work, at most 8.
 template <typename T, bool GRAD>
 sv_status launch_distill(sv::rows::DistillParams p, cudaStream_t stream) {
   constexpr int VW = sv::Tr<T>::VW;
+  const int o = distill_override();
+  if (o == 1 || (o == 0 && p.R >= sm_count())) {
+    const sv_status st = launch_distill_pipe<T, GRAD>(p, stream);
+    if (st != SV_ERR_UNSUPPORTED) return st;
+  }
   const long long nv = ceil_div((long long)p.V + (p.V % VW ? VW - 1 : 0), VW);
   int C = (int)std::min<long long>(sv::rows::kDiMaxC, ceil_div(nv, sv::rows::kDiThreads * 8));
   while (C < sv::rows::kDiMaxC && (long long)p.R * C < sm_count() && ceil_div(nv, C) > sv::rows::kDiThreads) ++C;

@@ -509,8 +509,7 @@ struct TopRowSmem {
 // costs one multiply-add and one exponential; the rounding of rho leaves with
 // scale().  Terms gather in short float32 chains that take() adds to the
 // two-float total, so a row of 2^24 tokens is summed as exactly as a short
-// one.  rho that leaves the range of exact multiply-adds (enormous logits or
-// tiny temperatures) takes the difference first.
+// one.  Beyond kNear the difference is taken first.
 struct RunningSum {
   float m = -INFINITY, rho = 0.f;
   F2 s{0.f, 0.f};
@@ -523,7 +522,7 @@ struct RunningSum {
       s.lo *= f;
       m = to;
       rho = m * c;
-      far = !(fabsf(rho) < 1.0e30f);
+      far = !(fabsf(rho) < kNear);
     }
   }
   // 2^((x - m) c), x <= m

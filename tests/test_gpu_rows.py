@@ -354,6 +354,13 @@ def test_top_large_rows(sv, top_path):
 
 # ------------------------------------------------------------------ distill
 
+@pytest.fixture(params=["distillpipe", "distillrow"])
+def distill_path(request, monkeypatch):
+    """Both kernels at every size: a persistent pipeline over rows, and a cluster per row."""
+    monkeypatch.setenv("SPECVERIFY_PATH", request.param)
+    return request.param
+
+
 def _record(seed, R, V, k, tail, unique=True):
     g = torch.Generator().manual_seed(seed)
     if unique:
@@ -368,10 +375,10 @@ def _record(seed, R, V, k, tail, unique=True):
 
 def _forms(sv, S, idx, lp, tail, T, w, form):
     d = [None if t is None else t.to(DEV) for t in (idx, lp, tail, w)]
-    x = S.to(DEV)
+    x = S.to(DEV, copy=True)
     if form == "fused":
         loss, grad = sv.distill_loss_grad(x, d[0], d[1], d[2], T, weight=d[3])
-        assert torch.equal(x.cpu().view(torch.uint8), S.view(torch.uint8)), "the student was written"
+        assert torch.equal(x.view(torch.uint8), S.to(DEV).view(torch.uint8)), "the student was written"
     elif form == "inplace":
         loss, grad = sv.distill_loss_grad(x, d[0], d[1], d[2], T, weight=d[3], out_grad=x)
         assert grad is x
@@ -407,7 +414,7 @@ def _student(seed, R, V, dtype):
 @pytest.mark.parametrize("k", [1, 8])
 @pytest.mark.parametrize("tail", [False, True])
 @pytest.mark.parametrize("form", ["fused", "autograd"])
-def test_distill_sizes(sv, dtype, V, k, tail, form):
+def test_distill_sizes(sv, distill_path, dtype, V, k, tail, form):
     if tail and V <= k:
         pytest.skip("no token is left for the tail (tested by itself)")
     idx, lp, t = _record(V + k, 3, V, k, tail)
@@ -417,7 +424,7 @@ def test_distill_sizes(sv, dtype, V, k, tail, form):
 @pytest.mark.parametrize("dtype", list(DTYPES))
 @pytest.mark.parametrize("V", [40000, 70001, 152064, 300007])
 @pytest.mark.parametrize("form", ["fused", "inplace", "autograd"])
-def test_distill_large_rows(sv, dtype, V, form):
+def test_distill_large_rows(sv, distill_path, dtype, V, form):
     """Rows over several CTAs of a cluster, and beyond its registers."""
     idx, lp, t = _record(V, 2, V, 64, True)
     idx[0, :4] = torch.tensor([0, V - 1, V // 2, 32768], dtype=torch.int32)
@@ -426,7 +433,7 @@ def test_distill_large_rows(sv, dtype, V, form):
 
 @pytest.mark.parametrize("k", [33, 512, 513, 1000, 1024])
 @pytest.mark.parametrize("form", ["fused", "inplace", "autograd"])
-def test_distill_wide_records(sv, k, form):
+def test_distill_wide_records(sv, distill_path, k, form):
     idx, lp, t = _record(k, 4, 3001, k, True)
     _check_distill(sv, _student(k, 4, 3001, "bf16"), idx, lp, t, 2.0, "bf16", form=form)
 
@@ -434,7 +441,7 @@ def test_distill_wide_records(sv, k, form):
 @pytest.mark.parametrize("V", [20, 40000])
 @pytest.mark.parametrize("tail", [False, True])
 @pytest.mark.parametrize("form", ["fused", "inplace", "autograd"])
-def test_distill_tokens_listed_twice_and_ignored(sv, V, tail, form):
+def test_distill_tokens_listed_twice_and_ignored(sv, distill_path, V, tail, form):
     idx, lp, t = _record(3, 6, V, 12, tail, unique=False)
     idx[1, 4:9] = idx[1, 3]
     idx[2] = 5
@@ -444,7 +451,7 @@ def test_distill_tokens_listed_twice_and_ignored(sv, V, tail, form):
 
 @pytest.mark.parametrize("dtype", list(DTYPES))
 @pytest.mark.parametrize("form", ["fused", "inplace", "autograd"])
-def test_distill_empty_masked_and_bad_rows(sv, dtype, form):
+def test_distill_empty_masked_and_bad_rows(sv, distill_path, dtype, form):
     V, k = 2003, 6
     S = _student(2, 14, V, dtype)
     idx, lp, t = _record(2, 14, V, k, True)
@@ -473,7 +480,7 @@ def test_distill_empty_masked_and_bad_rows(sv, dtype, form):
 
 
 @pytest.mark.parametrize("form", ["fused", "inplace", "autograd"])
-def test_distill_weights(sv, form):
+def test_distill_weights(sv, distill_path, form):
     """Weight 0 rows are not read (they hold NaN) and give zeros; others scale."""
     V = 5000
     S = _student(5, 5, V, "f32")
@@ -482,7 +489,55 @@ def test_distill_weights(sv, form):
     _check_distill(sv, S, idx, lp, t, 1.0, "f32", w=w, form=form)
 
 
-def test_distill_nothing_outside_the_list(sv):
+@pytest.mark.parametrize("R, V, dtype, k", [(1000, 700, "bf16", 16), (333, 40001, "f16", 100), (200, 70000, "f32", 256),
+                                            (160, 131000, "f32", 33), (155, 152064, "bf16", 7), (40, 262143, "bf16", 64)])
+@pytest.mark.parametrize("form", ["fused", "inplace", "autograd"])
+def test_distill_many_rows(sv, distill_path, R, V, dtype, k, form):
+    """More rows than clusters fit at once, a third of them of weight 0, some
+    with nothing to learn from, tokens listed twice here and there.  Rows are
+    checked against the oracle in part (the first, the last and a spread)."""
+    S = torch.randn(R, V, generator=torch.Generator(device=DEV).manual_seed(1), device=DEV).mul_(2.5).to(DTYPES[dtype])
+    g = torch.Generator().manual_seed(R)
+    idx = torch.randint(0, V, (R, k), generator=g, dtype=torch.int32)
+    idx[1::7, -1] = idx[1::7, 0]
+    idx[2::11] = -1
+    lp, t = torch.randn(R, k, generator=g) * 2, torch.randn(R, generator=g) + 2
+    t[2::22] = -math.inf
+    w = torch.rand(R, generator=g) + 0.1
+    w[::3] = 0.0
+    w[R - 1] = 1.0
+    pick = torch.unique(torch.cat([torch.arange(0, 4), torch.arange(R - 4, R), torch.linspace(0, R - 1, 40).long()]))
+    want_S = S[pick.to(DEV)].cpu()
+    loss, grad = _forms(sv, S, idx, lp, t, 1.3, w, form)
+    zero = (w == 0).to(DEV)
+    assert not loss[zero].any() and not grad[zero].any()
+    want_l, want_g, scale = rowsref.distill(_np(want_S), _np(idx[pick]), _np(lp[pick]), _np(t[pick]), 1.3, _np(w[pick]))
+    s, aw = (40 + _spread(_np(want_S) / 1.3)) * U, _np(w[pick])
+    _assert_close(_np(loss)[pick], want_l, 2 * s * aw + U * (np.abs(want_l) + aw * (1 + np.abs(_np(lp[pick])).max(-1))), "loss")
+    _assert_close(_np(grad[pick.to(DEV)]), want_g, (3 * s + 16 * U)[:, None] * scale + _half(dtype) * np.abs(want_g) * (1 + 1e-3) +
+                  _tiny(dtype), "gradient")
+
+
+@pytest.mark.parametrize("T", [1e-6, 1e-30, 1e4])
+@pytest.mark.parametrize("form", ["fused", "autograd"])
+def test_distill_extreme_temperatures(sv, distill_path, T, form):
+    """Exponents out of float32's range weigh nothing; nothing becomes NaN."""
+    V = 3000
+    S = _student(3, 3, V, "f32")
+    S[1] *= 1e18
+    idx, lp, t = _record(3, 3, V, 4, True)
+    idx[:, 0] = S.argmax(-1).int()                           # the student's only mass at low temperatures
+    lp[:, 1:], t[:] = -math.inf, -math.inf                   # which is also the teacher's
+    loss, grad = _forms(sv, S, idx, lp, t, T, None, form)
+    want_l, want_g, _ = rowsref.distill(_np(S), _np(idx), _np(lp), _np(t), T)
+    # the listed token holds all the teacher's mass: loss = -ln q there, a sum's logarithm
+    s = (40 + np.minimum(_spread(_np(S) / T), 120)) * U
+    _assert_close(_np(loss), want_l, 2 * s + U * np.abs(want_l), "loss")
+    assert np.isfinite(_np(grad)).all()
+    np.testing.assert_allclose(_np(grad), want_g, rtol=0, atol=float((3 * s.max() + 32 * U) / T))
+
+
+def test_distill_nothing_outside_the_list(sv, distill_path):
     """k covers the vocabulary: without a tail mass the loss is an ordinary
     divergence, with one it is infinite (no token could carry it)."""
     S = _student(1, 2, 6, "f32")
@@ -492,7 +547,7 @@ def test_distill_nothing_outside_the_list(sv):
     _check_distill(sv, S, idx, lp, t, 1.0, "f32", form="autograd")
 
 
-def test_distill_upstream_gradients_and_shapes(sv):
+def test_distill_upstream_gradients_and_shapes(sv, distill_path):
     """Row gradients of any size reach the student, also as an expanded view."""
     V = 900
     S = _student(8, 6, V, "f32").view(2, 3, V)
@@ -513,7 +568,7 @@ def test_distill_upstream_gradients_and_shapes(sv):
     assert e.shape == (0, 3)
 
 
-def test_distill_gradient_against_differences(sv):
+def test_distill_gradient_against_differences(sv, distill_path):
     """The gradient against differences of the library's own loss (float32):
     with step e the quotient is off by at most 2 (loss error) / (2 e) plus
     e^2 / 6 of a third derivative below 1 / T^3."""
