@@ -2,29 +2,29 @@
 // row, so that loading, summing, exchanging and writing overlap between
 // neighbouring rows instead of following one another within each.
 //
-// Per CTA, 16 streaming warps own the CTA's slice of every row through a ring
-// of kDpStages cp.async stages private to each thread (a thread reads back
-// only what it copied), and 8 list warps own what the teacher's list needs,
-// one listed token per thread.  In iteration t
+// The warps of a CTA have four roles and meet only where one needs what
+// another made (named barriers, two of each in turn; no spinning):
 //
-//   A  streaming warps: row t without its listed tokens -> (maximum, sum) per warp
-//      list warp 0:     row t - 1's statistics from the parts of all C CTAs
-//   -- block barrier
-//   B  streaming warps: row t - 1's gradient, out of the ring; row t + 2 into it
-//      list warps:      row t's part to all CTAs (one cluster barrier, waited
-//                       for at the end of the iteration); the listed tokens of
-//                       row t - 2 on top of its gradient, and its loss; the
-//                       list of row t + 2, whose loads were issued an
-//                       iteration earlier
+//   streaming (16 warps)  own the CTA's slice of every row through a ring of
+//       kDpStages cp.async stages private to each thread (a thread reads back
+//       only what it copied).  Per row t: sum the slice without its listed
+//       tokens to (maximum, sum); then write row t - 1's gradient out of the
+//       ring and start loading row t + 2 into the stage that frees.
+//   list (1 warp per 32 listed tokens)  a listed token per thread: the
+//       teacher's softmax and the student's weights there (two-float), the
+//       bitmap that takes the tokens out of the streams, and at the end the
+//       tokens' own gradient on top of the dense one.  The loads of a list
+//       are issued one row before they are used.
+//   exchange (1 warp)  the CTA's part of row t to all CTAs of the cluster (one
+//       cluster barrier per row) and from the C parts the row's statistics.
+//   loss (1 warp)  three logarithms per row.
 //
-// so every dependent chain (the gather of the listed tokens, the two-float
-// sums, the exchange, the float64 logarithms of the loss) has at least half an
-// iteration in which the streaming warps have work of their own.  The forward
-// pass alone has no B for the streaming warps; there the cluster barrier is
-// waited for at the end of the next A.
+// So every dependent chain - gather, two-float sums, exchange, logarithms -
+// has a whole row's streaming time to finish in.  The forward pass alone is
+// the same without the gradient.
 //
-// Bound: HBM, with the exponentials close behind (two per element at 16 per
-// clock and SM: 77 % of the time the bytes of a bf16 row take).
+// Bound: HBM, with instruction issue close behind (about 100 warp
+// instructions per 32 vectors of 16 bytes read and written).
 #pragma once
 
 #include "sv_distill.cuh"
@@ -33,17 +33,21 @@ namespace sv {
 namespace rows {
 
 constexpr int kDpSt = 512;              // streaming threads
-constexpr int kDpLi = 256;              // list threads: the largest list
-constexpr int kDpThreads = kDpSt + kDpLi;
+constexpr int kDpStWarps = kDpSt / 32;
+constexpr int kDpLi = 256;              // most list threads: the largest list
+constexpr int kDpMaxThreads = kDpSt + 32 + kDpLi + 32;
 constexpr int kDpU = 8;                 // vectors per streaming thread and row
 constexpr int kDpSlice = kDpSt * kDpU;  // vectors per CTA and row
 constexpr int kDpStages = 3;
 constexpr int kDpLists = 6;             // rows whose lists are alive
 
+// threads of a CTA for lists of k tokens
+__host__ __device__ constexpr int dp_threads(int k) { return kDpSt + 32 + (k + 31) / 32 * 32 + 32; }
+
 struct DpList {
   int sid[kDpLi];                       // listed tokens (-1: ignored)
   float sw[kDpLi], sq[kDpLi];           // the teacher's and the student's weights
-  float tm, km, ltail, wgt;
+  float tm, km, ltail, wgt, sc;         // sc = wgt / temperature
   F2 Z, WK, E1, wt;
   int live;                             // 0: weight 0, 1: nothing to learn from, 2: a row
   int infinite, twice;
@@ -57,17 +61,60 @@ template <typename T>
 struct DpSmem {
   uint4 ring[kDpStages][kDpU][kDpSt];
   uint32_t bits[2][kDpSlice * Tr<T>::VW / 32];
+  uint2 dirty[2][kDpStWarps];           // a byte per (warp, u): some vector there holds a listed token
   DpList list[kDpLists];
   DpStat stat[kDpLists];
-  float4 part[3][kDiMaxC];              // a row's parts: read while the next row's may be arriving
-  float4 wpart[2][kDpSt / 32];
+  float4 part[2][kDiMaxC];
+  float4 wpart[2][kDpStWarps];
   F2 lsum[kDpLi / 32][3];
   float2 lmax[kDpLi / 32];
   float tab[128];
 };
 
-__device__ __forceinline__ void list_barrier() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
-static_assert(kDpLi == 256, "list_barrier");
+// Named barriers: each pair alternates by row, so that the side that only
+// announces may be a row ahead of the side that waits.
+enum { DP_SUMMED = 1, DP_STAT = 3, DP_WRITTEN = 5, DP_LISTED = 7, DP_LIST = 9 };
+__device__ __forceinline__ void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
+__device__ __forceinline__ void bar_arrive(int id, int n) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(n) : "memory"); }
+
+// ln a to about 40 bits, a a normalised two-float number >= 2^-100: a float
+// logarithm y corrected by a e^-y - 1.
+__device__ __forceinline__ F2 f2_log(F2 a, const float* tab) {
+  const float y = logf(a.hi);
+  const F2 e = exp2_f2(f2_mul(F2{-y, 0.f}, F2{kLog2eHi, kLog2eLo}), tab);
+  const F2 r = f2_add(f2_mul(a, f2_norm(e.hi, e.lo)), F2{-1.f, 0.f});
+  return f2_add(F2{y, 0.f}, f2_norm(r.hi, r.lo - 0.5f * r.hi * r.hi));
+}
+
+// a - b with its rounding error
+__device__ __forceinline__ F2 two_diff(float a, float b) {
+  const float d = a - b;
+  const float bb = d - a;
+  return F2{d, (a - (d - bb)) + (-b - bb)};
+}
+
+// The largest element of U vectors (NaN are passed over).
+template <typename T, int U>
+__device__ __forceinline__ float max_of(const uint4 (&x)[U]) {
+  if (sizeof(T) == 4) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < U; ++u) m = fmaxf(m, Tr<T>::template vmax<false>(x[u]));
+    return m;
+  }
+  // packed: two elements an instruction
+  using P = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+  P m = *reinterpret_cast<const P*>(&x[0].x);
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    m = __hmax2(m, *reinterpret_cast<const P*>(&x[u].x));
+    m = __hmax2(m, *reinterpret_cast<const P*>(&x[u].y));
+    m = __hmax2(m, *reinterpret_cast<const P*>(&x[u].z));
+    m = __hmax2(m, *reinterpret_cast<const P*>(&x[u].w));
+  }
+  const float lo = __low2float(m), hi = __high2float(m);
+  return fmaxf(lo, hi);
+}
 
 // The statistics of a row from the C parts (one warp; lane 0 writes).
 __device__ __forceinline__ void dp_statistics(const float4* part, int C, const DpList& L, int k, F2 c, const float* tab,
@@ -95,8 +142,10 @@ __device__ __forceinline__ void dp_statistics(const float4* part, int C, const D
   if (lane == 0) {
     const float km = L.km;
     const float M = fmaxf(mt, km);
-    const F2 Et = mt == M ? F2{1.f, 0.f} : weight_f2(mt, M, c, tab);
-    const F2 Ek = km == M ? F2{1.f, 0.f} : weight_f2(km, M, c, tab);
+    // one of the two maxima is M
+    const F2 E = mt == km ? F2{1.f, 0.f} : weight_f2(fminf(mt, km), M, c, tab);
+    const F2 Et = mt == M ? F2{1.f, 0.f} : E;
+    const F2 Ek = km == M ? F2{1.f, 0.f} : E;
     const F2 S = f2_add(mt == M ? st : f2_mul(st, Et), km == M ? WK : f2_mul(WK, Ek));
     const bool good = S.hi > 0.f && S.hi < INFINITY;
     const float nan = __uint_as_float(0x7fffffffu);
@@ -121,30 +170,32 @@ __device__ __forceinline__ void dp_statistics(const float4* part, int C, const D
 }
 
 // The loss of a row (one warp: the three logarithms side by side).
-__device__ __forceinline__ void dp_loss(const DpList& L, const DpStat& s, double inv_t, float* loss) {
+__device__ __forceinline__ void dp_loss(const DpList& L, const DpStat& s, double inv_t, const float* tab, float* loss) {
   const int lane = threadIdx.x & 31;
   if (L.live != 2) {
     if (lane == 0) *loss = 0.f;
     return;
   }
   const F2 mine = lane == 0 ? L.Z : lane == 1 ? s.S : s.st;
-  const double lg = log(f2_double(mine));
-  const double lz = __shfl_sync(0xffffffffu, lg, 0), ls = __shfl_sync(0xffffffffu, lg, 1),
-               lt = __shfl_sync(0xffffffffu, lg, 2);
+  const F2 lg = mine.hi > 0.f ? f2_log(mine, tab) : F2{-INFINITY, 0.f};
+  const F2 lz{__shfl_sync(0xffffffffu, lg.hi, 0), __shfl_sync(0xffffffffu, lg.lo, 0)};
+  const F2 ls{__shfl_sync(0xffffffffu, lg.hi, 1), __shfl_sync(0xffffffffu, lg.lo, 1)};
+  const F2 lt{__shfl_sync(0xffffffffu, lg.hi, 2), __shfl_sync(0xffffffffu, lg.lo, 2)};
   if (lane == 0) {
     const double kr = L.km == -INFINITY ? 0.0 : (double)L.km;
     double e = f2_double(L.E1);
     if (L.wt.hi != 0.f)
-      e += f2_double(L.wt) * (((double)L.ltail - (double)L.tm) - (((double)s.mt - kr) * inv_t + lt));
-    double l = e / f2_double(L.Z) - lz + ls + ((double)s.M - kr) * inv_t;
+      e += f2_double(L.wt) * (((double)L.ltail - (double)L.tm) - (((double)s.mt - kr) * inv_t + f2_double(lt)));
+    double l = e / f2_double(L.Z) - f2_double(lz) + f2_double(ls) + ((double)s.M - kr) * inv_t;
     if (!(s.S.hi > 0.f && s.S.hi < INFINITY)) l = __longlong_as_double(0x7fffffffffffffffll);
     else if (L.infinite && l == l) l = (double)INFINITY;
     *loss = (float)((double)L.wgt * l);
   }
 }
 
-template <typename T, bool GRAD>
-__global__ void __launch_bounds__(kDpThreads, 1) distill_pipe_kernel(const DistillParams p) {
+// WHOLE: V is a multiple of the vector width, so every row is whole vectors.
+template <typename T, bool GRAD, bool WHOLE>
+__global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const DistillParams p) {
   using TR = Tr<T>;
   constexpr int VW = TR::VW;
   extern __shared__ __align__(16) unsigned char smem_raw[];
@@ -154,196 +205,108 @@ __global__ void __launch_bounds__(kDpThreads, 1) distill_pipe_kernel(const Disti
   const int g = blockIdx.x / C, NG = gridDim.x / C;
   const int n = (p.R - g + NG - 1) / NG;            // rows of this cluster: g, g + NG, ...
   const int k = p.k;
+  const int nl = (k + 31) / 32 * 32;                // list threads
   const F2 c{p.c, p.c_lo};
-  const bool streaming = tid < kDpSt;
   const T* student = static_cast<const T*>(p.student);
-  cluster_arrive();                                 // waited for before the first push: every CTA has started
+  // barrier sizes
+  const int n_summed = kDpSt + 32, n_stat = kDpSt + 32, n_written = kDpSt + nl + 32, n_listed = nl + kDpSt + 32;
+  // the CTA's vectors of a row [v0, v1)
+  auto slice = [&](int nv, int* v0, int* v1) {
+    *v0 = min(rank * p.SV, nv);
+    *v1 = min(*v0 + p.SV, nv);
+  };
 
-  // ---- streaming warps: the ring
-  auto issue = [&](int i) {                         // row i of the cluster into its stage
-    if (i < n) {
-      const int r = g + i * NG;
-      if (!p.weight || __ldg(p.weight + r) != 0.f) {
-        const Window<T, const T> win(student, (size_t)r, p.V);
-        const int v0 = min(rank * p.SV, win.vectors()), v1 = min(v0 + p.SV, win.vectors());
-        uint4(*st)[kDpSt] = sm.ring[i % kDpStages];
+  for (int i = tid; i < 128; i += blockDim.x) sm.tab[i] = i < 64 ? __ldg(kExp2Hi + i) : __ldg(kExp2Lo + i - 64);
+  __syncthreads();
+  cluster_arrive();
+  cluster_wait();                                   // every CTA of the cluster runs: its shared memory can be written
+
+  if (warp < kDpStWarps) {
+    // ================================================================ streaming
+    int v0 = 0, v1 = 0;
+    if (WHOLE) slice(p.V / VW, &v0, &v1);
+    int mine = (v1 - v0 - tid + kDpSt - 1) / kDpSt;  // vectors of this thread in a row (WHOLE)
+    const size_t nvr = (size_t)(p.V / VW);           // vectors from row to row (WHOLE)
+    float w_next = p.weight ? __ldg(p.weight + g) : 1.f;
+    auto issue = [&](int i) {                       // row i of the cluster into its stage
+      if (i < n) {
+        const int r = g + i * NG;
+        uint4* st = &sm.ring[i % kDpStages][0][tid];
+        if (w_next != 0.f) {
+          if (WHOLE) {
+            const uint4* src = reinterpret_cast<const uint4*>(student) + (size_t)r * nvr + v0 + tid;
+            const unsigned sa = (unsigned)__cvta_generic_to_shared(st);
 #pragma unroll
-        for (int u = 0; u < kDpU; ++u) {
-          const int v = v0 + u * kDpSt + tid;
-          if (v < v1) {
-            if (win.whole(v)) {
-              const unsigned sa = (unsigned)__cvta_generic_to_shared(&st[u][tid]);
-              asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(sa), "l"(win.base + (size_t)v * VW) : "memory");
-            } else {
-              st[u][tid] = win.load(v);
+            for (int u = 0; u < kDpU; ++u)
+              if (u < mine)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(sa + u * kDpSt * 16), "l"(src + u * kDpSt) : "memory");
+          } else {
+            const Window<T, const T> win(student, (size_t)r, p.V);
+            int w0, w1;
+            slice(win.vectors(), &w0, &w1);
+#pragma unroll
+            for (int u = 0; u < kDpU; ++u) {
+              const int v = w0 + u * kDpSt + tid;
+              if (v < w1) {
+                if (win.whole(v)) {
+                  const unsigned sa = (unsigned)__cvta_generic_to_shared(st + u * kDpSt);
+                  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(sa), "l"(win.base + (size_t)v * VW) : "memory");
+                } else {
+                  st[u * kDpSt] = win.load(v);
+                }
+              }
             }
           }
         }
+        if (p.weight && i + 1 < n) w_next = __ldg(p.weight + r + NG);
       }
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  };
-
-  // ---- list warps: a listed token per thread, loads an iteration ahead of their use
-  const int lt = tid - kDpSt, lw = lt >> 5;
-  int id1 = -1, id2 = -1;                           // of the row whose student value is loaded, and of the next
-  float lp1 = -INFINITY, lp2 = -INFINITY, s1 = -INFINITY;
-  auto load_list = [&](int i, int& id, float& lp) {
-    id = -1;
-    lp = -INFINITY;
-    if (i < n && lt < k) {
-      const size_t r = g + (size_t)i * NG;
-      const int v = __ldg(p.indices + r * k + lt);
-      if ((unsigned)v < (unsigned)p.V) id = v;
-      lp = __ldg(p.logprobs + r * k + lt);
-    }
-  };
-  auto load_student = [&](int i, int id) {
-    if (id < 0) return -INFINITY;
-    return Elem<T>::load(student + ((size_t)g + (size_t)i * NG) * p.V + id);
-  };
-  // the list of row i from (id1, lp1, s1)
-  auto prepare = [&](int i) {
-    if (i >= n) return;                             // the same for all list threads
-    const int r = g + i * NG;
-    DpList& L = sm.list[i % kDpLists];
-    uint32_t* bits = sm.bits[i & 1];
-    for (int w = lt; w < kDpSlice * VW / 32; w += kDpLi) bits[w] = 0u;
-    const float wgt = p.weight ? __ldg(p.weight + r) : 1.f;
-    const float ltail = p.tail ? __ldg(p.tail + r) : -INFINITY;
-    if (lt == 0) L.infinite = L.twice = 0;
-    const bool on = id1 >= 0;
-    const float lp = on ? lp1 : -INFINITY, s = on ? s1 : -INFINITY;
-    float tm = lp != lp ? INFINITY : lp, km = s;    // a NaN makes the maximum +inf, and the row NaN
-#pragma unroll
-    for (int m = 16; m >= 1; m >>= 1) {
-      tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, m));
-      km = fmaxf(km, __shfl_xor_sync(0xffffffffu, km, m));
-    }
-    if (lane == 0) sm.lmax[lw] = make_float2(tm, km);
-    list_barrier();
-    tm = ltail != ltail ? INFINITY : ltail;
-    km = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kDpLi / 32; ++w) {
-      tm = fmaxf(tm, sm.lmax[w].x);
-      km = fmaxf(km, sm.lmax[w].y);
-    }
-    const F2 l2e{kLog2eHi, kLog2eLo};
-    F2 w{0.f, 0.f}, ws{0.f, 0.f}, e1{0.f, 0.f};
-    if (lw * 32 < k) {                              // warps with listed tokens
-      const float kr = km == -INFINITY ? 0.f : km;
-      if (on) {
-        w = weight_f2(lp, tm, l2e, sm.tab);
-        ws = weight_f2(s, km, c, sm.tab);
-        if (w.hi != 0.f) {
-          if (s == -INFINITY) {
-            L.infinite = 1;
-          } else {
-            e1 = f2_mul(w, f2_from(((double)lp - (double)tm) - ((double)s - (double)kr) * p.inv_t));
-          }
-        }
-        const Window<T, const T> win(student, (size_t)r, p.V);
-        const int v0 = min(rank * p.SV, win.vectors()), v1 = min(v0 + p.SV, win.vectors());
-        const int o = id1 + win.a0 - v0 * VW;
-        if (o >= 0 && o < (v1 - v0) * VW) {
-          const uint32_t bit = 1u << (o & 31);
-          if (atomicOr(&bits[o >> 5], bit) & bit) L.twice = 1;
-        }
-      }
-      const F2 a = warp_sum_f2(w), b = warp_sum_f2(ws), d = warp_sum_f2(e1);
-      if (lane == 0) {
-        sm.lsum[lw][0] = a;
-        sm.lsum[lw][1] = b;
-        sm.lsum[lw][2] = d;
-      }
-    }
-    L.sid[lt] = id1;
-    L.sw[lt] = w.hi;
-    L.sq[lt] = ws.hi;
-    list_barrier();
-    if (lw == 1) {                                  // (warp 0 has the exchange to do)
-      F2 a{0.f, 0.f}, b{0.f, 0.f}, d{0.f, 0.f};
-      if (lane < (k + 31) / 32) {
-        a = sm.lsum[lane][0];
-        b = sm.lsum[lane][1];
-        d = sm.lsum[lane][2];
-      }
-#pragma unroll
-      for (int m = kDpLi / 64; m >= 1; m >>= 1) {
-        a = f2_add(a, f2_shfl_xor(a, m));
-        b = f2_add(b, f2_shfl_xor(b, m));
-        d = f2_add(d, f2_shfl_xor(d, m));
-      }
-      if (lane == 0) {
-        const F2 wt = p.tail ? weight_f2(ltail, tm, l2e, sm.tab) : F2{0.f, 0.f};
-        L.Z = f2_add(a, wt);
-        L.WK = b;
-        L.E1 = d;
-        L.wt = wt;
-        L.tm = tm;
-        L.km = km;
-        L.ltail = ltail;
-        L.wgt = wgt;
-        L.live = wgt == 0.f ? 0 : tm > -INFINITY ? 2 : 1;
-      }
-    }
-  };
-
-  for (int i = tid; i < 128; i += kDpThreads) sm.tab[i] = i < 64 ? __ldg(kExp2Hi + i) : __ldg(kExp2Lo + i - 64);
-  __syncthreads();
-  if (streaming) {
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
     issue(0);
     issue(1);
     if (!GRAD) issue(2);
-  } else {
-#pragma unroll 1
-    for (int i = 0; i < 2; ++i) {
-      load_list(i, id1, lp1);
-      s1 = load_student(i, id1);
-      prepare(i);
-      list_barrier();
-    }
-    load_list(2, id1, lp1);
-    s1 = load_student(2, id1);
-    load_list(3, id2, lp2);
-  }
-  cluster_wait();                                   // every CTA of the cluster has started
-  __syncthreads();
 
 #pragma unroll 1
-  for (int t = 0; t <= n + 1; ++t) {                // (the last row's list and loss come two iterations later)
-    // ---------------------------------------------------------------- A
-    if (streaming) {
+    for (int t = 0; t <= n; ++t) {
       if (t < n) {
+        // ---- row t without its listed tokens
         asm volatile("cp.async.wait_group %0;" ::"n"(GRAD ? 1 : 2) : "memory");
+        bar_sync(DP_LISTED + (t & 1), n_listed);
         if (sm.list[t % kDpLists].live != 0) {
-          const int r = g + t * NG;
-          const Window<T, const T> win(student, (size_t)r, p.V);
-          const int v0 = min(rank * p.SV, win.vectors()), v1 = min(v0 + p.SV, win.vectors());
-          const uint4(*st)[kDpSt] = sm.ring[t % kDpStages];
-          const unsigned char* bits = reinterpret_cast<const unsigned char*>(sm.bits[t & 1]);
+          const uint4* st = &sm.ring[t % kDpStages][0][tid];
+          int m_t = mine;
+          if (!WHOLE) {
+            const Window<T, const T> win(student, (size_t)(g + t * NG), p.V);
+            int w0, w1;
+            slice(win.vectors(), &w0, &w1);
+            m_t = (w1 - w0 - tid + kDpSt - 1) / kDpSt;
+          }
           uint4 x[kDpU];
-          float m = -INFINITY;
 #pragma unroll
           for (int u = 0; u < kDpU; ++u) {
-            const int lv = u * kDpSt + tid;
             x[u] = make_uint4(TR::kPadWord, TR::kPadWord, TR::kPadWord, TR::kPadWord);
-            if (v0 + lv < v1) x[u] = st[u][tid];
-            const uint32_t b = VW == 8 ? bits[lv] : (bits[lv >> 1] >> ((lv & 1) * 4)) & 15u;
-            if (b) {
-#pragma unroll
-              for (int e = 0; e < VW; ++e)
-                if ((b >> e) & 1u) TR::put(x[u], e, Elem<T>::kNegInf);
-            }
-            m = fmaxf(m, TR::template vmax<false>(x[u]));
+            if (u < m_t) x[u] = st[u * kDpSt];
           }
+          const uint2 dirty = sm.dirty[t & 1][warp];
+          if (dirty.x | dirty.y) {
+            const unsigned char* bits = reinterpret_cast<const unsigned char*>(sm.bits[t & 1]);
+#pragma unroll
+            for (int u = 0; u < kDpU; ++u) {
+              if (((u < 4 ? dirty.x : dirty.y) >> (8 * (u & 3))) & 0xffu) {
+                const int lv = u * kDpSt + tid;
+                const uint32_t b = VW == 8 ? bits[lv] : (bits[lv >> 1] >> ((lv & 1) * 4)) & 15u;
+#pragma unroll
+                for (int e = 0; e < VW; ++e)
+                  if ((b >> e) & 1u) TR::put(x[u], e, Elem<T>::kNegInf);
+              }
+            }
+          }
+          float m = max_of<T, kDpU>(x);
 #pragma unroll
           for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
           const float ref = m == -INFINITY ? 0.f : m, rho = ref * p.c;
           float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f, fix = 1.f;
           if (fabsf(rho) < kNear) {
-            // one multiply-add and one exponential a term; the rounding of rho leaves at the end
             fix = ex2_approx(-fmaf(ref, p.c, -rho));
 #pragma unroll
             for (int u = 0; u < kDpU; ++u)
@@ -354,7 +317,7 @@ __global__ void __launch_bounds__(kDpThreads, 1) distill_pipe_kernel(const Disti
                 a2 += ex2_approx(fmaf(TR::get(x[u], e + 2), p.c, -rho));
                 a3 += ex2_approx(fmaf(TR::get(x[u], e + 3), p.c, -rho));
               }
-          } else {                                  // enormous logits or a tiny temperature: the difference first
+          } else {
 #pragma unroll
             for (int u = 0; u < kDpU; ++u) {
 #pragma unroll 1
@@ -365,47 +328,48 @@ __global__ void __launch_bounds__(kDpThreads, 1) distill_pipe_kernel(const Disti
           s = f2_mul(warp_sum_f2(s), F2{fix, 0.f});
           if (lane == 0) sm.wpart[t & 1][warp] = make_float4(m, s.hi, s.lo, 0.f);
         }
+        bar_arrive(DP_SUMMED + (t & 1), n_summed);
+        if (!GRAD) issue(t + 3);
       }
-      if (!GRAD) issue(t + 3);
-    } else if (GRAD && lw == 0 && t >= 1 && t - 1 < n) {
-      dp_statistics(sm.part[(t - 1) % 3], C, sm.list[(t - 1) % kDpLists], k, c, sm.tab, sm.stat[(t - 1) % kDpLists], nullptr);
-    }
-    if (!GRAD && t >= 1) cluster_wait();            // row t - 1's parts are in
-    __syncthreads();
-    // ---------------------------------------------------------------- B
-    if (streaming) {
-      cluster_arrive();
-      if (GRAD) {
-        if (t >= 1 && t - 1 < n) {
-          const int i = t - 1, r = g + i * NG;
-          const Window<T> gwin(static_cast<T*>(p.grad), (size_t)r, p.V);
-          const int v0 = min(rank * p.SV, gwin.vectors()), v1 = min(v0 + p.SV, gwin.vectors());
+      // (the cluster barrier of row t - 1 is long complete; the exchange warp is who needs it)
+      if (t >= 1) cluster_wait();
+      if (t < n) cluster_arrive();
+      if (t >= 1) {
+        // ---- row t - 1's gradient
+        const int i = t - 1;
+        bar_sync(DP_STAT + (i & 1), n_stat);
+        if (GRAD) {
+          const int r = g + i * NG;
           const DpList& L = sm.list[i % kDpLists];
-          const uint4(*st)[kDpSt] = sm.ring[i % kDpStages];
+          const uint4* st = &sm.ring[i % kDpStages][0][tid];
           const bool row = L.live == 2;
-          const float mt = row ? sm.stat[i % kDpLists].mt : 0.f, rho = mt * p.c;
-          float gA = row ? (float)((double)L.wgt * p.inv_t) * sm.stat[i % kDpLists].A : 0.f;
+          const float mt = sm.stat[i % kDpLists].mt, rho = mt * p.c;
+          float gA = L.sc * sm.stat[i % kDpLists].A;
+          const Window<T> gwin(static_cast<T*>(p.grad), (size_t)r, p.V);
+          int w0 = v0, w1 = v1;
+          if (!WHOLE) slice(gwin.vectors(), &w0, &w1);
           if (!row) {
-            zero_slice_of(gwin, v0, v1, tid, kDpSt);
+            zero_slice_of(gwin, w0, w1, tid, kDpSt);
           } else if (fabsf(rho) < kNear) {
             gA *= ex2_approx(-fmaf(mt, p.c, -rho));
+            uint4* dst = reinterpret_cast<uint4*>(p.grad) + (size_t)r * nvr + v0 + tid;
 #pragma unroll
             for (int u = 0; u < kDpU; ++u) {
-              const int v = v0 + u * kDpSt + tid;
-              if (v < v1) {
-                const uint4 x = st[u][tid];
+              if (WHOLE ? u < mine : w0 + u * kDpSt + tid < w1) {
+                const uint4 x = st[u * kDpSt];
                 float gr[VW];
 #pragma unroll
                 for (int e = 0; e < VW; ++e) gr[e] = gA * ex2_approx(fmaf(TR::get(x, e), p.c, -rho));
-                gwin.store(v, Elem<T>::pack(gr));
+                if (WHOLE) __stcs(dst + u * kDpSt, Elem<T>::pack(gr));
+                else gwin.store(w0 + u * kDpSt + tid, Elem<T>::pack(gr));
               }
             }
           } else {
 #pragma unroll 1
             for (int u = 0; u < kDpU; ++u) {
-              const int v = v0 + u * kDpSt + tid;
-              if (v < v1) {
-                const uint4 x = st[u][tid];
+              const int v = w0 + u * kDpSt + tid;
+              if (v < w1) {
+                const uint4 x = st[u * kDpSt];
                 float gr[VW];
 #pragma unroll
                 for (int e = 0; e < VW; ++e) gr[e] = gA * ex2_approx((TR::get(x, e) - mt) * p.c);
@@ -414,70 +378,195 @@ __global__ void __launch_bounds__(kDpThreads, 1) distill_pipe_kernel(const Disti
             }
           }
         }
-        issue(t + 2);
+        __threadfence_block();
+        bar_arrive(DP_WRITTEN + (i & 1), n_written);
       }
-    } else {
-      if (lw == 0) {
-        if (t < n && sm.list[t % kDpLists].live != 0) {
-          // the CTA's part of row t: 16 warps' (maximum, sum)
-          const float4 v = lane < kDpSt / 32 ? sm.wpart[t & 1][lane] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
-          float m = v.x;
+      if (GRAD) issue(t + 2);
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+  } else if (warp == kDpStWarps) {
+    // ================================================================ exchange
+#pragma unroll 1
+    for (int t = 0; t < n; ++t) {
+      bar_sync(DP_LISTED + (t & 1), n_listed);
+      bar_sync(DP_SUMMED + (t & 1), n_summed);
+      const DpList& L = sm.list[t % kDpLists];
+      if (L.live != 0) {
+        const float4 v = lane < kDpStWarps ? sm.wpart[t & 1][lane] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+        float m = v.x;
 #pragma unroll
-          for (int o = 8; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-          m = __shfl_sync(0xffffffffu, m, 0);
-          F2 s{v.y, v.z};
-          if (v.x != m) s = v.x == -INFINITY ? F2{0.f, 0.f} : f2_mul(s, weight_f2(v.x, m, c, sm.tab));
-          if (lane >= kDpSt / 32) s = F2{0.f, 0.f};
+        for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        F2 s{v.y, v.z};
+        if (v.x != m) s = v.x == -INFINITY ? F2{0.f, 0.f} : f2_mul(s, weight_f2(v.x, m, c, sm.tab));
+        s = warp_sum_f2(s);
+        if (lane < C) push_f4(&sm.part[t & 1][rank], lane, make_float4(m, s.hi, s.lo, L.twice ? 1.f : 0.f));
+      }
+      __syncwarp();
+      cluster_arrive();
+      cluster_wait();
+      dp_statistics(sm.part[t & 1], C, L, k, c, sm.tab, sm.stat[t % kDpLists],
+                    !GRAD && rank == 0 && p.stats ? p.stats + (size_t)(g + t * NG) * 8 : nullptr);
+      __syncwarp();
+      bar_arrive(DP_STAT + (t & 1), n_stat);
+    }
+  } else if (warp == kDpStWarps + 1 + nl / 32) {
+    // ================================================================ loss
+#pragma unroll 1
+    for (int j = 0; j <= n + 1; ++j) {
+      if (j >= 1 && j <= n) cluster_wait();
+      if (j < n) cluster_arrive();
+      if (j >= 2) {
+        const int i = j - 2;
+        bar_sync(DP_WRITTEN + (i & 1), n_written);
+        if (rank == 0) dp_loss(sm.list[i % kDpLists], sm.stat[i % kDpLists], p.inv_t, sm.tab, p.loss + g + i * NG);
+      }
+    }
+  } else {
+    // ================================================================ list
+    const int lt = tid - kDpSt - 32, lw = lt >> 5;  // lt < nl
+    const F2 inv_t = f2_from(p.inv_t);
+    const F2 l2e{kLog2eHi, kLog2eLo};
+    int id1, id2;                                   // of the row whose student value is loaded, and of the next
+    float lp1, lp2, s1;
+    float wg1 = 1.f, tl1 = -INFINITY;               // the row's weight and tail
+    auto load_list = [&](int i, int& id, float& lp) {
+      id = -1;
+      lp = -INFINITY;
+      if (i < n && lt < k) {
+        const size_t r = (size_t)g + (size_t)i * NG;
+        const int v = __ldg(p.indices + r * k + lt);
+        if ((unsigned)v < (unsigned)p.V) id = v;
+        lp = __ldg(p.logprobs + r * k + lt);
+      }
+    };
+    auto load_student = [&](int i, int id) {
+      if (id < 0) return -INFINITY;
+      return Elem<T>::load(student + ((size_t)g + (size_t)i * NG) * p.V + id);
+    };
+    auto load_row = [&](int i) {
+      if (i < n) {
+        const int r = g + i * NG;
+        if (p.weight) wg1 = __ldg(p.weight + r);
+        if (p.tail) tl1 = __ldg(p.tail + r);
+      }
+    };
+    load_list(0, id1, lp1);
+    s1 = load_student(0, id1);
+    load_list(1, id2, lp2);
+    load_row(0);
+
+#pragma unroll 1
+    for (int j = 0; j <= n + 1; ++j) {
+      if (j < n) {
+        // ---- the list of row j
+        const float lp = id1 >= 0 ? lp1 : -INFINITY, s = s1, wgt = wg1, ltail = tl1;
+        const int id = id1;
+        id1 = id2;
+        lp1 = lp2;
+        s1 = load_student(j + 1, id1);
+        load_list(j + 2, id2, lp2);
+        load_row(j + 1);
+        DpList& L = sm.list[j % kDpLists];
+        uint32_t* bits = sm.bits[j & 1];
+        unsigned char* dirty = reinterpret_cast<unsigned char*>(sm.dirty[j & 1]);
+        for (int w = lt; w < kDpSlice * VW / 128; w += nl) reinterpret_cast<uint4*>(bits)[w] = make_uint4(0u, 0u, 0u, 0u);
+        if (lt < kDpStWarps * 8 / 4) reinterpret_cast<uint32_t*>(dirty)[lt] = 0u;
+        if (lt == 0) L.infinite = L.twice = 0;
+        float tm = lp != lp ? INFINITY : lp, km = s;  // a NaN makes the maximum +inf, and the row NaN
 #pragma unroll
-          for (int o = 8; o >= 1; o >>= 1) s = f2_add(s, f2_shfl_xor(s, o));
-          s = F2{__shfl_sync(0xffffffffu, s.hi, 0), __shfl_sync(0xffffffffu, s.lo, 0)};
-          if (lane < C)
-            push_f4(&sm.part[t % 3][rank], lane, make_float4(m, s.hi, s.lo, sm.list[t % kDpLists].twice ? 1.f : 0.f));
+        for (int m = 16; m >= 1; m >>= 1) {
+          tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, m));
+          km = fmaxf(km, __shfl_xor_sync(0xffffffffu, km, m));
+        }
+        if (lane == 0) sm.lmax[lw] = make_float2(tm, km);
+        bar_sync(DP_LIST, nl);
+        tm = ltail != ltail ? INFINITY : ltail;
+        for (int w = 0; w < nl / 32; ++w) {
+          tm = fmaxf(tm, sm.lmax[w].x);
+          km = fmaxf(km, sm.lmax[w].y);
+        }
+        F2 w{0.f, 0.f}, ws{0.f, 0.f}, e1{0.f, 0.f};
+        if (id >= 0) {
+          const float kr = km == -INFINITY ? 0.f : km;
+          w = weight_f2(lp, tm, l2e, sm.tab);
+          ws = weight_f2(s, km, c, sm.tab);
+          if (w.hi != 0.f) {
+            // w (ln p_j - ln q_j), up to the row's constants
+            if ((s - kr) * inv_t.hi < -1.0e30f) L.infinite = 1;
+            else e1 = f2_mul(w, f2_add(two_diff(lp, tm), f2_neg(f2_mul(two_diff(s, kr), inv_t))));
+          }
+          const Window<T, const T> win(student, (size_t)(g + j * NG), p.V);
+          int v0, v1;
+          slice(win.vectors(), &v0, &v1);
+          const int o = id + win.a0 - v0 * VW;
+          if (o >= 0 && o < (v1 - v0) * VW) {
+            const uint32_t bit = 1u << (o & 31);
+            if (atomicOr(&bits[o >> 5], bit) & bit) L.twice = 1;
+            const int lv = o / VW;                  // vector lv = u * kDpSt + thread
+            dirty[(lv % kDpSt) / 32 * 8 + lv / kDpSt] = 1;
+          }
+        }
+        L.sid[lt] = id;
+        L.sw[lt] = w.hi;
+        L.sq[lt] = ws.hi;
+        w = warp_sum_f2(w);
+        ws = warp_sum_f2(ws);
+        e1 = warp_sum_f2(e1);
+        if (lane == 0) {
+          sm.lsum[lw][0] = w;
+          sm.lsum[lw][1] = ws;
+          sm.lsum[lw][2] = e1;
+        }
+        bar_sync(DP_LIST, nl);
+        if (lt < 3) {                               // one of the three sums each
+          F2 a = sm.lsum[0][lt];
+          for (int q = 1; q < nl / 32; ++q) a = f2_add(a, sm.lsum[q][lt]);
+          if (lt == 0) {
+            const F2 wt = p.tail ? weight_f2(ltail, tm, l2e, sm.tab) : F2{0.f, 0.f};
+            L.Z = f2_add(a, wt);
+            L.wt = wt;
+            L.tm = tm;
+            L.km = km;
+            L.ltail = ltail;
+            L.wgt = wgt;
+            L.sc = wgt * inv_t.hi + wgt * inv_t.lo;
+            L.live = wgt == 0.f ? 0 : tm > -INFINITY ? 2 : 1;
+          } else if (lt == 1) {
+            L.WK = a;
+          } else {
+            L.E1 = a;
+          }
         }
         __syncwarp();
+        bar_arrive(DP_LISTED + (j & 1), n_listed);
       }
-      cluster_arrive();
-      if (!GRAD && lw == 0 && t >= 1 && t - 1 < n)
-        dp_statistics(sm.part[(t - 1) % 3], C, sm.list[(t - 1) % kDpLists], k, c, sm.tab, sm.stat[(t - 1) % kDpLists],
-                      rank == 0 && p.stats ? p.stats + (size_t)(g + (t - 1) * NG) * 8 : nullptr);
-      if (t >= 2 && t - 2 < n) {
-        const int i = t - 2, r = g + i * NG;
+      if (j >= 1 && j <= n) cluster_wait();
+      if (j < n) cluster_arrive();
+      if (j >= 2) {
+        // ---- the listed tokens of row j - 2, on top of its dense gradient
+        const int i = j - 2;
+        bar_sync(DP_WRITTEN + (i & 1), n_written);
         const DpList& L = sm.list[i % kDpLists];
-        const DpStat& s = sm.stat[i % kDpLists];
-        if (GRAD && L.live == 2 && lt < k && L.sid[lt] >= 0) {
+        if (GRAD && L.live == 2 && L.sid[lt] >= 0) {
+          const DpStat& s = sm.stat[i % kDpLists];
           const int id = L.sid[lt];
-          const Window<T> gwin(static_cast<T*>(p.grad), (size_t)r, p.V);
-          const int v0 = min(rank * p.SV, gwin.vectors()), v1 = min(v0 + p.SV, gwin.vectors());
+          const Window<T> gwin(static_cast<T*>(p.grad), (size_t)(g + i * NG), p.V);
+          int v0, v1;
+          slice(gwin.vectors(), &v0, &v1);
           const int o = id + gwin.a0;
           if (o >= v0 * VW && o < v1 * VW) {
             float w = L.sw[lt];
             if (s.twice) {
               w = 0.f;
-              for (int j = 0; j < k; ++j)
-                if (L.sid[j] == id) w += L.sw[j];
+              for (int q = 0; q < k; ++q)
+                if (L.sid[q] == id) w += L.sw[q];
             }
-            Elem<T>::store(gwin.base + o,
-                           (float)((double)L.wgt * p.inv_t) * (L.sq[lt] * (s.Es * s.invS) - w * f2_rcp(L.Z)));
+            Elem<T>::store(gwin.base + o, L.sc * (L.sq[lt] * (s.Es * s.invS) - w * f2_rcp(L.Z)));
           }
         }
-        if (rank == 0 && lw == kDpLi / 32 - 1) dp_loss(L, s, p.inv_t, p.loss + r);
       }
-      // the list of row t + 2, and the loads of the rows behind it
-      const float s2 = load_student(t + 3, id2);
-      int id3;
-      float lp3;
-      load_list(t + 4, id3, lp3);
-      prepare(t + 2);
-      id1 = id2;
-      lp1 = lp2;
-      s1 = s2;
-      id2 = id3;
-      lp2 = lp3;
     }
-    if (GRAD) cluster_wait();
   }
-  if (!GRAD) cluster_wait();
-  asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 }  // namespace rows

@@ -17,6 +17,7 @@ namespace rows {
 // Bits of an element type's own lowest value: -inf.
 template <typename T> struct Elem;
 template <> struct Elem<float> {
+  __device__ static __forceinline__ __nv_bfloat162 both_ru(float) { return __nv_bfloat162{}; }   // not used
   __device__ static __forceinline__ float load(const float* p) { return *p; }
   __device__ static __forceinline__ void store(float* p, float x) { *p = x; }
   __device__ static __forceinline__ uint32_t raw(const float* p) { return *reinterpret_cast<const uint32_t*>(p); }
@@ -28,6 +29,8 @@ template <> struct Elem<float> {
   }
 };
 template <> struct Elem<__nv_bfloat16> {
+  // the smallest value >= x, twice
+  __device__ static __forceinline__ __nv_bfloat162 both_ru(float x) { return __bfloat162bfloat162(__float2bfloat16_ru(x)); }
   __device__ static __forceinline__ float load(const __nv_bfloat16* p) { return __bfloat162float(*p); }
   __device__ static __forceinline__ void store(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
   __device__ static __forceinline__ uint32_t raw(const __nv_bfloat16* p) {
@@ -48,6 +51,7 @@ template <> struct Elem<__nv_bfloat16> {
   }
 };
 template <> struct Elem<__half> {
+  __device__ static __forceinline__ __half2 both_ru(float x) { return __half2half2(__float2half_ru(x)); }
   __device__ static __forceinline__ float load(const __half* p) { return __half2float(*p); }
   __device__ static __forceinline__ void store(__half* p, float x) { *p = __float2half_rn(x); }
   __device__ static __forceinline__ uint32_t raw(const __half* p) { return *reinterpret_cast<const unsigned short*>(p); }
@@ -180,6 +184,47 @@ __device__ __forceinline__ F2 weight_f2(float x, float m, F2 c, const float* tab
   const float de = (x - (d - bb)) + (-m - bb);
   const F2 y = exp2_f2(f2_mul(F2{d, de}, c), tab);
   return f2_norm(y.hi, y.lo);   // so that .hi alone is the rounded weight
+}
+
+// Sets the elements of x that are >= thr to -inf (thr may lie between two
+// values of T; NaN stay).
+template <typename T>
+__device__ __forceinline__ void clear_ge(uint4& x, float thr) {
+  if (sizeof(T) == 4) {
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+      if (__uint_as_float(word_of(x, t)) >= thr) set_word(x, t, Elem<T>::kNegInf);
+  } else {
+    using P = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+    const P lim = Elem<T>::both_ru(thr);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const uint32_t w = word_of(x, t);
+      const uint32_t m = __hge2_mask(*reinterpret_cast<const P*>(&w), lim);
+      set_word(x, t, (w & ~m) | (m & Tr<T>::kPadWord));
+    }
+  }
+}
+
+// Sums of weights 0 <= w <= 1 that come in any order: integers of 2^-50, so
+// the sum does not depend on which thread met which term.
+__device__ __forceinline__ unsigned long long weight_fixed(float w) { return (unsigned long long)(w * 1125899906842624.f); }
+__device__ __forceinline__ F2 fixed_f2(unsigned long long s) {
+  const float h = __ull2float_rz(s);
+  const float l = __ull2float_rz(s - (unsigned long long)h);
+  return F2{h * 8.8817841970012523e-16f, l * 8.8817841970012523e-16f};
+}
+template <int NW>
+__device__ __forceinline__ unsigned long long block_sum_u64(unsigned long long v, unsigned long long* sm) {
+#pragma unroll
+  for (int m = 16; m >= 1; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = v;
+  __syncthreads();
+  unsigned long long t = sm[0];
+#pragma unroll
+  for (int w = 1; w < NW; ++w) t += sm[w];
+  return t;
 }
 
 __device__ __forceinline__ double f2_double(F2 a) { return (double)a.hi + (double)a.lo; }

@@ -119,8 +119,8 @@ sv_status launch_top_u(const sv::rows::TopParams& p, cudaStream_t stream) {
 template <typename T>
 sv_status launch_top_rows(const sv::rows::TopParams& p, cudaStream_t stream) {
   auto kern = sv::rows::top_row_kernel<T>;
-  const int cap = std::max(512, p.k) + sv::rows::kTrStep;
-  const size_t smem = (size_t)sv::rows::kTrStages * sv::rows::kTrStep * sizeof(uint4) + (size_t)cap * (sizeof(uint4) + sizeof(int));
+  const size_t smem = (size_t)sv::rows::kTrStages * sv::rows::kTrStep * sizeof(uint4) +
+                      (size_t)sv::rows::tr_capacity(p.k) * sizeof(unsigned long long);
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
     cudaGetLastError();
     return SV_ERR_CUDA;
@@ -178,7 +178,7 @@ sv_status launch_distill_pipe(sv::rows::DistillParams p, cudaStream_t stream) {
   if (C > sv::rows::kDiMaxC || p.k > sv::rows::kDpLi) return SV_ERR_UNSUPPORTED;
   p.C = (int)C;
   p.SV = (int)ceil_div(nv, C);
-  auto kern = sv::rows::distill_pipe_kernel<T, GRAD>;
+  auto kern = p.V % VW == 0 ? sv::rows::distill_pipe_kernel<T, GRAD, true> : sv::rows::distill_pipe_kernel<T, GRAD, false>;
   const size_t smem = sizeof(sv::rows::DpSmem<T>);
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
     cudaGetLastError();
@@ -186,7 +186,7 @@ sv_status launch_distill_pipe(sv::rows::DistillParams p, cudaStream_t stream) {
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)p.C);
-  cfg.blockDim = dim3(sv::rows::kDpThreads);
+  cfg.blockDim = dim3((unsigned)sv::rows::dp_threads(p.k));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];

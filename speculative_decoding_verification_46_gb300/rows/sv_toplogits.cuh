@@ -66,6 +66,7 @@ struct TopSmem {
   float fred[kTlWarps];
   F2 f2red[kTlWarps];
   int ired[kTlWarps];
+  unsigned long long u64red[kTlWarps];
   double lns;
   unsigned long long kth;
   unsigned lmax;                        // okey of the largest candidate beyond the k best
@@ -180,18 +181,34 @@ __device__ __forceinline__ unsigned long long select_kth64(int k, int V, PickSme
   }
 }
 
-// The record of a row from its k best (keys sel[0 .. kk), any order) and the
-// rest's mass st relative to mt (0: none).  Ends with the outputs written.
+// The record of a row from its k best (keys sel[0 .. kk), any order; sorted
+// here) and the rest's mass st relative to mt (0: none).
 template <int NW>
-__device__ __forceinline__ void top_write(const TopParams& p, int r, const unsigned long long* sel, int kk, float mt,
-                                          F2 st, const float* tab, float* fred, F2* f2red, double* s_lns) {
+__device__ __forceinline__ void top_write(const TopParams& p, int r, unsigned long long* sel, int kk, float mt, F2 st,
+                                          const float* tab, F2* f2red, double* s_lns) {
+  constexpr int NT = NW * 32, E = kMaxK / NT;
   const int tid = threadIdx.x, k = p.k;
   const F2 c{p.c, p.c_lo};
-  float M = -INFINITY;
-  for (int j = tid; j < kk; j += NW * 32) M = fmaxf(M, comp_val(sel[j]));
-  M = block_max_n<NW>(M, fred);
+  unsigned long long mine[E];
+  int rank[E];
+#pragma unroll
+  for (int q = 0; q < E; ++q) {
+    const int e = tid + q * NT;
+    rank[q] = -1;
+    if (e < kk) {
+      mine[q] = sel[e];
+      rank[q] = 0;
+      for (int j = 0; j < kk; ++j) rank[q] += sel[j] > mine[q];
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < E; ++q)
+    if (rank[q] >= 0) sel[rank[q]] = mine[q];
+  __syncthreads();
+  const float M = comp_val(sel[0]);
   F2 sk{0.f, 0.f};
-  for (int j = tid; j < kk; j += NW * 32) sk = f2_add(sk, weight_f2(comp_val(sel[j]), M, c, tab));
+  for (int j = tid; j < kk; j += NT) sk = f2_add(sk, weight_f2(comp_val(sel[j]), M, c, tab));
   sk = block_sum_f2_n<NW>(sk, f2red);
   if (tid == 0) {
     const bool some = st.hi > 0.f;
@@ -202,16 +219,10 @@ __device__ __forceinline__ void top_write(const TopParams& p, int r, const unsig
   }
   __syncthreads();
   const double lns = *s_lns;
-  for (int e = tid; e < kk; e += NW * 32) {
-    const unsigned long long me = sel[e];
-    int rank = 0;
-    for (int j = 0; j < kk; ++j) rank += sel[j] > me;
-    p.indices[(size_t)r * k + rank] = comp_idx(me);
-    p.logprobs[(size_t)r * k + rank] = (float)(((double)comp_val(me) - (double)M) * p.inv_t - lns);
-  }
-  for (int j = kk + tid; j < k; j += NW * 32) {
-    p.indices[(size_t)r * k + j] = -1;
-    p.logprobs[(size_t)r * k + j] = -INFINITY;
+  for (int e = tid; e < k; e += NT) {
+    const bool on = e < kk;
+    p.indices[(size_t)r * k + e] = on ? comp_idx(sel[e]) : -1;
+    p.logprobs[(size_t)r * k + e] = on ? (float)(((double)comp_val(sel[e]) - (double)M) * p.inv_t - lns) : -INFINITY;
   }
 }
 
@@ -282,7 +293,7 @@ __device__ void top_finish_row(const TopParams& p, int r, TopSmem& sm) {
       if (key < K64 && key != 0ull) st = f2_add(st, weight_f2(comp_val(key), mt, c, sm.tab));
     }
     st = block_sum_f2_n<kTlWarps>(st, sm.f2red);
-    top_write<kTlWarps>(p, r, sm.sel, kk, mt, st, sm.tab, sm.fred, sm.f2red, &sm.lns);
+    top_write<kTlWarps>(p, r, sm.sel, kk, mt, st, sm.tab, sm.f2red, &sm.lns);
   } else {
     top_write_bad(p, r);
   }
@@ -399,7 +410,8 @@ __global__ void __launch_bounds__(kTlThreads, 4) top_slice_kernel(const TopParam
   if (!bad) {
     const uint32_t K = kth_key<TR::KEY_LOW_BIT, U>(key, k, sm.pick);
     const float tau = K == 0u ? -INFINITY : key_to_float(K);
-    // ---- the few vectors that reach tau go to shared memory and out of the registers
+    // ---- the few vectors that reach tau go to shared memory, their elements
+    // >= tau out of the registers
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (vm[u] >= tau && vm[u] > -INFINITY) {
@@ -408,23 +420,21 @@ __global__ void __launch_bounds__(kTlThreads, 4) top_slice_kernel(const TopParam
           sm.vec[pos] = x[u];
           sm.vid[pos] = v0 + u * kTlThreads + tid;
         }
-        x[u] = make_uint4(TR::kPadWord, TR::kPadWord, TR::kPadWord, TR::kPadWord);
-        vm[u] = -INFINITY;
+        clear_ge<T>(x[u], tau);
+        vm[u] = TR::template vmax<false>(x[u]);
       }
       mr = fmaxf(mr, vm[u]);
     }
     __syncthreads();
     const int NE = sm.nvec * VW;
     bool exact = NE > kTlVecs * VW;
-    // ---- their elements, one thread each: candidates, or rest
+    // ---- their elements, one thread each: the candidates
     if (!exact) {
       for (int e = tid; e < NE; e += kTlThreads) {
         const float xv = Elem<T>::load(reinterpret_cast<const T*>(sm.vec) + e);
         if (xv >= tau && xv > -INFINITY) {
           const int pos = atomicAdd(&sm.count, 1);
           if (pos < kTlCap) sm.cand[pos] = comp_key(xv, sm.vid[e / VW] * VW - win.a0 + e % VW);
-        } else {
-          mr = fmaxf(mr, xv);
         }
       }
       __syncthreads();
@@ -449,7 +459,8 @@ __global__ void __launch_bounds__(kTlThreads, 4) top_slice_kernel(const TopParam
     // ---- the mass of everything not listed, relative to its largest
     if (!exact) {
       mr = block_max_n<kTlWarps>(mr, sm.fred);         // its barriers publish kth and lmax too
-      if (sm.lmax != 0u) mr = fmaxf(mr, key_to_float(sm.lmax));
+      const float lmax = sm.lmax != 0u ? key_to_float(sm.lmax) : -INFINITY;
+      mr = fmaxf(mr, lmax);
       if (mr > -INFINITY) {
         float s0 = 0.f, s1 = 0.f;
 #pragma unroll
@@ -459,19 +470,22 @@ __global__ void __launch_bounds__(kTlThreads, 4) top_slice_kernel(const TopParam
             s0 += ex2_approx((TR::get(x[u], t) - mr) * p.c);
             s1 += ex2_approx((TR::get(x[u], t + 1) - mr) * p.c);
           }
-        for (int e = tid; e < NE; e += kTlThreads) {
-          const float xv = Elem<T>::load(reinterpret_cast<const T*>(sm.vec) + e);
-          if (xv < tau) s0 += ex2_approx((xv - mr) * p.c);
-        }
         s = f2_add(F2{s0, 0.f}, F2{s1, 0.f});
-        const unsigned long long kth = sm.kth;         // 0: the list holds all candidates
+      }
+      s = block_sum_f2_n<kTlWarps>(s, sm.f2red);
+      if (lmax > -INFINITY) {                          // candidates beyond the list, in whatever order they stand
+        const unsigned long long kth = sm.kth;
+        unsigned long long w = 0ull;
         for (int e = tid; e < N; e += kTlThreads) {
           const unsigned long long me = sm.cand[e];
-          if (me < kth) s = f2_add(s, weight_f2(comp_val(me), mr, F2{p.c, p.c_lo}, sm.tab));
+          if (me < kth) w += weight_fixed(weight_f2(comp_val(me), lmax, F2{p.c, p.c_lo}, sm.tab).hi);
         }
+        const F2 left = fixed_f2(block_sum_u64<kTlWarps>(w, sm.u64red));
+        s = f2_add(s, f2_mul(left, weight_f2(lmax, mr, F2{p.c, p.c_lo}, sm.tab)));
       }
+    } else {
+      s = block_sum_f2_n<kTlWarps>(s, sm.f2red);
     }
-    s = block_sum_f2_n<kTlWarps>(s, sm.f2red);
   }
   if (tid == 0) p.part[(size_t)r * p.H + h] = make_float4(mr, s.hi, s.lo, bad ? 1.f : 0.f);
   if (arrive_last(p.ticket + r, p.H, &sm.flag)) top_finish_row<T>(p, r, sm);
@@ -483,16 +497,22 @@ __global__ void __launch_bounds__(kTlThreads, 4) top_slice_kernel(const TopParam
 // 150 thousand tokens.  Here a CTA streams a whole row through a ring of
 // cp.async stages private to each thread and selects once.  `thr` is a lower
 // bound of the row's k-th largest value at any time: from the first step's
-// vector maxima, later from the elements set aside so far.  Vectors that reach
-// it are set aside in shared memory; everything else goes into the thread's
-// running (maximum, sum) at once.  When the vectors set aside exceed `trig`
-// (>= k) they are cut back to those that hold one of the k best so far - an
-// element equal to the k-th that comes later in the row loses the tie, so the
-// bound is strict from then on, and rows of ties or of rising values cost more
-// cuts but need no other path.
+// vector maxima, later from the candidates so far.  An element that reaches
+// it leaves the registers (its vector's number goes to a list, and after the
+// step's barrier one thread per element of those vectors, still in the ring,
+// adds the candidates to theirs); everything else goes into the thread's
+// running (maximum, sum) at once.  Raising thr costs a radix select over some
+// hundred candidates, and is done when their number has grown by k; when they
+// outgrow their buffer they are cut back to the k best.  An element equal to
+// the k-th best that comes later in the row loses the tie, so a raised bound
+// is strict, and rows of ties or of rising values cost more cuts but need no
+// other path.
 constexpr int kTrU = 4;                         // vectors per thread per step
-constexpr int kTrStages = 2;                    // steps in flight
+constexpr int kTrStages = 3;                    // ring stages: one read, one or two in flight
 constexpr int kTrStep = kTrU * kTlThreads;      // vectors per step
+constexpr int kTrFew = 96;                      // listed vectors a step that need no look at the buffer's end
+
+__host__ __device__ constexpr int tr_capacity(int k) { return 2048 > 2 * k + 1024 ? 2048 : 2 * k + 1024; }
 
 struct TopRowSmem {
   PickSmem pick;
@@ -500,8 +520,11 @@ struct TopRowSmem {
   float fred[kTlWarps];
   F2 f2red[kTlWarps];
   int ired[kTlWarps];
+  unsigned long long u64red[kTlWarps];
   double lns;
-  int nvec, count;
+  int nvec[3];                                  // listed vectors of a step, by step % 3
+  int nk, count;
+  uint16_t list[2][kTrStep];                    // their places in the step, by step % 2
 };
 
 // A thread's running (maximum, sum) of the elements that are not set aside.
@@ -543,10 +566,10 @@ __global__ void __launch_bounds__(kTlThreads, 3) top_row_kernel(const TopParams 
   extern __shared__ __align__(16) unsigned char smem_raw[];
   __shared__ TopRowSmem sm;
   const int tid = threadIdx.x, k = p.k, r = blockIdx.x;
-  const int trig = max(512, k);                                      // cap - kTrStep
-  uint4* ring = reinterpret_cast<uint4*>(smem_raw);                  // [kTrStages][kTrU][kTlThreads]
-  uint4* vec = ring + kTrStages * kTrStep;                           // [trig + kTrStep] set aside
-  int* vid = reinterpret_cast<int*>(vec + trig + kTrStep);           // their numbers in the window
+  const int cap = tr_capacity(k), trig = cap - 1024;
+  static_assert(kTrFew * 8 <= 1024, "a step of few listed vectors fits behind trig");
+  uint4* ring = reinterpret_cast<uint4*>(smem_raw);                            // [kTrStages][kTrU][kTlThreads]
+  unsigned long long* keys = reinterpret_cast<unsigned long long*>(ring + kTrStages * kTrStep);   // [cap] candidates
   const Window<T, const T> win(static_cast<const T*>(p.logits), (size_t)r, p.V);
   const int NV = win.vectors();
   const int steps = (NV + kTrStep - 1) / kTrStep;
@@ -568,56 +591,68 @@ __global__ void __launch_bounds__(kTlThreads, 3) top_row_kernel(const TopParams 
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-#pragma unroll
-  for (int s = 0; s < kTrStages; ++s) issue(s);
+  issue(0);
+  issue(1);
   load_exp2_table(sm.tab);
-  if (tid == 0) sm.nvec = 0;
+  if (tid == 0) sm.nvec[0] = sm.nvec[1] = sm.nvec[2] = sm.nk = 0;
+  __syncthreads();
 
-  float thr = -INFINITY;                                             // what is set aside from here on
-  float low = -INFINITY;                                             // what is among the best of those set aside
-  int bad = 0;
-  RunningSum acc;
   const float c = p.c;
-  // every element set aside that may be among the k best
-  auto candidates = [&](int n, auto f) {
-    for (int e = tid; e < n * VW; e += kTlThreads) {
-      const float xv = Elem<T>::load(reinterpret_cast<const T*>(vec) + e);
-      if (xv >= low && xv > -INFINITY) f(comp_key(xv, vid[e / VW] * VW - win.a0 + e % VW));
+  float thr = -INFINITY;
+  int look = min(trig, k + max(k, 64));                              // candidates at which thr is raised next
+  int bad = 0, flag = 0;
+  RunningSum acc;
+  auto all_keys = [&](int n, auto f) {
+    for (int e = tid; e < n; e += kTlThreads) f(keys[e]);
+  };
+  // adds the mass of keys that leave the candidates (any order) to thread 0's sum; top: the largest of them
+  auto leave = [&](float top, auto each) {
+    top = block_max_n<kTlWarps>(top, sm.fred);
+    if (top == -INFINITY) return;
+    unsigned long long w = 0ull;
+    each([&](unsigned long long key) { w += weight_fixed(weight_f2(comp_val(key), top, F2{p.c, p.c_lo}, sm.tab).hi); });
+    w = block_sum_u64<kTlWarps>(w, sm.u64red);
+    if (tid == 0) {
+      acc.raise(top, c);
+      const float f = acc.far ? acc.term_far(top, c) : acc.term(top, c);
+      acc.s = f2_add(acc.s, f2_mul(fixed_f2(w), F2{f, 0.f}));
     }
   };
+  // the smallest float above the value of K64 (which may have stopped early,
+  // with zeros below the digits it needed: a smaller bound then); keys of
+  // finite values start at 0x00800000
+  auto above = [&](unsigned long long K64) { return key_to_float(max((uint32_t)(K64 >> 32), 0x007fffffu) + 1u); };
+
 #pragma unroll 1
   for (int step = 0; step < steps; ++step) {
-    asm volatile("cp.async.wait_group %0;" ::"n"(kTrStages - 1) : "memory");
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
     uint4 x[kTrU];
     float vm[kTrU];
-    const uint4* slot = ring + (step % kTrStages) * kTrStep + tid;
+    const uint4* stage = ring + (step % kTrStages) * kTrStep;
 #pragma unroll
     for (int u = 0; u < kTrU; ++u) {
-      x[u] = step * kTrStep + u * kTlThreads + tid < NV ? slot[u * kTlThreads] : pad;
+      x[u] = step * kTrStep + u * kTlThreads + tid < NV ? stage[u * kTlThreads + tid] : pad;
       vm[u] = TR::template vmax<true>(x[u]);
       bad |= !(vm[u] < INFINITY);                                    // NaN or +inf
     }
-    issue(step + kTrStages);
     if (step == 0) {
       uint32_t key[kTrU];
 #pragma unroll
       for (int u = 0; u < kTrU; ++u) key[u] = vm[u] > -INFINITY ? okey(vm[u]) : 0u;
       const uint32_t K = kth_key<TR::KEY_LOW_BIT, kTrU>(key, k, sm.pick);
-      if (K != 0u) thr = low = key_to_float(K);
+      if (K != 0u) thr = key_to_float(K);
     }
-    int over = 0;
     float mc = -INFINITY;
 #pragma unroll
     for (int u = 0; u < kTrU; ++u) {
       if (vm[u] >= thr && vm[u] > -INFINITY) {
-        const int pos = atomicAdd(&sm.nvec, 1);
-        vec[pos] = x[u];
-        vid[pos] = step * kTrStep + u * kTlThreads + tid;
-        over |= pos >= trig;
-        x[u] = pad;
-      } else {
-        mc = fmaxf(mc, vm[u]);
+        const int pos = atomicAdd(&sm.nvec[step % 3], 1);
+        sm.list[step & 1][pos] = (uint16_t)(u * kTlThreads + tid);
+        flag |= pos >= kTrFew;
+        clear_ge<T>(x[u], thr);
+        vm[u] = TR::template vmax<false>(x[u]);
       }
+      mc = fmaxf(mc, vm[u]);
     }
     acc.raise(mc, c);
     if (acc.m > -INFINITY) {
@@ -639,79 +674,94 @@ __global__ void __launch_bounds__(kTlThreads, 3) top_row_kernel(const TopParams 
       }
       acc.take(s0 + s1);
     }
-    if (__syncthreads_or(over)) {
-      // cut back to the vectors that hold one of the k best so far
-      const int n = sm.nvec;
-      const unsigned long long K64 = select_kth64<T>(k, p.V, sm.pick, [&](auto f) { candidates(n, f); });
-      __syncthreads();
-      if (tid == 0) sm.nvec = 0;
+    if (tid == 0) sm.nvec[(step + 1) % 3] = 0;                       // last read two steps ago
+    const bool slow = __syncthreads_or(flag);                        // a buffer may be near its end, or thr is due
+    issue(step + 2);                                                 // into the stage that everyone has left
+    const int nv = sm.nvec[step % 3];
+    // every element of the listed vectors that reaches thr
+    auto listed = [&](auto f) {
+      for (int e = tid; e < nv * VW; e += kTlThreads) {
+        const int at = sm.list[step & 1][e / VW];
+        const float xv = Elem<T>::load(reinterpret_cast<const T*>(stage + at) + e % VW);
+        if (xv >= thr && xv > -INFINITY) f(comp_key(xv, (step * kTrStep + at) * VW - win.a0 + e % VW));
+      }
+    };
+    flag = 0;
+    if (!slow) {
+      listed([&](unsigned long long key) {
+        const int pos = atomicAdd(&sm.nk, 1);
+        keys[pos] = key;
+        flag |= pos >= look;
+      });
+    } else {
+      const int nk = sm.nk;
+      int fresh = 0;
+      listed([&](unsigned long long) { ++fresh; });
+      fresh = block_sum_int_w<kTlWarps>(fresh, sm.ired);             // its barriers: everyone has read nk
+      if (nk + fresh > trig && nk + fresh > k) {
+        // cut back to the k best
+        const unsigned long long K64 = select_kth64<T>(k, p.V, sm.pick, [&](auto f) {
+          all_keys(nk, f);
+          listed(f);
+        });
+        float top = -INFINITY;
+        auto leaving = [&](auto f) {
+          auto g = [&](unsigned long long key) { if (key < K64) f(key); };
+          all_keys(nk, g);
+          listed(g);
+        };
+        leaving([&](unsigned long long key) { top = fmaxf(top, comp_val(key)); });
+        leave(top, leaving);
+        __syncthreads();
+        if (tid == 0) sm.nk = 0;
 #pragma unroll 1
-      for (int e0 = 0; e0 < n; e0 += kTlThreads) {
-        const int e = e0 + tid;
-        uint4 y = pad;
-        int id = 0;
-        if (e < n) {
-          y = vec[e];
-          id = vid[e];
+        for (int e0 = 0; e0 < nk; e0 += kTlThreads) {
+          const unsigned long long key = e0 + tid < nk ? keys[e0 + tid] : 0ull;
+          __syncthreads();                                           // this round's keys are in registers
+          if (key != 0ull && key >= K64) keys[atomicAdd(&sm.nk, 1)] = key;
         }
-        bool keep = false;
-#pragma unroll
-        for (int t = 0; t < VW; ++t) {
-          const float xv = TR::get(y, t);
-          keep |= xv > -INFINITY && comp_key(xv, id * VW - win.a0 + t) >= K64;
-        }
-        __syncthreads();                                             // this round's vectors are in registers
-        if (keep) {
-          const int pos = atomicAdd(&sm.nvec, 1);
-          vec[pos] = y;
-          vid[pos] = id;
-        } else {
-#pragma unroll
-          for (int t = 0; t < VW; ++t) acc.add(TR::get(y, t), c);
+        __syncthreads();
+        listed([&](unsigned long long key) { if (key >= K64) keys[atomicAdd(&sm.nk, 1)] = key; });
+        __syncthreads();
+        thr = above(K64);
+        look = min(trig, k + max(k, 64));
+      } else {
+        listed([&](unsigned long long key) { keys[atomicAdd(&sm.nk, 1)] = key; });
+        __syncthreads();
+        if (nk + fresh > k) {
+          thr = fmaxf(thr, above(select_kth64<T>(k, p.V, sm.pick, [&](auto f) { all_keys(nk + fresh, f); })));
+          look = min(trig, nk + fresh + max(k, 64));
         }
       }
-      // K64 may have stopped early, with zeros below the digits that it
-      // needed: a smaller bound then.  Keys of finite values start at 0x00800000.
-      const uint32_t kv = max((uint32_t)(K64 >> 32), 0x007fffffu);
-      thr = key_to_float(kv + 1u);
-      low = key_to_float(max(kv, 0x00800000u));
-      __syncthreads();
     }
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
 
   // ---- the record
   bad = __syncthreads_or(bad);
-  const int n = sm.nvec;
-  unsigned long long* sel = reinterpret_cast<unsigned long long*>(ring);
-  int have = 0;
-  if (!bad) {
-    for (int e = tid; e < n * VW; e += kTlThreads) have += Elem<T>::load(reinterpret_cast<const T*>(vec) + e) > -INFINITY;
-    have = block_sum_int_w<kTlWarps>(have, sm.ired);
-  }
+  const int have = sm.nk;
   if (bad || have == 0) {
     top_write_bad(p, r);
     return;
   }
-  low = -INFINITY;                                                   // the record may reach any element set aside
-  const unsigned long long K64 = have > k ? select_kth64<T>(k, p.V, sm.pick, [&](auto f) { candidates(n, f); }) : 1ull;
-  __syncthreads();
+  unsigned long long* sel = reinterpret_cast<unsigned long long*>(ring);
   if (tid == 0) sm.count = 0;
+  const unsigned long long K64 = have > k ? select_kth64<T>(k, p.V, sm.pick, [&](auto f) { all_keys(have, f); }) : 1ull;
   __syncthreads();
-  candidates(n, [&](unsigned long long key) {
-    if (key >= K64) {
-      const int pos = atomicAdd(&sm.count, 1);
-      if (pos < kMaxK) sel[pos] = key;
-    } else {
-      acc.add(comp_val(key), c);
-    }
+  float top = -INFINITY;
+  all_keys(have, [&](unsigned long long key) {
+    if (key >= K64) sel[atomicAdd(&sm.count, 1)] = key;
+    else top = fmaxf(top, comp_val(key));
+  });
+  leave(top, [&](auto f) {
+    all_keys(have, [&](unsigned long long key) { if (key < K64) f(key); });
   });
   const float mt = block_max_n<kTlWarps>(acc.m, sm.fred);
   F2 st{0.f, 0.f};
   if (acc.m > -INFINITY)
     st = f2_mul(f2_mul(acc.s, F2{acc.scale(c), 0.f}), weight_f2(acc.m, mt, F2{p.c, p.c_lo}, sm.tab));
   st = block_sum_f2_n<kTlWarps>(st, sm.f2red);
-  top_write<kTlWarps>(p, r, sel, min(k, have), mt, st, sm.tab, sm.fred, sm.f2red, &sm.lns);
+  top_write<kTlWarps>(p, r, sel, min(k, have), mt, st, sm.tab, sm.f2red, &sm.lns);
 }
 
 }  // namespace rows
