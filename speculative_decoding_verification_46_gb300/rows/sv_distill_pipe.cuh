@@ -5,26 +5,24 @@
 // The warps of a CTA have four roles and meet only where one needs what
 // another made (named barriers, two of each in turn; no spinning):
 //
-//   streaming (16 warps)  own the CTA's slice of every row through a ring of
+//   streaming (22 warps)  own the CTA's slice of every row through a ring of
 //       kDpStages cp.async stages private to each thread (a thread reads back
 //       only what it copied).  Per row t: sum the slice without its listed
 //       tokens to (maximum, sum); then write row t - 1's gradient out of the
 //       ring and start loading row t + 2 into the stage that frees.
-//   list (1 warp per 32 listed tokens)  a listed token per thread: the
-//       teacher's softmax and the student's weights there (two-float), the
+//   list (1 warp per 32 listed tokens, 4 at most)  the teacher's softmax and the student's weights there (two-float), the
 //       bitmap that takes the tokens out of the streams, and at the end the
 //       tokens' own gradient on top of the dense one.  The loads of a list
 //       are issued one row before they are used.
 //   exchange (1 warp)  the CTA's part of row t to all CTAs of the cluster (one
 //       cluster barrier per row) and from the C parts the row's statistics.
-//   loss (1 warp)  three logarithms per row.
+//   loss (1 warp)  three logarithms per row; the CTAs take the rows in turn.
 //
 // So every dependent chain - gather, two-float sums, exchange, logarithms -
 // has a whole row's streaming time to finish in.  The forward pass alone is
 // the same without the gradient.
 //
-// Bound: HBM, with instruction issue close behind (about 100 warp
-// instructions per 32 vectors of 16 bytes read and written).
+// Bound: HBM, with instruction issue close behind.
 #pragma once
 
 #include "sv_distill.cuh"
@@ -32,21 +30,23 @@
 namespace sv {
 namespace rows {
 
-constexpr int kDpSt = 512;              // streaming threads
+constexpr int kDpSt = 704;              // streaming threads
 constexpr int kDpStWarps = kDpSt / 32;
-constexpr int kDpLi = 256;              // most list threads: the largest list
+constexpr int kDpLi = 128;              // most list threads
+constexpr int kDpMaxK = 2 * kDpLi;      // the largest list: two tokens a thread
 constexpr int kDpMaxThreads = kDpSt + 32 + kDpLi + 32;
-constexpr int kDpU = 8;                 // vectors per streaming thread and row
-constexpr int kDpSlice = kDpSt * kDpU;  // vectors per CTA and row
+constexpr int kDpSlice = 4096;          // most vectors per CTA and row
+constexpr int kDpU = (kDpSlice + kDpSt - 1) / kDpSt;   // per streaming thread
 constexpr int kDpStages = 3;
 constexpr int kDpLists = 6;             // rows whose lists are alive
 
-// threads of a CTA for lists of k tokens
-__host__ __device__ constexpr int dp_threads(int k) { return kDpSt + 32 + (k + 31) / 32 * 32 + 32; }
+// list threads, and threads of a CTA, for lists of k tokens
+__host__ __device__ constexpr int dp_list_threads(int k) { return k > kDpLi ? kDpLi : (k + 31) / 32 * 32; }
+__host__ __device__ constexpr int dp_threads(int k) { return kDpSt + 32 + dp_list_threads(k) + 32; }
 
 struct DpList {
-  int sid[kDpLi];                       // listed tokens (-1: ignored)
-  float sw[kDpLi], sq[kDpLi];           // the teacher's and the student's weights
+  int sid[kDpMaxK];                     // listed tokens (-1: ignored)
+  float sw[kDpMaxK], sq[kDpMaxK];       // the teacher's and the student's weights
   float tm, km, ltail, wgt, sc;         // sc = wgt / temperature
   F2 Z, WK, E1, wt;
   int live;                             // 0: weight 0, 1: nothing to learn from, 2: a row
@@ -54,18 +54,19 @@ struct DpList {
 };
 struct DpStat {
   float mt, A, M, invS, Es;
-  F2 S, st;
+  F2 S;
+  float st;
   int twice;
 };
 template <typename T>
 struct DpSmem {
-  uint4 ring[kDpStages][kDpU][kDpSt];
+  uint4 ring[kDpStages][kDpSlice];
   uint32_t bits[2][kDpSlice * Tr<T>::VW / 32];
   uint2 dirty[2][kDpStWarps];           // a byte per (warp, u): some vector there holds a listed token
   DpList list[kDpLists];
   DpStat stat[kDpLists];
-  float4 part[2][kDiMaxC];
-  float4 wpart[2][kDpStWarps];
+  float4 part[2][kDiMaxC];              // (maximum, sum, -, twice)
+  float2 wpart[2][kDpStWarps];
   F2 lsum[kDpLi / 32][3];
   float2 lmax[kDpLi / 32];
   float tab[128];
@@ -93,30 +94,9 @@ __device__ __forceinline__ F2 two_diff(float a, float b) {
   return F2{d, (a - (d - bb)) + (-b - bb)};
 }
 
-// The largest element of U vectors (NaN are passed over).
-template <typename T, int U>
-__device__ __forceinline__ float max_of(const uint4 (&x)[U]) {
-  if (sizeof(T) == 4) {
-    float m = -INFINITY;
-#pragma unroll
-    for (int u = 0; u < U; ++u) m = fmaxf(m, Tr<T>::template vmax<false>(x[u]));
-    return m;
-  }
-  // packed: two elements an instruction
-  using P = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
-  P m = *reinterpret_cast<const P*>(&x[0].x);
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    m = __hmax2(m, *reinterpret_cast<const P*>(&x[u].x));
-    m = __hmax2(m, *reinterpret_cast<const P*>(&x[u].y));
-    m = __hmax2(m, *reinterpret_cast<const P*>(&x[u].z));
-    m = __hmax2(m, *reinterpret_cast<const P*>(&x[u].w));
-  }
-  const float lo = __low2float(m), hi = __high2float(m);
-  return fmaxf(lo, hi);
-}
-
-// The statistics of a row from the C parts (one warp; lane 0 writes).
+// The statistics of a row from the C parts (one warp; lane 0 writes).  The
+// sum outside the list is float32 up to here: its error moves the loss by
+// q_t - p_t of it.  The row's whole sum is two-float, it moves the loss fully.
 __device__ __forceinline__ void dp_statistics(const float4* part, int C, const DpList& L, int k, F2 c, const float* tab,
                                               DpStat& out, float* stats) {
   const int lane = threadIdx.x & 31;
@@ -125,10 +105,9 @@ __device__ __forceinline__ void dp_statistics(const float4* part, int C, const D
   float mt = v.x;
 #pragma unroll
   for (int o = kDiMaxC / 2; o >= 1; o >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
-  F2 st{v.y, v.z};
-  if (v.x != mt) st = v.x == -INFINITY ? st : f2_mul(st, weight_f2(v.x, mt, c, tab));
+  float st = v.x == mt ? v.y : v.y * ex2_approx((v.x - mt) * c.hi);
 #pragma unroll
-  for (int o = kDiMaxC / 2; o >= 1; o >>= 1) st = f2_add(st, f2_shfl_xor(st, o));
+  for (int o = kDiMaxC / 2; o >= 1; o >>= 1) st += __shfl_xor_sync(0xffffffffu, st, o);
   F2 WK = L.WK;
   if (twice) {                          // a token's weight counts once, whatever the list says
     WK = F2{0.f, 0.f};
@@ -144,20 +123,18 @@ __device__ __forceinline__ void dp_statistics(const float4* part, int C, const D
     const float M = fmaxf(mt, km);
     // one of the two maxima is M
     const F2 E = mt == km ? F2{1.f, 0.f} : weight_f2(fminf(mt, km), M, c, tab);
-    const F2 Et = mt == M ? F2{1.f, 0.f} : E;
-    const F2 Ek = km == M ? F2{1.f, 0.f} : E;
-    const F2 S = f2_add(mt == M ? st : f2_mul(st, Et), km == M ? WK : f2_mul(WK, Ek));
+    const bool outside = mt == M;
+    const F2 S = f2_add(outside ? F2{st, 0.f} : f2_mul(F2{st, 0.f}, E), km == M ? WK : f2_mul(WK, E));
     const bool good = S.hi > 0.f && S.hi < INFINITY;
     const float nan = __uint_as_float(0x7fffffffu);
-    const float invS = good ? f2_rcp(S) : nan;
-    const float invZ = f2_rcp(L.Z);
+    const float invS = good ? __frcp_rn(S.hi) : nan;
+    const float invZ = __frcp_rn(L.Z.hi);
     const float pt = L.wt.hi * invZ;
-    const bool some = st.hi > 0.f;
     out.mt = mt == -INFINITY || !good ? 0.f : mt;
-    out.A = !good ? nan : !some ? 0.f : Et.hi * invS - (pt == 0.f ? 0.f : pt * f2_rcp(st));
+    out.A = !good ? nan : !(st > 0.f) ? 0.f : (outside ? invS : E.hi * invS) - (pt == 0.f ? 0.f : pt * __frcp_rn(st));
     out.M = M;
     out.invS = invS;
-    out.Es = Ek.hi;
+    out.Es = km == M ? 1.f : E.hi;
     out.S = S;
     out.st = st;
     out.twice = twice;
@@ -176,7 +153,7 @@ __device__ __forceinline__ void dp_loss(const DpList& L, const DpStat& s, double
     if (lane == 0) *loss = 0.f;
     return;
   }
-  const F2 mine = lane == 0 ? L.Z : lane == 1 ? s.S : s.st;
+  const F2 mine = lane == 0 ? L.Z : lane == 1 ? s.S : F2{s.st, 0.f};
   const F2 lg = mine.hi > 0.f ? f2_log(mine, tab) : F2{-INFINITY, 0.f};
   const F2 lz{__shfl_sync(0xffffffffu, lg.hi, 0), __shfl_sync(0xffffffffu, lg.lo, 0)};
   const F2 ls{__shfl_sync(0xffffffffu, lg.hi, 1), __shfl_sync(0xffffffffu, lg.lo, 1)};
@@ -200,12 +177,16 @@ __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const Di
   constexpr int VW = TR::VW;
   extern __shared__ __align__(16) unsigned char smem_raw[];
   DpSmem<T>& sm = *reinterpret_cast<DpSmem<T>*>(smem_raw);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int lane = threadIdx.x & 31;
   const int C = p.C, rank = blockIdx.x % C;
   const int g = blockIdx.x / C, NG = gridDim.x / C;
   const int n = (p.R - g + NG - 1) / NG;            // rows of this cluster: g, g + NG, ...
   const int k = p.k;
-  const int nl = (k + 31) / 32 * 32;                // list threads
+  const int nl = dp_list_threads(k);
+  // the roles, by warp: exchange, list, loss, streaming (the later warps of a
+  // scheduler wait for the earlier ones, and the streaming warps always have
+  // something to issue)
+  const int role = threadIdx.x < 32 ? 0 : threadIdx.x < 32 + nl ? 1 : threadIdx.x < 64 + nl ? 2 : 3;
   const F2 c{p.c, p.c_lo};
   const T* student = static_cast<const T*>(p.student);
   // barrier sizes
@@ -216,13 +197,14 @@ __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const Di
     *v1 = min(*v0 + p.SV, nv);
   };
 
-  for (int i = tid; i < 128; i += blockDim.x) sm.tab[i] = i < 64 ? __ldg(kExp2Hi + i) : __ldg(kExp2Lo + i - 64);
+  for (int i = threadIdx.x; i < 128; i += blockDim.x) sm.tab[i] = i < 64 ? __ldg(kExp2Hi + i) : __ldg(kExp2Lo + i - 64);
   __syncthreads();
   cluster_arrive();
   cluster_wait();                                   // every CTA of the cluster runs: its shared memory can be written
 
-  if (warp < kDpStWarps) {
+  if (role == 3) {
     // ================================================================ streaming
+    const int tid = threadIdx.x - 64 - nl, warp = tid >> 5;
     int v0 = 0, v1 = 0;
     if (WHOLE) slice(p.V / VW, &v0, &v1);
     int mine = (v1 - v0 - tid + kDpSt - 1) / kDpSt;  // vectors of this thread in a row (WHOLE)
@@ -231,7 +213,7 @@ __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const Di
     auto issue = [&](int i) {                       // row i of the cluster into its stage
       if (i < n) {
         const int r = g + i * NG;
-        uint4* st = &sm.ring[i % kDpStages][0][tid];
+        uint4* st = &sm.ring[i % kDpStages][tid];
         if (w_next != 0.f) {
           if (WHOLE) {
             const uint4* src = reinterpret_cast<const uint4*>(student) + (size_t)r * nvr + v0 + tid;
@@ -262,6 +244,11 @@ __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const Di
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
+    if (WHOLE) {                                    // a thread's last slot stays -inf where the slice ends before it
+      for (int s = 0; s < kDpStages; ++s)
+        for (int u = mine; u < kDpU && u * kDpSt + tid < kDpSlice; ++u)
+          sm.ring[s][u * kDpSt + tid] = make_uint4(TR::kPadWord, TR::kPadWord, TR::kPadWord, TR::kPadWord);
+    }
     issue(0);
     issue(1);
     if (!GRAD) issue(2);
@@ -273,7 +260,7 @@ __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const Di
         asm volatile("cp.async.wait_group %0;" ::"n"(GRAD ? 1 : 2) : "memory");
         bar_sync(DP_LISTED + (t & 1), n_listed);
         if (sm.list[t % kDpLists].live != 0) {
-          const uint4* st = &sm.ring[t % kDpStages][0][tid];
+          const uint4* st = &sm.ring[t % kDpStages][tid];
           int m_t = mine;
           if (!WHOLE) {
             const Window<T, const T> win(student, (size_t)(g + t * NG), p.V);
@@ -284,8 +271,12 @@ __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const Di
           uint4 x[kDpU];
 #pragma unroll
           for (int u = 0; u < kDpU; ++u) {
-            x[u] = make_uint4(TR::kPadWord, TR::kPadWord, TR::kPadWord, TR::kPadWord);
-            if (u < m_t) x[u] = st[u * kDpSt];
+            if (WHOLE && (u + 1) * kDpSt <= kDpSlice) {
+              x[u] = st[u * kDpSt];                 // -inf where this thread has no vector
+            } else {
+              x[u] = make_uint4(TR::kPadWord, TR::kPadWord, TR::kPadWord, TR::kPadWord);
+              if (u < m_t) x[u] = st[u * kDpSt];
+            }
           }
           const uint2 dirty = sm.dirty[t & 1][warp];
           if (dirty.x | dirty.y) {
@@ -294,46 +285,53 @@ __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const Di
             for (int u = 0; u < kDpU; ++u) {
               if (((u < 4 ? dirty.x : dirty.y) >> (8 * (u & 3))) & 0xffu) {
                 const int lv = u * kDpSt + tid;
-                const uint32_t b = VW == 8 ? bits[lv] : (bits[lv >> 1] >> ((lv & 1) * 4)) & 15u;
+                const uint32_t b = lv >= kDpSlice ? 0u : VW == 8 ? bits[lv] : (bits[lv >> 1] >> ((lv & 1) * 4)) & 15u;
 #pragma unroll
                 for (int e = 0; e < VW; ++e)
                   if ((b >> e) & 1u) TR::put(x[u], e, Elem<T>::kNegInf);
               }
             }
           }
-          float m = max_of<T, kDpU>(x);
+          float m = -INFINITY;
+#pragma unroll
+          for (int u = 0; u < kDpU; ++u) m = fmaxf(m, TR::template vmax<false>(x[u]));
 #pragma unroll
           for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
           const float ref = m == -INFINITY ? 0.f : m, rho = ref * p.c;
-          float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f, fix = 1.f;
+          float s, fix = 1.f;
           if (fabsf(rho) < kNear) {
             fix = ex2_approx(-fmaf(ref, p.c, -rho));
+            const Pair cc = pair_of(p.c, p.c), rr = pair_of(-rho, -rho);
+            Pair a0 = pair_of(0.f, 0.f), a1 = a0;
 #pragma unroll
             for (int u = 0; u < kDpU; ++u)
 #pragma unroll
               for (int e = 0; e < VW; e += 4) {
-                a0 += ex2_approx(fmaf(TR::get(x[u], e), p.c, -rho));
-                a1 += ex2_approx(fmaf(TR::get(x[u], e + 1), p.c, -rho));
-                a2 += ex2_approx(fmaf(TR::get(x[u], e + 2), p.c, -rho));
-                a3 += ex2_approx(fmaf(TR::get(x[u], e + 3), p.c, -rho));
+                a0 = pair_add(a0, pair_terms<T>(x[u], e, cc, rr));
+                a1 = pair_add(a1, pair_terms<T>(x[u], e + 2, cc, rr));
               }
+            float s0, s1;
+            unpair(pair_add(a0, a1), s0, s1);
+            s = s0 + s1;
           } else {
+            s = 0.f;
 #pragma unroll
             for (int u = 0; u < kDpU; ++u) {
 #pragma unroll 1
-              for (int e = 0; e < VW; ++e) a0 += ex2_approx((TR::get(x[u], e) - ref) * p.c);
+              for (int e = 0; e < VW; ++e) s += ex2_approx((TR::get(x[u], e) - ref) * p.c);
             }
           }
-          F2 s = f2_add(f2_add(F2{a0, 0.f}, F2{a1, 0.f}), f2_add(F2{a2, 0.f}, F2{a3, 0.f}));
-          s = f2_mul(warp_sum_f2(s), F2{fix, 0.f});
-          if (lane == 0) sm.wpart[t & 1][warp] = make_float4(m, s.hi, s.lo, 0.f);
+          // chains of 12 terms, then a tree
+#pragma unroll
+          for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+          if (lane == 0) sm.wpart[t & 1][warp] = make_float2(m, s * fix);
         }
         bar_arrive(DP_SUMMED + (t & 1), n_summed);
         if (!GRAD) issue(t + 3);
       }
       // (the cluster barrier of row t - 1 is long complete; the exchange warp is who needs it)
       if (t >= 1) cluster_wait();
-      if (t < n) cluster_arrive();
+      if (t < n) cluster_arrive_relaxed();
       if (t >= 1) {
         // ---- row t - 1's gradient
         const int i = t - 1;
@@ -341,7 +339,7 @@ __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const Di
         if (GRAD) {
           const int r = g + i * NG;
           const DpList& L = sm.list[i % kDpLists];
-          const uint4* st = &sm.ring[i % kDpStages][0][tid];
+          const uint4* st = &sm.ring[i % kDpStages][tid];
           const bool row = L.live == 2;
           const float mt = sm.stat[i % kDpLists].mt, rho = mt * p.c;
           float gA = L.sc * sm.stat[i % kDpLists].A;
@@ -353,13 +351,15 @@ __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const Di
           } else if (fabsf(rho) < kNear) {
             gA *= ex2_approx(-fmaf(mt, p.c, -rho));
             uint4* dst = reinterpret_cast<uint4*>(p.grad) + (size_t)r * nvr + v0 + tid;
+            const Pair cc = pair_of(p.c, p.c), rr = pair_of(-rho, -rho), gg = pair_of(gA, gA);
 #pragma unroll
             for (int u = 0; u < kDpU; ++u) {
               if (WHOLE ? u < mine : w0 + u * kDpSt + tid < w1) {
                 const uint4 x = st[u * kDpSt];
                 float gr[VW];
 #pragma unroll
-                for (int e = 0; e < VW; ++e) gr[e] = gA * ex2_approx(fmaf(TR::get(x, e), p.c, -rho));
+                for (int e = 0; e < VW; e += 2)
+                  unpair(pair_mul(gg, pair_terms<T>(x, e, cc, rr)), gr[e], gr[e + 1]);
                 if (WHOLE) __stcs(dst + u * kDpSt, Elem<T>::pack(gr));
                 else gwin.store(w0 + u * kDpSt + tid, Elem<T>::pack(gr));
               }
@@ -378,13 +378,12 @@ __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const Di
             }
           }
         }
-        __threadfence_block();
         bar_arrive(DP_WRITTEN + (i & 1), n_written);
       }
       if (GRAD) issue(t + 2);
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
-  } else if (warp == kDpStWarps) {
+  } else if (role == 0) {
     // ================================================================ exchange
 #pragma unroll 1
     for (int t = 0; t < n; ++t) {
@@ -392,14 +391,14 @@ __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const Di
       bar_sync(DP_SUMMED + (t & 1), n_summed);
       const DpList& L = sm.list[t % kDpLists];
       if (L.live != 0) {
-        const float4 v = lane < kDpStWarps ? sm.wpart[t & 1][lane] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+        const float2 v = lane < kDpStWarps ? sm.wpart[t & 1][lane] : make_float2(-INFINITY, 0.f);
         float m = v.x;
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        F2 s{v.y, v.z};
-        if (v.x != m) s = v.x == -INFINITY ? F2{0.f, 0.f} : f2_mul(s, weight_f2(v.x, m, c, sm.tab));
-        s = warp_sum_f2(s);
-        if (lane < C) push_f4(&sm.part[t & 1][rank], lane, make_float4(m, s.hi, s.lo, L.twice ? 1.f : 0.f));
+        float s = v.x == m ? v.y : v.y * ex2_approx((v.x - m) * p.c);
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (lane < C) push_f4(&sm.part[t & 1][rank], lane, make_float4(m, s, 0.f, L.twice ? 1.f : 0.f));
       }
       __syncwarp();
       cluster_arrive();
@@ -409,39 +408,46 @@ __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const Di
       __syncwarp();
       bar_arrive(DP_STAT + (t & 1), n_stat);
     }
-  } else if (warp == kDpStWarps + 1 + nl / 32) {
+  } else if (role == 2) {
     // ================================================================ loss
 #pragma unroll 1
     for (int j = 0; j <= n + 1; ++j) {
       if (j >= 1 && j <= n) cluster_wait();
-      if (j < n) cluster_arrive();
+      if (j < n) cluster_arrive_relaxed();
       if (j >= 2) {
         const int i = j - 2;
         bar_sync(DP_WRITTEN + (i & 1), n_written);
-        if (rank == 0) dp_loss(sm.list[i % kDpLists], sm.stat[i % kDpLists], p.inv_t, sm.tab, p.loss + g + i * NG);
+        if (i % C == rank) dp_loss(sm.list[i % kDpLists], sm.stat[i % kDpLists], p.inv_t, sm.tab, p.loss + g + i * NG);
       }
     }
   } else {
     // ================================================================ list
-    const int lt = tid - kDpSt - 32, lw = lt >> 5;  // lt < nl
+    const int lt = threadIdx.x - 32, lw = lt >> 5;  // lt < nl
     const F2 inv_t = f2_from(p.inv_t);
     const F2 l2e{kLog2eHi, kLog2eLo};
-    int id1, id2;                                   // of the row whose student value is loaded, and of the next
-    float lp1, lp2, s1;
+    // Two tokens a thread, lt and lt + nl.  What is loaded stays as it comes
+    // until the iteration that needs it: an index of the next row, a student's
+    // value of this one.
+    int id1[2], id2[2];
+    float lp1[2], lp2[2];
+    uint32_t s1[2];
     float wg1 = 1.f, tl1 = -INFINITY;               // the row's weight and tail
-    auto load_list = [&](int i, int& id, float& lp) {
-      id = -1;
-      lp = -INFINITY;
-      if (i < n && lt < k) {
-        const size_t r = (size_t)g + (size_t)i * NG;
-        const int v = __ldg(p.indices + r * k + lt);
-        if ((unsigned)v < (unsigned)p.V) id = v;
-        lp = __ldg(p.logprobs + r * k + lt);
+    auto load_list = [&](int i, int* id, float* lp) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        id[q] = -1;
+        lp[q] = -INFINITY;
+        if (i < n && lt + q * nl < k) {
+          const size_t at = ((size_t)g + (size_t)i * NG) * k + lt + q * nl;
+          id[q] = __ldg(p.indices + at);
+          lp[q] = __ldg(p.logprobs + at);
+        }
       }
     };
-    auto load_student = [&](int i, int id) {
-      if (id < 0) return -INFINITY;
-      return Elem<T>::load(student + ((size_t)g + (size_t)i * NG) * p.V + id);
+    auto load_student = [&](int i, const int* id) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        if ((unsigned)id[q] < (unsigned)p.V) s1[q] = Elem<T>::raw(student + ((size_t)g + (size_t)i * NG) * p.V + id[q]);
     };
     auto load_row = [&](int i) {
       if (i < n) {
@@ -451,7 +457,7 @@ __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const Di
       }
     };
     load_list(0, id1, lp1);
-    s1 = load_student(0, id1);
+    load_student(0, id1);
     load_list(1, id2, lp2);
     load_row(0);
 
@@ -459,20 +465,30 @@ __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const Di
     for (int j = 0; j <= n + 1; ++j) {
       if (j < n) {
         // ---- the list of row j
-        const float lp = id1 >= 0 ? lp1 : -INFINITY, s = s1, wgt = wg1, ltail = tl1;
-        const int id = id1;
-        id1 = id2;
-        lp1 = lp2;
-        s1 = load_student(j + 1, id1);
+        int id[2];
+        float lp[2], s[2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const bool on = (unsigned)id1[q] < (unsigned)p.V;
+          id[q] = on ? id1[q] : -1;
+          lp[q] = on ? lp1[q] : -INFINITY;
+          s[q] = on ? Elem<T>::of_raw(s1[q]) : -INFINITY;
+          id1[q] = id2[q];
+          lp1[q] = lp2[q];
+        }
+        const float wgt = wg1, ltail = tl1;
+        load_student(j + 1, id1);
         load_list(j + 2, id2, lp2);
         load_row(j + 1);
         DpList& L = sm.list[j % kDpLists];
         uint32_t* bits = sm.bits[j & 1];
         unsigned char* dirty = reinterpret_cast<unsigned char*>(sm.dirty[j & 1]);
         for (int w = lt; w < kDpSlice * VW / 128; w += nl) reinterpret_cast<uint4*>(bits)[w] = make_uint4(0u, 0u, 0u, 0u);
-        if (lt < kDpStWarps * 8 / 4) reinterpret_cast<uint32_t*>(dirty)[lt] = 0u;
+        for (int w = lt; w < kDpStWarps * 2; w += nl) reinterpret_cast<uint32_t*>(dirty)[w] = 0u;
         if (lt == 0) L.infinite = L.twice = 0;
-        float tm = lp != lp ? INFINITY : lp, km = s;  // a NaN makes the maximum +inf, and the row NaN
+        // a NaN makes the maximum +inf, and the row NaN
+        float tm = fmaxf(lp[0] != lp[0] ? INFINITY : lp[0], lp[1] != lp[1] ? INFINITY : lp[1]);
+        float km = fmaxf(s[0], s[1]);
 #pragma unroll
         for (int m = 16; m >= 1; m >>= 1) {
           tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, m));
@@ -486,29 +502,40 @@ __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const Di
           km = fmaxf(km, sm.lmax[w].y);
         }
         F2 w{0.f, 0.f}, ws{0.f, 0.f}, e1{0.f, 0.f};
-        if (id >= 0) {
-          const float kr = km == -INFINITY ? 0.f : km;
-          w = weight_f2(lp, tm, l2e, sm.tab);
-          ws = weight_f2(s, km, c, sm.tab);
-          if (w.hi != 0.f) {
-            // w (ln p_j - ln q_j), up to the row's constants
-            if ((s - kr) * inv_t.hi < -1.0e30f) L.infinite = 1;
-            else e1 = f2_mul(w, f2_add(two_diff(lp, tm), f2_neg(f2_mul(two_diff(s, kr), inv_t))));
+        const Window<T, const T> win(student, (size_t)(g + j * NG), p.V);
+        int v0, v1;
+        slice(win.vectors(), &v0, &v1);
+#pragma unroll 1
+        for (int q = 0; q < 2; ++q) {
+          if (q == 1 && k <= nl) break;             // (uniform) one token a thread
+          const int id_q = q ? id[1] : id[0];
+          const float lp_q = q ? lp[1] : lp[0], s_q = q ? s[1] : s[0];
+          F2 w_q{0.f, 0.f}, ws_q{0.f, 0.f};
+          if (id_q >= 0) {
+            const float kr = km == -INFINITY ? 0.f : km;
+            w_q = weight_f2(lp_q, tm, l2e, sm.tab);
+            ws_q = weight_f2(s_q, km, c, sm.tab);
+            if (w_q.hi != 0.f) {
+              // w (ln p_j - ln q_j), up to the row's constants
+              if ((s_q - kr) * inv_t.hi < -1.0e30f) L.infinite = 1;
+              else e1 = f2_add(e1, f2_mul(w_q, f2_add(two_diff(lp_q, tm), f2_neg(f2_mul(two_diff(s_q, kr), inv_t)))));
+            }
+            const int o = id_q + win.a0 - v0 * VW;
+            if (o >= 0 && o < (v1 - v0) * VW) {
+              const uint32_t bit = 1u << (o & 31);
+              if (atomicOr(&bits[o >> 5], bit) & bit) L.twice = 1;
+              const int lv = o / VW;                // vector lv = u * kDpSt + thread
+              dirty[(lv % kDpSt) / 32 * 8 + lv / kDpSt] = 1;
+            }
+            w = f2_add(w, w_q);
+            ws = f2_add(ws, ws_q);
           }
-          const Window<T, const T> win(student, (size_t)(g + j * NG), p.V);
-          int v0, v1;
-          slice(win.vectors(), &v0, &v1);
-          const int o = id + win.a0 - v0 * VW;
-          if (o >= 0 && o < (v1 - v0) * VW) {
-            const uint32_t bit = 1u << (o & 31);
-            if (atomicOr(&bits[o >> 5], bit) & bit) L.twice = 1;
-            const int lv = o / VW;                  // vector lv = u * kDpSt + thread
-            dirty[(lv % kDpSt) / 32 * 8 + lv / kDpSt] = 1;
+          if (lt + q * nl < kDpMaxK) {
+            L.sid[lt + q * nl] = id_q;
+            L.sw[lt + q * nl] = w_q.hi;
+            L.sq[lt + q * nl] = ws_q.hi;
           }
         }
-        L.sid[lt] = id;
-        L.sw[lt] = w.hi;
-        L.sq[lt] = ws.hi;
         w = warp_sum_f2(w);
         ws = warp_sum_f2(ws);
         e1 = warp_sum_f2(e1);
@@ -541,27 +568,28 @@ __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const Di
         bar_arrive(DP_LISTED + (j & 1), n_listed);
       }
       if (j >= 1 && j <= n) cluster_wait();
-      if (j < n) cluster_arrive();
+      if (j < n) cluster_arrive_relaxed();
       if (j >= 2) {
         // ---- the listed tokens of row j - 2, on top of its dense gradient
         const int i = j - 2;
         bar_sync(DP_WRITTEN + (i & 1), n_written);
         const DpList& L = sm.list[i % kDpLists];
-        if (GRAD && L.live == 2 && L.sid[lt] >= 0) {
+        if (GRAD && L.live == 2) {
           const DpStat& s = sm.stat[i % kDpLists];
-          const int id = L.sid[lt];
           const Window<T> gwin(static_cast<T*>(p.grad), (size_t)(g + i * NG), p.V);
           int v0, v1;
           slice(gwin.vectors(), &v0, &v1);
-          const int o = id + gwin.a0;
-          if (o >= v0 * VW && o < v1 * VW) {
-            float w = L.sw[lt];
+          for (int e = lt; e < k; e += nl) {
+            const int id = L.sid[e];
+            const int o = id + gwin.a0;
+            if (id < 0 || o < v0 * VW || o >= v1 * VW) continue;
+            float w = L.sw[e];
             if (s.twice) {
               w = 0.f;
               for (int q = 0; q < k; ++q)
                 if (L.sid[q] == id) w += L.sw[q];
             }
-            Elem<T>::store(gwin.base + o, L.sc * (L.sq[lt] * (s.Es * s.invS) - w * f2_rcp(L.Z)));
+            Elem<T>::store(gwin.base + o, L.sc * (L.sq[e] * (s.Es * s.invS) - w * __frcp_rn(L.Z.hi)));
           }
         }
       }

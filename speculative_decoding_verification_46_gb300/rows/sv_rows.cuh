@@ -17,6 +17,7 @@ namespace rows {
 // Bits of an element type's own lowest value: -inf.
 template <typename T> struct Elem;
 template <> struct Elem<float> {
+  __device__ static __forceinline__ float of_raw(uint32_t r) { return __uint_as_float(r); }
   __device__ static __forceinline__ __nv_bfloat162 both_ru(float) { return __nv_bfloat162{}; }   // not used
   __device__ static __forceinline__ float load(const float* p) { return *p; }
   __device__ static __forceinline__ void store(float* p, float x) { *p = x; }
@@ -29,6 +30,7 @@ template <> struct Elem<float> {
   }
 };
 template <> struct Elem<__nv_bfloat16> {
+  __device__ static __forceinline__ float of_raw(uint32_t r) { return __uint_as_float(r << 16); }
   // the smallest value >= x, twice
   __device__ static __forceinline__ __nv_bfloat162 both_ru(float x) { return __bfloat162bfloat162(__float2bfloat16_ru(x)); }
   __device__ static __forceinline__ float load(const __nv_bfloat16* p) { return __bfloat162float(*p); }
@@ -51,6 +53,7 @@ template <> struct Elem<__nv_bfloat16> {
   }
 };
 template <> struct Elem<__half> {
+  __device__ static __forceinline__ float of_raw(uint32_t r) { return __half2float(__ushort_as_half((unsigned short)r)); }
   __device__ static __forceinline__ __half2 both_ru(float x) { return __half2half2(__float2half_ru(x)); }
   __device__ static __forceinline__ float load(const __half* p) { return __half2float(*p); }
   __device__ static __forceinline__ void store(__half* p, float x) { *p = __float2half_rn(x); }
@@ -121,6 +124,41 @@ struct Window {
     }
   }
 };
+
+// ------------------------------------------------------------ paired float32
+// Two float32 operations an instruction (add, multiply and multiply-add).
+
+struct Pair {
+  unsigned long long v;
+};
+__device__ __forceinline__ Pair pair_of(float a, float b) {
+  Pair p;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(p.v) : "f"(a), "f"(b));
+  return p;
+}
+__device__ __forceinline__ void unpair(Pair p, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p.v)); }
+__device__ __forceinline__ Pair pair_fma(Pair a, Pair b, Pair c) {
+  Pair d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return d;
+}
+__device__ __forceinline__ Pair pair_mul(Pair a, Pair b) {
+  Pair d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+  return d;
+}
+__device__ __forceinline__ Pair pair_add(Pair a, Pair b) {
+  Pair d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+  return d;
+}
+// Elements t and t + 1 of a vector (t even), and 2^(x c - rho) of both.
+template <typename T>
+__device__ __forceinline__ Pair pair_terms(const uint4& x, int t, Pair c, Pair minus_rho) {
+  float a, b;
+  unpair(pair_fma(pair_of(Tr<T>::get(x, t), Tr<T>::get(x, t + 1)), c, minus_rho), a, b);
+  return pair_of(ex2_approx(a), ex2_approx(b));
+}
 
 // ------------------------------------------------------------ block reductions
 

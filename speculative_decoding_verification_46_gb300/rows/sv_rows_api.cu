@@ -118,7 +118,7 @@ sv_status launch_top_u(const sv::rows::TopParams& p, cudaStream_t stream) {
 }
 template <typename T>
 sv_status launch_top_rows(const sv::rows::TopParams& p, cudaStream_t stream) {
-  auto kern = sv::rows::top_row_kernel<T>;
+  auto kern = p.V % sv::Tr<T>::VW == 0 ? sv::rows::top_row_kernel<T, true> : sv::rows::top_row_kernel<T, false>;
   const size_t smem = (size_t)sv::rows::kTrStages * sv::rows::kTrStep * sizeof(uint4) +
                       (size_t)sv::rows::tr_capacity(p.k) * sizeof(unsigned long long);
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
@@ -175,7 +175,7 @@ sv_status launch_distill_pipe(sv::rows::DistillParams p, cudaStream_t stream) {
   constexpr int VW = sv::Tr<T>::VW;
   const long long nv = ceil_div((long long)p.V + (p.V % VW ? VW - 1 : 0), VW);
   const long long C = ceil_div(nv, sv::rows::kDpSlice);
-  if (C > sv::rows::kDiMaxC || p.k > sv::rows::kDpLi) return SV_ERR_UNSUPPORTED;
+  if (C > sv::rows::kDiMaxC || p.k > sv::rows::kDpMaxK) return SV_ERR_UNSUPPORTED;
   p.C = (int)C;
   p.SV = (int)ceil_div(nv, C);
   auto kern = p.V % VW == 0 ? sv::rows::distill_pipe_kernel<T, GRAD, true> : sv::rows::distill_pipe_kernel<T, GRAD, false>;

@@ -552,14 +552,10 @@ struct RunningSum {
   __device__ __forceinline__ float term(float x, float c) const { return ex2_approx(fmaf(x, c, -rho)); }
   __device__ __forceinline__ float term_far(float x, float c) const { return ex2_approx((x - m) * c); }
   __device__ __forceinline__ void take(float t) { s = f2_add(s, F2{t, 0.f}); }
-  __device__ __forceinline__ void add(float x, float c) {
-    if (x == -INFINITY) return;
-    raise(x, c);
-    take(far ? term_far(x, c) : term(x, c));
-  }
 };
 
-template <typename T>
+// WHOLE: V is a multiple of the vector width, so every row is whole vectors.
+template <typename T, bool WHOLE>
 __global__ void __launch_bounds__(kTlThreads, 3) top_row_kernel(const TopParams p) {
   using TR = Tr<T>;
   constexpr int VW = TR::VW;
@@ -577,16 +573,16 @@ __global__ void __launch_bounds__(kTlThreads, 3) top_row_kernel(const TopParams 
 
   auto issue = [&](int step) {
     uint4* slot = ring + (step % kTrStages) * kTrStep + tid;
+    const T* src = win.base + ((size_t)step * kTrStep + tid) * VW;
+    const int v0 = step * kTrStep + tid;
 #pragma unroll
     for (int u = 0; u < kTrU; ++u) {
-      const int v = step * kTrStep + u * kTlThreads + tid;
-      if (v < NV) {
-        if (win.whole(v)) {
-          const unsigned sa = (unsigned)__cvta_generic_to_shared(slot + u * kTlThreads);
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(sa), "l"(win.base + (size_t)v * VW) : "memory");
-        } else {
-          slot[u * kTlThreads] = win.load(v);
-        }
+      const int v = v0 + u * kTlThreads;
+      if (v < NV && (WHOLE || win.whole(v))) {
+        const unsigned sa = (unsigned)__cvta_generic_to_shared(slot + u * kTlThreads);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(sa), "l"(src + u * kTlThreads * VW) : "memory");
+      } else if (step < steps) {
+        slot[u * kTlThreads] = !WHOLE && v < NV ? win.load(v) : pad;
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -600,7 +596,7 @@ __global__ void __launch_bounds__(kTlThreads, 3) top_row_kernel(const TopParams 
   const float c = p.c;
   float thr = -INFINITY;
   int look = min(trig, k + max(k, 64));                              // candidates at which thr is raised next
-  int bad = 0, flag = 0;
+  int flag = 0;
   RunningSum acc;
   auto all_keys = [&](int n, auto f) {
     for (int e = tid; e < n; e += kTlThreads) f(keys[e]);
@@ -631,9 +627,8 @@ __global__ void __launch_bounds__(kTlThreads, 3) top_row_kernel(const TopParams 
     const uint4* stage = ring + (step % kTrStages) * kTrStep;
 #pragma unroll
     for (int u = 0; u < kTrU; ++u) {
-      x[u] = step * kTrStep + u * kTlThreads + tid < NV ? stage[u * kTlThreads + tid] : pad;
-      vm[u] = TR::template vmax<true>(x[u]);
-      bad |= !(vm[u] < INFINITY);                                    // NaN or +inf
+      x[u] = stage[u * kTlThreads + tid];
+      vm[u] = TR::template vmax<false>(x[u]);
     }
     if (step == 0) {
       uint32_t key[kTrU];
@@ -655,7 +650,8 @@ __global__ void __launch_bounds__(kTlThreads, 3) top_row_kernel(const TopParams 
       mc = fmaxf(mc, vm[u]);
     }
     acc.raise(mc, c);
-    if (acc.m > -INFINITY) {
+    {
+      // (with nothing but -inf so far rho is 0 and the terms are 0, or NaN)
       float s0 = 0.f, s1 = 0.f;
       if (!acc.far) {
 #pragma unroll
@@ -737,9 +733,14 @@ __global__ void __launch_bounds__(kTlThreads, 3) top_row_kernel(const TopParams 
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
 
+  __syncthreads();                                                   // the last step's candidates are in
+
   // ---- the record
-  bad = __syncthreads_or(bad);
+  // a NaN is in its thread's sum, +inf among the candidates
   const int have = sm.nk;
+  int bad = acc.s.hi != acc.s.hi;
+  for (int e = tid; e < have; e += kTlThreads) bad |= comp_val(keys[e]) == INFINITY;
+  bad = __syncthreads_or(bad);
   if (bad || have == 0) {
     top_write_bad(p, r);
     return;
