@@ -4,15 +4,22 @@
 // It counts the sequence's history and drafts that fall into the tile in
 // shared memory (a word per token: occurrences, and flags for prompt, draft
 // and bias; integer atomics, so the order of arrival does not matter) and
-// lists the tokens it met.  The rows then pass through in 16-byte vectors
-// with the mask applied and nothing else done, and only the listed tokens,
-// some hundreds of a tile's thousands, are computed and overwritten
-// afterwards.  So the pass that moves the bytes costs no more than a copy,
-// whatever the history holds, and an in-place call without a mask touches
-// the listed tokens alone.
+// lists the tokens it met: some hundreds of a tile's thousands.  Only those
+// are computed; everything else of a row is copied or masked in 16-byte
+// vectors, so the pass that moves the bytes costs no more than a copy,
+// whatever the history holds.  A row i differs from row 0 of its sequence
+// only by the drafts before it: tokens with the draft flag add them up from
+// the list of drafts.
 //
-// A row i differs from row 0 of its sequence only by the drafts before it:
-// tokens with the draft flag add them up from the list of drafts.
+//   adjust_staged_kernel   out is another tensor and there are listed tokens:
+//       each row of the tile passes through shared memory (a ring of
+//       cp.async stages, the next rows loading meanwhile), where its listed
+//       tokens are changed before it is written.  Changing them in `out`
+//       afterwards instead, with the kernel below, read and wrote their
+//       sectors a second time: 304 MB read from DRAM for 175 MB of logits, 9
+//       rows of 64 sequences after 8192 tokens.
+//   adjust_direct_kernel   in place (only vectors that a mask changes and the
+//       listed tokens are touched), or nothing is listed (a masked copy).
 //
 // The bound is HBM: every row is read and written once (vectors that a mask
 // rules out altogether are not read).
@@ -23,8 +30,9 @@
 namespace sv {
 namespace rows {
 
-constexpr int kAdThreads = 256;
-constexpr int kAdMaxTile = 8192;          // tokens per tile: 48 KB of shared memory, four CTAs per SM
+constexpr int kAdThreads = 512;           // two vectors of 16 bytes each per row of a full tile
+constexpr int kAdTileBytes = 16384;       // bytes of a row in a tile
+constexpr int kAdStages = 3;
 constexpr uint32_t kAdPrompt = 1u << 31;  // the token stands in the prompt
 constexpr uint32_t kAdDraft = 1u << 30;   // the token is one of the round's drafts
 constexpr uint32_t kAdBias = 1u << 29;    // the token has a bias
@@ -62,103 +70,262 @@ __device__ __forceinline__ void adjust_note(uint32_t* cnt, uint16_t* list, int* 
   }
 }
 
+// What the CTA has in shared memory.
 template <typename T>
-__global__ void __launch_bounds__(kAdThreads, 4) adjust_kernel(const AdjustParams p) {
+struct AdjustTile {
+  uint32_t* cnt;    // [tile]
+  int2* blist;      // [NB] (offset, entry)
+  uint16_t* list;   // [tile]
+  int* draft;       // [gamma]
+  int* nlist;
+  int* nb;
+  int b, t0, n, gb;
+};
+
+// The tile's tokens of the sequence; complete after the next barrier.
+template <typename T>
+__device__ __forceinline__ void adjust_collect(const AdjustParams& p, const AdjustTile<T>& s) {
+  const int tid = threadIdx.x, b = s.b, G = p.G1 - 1;
+  for (int i = tid; i < p.tile / 4; i += kAdThreads) reinterpret_cast<uint4*>(s.cnt)[i] = make_uint4(0u, 0u, 0u, 0u);
+  if (tid == 0) *s.nlist = *s.nb = 0;
+  if (p.count && p.draft && tid < s.gb) s.draft[tid] = __ldg(p.draft + (size_t)b * G + tid);
+  int len = 0, np = 0;
+  if (p.count && p.history) {
+    len = min(max(__ldg(p.history_len + b), 0), p.H);
+    np = p.prompt_len ? min(max(__ldg(p.prompt_len + b), 0), len) : 0;
+  }
+  const int32_t* h = p.history + (size_t)b * p.H;
+  __syncthreads();
+  for (int i0 = tid; i0 < len; i0 += 8 * kAdThreads) {
+    int tok[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) tok[u] = i0 + u * kAdThreads < len ? __ldg(h + i0 + u * kAdThreads) : -1;
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      adjust_note(s.cnt, s.list, s.nlist, tok[u], s.t0, s.n, i0 + u * kAdThreads < np ? kAdPrompt : 0u);
+  }
+  if (p.count && p.draft && tid < s.gb) adjust_note(s.cnt, s.list, s.nlist, s.draft[tid], s.t0, s.n, kAdDraft);
+  for (int i = tid; i < p.NB; i += kAdThreads) {
+    const int tok = __ldg(p.bias_tokens + (size_t)b * p.NB + i);
+    adjust_note(s.cnt, s.list, s.nlist, tok, s.t0, s.n, kAdBias);
+    if (tok >= s.t0 && tok < s.t0 + s.n) s.blist[atomicAdd(s.nb, 1)] = make_int2(tok - s.t0, i);
+  }
+}
+
+struct AdjustPenalties {
+  float rep, freq, pres;
+  __device__ __forceinline__ AdjustPenalties(const AdjustParams& p, int b)
+      : rep(p.repetition ? __ldg(p.repetition + b) : 1.f), freq(p.frequency ? __ldg(p.frequency + b) : 0.f),
+        pres(p.presence ? __ldg(p.presence + b) : 0.f) {}
+};
+
+// The mask row of a logits row: nullptr and *none = false without one, *none
+// = true where nothing is allowed.
+__device__ __forceinline__ const uint32_t* adjust_mask_row(const AdjustParams& p, size_t row, bool* none) {
+  int mi = -1;
+  if (p.mask) mi = p.mask_index ? __ldg(p.mask_index + row) : (int)row;
+  *none = mi >= p.M;
+  return mi >= 0 && mi < p.M ? p.mask + (size_t)mi * p.W : nullptr;
+}
+
+// The mask bits of the VW tokens from v on (v may lie up to VW - 1 before the row).
+template <int VW>
+__device__ __forceinline__ uint32_t adjust_bits(const uint32_t* mrow, int W, int v) {
+  const int w = max(v, 0) >> 5, sh = v - (w << 5);
+  const uint32_t lo = __ldg(mrow + w);
+  const uint32_t hi = (sh + VW > 32 && w + 1 < W) ? __ldg(mrow + w + 1) : 0u;
+  return (sh >= 0 ? __funnelshift_r(lo, hi, sh) : lo << -sh) & ((1u << VW) - 1u);
+}
+
+// The new value of the listed token at tile offset o in row i, from x.
+// false: the row leaves it as it is.
+template <typename T>
+__device__ __forceinline__ bool adjust_value(const AdjustParams& p, const AdjustTile<T>& s, const AdjustPenalties& pen,
+                                             int i, int o, const uint32_t* mrow, float* x) {
+  const uint32_t w = s.cnt[o];
+  const int v = s.t0 + o;
+  int c = (int)(w & kAdCount);
+  if (w & kAdDraft)
+    for (int j = 0; j < i; ++j) c += (s.draft[j] == v);
+  const bool seen = (w & kAdPrompt) || c > 0;
+  if (!seen && !(w & kAdBias)) return false;
+  if (mrow && !((__ldg(mrow + (v >> 5)) >> (v & 31)) & 1u)) return false;
+  float y = *x;
+  if (seen) {
+    y = y > 0.f ? __fdiv_rn(y, pen.rep) : y * pen.rep;
+    y -= fmaf(pen.freq, (float)c, c > 0 ? pen.pres : 0.f);
+  }
+  if (w & kAdBias) {
+    int last = -1;
+    for (int k = 0; k < *s.nb; ++k)
+      if (s.blist[k].x == o) last = max(last, s.blist[k].y);
+    y += __ldg(p.bias_values + (size_t)s.b * p.NB + last);
+  }
+  *x = y;
+  return true;
+}
+
+template <typename T>
+__device__ __forceinline__ AdjustTile<T> adjust_tile(const AdjustParams& p, unsigned char* smem, int* draft, int* counters) {
+  AdjustTile<T> s;
+  s.cnt = reinterpret_cast<uint32_t*>(smem);
+  s.blist = reinterpret_cast<int2*>(s.cnt + p.tile);
+  s.list = reinterpret_cast<uint16_t*>(s.blist + p.NB);
+  s.draft = draft;
+  s.nlist = counters;
+  s.nb = counters + 1;
+  s.b = blockIdx.x / p.tiles;
+  s.t0 = (blockIdx.x - s.b * p.tiles) * p.tile;
+  s.n = min(p.tile, p.V - s.t0);
+  s.gb = p.gamma_b ? min(max(__ldg(p.gamma_b + s.b), 0), p.G1 - 1) : p.G1 - 1;
+  return s;
+}
+
+// A vector with what the mask rules out set to -inf.
+template <typename T>
+__device__ __forceinline__ void adjust_masked(uint4& x, uint32_t bits) {
+  using TR = Tr<T>;
+  if (bits == (1u << TR::VW) - 1u) return;
+#pragma unroll
+  for (int t = 0; t < TR::VW; ++t)
+    if (!((bits >> t) & 1u)) TR::put(x, t, Elem<T>::kNegInf);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kAdThreads, 2) adjust_staged_kernel(const AdjustParams p) {
   using TR = Tr<T>;
   constexpr int VW = TR::VW;
   constexpr uint32_t kFull = (1u << VW) - 1u;
   extern __shared__ __align__(16) unsigned char smem_raw[];
-  uint32_t* cnt = reinterpret_cast<uint32_t*>(smem_raw);                        // [tile]
-  int2* blist = reinterpret_cast<int2*>(cnt + p.tile);                          // [NB] (offset, entry)
-  uint16_t* list = reinterpret_cast<uint16_t*>(blist + p.NB);                   // [tile]
   __shared__ int sdraft[kMaxG1];
-  __shared__ int nlist, nb;
+  __shared__ int counters[2];
   const int tid = threadIdx.x;
-  const int b = blockIdx.x / p.tiles;
-  const int t0 = (blockIdx.x - b * p.tiles) * p.tile;
-  const int n = min(p.tile, p.V - t0);
-  const int G = p.G1 - 1;
-  const int gb = p.gamma_b ? min(max(__ldg(p.gamma_b + b), 0), G) : G;
-  const bool sparse = p.count || p.NB;
+  const int SV = p.tile / VW + 1;                                  // vectors of a stage: a row may start inside one
+  uint4* ring = reinterpret_cast<uint4*>(smem_raw);                // [kAdStages][SV]
+  const AdjustTile<T> s = adjust_tile<T>(p, smem_raw + (size_t)kAdStages * SV * sizeof(uint4), sdraft, counters);
 
-  // ---- the tile's tokens of the sequence
-  if (sparse) {
-    for (int i = tid; i < p.tile; i += kAdThreads) cnt[i] = 0u;
-    if (tid == 0) nlist = nb = 0;
-    if (p.count && p.draft && tid < gb) sdraft[tid] = __ldg(p.draft + (size_t)b * G + tid);
-    __syncthreads();
-    if (p.count) {
-      if (p.history) {
-        const int len = min(max(__ldg(p.history_len + b), 0), p.H);
-        const int np = p.prompt_len ? min(max(__ldg(p.prompt_len + b), 0), len) : 0;
-        const int32_t* h = p.history + (size_t)b * p.H;
-        for (int i0 = tid; i0 < len; i0 += 8 * kAdThreads) {
-          int tok[8];
-#pragma unroll
-          for (int u = 0; u < 8; ++u) tok[u] = i0 + u * kAdThreads < len ? __ldg(h + i0 + u * kAdThreads) : -1;
-#pragma unroll
-          for (int u = 0; u < 8; ++u)
-            adjust_note(cnt, list, &nlist, tok[u], t0, n, i0 + u * kAdThreads < np ? kAdPrompt : 0u);
+  auto issue = [&](int i) {                                        // row i of the sequence into its stage
+    if (i <= s.gb) {
+      const size_t row = (size_t)s.b * p.G1 + i;
+      bool none;
+      const uint32_t* mrow = adjust_mask_row(p, row, &none);
+      const size_t e0 = row * (size_t)p.V + s.t0;
+      const int a = (int)(e0 % VW);
+      const T* src = static_cast<const T*>(p.logits) + (e0 - a);
+      uint4* st = ring + (size_t)(i % kAdStages) * SV;
+      const int nv = none ? 0 : (a + s.n + VW - 1) / VW;
+      for (int j = tid; j < nv; j += kAdThreads) {
+        const int o = j * VW - a;
+        if (o >= 0 && o + VW <= s.n) {
+          if (!mrow || adjust_bits<VW>(mrow, p.W, s.t0 + o) != 0u) {
+            const unsigned sa = (unsigned)__cvta_generic_to_shared(st + j);
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(sa), "l"(src + (size_t)j * VW) : "memory");
+          }
+        } else {
+          for (int t = 0; t < VW; ++t)
+            if (o + t >= 0 && o + t < s.n)
+              Elem<T>::store_raw(reinterpret_cast<T*>(st + j) + t, Elem<T>::raw(src + (size_t)j * VW + t));
         }
       }
-      if (p.draft && tid < gb) adjust_note(cnt, list, &nlist, sdraft[tid], t0, n, kAdDraft);
     }
-    for (int i = tid; i < p.NB; i += kAdThreads) {
-      const int tok = __ldg(p.bias_tokens + (size_t)b * p.NB + i);
-      adjust_note(cnt, list, &nlist, tok, t0, n, kAdBias);
-      if (tok >= t0 && tok < t0 + n) blist[atomicAdd(&nb, 1)] = make_int2(tok - t0, i);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int i = 0; i < kAdStages - 1; ++i) issue(i);
+  const AdjustPenalties pen(p, s.b);
+  adjust_collect(p, s);
+
+  for (int i = 0; i <= s.gb; ++i) {
+    issue(i + kAdStages - 1);                                      // its stage was written out an iteration ago
+    asm volatile("cp.async.wait_group %0;" ::"n"(kAdStages - 1) : "memory");
+    __syncthreads();                                               // row i is in (and, first, the counts are)
+    const size_t row = (size_t)s.b * p.G1 + i;
+    bool none;
+    const uint32_t* mrow = adjust_mask_row(p, row, &none);
+    const size_t e0 = row * (size_t)p.V + s.t0;
+    const int a = (int)(e0 % VW);
+    uint4* st = ring + (size_t)(i % kAdStages) * SV;
+    if (!none) {
+      T* elem = reinterpret_cast<T*>(st) + a;
+      const int nl = *s.nlist;
+      for (int e = tid; e < nl; e += kAdThreads) {
+        const int o = s.list[e];
+        float x = Elem<T>::load(elem + o);
+        if (adjust_value(p, s, pen, i, o, mrow, &x)) Elem<T>::store(elem + o, x);
+      }
+    }
+    __syncthreads();
+    T* dst = static_cast<T*>(p.out) + (e0 - a);
+    const int nv = (a + s.n + VW - 1) / VW;
+    for (int j = tid; j < nv; j += kAdThreads) {
+      const int o = j * VW - a;
+      const uint32_t bits = none ? 0u : mrow ? adjust_bits<VW>(mrow, p.W, s.t0 + o) : kFull;
+      uint4 x = make_uint4(TR::kPadWord, TR::kPadWord, TR::kPadWord, TR::kPadWord);
+      if (bits != 0u) {
+        x = st[j];
+        adjust_masked<T>(x, bits);
+      }
+      if (o >= 0 && o + VW <= s.n) {
+        __stcs(reinterpret_cast<uint4*>(dst + (size_t)j * VW), x);
+      } else {
+#pragma unroll
+        for (int t = 0; t < VW; ++t)
+          if (o + t >= 0 && o + t < s.n) Elem<T>::store_raw(dst + (size_t)j * VW + t, raw_of<T>(x, t));
+      }
     }
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kAdThreads, 2) adjust_direct_kernel(const AdjustParams p) {
+  using TR = Tr<T>;
+  constexpr int VW = TR::VW;
+  constexpr uint32_t kFull = (1u << VW) - 1u;
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  __shared__ int sdraft[kMaxG1];
+  __shared__ int counters[2];
+  const int tid = threadIdx.x;
+  const bool sparse = p.count || p.NB;
+  const AdjustTile<T> s = adjust_tile<T>(p, smem_raw, sdraft, counters);
+  if (sparse) adjust_collect(p, s);
 
   // ---- the rows, masked
-  for (int i = 0; i <= gb; ++i) {
-    const size_t row = (size_t)b * p.G1 + i;
-    int mi = -1;
-    if (p.mask) mi = p.mask_index ? __ldg(p.mask_index + row) : (int)row;
-    if (!p.copy && mi < 0) continue;
-    const bool none = mi >= p.M;                                   // nothing is allowed
-    const uint32_t* mrow = mi >= 0 && !none ? p.mask + (size_t)mi * p.W : nullptr;
-    const size_t e0 = row * (size_t)p.V + t0;
+  for (int i = 0; i <= s.gb; ++i) {
+    const size_t row = (size_t)s.b * p.G1 + i;
+    bool none;
+    const uint32_t* mrow = adjust_mask_row(p, row, &none);
+    if (!p.copy && !mrow && !none) continue;
+    const size_t e0 = row * (size_t)p.V + s.t0;
     const int a = (int)(e0 % VW);
     const T* src = static_cast<const T*>(p.logits) + (e0 - a);
     T* dst = static_cast<T*>(p.out) + (e0 - a);
-    const int nv = (a + n + VW - 1) / VW;
-    for (int j0 = tid; j0 < nv; j0 += 4 * kAdThreads) {
-      uint4 x[4];
-      uint32_t bits[4];
+    const int nv = (a + s.n + VW - 1) / VW;
+    for (int j0 = tid; j0 < nv; j0 += 2 * kAdThreads) {
+      uint4 x[2];
+      uint32_t bits[2];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < 2; ++u) {
         const int j = j0 + u * kAdThreads;
         const int o = j * VW - a;                                  // tile offset of the vector's first element
         bits[u] = none ? 0u : kFull;
-        if (j < nv && mrow) {
-          const int v = t0 + o;                                    // may reach VW - 1 before the row
-          const int w = max(v, 0) >> 5, sh = v - (w << 5);
-          uint32_t lo = __ldg(mrow + w);
-          const uint32_t hi = (sh + VW > 32 && w + 1 < p.W) ? __ldg(mrow + w + 1) : 0u;
-          bits[u] = (sh >= 0 ? __funnelshift_r(lo, hi, sh) : lo << -sh) & kFull;
-        }
-        const bool whole = o >= 0 && o + VW <= n;
+        if (j < nv && mrow) bits[u] = adjust_bits<VW>(mrow, p.W, s.t0 + o);
+        const bool whole = o >= 0 && o + VW <= s.n;
         if (j < nv && whole && bits[u] != 0u && (p.copy || bits[u] != kFull))
-          x[u] = __ldcs(reinterpret_cast<const uint4*>(src + (size_t)j * VW));
+          x[u] = *reinterpret_cast<const uint4*>(src + (size_t)j * VW);
       }
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < 2; ++u) {
         const int j = j0 + u * kAdThreads;
         if (j >= nv || (!p.copy && bits[u] == kFull)) continue;
         const int o = j * VW - a;
-        if (o >= 0 && o + VW <= n) {
-          if (bits[u] == 0u) {
-            x[u] = make_uint4(TR::kPadWord, TR::kPadWord, TR::kPadWord, TR::kPadWord);
-          } else if (bits[u] != kFull) {
-#pragma unroll
-            for (int t = 0; t < VW; ++t)
-              if (!((bits[u] >> t) & 1u)) TR::put(x[u], t, Elem<T>::kNegInf);
-          }
-          __stcs(reinterpret_cast<uint4*>(dst + (size_t)j * VW), x[u]);
+        if (o >= 0 && o + VW <= s.n) {
+          if (bits[u] == 0u) x[u] = make_uint4(TR::kPadWord, TR::kPadWord, TR::kPadWord, TR::kPadWord);
+          else adjust_masked<T>(x[u], bits[u]);
+          *reinterpret_cast<uint4*>(dst + (size_t)j * VW) = x[u];
         } else {
           for (int t = 0; t < VW; ++t) {
-            if (o + t < 0 || o + t >= n) continue;
+            if (o + t < 0 || o + t >= s.n) continue;
             const bool ok = (bits[u] >> t) & 1u;
             if (ok && !p.copy) continue;
             Elem<T>::store_raw(dst + (size_t)j * VW + t,
@@ -169,43 +336,22 @@ __global__ void __launch_bounds__(kAdThreads, 4) adjust_kernel(const AdjustParam
     }
   }
   if (!sparse) return;
-  __syncthreads();   // the counts are complete, and the rows written
+  __syncthreads();   // the counts are complete, and the rows masked
 
-  // ---- the listed tokens of every row
-  const int nl = nlist;
-  if (nl == 0) return;
-  const float rep = p.repetition ? __ldg(p.repetition + b) : 1.f;
-  const float freq = p.frequency ? __ldg(p.frequency + b) : 0.f;
-  const float pres = p.presence ? __ldg(p.presence + b) : 0.f;
-  const long long items = (long long)nl * (gb + 1);
-  for (long long it = tid; it < items; it += kAdThreads) {
-    const int i = (int)(it / nl);
-    const int o = list[(int)(it - (long long)i * nl)];
-    const uint32_t w = cnt[o];
-    int c = (int)(w & kAdCount);
-    if (w & kAdDraft)
-      for (int j = 0; j < i; ++j) c += (sdraft[j] == t0 + o);
-    const bool seen = (w & kAdPrompt) || c > 0;
-    if (!seen && !(w & kAdBias)) continue;
-    const size_t row = (size_t)b * p.G1 + i;
-    if (p.mask) {
-      const int mi = p.mask_index ? __ldg(p.mask_index + row) : (int)row;
-      const int v = t0 + o;
-      if (mi >= p.M || (mi >= 0 && !((__ldg(p.mask + (size_t)mi * p.W + (v >> 5)) >> (v & 31)) & 1u))) continue;
+  // ---- the listed tokens of every row, in place
+  const int nl = *s.nlist;
+  const AdjustPenalties pen(p, s.b);
+  for (int i = 0; i <= s.gb; ++i) {
+    const size_t row = (size_t)s.b * p.G1 + i;
+    bool none;
+    const uint32_t* mrow = adjust_mask_row(p, row, &none);
+    if (none) continue;
+    T* elem = static_cast<T*>(p.out) + row * (size_t)p.V + s.t0;
+    for (int e = tid; e < nl; e += kAdThreads) {
+      const int o = s.list[e];
+      float x = Elem<T>::load(elem + o);
+      if (adjust_value(p, s, pen, i, o, mrow, &x)) Elem<T>::store(elem + o, x);
     }
-    const size_t e = row * (size_t)p.V + t0 + o;
-    float x = Elem<T>::load(static_cast<const T*>(p.logits) + e);
-    if (seen) {
-      x = x > 0.f ? __fdiv_rn(x, rep) : x * rep;
-      x -= fmaf(freq, (float)c, c > 0 ? pres : 0.f);
-    }
-    if (w & kAdBias) {
-      int last = -1;
-      for (int k = 0; k < nb; ++k)
-        if (blist[k].x == o) last = max(last, blist[k].y);
-      x += __ldg(p.bias_values + (size_t)b * p.NB + last);
-    }
-    Elem<T>::store(static_cast<T*>(p.out) + e, x);
   }
 }
 

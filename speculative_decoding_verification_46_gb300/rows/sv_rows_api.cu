@@ -58,31 +58,35 @@ void exponent_scale(float temperature, float* hi, float* lo) {
 
 // ---------------------------------------------------------------- adjust
 
+// Tokens per tile: 16 KB of a row where that still gives every SM two CTAs,
+// fewer for small calls, down to 256 tokens; the tiles of a row are then made
+// equal.
+void choose_tile(sv::rows::AdjustParams& p, int elem) {
+  const long long want = 2ll * sm_count();
+  long long tile = ceil_div((long long)p.B * p.V, want);
+  tile = std::min<long long>(std::max<long long>(tile, 256), sv::rows::kAdTileBytes / elem);
+  p.tiles = (int)ceil_div(p.V, tile);
+  p.tile = (int)(ceil_div(ceil_div(p.V, p.tiles), 64) * 64);
+  p.tiles = (int)ceil_div(p.V, p.tile);
+}
+
 template <typename T>
-sv_status launch_adjust(const sv::rows::AdjustParams& p, cudaStream_t stream) {
-  auto kern = sv::rows::adjust_kernel<T>;
-  const bool sparse = p.count || p.NB;
-  const size_t smem = sparse ? (size_t)p.tile * 6 + (size_t)p.NB * 8 : 0;
+sv_status launch_adjust(sv::rows::AdjustParams p, cudaStream_t stream) {
+  choose_tile(p, (int)sizeof(T));
+  const long long grid = (long long)p.B * p.tiles;
+  if (grid > 0x7fffffffll) return SV_ERR_UNSUPPORTED;
+  const bool sparse = p.count || p.NB, staged = p.copy && sparse;
+  auto kern = staged ? sv::rows::adjust_staged_kernel<T> : sv::rows::adjust_direct_kernel<T>;
+  size_t smem = sparse ? (size_t)p.tile * 6 + (size_t)p.NB * 8 : 0;
+  if (staged) smem += (size_t)sv::rows::kAdStages * (p.tile / sv::Tr<T>::VW + 1) * 16;
   // (the kernel's static shared memory counts toward the 48 KB that need no opt-in)
   if (smem > 32 * 1024 &&
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
     cudaGetLastError();
     return SV_ERR_CUDA;
   }
-  const long long grid = (long long)p.B * p.tiles;
   kern<<<(unsigned)grid, sv::rows::kAdThreads, smem, stream>>>(p);
   return launched();
-}
-
-// Tokens per tile: 8192 where that still gives every SM four CTAs, fewer for
-// small calls, down to 256; the tiles of a row are then made equal.
-void choose_tile(sv::rows::AdjustParams& p) {
-  const long long want = 4ll * sm_count();
-  long long tile = ceil_div((long long)p.B * p.V, want);
-  tile = std::min<long long>(std::max<long long>(tile, 256), sv::rows::kAdMaxTile);
-  p.tiles = (int)ceil_div(p.V, tile);
-  p.tile = (int)(ceil_div(ceil_div(p.V, p.tiles), 64) * 64);
-  p.tiles = (int)ceil_div(p.V, p.tile);
 }
 
 // ---------------------------------------------------------------- top logits
@@ -324,8 +328,6 @@ extern "C" sv_status sv_adjust_logits(int B, int gamma, int V, const void* logit
   p.W = (V + 31) / 32;
   p.mask_index = mask_index;
   if (!p.copy && !p.count && !p.NB && !p.mask) return SV_OK;   // nothing to do in place
-  choose_tile(p);
-  if ((long long)p.B * p.tiles > 0x7fffffffll) return SV_ERR_UNSUPPORTED;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   switch (dtype) {
     case SV_DTYPE_F32: return launch_adjust<float>(p, s);
