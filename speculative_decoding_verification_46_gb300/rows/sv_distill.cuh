@@ -61,8 +61,6 @@ __device__ __forceinline__ float weight_fast(float d, float c, float c_lo) {
 }
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-// for threads that have written nothing the other CTAs read
-__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 // Store v at the address `local` has in the shared memory of CTA `rank` of the cluster.

@@ -2,8 +2,12 @@
 // row, so that loading, summing, exchanging and writing overlap between
 // neighbouring rows instead of following one another within each.
 //
-// The warps of a CTA have four roles and meet only where one needs what
-// another made (named barriers, two of each in turn; no spinning):
+// The warps of a CTA have four roles and wait for one another only where one
+// needs what another made, through mbarriers in shared memory: a warp that
+// finds its barrier complete goes on alone, so the streaming warps drift
+// apart and keep the pipes busy with different phases.  (With named barriers,
+// which make all waiting warps meet, half of the time went to the slowest of
+// them.)
 //
 //   streaming (22 warps)  own the CTA's slice of every row through a ring of
 //       kDpStages cp.async stages private to each thread (a thread reads back
@@ -14,13 +18,17 @@
 //       bitmap that takes the tokens out of the streams, and at the end the
 //       tokens' own gradient on top of the dense one.  The loads of a list
 //       are issued one row before they are used.
-//   exchange (1 warp)  the CTA's part of row t to all CTAs of the cluster (one
-//       cluster barrier per row) and from the C parts the row's statistics.
+//   exchange (1 warp)  the CTA's part of row t to all CTAs of the cluster, and
+//       from the C parts the row's statistics.
 //   loss (1 warp)  three logarithms per row; the CTAs take the rows in turn.
 //
 // So every dependent chain - gather, two-float sums, exchange, logarithms -
 // has a whole row's streaming time to finish in.  The forward pass alone is
 // the same without the gradient.
+//
+// Every wait is bounded: a role that gives up leaves its loop, the others
+// follow as their own waits run out, and the losses not yet written become
+// NaN.
 //
 // Bound: HBM, with instruction issue close behind.
 #pragma once
@@ -66,17 +74,64 @@ struct DpSmem {
   DpList list[kDpLists];
   DpStat stat[kDpLists];
   float4 part[2][kDiMaxC];              // (maximum, sum, -, twice)
-  float2 wpart[2][kDpStWarps];
+  float2 wpart[4][kDpStWarps];
   F2 lsum[kDpLi / 32][3];
   float2 lmax[kDpLi / 32];
   float tab[128];
+  // mbarriers, each a ring over rows
+  unsigned long long summed[4];         // streaming warps -> exchange, list: row t is summed
+  unsigned long long known[4];          // exchange -> streaming: row t's statistics
+  unsigned long long parts[2];          // exchange warps of all CTAs -> exchange: row t's parts
+  unsigned long long listed[2];         // list -> streaming: row t's list
+  unsigned long long written[2];        // streaming warps -> list: row t's dense gradient
+  unsigned long long ready[kDpLists];   // exchange -> loss: row t's statistics
+  unsigned long long done[kDpLists];    // loss -> list: row t's loss is written, its list may be reused
 };
 
-// Named barriers: each pair alternates by row, so that the side that only
-// announces may be a row ahead of the side that waits.
-enum { DP_SUMMED = 1, DP_STAT = 3, DP_WRITTEN = 5, DP_LISTED = 7, DP_LIST = 9 };
-__device__ __forceinline__ void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
-__device__ __forceinline__ void bar_arrive(int id, int n) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(n) : "memory"); }
+// The list warps' own meeting point (all of them wait, so a named barrier);
+// returns whether all of them say yes.
+__device__ __forceinline__ bool list_meet(int n, bool yes) {
+  uint32_t all;
+  asm volatile("{\n.reg .pred p, q;\nsetp.ne.u32 p, %2, 0;\nbarrier.cta.red.and.pred q, 1, %1, p;\nselp.u32 %0, 1, 0, q;\n}"
+               : "=r"(all) : "r"(n), "r"((uint32_t)yes) : "memory");
+  return all != 0u;
+}
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void mb_init(unsigned long long* b, int count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(b)), "r"(count) : "memory");
+}
+// One arrival for the calling warp, after everything its lanes did.
+__device__ __forceinline__ void mb_arrive(unsigned long long* b) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0)
+    asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_addr(b)) : "memory");
+}
+// Wait for phase `phase` (0, 1, ...) of the barrier, all lanes; false: given up
+// (after 20 ms at least; a row takes microseconds).
+constexpr int kDpPatience = 1 << 20;
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool mb_wait(unsigned long long* b, int phase) {
+  const uint32_t a = smem_addr(b), parity = phase & 1;
+  uint32_t done = 0u;
+#pragma unroll 1
+  for (int i = 0; i < kDpPatience && !done; ++i) {
+    if (CLUSTER)
+      asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
+                   : "=r"(done) : "r"(a), "r"(parity) : "memory");
+    else
+      asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
+                   : "=r"(done) : "r"(a), "r"(parity) : "memory");
+  }
+  return __all_sync(0xffffffffu, done != 0u);
+}
+// Arrive at the barrier that `b` is in CTA `rank` of the cluster, after this
+// thread's writes to that CTA's shared memory.
+__device__ __forceinline__ void mb_arrive_remote(unsigned long long* b, int rank) {
+  uint32_t d;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(d) : "r"(smem_addr(b)), "r"(rank));
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(d) : "memory");
+}
 
 // ln a to about 40 bits, a a normalised two-float number >= 2^-100: a float
 // logarithm y corrected by a e^-y - 1.
@@ -189,8 +244,6 @@ __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const Di
   const int role = threadIdx.x < 32 ? 0 : threadIdx.x < 32 + nl ? 1 : threadIdx.x < 64 + nl ? 2 : 3;
   const F2 c{p.c, p.c_lo};
   const T* student = static_cast<const T*>(p.student);
-  // barrier sizes
-  const int n_summed = kDpSt + 32, n_stat = kDpSt + 32, n_written = kDpSt + nl + 32, n_listed = nl + kDpSt + 32;
   // the CTA's vectors of a row [v0, v1)
   auto slice = [&](int nv, int* v0, int* v1) {
     *v0 = min(rank * p.SV, nv);
@@ -198,9 +251,25 @@ __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const Di
   };
 
   for (int i = threadIdx.x; i < 128; i += blockDim.x) sm.tab[i] = i < 64 ? __ldg(kExp2Hi + i) : __ldg(kExp2Lo + i - 64);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 4; ++i) {
+      mb_init(&sm.summed[i], kDpStWarps);
+      mb_init(&sm.known[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mb_init(&sm.parts[i], C);
+      mb_init(&sm.listed[i], 1);
+      mb_init(&sm.written[i], kDpStWarps);
+    }
+    for (int i = 0; i < kDpLists; ++i) {
+      mb_init(&sm.ready[i], 1);
+      mb_init(&sm.done[i], 1);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
   __syncthreads();
   cluster_arrive();
-  cluster_wait();                                   // every CTA of the cluster runs: its shared memory can be written
+  cluster_wait();                                   // every CTA of the cluster runs, its barriers stand
 
   if (role == 3) {
     // ================================================================ streaming
@@ -258,7 +327,7 @@ __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const Di
       if (t < n) {
         // ---- row t without its listed tokens
         asm volatile("cp.async.wait_group %0;" ::"n"(GRAD ? 1 : 2) : "memory");
-        bar_sync(DP_LISTED + (t & 1), n_listed);
+        if (!mb_wait(&sm.listed[t & 1], t >> 1)) break;
         if (sm.list[t % kDpLists].live != 0) {
           const uint4* st = &sm.ring[t % kDpStages][tid];
           int m_t = mine;
@@ -324,19 +393,19 @@ __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const Di
           // chains of 12 terms, then a tree
 #pragma unroll
           for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-          if (lane == 0) sm.wpart[t & 1][warp] = make_float2(m, s * fix);
+          if (lane == 0) sm.wpart[t & 3][warp] = make_float2(m, s * fix);
         }
-        bar_arrive(DP_SUMMED + (t & 1), n_summed);
+        mb_arrive(&sm.summed[t & 3]);
         if (!GRAD) issue(t + 3);
       }
-      // (the cluster barrier of row t - 1 is long complete; the exchange warp is who needs it)
-      if (t >= 1) cluster_wait();
-      if (t < n) cluster_arrive_relaxed();
-      if (t >= 1) {
+      if (!GRAD) {
+        // the ring of the warps' parts holds four rows
+        if (t >= 3 && !mb_wait(&sm.known[(t - 3) & 3], (t - 3) >> 2)) break;
+      } else if (t >= 1) {
         // ---- row t - 1's gradient
         const int i = t - 1;
-        bar_sync(DP_STAT + (i & 1), n_stat);
-        if (GRAD) {
+        if (!mb_wait(&sm.known[i & 3], i >> 2)) break;
+        {
           const int r = g + i * NG;
           const DpList& L = sm.list[i % kDpLists];
           const uint4* st = &sm.ring[i % kDpStages][tid];
@@ -378,7 +447,7 @@ __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const Di
             }
           }
         }
-        bar_arrive(DP_WRITTEN + (i & 1), n_written);
+        mb_arrive(&sm.written[i & 1]);
       }
       if (GRAD) issue(t + 2);
     }
@@ -387,11 +456,10 @@ __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const Di
     // ================================================================ exchange
 #pragma unroll 1
     for (int t = 0; t < n; ++t) {
-      bar_sync(DP_LISTED + (t & 1), n_listed);
-      bar_sync(DP_SUMMED + (t & 1), n_summed);
+      if (!mb_wait(&sm.summed[t & 3], t >> 2)) break;  // (which follows row t's list)
       const DpList& L = sm.list[t % kDpLists];
       if (L.live != 0) {
-        const float2 v = lane < kDpStWarps ? sm.wpart[t & 1][lane] : make_float2(-INFINITY, 0.f);
+        const float2 v = lane < kDpStWarps ? sm.wpart[t & 3][lane] : make_float2(-INFINITY, 0.f);
         float m = v.x;
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -400,26 +468,24 @@ __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const Di
         for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
         if (lane < C) push_f4(&sm.part[t & 1][rank], lane, make_float4(m, s, 0.f, L.twice ? 1.f : 0.f));
       }
-      __syncwarp();
-      cluster_arrive();
-      cluster_wait();
+      if (lane < C) mb_arrive_remote(&sm.parts[t & 1], lane);
+      if (!mb_wait<true>(&sm.parts[t & 1], t >> 1)) break;
       dp_statistics(sm.part[t & 1], C, L, k, c, sm.tab, sm.stat[t % kDpLists],
                     !GRAD && rank == 0 && p.stats ? p.stats + (size_t)(g + t * NG) * 8 : nullptr);
-      __syncwarp();
-      bar_arrive(DP_STAT + (t & 1), n_stat);
+      mb_arrive(&sm.known[t & 3]);
+      mb_arrive(&sm.ready[t % kDpLists]);
     }
   } else if (role == 2) {
     // ================================================================ loss
+    int i = 0;
 #pragma unroll 1
-    for (int j = 0; j <= n + 1; ++j) {
-      if (j >= 1 && j <= n) cluster_wait();
-      if (j < n) cluster_arrive_relaxed();
-      if (j >= 2) {
-        const int i = j - 2;
-        bar_sync(DP_WRITTEN + (i & 1), n_written);
-        if (i % C == rank) dp_loss(sm.list[i % kDpLists], sm.stat[i % kDpLists], p.inv_t, sm.tab, p.loss + g + i * NG);
-      }
+    for (; i < n; ++i) {
+      if (!mb_wait(&sm.ready[i % kDpLists], i / kDpLists)) break;
+      if (i % C == rank) dp_loss(sm.list[i % kDpLists], sm.stat[i % kDpLists], p.inv_t, sm.tab, p.loss + g + i * NG);
+      mb_arrive(&sm.done[i % kDpLists]);
     }
+    for (; i < n; ++i)                              // given up
+      if (i % C == rank && lane == 0) p.loss[g + i * NG] = __uint_as_float(0x7fffffffu);
   } else {
     // ================================================================ list
     const int lt = threadIdx.x - 32, lw = lt >> 5;  // lt < nl
@@ -432,6 +498,7 @@ __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const Di
     float lp1[2], lp2[2];
     uint32_t s1[2];
     float wg1 = 1.f, tl1 = -INFINITY;               // the row's weight and tail
+    bool ok = true;
     auto load_list = [&](int i, int* id, float* lp) {
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
@@ -462,7 +529,7 @@ __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const Di
     load_row(0);
 
 #pragma unroll 1
-    for (int j = 0; j <= n + 1; ++j) {
+    for (int j = 0; j <= (GRAD ? n + 1 : n - 1); ++j) {
       if (j < n) {
         // ---- the list of row j
         int id[2];
@@ -480,6 +547,9 @@ __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const Di
         load_student(j + 1, id1);
         load_list(j + 2, id2, lp2);
         load_row(j + 1);
+        // the bitmap was row j - 2's, the list row j - kDpLists's
+        if (j >= 2) ok &= mb_wait(&sm.summed[(j - 2) & 3], (j - 2) >> 2);
+        if (j >= kDpLists) ok &= mb_wait(&sm.done[j % kDpLists], j / kDpLists - 1);
         DpList& L = sm.list[j % kDpLists];
         uint32_t* bits = sm.bits[j & 1];
         unsigned char* dirty = reinterpret_cast<unsigned char*>(sm.dirty[j & 1]);
@@ -495,7 +565,7 @@ __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const Di
           km = fmaxf(km, __shfl_xor_sync(0xffffffffu, km, m));
         }
         if (lane == 0) sm.lmax[lw] = make_float2(tm, km);
-        bar_sync(DP_LIST, nl);
+        if (!list_meet(nl, ok)) break;              // one gave up: all do, here
         tm = ltail != ltail ? INFINITY : ltail;
         for (int w = 0; w < nl / 32; ++w) {
           tm = fmaxf(tm, sm.lmax[w].x);
@@ -544,7 +614,7 @@ __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const Di
           sm.lsum[lw][1] = ws;
           sm.lsum[lw][2] = e1;
         }
-        bar_sync(DP_LIST, nl);
+        list_meet(nl, true);
         if (lt < 3) {                               // one of the three sums each
           F2 a = sm.lsum[0][lt];
           for (int q = 1; q < nl / 32; ++q) a = f2_add(a, sm.lsum[q][lt]);
@@ -564,17 +634,14 @@ __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const Di
             L.E1 = a;
           }
         }
-        __syncwarp();
-        bar_arrive(DP_LISTED + (j & 1), n_listed);
+        if (lw == 0) mb_arrive(&sm.listed[j & 1]);  // (the other list warps' part lies before the barrier above)
       }
-      if (j >= 1 && j <= n) cluster_wait();
-      if (j < n) cluster_arrive_relaxed();
-      if (j >= 2) {
+      if (GRAD && j >= 2) {
         // ---- the listed tokens of row j - 2, on top of its dense gradient
         const int i = j - 2;
-        bar_sync(DP_WRITTEN + (i & 1), n_written);
+        ok &= mb_wait(&sm.written[i & 1], i >> 1);
         const DpList& L = sm.list[i % kDpLists];
-        if (GRAD && L.live == 2) {
+        if (ok && L.live == 2) {
           const DpStat& s = sm.stat[i % kDpLists];
           const Window<T> gwin(static_cast<T*>(p.grad), (size_t)(g + i * NG), p.V);
           int v0, v1;
@@ -595,6 +662,8 @@ __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const Di
       }
     }
   }
+  cluster_arrive();
+  cluster_wait();                                   // nobody leaves while its shared memory may be written
 }
 
 }  // namespace rows
