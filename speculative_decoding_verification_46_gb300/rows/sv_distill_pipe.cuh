@@ -14,7 +14,7 @@
 //       only what it copied).  Per row t: sum the slice without its listed
 //       tokens to (maximum, sum); then write row t - 1's gradient out of the
 //       ring and start loading row t + 2 into the stage that frees.
-//   list (1 warp per 32 listed tokens, 4 at most)  the teacher's softmax and the student's weights there (two-float), the
+//   list (two groups of up to 2 warps, a row each in turn)  the teacher's softmax and the student's weights there (two-float), the
 //       bitmap that takes the tokens out of the streams, and at the end the
 //       tokens' own gradient on top of the dense one.  The loads of a list
 //       are issued one row before they are used.
@@ -40,17 +40,18 @@ namespace rows {
 
 constexpr int kDpSt = 704;              // streaming threads
 constexpr int kDpStWarps = kDpSt / 32;
-constexpr int kDpLi = 128;              // most list threads
-constexpr int kDpMaxK = 2 * kDpLi;      // the largest list: two tokens a thread
-constexpr int kDpMaxThreads = kDpSt + 32 + kDpLi + 32;
+constexpr int kDpLi = 64;               // most list threads of a group
+constexpr int kDpLiE = 4;               // tokens a list thread
+constexpr int kDpMaxK = kDpLiE * kDpLi; // the largest list
+constexpr int kDpMaxThreads = kDpSt + 32 + 2 * kDpLi + 32;
 constexpr int kDpSlice = 4096;          // most vectors per CTA and row
 constexpr int kDpU = (kDpSlice + kDpSt - 1) / kDpSt;   // per streaming thread
 constexpr int kDpStages = 3;
 constexpr int kDpLists = 6;             // rows whose lists are alive
 
-// list threads, and threads of a CTA, for lists of k tokens
-__host__ __device__ constexpr int dp_list_threads(int k) { return k > kDpLi ? kDpLi : (k + 31) / 32 * 32; }
-__host__ __device__ constexpr int dp_threads(int k) { return kDpSt + 32 + dp_list_threads(k) + 32; }
+// list threads of a group, and threads of a CTA, for lists of k tokens
+__host__ __device__ constexpr int dp_list_threads(int k) { return k > 32 ? kDpLi : 32; }
+__host__ __device__ constexpr int dp_threads(int k) { return kDpSt + 32 + 2 * dp_list_threads(k) + 32; }
 
 struct DpList {
   int sid[kDpMaxK];                     // listed tokens (-1: ignored)
@@ -75,25 +76,25 @@ struct DpSmem {
   DpStat stat[kDpLists];
   float4 part[2][kDiMaxC];              // (maximum, sum, -, twice)
   float2 wpart[4][kDpStWarps];
-  F2 lsum[kDpLi / 32][3];
-  float2 lmax[kDpLi / 32];
+  F2 lsum[2][kDpLi / 32][3];            // by group
+  float2 lmax[2][kDpLi / 32];
   float tab[128];
   // mbarriers, each a ring over rows
   unsigned long long summed[4];         // streaming warps -> exchange, list: row t is summed
   unsigned long long known[4];          // exchange -> streaming: row t's statistics
   unsigned long long parts[2];          // exchange warps of all CTAs -> exchange: row t's parts
   unsigned long long listed[2];         // list -> streaming: row t's list
-  unsigned long long written[2];        // streaming warps -> list: row t's dense gradient
+  unsigned long long written[4];        // streaming warps -> list: row t's dense gradient
   unsigned long long ready[kDpLists];   // exchange -> loss: row t's statistics
   unsigned long long done[kDpLists];    // loss -> list: row t's loss is written, its list may be reused
 };
 
-// The list warps' own meeting point (all of them wait, so a named barrier);
-// returns whether all of them say yes.
-__device__ __forceinline__ bool list_meet(int n, bool yes) {
+// The meeting point of a list group (all of its warps wait, so a named
+// barrier); returns whether all of them say yes.
+__device__ __forceinline__ bool list_meet(int group, int n, bool yes) {
   uint32_t all;
-  asm volatile("{\n.reg .pred p, q;\nsetp.ne.u32 p, %2, 0;\nbarrier.cta.red.and.pred q, 1, %1, p;\nselp.u32 %0, 1, 0, q;\n}"
-               : "=r"(all) : "r"(n), "r"((uint32_t)yes) : "memory");
+  asm volatile("{\n.reg .pred p, q;\nsetp.ne.u32 p, %2, 0;\nbarrier.cta.red.and.pred q, %3, %1, p;\nselp.u32 %0, 1, 0, q;\n}"
+               : "=r"(all) : "r"(n), "r"((uint32_t)yes), "r"(1 + group) : "memory");
   return all != 0u;
 }
 
@@ -237,11 +238,11 @@ __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const Di
   const int g = blockIdx.x / C, NG = gridDim.x / C;
   const int n = (p.R - g + NG - 1) / NG;            // rows of this cluster: g, g + NG, ...
   const int k = p.k;
-  const int nl = dp_list_threads(k);
+  const int nl = dp_list_threads(k);                // list threads of a group
   // the roles, by warp: exchange, list, loss, streaming (the later warps of a
   // scheduler wait for the earlier ones, and the streaming warps always have
   // something to issue)
-  const int role = threadIdx.x < 32 ? 0 : threadIdx.x < 32 + nl ? 1 : threadIdx.x < 64 + nl ? 2 : 3;
+  const int role = threadIdx.x < 32 ? 0 : threadIdx.x < 32 + 2 * nl ? 1 : threadIdx.x < 64 + 2 * nl ? 2 : 3;
   const F2 c{p.c, p.c_lo};
   const T* student = static_cast<const T*>(p.student);
   // the CTA's vectors of a row [v0, v1)
@@ -255,11 +256,11 @@ __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const Di
     for (int i = 0; i < 4; ++i) {
       mb_init(&sm.summed[i], kDpStWarps);
       mb_init(&sm.known[i], 1);
+      mb_init(&sm.written[i], kDpStWarps);
     }
     for (int i = 0; i < 2; ++i) {
       mb_init(&sm.parts[i], C);
       mb_init(&sm.listed[i], 1);
-      mb_init(&sm.written[i], kDpStWarps);
     }
     for (int i = 0; i < kDpLists; ++i) {
       mb_init(&sm.ready[i], 1);
@@ -273,7 +274,7 @@ __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const Di
 
   if (role == 3) {
     // ================================================================ streaming
-    const int tid = threadIdx.x - 64 - nl, warp = tid >> 5;
+    const int tid = threadIdx.x - 64 - 2 * nl, warp = tid >> 5;
     int v0 = 0, v1 = 0;
     if (WHOLE) slice(p.V / VW, &v0, &v1);
     int mine = (v1 - v0 - tid + kDpSt - 1) / kDpSt;  // vectors of this thread in a row (WHOLE)
@@ -447,7 +448,7 @@ __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const Di
             }
           }
         }
-        mb_arrive(&sm.written[i & 1]);
+        mb_arrive(&sm.written[i & 3]);
       }
       if (GRAD) issue(t + 2);
     }
@@ -488,20 +489,21 @@ __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const Di
       if (i % C == rank && lane == 0) p.loss[g + i * NG] = __uint_as_float(0x7fffffffu);
   } else {
     // ================================================================ list
-    const int lt = threadIdx.x - 32, lw = lt >> 5;  // lt < nl
+    const int group = threadIdx.x - 32 >= nl;       // rows of this parity
+    const int lt = threadIdx.x - 32 - group * nl, lw = lt >> 5;   // lt < nl
     const F2 inv_t = f2_from(p.inv_t);
     const F2 l2e{kLog2eHi, kLog2eLo};
-    // Two tokens a thread, lt and lt + nl.  What is loaded stays as it comes
-    // until the iteration that needs it: an index of the next row, a student's
-    // value of this one.
-    int id1[2], id2[2];
-    float lp1[2], lp2[2];
-    uint32_t s1[2];
+    // Up to kDpLiE tokens a thread, nl apart.  What is loaded stays as it
+    // comes until the iteration that needs it: the indices of the group's next
+    // row, the student's values of this one.
+    int id1[kDpLiE], id2[kDpLiE];
+    float lp1[kDpLiE], lp2[kDpLiE];
+    uint32_t s1[kDpLiE];
     float wg1 = 1.f, tl1 = -INFINITY;               // the row's weight and tail
     bool ok = true;
     auto load_list = [&](int i, int* id, float* lp) {
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
+      for (int q = 0; q < kDpLiE; ++q) {
         id[q] = -1;
         lp[q] = -INFINITY;
         if (i < n && lt + q * nl < k) {
@@ -513,7 +515,7 @@ __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const Di
     };
     auto load_student = [&](int i, const int* id) {
 #pragma unroll
-      for (int q = 0; q < 2; ++q)
+      for (int q = 0; q < kDpLiE; ++q)
         if ((unsigned)id[q] < (unsigned)p.V) s1[q] = Elem<T>::raw(student + ((size_t)g + (size_t)i * NG) * p.V + id[q]);
     };
     auto load_row = [&](int i) {
@@ -523,30 +525,34 @@ __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const Di
         if (p.tail) tl1 = __ldg(p.tail + r);
       }
     };
-    load_list(0, id1, lp1);
-    load_student(0, id1);
-    load_list(1, id2, lp2);
-    load_row(0);
+    load_list(group, id1, lp1);
+    load_student(group, id1);
+    load_list(group + 2, id2, lp2);
+    load_row(group);
 
 #pragma unroll 1
-    for (int j = 0; j <= (GRAD ? n + 1 : n - 1); ++j) {
+    for (int j = group; j <= (GRAD ? n + 1 : n - 1); j += 2) {
       if (j < n) {
         // ---- the list of row j
-        int id[2];
-        float lp[2], s[2];
+        int id[kDpLiE];
+        float lp[kDpLiE], s[kDpLiE];
+        // a NaN makes the maximum +inf, and the row NaN
+        float tm = -INFINITY, km = -INFINITY;
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
+        for (int q = 0; q < kDpLiE; ++q) {
           const bool on = (unsigned)id1[q] < (unsigned)p.V;
           id[q] = on ? id1[q] : -1;
           lp[q] = on ? lp1[q] : -INFINITY;
           s[q] = on ? Elem<T>::of_raw(s1[q]) : -INFINITY;
+          tm = fmaxf(tm, lp[q] != lp[q] ? INFINITY : lp[q]);
+          km = fmaxf(km, s[q]);
           id1[q] = id2[q];
           lp1[q] = lp2[q];
         }
         const float wgt = wg1, ltail = tl1;
-        load_student(j + 1, id1);
-        load_list(j + 2, id2, lp2);
-        load_row(j + 1);
+        load_student(j + 2, id1);
+        load_list(j + 4, id2, lp2);
+        load_row(j + 2);
         // the bitmap was row j - 2's, the list row j - kDpLists's
         if (j >= 2) ok &= mb_wait(&sm.summed[(j - 2) & 3], (j - 2) >> 2);
         if (j >= kDpLists) ok &= mb_wait(&sm.done[j % kDpLists], j / kDpLists - 1);
@@ -556,30 +562,28 @@ __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const Di
         for (int w = lt; w < kDpSlice * VW / 128; w += nl) reinterpret_cast<uint4*>(bits)[w] = make_uint4(0u, 0u, 0u, 0u);
         for (int w = lt; w < kDpStWarps * 2; w += nl) reinterpret_cast<uint32_t*>(dirty)[w] = 0u;
         if (lt == 0) L.infinite = L.twice = 0;
-        // a NaN makes the maximum +inf, and the row NaN
-        float tm = fmaxf(lp[0] != lp[0] ? INFINITY : lp[0], lp[1] != lp[1] ? INFINITY : lp[1]);
-        float km = fmaxf(s[0], s[1]);
 #pragma unroll
         for (int m = 16; m >= 1; m >>= 1) {
           tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, m));
           km = fmaxf(km, __shfl_xor_sync(0xffffffffu, km, m));
         }
-        if (lane == 0) sm.lmax[lw] = make_float2(tm, km);
-        if (!list_meet(nl, ok)) break;              // one gave up: all do, here
+        if (lane == 0) sm.lmax[group][lw] = make_float2(tm, km);
+        if (!list_meet(group, nl, ok)) break;              // one gave up: all do, here
         tm = ltail != ltail ? INFINITY : ltail;
         for (int w = 0; w < nl / 32; ++w) {
-          tm = fmaxf(tm, sm.lmax[w].x);
-          km = fmaxf(km, sm.lmax[w].y);
+          tm = fmaxf(tm, sm.lmax[group][w].x);
+          km = fmaxf(km, sm.lmax[group][w].y);
         }
         F2 w{0.f, 0.f}, ws{0.f, 0.f}, e1{0.f, 0.f};
         const Window<T, const T> win(student, (size_t)(g + j * NG), p.V);
         int v0, v1;
         slice(win.vectors(), &v0, &v1);
+        static_assert(kDpLiE == 4, "the selection below");
+        auto pick = [](int q, auto a0, auto a1, auto a2, auto a3) { return q < 2 ? (q == 0 ? a0 : a1) : (q == 2 ? a2 : a3); };
 #pragma unroll 1
-        for (int q = 0; q < 2; ++q) {
-          if (q == 1 && k <= nl) break;             // (uniform) one token a thread
-          const int id_q = q ? id[1] : id[0];
-          const float lp_q = q ? lp[1] : lp[0], s_q = q ? s[1] : s[0];
+        for (int q = 0; q * nl < k; ++q) {
+          const int id_q = pick(q, id[0], id[1], id[2], id[3]);
+          const float lp_q = pick(q, lp[0], lp[1], lp[2], lp[3]), s_q = pick(q, s[0], s[1], s[2], s[3]);
           F2 w_q{0.f, 0.f}, ws_q{0.f, 0.f};
           if (id_q >= 0) {
             const float kr = km == -INFINITY ? 0.f : km;
@@ -600,24 +604,22 @@ __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const Di
             w = f2_add(w, w_q);
             ws = f2_add(ws, ws_q);
           }
-          if (lt + q * nl < kDpMaxK) {
-            L.sid[lt + q * nl] = id_q;
-            L.sw[lt + q * nl] = w_q.hi;
-            L.sq[lt + q * nl] = ws_q.hi;
-          }
+          L.sid[lt + q * nl] = id_q;
+          L.sw[lt + q * nl] = w_q.hi;
+          L.sq[lt + q * nl] = ws_q.hi;
         }
         w = warp_sum_f2(w);
         ws = warp_sum_f2(ws);
         e1 = warp_sum_f2(e1);
         if (lane == 0) {
-          sm.lsum[lw][0] = w;
-          sm.lsum[lw][1] = ws;
-          sm.lsum[lw][2] = e1;
+          sm.lsum[group][lw][0] = w;
+          sm.lsum[group][lw][1] = ws;
+          sm.lsum[group][lw][2] = e1;
         }
-        list_meet(nl, true);
+        list_meet(group, nl, true);
         if (lt < 3) {                               // one of the three sums each
-          F2 a = sm.lsum[0][lt];
-          for (int q = 1; q < nl / 32; ++q) a = f2_add(a, sm.lsum[q][lt]);
+          F2 a = sm.lsum[group][0][lt];
+          for (int q = 1; q < nl / 32; ++q) a = f2_add(a, sm.lsum[group][q][lt]);
           if (lt == 0) {
             const F2 wt = p.tail ? weight_f2(ltail, tm, l2e, sm.tab) : F2{0.f, 0.f};
             L.Z = f2_add(a, wt);
@@ -639,7 +641,7 @@ __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const Di
       if (GRAD && j >= 2) {
         // ---- the listed tokens of row j - 2, on top of its dense gradient
         const int i = j - 2;
-        ok &= mb_wait(&sm.written[i & 1], i >> 1);
+        ok &= mb_wait(&sm.written[i & 3], i >> 2);
         const DpList& L = sm.list[i % kDpLists];
         if (ok && L.live == 2) {
           const DpStat& s = sm.stat[i % kDpLists];
