@@ -70,8 +70,8 @@ struct DpStat {
 template <typename T>
 struct DpSmem {
   uint4 ring[kDpStages][kDpSlice];
-  uint32_t bits[2][kDpSlice * Tr<T>::VW / 32];
-  uint2 dirty[2][kDpStWarps];           // a byte per (warp, u): some vector there holds a listed token
+  uint32_t bits[3][kDpSlice * Tr<T>::VW / 32];
+  uint2 dirty[3][kDpStWarps];           // a byte per (warp, u): some vector there holds a listed token
   DpList list[kDpLists];
   DpStat stat[kDpLists];
   float4 part[2][kDiMaxC];              // (maximum, sum, -, twice)
@@ -83,7 +83,7 @@ struct DpSmem {
   unsigned long long summed[4];         // streaming warps -> exchange, list: row t is summed
   unsigned long long known[4];          // exchange -> streaming: row t's statistics
   unsigned long long parts[2];          // exchange warps of all CTAs -> exchange: row t's parts
-  unsigned long long listed[2];         // list -> streaming: row t's list
+  unsigned long long listed[4];         // list -> streaming: row t's list
   unsigned long long written[4];        // streaming warps -> list: row t's dense gradient
   unsigned long long ready[kDpLists];   // exchange -> loss: row t's statistics
   unsigned long long done[kDpLists];    // loss -> list: row t's loss is written, its list may be reused
@@ -257,11 +257,9 @@ __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const Di
       mb_init(&sm.summed[i], kDpStWarps);
       mb_init(&sm.known[i], 1);
       mb_init(&sm.written[i], kDpStWarps);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mb_init(&sm.parts[i], C);
       mb_init(&sm.listed[i], 1);
     }
+    for (int i = 0; i < 2; ++i) mb_init(&sm.parts[i], C);
     for (int i = 0; i < kDpLists; ++i) {
       mb_init(&sm.ready[i], 1);
       mb_init(&sm.done[i], 1);
@@ -328,7 +326,7 @@ __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const Di
       if (t < n) {
         // ---- row t without its listed tokens
         asm volatile("cp.async.wait_group %0;" ::"n"(GRAD ? 1 : 2) : "memory");
-        if (!mb_wait(&sm.listed[t & 1], t >> 1)) break;
+        if (!mb_wait(&sm.listed[t & 3], t >> 2)) break;
         if (sm.list[t % kDpLists].live != 0) {
           const uint4* st = &sm.ring[t % kDpStages][tid];
           int m_t = mine;
@@ -348,9 +346,9 @@ __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const Di
               if (u < m_t) x[u] = st[u * kDpSt];
             }
           }
-          const uint2 dirty = sm.dirty[t & 1][warp];
+          const uint2 dirty = sm.dirty[t % 3][warp];
           if (dirty.x | dirty.y) {
-            const unsigned char* bits = reinterpret_cast<const unsigned char*>(sm.bits[t & 1]);
+            const unsigned char* bits = reinterpret_cast<const unsigned char*>(sm.bits[t % 3]);
 #pragma unroll
             for (int u = 0; u < kDpU; ++u) {
               if (((u < 4 ? dirty.x : dirty.y) >> (8 * (u & 3))) & 0xffu) {
@@ -553,12 +551,12 @@ __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const Di
         load_student(j + 2, id1);
         load_list(j + 4, id2, lp2);
         load_row(j + 2);
-        // the bitmap was row j - 2's, the list row j - kDpLists's
-        if (j >= 2) ok &= mb_wait(&sm.summed[(j - 2) & 3], (j - 2) >> 2);
+        // the bitmap was row j - 3's, the list row j - kDpLists's
+        if (j >= 3) ok &= mb_wait(&sm.summed[(j - 3) & 3], (j - 3) >> 2);
         if (j >= kDpLists) ok &= mb_wait(&sm.done[j % kDpLists], j / kDpLists - 1);
         DpList& L = sm.list[j % kDpLists];
-        uint32_t* bits = sm.bits[j & 1];
-        unsigned char* dirty = reinterpret_cast<unsigned char*>(sm.dirty[j & 1]);
+        uint32_t* bits = sm.bits[j % 3];
+        unsigned char* dirty = reinterpret_cast<unsigned char*>(sm.dirty[j % 3]);
         for (int w = lt; w < kDpSlice * VW / 128; w += nl) reinterpret_cast<uint4*>(bits)[w] = make_uint4(0u, 0u, 0u, 0u);
         for (int w = lt; w < kDpStWarps * 2; w += nl) reinterpret_cast<uint32_t*>(dirty)[w] = 0u;
         if (lt == 0) L.infinite = L.twice = 0;
@@ -636,7 +634,7 @@ __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const Di
             L.E1 = a;
           }
         }
-        if (lw == 0) mb_arrive(&sm.listed[j & 1]);  // (the other list warps' part lies before the barrier above)
+        if (lw == 0) mb_arrive(&sm.listed[j & 3]);  // (the other list warps' part lies before the barrier above)
       }
       if (GRAD && j >= 2) {
         // ---- the listed tokens of row j - 2, on top of its dense gradient
