@@ -532,18 +532,21 @@ __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const Di
     for (int j = group; j <= (GRAD ? n + 1 : n - 1); j += 2) {
       if (j < n) {
         // ---- the list of row j
-        int id[kDpLiE];
-        float lp[kDpLiE], s[kDpLiE];
+        // (the bitmap was row j - 3's, the list row j - kDpLists's)
+        if (j >= 3) ok &= mb_wait(&sm.summed[(j - 3) & 3], (j - 3) >> 2);
+        if (j >= kDpLists) ok &= mb_wait(&sm.done[j % kDpLists], j / kDpLists - 1);
+        DpList& L = sm.list[j % kDpLists];
         // a NaN makes the maximum +inf, and the row NaN
         float tm = -INFINITY, km = -INFINITY;
 #pragma unroll
         for (int q = 0; q < kDpLiE; ++q) {
           const bool on = (unsigned)id1[q] < (unsigned)p.V;
-          id[q] = on ? id1[q] : -1;
-          lp[q] = on ? lp1[q] : -INFINITY;
-          s[q] = on ? Elem<T>::of_raw(s1[q]) : -INFINITY;
-          tm = fmaxf(tm, lp[q] != lp[q] ? INFINITY : lp[q]);
-          km = fmaxf(km, s[q]);
+          const float lp = on ? lp1[q] : -INFINITY, s = on ? Elem<T>::of_raw(s1[q]) : -INFINITY;
+          tm = fmaxf(tm, lp != lp ? INFINITY : lp);
+          km = fmaxf(km, s);
+          L.sid[lt + q * nl] = on ? id1[q] : -1;    // this thread's own places, until the weights replace the values
+          L.sw[lt + q * nl] = lp;
+          L.sq[lt + q * nl] = s;
           id1[q] = id2[q];
           lp1[q] = lp2[q];
         }
@@ -551,10 +554,6 @@ __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const Di
         load_student(j + 2, id1);
         load_list(j + 4, id2, lp2);
         load_row(j + 2);
-        // the bitmap was row j - 3's, the list row j - kDpLists's
-        if (j >= 3) ok &= mb_wait(&sm.summed[(j - 3) & 3], (j - 3) >> 2);
-        if (j >= kDpLists) ok &= mb_wait(&sm.done[j % kDpLists], j / kDpLists - 1);
-        DpList& L = sm.list[j % kDpLists];
         uint32_t* bits = sm.bits[j % 3];
         unsigned char* dirty = reinterpret_cast<unsigned char*>(sm.dirty[j % 3]);
         for (int w = lt; w < kDpSlice * VW / 128; w += nl) reinterpret_cast<uint4*>(bits)[w] = make_uint4(0u, 0u, 0u, 0u);
@@ -576,12 +575,11 @@ __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const Di
         const Window<T, const T> win(student, (size_t)(g + j * NG), p.V);
         int v0, v1;
         slice(win.vectors(), &v0, &v1);
-        static_assert(kDpLiE == 4, "the selection below");
-        auto pick = [](int q, auto a0, auto a1, auto a2, auto a3) { return q < 2 ? (q == 0 ? a0 : a1) : (q == 2 ? a2 : a3); };
 #pragma unroll 1
         for (int q = 0; q * nl < k; ++q) {
-          const int id_q = pick(q, id[0], id[1], id[2], id[3]);
-          const float lp_q = pick(q, lp[0], lp[1], lp[2], lp[3]), s_q = pick(q, s[0], s[1], s[2], s[3]);
+          const int at = lt + q * nl;
+          const int id_q = L.sid[at];
+          const float lp_q = L.sw[at], s_q = L.sq[at];
           F2 w_q{0.f, 0.f}, ws_q{0.f, 0.f};
           if (id_q >= 0) {
             const float kr = km == -INFINITY ? 0.f : km;
@@ -602,9 +600,8 @@ __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const Di
             w = f2_add(w, w_q);
             ws = f2_add(ws, ws_q);
           }
-          L.sid[lt + q * nl] = id_q;
-          L.sw[lt + q * nl] = w_q.hi;
-          L.sq[lt + q * nl] = ws_q.hi;
+          L.sw[at] = w_q.hi;
+          L.sq[at] = ws_q.hi;
         }
         w = warp_sum_f2(w);
         ws = warp_sum_f2(ws);
