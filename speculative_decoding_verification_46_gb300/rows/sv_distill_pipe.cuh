@@ -18,9 +18,9 @@
 //       bitmap that takes the tokens out of the streams, and at the end the
 //       tokens' own gradient on top of the dense one.  The loads of a list
 //       are issued one row before they are used.
-//   exchange (1 warp)  the CTA's part of row t to all CTAs of the cluster, and
-//       from the C parts the row's statistics.
-//   loss (1 warp)  three logarithms per row; the CTAs take the rows in turn.
+//   parts (1 warp)  the CTA's part of row t to all CTAs of the cluster.
+//   statistics (1 warp)  from the C parts the row's statistics, and its loss;
+//       the CTAs take the losses in turn.
 //
 // So every dependent chain - gather, two-float sums, exchange, logarithms -
 // has a whole row's streaming time to finish in.  The forward pass alone is
@@ -48,6 +48,8 @@ constexpr int kDpSlice = 4096;          // most vectors per CTA and row
 constexpr int kDpU = (kDpSlice + kDpSt - 1) / kDpSt;   // per streaming thread
 constexpr int kDpStages = 3;
 constexpr int kDpLists = 6;             // rows whose lists are alive
+constexpr int kDpParts = 8;             // rows whose parts may arrive: a CTA's streams are at most 4 rows behind
+                                        // another's statistics, and those at most 4 behind its own
 
 // list threads of a group, and threads of a CTA, for lists of k tokens
 __host__ __device__ constexpr int dp_list_threads(int k) { return k > 32 ? kDpLi : 32; }
@@ -74,19 +76,18 @@ struct DpSmem {
   uint2 dirty[3][kDpStWarps];           // a byte per (warp, u): some vector there holds a listed token
   DpList list[kDpLists];
   DpStat stat[kDpLists];
-  float4 part[2][kDiMaxC];              // (maximum, sum, -, twice)
+  float4 part[kDpParts][kDiMaxC];       // (maximum, sum, -, twice)
   float2 wpart[4][kDpStWarps];
   F2 lsum[2][kDpLi / 32][3];            // by group
   float2 lmax[2][kDpLi / 32];
   float tab[128];
   // mbarriers, each a ring over rows
-  unsigned long long summed[4];         // streaming warps -> exchange, list: row t is summed
-  unsigned long long known[4];          // exchange -> streaming: row t's statistics
-  unsigned long long parts[2];          // exchange warps of all CTAs -> exchange: row t's parts
+  unsigned long long summed[4];         // streaming warps -> parts, list: row t is summed
+  unsigned long long known[4];          // statistics -> streaming: row t's statistics
   unsigned long long listed[4];         // list -> streaming: row t's list
   unsigned long long written[4];        // streaming warps -> list: row t's dense gradient
-  unsigned long long ready[kDpLists];   // exchange -> loss: row t's statistics
-  unsigned long long done[kDpLists];    // loss -> list: row t's loss is written, its list may be reused
+  unsigned long long parts[kDpParts];   // parts warps of all CTAs -> statistics
+  unsigned long long done[kDpLists];    // statistics -> list: row t's loss is written, its list may be reused
 };
 
 // The meeting point of a list group (all of its warps wait, so a named
@@ -202,8 +203,10 @@ __device__ __forceinline__ void dp_statistics(const float4* part, int C, const D
   }
 }
 
-// The loss of a row (one warp: the three logarithms side by side).
-__device__ __forceinline__ void dp_loss(const DpList& L, const DpStat& s, double inv_t, const float* tab, float* loss) {
+// The loss of a row (one warp: the three logarithms side by side), in
+// two-float throughout: loss / weight = sum_j p_j (ln p_j - ln q_j) + p_t (ln p_t
+// - ln q_t), with the row's constants (ln Z, ln S) taken out of the sums.
+__device__ __forceinline__ void dp_loss(const DpList& L, const DpStat& s, F2 inv_t, const float* tab, float* loss) {
   const int lane = threadIdx.x & 31;
   if (L.live != 2) {
     if (lane == 0) *loss = 0.f;
@@ -215,14 +218,28 @@ __device__ __forceinline__ void dp_loss(const DpList& L, const DpStat& s, double
   const F2 ls{__shfl_sync(0xffffffffu, lg.hi, 1), __shfl_sync(0xffffffffu, lg.lo, 1)};
   const F2 lt{__shfl_sync(0xffffffffu, lg.hi, 2), __shfl_sync(0xffffffffu, lg.lo, 2)};
   if (lane == 0) {
-    const double kr = L.km == -INFINITY ? 0.0 : (double)L.km;
-    double e = f2_double(L.E1);
-    if (L.wt.hi != 0.f)
-      e += f2_double(L.wt) * (((double)L.ltail - (double)L.tm) - (((double)s.mt - kr) * inv_t + f2_double(lt)));
-    double l = e / f2_double(L.Z) - f2_double(lz) + f2_double(ls) + ((double)s.M - kr) * inv_t;
-    if (!(s.S.hi > 0.f && s.S.hi < INFINITY)) l = __longlong_as_double(0x7fffffffffffffffll);
-    else if (L.infinite && l == l) l = (double)INFINITY;
-    *loss = (float)((double)L.wgt * l);
+    const float kr = L.km == -INFINITY ? s.M : L.km;
+    const bool tail = L.wt.hi != 0.f;
+    // p wants what q has nothing of, or less than float32 can say
+    const bool infinite = L.infinite || (s.M - kr) * inv_t.hi > 1.0e30f ||
+                          (tail && (!(s.st > 0.f) || (s.mt - kr) * inv_t.hi < -1.0e30f));
+    float l;
+    if (!(s.S.hi > 0.f && s.S.hi < INFINITY) || L.Z.hi != L.Z.hi) {
+      l = __uint_as_float(0x7fffffffu);
+    } else if (infinite) {
+      l = INFINITY;
+    } else {
+      F2 e = L.E1;
+      if (tail)
+        e = f2_add(e, f2_mul(L.wt, f2_add(two_diff(L.ltail, L.tm), f2_neg(f2_add(f2_mul(two_diff(s.mt, kr), inv_t), lt)))));
+      const float q = e.hi * __frcp_rn(L.Z.hi);      // e / Z: a quotient and its remainder's
+      const F2 rem = f2_add(e, f2_neg(f2_mul(L.Z, F2{q, 0.f})));
+      F2 sum = f2_norm(q, rem.hi * __frcp_rn(L.Z.hi));
+      sum = f2_add(sum, f2_add(ls, f2_neg(lz)));
+      sum = f2_add(sum, f2_mul(two_diff(s.M, kr), inv_t));
+      l = sum.hi;
+    }
+    *loss = L.wgt * l;
   }
 }
 
@@ -239,9 +256,7 @@ __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const Di
   const int n = (p.R - g + NG - 1) / NG;            // rows of this cluster: g, g + NG, ...
   const int k = p.k;
   const int nl = dp_list_threads(k);                // list threads of a group
-  // the roles, by warp: exchange, list, loss, streaming (the later warps of a
-  // scheduler wait for the earlier ones, and the streaming warps always have
-  // something to issue)
+  // the roles, by warp: parts, list, statistics, streaming
   const int role = threadIdx.x < 32 ? 0 : threadIdx.x < 32 + 2 * nl ? 1 : threadIdx.x < 64 + 2 * nl ? 2 : 3;
   const F2 c{p.c, p.c_lo};
   const T* student = static_cast<const T*>(p.student);
@@ -259,11 +274,8 @@ __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const Di
       mb_init(&sm.written[i], kDpStWarps);
       mb_init(&sm.listed[i], 1);
     }
-    for (int i = 0; i < 2; ++i) mb_init(&sm.parts[i], C);
-    for (int i = 0; i < kDpLists; ++i) {
-      mb_init(&sm.ready[i], 1);
-      mb_init(&sm.done[i], 1);
-    }
+    for (int i = 0; i < kDpParts; ++i) mb_init(&sm.parts[i], C);
+    for (int i = 0; i < kDpLists; ++i) mb_init(&sm.done[i], 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   __syncthreads();
@@ -452,7 +464,7 @@ __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const Di
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
   } else if (role == 0) {
-    // ================================================================ exchange
+    // ================================================================ parts
 #pragma unroll 1
     for (int t = 0; t < n; ++t) {
       if (!mb_wait(&sm.summed[t & 3], t >> 2)) break;  // (which follows row t's list)
@@ -465,26 +477,28 @@ __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const Di
         float s = v.x == m ? v.y : v.y * ex2_approx((v.x - m) * p.c);
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        if (lane < C) push_f4(&sm.part[t & 1][rank], lane, make_float4(m, s, 0.f, L.twice ? 1.f : 0.f));
+        if (lane < C) push_f4(&sm.part[t % kDpParts][rank], lane, make_float4(m, s, 0.f, L.twice ? 1.f : 0.f));
       }
-      if (lane < C) mb_arrive_remote(&sm.parts[t & 1], lane);
-      if (!mb_wait<true>(&sm.parts[t & 1], t >> 1)) break;
-      dp_statistics(sm.part[t & 1], C, L, k, c, sm.tab, sm.stat[t % kDpLists],
-                    !GRAD && rank == 0 && p.stats ? p.stats + (size_t)(g + t * NG) * 8 : nullptr);
-      mb_arrive(&sm.known[t & 3]);
-      mb_arrive(&sm.ready[t % kDpLists]);
+      if (lane < C) mb_arrive_remote(&sm.parts[t % kDpParts], lane);
+      __syncwarp();
     }
   } else if (role == 2) {
-    // ================================================================ loss
-    int i = 0;
+    // ================================================================ statistics
+    const F2 inv_t = f2_from(p.inv_t);
+    int t = 0;
 #pragma unroll 1
-    for (; i < n; ++i) {
-      if (!mb_wait(&sm.ready[i % kDpLists], i / kDpLists)) break;
-      if (i % C == rank) dp_loss(sm.list[i % kDpLists], sm.stat[i % kDpLists], p.inv_t, sm.tab, p.loss + g + i * NG);
-      mb_arrive(&sm.done[i % kDpLists]);
+    for (; t < n; ++t) {
+      if (!mb_wait<true>(&sm.parts[t % kDpParts], t / kDpParts)) break;
+      const DpList& L = sm.list[t % kDpLists];
+      DpStat& s = sm.stat[t % kDpLists];
+      dp_statistics(sm.part[t % kDpParts], C, L, k, c, sm.tab, s,
+                    !GRAD && rank == 0 && p.stats ? p.stats + (size_t)(g + t * NG) * 8 : nullptr);
+      mb_arrive(&sm.known[t & 3]);
+      if (t % C == rank) dp_loss(L, s, inv_t, sm.tab, p.loss + g + t * NG);
+      mb_arrive(&sm.done[t % kDpLists]);
     }
-    for (; i < n; ++i)                              // given up
-      if (i % C == rank && lane == 0) p.loss[g + i * NG] = __uint_as_float(0x7fffffffu);
+    for (; t < n; ++t)                              // given up
+      if (t % C == rank && lane == 0) p.loss[g + t * NG] = __uint_as_float(0x7fffffffu);
   } else {
     // ================================================================ list
     const int group = threadIdx.x - 32 >= nl;       // rows of this parity
