@@ -77,10 +77,22 @@ struct AdjustTile {
   int2* blist;      // [NB] (offset, entry)
   uint16_t* list;   // [tile]
   int* draft;       // [gamma]
+  int* mask;        // [gamma + 1] the rows' mask rows: -1 none, -2 nothing is allowed
   int* nlist;
   int* nb;
   int b, t0, n, gb;
 };
+constexpr int kAdNone = -1, kAdNothing = -2;
+
+// The rows' mask rows; complete after the next barrier.
+template <typename T>
+__device__ __forceinline__ void adjust_masks(const AdjustParams& p, const AdjustTile<T>& s) {
+  if ((int)threadIdx.x > s.gb) return;
+  const size_t row = (size_t)s.b * p.G1 + threadIdx.x;
+  int mi = -1;
+  if (p.mask) mi = p.mask_index ? __ldg(p.mask_index + row) : (int)row;
+  s.mask[threadIdx.x] = mi < 0 ? kAdNone : mi < p.M ? mi : kAdNothing;
+}
 
 // The tile's tokens of the sequence; complete after the next barrier.
 template <typename T>
@@ -119,15 +131,6 @@ struct AdjustPenalties {
         pres(p.presence ? __ldg(p.presence + b) : 0.f) {}
 };
 
-// The mask row of a logits row: nullptr and *none = false without one, *none
-// = true where nothing is allowed.
-__device__ __forceinline__ const uint32_t* adjust_mask_row(const AdjustParams& p, size_t row, bool* none) {
-  int mi = -1;
-  if (p.mask) mi = p.mask_index ? __ldg(p.mask_index + row) : (int)row;
-  *none = mi >= p.M;
-  return mi >= 0 && mi < p.M ? p.mask + (size_t)mi * p.W : nullptr;
-}
-
 // The mask bits of the VW tokens from v on (v may lie up to VW - 1 before the row).
 template <int VW>
 __device__ __forceinline__ uint32_t adjust_bits(const uint32_t* mrow, int W, int v) {
@@ -137,41 +140,52 @@ __device__ __forceinline__ uint32_t adjust_bits(const uint32_t* mrow, int W, int
   return (sh >= 0 ? __funnelshift_r(lo, hi, sh) : lo << -sh) & ((1u << VW) - 1u);
 }
 
-// The new value of the listed token at tile offset o in row i, from x.
-// false: the row leaves it as it is.
+// What row i does to the listed token at tile offset o (the row's mask aside).
+struct AdjustChange {
+  float less, bias;   // frequency and presence together; the bias
+  bool seen, biased;
+  __device__ __forceinline__ bool any() const { return seen || biased; }
+  __device__ __forceinline__ float apply(float x, float rep) const {
+    if (seen) {
+      x = x > 0.f ? __fdiv_rn(x, rep) : x * rep;
+      x -= less;
+    }
+    return biased ? x + bias : x;
+  }
+};
 template <typename T>
-__device__ __forceinline__ bool adjust_value(const AdjustParams& p, const AdjustTile<T>& s, const AdjustPenalties& pen,
-                                             int i, int o, const uint32_t* mrow, float* x) {
+__device__ __forceinline__ AdjustChange adjust_change(const AdjustParams& p, const AdjustTile<T>& s,
+                                                      const AdjustPenalties& pen, int i, int o) {
   const uint32_t w = s.cnt[o];
-  const int v = s.t0 + o;
   int c = (int)(w & kAdCount);
   if (w & kAdDraft)
-    for (int j = 0; j < i; ++j) c += (s.draft[j] == v);
-  const bool seen = (w & kAdPrompt) || c > 0;
-  if (!seen && !(w & kAdBias)) return false;
-  if (mrow && !((__ldg(mrow + (v >> 5)) >> (v & 31)) & 1u)) return false;
-  float y = *x;
-  if (seen) {
-    y = y > 0.f ? __fdiv_rn(y, pen.rep) : y * pen.rep;
-    y -= fmaf(pen.freq, (float)c, c > 0 ? pen.pres : 0.f);
-  }
-  if (w & kAdBias) {
+    for (int j = 0; j < i; ++j) c += (s.draft[j] == s.t0 + o);
+  AdjustChange a;
+  a.seen = (w & kAdPrompt) || c > 0;
+  a.less = fmaf(pen.freq, (float)c, c > 0 ? pen.pres : 0.f);
+  a.biased = w & kAdBias;
+  a.bias = 0.f;
+  if (a.biased) {
     int last = -1;
     for (int k = 0; k < *s.nb; ++k)
       if (s.blist[k].x == o) last = max(last, s.blist[k].y);
-    y += __ldg(p.bias_values + (size_t)s.b * p.NB + last);
+    a.bias = __ldg(p.bias_values + (size_t)s.b * p.NB + last);
   }
-  *x = y;
-  return true;
+  return a;
+}
+// whether the mask row lets token v pass
+__device__ __forceinline__ bool adjust_allowed(const uint32_t* mrow, int v) {
+  return !mrow || ((__ldg(mrow + (v >> 5)) >> (v & 31)) & 1u);
 }
 
 template <typename T>
-__device__ __forceinline__ AdjustTile<T> adjust_tile(const AdjustParams& p, unsigned char* smem, int* draft, int* counters) {
+__device__ __forceinline__ AdjustTile<T> adjust_tile(const AdjustParams& p, unsigned char* smem, int* draft, int* mask, int* counters) {
   AdjustTile<T> s;
   s.cnt = reinterpret_cast<uint32_t*>(smem);
   s.blist = reinterpret_cast<int2*>(s.cnt + p.tile);
   s.list = reinterpret_cast<uint16_t*>(s.blist + p.NB);
   s.draft = draft;
+  s.mask = mask;
   s.nlist = counters;
   s.nb = counters + 1;
   s.b = blockIdx.x / p.tiles;
@@ -191,32 +205,34 @@ __device__ __forceinline__ void adjust_masked(uint4& x, uint32_t bits) {
     if (!((bits >> t) & 1u)) TR::put(x, t, Elem<T>::kNegInf);
 }
 
-template <typename T>
+// WHOLE: V is a multiple of the vector width, so every row is whole vectors.
+template <typename T, bool WHOLE>
 __global__ void __launch_bounds__(kAdThreads, 2) adjust_staged_kernel(const AdjustParams p) {
   using TR = Tr<T>;
   constexpr int VW = TR::VW;
-  constexpr uint32_t kFull = (1u << VW) - 1u;
   extern __shared__ __align__(16) unsigned char smem_raw[];
-  __shared__ int sdraft[kMaxG1];
+  __shared__ int sdraft[kMaxG1], smask[kMaxG1];
   __shared__ int counters[2];
   const int tid = threadIdx.x;
   const int SV = p.tile / VW + 1;                                  // vectors of a stage: a row may start inside one
   uint4* ring = reinterpret_cast<uint4*>(smem_raw);                // [kAdStages][SV]
-  const AdjustTile<T> s = adjust_tile<T>(p, smem_raw + (size_t)kAdStages * SV * sizeof(uint4), sdraft, counters);
+  const AdjustTile<T> s = adjust_tile<T>(p, smem_raw + (size_t)kAdStages * SV * sizeof(uint4), sdraft, smask, counters);
+  const size_t first = (size_t)s.b * p.G1 * (size_t)p.V + s.t0;    // row 0's first element in the tile
+  const T* logits = static_cast<const T*>(p.logits);
+  T* out = static_cast<T*>(p.out);
 
   auto issue = [&](int i) {                                        // row i of the sequence into its stage
-    if (i <= s.gb) {
-      const size_t row = (size_t)s.b * p.G1 + i;
-      bool none;
-      const uint32_t* mrow = adjust_mask_row(p, row, &none);
-      const size_t e0 = row * (size_t)p.V + s.t0;
-      const int a = (int)(e0 % VW);
-      const T* src = static_cast<const T*>(p.logits) + (e0 - a);
-      uint4* st = ring + (size_t)(i % kAdStages) * SV;
-      const int nv = none ? 0 : (a + s.n + VW - 1) / VW;
+    const int mi = i <= s.gb ? smask[i] : kAdNothing;
+    if (mi != kAdNothing) {
+      const uint32_t* mrow = mi >= 0 ? p.mask + (size_t)mi * p.W : nullptr;
+      const size_t e0 = first + (size_t)i * p.V;
+      const int a = WHOLE ? 0 : (int)(e0 % VW);
+      const T* src = logits + (e0 - a);
+      uint4* st = ring + (i % kAdStages) * SV;
+      const int nv = (a + s.n + VW - 1) / VW;
       for (int j = tid; j < nv; j += kAdThreads) {
         const int o = j * VW - a;
-        if (o >= 0 && o + VW <= s.n) {
+        if (WHOLE || (o >= 0 && o + VW <= s.n)) {
           if (!mrow || adjust_bits<VW>(mrow, p.W, s.t0 + o) != 0u) {
             const unsigned sa = (unsigned)__cvta_generic_to_shared(st + j);
             asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(sa), "l"(src + (size_t)j * VW) : "memory");
@@ -230,42 +246,61 @@ __global__ void __launch_bounds__(kAdThreads, 2) adjust_staged_kernel(const Adju
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
+  adjust_masks(p, s);
+  __syncthreads();
 #pragma unroll
   for (int i = 0; i < kAdStages - 1; ++i) issue(i);
   const AdjustPenalties pen(p, s.b);
   adjust_collect(p, s);
+  __syncthreads();
+  // a thread's first listed token keeps what is done to it: the same in every
+  // row, unless it is drafted
+  const int nl = *s.nlist;
+  int mine = -1;
+  AdjustChange change{0.f, 0.f, false, false};
+  if (tid < nl) {
+    mine = s.list[tid];
+    if (s.cnt[mine] & kAdDraft) mine = -1;
+    else change = adjust_change(p, s, pen, 0, mine);
+  }
 
   for (int i = 0; i <= s.gb; ++i) {
     issue(i + kAdStages - 1);                                      // its stage was written out an iteration ago
     asm volatile("cp.async.wait_group %0;" ::"n"(kAdStages - 1) : "memory");
-    __syncthreads();                                               // row i is in (and, first, the counts are)
-    const size_t row = (size_t)s.b * p.G1 + i;
-    bool none;
-    const uint32_t* mrow = adjust_mask_row(p, row, &none);
-    const size_t e0 = row * (size_t)p.V + s.t0;
-    const int a = (int)(e0 % VW);
-    uint4* st = ring + (size_t)(i % kAdStages) * SV;
-    if (!none) {
+    __syncthreads();                                               // row i is in
+    const int mi = smask[i];
+    const uint32_t* mrow = mi >= 0 ? p.mask + (size_t)mi * p.W : nullptr;
+    const size_t e0 = first + (size_t)i * p.V;
+    const int a = WHOLE ? 0 : (int)(e0 % VW);
+    uint4* st = ring + (i % kAdStages) * SV;
+    if (mi != kAdNothing) {
       T* elem = reinterpret_cast<T*>(st) + a;
-      const int nl = *s.nlist;
-      for (int e = tid; e < nl; e += kAdThreads) {
+      if (mine >= 0 && change.any() && adjust_allowed(mrow, s.t0 + mine))
+        Elem<T>::store(elem + mine, change.apply(Elem<T>::load(elem + mine), pen.rep));
+      for (int e = mine >= 0 ? tid + kAdThreads : tid; e < nl; e += kAdThreads) {
         const int o = s.list[e];
-        float x = Elem<T>::load(elem + o);
-        if (adjust_value(p, s, pen, i, o, mrow, &x)) Elem<T>::store(elem + o, x);
+        const AdjustChange ch = adjust_change(p, s, pen, i, o);
+        if (ch.any() && adjust_allowed(mrow, s.t0 + o))
+          Elem<T>::store(elem + o, ch.apply(Elem<T>::load(elem + o), pen.rep));
       }
     }
     __syncthreads();
-    T* dst = static_cast<T*>(p.out) + (e0 - a);
+    T* dst = out + (e0 - a);
     const int nv = (a + s.n + VW - 1) / VW;
     for (int j = tid; j < nv; j += kAdThreads) {
       const int o = j * VW - a;
-      const uint32_t bits = none ? 0u : mrow ? adjust_bits<VW>(mrow, p.W, s.t0 + o) : kFull;
-      uint4 x = make_uint4(TR::kPadWord, TR::kPadWord, TR::kPadWord, TR::kPadWord);
-      if (bits != 0u) {
+      uint4 x;
+      if (mi == kAdNone) {
         x = st[j];
-        adjust_masked<T>(x, bits);
+      } else {
+        x = make_uint4(TR::kPadWord, TR::kPadWord, TR::kPadWord, TR::kPadWord);
+        const uint32_t bits = mrow ? adjust_bits<VW>(mrow, p.W, s.t0 + o) : 0u;
+        if (bits != 0u) {
+          x = st[j];
+          adjust_masked<T>(x, bits);
+        }
       }
-      if (o >= 0 && o + VW <= s.n) {
+      if (WHOLE || (o >= 0 && o + VW <= s.n)) {
         __stcs(reinterpret_cast<uint4*>(dst + (size_t)j * VW), x);
       } else {
 #pragma unroll
@@ -283,19 +318,22 @@ __global__ void __launch_bounds__(kAdThreads, 2) adjust_direct_kernel(const Adju
   constexpr int VW = TR::VW;
   constexpr uint32_t kFull = (1u << VW) - 1u;
   extern __shared__ __align__(16) unsigned char smem_raw[];
-  __shared__ int sdraft[kMaxG1];
+  __shared__ int sdraft[kMaxG1], smask[kMaxG1];
   __shared__ int counters[2];
   const int tid = threadIdx.x;
   const bool sparse = p.count || p.NB;
-  const AdjustTile<T> s = adjust_tile<T>(p, smem_raw, sdraft, counters);
+  const AdjustTile<T> s = adjust_tile<T>(p, smem_raw, sdraft, smask, counters);
+  adjust_masks(p, s);
   if (sparse) adjust_collect(p, s);
+  __syncthreads();
 
   // ---- the rows, masked
   for (int i = 0; i <= s.gb; ++i) {
     const size_t row = (size_t)s.b * p.G1 + i;
-    bool none;
-    const uint32_t* mrow = adjust_mask_row(p, row, &none);
-    if (!p.copy && !mrow && !none) continue;
+    const int mi = smask[i];
+    const bool none = mi == kAdNothing;
+    const uint32_t* mrow = mi >= 0 ? p.mask + (size_t)mi * p.W : nullptr;
+    if (!p.copy && mi == kAdNone) continue;
     const size_t e0 = row * (size_t)p.V + s.t0;
     const int a = (int)(e0 % VW);
     const T* src = static_cast<const T*>(p.logits) + (e0 - a);
@@ -336,21 +374,21 @@ __global__ void __launch_bounds__(kAdThreads, 2) adjust_direct_kernel(const Adju
     }
   }
   if (!sparse) return;
-  __syncthreads();   // the counts are complete, and the rows masked
+  __syncthreads();   // the rows are masked
 
   // ---- the listed tokens of every row, in place
   const int nl = *s.nlist;
   const AdjustPenalties pen(p, s.b);
   for (int i = 0; i <= s.gb; ++i) {
     const size_t row = (size_t)s.b * p.G1 + i;
-    bool none;
-    const uint32_t* mrow = adjust_mask_row(p, row, &none);
-    if (none) continue;
+    const int mi = smask[i];
+    const uint32_t* mrow = mi >= 0 ? p.mask + (size_t)mi * p.W : nullptr;
+    if (mi == kAdNothing) continue;
     T* elem = static_cast<T*>(p.out) + row * (size_t)p.V + s.t0;
     for (int e = tid; e < nl; e += kAdThreads) {
       const int o = s.list[e];
-      float x = Elem<T>::load(elem + o);
-      if (adjust_value(p, s, pen, i, o, mrow, &x)) Elem<T>::store(elem + o, x);
+      const AdjustChange ch = adjust_change(p, s, pen, i, o);
+      if (ch.any() && adjust_allowed(mrow, s.t0 + o)) Elem<T>::store(elem + o, ch.apply(Elem<T>::load(elem + o), pen.rep));
     }
   }
 }

@@ -76,7 +76,8 @@ sv_status launch_adjust(sv::rows::AdjustParams p, cudaStream_t stream) {
   const long long grid = (long long)p.B * p.tiles;
   if (grid > 0x7fffffffll) return SV_ERR_UNSUPPORTED;
   const bool sparse = p.count || p.NB, staged = p.copy && sparse;
-  auto kern = staged ? sv::rows::adjust_staged_kernel<T> : sv::rows::adjust_direct_kernel<T>;
+  auto kern = !staged ? sv::rows::adjust_direct_kernel<T>
+              : p.V % sv::Tr<T>::VW == 0 ? sv::rows::adjust_staged_kernel<T, true> : sv::rows::adjust_staged_kernel<T, false>;
   size_t smem = sparse ? (size_t)p.tile * 6 + (size_t)p.NB * 8 : 0;
   if (staged) smem += (size_t)sv::rows::kAdStages * (p.tile / sv::Tr<T>::VW + 1) * 16;
   // (the kernel's static shared memory counts toward the 48 KB that need no opt-in)

@@ -507,12 +507,12 @@ __global__ void __launch_bounds__(kTlThreads, 4) top_slice_kernel(const TopParam
 // the k-th best that comes later in the row loses the tie, so a raised bound
 // is strict, and rows of ties or of rising values cost more cuts but need no
 // other path.
-constexpr int kTrU = 4;                         // vectors per thread per step
+constexpr int kTrU = 3;                         // vectors per thread per step (four CTAs per SM)
 constexpr int kTrStages = 3;                    // ring stages: one read, one or two in flight
 constexpr int kTrStep = kTrU * kTlThreads;      // vectors per step
-constexpr int kTrFew = 96;                      // listed vectors a step that need no look at the buffer's end
+constexpr int kTrFew = 64;                      // listed vectors a step that need no look at the buffer's end
 
-__host__ __device__ constexpr int tr_capacity(int k) { return 2048 > 2 * k + 1024 ? 2048 : 2 * k + 1024; }
+__host__ __device__ constexpr int tr_capacity(int k) { return 1024 > 2 * k + 512 ? 1024 : 2 * k + 512; }
 
 struct TopRowSmem {
   PickSmem pick;
@@ -556,14 +556,14 @@ struct RunningSum {
 
 // WHOLE: V is a multiple of the vector width, so every row is whole vectors.
 template <typename T, bool WHOLE>
-__global__ void __launch_bounds__(kTlThreads, 3) top_row_kernel(const TopParams p) {
+__global__ void __launch_bounds__(kTlThreads, 4) top_row_kernel(const TopParams p) {
   using TR = Tr<T>;
   constexpr int VW = TR::VW;
   extern __shared__ __align__(16) unsigned char smem_raw[];
   __shared__ TopRowSmem sm;
   const int tid = threadIdx.x, k = p.k, r = blockIdx.x;
-  const int cap = tr_capacity(k), trig = cap - 1024;
-  static_assert(kTrFew * 8 <= 1024, "a step of few listed vectors fits behind trig");
+  const int cap = tr_capacity(k), trig = cap - 512;
+  static_assert(kTrFew * 8 <= 512, "a step of few listed vectors fits behind trig");
   uint4* ring = reinterpret_cast<uint4*>(smem_raw);                            // [kTrStages][kTrU][kTlThreads]
   unsigned long long* keys = reinterpret_cast<unsigned long long*>(ring + kTrStages * kTrStep);   // [cap] candidates
   const Window<T, const T> win(static_cast<const T*>(p.logits), (size_t)r, p.V);
@@ -654,13 +654,13 @@ __global__ void __launch_bounds__(kTlThreads, 3) top_row_kernel(const TopParams 
       // (with nothing but -inf so far rho is 0 and the terms are 0, or NaN)
       float s0 = 0.f, s1 = 0.f;
       if (!acc.far) {
+        const Pair cc = pair_of(c, c), rr = pair_of(-acc.rho, -acc.rho);
+        Pair a = pair_of(0.f, 0.f);
 #pragma unroll
         for (int u = 0; u < kTrU; ++u)
 #pragma unroll
-          for (int t = 0; t < VW; t += 2) {
-            s0 += acc.term(TR::get(x[u], t), c);
-            s1 += acc.term(TR::get(x[u], t + 1), c);
-          }
+          for (int t = 0; t < VW; t += 2) a = pair_add(a, pair_terms<T>(x[u], t, cc, rr));
+        unpair(a, s0, s1);
       } else {
 #pragma unroll
         for (int u = 0; u < kTrU; ++u) {
