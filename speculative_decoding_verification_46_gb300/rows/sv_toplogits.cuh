@@ -510,9 +510,12 @@ __global__ void __launch_bounds__(kTlThreads, 4) top_slice_kernel(const TopParam
 constexpr int kTrU = 3;                         // vectors per thread per step (four CTAs per SM)
 constexpr int kTrStages = 3;                    // ring stages: one read, one or two in flight
 constexpr int kTrStep = kTrU * kTlThreads;      // vectors per step
-constexpr int kTrFew = 64;                      // listed vectors a step that need no look at the buffer's end
 
-__host__ __device__ constexpr int tr_capacity(int k) { return 1024 > 2 * k + 512 ? 1024 : 2 * k + 512; }
+// Listed vectors a step that need no look at the buffer's end; candidates at
+// which it is cut back; its size.
+__host__ __device__ constexpr int tr_few(int k) { return k + k / 4 < 64 ? 64 : k + k / 4 < kTrStep ? k + k / 4 : kTrStep; }
+__host__ __device__ constexpr int tr_trigger(int k) { return 2 * k + 64 < 512 ? 512 : 2 * k + 64; }
+__host__ __device__ constexpr int tr_capacity(int k) { return tr_trigger(k) + 8 * tr_few(k); }
 
 struct TopRowSmem {
   PickSmem pick;
@@ -562,19 +565,18 @@ __global__ void __launch_bounds__(kTlThreads, 4) top_row_kernel(const TopParams 
   extern __shared__ __align__(16) unsigned char smem_raw[];
   __shared__ TopRowSmem sm;
   const int tid = threadIdx.x, k = p.k, r = blockIdx.x;
-  const int cap = tr_capacity(k), trig = cap - 512;
-  static_assert(kTrFew * 8 <= 512, "a step of few listed vectors fits behind trig");
+  const int trig = tr_trigger(k), few = tr_few(k);
   uint4* ring = reinterpret_cast<uint4*>(smem_raw);                            // [kTrStages][kTrU][kTlThreads]
-  unsigned long long* keys = reinterpret_cast<unsigned long long*>(ring + kTrStages * kTrStep);   // [cap] candidates
+  unsigned long long* keys = reinterpret_cast<unsigned long long*>(ring + kTrStages * kTrStep);   // [tr_capacity(k)] candidates
   const Window<T, const T> win(static_cast<const T*>(p.logits), (size_t)r, p.V);
   const int NV = win.vectors();
   const int steps = (NV + kTrStep - 1) / kTrStep;
   const uint4 pad = make_uint4(TR::kPadWord, TR::kPadWord, TR::kPadWord, TR::kPadWord);
 
+  const T* src = win.base + (size_t)tid * VW;                                  // this thread's next vectors
+  int v0 = tid;
+  uint4* slot = ring + tid;                                                    // and where they go
   auto issue = [&](int step) {
-    uint4* slot = ring + (step % kTrStages) * kTrStep + tid;
-    const T* src = win.base + ((size_t)step * kTrStep + tid) * VW;
-    const int v0 = step * kTrStep + tid;
 #pragma unroll
     for (int u = 0; u < kTrU; ++u) {
       const int v = v0 + u * kTlThreads;
@@ -586,6 +588,9 @@ __global__ void __launch_bounds__(kTlThreads, 4) top_row_kernel(const TopParams 
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
+    src += kTrStep * VW;
+    v0 += kTrStep;
+    slot = slot == ring + (kTrStages - 1) * kTrStep + tid ? ring + tid : slot + kTrStep;
   };
   issue(0);
   issue(1);
@@ -643,7 +648,7 @@ __global__ void __launch_bounds__(kTlThreads, 4) top_row_kernel(const TopParams 
       if (vm[u] >= thr && vm[u] > -INFINITY) {
         const int pos = atomicAdd(&sm.nvec[step % 3], 1);
         sm.list[step & 1][pos] = (uint16_t)(u * kTlThreads + tid);
-        flag |= pos >= kTrFew;
+        flag |= pos >= few;
         clear_ge<T>(x[u], thr);
         vm[u] = TR::template vmax<false>(x[u]);
       }
