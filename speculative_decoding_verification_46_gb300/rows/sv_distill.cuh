@@ -52,8 +52,6 @@ struct DistillParams {
   void* grad;
 };
 
-constexpr float kLog2eHi = 1.442695022e+00f, kLog2eLo = 1.925963033e-08f;
-
 // 2^(d (c + c_lo)), one correction step: the weight of a value that lies d
 // below its reference.
 __device__ __forceinline__ float weight_fast(float d, float c, float c_lo) {

@@ -135,22 +135,6 @@ __device__ __forceinline__ void mb_arrive_remote(unsigned long long* b, int rank
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(d) : "memory");
 }
 
-// ln a to about 40 bits, a a normalised two-float number >= 2^-100: a float
-// logarithm y corrected by a e^-y - 1.
-__device__ __forceinline__ F2 f2_log(F2 a, const float* tab) {
-  const float y = logf(a.hi);
-  const F2 e = exp2_f2(f2_mul(F2{-y, 0.f}, F2{kLog2eHi, kLog2eLo}), tab);
-  const F2 r = f2_add(f2_mul(a, f2_norm(e.hi, e.lo)), F2{-1.f, 0.f});
-  return f2_add(F2{y, 0.f}, f2_norm(r.hi, r.lo - 0.5f * r.hi * r.hi));
-}
-
-// a - b with its rounding error
-__device__ __forceinline__ F2 two_diff(float a, float b) {
-  const float d = a - b;
-  const float bb = d - a;
-  return F2{d, (a - (d - bb)) + (-b - bb)};
-}
-
 // The statistics of a row from the C parts (one warp; lane 0 writes).  The
 // sum outside the list is float32 up to here: its error moves the loss by
 // q_t - p_t of it.  The row's whole sum is two-float, it moves the loss fully.

@@ -49,6 +49,11 @@ sv_status launched() {
   return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
 
+sv::F2 two_float(double d) {
+  const float hi = (float)d;
+  return sv::F2{hi, (float)(d - (double)hi)};
+}
+
 // log2(e) / temperature as a float pair
 void exponent_scale(float temperature, float* hi, float* lo) {
   const double c = 1.4426950408889634 / (double)temperature;
@@ -366,7 +371,7 @@ extern "C" sv_status sv_top_logits(int R, int V, const void* logits, sv_dtype dt
   p.KP = 1;
   while (p.KP < 8 && sv::rows::kTlThreads * p.KP < 2 * k) p.KP *= 2;
   exponent_scale(temperature, &p.c, &p.c_lo);
-  p.inv_t = 1.0 / (double)temperature;
+  p.inv_t = two_float(1.0 / (double)temperature);
   p.logits = logits;
   p.indices = indices;
   p.logprobs = logprobs;

@@ -34,7 +34,7 @@ struct TopParams {
   int H, SV;                      // slices per row, vectors per slice
   int KP;                         // group maxima per thread that tau is chosen from
   float c, c_lo;                  // log2(e) / temperature
-  double inv_t;                   // 1 / temperature
+  F2 inv_t;                       // 1 / temperature
   const void* logits;
   int32_t* indices;
   float* logprobs;
@@ -67,7 +67,7 @@ struct TopSmem {
   F2 f2red[kTlWarps];
   int ired[kTlWarps];
   unsigned long long u64red[kTlWarps];
-  double lns;
+  F2 lns;
   unsigned long long kth;
   unsigned lmax;                        // okey of the largest candidate beyond the k best
   int count, nvec, flag;
@@ -181,11 +181,18 @@ __device__ __forceinline__ unsigned long long select_kth64(int k, int V, PickSme
   }
 }
 
+// (x - m) / temperature, x <= m; one float where it leaves the range that
+// two-float products have.
+__device__ __forceinline__ F2 top_scaled(float x, float m, F2 inv_t) {
+  const float f = (x - m) * inv_t.hi;
+  return f > -1.0e30f ? f2_mul(two_diff(x, m), inv_t) : F2{f, 0.f};
+}
+
 // The record of a row from its k best (keys sel[0 .. kk), any order; sorted
 // here) and the rest's mass st relative to mt (0: none).
 template <int NW>
 __device__ __forceinline__ void top_write(const TopParams& p, int r, unsigned long long* sel, int kk, float mt, F2 st,
-                                          const float* tab, F2* f2red, double* s_lns) {
+                                          const float* tab, F2* f2red, F2* s_lns) {
   constexpr int NT = NW * 32, E = kMaxK / NT;
   const int tid = threadIdx.x, k = p.k;
   const F2 c{p.c, p.c_lo};
@@ -210,19 +217,29 @@ __device__ __forceinline__ void top_write(const TopParams& p, int r, unsigned lo
   F2 sk{0.f, 0.f};
   for (int j = tid; j < kk; j += NT) sk = f2_add(sk, weight_f2(comp_val(sel[j]), M, c, tab));
   sk = block_sum_f2_n<NW>(sk, f2red);
-  if (tid == 0) {
+  // ln of the whole row's sum relative to M, and of the rest's relative to mt
+  if (tid < 32) {
     const bool some = st.hi > 0.f;
-    const F2 tail_m = some ? f2_mul(st, weight_f2(mt, M, c, tab)) : F2{0.f, 0.f};
-    const double lns = log(f2_double(f2_add(sk, tail_m)));
-    *s_lns = lns;
-    p.tail[r] = some ? (float)(((double)mt - (double)M) * p.inv_t + log(f2_double(st)) - lns) : -INFINITY;
+    const F2 all = some ? f2_add(sk, f2_mul(st, weight_f2(mt, M, c, tab))) : sk;
+    const F2 lg = f2_log(tid == 1 && some ? st : all, tab);
+    const F2 lt{__shfl_sync(0xffffffffu, lg.hi, 1), __shfl_sync(0xffffffffu, lg.lo, 1)};
+    if (tid == 0) {
+      *s_lns = lg;
+      const F2 d = top_scaled(mt, M, p.inv_t);
+      p.tail[r] = some ? (d.hi > -1.0e30f ? f2_add(d, f2_add(lt, f2_neg(lg))).hi : d.hi) : -INFINITY;
+    }
   }
   __syncthreads();
-  const double lns = *s_lns;
+  const F2 lns = *s_lns;
   for (int e = tid; e < k; e += NT) {
     const bool on = e < kk;
+    float lp = -INFINITY;
+    if (on) {
+      const F2 d = top_scaled(comp_val(sel[e]), M, p.inv_t);
+      lp = d.hi > -1.0e30f ? f2_add(d, f2_neg(lns)).hi : d.hi;
+    }
     p.indices[(size_t)r * k + e] = on ? comp_idx(sel[e]) : -1;
-    p.logprobs[(size_t)r * k + e] = on ? (float)(((double)comp_val(sel[e]) - (double)M) * p.inv_t - lns) : -INFINITY;
+    p.logprobs[(size_t)r * k + e] = lp;
   }
 }
 
@@ -524,7 +541,7 @@ struct TopRowSmem {
   F2 f2red[kTlWarps];
   int ired[kTlWarps];
   unsigned long long u64red[kTlWarps];
-  double lns;
+  F2 lns;
   int nvec[3];                                  // listed vectors of a step, by step % 3
   int nk, count;
   uint16_t list[2][kTrStep];                    // their places in the step, by step % 2
