@@ -531,7 +531,7 @@ constexpr int kTrStep = kTrU * kTlThreads;      // vectors per step
 // Listed vectors a step that need no look at the buffer's end; candidates at
 // which it is cut back; its size.
 __host__ __device__ constexpr int tr_few(int k) { return k + k / 4 < 64 ? 64 : k + k / 4 < kTrStep ? k + k / 4 : kTrStep; }
-__host__ __device__ constexpr int tr_trigger(int k) { return 2 * k + 64 < 512 ? 512 : 2 * k + 64; }
+__host__ __device__ constexpr int tr_trigger(int k) { return 4 * k + 64 < 512 ? 512 : 4 * k + 64; }
 __host__ __device__ constexpr int tr_capacity(int k) { return tr_trigger(k) + 8 * tr_few(k); }
 
 struct TopRowSmem {
