@@ -9,9 +9,6 @@ and pass their addresses.  There is no fallback.
 
 from __future__ import annotations
 
-import contextlib
-import ctypes
-
 import torch
 
 from ._binding import (_TORCH_DTYPE, SV_ERR_INVALID_ARG, SV_OK, SvError, _addr, _c_float, _c_int, _c_ptr, _c_size,
@@ -91,7 +88,7 @@ def sv_distill_loss_grad(R, V, student, dtype, indices, logprobs, tail, k, tempe
 
 def _need(name, t, dtype, shape, device):
     """t is None, or a contiguous CUDA tensor of this type and shape on `device`."""
-    if t is None:
+    if t is None or (t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous()):
         return
     _need_cuda(name, t, dtype)
     if tuple(t.shape) != tuple(shape):
@@ -106,20 +103,33 @@ def _need_rows(name, t):
         raise ValueError(f"unsupported {name} dtype {t.dtype}")
 
 
-@contextlib.contextmanager
+class _Here:
+    """The device is current already: nothing to enter or leave."""
+
+    def __enter__(self):
+        pass
+
+    def __exit__(self, *exc):
+        return False
+
+
+_HERE = _Here()
+
+
 def _on(device, stream):
-    """Run on `stream` (or the device's current stream) with the rows' device
-    current; what is allocated inside belongs to that stream."""
+    """A context for `stream` (or the device's current stream) with the rows'
+    device current; what is allocated inside belongs to that stream."""
     if stream is not None:
         if stream.device != device:
             raise ValueError(f"stream is on {stream.device}, the rows on {device}")
-        with torch.cuda.stream(stream):
-            yield stream.cuda_stream
-    elif torch.cuda.current_device() != device.index:
-        with torch.cuda.device(device):
-            yield torch.cuda.current_stream(device).cuda_stream
-    else:
-        yield torch.cuda.current_stream(device).cuda_stream
+        return torch.cuda.stream(stream)
+    if torch.cuda.current_device() != device.index:
+        return torch.cuda.device(device)
+    return _HERE
+
+
+def _handle(device):
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def adjust_logits(logits, *, draft=None, history=None, history_len=None, prompt_len=None, repetition=None,
@@ -157,8 +167,9 @@ def adjust_logits(logits, *, draft=None, history=None, history_len=None, prompt_
     _need("history", history, i32, (B, H), dev)
     _need("history_len", history_len, i32, (B,), dev)
     _need("prompt_len", prompt_len, i32, (B,), dev)
-    for name, t in (("repetition", repetition), ("frequency", frequency), ("presence", presence)):
-        _need(name, t, f32, (B,), dev)
+    _need("repetition", repetition, f32, (B,), dev)
+    _need("frequency", frequency, f32, (B,), dev)
+    _need("presence", presence, f32, (B,), dev)
     _need("bias_tokens", bias_tokens, i32, (B, NB), dev)
     _need("bias_values", bias_values, f32, (B, NB), dev)
     _need("mask", mask, i32, (M, (V + 31) // 32), dev)
@@ -173,13 +184,13 @@ def adjust_logits(logits, *, draft=None, history=None, history_len=None, prompt_
         raise ValueError("mask_index needs mask")
     if mask is not None and mask_index is None and M != B * G1:
         raise ValueError(f"without mask_index the mask has one row per logits row: {B * G1}, got {M}")
-    with _on(dev, stream) as handle:
+    with _on(dev, stream):
         if out is None:
             out = torch.zeros_like(logits) if gamma_b is not None else torch.empty_like(logits)
         st = sv_adjust_logits(B, G1 - 1, V, _addr(logits), _TORCH_DTYPE[logits.dtype], _addr(out), _addr(draft),
                               _addr(gamma_b), _addr(history), H, _addr(history_len), _addr(prompt_len),
                               _addr(repetition), _addr(frequency), _addr(presence), _addr(bias_tokens),
-                              _addr(bias_values), NB, _addr(mask), M, _addr(mask_index), handle)
+                              _addr(bias_values), NB, _addr(mask), M, _addr(mask_index), _handle(dev))
     if st != SV_OK:
         raise SvError(st, "sv_adjust_logits")
     return out
@@ -221,7 +232,7 @@ def top_logits(logits, k, temperature=1.0, *, workspace=None, stream=None, outpu
             _need(name, t, dt, shape, dev)
     if not 1 <= k <= 1024:
         raise ValueError(f"k must be in 1..1024, got {k}")
-    with _on(dev, stream) as handle:
+    with _on(dev, stream):
         if outputs is None:
             outputs = (torch.empty(lead + (k,), dtype=torch.int32, device=dev),
                        torch.empty(lead + (k,), dtype=torch.float32, device=dev),
@@ -230,7 +241,7 @@ def top_logits(logits, k, temperature=1.0, *, workspace=None, stream=None, outpu
             workspace = alloc_top_logits_workspace(R, V, k, dev)
         indices, logprobs, tail = outputs
         st = sv_top_logits(R, V, _addr(logits), _TORCH_DTYPE[logits.dtype], k, temperature, _addr(indices),
-                           _addr(logprobs), _addr(tail), _addr(workspace), workspace.numel(), handle)
+                           _addr(logprobs), _addr(tail), _addr(workspace), workspace.numel(), _handle(dev))
     if st != SV_OK:
         raise SvError(st, "sv_top_logits")
     return indices, logprobs, tail
@@ -259,13 +270,13 @@ class _DistillLoss(torch.autograd.Function):
     def forward(ctx, student, indices, logprobs, tail, temperature, weight):
         R, V, k = student.numel() // student.shape[-1], student.shape[-1], indices.shape[-1]
         dev = student.device
-        with _on(dev, None) as handle:
+        with _on(dev, None):
             loss = torch.empty(student.shape[:-1], dtype=torch.float32, device=dev)
             stats = None
             if ctx.needs_input_grad[0]:
                 stats = torch.empty(R, SV_DISTILL_STAT_WORDS, dtype=torch.float32, device=dev)
             st = sv_distill_forward(R, V, _addr(student), _TORCH_DTYPE[student.dtype], _addr(indices), _addr(logprobs),
-                                    _addr(tail), k, temperature, _addr(weight), _addr(loss), _addr(stats), handle)
+                                    _addr(tail), k, temperature, _addr(weight), _addr(loss), _addr(stats), _handle(dev))
         if st != SV_OK:
             raise SvError(st, "sv_distill_forward")
         ctx.save_for_backward(student, indices, logprobs, weight, stats)
@@ -279,12 +290,12 @@ class _DistillLoss(torch.autograd.Function):
         if stats is None:
             return (None,) * 6
         R, V, k = student.numel() // student.shape[-1], student.shape[-1], indices.shape[-1]
-        with _on(student.device, None) as handle:
+        with _on(student.device, None):
             grad_loss = grad_loss.contiguous()
             grad = torch.empty_like(student)
             st = sv_distill_backward(R, V, _addr(student), _TORCH_DTYPE[student.dtype], _addr(indices),
                                      _addr(logprobs), k, ctx.temperature, _addr(weight), _addr(stats),
-                                     _addr(grad_loss), _addr(grad), handle)
+                                     _addr(grad_loss), _addr(grad), _handle(student.device))
         if st != SV_OK:
             raise SvError(st, "sv_distill_backward")
         return grad, None, None, None, None, None
@@ -319,11 +330,11 @@ def distill_loss_grad(student, indices, logprobs, tail=None, temperature=1.0, *,
     R, V, k = _check_distill(student, indices, logprobs, tail, weight)
     dev = student.device
     _need("out_grad", out_grad, student.dtype, student.shape, dev)
-    with _on(dev, stream) as handle:
+    with _on(dev, stream):
         loss = torch.empty(student.shape[:-1], dtype=torch.float32, device=dev)
         grad = torch.empty_like(student, requires_grad=False) if out_grad is None else out_grad
         st = sv_distill_loss_grad(R, V, _addr(student), _TORCH_DTYPE[student.dtype], _addr(indices), _addr(logprobs),
-                                  _addr(tail), k, temperature, _addr(weight), _addr(loss), _addr(grad), handle)
+                                  _addr(tail), k, temperature, _addr(weight), _addr(loss), _addr(grad), _handle(dev))
     if st != SV_OK:
         raise SvError(st, "sv_distill_loss_grad")
     return loss, grad

@@ -52,6 +52,42 @@ struct DistillParams {
   void* grad;
 };
 
+// Beyond this a divergence is called infinite.
+constexpr float kDiFar = 1.0e30f;
+
+// w ((lp - tm) - (s - kr) / temperature): a listed token's term of the loss,
+// up to the row's constants.
+__device__ __forceinline__ F2 distill_term(F2 w, float lp, float tm, float s, float kr, F2 inv_t) {
+  return f2_mul(w, f2_add(two_diff(lp, tm), f2_neg(f2_mul(two_diff(s, kr), inv_t))));
+}
+
+// The loss of a row of weight 1 (all lanes of a warp; the three logarithms
+// side by side), in two-float throughout: sum_j p_j (ln p_j - ln q_j) + p_t
+// (ln p_t - ln q_t), with the row's constants (ln Z, ln S) taken out of the
+// sums.  E1: the sum of the listed tokens' terms.
+__device__ __forceinline__ float distill_loss(F2 Z, F2 S, F2 st, F2 E1, F2 wt, float ltail, float tm, float mt, float km,
+                                              float M, bool infinite, F2 inv_t, const float* tab) {
+  const int lane = threadIdx.x & 31;
+  const F2 mine = lane == 0 ? Z : lane == 1 ? S : st;
+  const F2 lg = mine.hi > 0.f ? f2_log(mine, tab) : F2{-INFINITY, 0.f};
+  const F2 lz{__shfl_sync(0xffffffffu, lg.hi, 0), __shfl_sync(0xffffffffu, lg.lo, 0)};
+  const F2 ls{__shfl_sync(0xffffffffu, lg.hi, 1), __shfl_sync(0xffffffffu, lg.lo, 1)};
+  const F2 lt{__shfl_sync(0xffffffffu, lg.hi, 2), __shfl_sync(0xffffffffu, lg.lo, 2)};
+  const float kr = km == -INFINITY ? M : km;
+  const bool tail = wt.hi != 0.f;
+  if (!(S.hi > 0.f && S.hi < INFINITY) || Z.hi != Z.hi) return __uint_as_float(0x7fffffffu);
+  // p wants what q has nothing of, or less than float32 can say
+  if (infinite || (M - kr) * inv_t.hi > kDiFar || (tail && (!(st.hi > 0.f) || (mt - kr) * inv_t.hi < -kDiFar)))
+    return INFINITY;
+  F2 e = E1;
+  if (tail) e = f2_add(e, f2_mul(wt, f2_add(two_diff(ltail, tm), f2_neg(f2_add(f2_mul(two_diff(mt, kr), inv_t), lt)))));
+  const float q = e.hi * __frcp_rn(Z.hi);            // e / Z: a quotient and its remainder's
+  const F2 rem = f2_add(e, f2_neg(f2_mul(Z, F2{q, 0.f})));
+  F2 sum = f2_norm(q, rem.hi * __frcp_rn(Z.hi));
+  sum = f2_add(sum, f2_add(ls, f2_neg(lz)));
+  return f2_add(sum, f2_mul(two_diff(M, kr), inv_t)).hi;
+}
+
 // 2^(d (c + c_lo)), one correction step: the weight of a value that lies d
 // below its reference.
 __device__ __forceinline__ float weight_fast(float d, float c, float c_lo) {
@@ -160,7 +196,7 @@ __global__ void __launch_bounds__(kDiThreads, 2) distill_kernel(const DistillPar
     }
     return;
   }
-  const F2 l2e{kLog2eHi, kLog2eLo};
+  const F2 l2e{kLog2eHi, kLog2eLo}, inv_t = f2_from(p.inv_t);
   F2 Z{0.f, 0.f}, WK{0.f, 0.f}, E1{0.f, 0.f};
   const F2 wt = p.tail ? weight_f2(ltail, tm, l2e, sm.tab) : F2{0.f, 0.f};
   const float kr = km == -INFINITY ? 0.f : km;      // the reference of the listed tokens' logarithms
@@ -174,13 +210,9 @@ __global__ void __launch_bounds__(kDiThreads, 2) distill_kernel(const DistillPar
         ws = weight_f2(sv_[q], km, c, sm.tab);
         Z = f2_add(Z, w);
         WK = f2_add(WK, ws);
-        if (w.hi != 0.f) {                          // w (ln p_j - ln q_j), up to the row's constants
-          if (sv_[q] == -INFINITY) {
-            sm.infinite = 1;
-          } else {
-            const double d = ((double)lpv[q] - (double)tm) - ((double)sv_[q] - (double)kr) * p.inv_t;
-            E1 = f2_add(E1, f2_mul(w, f2_from(d)));
-          }
+        if (w.hi != 0.f) {
+          if ((sv_[q] - kr) * inv_t.hi < -kDiFar) sm.infinite = 1;
+          else E1 = f2_add(E1, distill_term(w, lpv[q], tm, sv_[q], kr, inv_t));
         }
       }
       sm.sw[j] = w.hi;
@@ -344,19 +376,9 @@ __global__ void __launch_bounds__(kDiThreads, 2) distill_kernel(const DistillPar
       Elem<T>::store(gwin.base + gwin.a0 + id, sc * (sm.sq[j] * qs - w * invZ));
     }
   }
-  if (rank == 0 && tid == 0) {
-    // loss / weight = sum_j p_j (ln p_j - ln q_j) + p_t (ln p_t - ln q_t), the
-    // row's constants (ln Z, ln S) taken out of the sums
-    const double Zd = f2_double(Z), Sd = f2_double(sm.S);
-    double e = f2_double(E1);
-    if (wt.hi != 0.f) {
-      const double std_ = f2_double(sm.st);
-      e += f2_double(wt) * (((double)ltail - (double)tm) - (((double)sm.mt - (double)kr) * p.inv_t + log(std_)));
-    }
-    double l = e / Zd - log(Zd) + log(Sd) + ((double)sm.M - (double)kr) * p.inv_t;
-    if (!(Sd > 0.0 && Sd < (double)INFINITY)) l = __longlong_as_double(0x7fffffffffffffffll);
-    else if (sm.infinite && l == l) l = (double)INFINITY;
-    p.loss[r] = (float)((double)wgt * l);
+  if (rank == 0 && warp == 0) {
+    const float l = distill_loss(Z, sm.S, sm.st, E1, wt, ltail, tm, sm.mt, km, sm.M, sm.infinite, inv_t, sm.tab);
+    if (lane == 0) p.loss[r] = wgt * l;
   }
 }
 

@@ -187,44 +187,12 @@ __device__ __forceinline__ void dp_statistics(const float4* part, int C, const D
   }
 }
 
-// The loss of a row (one warp: the three logarithms side by side), in
-// two-float throughout: loss / weight = sum_j p_j (ln p_j - ln q_j) + p_t (ln p_t
-// - ln q_t), with the row's constants (ln Z, ln S) taken out of the sums.
+// The loss of a row (one warp).
 __device__ __forceinline__ void dp_loss(const DpList& L, const DpStat& s, F2 inv_t, const float* tab, float* loss) {
-  const int lane = threadIdx.x & 31;
-  if (L.live != 2) {
-    if (lane == 0) *loss = 0.f;
-    return;
-  }
-  const F2 mine = lane == 0 ? L.Z : lane == 1 ? s.S : F2{s.st, 0.f};
-  const F2 lg = mine.hi > 0.f ? f2_log(mine, tab) : F2{-INFINITY, 0.f};
-  const F2 lz{__shfl_sync(0xffffffffu, lg.hi, 0), __shfl_sync(0xffffffffu, lg.lo, 0)};
-  const F2 ls{__shfl_sync(0xffffffffu, lg.hi, 1), __shfl_sync(0xffffffffu, lg.lo, 1)};
-  const F2 lt{__shfl_sync(0xffffffffu, lg.hi, 2), __shfl_sync(0xffffffffu, lg.lo, 2)};
-  if (lane == 0) {
-    const float kr = L.km == -INFINITY ? s.M : L.km;
-    const bool tail = L.wt.hi != 0.f;
-    // p wants what q has nothing of, or less than float32 can say
-    const bool infinite = L.infinite || (s.M - kr) * inv_t.hi > 1.0e30f ||
-                          (tail && (!(s.st > 0.f) || (s.mt - kr) * inv_t.hi < -1.0e30f));
-    float l;
-    if (!(s.S.hi > 0.f && s.S.hi < INFINITY) || L.Z.hi != L.Z.hi) {
-      l = __uint_as_float(0x7fffffffu);
-    } else if (infinite) {
-      l = INFINITY;
-    } else {
-      F2 e = L.E1;
-      if (tail)
-        e = f2_add(e, f2_mul(L.wt, f2_add(two_diff(L.ltail, L.tm), f2_neg(f2_add(f2_mul(two_diff(s.mt, kr), inv_t), lt)))));
-      const float q = e.hi * __frcp_rn(L.Z.hi);      // e / Z: a quotient and its remainder's
-      const F2 rem = f2_add(e, f2_neg(f2_mul(L.Z, F2{q, 0.f})));
-      F2 sum = f2_norm(q, rem.hi * __frcp_rn(L.Z.hi));
-      sum = f2_add(sum, f2_add(ls, f2_neg(lz)));
-      sum = f2_add(sum, f2_mul(two_diff(s.M, kr), inv_t));
-      l = sum.hi;
-    }
-    *loss = L.wgt * l;
-  }
+  float l = 0.f;
+  if (L.live == 2)
+    l = L.wgt * distill_loss(L.Z, s.S, F2{s.st, 0.f}, L.E1, L.wt, L.ltail, L.tm, s.mt, L.km, s.M, L.infinite, inv_t, tab);
+  if ((threadIdx.x & 31) == 0) *loss = l;
 }
 
 // WHOLE: V is a multiple of the vector width, so every row is whole vectors.
@@ -585,8 +553,8 @@ __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const Di
             ws_q = weight_f2(s_q, km, c, sm.tab);
             if (w_q.hi != 0.f) {
               // w (ln p_j - ln q_j), up to the row's constants
-              if ((s_q - kr) * inv_t.hi < -1.0e30f) L.infinite = 1;
-              else e1 = f2_add(e1, f2_mul(w_q, f2_add(two_diff(lp_q, tm), f2_neg(f2_mul(two_diff(s_q, kr), inv_t)))));
+              if ((s_q - kr) * inv_t.hi < -kDiFar) L.infinite = 1;
+              else e1 = f2_add(e1, distill_term(w_q, lp_q, tm, s_q, kr, inv_t));
             }
             const int o = id_q + win.a0 - v0 * VW;
             if (o >= 0 && o < (v1 - v0) * VW) {
