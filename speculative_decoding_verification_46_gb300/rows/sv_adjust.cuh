@@ -63,8 +63,8 @@ struct AdjustParams {
 // One more token of the sequence: note it if it falls into the tile.
 __device__ __forceinline__ void adjust_note(uint32_t* cnt, uint16_t* list, int* nlist, int token, int t0, int n,
                                             uint32_t flag) {
-  const unsigned o = (unsigned)(token - t0);
-  if (token >= 0 && o < (unsigned)n) {
+  const unsigned o = (unsigned)token - (unsigned)t0;   // a negative token is far out
+  if (o < (unsigned)n) {
     const uint32_t old = flag ? atomicOr(cnt + o, flag) : atomicAdd(cnt + o, 1u);
     if (old == 0u) list[atomicAdd(nlist, 1)] = (uint16_t)o;   // the first to meet it lists it
   }
@@ -94,35 +94,69 @@ __device__ __forceinline__ void adjust_masks(const AdjustParams& p, const Adjust
   s.mask[threadIdx.x] = mi < 0 ? kAdNone : mi < p.M ? mi : kAdNothing;
 }
 
-// The tile's tokens of the sequence; complete after the next barrier.
+// The tile's tokens of the sequence.  start() issues every load that depends
+// on nothing (the history's first 8192 tokens before its length is known, four
+// tokens a load where its rows are 16-byte aligned), so that a tile's
+// preparation is one round trip to memory and not one after another; finish()
+// counts, and is complete after the next barrier.
 template <typename T>
-__device__ __forceinline__ void adjust_collect(const AdjustParams& p, const AdjustTile<T>& s) {
-  const int tid = threadIdx.x, b = s.b, G = p.G1 - 1;
-  for (int i = tid; i < p.tile / 4; i += kAdThreads) reinterpret_cast<uint4*>(s.cnt)[i] = make_uint4(0u, 0u, 0u, 0u);
-  if (tid == 0) *s.nlist = *s.nb = 0;
-  if (p.count && p.draft && tid < s.gb) s.draft[tid] = __ldg(p.draft + (size_t)b * G + tid);
-  int len = 0, np = 0;
-  if (p.count && p.history) {
-    len = min(max(__ldg(p.history_len + b), 0), p.H);
-    np = p.prompt_len ? min(max(__ldg(p.prompt_len + b), 0), len) : 0;
+struct AdjustCollect {
+  int4 tok[4];
+  int len, np, quads, draft;
+  __device__ __forceinline__ const int32_t* history(const AdjustParams& p, const AdjustTile<T>& s) const {
+    return p.history + (size_t)s.b * p.H;
   }
-  const int32_t* h = p.history + (size_t)b * p.H;
-  __syncthreads();
-  for (int i0 = tid; i0 < len; i0 += 8 * kAdThreads) {
-    int tok[8];
+  __device__ __forceinline__ void start(const AdjustParams& p, const AdjustTile<T>& s) {
+    const int tid = threadIdx.x;
+    len = np = quads = 0;
+    draft = p.count && p.draft && tid < p.G1 - 1 ? __ldg(p.draft + (size_t)s.b * (p.G1 - 1) + tid) : -1;
+    if (p.count && p.history) {
+      len = __ldg(p.history_len + s.b);
+      np = p.prompt_len ? __ldg(p.prompt_len + s.b) : 0;
+      const int32_t* h = history(p, s);
+      quads = (reinterpret_cast<uintptr_t>(h) & 15u) == 0 ? p.H >> 2 : 0;
 #pragma unroll
-    for (int u = 0; u < 8; ++u) tok[u] = i0 + u * kAdThreads < len ? __ldg(h + i0 + u * kAdThreads) : -1;
+      for (int u = 0; u < 4; ++u) {
+        const int q = tid + u * kAdThreads;
+        tok[u] = q < quads ? __ldg(reinterpret_cast<const int4*>(h) + q) : make_int4(-1, -1, -1, -1);
+      }
+    }
+    for (int i = tid; i < p.tile / 4; i += kAdThreads) reinterpret_cast<uint4*>(s.cnt)[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (tid == 0) *s.nlist = *s.nb = 0;
+  }
+  __device__ __forceinline__ void note(const AdjustTile<T>& s, int i, int token) const {
+    if (i < len) adjust_note(s.cnt, s.list, s.nlist, token, s.t0, s.n, i < np ? kAdPrompt : 0u);
+  }
+  __device__ __forceinline__ void note(const AdjustTile<T>& s, int q, const int4& t) const {
+    note(s, 4 * q, t.x);
+    note(s, 4 * q + 1, t.y);
+    note(s, 4 * q + 2, t.z);
+    note(s, 4 * q + 3, t.w);
+  }
+  // a barrier lies between start and finish
+  __device__ __forceinline__ void finish(const AdjustParams& p, const AdjustTile<T>& s) {
+    const int tid = threadIdx.x;
+    if (p.count && p.history) {
+      len = min(max(len, 0), p.H);
+      np = min(max(np, 0), len);
+      const int32_t* h = history(p, s);
 #pragma unroll
-    for (int u = 0; u < 8; ++u)
-      adjust_note(s.cnt, s.list, s.nlist, tok[u], s.t0, s.n, i0 + u * kAdThreads < np ? kAdPrompt : 0u);
+      for (int u = 0; u < 4; ++u) note(s, tid + u * kAdThreads, tok[u]);
+      for (int q = tid + 4 * kAdThreads; 4 * q < len && q < quads; q += kAdThreads)
+        note(s, q, __ldg(reinterpret_cast<const int4*>(h) + q));
+      for (int i = 4 * quads + tid; i < len; i += kAdThreads) note(s, i, __ldg(h + i));
+    }
+    if (p.count && p.draft && tid < s.gb) {
+      s.draft[tid] = draft;
+      adjust_note(s.cnt, s.list, s.nlist, draft, s.t0, s.n, kAdDraft);
+    }
+    for (int i = tid; i < p.NB; i += kAdThreads) {
+      const int tok_i = __ldg(p.bias_tokens + (size_t)s.b * p.NB + i);
+      adjust_note(s.cnt, s.list, s.nlist, tok_i, s.t0, s.n, kAdBias);
+      if (tok_i >= s.t0 && tok_i < s.t0 + s.n) s.blist[atomicAdd(s.nb, 1)] = make_int2(tok_i - s.t0, i);
+    }
   }
-  if (p.count && p.draft && tid < s.gb) adjust_note(s.cnt, s.list, s.nlist, s.draft[tid], s.t0, s.n, kAdDraft);
-  for (int i = tid; i < p.NB; i += kAdThreads) {
-    const int tok = __ldg(p.bias_tokens + (size_t)b * p.NB + i);
-    adjust_note(s.cnt, s.list, s.nlist, tok, s.t0, s.n, kAdBias);
-    if (tok >= s.t0 && tok < s.t0 + s.n) s.blist[atomicAdd(s.nb, 1)] = make_int2(tok - s.t0, i);
-  }
-}
+};
 
 struct AdjustPenalties {
   float rep, freq, pres;
@@ -246,12 +280,14 @@ __global__ void __launch_bounds__(kAdThreads, 2) adjust_staged_kernel(const Adju
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
+  AdjustCollect<T> collect;
+  collect.start(p, s);
+  const AdjustPenalties pen(p, s.b);
   adjust_masks(p, s);
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < kAdStages - 1; ++i) issue(i);
-  const AdjustPenalties pen(p, s.b);
-  adjust_collect(p, s);
+  collect.finish(p, s);
   __syncthreads();
   // a thread's first listed token keeps what is done to it: the same in every
   // row, unless it is drafted
@@ -323,52 +359,62 @@ __global__ void __launch_bounds__(kAdThreads, 2) adjust_direct_kernel(const Adju
   const int tid = threadIdx.x;
   const bool sparse = p.count || p.NB;
   const AdjustTile<T> s = adjust_tile<T>(p, smem_raw, sdraft, smask, counters);
+  AdjustCollect<T> collect;
+  if (sparse) collect.start(p, s);
   adjust_masks(p, s);
-  if (sparse) adjust_collect(p, s);
   __syncthreads();
+  if (sparse) {
+    collect.finish(p, s);
+    __syncthreads();
+  }
 
-  // ---- the rows, masked
-  for (int i = 0; i <= s.gb; ++i) {
-    const size_t row = (size_t)s.b * p.G1 + i;
-    const int mi = smask[i];
-    const bool none = mi == kAdNothing;
-    const uint32_t* mrow = mi >= 0 ? p.mask + (size_t)mi * p.W : nullptr;
-    if (!p.copy && mi == kAdNone) continue;
-    const size_t e0 = row * (size_t)p.V + s.t0;
-    const int a = (int)(e0 % VW);
-    const T* src = static_cast<const T*>(p.logits) + (e0 - a);
-    T* dst = static_cast<T*>(p.out) + (e0 - a);
-    const int nv = (a + s.n + VW - 1) / VW;
-    for (int j0 = tid; j0 < nv; j0 += 2 * kAdThreads) {
-      uint4 x[2];
-      uint32_t bits[2];
+  // ---- the rows, masked: the tile's vectors of all rows, four at a time (a
+  // vector waits for its mask before it is known whether it is read)
+  const int per = p.tile / VW + 1;                                 // vectors of a row, at most
+  const long long items = (long long)(s.gb + 1) * per;
+  for (long long it0 = tid; it0 < items; it0 += 4 * kAdThreads) {
+    uint4 x[4];
+    uint32_t bits[4];
+    int row[4], at[4];                                             // the row, and the vector's first element in the tile
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int j = j0 + u * kAdThreads;
-        const int o = j * VW - a;                                  // tile offset of the vector's first element
-        bits[u] = none ? 0u : kFull;
-        if (j < nv && mrow) bits[u] = adjust_bits<VW>(mrow, p.W, s.t0 + o);
-        const bool whole = o >= 0 && o + VW <= s.n;
-        if (j < nv && whole && bits[u] != 0u && (p.copy || bits[u] != kFull))
-          x[u] = *reinterpret_cast<const uint4*>(src + (size_t)j * VW);
+    for (int u = 0; u < 4; ++u) {
+      const long long it = it0 + u * kAdThreads;
+      const int i = it < items ? (int)(it / per) : 0;
+      const int a = (int)((((size_t)s.b * p.G1 + i) * (size_t)p.V + s.t0) % VW);
+      row[u] = i;
+      at[u] = (int)(it - (long long)i * per) * VW - a;
+      if (it >= items || at[u] >= s.n) row[u] = -1;                // no such vector
+      bits[u] = kFull;
+      if (row[u] >= 0) {
+        const int mi = smask[i];
+        if (mi == kAdNothing) bits[u] = 0u;
+        else if (mi >= 0) bits[u] = adjust_bits<VW>(p.mask + (size_t)mi * p.W, p.W, s.t0 + at[u]);
+        if (!p.copy && bits[u] == kFull) row[u] = -1;              // nothing changes
       }
+    }
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int j = j0 + u * kAdThreads;
-        if (j >= nv || (!p.copy && bits[u] == kFull)) continue;
-        const int o = j * VW - a;
-        if (o >= 0 && o + VW <= s.n) {
-          if (bits[u] == 0u) x[u] = make_uint4(TR::kPadWord, TR::kPadWord, TR::kPadWord, TR::kPadWord);
-          else adjust_masked<T>(x[u], bits[u]);
-          *reinterpret_cast<uint4*>(dst + (size_t)j * VW) = x[u];
-        } else {
-          for (int t = 0; t < VW; ++t) {
-            if (o + t < 0 || o + t >= s.n) continue;
-            const bool ok = (bits[u] >> t) & 1u;
-            if (ok && !p.copy) continue;
-            Elem<T>::store_raw(dst + (size_t)j * VW + t,
-                               ok ? Elem<T>::raw(src + (size_t)j * VW + t) : Elem<T>::kNegInf);
-          }
+    for (int u = 0; u < 4; ++u) {
+      const T* src = static_cast<const T*>(p.logits) + ((size_t)s.b * p.G1 + row[u]) * (size_t)p.V + s.t0;
+      if (row[u] >= 0 && bits[u] != 0u && at[u] >= 0 && at[u] + VW <= s.n)
+        x[u] = *reinterpret_cast<const uint4*>(src + at[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (row[u] < 0) continue;
+      const size_t e0 = ((size_t)s.b * p.G1 + row[u]) * (size_t)p.V + s.t0;
+      const T* src = static_cast<const T*>(p.logits) + e0;
+      T* dst = static_cast<T*>(p.out) + e0;
+      if (at[u] >= 0 && at[u] + VW <= s.n) {
+        if (bits[u] == 0u) x[u] = make_uint4(TR::kPadWord, TR::kPadWord, TR::kPadWord, TR::kPadWord);
+        else adjust_masked<T>(x[u], bits[u]);
+        *reinterpret_cast<uint4*>(dst + at[u]) = x[u];
+      } else {
+        for (int t = 0; t < VW; ++t) {
+          const int o = at[u] + t;
+          if (o < 0 || o >= s.n) continue;
+          const bool ok = (bits[u] >> t) & 1u;
+          if (ok && !p.copy) continue;
+          Elem<T>::store_raw(dst + o, ok ? Elem<T>::raw(src + o) : Elem<T>::kNegInf);
         }
       }
     }
