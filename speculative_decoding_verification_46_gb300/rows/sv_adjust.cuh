@@ -60,13 +60,14 @@ struct AdjustParams {
   const int32_t* mask_index;
 };
 
-// One more token of the sequence: note it if it falls into the tile.
-__device__ __forceinline__ void adjust_note(uint32_t* cnt, uint16_t* list, int* nlist, int token, int t0, int n,
-                                            uint32_t flag) {
+// One more token of the sequence: note it if it falls into the tile.  Nothing
+// waits for the atomic's result (with a list entry for the first to meet a
+// token, a warp waited some 200 cycles for each of its tokens in the tile).
+__device__ __forceinline__ void adjust_note(uint32_t* cnt, int token, int t0, int n, uint32_t flag) {
   const unsigned o = (unsigned)token - (unsigned)t0;   // a negative token is far out
   if (o < (unsigned)n) {
-    const uint32_t old = flag ? atomicOr(cnt + o, flag) : atomicAdd(cnt + o, 1u);
-    if (old == 0u) list[atomicAdd(nlist, 1)] = (uint16_t)o;   // the first to meet it lists it
+    if (flag) atomicOr(cnt + o, flag);
+    else atomicAdd(cnt + o, 1u);
   }
 }
 
@@ -125,7 +126,7 @@ struct AdjustCollect {
     if (tid == 0) *s.nlist = *s.nb = 0;
   }
   __device__ __forceinline__ void note(const AdjustTile<T>& s, int i, int token) const {
-    if (i < len) adjust_note(s.cnt, s.list, s.nlist, token, s.t0, s.n, i < np ? kAdPrompt : 0u);
+    if (i < len) adjust_note(s.cnt, token, s.t0, s.n, i < np ? kAdPrompt : 0u);
   }
   __device__ __forceinline__ void note(const AdjustTile<T>& s, int q, const int4& t) const {
     note(s, 4 * q, t.x);
@@ -148,12 +149,33 @@ struct AdjustCollect {
     }
     if (p.count && p.draft && tid < s.gb) {
       s.draft[tid] = draft;
-      adjust_note(s.cnt, s.list, s.nlist, draft, s.t0, s.n, kAdDraft);
+      adjust_note(s.cnt, draft, s.t0, s.n, kAdDraft);
     }
     for (int i = tid; i < p.NB; i += kAdThreads) {
       const int tok_i = __ldg(p.bias_tokens + (size_t)s.b * p.NB + i);
-      adjust_note(s.cnt, s.list, s.nlist, tok_i, s.t0, s.n, kAdBias);
+      adjust_note(s.cnt, tok_i, s.t0, s.n, kAdBias);
       if (tok_i >= s.t0 && tok_i < s.t0 + s.n) s.blist[atomicAdd(s.nb, 1)] = make_int2(tok_i - s.t0, i);
+    }
+    __syncthreads();
+    // the tokens met: four words a thread at a time, one reservation a warp
+    for (int w0 = 0; w0 < p.tile / 4; w0 += kAdThreads) {
+      const int w = w0 + tid;
+      uint4 c = make_uint4(0u, 0u, 0u, 0u);
+      if (w < p.tile / 4) c = reinterpret_cast<const uint4*>(s.cnt)[w];
+      const int mine = (c.x != 0u) + (c.y != 0u) + (c.z != 0u) + (c.w != 0u);
+      int upto = mine;
+#pragma unroll
+      for (int m = 1; m < 32; m <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, upto, m);
+        if ((tid & 31) >= m) upto += v;
+      }
+      int at = 0;
+      if ((tid & 31) == 31 && upto > 0) at = atomicAdd(s.nlist, upto);
+      at = __shfl_sync(0xffffffffu, at, 31) + upto - mine;
+      if (c.x != 0u) s.list[at++] = (uint16_t)(4 * w);
+      if (c.y != 0u) s.list[at++] = (uint16_t)(4 * w + 1);
+      if (c.z != 0u) s.list[at++] = (uint16_t)(4 * w + 2);
+      if (c.w != 0u) s.list[at] = (uint16_t)(4 * w + 3);
     }
   }
 };
