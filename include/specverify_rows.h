@@ -136,6 +136,8 @@ sv_status sv_top_logits(int R, int V, const void* logits, sv_dtype dtype, int k,
  *   stats       [R][SV_DISTILL_STAT_WORDS] float32 written by the forward
  *               pass for the backward pass of the same inputs
  *   grad_loss   [R] float32, the gradient with respect to each row's loss
+ *               (grad_loss_stride 1), or one value for all rows
+ *               (grad_loss_stride 0, what a sum of the losses hands back)
  *   grad        [R][V] of `dtype`; sv_distill_loss_grad forms the gradient of
  *               the sum of the losses.  grad may be student itself (in
  *               place), otherwise the two must not overlap.
@@ -150,7 +152,8 @@ sv_status sv_distill_forward(int R, int V, const void* student, sv_dtype dtype, 
                              float* loss, float* stats, sv_stream_t stream);
 sv_status sv_distill_backward(int R, int V, const void* student, sv_dtype dtype, const int32_t* indices,
                               const float* logprobs, int k, float temperature, const float* weight,
-                              const float* stats, const float* grad_loss, void* grad, sv_stream_t stream);
+                              const float* stats, const float* grad_loss, int grad_loss_stride, void* grad,
+                              sv_stream_t stream);
 sv_status sv_distill_loss_grad(int R, int V, const void* student, sv_dtype dtype, const int32_t* indices,
                                const float* logprobs, const float* tail, int k, float temperature, const float* weight,
                                float* loss, void* grad, sv_stream_t stream);

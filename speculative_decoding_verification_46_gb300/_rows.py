@@ -38,7 +38,7 @@ def _lib():
                                            _c_ptr, _c_ptr, _c_ptr, _c_ptr]
         lib.sv_distill_forward.restype = _c_int
         lib.sv_distill_backward.argtypes = [_c_int, _c_int, _c_ptr, _c_int, _c_ptr, _c_ptr, _c_int, _c_float, _c_ptr,
-                                            _c_ptr, _c_ptr, _c_ptr, _c_ptr]
+                                            _c_ptr, _c_ptr, _c_int, _c_ptr, _c_ptr]
         lib.sv_distill_backward.restype = _c_int
         lib.sv_distill_loss_grad.argtypes = [_c_int, _c_int, _c_ptr, _c_int, _c_ptr, _c_ptr, _c_ptr, _c_int, _c_float,
                                              _c_ptr, _c_ptr, _c_ptr, _c_ptr]
@@ -72,10 +72,10 @@ def sv_distill_forward(R, V, student, dtype, indices, logprobs, tail, k, tempera
                                          loss, stats, stream))
 
 
-def sv_distill_backward(R, V, student, dtype, indices, logprobs, k, temperature, weight, stats, grad_loss, grad,
-                        stream) -> int:
+def sv_distill_backward(R, V, student, dtype, indices, logprobs, k, temperature, weight, stats, grad_loss,
+                        grad_loss_stride, grad, stream) -> int:
     return int(_lib().sv_distill_backward(R, V, student, dtype, indices, logprobs, k, float(temperature), weight, stats,
-                                          grad_loss, grad, stream))
+                                          grad_loss, grad_loss_stride, grad, stream))
 
 
 def sv_distill_loss_grad(R, V, student, dtype, indices, logprobs, tail, k, temperature, weight, loss, grad,
@@ -291,11 +291,14 @@ class _DistillLoss(torch.autograd.Function):
             return (None,) * 6
         R, V, k = student.numel() // student.shape[-1], student.shape[-1], indices.shape[-1]
         with _on(student.device, None):
-            grad_loss = grad_loss.contiguous()
+            # a sum of the losses hands back one value, expanded
+            stride = 0 if not any(grad_loss.stride()) else 1
+            if stride:
+                grad_loss = grad_loss.contiguous()
             grad = torch.empty_like(student)
             st = sv_distill_backward(R, V, _addr(student), _TORCH_DTYPE[student.dtype], _addr(indices),
                                      _addr(logprobs), k, ctx.temperature, _addr(weight), _addr(stats),
-                                     _addr(grad_loss), _addr(grad), _handle(student.device))
+                                     _addr(grad_loss), stride, _addr(grad), _handle(student.device))
         if st != SV_OK:
             raise SvError(st, "sv_distill_backward")
         return grad, None, None, None, None, None

@@ -47,6 +47,7 @@ struct DistillParams {
   const float* tail;
   const float* weight;
   const float* grad_loss;            // backward
+  int up_stride;                     // 0: grad_loss is one value
   float* loss;
   float* stats;                      // [R][8]: mt, A, teacher maximum, 1 / Z, M, 1 / S, listed twice, usable
   void* grad;
@@ -394,7 +395,7 @@ __global__ void __launch_bounds__(kDiBwThreads, 4) distill_backward_kernel(const
   const int NV = win.vectors();
   const int v0 = min(h * p.SV, NV), v1 = min(v0 + p.SV, NV);
   const float wgt = p.weight ? __ldg(p.weight + r) : 1.f;
-  const float up = __ldg(p.grad_loss + r);
+  const float up = __ldg(p.grad_loss + (size_t)r * p.up_stride);
   const float* st = p.stats + (size_t)r * 8;
   if (wgt == 0.f || up == 0.f || __ldg(st + 7) == 0.f) {
     zero_slice(gwin, v0, v1);

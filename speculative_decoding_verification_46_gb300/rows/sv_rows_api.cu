@@ -45,6 +45,20 @@ int sm_count() {
   return n;
 }
 
+// Opt in to `smem` bytes of dynamic shared memory, once per kernel (`set`: a
+// static of the launch site), device and size.
+bool allow_smem(std::atomic<int> (&set)[64], const void* kern, size_t smem) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+  if (set[dev].load(std::memory_order_acquire) >= (int)smem) return true;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
+    cudaGetLastError();
+    return false;
+  }
+  set[dev].store((int)smem, std::memory_order_release);
+  return true;
+}
+
 sv_status launched() {
   return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
@@ -86,11 +100,9 @@ sv_status launch_adjust(sv::rows::AdjustParams p, cudaStream_t stream) {
   size_t smem = sparse ? (size_t)p.tile * 6 + (size_t)p.NB * 8 : 0;
   if (staged) smem += (size_t)sv::rows::kAdStages * (p.tile / sv::Tr<T>::VW + 1) * 16;
   // (the kernel's static shared memory counts toward the 48 KB that need no opt-in)
-  if (smem > 32 * 1024 &&
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
-    cudaGetLastError();
-    return SV_ERR_CUDA;
-  }
+  static std::atomic<int> set[3][64];
+  const int which = !staged ? 0 : p.V % sv::Tr<T>::VW == 0 ? 1 : 2;
+  if (smem > 32 * 1024 && !allow_smem(set[which], (const void*)kern, smem)) return SV_ERR_CUDA;
   kern<<<(unsigned)grid, sv::rows::kAdThreads, smem, stream>>>(p);
   return launched();
 }
@@ -134,10 +146,8 @@ sv_status launch_top_rows(const sv::rows::TopParams& p, cudaStream_t stream) {
   auto kern = p.V % sv::Tr<T>::VW == 0 ? sv::rows::top_row_kernel<T, true> : sv::rows::top_row_kernel<T, false>;
   const size_t smem = (size_t)sv::rows::kTrStages * sv::rows::kTrStep * sizeof(uint4) +
                       (size_t)sv::rows::tr_capacity(p.k) * sizeof(unsigned long long);
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
-    cudaGetLastError();
-    return SV_ERR_CUDA;
-  }
+  static std::atomic<int> set[2][64];
+  if (!allow_smem(set[p.V % sv::Tr<T>::VW == 0], (const void*)kern, smem)) return SV_ERR_CUDA;
   kern<<<(unsigned)p.R, sv::rows::kTlThreads, smem, stream>>>(p);
   return launched();
 }
@@ -193,10 +203,8 @@ sv_status launch_distill_pipe(sv::rows::DistillParams p, cudaStream_t stream) {
   p.SV = (int)ceil_div(nv, C);
   auto kern = p.V % VW == 0 ? sv::rows::distill_pipe_kernel<T, GRAD, true> : sv::rows::distill_pipe_kernel<T, GRAD, false>;
   const size_t smem = sizeof(sv::rows::DpSmem<T>);
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
-    cudaGetLastError();
-    return SV_ERR_CUDA;
-  }
+  static std::atomic<int> set[2][64];
+  if (!allow_smem(set[p.V % VW == 0], (const void*)kern, smem)) return SV_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)p.C);
   cfg.blockDim = dim3((unsigned)sv::rows::dp_threads(p.k));
@@ -414,15 +422,18 @@ extern "C" sv_status sv_distill_forward(int R, int V, const void* student, sv_dt
 
 extern "C" sv_status sv_distill_backward(int R, int V, const void* student, sv_dtype dtype, const int32_t* indices,
                                          const float* logprobs, int k, float temperature, const float* weight,
-                                         const float* stats, const float* grad_loss, void* grad, sv_stream_t stream) {
+                                         const float* stats, const float* grad_loss, int grad_loss_stride, void* grad,
+                                         sv_stream_t stream) {
   const sv_status st = check_distill(R, V, student, dtype, indices, logprobs, k, temperature);
   if (st != SV_OK || R == 0) return st;
-  if (!stats || !aligned16(stats) || !grad_loss || !grad || !aligned16(grad) ||
+  if (!stats || !aligned16(stats) || !grad_loss || grad_loss_stride < 0 || grad_loss_stride > 1 || !grad ||
+      !aligned16(grad) ||
       !same_or_apart(student, grad, (size_t)R * V * elem_size(dtype)))
     return SV_ERR_INVALID_ARG;
   sv::rows::DistillParams p = distill_params(R, V, student, indices, logprobs, nullptr, k, temperature, weight);
   p.stats = const_cast<float*>(stats);
   p.grad_loss = grad_loss;
+  p.up_stride = grad_loss_stride;
   p.grad = grad;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   switch (dtype) {

@@ -94,14 +94,15 @@ def test_top_workspace(sv):
 
 def _distill(sv, which, **kw):
     a = dict(R=4, V=100, student=A, dtype=sv.SV_DTYPE_F32, indices=A + 8192, logprobs=A + 12288, tail=A + 16384, k=8,
-             temperature=1.0, weight=None, loss=A + 20480, stats=A + 24576, grad_loss=A + 28672, grad=A + 32768)
+             temperature=1.0, weight=None, loss=A + 20480, stats=A + 24576, grad_loss=A + 28672, stride=1,
+             grad=A + 32768)
     a.update(kw)
     head = [a[n] for n in ("R", "V", "student", "dtype", "indices", "logprobs")]
     if which == "forward":
         return sv.sv_distill_forward(*head, a["tail"], a["k"], a["temperature"], a["weight"], a["loss"], a["stats"], None)
     if which == "backward":
-        return sv.sv_distill_backward(*head, a["k"], a["temperature"], a["weight"], a["stats"], a["grad_loss"], a["grad"],
-                                      None)
+        return sv.sv_distill_backward(*head, a["k"], a["temperature"], a["weight"], a["stats"], a["grad_loss"], a["stride"],
+                                      a["grad"], None)
     return sv.sv_distill_loss_grad(*head, a["tail"], a["k"], a["temperature"], a["weight"], a["loss"], a["grad"], None)
 
 
@@ -115,7 +116,7 @@ def test_distill_refuses(sv, which, kw):
 
 @pytest.mark.parametrize("which, kw", [("forward", dict(loss=None)), ("forward", dict(stats=A + 4)),
                                        ("backward", dict(stats=None)), ("backward", dict(grad_loss=None)),
-                                       ("backward", dict(grad=None)), ("backward", dict(grad=A + 16)),
+                                       ("backward", dict(grad=None)), ("backward", dict(stride=-1)), ("backward", dict(stride=2)), ("backward", dict(grad=A + 16)),
                                        ("backward", dict(grad=A + 32772)), ("loss_grad", dict(loss=None)),
                                        ("loss_grad", dict(grad=None)), ("loss_grad", dict(grad=A + 1584)),
                                        ("loss_grad", dict(grad=A + 32776))])
