@@ -100,7 +100,9 @@ sv_status sv_adjust_logits(int B, int gamma, int V, const void* logits, sv_dtype
  * k in 1..SV_MAX_TOP_K; logits [R][V] of `dtype`, R in 0..SV_MAX_ROWS.  The
  * workspace follows the contract of specverify.h (zero-filled before its
  * first use, left zero-filled, one per concurrent call);
- * sv_top_logits_workspace_bytes returns 0 for invalid sizes.
+ * sv_top_logits_workspace_bytes returns 0 for invalid sizes (it asks the
+ * current device for its number of SMs: with at least as many rows a call
+ * needs no more than the minimum).
  */
 size_t sv_top_logits_workspace_bytes(int R, int V, int k);
 sv_status sv_top_logits(int R, int V, const void* logits, sv_dtype dtype, int k, float temperature,

@@ -128,6 +128,12 @@ def _on(device, stream):
     return _HERE
 
 
+def _written(t):
+    """The caller's tensor has been written: autograd graphs that saved it must notice."""
+    if not t.is_inference():
+        torch.autograd.graph.increment_version(t)
+
+
 def _handle(device):
     return torch._C._cuda_getCurrentRawStream(device.index)
 
@@ -184,6 +190,7 @@ def adjust_logits(logits, *, draft=None, history=None, history_len=None, prompt_
         raise ValueError("mask_index needs mask")
     if mask is not None and mask_index is None and M != B * G1:
         raise ValueError(f"without mask_index the mask has one row per logits row: {B * G1}, got {M}")
+    given = out
     with _on(dev, stream):
         if out is None:
             out = torch.zeros_like(logits) if gamma_b is not None else torch.empty_like(logits)
@@ -193,11 +200,16 @@ def adjust_logits(logits, *, draft=None, history=None, history_len=None, prompt_
                               _addr(bias_values), NB, _addr(mask), M, _addr(mask_index), _handle(dev))
     if st != SV_OK:
         raise SvError(st, "sv_adjust_logits")
+    if given is not None:
+        _written(given)
     return out
 
 
 def alloc_top_logits_workspace(rows: int, V: int, k: int, device=None) -> torch.Tensor:
     """A zero-filled device workspace large enough for top_logits on `rows` rows."""
+    device = torch.device("cuda" if device is None else device)
+    if device.index is None:
+        device = torch.device("cuda", torch.cuda.current_device())
     with torch.cuda.device(device):
         n = sv_top_logits_workspace_bytes(rows, V, k)
     if n == 0:
@@ -232,6 +244,7 @@ def top_logits(logits, k, temperature=1.0, *, workspace=None, stream=None, outpu
             _need(name, t, dt, shape, dev)
     if not 1 <= k <= 1024:
         raise ValueError(f"k must be in 1..1024, got {k}")
+    given = outputs
     with _on(dev, stream):
         if outputs is None:
             outputs = (torch.empty(lead + (k,), dtype=torch.int32, device=dev),
@@ -244,6 +257,8 @@ def top_logits(logits, k, temperature=1.0, *, workspace=None, stream=None, outpu
                            _addr(logprobs), _addr(tail), _addr(workspace), workspace.numel(), _handle(dev))
     if st != SV_OK:
         raise SvError(st, "sv_top_logits")
+    for t in given or ():
+        _written(t)
     return indices, logprobs, tail
 
 
@@ -268,7 +283,7 @@ def _check_distill(student, indices, logprobs, tail, weight):
 class _DistillLoss(torch.autograd.Function):
     @staticmethod
     def forward(ctx, student, indices, logprobs, tail, temperature, weight):
-        R, V, k = student.numel() // student.shape[-1], student.shape[-1], indices.shape[-1]
+        R, V, k = student.numel() // max(student.shape[-1], 1), student.shape[-1], indices.shape[-1]
         dev = student.device
         with _on(dev, None):
             loss = torch.empty(student.shape[:-1], dtype=torch.float32, device=dev)
@@ -340,4 +355,6 @@ def distill_loss_grad(student, indices, logprobs, tail=None, temperature=1.0, *,
                                   _addr(tail), k, temperature, _addr(weight), _addr(loss), _addr(grad), _handle(dev))
     if st != SV_OK:
         raise SvError(st, "sv_distill_loss_grad")
+    if out_grad is not None:
+        _written(out_grad)
     return loss, grad

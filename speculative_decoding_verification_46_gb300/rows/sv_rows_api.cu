@@ -109,6 +109,20 @@ sv_status launch_adjust(sv::rows::AdjustParams p, cudaStream_t stream) {
 
 // ---------------------------------------------------------------- top logits
 
+// SPECVERIFY_PATH=toprow / =topslice overrides the choice between rows and slices (tests cover both).
+int top_override() {
+  const char* e = std::getenv("SPECVERIFY_PATH");
+  return !e ? 0 : std::strcmp(e, "toprow") == 0 ? 1 : std::strcmp(e, "topslice") == 0 ? 2 : 0;
+}
+
+// A CTA per row from as many rows as SMs on, slices of rows for fewer (152064
+// bf16, k 64: 100 rows 31 us in slices, 39 in one CTA each; 152 rows 41 and
+// 38; 608 rows 133 and 64).
+bool top_by_rows(long long R) {
+  const int o = top_override();
+  return o == 1 || (o == 0 && R >= sm_count());
+}
+
 struct TopLayout {
   size_t ticket, part, lists, total;
   int H, SV;
@@ -152,16 +166,9 @@ sv_status launch_top_rows(const sv::rows::TopParams& p, cudaStream_t stream) {
   return launched();
 }
 
-// SPECVERIFY_PATH=toprow / =topslice overrides the choice below (tests cover both).
-int top_override() {
-  const char* e = std::getenv("SPECVERIFY_PATH");
-  return !e ? 0 : std::strcmp(e, "toprow") == 0 ? 1 : std::strcmp(e, "topslice") == 0 ? 2 : 0;
-}
-
 template <typename T>
 sv_status launch_top(const sv::rows::TopParams& p, cudaStream_t stream) {
-  const int o = top_override();
-  if (o == 1 || (o == 0 && p.R >= sm_count())) return launch_top_rows<T>(p, stream);
+  if (top_by_rows(p.R)) return launch_top_rows<T>(p, stream);
   const int u = (int)ceil_div(p.SV, sv::rows::kTlThreads);
   if (u <= 1) return launch_top_u<T, 1>(p, stream);
   if (u <= 2) return launch_top_u<T, 2>(p, stream);
@@ -223,7 +230,7 @@ sv_status launch_distill_pipe(sv::rows::DistillParams p, cudaStream_t stream) {
   if (clusters == 0) {
     if (cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg) != cudaSuccess || clusters < 1) {
       cudaGetLastError();
-      return SV_ERR_CUDA;
+      return SV_ERR_UNSUPPORTED;   // no room for such a cluster: the other form
     }
     fit[dev][p.C].store(clusters, std::memory_order_relaxed);
   }
@@ -359,6 +366,7 @@ extern "C" sv_status sv_adjust_logits(int B, int gamma, int V, const void* logit
 
 extern "C" size_t sv_top_logits_workspace_bytes(int R, int V, int k) {
   if (!rows_ok(R, V) || k < 1 || k > SV_MAX_TOP_K) return 0;
+  if (top_by_rows(R)) return kAlign;   // nothing passes between CTAs
   // one size for every type: a float32 row has the most slices
   const size_t a = top_layout(R, V, k, 4, sm_count()).total, b = top_layout(R, V, k, 8, sm_count()).total;
   return std::max<size_t>(std::max(a, b), kAlign);

@@ -744,6 +744,46 @@ def test_training_step_captured_while_an_eager_graph_lives(sv):
     assert float((grad - x.grad).abs().max()) <= 2 * (3 * 70 + 16) * U
 
 
+def test_writes_into_given_tensors_are_seen_by_autograd(sv):
+    """A graph that saved a tensor refuses its backward pass after a call has
+    written over it; a gradient in place of the student likewise."""
+    x = torch.randn(2, 1, 64, device=DEV, requires_grad=True)
+    y = (x * 1).view(2, 1, 64)
+    saved = (y * y).sum()
+    pres, hist, n = torch.ones(2, device=DEV), torch.zeros(2, 1, dtype=torch.int32, device=DEV), torch.ones(2, dtype=torch.int32, device=DEV)
+    with torch.no_grad():
+        sv.adjust_logits(y, history=hist, history_len=n, presence=pres, out=y)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        saved.backward()
+    idx, lp = torch.zeros(2, 4, dtype=torch.int32, device=DEV), torch.zeros(2, 4, device=DEV)
+    s = torch.randn(2, 64, device=DEV, requires_grad=True)
+    t = s * 1
+    loss = sv.distill_loss(t, idx, lp).sum()
+    sv.distill_loss_grad(t.detach(), idx, lp, out_grad=t.detach())
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    with torch.inference_mode():                             # no versions there, and none needed
+        z = torch.randn(2, 1, 64, device=DEV)
+        sv.adjust_logits(z, history=hist, history_len=n, presence=pres, out=z)
+
+
+def test_a_workspace_by_default_and_two_streams_at_once(sv):
+    """Calls on two streams at the same time, each with its own workspace,
+    give what they give alone."""
+    a, b = _top_rows(1, 40, 60000, "bf16").to(DEV), _top_rows(2, 40, 60000, "bf16").to(DEV)
+    idx, lp, t = (v.to(DEV) for v in _record(5, 200, 30000, 20, True))
+    S = _student(5, 200, 30000, "bf16").to(DEV)
+    alone = [sv.top_logits(a, 30), sv.top_logits(b, 30), sv.distill_loss_grad(S, idx, lp, t), sv.distill_loss_grad(S, idx, lp, t)]
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(5):
+        got = [sv.top_logits(a, 30, stream=s1), sv.top_logits(b, 30, stream=s2), sv.distill_loss_grad(S, idx, lp, t, stream=s1),
+               sv.distill_loss_grad(S, idx, lp, t, stream=s2)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(u, v) for g, w in zip(got, alone) for u, v in zip(g, w))
+    assert sv.alloc_top_logits_workspace(3, 1000, 4).is_cuda
+
+
 def test_results_do_not_depend_on_the_run(sv):
     """No sum's order depends on the schedule: repeated calls agree bit for bit."""
     L, a = _adjust_inputs(5, 8, 4, 20000, "f32", H=3000, NB=100)
