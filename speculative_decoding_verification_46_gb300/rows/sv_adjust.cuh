@@ -22,7 +22,12 @@
 //       listed tokens are touched), or nothing is listed (a masked copy).
 //
 // The bound is HBM: every row is read and written once (vectors that a mask
-// rules out altogether are not read).
+// rules out altogether are not read).  256 sequences, gamma 8, V = 152064 bf16,
+// histories of 8192: 266 us, 5.0 TB/s (0.74 of the measured copy); what is
+// left is the tiles' preparation, of which two CTAs an SM hide only part (the
+// same at gamma 0, where it is most of the work: 87 us for 162 MB).  A tile of
+// 16 KB of a row and 512 threads: smaller ones count the history more often
+// (8 KB and 256 threads: 265 us, and 99 at gamma 0).
 #pragma once
 
 #include "sv_rows.cuh"

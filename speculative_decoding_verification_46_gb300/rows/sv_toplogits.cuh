@@ -14,8 +14,11 @@
 // over the 64-bit keys (value, ~index), ranks them, and adds what the lists
 // hold beyond them to the mass outside.
 //
-// The bound is HBM for many rows (each row is read once) and the chain of
-// barriers of the selection for few.
+// top_row_kernel, further down, is the form for many rows (one CTA a row, no
+// hand-over).  Both read a row once.  Few rows are bound by the selection's
+// chain of barriers (one row of 152064 bf16, k = 64: 16 us; 20 rows of 1024
+// float32, k = 8: 9 us), many by instruction issue: 2304 rows of 152064 bf16, k
+// = 64: 220 us, 3.2 TB/s (0.47 of the measured copy; in slices 469 us).
 #pragma once
 
 #include "sv_rows.cuh"
