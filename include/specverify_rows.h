@@ -102,7 +102,7 @@ sv_status sv_adjust_logits(int B, int gamma, int V, const void* logits, sv_dtype
  * first use, left zero-filled, one per concurrent call);
  * sv_top_logits_workspace_bytes returns 0 for invalid sizes (it asks the
  * current device for its number of SMs: with at least as many rows a call
- * needs no more than the minimum).
+ * needs no more than the minimum, so fewer rows can need more than many).
  */
 size_t sv_top_logits_workspace_bytes(int R, int V, int k);
 sv_status sv_top_logits(int R, int V, const void* logits, sv_dtype dtype, int k, float temperature,

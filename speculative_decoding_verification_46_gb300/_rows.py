@@ -206,14 +206,17 @@ def adjust_logits(logits, *, draft=None, history=None, history_len=None, prompt_
 
 
 def alloc_top_logits_workspace(rows: int, V: int, k: int, device=None) -> torch.Tensor:
-    """A zero-filled device workspace large enough for top_logits on `rows` rows."""
+    """A zero-filled device workspace large enough for top_logits on up to `rows` rows."""
     device = torch.device("cuda" if device is None else device)
     if device.index is None:
         device = torch.device("cuda", torch.cuda.current_device())
     with torch.cuda.device(device):
         n = sv_top_logits_workspace_bytes(rows, V, k)
-    if n == 0:
-        raise SvError(SV_ERR_INVALID_ARG, "sv_top_logits_workspace_bytes")
+        if n == 0:
+            raise SvError(SV_ERR_INVALID_ARG, "sv_top_logits_workspace_bytes")
+        # fewer rows than SMs are taken in slices and need more than many rows do
+        sms = torch.cuda.get_device_properties(device).multi_processor_count
+        n = max([n] + [sv_top_logits_workspace_bytes(r, V, k) for r in range(1, min(rows, sms + 1))])
     return torch.zeros(n, dtype=torch.uint8, device=device)
 
 
@@ -251,7 +254,10 @@ def top_logits(logits, k, temperature=1.0, *, workspace=None, stream=None, outpu
                        torch.empty(lead + (k,), dtype=torch.float32, device=dev),
                        torch.empty(lead, dtype=torch.float32, device=dev))
         if workspace is None:
-            workspace = alloc_top_logits_workspace(R, V, k, dev)
+            n = sv_top_logits_workspace_bytes(R, V, k)
+            if n == 0:
+                raise SvError(SV_ERR_INVALID_ARG, "sv_top_logits")
+            workspace = torch.zeros(n, dtype=torch.uint8, device=dev)
         indices, logprobs, tail = outputs
         st = sv_top_logits(R, V, _addr(logits), _TORCH_DTYPE[logits.dtype], k, temperature, _addr(indices),
                            _addr(logprobs), _addr(tail), _addr(workspace), workspace.numel(), _handle(dev))

@@ -331,6 +331,14 @@ def test_top_extreme_temperatures(sv, top_path, dtype, T):
     assert not np.isnan(tail).any()
 
 
+def test_top_workspace_of_many_rows_serves_fewer(sv):
+    x = _top_rows(3, 400, 2500, "bf16")
+    ws = sv.alloc_top_logits_workspace(400, 2500, 7, DEV)
+    for rows in (400, 1, 20, 151, 152, 60, 400):
+        _check_top(sv, x[:rows], 7, 1.0, "bf16", workspace=ws)
+        assert int(ws.count_nonzero()) == 0
+
+
 def test_top_shapes_workspace_and_outputs(sv):
     x = _top_rows(3, 12, 2500, "bf16").view(2, 2, 3, 2500)
     ws = sv.alloc_top_logits_workspace(12, 2500, 40, DEV)
