@@ -167,7 +167,7 @@ def adjust_logits(logits, *, draft=None, history=None, history_len=None, prompt_
         raise ValueError("logits has no rows: [B, gamma+1, V] with gamma >= 0")
     H = history.shape[1] if history is not None and history.dim() == 2 else 0
     NB = bias_tokens.shape[1] if bias_tokens is not None and bias_tokens.dim() == 2 else 0
-    M = mask.shape[0] if mask is not None else 0
+    M = mask.shape[0] if mask is not None and mask.dim() == 2 else 0
     i32, f32 = torch.int32, torch.float32
     _need("draft", draft, i32, (B, G1 - 1), dev)
     _need("history", history, i32, (B, H), dev)
@@ -190,6 +190,9 @@ def adjust_logits(logits, *, draft=None, history=None, history_len=None, prompt_
         raise ValueError("mask_index needs mask")
     if mask is not None and mask_index is None and M != B * G1:
         raise ValueError(f"without mask_index the mask has one row per logits row: {B * G1}, got {M}")
+    # a table without rows has no address, and NULL would allow every token:
+    # any other address says that the table is there (with M = 0 it is not read)
+    table = _addr(mask_index) if mask_index is not None and M == 0 else _addr(mask)
     given = out
     with _on(dev, stream):
         if out is None:
@@ -197,7 +200,7 @@ def adjust_logits(logits, *, draft=None, history=None, history_len=None, prompt_
         st = sv_adjust_logits(B, G1 - 1, V, _addr(logits), _TORCH_DTYPE[logits.dtype], _addr(out), _addr(draft),
                               _addr(gamma_b), _addr(history), H, _addr(history_len), _addr(prompt_len),
                               _addr(repetition), _addr(frequency), _addr(presence), _addr(bias_tokens),
-                              _addr(bias_values), NB, _addr(mask), M, _addr(mask_index), _handle(dev))
+                              _addr(bias_values), NB, table, M, _addr(mask_index), _handle(dev))
     if st != SV_OK:
         raise SvError(st, "sv_adjust_logits")
     if given is not None:

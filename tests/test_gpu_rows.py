@@ -141,6 +141,17 @@ def test_adjust_ragged_and_in_place(sv, dtype, V, mode):
     _check_adjust(sv, L, a, dtype, inplace=mode == "inplace", out_fill=7.0 if mode == "given" else None)
 
 
+def test_adjust_mask_table_without_rows(sv):
+    """A negative index allows everything, one beyond the table nothing, also
+    where the table has no rows."""
+    L = torch.randn(2, 2, 70, device=DEV)
+    mi = torch.tensor([[-1, 0], [3, -1]], dtype=torch.int32, device=DEV)
+    got = sv.adjust_logits(L, mask=torch.zeros(0, 3, dtype=torch.int32, device=DEV), mask_index=mi)
+    assert torch.equal(got, torch.where((mi < 0)[..., None], L, torch.full_like(L, -math.inf)))
+    with pytest.raises(ValueError):
+        sv.adjust_logits(L, mask=torch.zeros((), dtype=torch.int32, device=DEV), mask_index=mi)
+
+
 @pytest.mark.parametrize("only", ["mask", "bias", "repetition", "frequency", "presence", "draft", "prompt", "none", "dense_mask"])
 @pytest.mark.parametrize("inplace", [False, True])
 def test_adjust_parts_alone(sv, only, inplace):
