@@ -639,6 +639,22 @@ def test_refusals_of_the_wrappers(sv):
         sv.distill_loss(L, torch.zeros(2, 3, 4, **i32), torch.zeros(2, 3, 4, device=DEV), temperature=-1.0)
 
 
+def test_loss_without_a_gradient_is_the_same(sv):
+    """No autograd node where nobody asks for a gradient; forward-mode
+    differentiation is refused, not dropped."""
+    x = torch.randn(5, 300, device=DEV)
+    idx, lp, tail = sv.top_logits(torch.randn(5, 300, device=DEV), 9)
+    want = sv.distill_loss(x.clone().requires_grad_(), idx, lp, tail)
+    assert want.requires_grad
+    with torch.no_grad():
+        off = sv.distill_loss(x.clone().requires_grad_(), idx, lp, tail)
+    for got in (sv.distill_loss(x, idx, lp, tail), off):
+        assert not got.requires_grad and torch.equal(got, want.detach())
+    with torch.autograd.forward_ad.dual_level():
+        with pytest.raises((RuntimeError, NotImplementedError)):
+            sv.distill_loss(torch.autograd.forward_ad.make_dual(x, torch.ones_like(x)), idx, lp, tail)
+
+
 def test_double_backward_is_refused(sv):
     x = torch.randn(1, 40, device=DEV, requires_grad=True)
     loss = sv.distill_loss(x, torch.zeros(1, 1, dtype=torch.int32, device=DEV), torch.zeros(1, 1, device=DEV))
