@@ -398,18 +398,18 @@ __global__ void __launch_bounds__(kAdThreads, 2) adjust_direct_kernel(const Adju
   // ---- the rows, masked: the tile's vectors of all rows, four at a time (a
   // vector waits for its mask before it is known whether it is read)
   const int per = p.tile / VW + 1;                                 // vectors of a row, at most
-  const long long items = (long long)(s.gb + 1) * per;
-  for (long long it0 = tid; it0 < items; it0 += 4 * kAdThreads) {
+  const int items = (s.gb + 1) * per;
+  for (int it0 = tid; it0 < items; it0 += 4 * kAdThreads) {
     uint4 x[4];
     uint32_t bits[4];
     int row[4], at[4];                                             // the row, and the vector's first element in the tile
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const long long it = it0 + u * kAdThreads;
-      const int i = it < items ? (int)(it / per) : 0;
+      const int it = it0 + u * kAdThreads;
+      const int i = it < items ? (int)((unsigned)it / (unsigned)per) : 0;
       const int a = (int)((((size_t)s.b * p.G1 + i) * (size_t)p.V + s.t0) % VW);
       row[u] = i;
-      at[u] = (int)(it - (long long)i * per) * VW - a;
+      at[u] = (it - i * per) * VW - a;
       if (it >= items || at[u] >= s.n) row[u] = -1;                // no such vector
       bits[u] = kFull;
       if (row[u] >= 0) {
