@@ -94,14 +94,14 @@ sv_status launch_adjust(sv::rows::AdjustParams p, cudaStream_t stream) {
   const long long grid = (long long)p.B * p.tiles;
   if (grid > 0x7fffffffll) return SV_ERR_UNSUPPORTED;
   const bool sparse = p.count || p.NB, staged = p.copy && sparse;
-  auto kern = !staged ? sv::rows::adjust_direct_kernel<T>
-              : p.V % sv::Tr<T>::VW == 0 ? sv::rows::adjust_staged_kernel<T, true> : sv::rows::adjust_staged_kernel<T, false>;
+  const bool whole = p.V % sv::Tr<T>::VW == 0;
+  auto kern = staged ? whole ? sv::rows::adjust_staged_kernel<T, true> : sv::rows::adjust_staged_kernel<T, false>
+              : whole ? sv::rows::adjust_direct_kernel<T, true> : sv::rows::adjust_direct_kernel<T, false>;
   size_t smem = sparse ? (size_t)p.tile * 6 + (size_t)p.NB * 8 : 0;
   if (staged) smem += (size_t)sv::rows::kAdStages * (p.tile / sv::Tr<T>::VW + 1) * 16;
   // (the kernel's static shared memory counts toward the 48 KB that need no opt-in)
-  static std::atomic<int> set[3][64];
-  const int which = !staged ? 0 : p.V % sv::Tr<T>::VW == 0 ? 1 : 2;
-  if (smem > 32 * 1024 && !allow_smem(set[which], (const void*)kern, smem)) return SV_ERR_CUDA;
+  static std::atomic<int> set[4][64];
+  if (smem > 32 * 1024 && !allow_smem(set[2 * staged + whole], (const void*)kern, smem)) return SV_ERR_CUDA;
   kern<<<(unsigned)grid, sv::rows::kAdThreads, smem, stream>>>(p);
   return launched();
 }
