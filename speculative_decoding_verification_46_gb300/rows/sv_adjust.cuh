@@ -76,6 +76,19 @@ __device__ __forceinline__ void adjust_note(uint32_t* cnt, int token, int t0, in
   }
 }
 
+// The same for tokens that are all in the prompt, or all behind it: four
+// instructions a token, no branch.  cnt: a shared-memory address.
+template <bool PROMPT>
+__device__ __forceinline__ void adjust_note_all(unsigned cnt, int token, int t0, int n) {
+  const unsigned o = (unsigned)token - (unsigned)t0;
+  if (PROMPT)
+    asm volatile("{\n\t.reg .pred in;\n\tsetp.lt.u32 in, %1, %2;\n\t@in red.shared.or.b32 [%0], %3;\n\t}"
+                 ::"r"(cnt + 4u * o), "r"(o), "r"((unsigned)n), "r"(kAdPrompt) : "memory");
+  else
+    asm volatile("{\n\t.reg .pred in;\n\tsetp.lt.u32 in, %1, %2;\n\t@in red.shared.add.u32 [%0], 1;\n\t}"
+                 ::"r"(cnt + 4u * o), "r"(o), "r"((unsigned)n) : "memory");
+}
+
 // What the CTA has in shared memory.
 template <typename T>
 struct AdjustTile {
@@ -133,11 +146,27 @@ struct AdjustCollect {
   __device__ __forceinline__ void note(const AdjustTile<T>& s, int i, int token) const {
     if (i < len) adjust_note(s.cnt, token, s.t0, s.n, i < np ? kAdPrompt : 0u);
   }
+  // four tokens from position 4 q on; a warp's lanes hold 128 in a row
   __device__ __forceinline__ void note(const AdjustTile<T>& s, int q, const int4& t) const {
-    note(s, 4 * q, t.x);
-    note(s, 4 * q + 1, t.y);
-    note(s, 4 * q + 2, t.z);
-    note(s, 4 * q + 3, t.w);
+    const int first = 4 * (q - (int)(threadIdx.x & 31)), last = first + 127;
+    const unsigned cnt = (unsigned)__cvta_generic_to_shared(s.cnt);
+    if (first >= len) return;
+    if (first >= np && last < len) {
+      adjust_note_all<false>(cnt, t.x, s.t0, s.n);
+      adjust_note_all<false>(cnt, t.y, s.t0, s.n);
+      adjust_note_all<false>(cnt, t.z, s.t0, s.n);
+      adjust_note_all<false>(cnt, t.w, s.t0, s.n);
+    } else if (last < np) {
+      adjust_note_all<true>(cnt, t.x, s.t0, s.n);
+      adjust_note_all<true>(cnt, t.y, s.t0, s.n);
+      adjust_note_all<true>(cnt, t.z, s.t0, s.n);
+      adjust_note_all<true>(cnt, t.w, s.t0, s.n);
+    } else {
+      note(s, 4 * q, t.x);
+      note(s, 4 * q + 1, t.y);
+      note(s, 4 * q + 2, t.z);
+      note(s, 4 * q + 3, t.w);
+    }
   }
   // a barrier lies between start and finish
   __device__ __forceinline__ void finish(const AdjustParams& p, const AdjustTile<T>& s) {
@@ -162,25 +191,31 @@ struct AdjustCollect {
       if (tok_i >= s.t0 && tok_i < s.t0 + s.n) s.blist[atomicAdd(s.nb, 1)] = make_int2(tok_i - s.t0, i);
     }
     __syncthreads();
-    // the tokens met: four words a thread at a time, one reservation a warp
-    for (int w0 = 0; w0 < p.tile / 4; w0 += kAdThreads) {
-      const int w = w0 + tid;
-      uint4 c = make_uint4(0u, 0u, 0u, 0u);
-      if (w < p.tile / 4) c = reinterpret_cast<const uint4*>(s.cnt)[w];
-      const int mine = (c.x != 0u) + (c.y != 0u) + (c.z != 0u) + (c.w != 0u);
-      int upto = mine;
+    // the tokens met: sixteen words a thread, one reservation a warp
+    static_assert(kAdTileBytes / 2 <= 16 * kAdThreads, "a tile is looked through once");
+    uint32_t met = 0u;                                               // bit 4 u + t: word t of the thread's u-th four
 #pragma unroll
-      for (int m = 1; m < 32; m <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, upto, m);
-        if ((tid & 31) >= m) upto += v;
+    for (int u = 0; u < 4; ++u) {
+      const int w = tid + u * kAdThreads;
+      if (w < p.tile / 4) {
+        const uint4 c = reinterpret_cast<const uint4*>(s.cnt)[w];
+        met |= (c.x != 0u ? 1u : 0u) << (4 * u) | (c.y != 0u ? 2u : 0u) << (4 * u) | (c.z != 0u ? 4u : 0u) << (4 * u) |
+               (c.w != 0u ? 8u : 0u) << (4 * u);
       }
-      int at = 0;
-      if ((tid & 31) == 31 && upto > 0) at = atomicAdd(s.nlist, upto);
-      at = __shfl_sync(0xffffffffu, at, 31) + upto - mine;
-      if (c.x != 0u) s.list[at++] = (uint16_t)(4 * w);
-      if (c.y != 0u) s.list[at++] = (uint16_t)(4 * w + 1);
-      if (c.z != 0u) s.list[at++] = (uint16_t)(4 * w + 2);
-      if (c.w != 0u) s.list[at] = (uint16_t)(4 * w + 3);
+    }
+    const int mine = __popc(met);
+    int upto = mine;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, upto, m);
+      if ((tid & 31) >= m) upto += v;
+    }
+    int at = 0;
+    if ((tid & 31) == 31 && upto > 0) at = atomicAdd(s.nlist, upto);
+    at = __shfl_sync(0xffffffffu, at, 31) + upto - mine;
+    for (; met; met &= met - 1u) {
+      const int k = __ffs(met) - 1;
+      s.list[at++] = (uint16_t)(4 * (tid + (k >> 2) * kAdThreads) + (k & 3));
     }
   }
 };
