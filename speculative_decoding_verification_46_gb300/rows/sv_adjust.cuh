@@ -23,11 +23,14 @@
 //
 // The bound is HBM: every row is read and written once (vectors that a mask
 // rules out altogether are not read).  256 sequences, gamma 8, V = 152064 bf16,
-// histories of 8192: 266 us, 5.0 TB/s (0.74 of the measured copy); what is
-// left is the tiles' preparation, of which two CTAs an SM hide only part (the
-// same at gamma 0, where it is most of the work: 87 us for 162 MB).  A tile of
-// 16 KB of a row and 512 threads: smaller ones count the history more often
-// (8 KB and 256 threads: 265 us, and 99 at gamma 0).
+// histories of 8192: 241 us, 5.6 TB/s (0.82 of the measured copy); what is
+// left is the tiles' preparation, which is instructions (at gamma 0, where it
+// is most of the work, 70 us for 162 MB; issue slots were 0.67 busy at 87 us)
+// and which three CTAs an SM hide in part.  A tile is 12 KB of a row and 384
+// threads: 16 KB and 512 threads, two CTAs an SM, 255 us, and 72 at gamma 0;
+// 8 KB and 256 threads, four, 256 and 86 (the history is counted more often).
+// CTAs that stay and load the next tile's history ahead: 305 (two an SM; they
+// prepare at the same time, where CTAs launched one by one drift apart).
 #pragma once
 
 #include "sv_rows.cuh"
@@ -35,8 +38,8 @@
 namespace sv {
 namespace rows {
 
-constexpr int kAdThreads = 512;           // two vectors of 16 bytes each per row of a full tile
-constexpr int kAdTileBytes = 16384;       // bytes of a row in a tile
+constexpr int kAdThreads = 384;           // two vectors of 16 bytes each per row of a full tile
+constexpr int kAdTileBytes = 32 * kAdThreads;   // bytes of a row in a tile
 constexpr int kAdStages = 3;
 constexpr uint32_t kAdPrompt = 1u << 31;  // the token stands in the prompt
 constexpr uint32_t kAdDraft = 1u << 30;   // the token is one of the round's drafts
@@ -114,8 +117,8 @@ __device__ __forceinline__ void adjust_masks(const AdjustParams& p, const Adjust
 }
 
 // The tile's tokens of the sequence.  start() issues every load that depends
-// on nothing (the history's first 8192 tokens before its length is known, four
-// tokens a load where its rows are 16-byte aligned), so that a tile's
+// on nothing (sixteen of the history's tokens a thread before its length is known,
+// four tokens a load where its rows are 16-byte aligned), so that a tile's
 // preparation is one round trip to memory and not one after another; finish()
 // counts, and is complete after the next barrier.
 template <typename T>
@@ -316,7 +319,7 @@ __device__ __forceinline__ void adjust_masked(uint4& x, uint32_t bits) {
 
 // WHOLE: V is a multiple of the vector width, so every row is whole vectors.
 template <typename T, bool WHOLE>
-__global__ void __launch_bounds__(kAdThreads, 2) adjust_staged_kernel(const AdjustParams p) {
+__global__ void __launch_bounds__(kAdThreads, 3) adjust_staged_kernel(const AdjustParams p) {
   using TR = Tr<T>;
   constexpr int VW = TR::VW;
   extern __shared__ __align__(16) unsigned char smem_raw[];
@@ -424,7 +427,7 @@ __global__ void __launch_bounds__(kAdThreads, 2) adjust_staged_kernel(const Adju
 }
 
 template <typename T, bool WHOLE>
-__global__ void __launch_bounds__(kAdThreads, 2) adjust_direct_kernel(const AdjustParams p) {
+__global__ void __launch_bounds__(kAdThreads, 3) adjust_direct_kernel(const AdjustParams p) {
   using TR = Tr<T>;
   constexpr int VW = TR::VW;
   constexpr uint32_t kFull = (1u << VW) - 1u;
@@ -447,7 +450,7 @@ __global__ void __launch_bounds__(kAdThreads, 2) adjust_direct_kernel(const Adju
   // vector waits for its mask before it is known whether it is read).  The
   // bound next to HBM is instruction issue, so the rows' vectors are counted
   // without divisions: 64 sequences, gamma 4, V = 128256 bf16, half of it
-  // allowed, in place: 34 us (169 MB, 0.73 of the measured copy); 2% allowed: 29.
+  // allowed, in place: 29 us (169 MB, 0.85 of the measured copy); 2% allowed: 26.
   const size_t first = (size_t)s.b * p.G1 * (size_t)p.V + s.t0;    // row 0's first element in the tile
   const T* logits = static_cast<const T*>(p.logits) + first;
   T* out = static_cast<T*>(p.out) + first;

@@ -77,11 +77,11 @@ void exponent_scale(float temperature, float* hi, float* lo) {
 
 // ---------------------------------------------------------------- adjust
 
-// Tokens per tile: 16 KB of a row, fewer for small calls, as long as every CTA
-// is resident at once (two an SM) and down to 256 tokens; the tiles of a row
+// Tokens per tile: 12 KB of a row, fewer for small calls, as long as every CTA
+// is resident at once (three an SM) and down to 256 tokens; the tiles of a row
 // are then made equal.
 void choose_tile(sv::rows::AdjustParams& p, int elem) {
-  const long long at_once = 2ll * sm_count() / p.B;
+  const long long at_once = 3ll * sm_count() / p.B;
   const long long tiles =
       std::max<long long>(ceil_div(p.V, sv::rows::kAdTileBytes / elem), std::min<long long>(at_once, ceil_div(p.V, 256)));
   p.tile = (int)(ceil_div(ceil_div(p.V, tiles), 64) * 64);
