@@ -203,6 +203,31 @@ def test_adjust_long_history_and_many_drafts(sv):
     _check_adjust(sv, L, a, "f32")
 
 
+@pytest.mark.parametrize("H", [128, 1000, 6148, 9001])
+def test_adjust_prompt_ends_anywhere(sv, H):
+    """Prompts and histories that end inside, at and beside the runs of tokens
+    that a warp counts at once."""
+    V, ends = 500, [0, 1, 127, 128, 129, 255, 256, 257, 640, 6143, 6144, 6145, 9000]
+    pairs = [(a, b) for a in ends for b in ends if a <= b <= H]
+    L, a = _adjust_inputs(H, len(pairs), 1, V, "f32", H=H, M=0)
+    a["prompt_len"] = torch.tensor([p[0] for p in pairs], dtype=torch.int32)
+    a["history_len"] = torch.tensor([p[1] for p in pairs], dtype=torch.int32)
+    _check_adjust(sv, L, a, "f32")
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("V", [40, 1000, 1003, 13000, 13001])
+@pytest.mark.parametrize("G", [0, 8, 33])
+@pytest.mark.parametrize("mode", ["new", "inplace"])
+def test_adjust_masks_alone(sv, dtype, V, G, mode):
+    L, a = _adjust_inputs(V + G, 2, G, V, dtype, M=7, ragged=True)
+    a = {k: a[k] for k in ("mask", "mask_index", "gamma_b")}
+    a["mask"][2] &= a["mask"][3] & a["mask"][4] & a["mask"][5]      # few allowed
+    L[0, 0, :: 3] = float("nan")
+    L[1, 0, 1 :: 5] = float("inf")
+    _check_adjust(sv, L, a, dtype, inplace=mode == "inplace", out_fill=3.0 if mode == "new" else None)
+
+
 def test_adjust_large_vocabulary_offsets(sv):
     """More than 2^31 elements: the last row's tokens are reached."""
     V, B = (1 << 24), 130
