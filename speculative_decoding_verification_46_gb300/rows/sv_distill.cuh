@@ -117,7 +117,8 @@ struct DistillSmem {
   uint32_t bits[kDiThreads * U * Tr<T>::VW / 32];   // the chunk's listed tokens
   int sid[kMaxK];                                   // listed tokens (-1: ignored)
   float sw[kMaxK];                                  // the teacher's weights, relative to its maximum
-  float sq[kMaxK];                                  // the student's, relative to mk
+  float sq[kMaxK];                                  // the student's, relative to km
+  float sx[kMaxK];                                  // the student's logits at the listed tokens
   float tab[128];
   float4 part[kDiMaxC];                             // (maximum, sum, twice) of every CTA of the cluster
   float fred[kDiWarps];
@@ -190,6 +191,7 @@ __global__ void __launch_bounds__(kDiThreads, 2) distill_kernel(const DistillPar
         km = fmaxf(km, sv_[q]);
       }
       sm.sid[j] = id;
+      sm.sx[j] = sv_[q];
     }
   }
   tm = block_max_n<kDiWarps>(tm, sm.fred);
@@ -300,11 +302,12 @@ __global__ void __launch_bounds__(kDiThreads, 2) distill_kernel(const DistillPar
   cluster_wait();
   const bool twice = __syncthreads_or(tid < p.C && sm.part[tid < p.C ? tid : 0].w != 0.f);
   if (twice) {                                      // a token's weight counts once, whatever the list says
+    // (from shared memory: in place, other CTAs write the row's gradient from here on)
     F2 w1{0.f, 0.f};
     for (int j = tid; j < k; j += kDiThreads) {
       bool first = sm.sid[j] >= 0;
       for (int i = 0; i < j && first; ++i) first = sm.sid[i] != sm.sid[j];
-      if (first) w1 = f2_add(w1, weight_f2(Elem<T>::load(win.base + win.a0 + sm.sid[j]), km, c, sm.tab));
+      if (first) w1 = f2_add(w1, weight_f2(sm.sx[j], km, c, sm.tab));
     }
     WK = block_sum_f2_n<kDiWarps>(w1, sm.f2red);
   }
