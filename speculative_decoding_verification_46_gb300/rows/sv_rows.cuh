@@ -206,9 +206,10 @@ __device__ __forceinline__ int block_sum_int_w(int v, int* sm) {
   return t;
 }
 
-// 2^((x - m) c) is formed as 2^(x c - rho), rho = round(m c), one multiply-add
+// 2^((x - m) c) is formed as 2^(x c - rho), rho = m c rounded, one multiply-add
 // and one exponential, where |rho| stays below this: rho is then off by at
-// most half, which a factor common to all terms takes back.  Beyond it
+// most half, which a factor common to all terms takes back (2^(rho - m c),
+// its exponent from one multiply-add).  Beyond it
 // (enormous logits or tiny temperatures) the difference is taken first.
 constexpr float kNear = 8.0e6f;
 

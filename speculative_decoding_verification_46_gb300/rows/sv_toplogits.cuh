@@ -551,24 +551,32 @@ struct TopRowSmem {
 };
 
 // A thread's running (maximum, sum) of the elements that are not set aside.
-// The sum is relative to rho = round(m c) in units of log2, so that a term
-// costs one multiply-add and one exponential; the rounding of rho leaves with
-// scale().  Terms gather in short float32 chains that take() adds to the
-// two-float total, so a row of 2^24 tokens is summed as exactly as a short
-// one.  Beyond kNear the difference is taken first.
+// The sum is relative to an integer rho next to m c in units of log2, so that
+// a term costs one multiply-add and one exponential, and a risen maximum
+// rescales the sum by a power of two, which the exponential instruction forms
+// exactly: a row may raise it at every step, whatever its logits have in
+// common (a reference that is not kept through a raise, m c itself, left the
+// sum's logarithm off by 2e-4 at logits around 1e4, by 0.08 around 3e6).  What
+// rho leaves of m c is taken back by scale().  Terms gather in short float32
+// chains that take() adds to the two-float total, so a row of 2^24 tokens is
+// summed as exactly as a short one.  Beyond kNear the difference is taken first.
 struct RunningSum {
-  float m = -INFINITY, rho = 0.f;
+  float m = -INFINITY, rho = -kNear;   // below any reference: what is rescaled then is 0, or NaN
   F2 s{0.f, 0.f};
   bool far = false;
   __device__ __forceinline__ float scale(float c) const { return far || m == -INFINITY ? 1.f : ex2_approx(-fmaf(m, c, -rho)); }
   __device__ __forceinline__ void raise(float to, float c) {
     if (to > m) {
-      const float f = m == -INFINITY ? 0.f : ex2_approx((m - to) * c) * scale(c);
+      const float r = rintf(to * c);
+      const bool to_far = !(fabsf(r) < kNear);
+      float f;
+      if (!far && !to_far) f = ex2_approx(rho - r);   // the difference of integers below 2^23 is exact
+      else f = m == -INFINITY ? 0.f : ex2_approx((m - to) * c) * scale(c) * (to_far ? 1.f : ex2_approx(fmaf(to, c, -r)));
       s.hi *= f;
       s.lo *= f;
       m = to;
-      rho = m * c;
-      far = !(fabsf(rho) < kNear);
+      rho = r;
+      far = to_far;
     }
   }
   // 2^((x - m) c), x <= m
@@ -676,7 +684,7 @@ __global__ void __launch_bounds__(kTlThreads, 4) top_row_kernel(const TopParams 
     }
     acc.raise(mc, c);
     {
-      // (with nothing but -inf so far rho is 0 and the terms are 0, or NaN)
+      // (with nothing but -inf so far the terms are 0, or NaN)
       float s0 = 0.f, s1 = 0.f;
       if (!acc.far) {
         const Pair cc = pair_of(c, c), rr = pair_of(-acc.rho, -acc.rho);

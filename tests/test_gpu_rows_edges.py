@@ -6,7 +6,8 @@ test_gpu_rows.py, or bit for bit against another form of the same call."""
 import pytest
 import torch
 
-from test_gpu_rows import DEV, DTYPES, _check_distill, _record, _student, distill_path, sv  # noqa: F401
+from test_gpu_rows import (DEV, DTYPES, _check_distill, _check_top, _record, _student, _top_rows, distill_path,  # noqa: F401
+                           sv, top_path)
 
 pytestmark = pytest.mark.gpu
 
@@ -40,3 +41,25 @@ def test_distill_tokens_listed_twice_in_wide_rows(sv, distill_path, form, k):
     idx, lp, t = _record(4, 3, 60000, k, True)
     idx[:, 1::2] = idx[:, 0::2]
     _check_distill(sv, S, idx, lp, t, 1.0, "f32", form=form)
+
+
+# ------------------------------------------------------------------ large common offsets
+
+@pytest.mark.parametrize("offset", [0.0, 100.0, 1e4, -1e4, 2e5, 3e6, -3e6, 5545177.0, -5545177.0, 6e6])
+@pytest.mark.parametrize("order", ["rising", "as_they_come", "falling"])
+@pytest.mark.parametrize("T, k", [(1.0, 3), (1.0, 300), (0.7, 20)])
+def test_top_rows_with_a_common_offset(sv, top_path, offset, order, T, k):
+    """The mass outside keeps its accuracy where every step of a row raises the
+    maximum, whatever the logits have in common (beyond 8e6 T / log2(e), about
+    5.5e6, terms are formed another way, and rows rise across that border)."""
+    x = _top_rows(11, 3, 60001, "f32")
+    if order != "as_they_come":
+        x = torch.sort(x, -1, descending=order == "falling").values
+    _check_top(sv, x + offset, k, T, "f32")
+
+
+@pytest.mark.parametrize("dtype, offset", [("bf16", 200.0), ("bf16", -3000.0), ("f16", 1000.0), ("f16", -200.0)])
+@pytest.mark.parametrize("order", ["rising", "falling"])
+def test_top_16_bit_rows_with_a_common_offset(sv, top_path, dtype, offset, order):
+    x = torch.sort(_top_rows(12, 3, 100003, "f32"), -1, descending=order == "falling").values
+    _check_top(sv, (x + offset).to(DTYPES[dtype]), 40, 0.8, dtype)
