@@ -95,10 +95,14 @@ __device__ __forceinline__ float distill_loss(F2 Z, F2 S, F2 st, F2 E1, F2 wt, f
   return f2_add(sum, f2_mul(two_diff(M, kr), inv_t)).hi;
 }
 
-// 2^(d (c + c_lo)), one correction step: the weight of a value that lies d
-// below its reference.
+// 2^(d (c + c_lo)), d <= 0: the weight of a value that lies d below its
+// reference.  One exponential, corrected to first order for the product's
+// rounding and for c_lo.
 __device__ __forceinline__ float weight_fast(float d, float c, float c_lo) {
-  return d * c < -150.f ? 0.f : q_weight(d, 0.f, c, c_lo);
+  const float p = d * c;
+  if (p < -150.f) return 0.f;   // also where the product leaves float32's range
+  const float y = ex2_approx(p), e = fmaf(d, c_lo, fmaf(d, c, -p));
+  return fmaf(y * 6.931471825e-01f, e, y);
 }
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }

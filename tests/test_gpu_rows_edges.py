@@ -63,3 +63,19 @@ def test_top_rows_with_a_common_offset(sv, top_path, offset, order, T, k):
 def test_top_16_bit_rows_with_a_common_offset(sv, top_path, dtype, offset, order):
     x = torch.sort(_top_rows(12, 3, 100003, "f32"), -1, descending=order == "falling").values
     _check_top(sv, (x + offset).to(DTYPES[dtype]), 40, 0.8, dtype)
+
+
+# ------------------------------------------------------------------ wide temperatures
+
+@pytest.mark.parametrize("T", [100.0, 1e3, 1e4, 1e6])
+@pytest.mark.parametrize("below", [0.5, 2.0, 10.0, 60.0])
+@pytest.mark.parametrize("form", ["fused", "autograd"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_distill_listed_tokens_far_below_at_high_temperatures(sv, distill_path, T, below, form, dtype):
+    """A listed logit far below the row's maximum still has weight where the
+    temperature is as large."""
+    S = (_student(7, 4, 2000, "f32") * T / 8).to(DTYPES[dtype])
+    idx, lp, t = _record(7, 4, 2000, 9, True)
+    idx[3, 5] = idx[3, 4]
+    S[torch.arange(4)[:, None], idx.long()] = (S.float().max() - below * T * (1 + torch.rand(4, 9))).to(DTYPES[dtype])
+    _check_distill(sv, S, idx, lp, t, T, dtype, form=form)
