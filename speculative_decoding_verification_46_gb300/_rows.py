@@ -19,13 +19,16 @@ SV_MAX_HISTORY = 1 << 23
 SV_MAX_BIAS = 1024
 SV_DISTILL_STAT_WORDS = 8
 
-_declared = False
+_declared = None   # the library object whose signatures are declared
 
 
 def _lib():
     global _declared
     lib = load_library()
-    if not _declared:
+    # Threads whose first calls meet may each have loaded an object of their
+    # own: what is declared is asked of the object at hand (a call without
+    # signatures would pass addresses as 32-bit integers).
+    if _declared is not lib:
         lib.sv_adjust_logits.argtypes = [_c_int, _c_int, _c_int, _c_ptr, _c_int, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_int,
                                          _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_int, _c_ptr, _c_int,
                                          _c_ptr, _c_ptr]
@@ -44,7 +47,7 @@ def _lib():
         lib.sv_distill_loss_grad.argtypes = [_c_int, _c_int, _c_ptr, _c_int, _c_ptr, _c_ptr, _c_ptr, _c_int, _c_float,
                                              _c_ptr, _c_ptr, _c_ptr, _c_ptr]
         lib.sv_distill_loss_grad.restype = _c_int
-        _declared = True
+        _declared = lib
     return lib
 
 
