@@ -45,17 +45,19 @@ int sm_count() {
   return n;
 }
 
-// Opt in to `smem` bytes of dynamic shared memory, once per kernel (`set`: a
-// static of the launch site), device and size.
-bool allow_smem(std::atomic<int> (&set)[64], const void* kern, size_t smem) {
+// Opt in to `most` bytes of dynamic shared memory, the most that any launch of
+// the kernel asks for, once per kernel (`set`: a static of the launch site)
+// and device.  One size for all calls: threads that come here together set the
+// same limit, and none lowers another's between its opt-in and its launch.
+bool allow_smem(std::atomic<bool> (&set)[64], const void* kern, size_t most) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
-  if (set[dev].load(std::memory_order_acquire) >= (int)smem) return true;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
+  if (set[dev].load(std::memory_order_acquire)) return true;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) != cudaSuccess) {
     cudaGetLastError();
     return false;
   }
-  set[dev].store((int)smem, std::memory_order_release);
+  set[dev].store(true, std::memory_order_release);
   return true;
 }
 
@@ -88,6 +90,15 @@ void choose_tile(sv::rows::AdjustParams& p, int elem) {
   p.tiles = (int)ceil_div(p.V, p.tile);
 }
 
+// Dynamic shared memory of an adjust kernel: the listed tokens' part and, where
+// rows pass through shared memory, the stages.
+template <typename T>
+size_t adjust_smem(int tile, int NB, bool sparse, bool staged) {
+  size_t smem = sparse ? (size_t)tile * 6 + (size_t)NB * 8 : 0;
+  if (staged) smem += (size_t)sv::rows::kAdStages * (tile / sv::Tr<T>::VW + 1) * 16;
+  return smem;
+}
+
 template <typename T>
 sv_status launch_adjust(sv::rows::AdjustParams p, cudaStream_t stream) {
   choose_tile(p, (int)sizeof(T));
@@ -97,11 +108,12 @@ sv_status launch_adjust(sv::rows::AdjustParams p, cudaStream_t stream) {
   const bool whole = p.V % sv::Tr<T>::VW == 0;
   auto kern = staged ? whole ? sv::rows::adjust_staged_kernel<T, true> : sv::rows::adjust_staged_kernel<T, false>
               : whole ? sv::rows::adjust_direct_kernel<T, true> : sv::rows::adjust_direct_kernel<T, false>;
-  size_t smem = sparse ? (size_t)p.tile * 6 + (size_t)p.NB * 8 : 0;
-  if (staged) smem += (size_t)sv::rows::kAdStages * (p.tile / sv::Tr<T>::VW + 1) * 16;
+  const size_t smem = adjust_smem<T>(p.tile, p.NB, sparse, staged);
   // (the kernel's static shared memory counts toward the 48 KB that need no opt-in)
-  static std::atomic<int> set[4][64];
-  if (smem > 32 * 1024 && !allow_smem(set[2 * staged + whole], (const void*)kern, smem)) return SV_ERR_CUDA;
+  static std::atomic<bool> set[4][64];
+  if (smem > 32 * 1024 && !allow_smem(set[2 * staged + whole], (const void*)kern,
+                                      adjust_smem<T>(sv::rows::kAdTileBytes / (int)sizeof(T), SV_MAX_BIAS, true, staged)))
+    return SV_ERR_CUDA;
   kern<<<(unsigned)grid, sv::rows::kAdThreads, smem, stream>>>(p);
   return launched();
 }
@@ -157,11 +169,13 @@ sv_status launch_top_u(const sv::rows::TopParams& p, cudaStream_t stream) {
 template <typename T>
 sv_status launch_top_rows(const sv::rows::TopParams& p, cudaStream_t stream) {
   auto kern = p.V % sv::Tr<T>::VW == 0 ? sv::rows::top_row_kernel<T, true> : sv::rows::top_row_kernel<T, false>;
-  const size_t smem = (size_t)sv::rows::kTrStages * sv::rows::kTrStep * sizeof(uint4) +
-                      (size_t)sv::rows::tr_capacity(p.k) * sizeof(unsigned long long);
-  static std::atomic<int> set[2][64];
-  if (!allow_smem(set[p.V % sv::Tr<T>::VW == 0], (const void*)kern, smem)) return SV_ERR_CUDA;
-  kern<<<(unsigned)p.R, sv::rows::kTlThreads, smem, stream>>>(p);
+  const auto smem = [](int k) {
+    return (size_t)sv::rows::kTrStages * sv::rows::kTrStep * sizeof(uint4) +
+           (size_t)sv::rows::tr_capacity(k) * sizeof(unsigned long long);
+  };
+  static std::atomic<bool> set[2][64];
+  if (!allow_smem(set[p.V % sv::Tr<T>::VW == 0], (const void*)kern, smem(SV_MAX_TOP_K))) return SV_ERR_CUDA;
+  kern<<<(unsigned)p.R, sv::rows::kTlThreads, smem(p.k), stream>>>(p);
   return launched();
 }
 
@@ -209,7 +223,7 @@ sv_status launch_distill_pipe(sv::rows::DistillParams p, cudaStream_t stream) {
   p.SV = (int)ceil_div(nv, C);
   auto kern = p.V % VW == 0 ? sv::rows::distill_pipe_kernel<T, GRAD, true> : sv::rows::distill_pipe_kernel<T, GRAD, false>;
   const size_t smem = sizeof(sv::rows::DpSmem<T>);
-  static std::atomic<int> set[2][64];
+  static std::atomic<bool> set[2][64];
   if (!allow_smem(set[p.V % VW == 0], (const void*)kern, smem)) return SV_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)p.C);

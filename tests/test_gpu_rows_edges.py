@@ -3,6 +3,10 @@ other CTAs, long common offsets, wide temperatures, threads, streams and waits
 that give up.  Against the float64 oracle with the tolerances of
 test_gpu_rows.py, or bit for bit against another form of the same call."""
 
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -79,3 +83,71 @@ def test_distill_listed_tokens_far_below_at_high_temperatures(sv, distill_path, 
     idx[3, 5] = idx[3, 4]
     S[torch.arange(4)[:, None], idx.long()] = (S.float().max() - below * T * (1 + torch.rand(4, 9))).to(DTYPES[dtype])
     _check_distill(sv, S, idx, lp, t, T, dtype, form=form)
+
+
+# ------------------------------------------------------------------ threads
+
+_HARNESS = """
+#include <atomic>
+#include <cstdint>
+#include <thread>
+#include <vector>
+typedef int (*adjust_fn)(int, int, int, const void*, int, void*, const int32_t*, const int32_t*, const int32_t*, int, const int32_t*,
+                         const int32_t*, const float*, const float*, const float*, const int32_t*, const float*, int, const uint32_t*,
+                         int, const int32_t*, void*);
+// n threads, each on its own stream and output; at every step they start together
+extern "C" int refused(adjust_fn call, int n, int B, int V, int dtype, const void* x, void** out, const int32_t* tokens,
+                       const float* values, void** stream) {
+  std::atomic<int> here{0}, bad{0};
+  std::vector<std::thread> threads;
+  for (int i = 0; i < n; ++i)
+    threads.emplace_back([&, i] {
+      for (int step = 0; step < 1024 / n; ++step) {
+        here.fetch_add(1);
+        while (here.load() < n * (step + 1)) {}
+        if (call(B, 0, V, x, dtype, out[i], 0, 0, 0, 0, 0, 0, 0, 0, 0, tokens, values, step * n + n - i, 0, 0, 0, stream[i]) != 0) ++bad;
+      }
+    });
+  for (auto& t : threads) t.join();
+  return bad;
+}
+"""
+
+_THREADS = """
+import ctypes, sys
+sys.path.insert(0, {root!r})
+import torch
+import speculative_decoding_verification_46_gb300 as sv
+
+# many sequences of one full tile each, and lists that grow from call to call: every call needs more shared memory
+# than all steps before, a little more or less than those beside it
+B, V, n = 512, 6144, 8
+x = torch.zeros(B, 1, V, dtype=torch.{dtype}, device="cuda")
+outs = [torch.empty_like(x) for _ in range(n)]
+streams = [torch.cuda.Stream() for _ in range(n)]
+tokens, values = torch.full((B * 1024,), -1, dtype=torch.int32, device="cuda"), torch.zeros(B * 1024, device="cuda")
+torch.cuda.synchronize()
+call = ctypes.cast(sv._rows._lib().sv_adjust_logits, ctypes.c_void_p)
+many = lambda values: (ctypes.c_void_p * n)(*values)
+refused = ctypes.CDLL({harness!r}).refused
+refused.argtypes = [ctypes.c_void_p] + [ctypes.c_int] * 4 + [ctypes.c_void_p] * 5
+print(refused(call, n, B, V, sv._rows._TORCH_DTYPE[x.dtype], x.data_ptr(), many(o.data_ptr() for o in outs), tokens.data_ptr(),
+              values.data_ptr(), many(s.cuda_stream for s in streams)))
+torch.cuda.synchronize()
+assert all(torch.equal(o, x) for o in outs)
+"""
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16", "float32"])
+def test_calls_of_many_threads_that_need_more_and_more_shared_memory(sv, tmp_path, dtype):
+    """Threads whose calls need different amounts of shared memory, more than
+    any call before: none takes another's away (in a process of its own, where
+    no earlier call has asked for the most)."""
+    (tmp_path / "harness.cpp").write_text(_HARNESS)
+    harness = str(tmp_path / "harness.so")
+    subprocess.run(["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-pthread", "-o", harness, str(tmp_path / "harness.cpp")], check=True)
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    out = subprocess.run([sys.executable, "-c", _THREADS.format(root=root, dtype=dtype, harness=harness)], capture_output=True, text=True,
+                         timeout=240)
+    assert out.returncode == 0, out.stderr
+    assert int(out.stdout) == 0, f"{out.stdout.strip()} of 1024 calls were refused"
