@@ -107,6 +107,16 @@ def _need_rows(name, t):
         raise ValueError(f"unsupported {name} dtype {t.dtype}")
 
 
+def _need_constants(names, *tensors):
+    """Nobody asks for a gradient that goes through these (or None): none is formed."""
+    forward, wanted = forward_ad._current_level >= 0, torch.is_grad_enabled()
+    if not (forward or wanted):
+        return
+    for i, t in enumerate(tensors):
+        if t is not None and ((t.requires_grad and wanted) or (forward and forward_ad.unpack_dual(t).tangent is not None)):
+            raise ValueError(f"no gradient is formed for {names.split()[i]}: detach it")
+
+
 class _Here:
     """The device is current already: nothing to enter or leave."""
 
@@ -160,8 +170,11 @@ def adjust_logits(logits, *, draft=None, history=None, history_len=None, prompt_
     gamma_b [B] int32: a ragged round, the rows behind a sequence's last are
     not touched.  All contiguous CUDA tensors on one device; what is None is
     off.  out: where to write (logits itself: in place); by default a new
-    tensor, whose untouched rows hold zeros.  Returns out.
+    tensor, whose untouched rows hold zeros.  Returns out.  No gradient is
+    formed: outside torch.no_grad() tensors that require one are refused.
     """
+    _need_constants("logits repetition frequency presence bias_values out", logits, repetition, frequency, presence,
+                    bias_values, out)
     if logits.dim() != 3:
         raise ValueError(f"logits must be [B, gamma+1, V], got {tuple(logits.shape)}")
     B, G1, V = logits.shape
@@ -236,8 +249,11 @@ def top_logits(logits, k, temperature=1.0, *, workspace=None, stream=None, outpu
     log-probabilities under softmax(logits / temperature), and the log of the
     mass outside them.  A row of fewer than k tokens above -inf is padded with
     index -1.  workspace: from alloc_top_logits_workspace, kept by the caller
-    (one per concurrent call).
+    (one per concurrent call).  outputs: (indices, logprobs, tail) to write
+    into.  No gradient is formed: outside torch.no_grad() tensors that require
+    one are refused.
     """
+    _need_constants("logits indices logprobs tail", logits, *(outputs or ()))
     _need_rows("logits", logits)
     if logits.dim() < 1:
         raise ValueError("logits must be [..., V]")
@@ -276,6 +292,7 @@ def top_logits(logits, k, temperature=1.0, *, workspace=None, stream=None, outpu
 
 
 def _check_distill(student, indices, logprobs, tail, weight):
+    _need_constants("logprobs tail weight", logprobs, tail, weight)
     _need_rows("student", student)
     if student.dim() < 1 or indices.dim() < 1:
         raise ValueError("student must be [..., V] and indices [..., k]")
@@ -285,10 +302,6 @@ def _check_distill(student, indices, logprobs, tail, weight):
     _need("logprobs", logprobs, torch.float32, lead + (k,), dev)
     _need("tail", tail, torch.float32, lead, dev)
     _need("weight", weight, torch.float32, lead, dev)
-    if torch.is_grad_enabled():
-        for name, t in (("logprobs", logprobs), ("tail", tail), ("weight", weight)):
-            if t is not None and t.requires_grad:
-                raise ValueError(f"no gradient is formed for {name}: detach it")
     V = student.shape[-1]
     return student.numel() // max(V, 1), V, k
 
@@ -366,6 +379,10 @@ def distill_loss_grad(student, indices, logprobs, tail=None, temperature=1.0, *,
     autograd, so it can be captured into a CUDA graph whatever autograd graphs
     are alive.
     """
+    _need_constants("out_grad", out_grad)
+    if forward_ad._current_level >= 0:
+        with torch.no_grad():                # a tangent would be dropped; backward mode is documented above
+            _need_constants("student", student)
     R, V, k = _check_distill(student, indices, logprobs, tail, weight)
     dev = student.device
     _need("out_grad", out_grad, student.dtype, student.shape, dev)
