@@ -146,7 +146,10 @@ sv_status sv_top_logits(int R, int V, const void* logits, sv_dtype dtype, int k,
  *
  * A row with no usable entry and no tail has loss 0 and gradient 0.  A student
  * row that holds NaN or +inf, or only -inf, or a teacher row that holds NaN,
- * gives NaN.  No workspace.
+ * gives NaN.  Warps that wait for one another do so for a second or so at most,
+ * where a row takes microseconds; if a wait runs out nevertheless, losses,
+ * statistics and gradients of all rows that it may concern are NaN throughout.
+ * No workspace.
  */
 #define SV_DISTILL_STAT_WORDS 8
 sv_status sv_distill_forward(int R, int V, const void* student, sv_dtype dtype, const int32_t* indices,

@@ -54,6 +54,7 @@ struct DistillParams {
   const float* weight;
   const float* grad_loss;            // backward
   int up_stride;                     // 0: grad_loss is one value
+  int stop;                          // persistent form: the cluster's row at which it gives up (tests; -1: none)
   float* loss;
   float* stats;                      // [R][8]: mt, A, teacher maximum, 1 / Z, M, 1 / S, listed twice, usable
   void* grad;

@@ -27,9 +27,11 @@
 // has a whole row's streaming time to finish in.  The forward pass alone is
 // the same without the gradient.
 //
-// Every wait is bounded: a role that gives up leaves its loop, the others
-// follow as their own waits run out, and the losses not yet written become
-// NaN.
+// Every wait is bounded.  A role that gives up notes it in every CTA of the
+// cluster and leaves its loop, the others follow as their own waits run out,
+// and when all have left, losses, statistics and gradients of all the
+// cluster's rows are overwritten with NaN: what was finished in time cannot be
+// told from what was not.
 //
 // Bound: HBM, with instruction issue close behind (loss and gradient: 4096 rows
 // of 128256 bf16, k = 64, a tenth of weight 0: 344 us, 5.8 TB/s, 0.85 of the
@@ -96,7 +98,9 @@ struct DpSmem {
   unsigned long long written[4];        // streaming warps -> list: row t's dense gradient
   unsigned long long parts[kDpParts];   // parts warps of all CTAs -> statistics
   unsigned long long done[kDpLists];    // statistics -> list: row t's loss is written, its list may be reused
+  uint32_t gave_up;                     // a wait somewhere in the cluster ran out
 };
+static_assert(sizeof(DpSmem<float>) <= 227 * 1024 && sizeof(DpSmem<__half>) <= 227 * 1024, "a CTA's shared memory");
 
 // The meeting point of a list group (all of its warps wait, so a named
 // barrier); returns whether all of them say yes.
@@ -117,9 +121,11 @@ __device__ __forceinline__ void mb_arrive(unsigned long long* b) {
   if ((threadIdx.x & 31) == 0)
     asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_addr(b)) : "memory");
 }
-// Wait for phase `phase` (0, 1, ...) of the barrier, all lanes; false: given up
-// (after 20 ms at least; a row takes microseconds).
-constexpr int kDpPatience = 1 << 20;
+// Wait for phase `phase` (0, 1, ...) of the barrier, all lanes; false: given
+// up after about a second (a try that finds nothing lasts 3.9 us; a row takes
+// microseconds).  The limit is a constant: read from the parameters it cost
+// the fused call 1% (351 us against 347, 4096 rows of 128256 bf16, k 64).
+constexpr int kDpPatience = 1 << 18;
 template <bool CLUSTER = false>
 __device__ __forceinline__ bool mb_wait(unsigned long long* b, int phase) {
   const uint32_t a = smem_addr(b), parity = phase & 1;
@@ -134,6 +140,17 @@ __device__ __forceinline__ bool mb_wait(unsigned long long* b, int phase) {
                    : "=r"(done) : "r"(a), "r"(parity) : "memory");
   }
   return __all_sync(0xffffffffu, done != 0u);
+}
+// A warp gives up: every CTA of the cluster will know (they all stay until the
+// last barrier of the kernel).
+__device__ __forceinline__ void dp_give_up(uint32_t* flag, int C) {
+  const int lane = threadIdx.x & 31;
+  if (lane < C) {
+    uint32_t d;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(d) : "r"(smem_addr(flag)), "r"(lane));
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(d), "r"(1u) : "memory");
+  }
+  __syncwarp();
 }
 // Arrive at the barrier that `b` is in CTA `rank` of the cluster, after this
 // thread's writes to that CTA's shared memory.
@@ -203,6 +220,27 @@ __device__ __forceinline__ void dp_loss(const DpList& L, const DpStat& s, F2 inv
   if ((threadIdx.x & 31) == 0) *loss = l;
 }
 
+// A wait of the cluster ran out: NaN for all of its rows (their order and
+// division among the CTAs as in the kernel).
+template <typename T, bool GRAD>
+__device__ __noinline__ void dp_mark(void* grad, float* loss, float* stats, int V, int SV, int g, int NG, int n, int rank) {
+  const float nan = __uint_as_float(0x7fffffffu);
+  float x[Tr<T>::VW];
+#pragma unroll
+  for (int e = 0; e < Tr<T>::VW; ++e) x[e] = nan;
+  const uint4 nans = Elem<T>::pack(x);
+  for (int t = 0; t < n; ++t) {
+    const int r = g + t * NG;
+    if (GRAD) {
+      const Window<T> gwin(static_cast<T*>(grad), (size_t)r, V);
+      const int nv = gwin.vectors(), v0 = min(rank * SV, nv), v1 = min(v0 + SV, nv);
+      for (int v = v0 + (int)threadIdx.x; v < v1; v += (int)blockDim.x) gwin.store(v, nans);
+    }
+    if (rank == 0 && threadIdx.x == 0) loss[r] = nan;
+    if (!GRAD && rank == 0 && stats && threadIdx.x < 8) stats[(size_t)r * 8 + threadIdx.x] = nan;
+  }
+}
+
 // WHOLE: V is a multiple of the vector width, so every row is whole vectors.
 template <typename T, bool GRAD, bool WHOLE>
 __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const DistillParams p) {
@@ -228,6 +266,7 @@ __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const Di
 
   for (int i = threadIdx.x; i < 128; i += blockDim.x) sm.tab[i] = i < 64 ? __ldg(kExp2Hi + i) : __ldg(kExp2Lo + i - 64);
   if (threadIdx.x == 0) {
+    sm.gave_up = 0u;
     for (int i = 0; i < 4; ++i) {
       mb_init(&sm.summed[i], kDpStWarps);
       mb_init(&sm.known[i], 1);
@@ -298,7 +337,7 @@ __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const Di
       if (t < n) {
         // ---- row t without its listed tokens
         asm volatile("cp.async.wait_group %0;" ::"n"(GRAD ? 1 : 2) : "memory");
-        if (!mb_wait(&sm.listed[t & 3], t >> 2)) break;
+        if (!mb_wait(&sm.listed[t & 3], t >> 2)) { dp_give_up(&sm.gave_up, C); break; }
         if (sm.list[t % kDpLists].live != 0) {
           const uint4* st = &sm.ring[t % kDpStages][tid];
           int m_t = mine;
@@ -371,11 +410,11 @@ __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const Di
       }
       if (!GRAD) {
         // the ring of the warps' parts holds four rows
-        if (t >= 3 && !mb_wait(&sm.known[(t - 3) & 3], (t - 3) >> 2)) break;
+        if (t >= 3 && !mb_wait(&sm.known[(t - 3) & 3], (t - 3) >> 2)) { dp_give_up(&sm.gave_up, C); break; }
       } else if (t >= 1) {
         // ---- row t - 1's gradient
         const int i = t - 1;
-        if (!mb_wait(&sm.known[i & 3], i >> 2)) break;
+        if (!mb_wait(&sm.known[i & 3], i >> 2)) { dp_give_up(&sm.gave_up, C); break; }
         {
           const int r = g + i * NG;
           const DpList& L = sm.list[i % kDpLists];
@@ -425,9 +464,11 @@ __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const Di
     asm volatile("cp.async.wait_group 0;" ::: "memory");
   } else if (role == 0) {
     // ================================================================ parts
+    const int last = rank == 0 ? (int)min((unsigned)n, (unsigned)p.stop) : n;   // n for -1
 #pragma unroll 1
-    for (int t = 0; t < n; ++t) {
-      if (!mb_wait(&sm.summed[t & 3], t >> 2)) break;  // (which follows row t's list)
+    for (int t = 0; t < last; ++t) {
+      // (a summed row's list stands too)
+      if (!mb_wait(&sm.summed[t & 3], t >> 2)) { dp_give_up(&sm.gave_up, C); break; }
       const DpList& L = sm.list[t % kDpLists];
       if (L.live != 0) {
         const float2 v = lane < kDpStWarps ? sm.wpart[t & 3][lane] : make_float2(-INFINITY, 0.f);
@@ -442,13 +483,13 @@ __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const Di
       if (lane < C) mb_arrive_remote(&sm.parts[t % kDpParts], lane);
       __syncwarp();
     }
+    if (last < n) dp_give_up(&sm.gave_up, C);
   } else if (role == 2) {
     // ================================================================ statistics
     const F2 inv_t = f2_from(p.inv_t);
-    int t = 0;
 #pragma unroll 1
-    for (; t < n; ++t) {
-      if (!mb_wait<true>(&sm.parts[t % kDpParts], t / kDpParts)) break;
+    for (int t = 0; t < n; ++t) {
+      if (!mb_wait<true>(&sm.parts[t % kDpParts], t / kDpParts)) { dp_give_up(&sm.gave_up, C); break; }
       const DpList& L = sm.list[t % kDpLists];
       DpStat& s = sm.stat[t % kDpLists];
       dp_statistics(sm.part[t % kDpParts], C, L, k, c, sm.tab, s,
@@ -457,8 +498,6 @@ __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const Di
       if (t % C == rank) dp_loss(L, s, inv_t, sm.tab, p.loss + g + t * NG);
       mb_arrive(&sm.done[t % kDpLists]);
     }
-    for (; t < n; ++t)                              // given up
-      if (t % C == rank && lane == 0) p.loss[g + t * NG] = __uint_as_float(0x7fffffffu);
   } else {
     // ================================================================ list
     const int group = threadIdx.x - 32 >= nl;       // rows of this parity
@@ -507,8 +546,8 @@ __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const Di
       if (j < n) {
         // ---- the list of row j
         // (the bitmap was row j - 3's, the list row j - kDpLists's)
-        if (j >= 3) ok &= mb_wait(&sm.summed[(j - 3) & 3], (j - 3) >> 2);
-        if (j >= kDpLists) ok &= mb_wait(&sm.done[j % kDpLists], j / kDpLists - 1);
+        if (j >= 3) ok = ok && mb_wait(&sm.summed[(j - 3) & 3], (j - 3) >> 2);
+        if (j >= kDpLists) ok = ok && mb_wait(&sm.done[j % kDpLists], j / kDpLists - 1);
         DpList& L = sm.list[j % kDpLists];
         // a NaN makes the maximum +inf, and the row NaN
         float tm = -INFINITY, km = -INFINITY;
@@ -632,9 +671,11 @@ __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const Di
         }
       }
     }
+    if (!ok) dp_give_up(&sm.gave_up, C);            // (a group that leaves together has one that knows why)
   }
   cluster_arrive();
   cluster_wait();                                   // nobody leaves while its shared memory may be written
+  if (sm.gave_up != 0u) dp_mark<T, GRAD>(p.grad, p.loss, p.stats, p.V, p.SV, g, NG, n, rank);
 }
 
 }  // namespace rows

@@ -211,6 +211,20 @@ sv_status launch_distill_u(sv::rows::DistillParams p, cudaStream_t stream) {
   return launched();
 }
 
+// SPECVERIFY_PATH=distillrow takes a cluster per row everywhere (tests cover both).
+int distill_override() {
+  const char* e = std::getenv("SPECVERIFY_PATH");
+  return e && std::strcmp(e, "distillrow") == 0 ? 2 : 0;
+}
+
+// SPECVERIFY_PATH=distillstopN: in the persistent form, one warp of each
+// cluster leaves at the cluster's row N, so that the other warps' waits run out
+// (tests see what is left then).
+int distill_stop() {
+  const char* e = std::getenv("SPECVERIFY_PATH");
+  return e && std::strncmp(e, "distillstop", 11) == 0 ? std::atoi(e + 11) : -1;
+}
+
 // The persistent form (sv_distill_pipe.cuh): as many clusters as fit at once.
 // Returns SV_ERR_UNSUPPORTED where it does not apply.
 template <typename T, bool GRAD>
@@ -221,6 +235,7 @@ sv_status launch_distill_pipe(sv::rows::DistillParams p, cudaStream_t stream) {
   if (C > sv::rows::kDiMaxC || p.k > sv::rows::kDpMaxK) return SV_ERR_UNSUPPORTED;
   p.C = (int)C;
   p.SV = (int)ceil_div(nv, C);
+  p.stop = distill_stop();
   auto kern = p.V % VW == 0 ? sv::rows::distill_pipe_kernel<T, GRAD, true> : sv::rows::distill_pipe_kernel<T, GRAD, false>;
   const size_t smem = sizeof(sv::rows::DpSmem<T>);
   static std::atomic<bool> set[2][64];
@@ -253,12 +268,6 @@ sv_status launch_distill_pipe(sv::rows::DistillParams p, cudaStream_t stream) {
     return SV_ERR_CUDA;
   }
   return launched();
-}
-
-// SPECVERIFY_PATH=distillrow takes a cluster per row everywhere (tests cover both).
-int distill_override() {
-  const char* e = std::getenv("SPECVERIFY_PATH");
-  return e && std::strcmp(e, "distillrow") == 0 ? 2 : 0;
 }
 
 // The persistent form wherever it applies: with few rows it is as fast as a

@@ -10,8 +10,8 @@ import sys
 import pytest
 import torch
 
-from test_gpu_rows import (DEV, DTYPES, _check_distill, _check_top, _record, _student, _top_rows, distill_path,  # noqa: F401
-                           sv, top_path)
+from test_gpu_rows import (DEV, DTYPES, _check_distill, _check_top, _forms, _record, _student, _top_rows,  # noqa: F401
+                           distill_path, sv, top_path)
 
 pytestmark = pytest.mark.gpu
 
@@ -151,3 +151,32 @@ def test_calls_of_many_threads_that_need_more_and_more_shared_memory(sv, tmp_pat
                          timeout=240)
     assert out.returncode == 0, out.stderr
     assert int(out.stdout) == 0, f"{out.stdout.strip()} of 1024 calls were refused"
+
+
+# ------------------------------------------------------------------ waits that run out
+
+@pytest.mark.parametrize("R, V, dtype, k, stop", [(300, 70000, "f32", 33, 2), (400, 40001, "bf16", 8, 5), (400, 40001, "bf16", 8, 0),
+                                                  (160, 152064, "f16", 200, 4), (3, 900, "f32", 5, 0), (300, 70000, "f32", 33, 1000)])
+@pytest.mark.parametrize("form", ["fused", "inplace", "autograd"])
+def test_rows_of_a_pipeline_that_gives_up_are_nan_throughout(sv, monkeypatch, R, V, dtype, k, stop, form):
+    """One warp of each cluster leaves at the cluster's row `stop` and the
+    waits of the others run out: a row is what it always is, or NaN in its loss
+    and all of its gradient, never a part of either; and the next call is as
+    usual."""
+    S = torch.randn(R, V, generator=torch.Generator(device=DEV).manual_seed(1), device=DEV).mul_(2.5).to(DTYPES[dtype])
+    idx, lp, t = _record(R, R, V, k, True)
+    idx[1::7, -1] = idx[1::7, 0]
+    w = torch.rand(R, generator=torch.Generator().manual_seed(2)) + 0.1
+    w[2::5] = 0.0
+    want = _forms(sv, S, idx, lp, t, 1.1, w, form)
+    monkeypatch.setenv("SPECVERIFY_PATH", f"distillstop{stop}")
+    loss, grad = _forms(sv, S, idx, lp, t, 1.1, w, form)
+    lost = loss.isnan()
+    assert torch.equal(loss[~lost], want[0][~lost]) and torch.equal(grad[~lost], want[1][~lost])
+    assert int(lost.sum()) == R if stop == 0 else not lost.any() if stop == 1000 else 0 < int(lost.sum())
+    if form == "autograd":
+        lost &= (w != 0).to(DEV)                              # the backward pass asks the weight first
+    assert grad[lost].isnan().all()
+    monkeypatch.delenv("SPECVERIFY_PATH")
+    again = _forms(sv, S, idx, lp, t, 1.1, w, form)
+    assert torch.equal(again[0], want[0]) and torch.equal(again[1], want[1])
