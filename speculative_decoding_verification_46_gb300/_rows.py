@@ -132,7 +132,8 @@ _HERE = _Here()
 
 def _on(device, stream):
     """A context for `stream` (or the device's current stream) with the rows'
-    device current; what is allocated inside belongs to that stream."""
+    device current; what is allocated inside belongs to that stream.  The
+    caller orders `stream` behind what makes the inputs."""
     if stream is not None:
         if stream.device != device:
             raise ValueError(f"stream is on {stream.device}, the rows on {device}")
@@ -140,6 +141,15 @@ def _on(device, stream):
     if torch.cuda.current_device() != device.index:
         return torch.cuda.device(device)
     return _HERE
+
+
+def _read_on(stream, *tensors):
+    """The caller may drop these (or None) as soon as the call returns: their
+    memory is not handed out again before `stream` has come to this point."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
 
 
 def _written(t):
@@ -172,6 +182,8 @@ def adjust_logits(logits, *, draft=None, history=None, history_len=None, prompt_
     off.  out: where to write (logits itself: in place); by default a new
     tensor, whose untouched rows hold zeros.  Returns out.  No gradient is
     formed: outside torch.no_grad() tensors that require one are refused.
+    stream: where to run, by default the device's current stream; the caller
+    orders it behind what makes the inputs, and may drop them after the call.
     """
     _need_constants("logits repetition frequency presence bias_values out", logits, repetition, frequency, presence,
                     bias_values, out)
@@ -212,6 +224,8 @@ def adjust_logits(logits, *, draft=None, history=None, history_len=None, prompt_
     table = _addr(mask_index) if mask_index is not None and M == 0 else _addr(mask)
     given = out
     with _on(dev, stream):
+        _read_on(stream, logits, draft, history, history_len, prompt_len, repetition, frequency, presence, bias_tokens,
+                 bias_values, mask, mask_index, gamma_b, out)
         if out is None:
             out = torch.zeros_like(logits) if gamma_b is not None else torch.empty_like(logits)
         st = sv_adjust_logits(B, G1 - 1, V, _addr(logits), _TORCH_DTYPE[logits.dtype], _addr(out), _addr(draft),
@@ -251,7 +265,7 @@ def top_logits(logits, k, temperature=1.0, *, workspace=None, stream=None, outpu
     index -1.  workspace: from alloc_top_logits_workspace, kept by the caller
     (one per concurrent call).  outputs: (indices, logprobs, tail) to write
     into.  No gradient is formed: outside torch.no_grad() tensors that require
-    one are refused.
+    one are refused.  stream: as in adjust_logits.
     """
     _need_constants("logits indices logprobs tail", logits, *(outputs or ()))
     _need_rows("logits", logits)
@@ -272,6 +286,7 @@ def top_logits(logits, k, temperature=1.0, *, workspace=None, stream=None, outpu
         raise ValueError(f"k must be in 1..1024, got {k}")
     given = outputs
     with _on(dev, stream):
+        _read_on(stream, logits, workspace, *(outputs or ()))
         if outputs is None:
             outputs = (torch.empty(lead + (k,), dtype=torch.int32, device=dev),
                        torch.empty(lead + (k,), dtype=torch.float32, device=dev),
@@ -377,7 +392,7 @@ def distill_loss_grad(student, indices, logprobs, tail=None, temperature=1.0, *,
     with respect to student).  out_grad: where the gradient goes (student
     itself: in place).  Arguments as distill_loss; nothing is recorded for
     autograd, so it can be captured into a CUDA graph whatever autograd graphs
-    are alive.
+    are alive.  stream: as in adjust_logits.
     """
     _need_constants("out_grad", out_grad)
     if forward_ad._current_level >= 0:
@@ -387,6 +402,7 @@ def distill_loss_grad(student, indices, logprobs, tail=None, temperature=1.0, *,
     dev = student.device
     _need("out_grad", out_grad, student.dtype, student.shape, dev)
     with _on(dev, stream):
+        _read_on(stream, student, indices, logprobs, tail, weight, out_grad)
         loss = torch.empty(student.shape[:-1], dtype=torch.float32, device=dev)
         grad = torch.empty_like(student, requires_grad=False) if out_grad is None else out_grad
         st = sv_distill_loss_grad(R, V, _addr(student), _TORCH_DTYPE[student.dtype], _addr(indices), _addr(logprobs),

@@ -180,3 +180,38 @@ def test_rows_of_a_pipeline_that_gives_up_are_nan_throughout(sv, monkeypatch, R,
     monkeypatch.delenv("SPECVERIFY_PATH")
     again = _forms(sv, S, idx, lp, t, 1.1, w, form)
     assert torch.equal(again[0], want[0]) and torch.equal(again[1], want[1])
+
+
+# ------------------------------------------------------------------ streams
+
+def test_inputs_may_be_dropped_after_a_call_on_another_stream(sv):
+    """Memory of inputs that the caller lets go of is not handed out again
+    while the given stream has yet to read it."""
+    R, V, k = 48, 50000, 9
+    g = torch.Generator(device=DEV).manual_seed(3)
+    made = dict(logits=torch.randn(R, 1, V, generator=g, device=DEV),
+                history=torch.randint(0, V, (R, 3000), generator=g, device=DEV, dtype=torch.int32),
+                history_len=torch.full((R,), 3000, device=DEV, dtype=torch.int32), presence=torch.rand(R, generator=g, device=DEV),
+                bias_tokens=torch.randint(0, V, (R, 500), generator=g, device=DEV, dtype=torch.int32),
+                bias_values=torch.randn(R, 500, generator=g, device=DEV),
+                mask=torch.randint(-2 ** 31, 2 ** 31, (R, (V + 31) // 32), generator=g, device=DEV).to(torch.int32))
+    idx, lp, t = (x.to(DEV) for x in _record(2, R, V, k, True))
+    record = dict(indices=idx, logprobs=lp, tail=t, weight=torch.rand(R, generator=g, device=DEV))
+    calls = [lambda a, **kw: [sv.adjust_logits(**a, **kw)], lambda a, **kw: list(sv.top_logits(a["logits"], k, **kw)),
+             lambda a, **kw: list(sv.distill_loss_grad(a["logits"].view(R, V), **{n: a[n] for n in record}, **kw))]
+    for call, names in zip(calls, (made, ["logits"], ["logits", *record])):
+        inputs = {n: made[n] if n in made else record[n] for n in names}
+        want = call(dict(inputs))
+        torch.cuda.synchronize()
+        side = torch.cuda.Stream()
+        copies = {n: x.clone() for n, x in inputs.items()}
+        sizes = [(x.shape, x.dtype) for x in copies.values()]
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(100_000_000)
+        got = call(copies, stream=side)
+        copies.clear()
+        for _ in range(3):                                    # what is allocated now must not be what they were
+            [torch.zeros(shape, dtype=dtype, device=DEV) for shape, dtype in sizes]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
