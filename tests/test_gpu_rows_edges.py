@@ -215,3 +215,60 @@ def test_inputs_may_be_dropped_after_a_call_on_another_stream(sv):
             [torch.zeros(shape, dtype=dtype, device=DEV) for shape, dtype in sizes]
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+# ------------------------------------------------------------------ more than 2^31 elements
+
+@pytest.mark.parametrize("V", [128256, 128003])
+def test_rows_beyond_32_bit_offsets(sv, V):
+    """The last rows of a tensor of more than 2^31 elements are what they are
+    in a tensor of their own (from a row on that starts at the same place of a
+    16-byte vector), in every operator."""
+    R, n, k = 17000, 200, 20
+    assert R * V > 2 ** 31 and (R - n) * V % 8 == 0
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB")
+    g = torch.Generator(device=DEV).manual_seed(5)
+    x = torch.empty(R, V, dtype=torch.bfloat16, device=DEV)
+    for r in range(0, R, 1000):
+        x[r:r + 1000] = torch.randn(1000, V, generator=g, device=DEV) * 2.5
+    last = x[R - n:].clone()
+    h = torch.randint(0, V, (R, 100), generator=g, device=DEV, dtype=torch.int32)
+    lens, pen = torch.full((R,), 100, device=DEV, dtype=torch.int32), torch.rand(R, generator=g, device=DEV) + 0.5
+    at = slice(R - n, None)
+
+    def adjust(rows, part):
+        return sv.adjust_logits(rows.unsqueeze(1), history=h[part].contiguous(), history_len=lens[part].contiguous(),
+                                repetition=pen[part].contiguous(), presence=pen[part].contiguous()).squeeze(1)
+
+    assert torch.equal(adjust(x, slice(None))[at], adjust(last, at))
+    rec, own = sv.top_logits(x, k), sv.top_logits(last, k)
+    assert all(torch.equal(a[at], b) for a, b in zip(rec, own))
+    w = torch.rand(R, generator=g, device=DEV)
+    loss, grad = sv.distill_loss_grad(x, *rec, 1.2, weight=w)
+    want = sv.distill_loss_grad(last, *own, 1.2, weight=w[at].contiguous())
+    assert torch.equal(loss[at], want[0]) and torch.equal(grad[at], want[1])
+    del grad
+    sv.distill_loss_grad(x, *rec, 1.2, weight=w, out_grad=x)
+    assert torch.equal(x[at], want[1])
+    x[at] = last
+    y, z = x.requires_grad_(), last.clone().requires_grad_()
+    (a,) = torch.autograd.grad(sv.distill_loss(y, *rec, 1.2, weight=w).sum(), y)
+    (b,) = torch.autograd.grad(sv.distill_loss(z, *own, 1.2, weight=w[at].contiguous()).sum(), z)
+    assert torch.equal(a[at], b)
+
+
+def test_wide_records_beyond_32_bit_offsets(sv):
+    """The same for the form with a cluster per row (lists above 256 tokens)."""
+    R, n, k, V = 17000, 40, 300, 128256
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB")
+    g = torch.Generator(device=DEV).manual_seed(6)
+    x = torch.empty(R, V, dtype=torch.bfloat16, device=DEV)
+    for r in range(0, R, 1000):
+        x[r:r + 1000] = torch.randn(1000, V, generator=g, device=DEV) * 2.5
+    idx = torch.randint(0, V, (R, k), generator=g, device=DEV, dtype=torch.int32)
+    lp, at = torch.randn(R, k, generator=g, device=DEV), slice(R - n, None)
+    want = sv.distill_loss_grad(x[at].clone(), idx[at].contiguous(), lp[at].contiguous())
+    loss, _ = sv.distill_loss_grad(x, idx, lp, out_grad=x)
+    assert torch.equal(loss[at], want[0]) and torch.equal(x[at], want[1])
