@@ -122,7 +122,8 @@ sv_status sv_top_logits(int R, int V, const void* logits, sv_dtype dtype, int k,
  *        ( q_v - sum_{j: indices_j = v} p_j     v listed
  *          q_v (1 - p_t / q_t)                  otherwise )
  *
- * (p_t = 0 without a tail; terms with p = 0 are 0.)  The softmax over the
+ * (p_t = 0 without a tail; terms with p = 0 are 0, and so are those of a p
+ * that lies below float32's range, 2^-125 of the largest.)  The softmax over the
  * listed values makes them logits as much as log-probabilities: a constant
  * added to a row's values (tail included) changes nothing.  The loss is not
  * scaled by temperature^2.
@@ -145,8 +146,8 @@ sv_status sv_top_logits(int R, int V, const void* logits, sv_dtype dtype, int k,
  *               place), otherwise the two must not overlap.
  *
  * A row with no usable entry and no tail has loss 0 and gradient 0.  A student
- * row that holds NaN or +inf, or only -inf, or a teacher row that holds NaN,
- * gives NaN.  Warps that wait for one another do so for a second or so at most,
+ * row that holds NaN or +inf, or only -inf, or a teacher row that holds NaN or
+ * +inf, gives NaN.  Warps that wait for one another do so for a second or so at most,
  * where a row takes microseconds; if a wait runs out nevertheless, losses,
  * statistics and gradients of all rows that it may concern are NaN throughout.
  * No workspace.

@@ -337,7 +337,8 @@ __global__ void __launch_bounds__(kDiThreads, 2) distill_kernel(const DistillPar
       const float pt = wt.hi * f2_rcp(Z);
       const bool some = st.hi > 0.f;
       sm.mt = mt == -INFINITY ? 0.f : mt;
-      sm.A = !good ? nan : !some ? 0.f : Et.hi * invS - (pt == 0.f ? 0.f : pt * f2_rcp(st));
+      // (without mass outside nothing is to be formed there, but a teacher's NaN shows)
+      sm.A = !good || pt != pt ? nan : !some ? 0.f : Et.hi * invS - (pt == 0.f ? 0.f : pt * f2_rcp(st));
       sm.M = M;
       sm.invS = invS;
       sm.Es = Ek.hi;

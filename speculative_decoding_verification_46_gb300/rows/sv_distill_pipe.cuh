@@ -197,7 +197,7 @@ __device__ __forceinline__ void dp_statistics(const float4* part, int C, const D
     const float invZ = __frcp_rn(L.Z.hi);
     const float pt = L.wt.hi * invZ;
     out.mt = mt == -INFINITY || !good ? 0.f : mt;
-    out.A = !good ? nan : !(st > 0.f) ? 0.f : (outside ? invS : E.hi * invS) - (pt == 0.f ? 0.f : pt * __frcp_rn(st));
+    out.A = !good || pt != pt ? nan : !(st > 0.f) ? 0.f : (outside ? invS : E.hi * invS) - (pt == 0.f ? 0.f : pt * __frcp_rn(st));
     out.M = M;
     out.invS = invS;
     out.Es = km == M ? 1.f : E.hi;

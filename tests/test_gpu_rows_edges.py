@@ -85,6 +85,24 @@ def test_distill_listed_tokens_far_below_at_high_temperatures(sv, distill_path, 
     _check_distill(sv, S, idx, lp, t, T, dtype, form=form)
 
 
+# ------------------------------------------------------------------ bad teachers
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("k", [6, 300])
+@pytest.mark.parametrize("form", ["fused", "inplace", "autograd"])
+def test_distill_bad_teacher_of_a_student_without_mass_outside(sv, distill_path, dtype, k, form):
+    """A teacher's NaN or +inf makes the whole row NaN, also where the student
+    has nothing outside the list to move."""
+    V = 2003
+    S = _student(3, 6, V, dtype)
+    idx, lp, t = _record(3, 6, V, k, True)
+    outside = torch.ones(6, V, dtype=torch.bool).scatter_(1, idx.long(), False)
+    S[outside] = -float("inf")
+    lp[0, 2], lp[1, 0], t[2], t[3], t[4] = float("nan"), float("inf"), float("nan"), float("inf"), -float("inf")
+    _check_distill(sv, S, idx, lp, t, 1.0, dtype, form=form)
+    _check_distill(sv, S[:2], idx[:2], lp[:2], None, 1.0, dtype, form=form)
+
+
 # ------------------------------------------------------------------ threads
 
 _HARNESS = """
