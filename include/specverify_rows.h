@@ -151,6 +151,11 @@ sv_status sv_top_logits(int R, int V, const void* logits, sv_dtype dtype, int k,
  * where a row takes microseconds; if a wait runs out nevertheless, losses,
  * statistics and gradients of all rows that it may concern are NaN throughout.
  * No workspace.
+ *
+ * The calls that form the loss are fastest for k <= 256 and rows of at most
+ * 131072 float32 or 262144 16-bit values; beyond, another kernel takes two to
+ * three times as long (512 float32 rows, k = 64: 66 us at V = 131072, 212 at
+ * V = 152064).
  */
 #define SV_DISTILL_STAT_WORDS 8
 sv_status sv_distill_forward(int R, int V, const void* student, sv_dtype dtype, const int32_t* indices,

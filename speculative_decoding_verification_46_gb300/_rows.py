@@ -374,7 +374,9 @@ def distill_loss(student, indices, logprobs, tail=None, temperature=1.0, *, weig
     float32 scales each row's loss, and a row of weight 0 may hold anything.  Returns
     the rows' losses [...] float32: weight * KL(teacher || student), both at
     `temperature`.  The gradient has the student's type.  Runs on the current
-    stream.
+    stream.  A backward pass into a leaf's .grad that is captured into a CUDA
+    graph wants no eager autograd graph of that leaf alive (PyTorch's engine
+    ends the process otherwise); distill_loss_grad has no such condition.
     """
     _check_distill(student, indices, logprobs, tail, weight)
     temperature = float(temperature)

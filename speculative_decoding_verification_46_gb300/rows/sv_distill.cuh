@@ -22,9 +22,10 @@
 // twice.
 //
 // It is the form for lists of more than 256 tokens and rows beyond the
-// persistent form's reach (sv_distill_pipe.cuh, which is up to three times as
-// fast: 1024 rows of 152064 bf16, k = 128: 225 us here, 95 there), bound by
-// the latency of a row's phases, of which two CTAs an SM overlap.
+// persistent form's reach (sv_distill_pipe.cuh, which is two to three times as
+// fast: the loss of 1024 rows of 152064 bf16, k = 128: 225 us here, 91 there;
+// with the gradient 284 and 135), bound by the latency of a row's phases, of
+// which two CTAs an SM overlap.
 //
 // distill_backward_kernel forms the gradient from the forward pass's row
 // statistics: no reduction, one CTA per slice.  HBM: 2048 rows of 128256 bf16 in
@@ -98,7 +99,9 @@ __device__ __forceinline__ float distill_loss(F2 Z, F2 S, F2 st, F2 E1, F2 wt, f
 
 // 2^(d (c + c_lo)), d <= 0: the weight of a value that lies d below its
 // reference.  One exponential, corrected to first order for the product's
-// rounding and for c_lo.
+// rounding and for c_lo: the instruction's 2^-22 is what is left, as in every
+// term outside the list (the fused call has two-float weights here because
+// its loss, a small difference, needs them).
 __device__ __forceinline__ float weight_fast(float d, float c, float c_lo) {
   const float p = d * c;
   if (p < -150.f) return 0.f;   // also where the product leaves float32's range

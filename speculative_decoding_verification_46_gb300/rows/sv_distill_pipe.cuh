@@ -36,7 +36,7 @@
 // Bound: HBM, with instruction issue close behind (loss and gradient: 4096 rows
 // of 128256 bf16, k = 64, a tenth of weight 0: 344 us, 5.8 TB/s, 0.85 of the
 // measured copy); the loss alone by the streaming warps' instructions and
-// latency (2048 rows, 0.47 GB: 123 us, 0.57).  A slice of 64 KB in three stages
+// latency (2048 rows, 0.47 GB: 114 us, 0.61).  A slice of 64 KB in three stages
 // fills an SM's shared memory, so a row of 128256 bf16 is 4 CTAs and 36 clusters
 // are resident (144 of 152 SMs); 22 streaming warps of at most 6 vectors a
 // thread and row leave 72 registers a thread (16 warps of 8: 483 us against 416
@@ -176,6 +176,7 @@ __device__ __forceinline__ void dp_statistics(const float4* part, int C, const D
   for (int o = kDiMaxC / 2; o >= 1; o >>= 1) st += __shfl_xor_sync(0xffffffffu, st, o);
   F2 WK = L.WK;
   if (twice) {                          // a token's weight counts once, whatever the list says
+    // (float32 weights here, off by half a step each, as the gradient's are; their sum is two-float)
     WK = F2{0.f, 0.f};
     for (int j = lane; j < k; j += 32) {
       bool first = L.sid[j] >= 0;
@@ -464,6 +465,7 @@ __global__ void __launch_bounds__(kDpMaxThreads, 1) distill_pipe_kernel(const Di
     asm volatile("cp.async.wait_group 0;" ::: "memory");
   } else if (role == 0) {
     // ================================================================ parts
+    // (float32, a tree over 22 warps: the part outside the list, see dp_statistics)
     const int last = rank == 0 ? (int)min((unsigned)n, (unsigned)p.stop) : n;   // n for -1
 #pragma unroll 1
     for (int t = 0; t < last; ++t) {

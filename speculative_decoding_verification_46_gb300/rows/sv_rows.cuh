@@ -18,7 +18,6 @@ namespace rows {
 template <typename T> struct Elem;
 template <> struct Elem<float> {
   __device__ static __forceinline__ float of_raw(uint32_t r) { return __uint_as_float(r); }
-  __device__ static __forceinline__ __nv_bfloat162 both_ru(float) { return __nv_bfloat162{}; }   // not used
   __device__ static __forceinline__ float load(const float* p) { return *p; }
   __device__ static __forceinline__ void store(float* p, float x) { *p = x; }
   __device__ static __forceinline__ uint32_t raw(const float* p) { return *reinterpret_cast<const uint32_t*>(p); }
@@ -229,7 +228,7 @@ __device__ __forceinline__ F2 weight_f2(float x, float m, F2 c, const float* tab
 // values of T; NaN stay).
 template <typename T>
 __device__ __forceinline__ void clear_ge(uint4& x, float thr) {
-  if (sizeof(T) == 4) {
+  if constexpr (sizeof(T) == 4) {
 #pragma unroll
     for (int t = 0; t < 4; ++t)
       if (__uint_as_float(word_of(x, t)) >= thr) set_word(x, t, Elem<T>::kNegInf);
@@ -266,7 +265,6 @@ __device__ __forceinline__ unsigned long long block_sum_u64(unsigned long long v
   return t;
 }
 
-__device__ __forceinline__ double f2_double(F2 a) { return (double)a.hi + (double)a.lo; }
 __device__ __forceinline__ F2 f2_from(double d) {
   const float h = (float)d;
   return F2{h, (float)(d - (double)h)};

@@ -126,9 +126,16 @@ int top_override() {
   return !e ? 0 : std::strcmp(e, "toprow") == 0 ? 1 : std::strcmp(e, "topslice") == 0 ? 2 : 0;
 }
 
-// A CTA per row from as many rows as SMs on, slices of rows for fewer (152064
-// bf16, k 64: 100 rows 31 us in slices, 39 in one CTA each; 152 rows 41 and
-// 38; 608 rows 133 and 64).
+// A CTA per row from as many rows as SMs on, slices of rows for fewer.  In us,
+// slices and one CTA each, bf16:
+//   152064 tokens   k 8        k 64       k 256
+//     100 rows      26   28    33   39    72   56
+//     152 rows      33   29    44   39    97   58
+//     608 rows      104  50    135  65    299  125
+//   32000 tokens
+//     100 rows      15   14    17   20    34   32
+//     152 rows      15   15    17   22    31   32
+//     608 rows      34   23    42   31    87   65
 bool top_by_rows(long long R) {
   const int o = top_override();
   return o == 1 || (o == 0 && R >= sm_count());
@@ -143,7 +150,7 @@ struct TopLayout {
 // would leave SMs without work, as long as a slice holds 8 k elements (its
 // candidates are then a small part of it) and the slices' lists stay a short
 // piece of work for the CTA that joins them (one row of 152064 bf16, k 64: 74
-// slices 32 us, 32 slices 20).
+// slices 40 us, 32 slices 18).
 TopLayout top_layout(long long R, int V, int k, int VW, int sms) {
   TopLayout L{};
   const long long nv = ceil_div((long long)V + (V % VW ? VW - 1 : 0), VW);
@@ -271,9 +278,9 @@ sv_status launch_distill_pipe(sv::rows::DistillParams p, cudaStream_t stream) {
 }
 
 // The persistent form wherever it applies: with few rows it is as fast as a
-// cluster per row (20 rows of 1024 float32: 9.3 us against 8.8; 64 of 128256
-// bf16: 11.3 against 14.9), with many it is far ahead (4000 rows of 1024 bf16:
-// 65 us against 131; 500 of 50001 f16: 25 against 46).  A cluster per row
+// cluster per row (the loss of 20 rows of 1024 float32: 9.2 us against 9.0; 64
+// of 128256 bf16: 11.5 against 15.2), with many it is far ahead (4000 rows of
+// 1024 bf16: 66 us against 130; 500 of 50001 f16: 25 against 48).  A cluster per row
 // remains for longer lists and larger vocabularies.  CTAs per row there: as
 // few as hold the row in registers (8 vectors per thread), more where the
 // rows alone would leave SMs without work, at most 8.
