@@ -393,10 +393,11 @@ def distill_loss_grad(student, indices, logprobs, tail=None, temperature=1.0, *,
     (sv_distill_loss_grad): returns (loss [...] float32, gradient of loss.sum()
     with respect to student).  out_grad: where the gradient goes (student
     itself: in place).  Arguments as distill_loss; nothing is recorded for
-    autograd, so it can be captured into a CUDA graph whatever autograd graphs
+    autograd (student.backward(grad) hands the gradient on to what made the
+    student), so it can be captured into a CUDA graph whatever autograd graphs
     are alive.  stream: as in adjust_logits.
     """
-    _need_constants("out_grad", out_grad)
+    _need_constants("out_grad", None if out_grad is student else out_grad)
     if forward_ad._current_level >= 0:
         with torch.no_grad():                # a tangent would be dropped; backward mode is documented above
             _need_constants("student", student)

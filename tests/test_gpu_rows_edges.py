@@ -47,6 +47,29 @@ def test_distill_tokens_listed_twice_in_wide_rows(sv, distill_path, form, k):
     _check_distill(sv, S, idx, lp, t, 1.0, "f32", form=form)
 
 
+def test_the_gradient_in_place_of_rows_that_a_model_made(sv):
+    """Rows that require a gradient turn into it, and it is handed on to what
+    made them: the parameters' gradients are those of the autograd form."""
+    R, D, V = 40, 64, 3000
+    g = torch.Generator(device=DEV).manual_seed(4)
+    h, W0 = torch.randn(R, D, generator=g, device=DEV), torch.randn(D, V, generator=g, device=DEV) / 8
+    idx, lp, t = (x.to(DEV) for x in _record(4, R, V, 12, True))
+    grads = []
+    for fused in (False, True):
+        W = W0.clone().requires_grad_()
+        rows = h @ W
+        if fused:
+            _, grad = sv.distill_loss_grad(rows, idx, lp, t, out_grad=rows)
+            assert grad is rows
+            rows.backward(grad.detach())
+        else:
+            sv.distill_loss(rows, idx, lp, t).sum().backward()
+        grads.append(W.grad)
+    # two forms of one formula, each within (3 s + 16 u) of its magnitudes (at most 2 an element), summed over the rows
+    tol = R * 2 * (3 * (40 + 60) + 16) * 2.0 ** -24 * float(h.abs().max())
+    assert float((grads[0] - grads[1]).abs().max()) <= tol
+
+
 # ------------------------------------------------------------------ large common offsets
 
 @pytest.mark.parametrize("offset", [0.0, 100.0, 1e4, -1e4, 2e5, 3e6, -3e6, 5545177.0, -5545177.0, 6e6])

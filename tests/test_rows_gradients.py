@@ -40,6 +40,13 @@ def test_refuses_what_wants_a_gradient(name, call):
         call()
 
 
+def test_the_gradient_may_take_the_place_of_a_student_that_requires_one():
+    """Documented: nothing is recorded, and the caller hands the gradient on."""
+    for student in (_grad(2, 3, 16), _grad(2, 3, 16) * 2):
+        with pytest.raises(ValueError, match="CUDA"):
+            sv.distill_loss_grad(student, IDX, LP, out_grad=student)
+
+
 def test_refuses_forward_mode():
     with forward_ad.dual_level():
         dual = forward_ad.make_dual(torch.zeros(2, 3, 16), torch.ones(2, 3, 16))
