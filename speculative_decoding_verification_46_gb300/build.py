@@ -5,7 +5,8 @@
 The output goes to ``speculative_decoding_verification_46_gb300/lib/`` (git
 ignored).  The library is rebuilt when a source or header is newer than it.
 The verify step's sources are in ``csrc/``, those of the operators on logits
-rows in ``rows/``; the translation units are compiled side by side.
+rows in ``rows/``, on the key/value cache in ``cache/``; the translation units
+are compiled side by side.
 """
 
 from __future__ import annotations
@@ -18,17 +19,19 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 ROWS = os.path.join(PKG, "rows")
+CACHE = os.path.join(PKG, "cache")
 INCLUDE = os.path.join(ROOT, "include")
 LIBDIR = os.path.join(PKG, "lib")
 LIBNAME = "libspecverify.so"
 LIB_PATH = os.path.join(LIBDIR, LIBNAME)
 
-SOURCES = [os.path.join(CSRC, "sv_api.cu"), os.path.join(CSRC, "sv_noalloc.cu"), os.path.join(ROWS, "sv_rows_api.cu")]
+SOURCES = [os.path.join(CSRC, "sv_api.cu"), os.path.join(CSRC, "sv_noalloc.cu"), os.path.join(ROWS, "sv_rows_api.cu"),
+           os.path.join(CACHE, "sv_cache_api.cu")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
 def _inputs():
-    files = [os.path.join(d, f) for d in (CSRC, ROWS) for f in os.listdir(d) if f.endswith((".cu", ".cuh", ".h"))]
+    files = [os.path.join(d, f) for d in (CSRC, ROWS, CACHE) for f in os.listdir(d) if f.endswith((".cu", ".cuh", ".h"))]
     files += [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE) if f.endswith(".h")]
     return files
 

@@ -1,0 +1,294 @@
+// Host side of the operators on the paged 4-bit cache: argument validation and
+// launches for the C ABI declared in include/specverify_cache.h.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+#include <cstddef>
+#include <cstdint>
+
+#include "specverify_cache.h"
+#include "sv_attend.cuh"
+#include "sv_kv4.cuh"
+#include "sv_plan.cuh"
+
+namespace {
+
+constexpr size_t kAlign = 256;
+size_t up(size_t x) { return (x + kAlign - 1) & ~(kAlign - 1); }
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool model_type(sv_dtype dt) { return dt == SV_DTYPE_BF16 || dt == SV_DTYPE_F16; }
+bool page_ok(int page) { return page >= 16 && page <= SV_MAX_CACHE_PAGE && page % 16 == 0; }
+bool rows_ok(int B, int gamma) {
+  return B >= 0 && gamma >= 0 && gamma < SV_MAX_CACHE_ROWS && (long long)B * (gamma + 1ll) <= SV_MAX_CACHE_ROWS;
+}
+bool cache_ok(int heads, int D, int page, int pages) {
+  return heads >= 1 && heads <= SV_MAX_CACHE_HEADS && (D == 64 || D == 128) && page_ok(page) && pages >= 0 &&
+         (long long)pages * page <= SV_MAX_CACHE_SLOTS;
+}
+bool strides_ok(const int64_t* s) {
+  if (!s) return false;
+  for (int i = 0; i < 3; ++i)
+    if (s[i] < 0 || s[i] % 8) return false;
+  return true;
+}
+
+int device_index() {
+  int dev = 0;
+  return cudaGetDevice(&dev) == cudaSuccess ? dev : -1;
+}
+int sm_count() {
+  static std::atomic<int> cached[64];
+  const int dev = device_index();
+  if (dev < 0) return 152;
+  if (dev < 64 && cached[dev].load(std::memory_order_relaxed) > 0) return cached[dev].load(std::memory_order_relaxed);
+  int n = 0;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 152;
+  if (dev < 64) cached[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+// Opt in to `most` bytes of dynamic shared memory, the most that any launch of
+// the kernel asks for, once per kernel (`set`: a static of the launch site) and
+// device: threads that come here together set the same limit.
+bool allow_smem(std::atomic<bool> (&set)[64], const void* kern, size_t most) {
+  const int dev = device_index();
+  if (dev < 0 || dev >= 64) return false;
+  if (set[dev].load(std::memory_order_acquire)) return true;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) != cudaSuccess) {
+    cudaGetLastError();
+    return false;
+  }
+  set[dev].store(true, std::memory_order_release);
+  return true;
+}
+
+sv_status launched() { return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA; }
+
+template <typename K, typename P>
+sv_status launch(K kern, dim3 grid, unsigned block, size_t smem, cudaStream_t stream, const P& p,
+                 cudaLaunchAttribute* attr) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) {
+    cudaGetLastError();
+    return SV_ERR_CUDA;
+  }
+  return launched();
+}
+
+// ---------------------------------------------------------------- store
+
+sv::cache::StoreParams store_params(int R, int rows, int heads, int page, int pages, const int32_t* slots) {
+  sv::cache::StoreParams p{};
+  p.R = R;
+  p.rows = rows;
+  p.H = heads;
+  p.page = page;
+  p.slots_end = (long long)pages * page;
+  p.slots = slots;
+  return p;
+}
+
+// CTAs for a group of D / 8 lanes per (row, head); 0: too many
+unsigned store_grid(int R, int heads, int D) {
+  const long long ctas = ((long long)R * heads * (D / 8) + sv::cache::kStoreThreads - 1) / sv::cache::kStoreThreads;
+  return ctas > 0x7fffffffll ? 0u : (unsigned)ctas;
+}
+
+// ---------------------------------------------------------------- attend
+
+int attend_ctas_per_sm(int MT) { return MT == 1 ? 3 : 2; }
+int attend_row_tiles(int rows) { return rows <= 16 ? 1 : 2; }
+
+struct AttendLayout {
+  size_t desc, part, total;
+};
+AttendLayout attend_layout(int MT, int D, int ctas) {
+  AttendLayout L;
+  L.desc = 0;
+  L.part = up((size_t)ctas * sizeof(int4));
+  L.total = L.part + up((size_t)2 * ctas * sv::cache::part_floats(16 * MT, D) * sizeof(float));
+  return L;
+}
+
+template <typename T, int D, int MT>
+sv_status launch_attend(sv::cache::AttendParams p, void* workspace, cudaStream_t stream) {
+  using Shape = sv::cache::AttendShape<T, D, MT>;
+  auto kern = sv::cache::attend_kernel<T, D, MT>;
+  static std::atomic<bool> set[64];
+  if (!allow_smem(set, (const void*)kern, Shape::kSmem)) return SV_ERR_CUDA;
+  const int ctas = sm_count() * attend_ctas_per_sm(MT);
+  const AttendLayout L = attend_layout(MT, D, ctas);
+  p.desc = reinterpret_cast<int4*>(static_cast<unsigned char*>(workspace) + L.desc);
+  p.part = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + L.part);
+  kern<<<ctas, sv::cache::kAtThreads, Shape::kSmem, stream>>>(p);
+  const sv_status st = launched();
+  if (st != SV_OK) return st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  return launch(sv::cache::attend_join_kernel<T, D, Shape::TR>, dim3(ctas, 4), sv::cache::kAtJoinThreads, 0, stream, p,
+                attr);
+}
+
+template <typename T, int D>
+sv_status launch_attend_rows(const sv::cache::AttendParams& p, void* workspace, cudaStream_t stream) {
+  return attend_row_tiles(p.rows * p.G) == 1 ? launch_attend<T, D, 1>(p, workspace, stream)
+                                             : launch_attend<T, D, 2>(p, workspace, stream);
+}
+
+bool attend_sizes_ok(int gamma, int heads, int G, int D) {
+  return gamma >= 0 && gamma <= SV_MAX_GAMMA && heads >= 1 && heads <= SV_MAX_CACHE_HEADS && G >= 1 &&
+         G <= SV_MAX_CACHE_GROUP && (D == 64 || D == 128);
+}
+
+}  // namespace
+
+extern "C" sv_status sv_plan_round(int B, int gamma, int page, int N, int pool, int32_t* lengths, const int32_t* kept,
+                                   const int32_t* gamma_b, int32_t* block_table, int32_t* blocks, int32_t* free_blocks,
+                                   int32_t* free_count, int32_t* slots, int32_t* positions, int32_t* status,
+                                   sv_stream_t stream) {
+  if (!rows_ok(B, gamma) || B > SV_MAX_PLAN_SEQUENCES || !page_ok(page) || N < 0 || pool < 0 ||
+      (long long)B * N > SV_MAX_CACHE_SLOTS || (long long)N * page > SV_MAX_CACHE_SLOTS ||
+      (long long)pool * page > SV_MAX_CACHE_SLOTS)
+    return SV_ERR_INVALID_ARG;
+  if (B == 0) return SV_OK;
+  if (!lengths || !blocks || !free_count || !slots || !positions || !status || (N > 0 && !block_table) ||
+      (pool > 0 && !free_blocks))
+    return SV_ERR_INVALID_ARG;
+  sv::cache::PlanParams p{};
+  p.B = B;
+  p.rows = gamma + 1;
+  p.page = page;
+  p.N = N;
+  p.pool = pool;
+  p.lengths = lengths;
+  p.kept = kept;
+  p.gamma_b = gamma_b;
+  p.table = block_table;
+  p.blocks = blocks;
+  p.free_blocks = free_blocks;
+  p.free_count = free_count;
+  p.slots = slots;
+  p.positions = positions;
+  p.status = status;
+  static std::atomic<bool> set[64];
+  if (!allow_smem(set, (const void*)sv::cache::plan_round_kernel, sv::cache::plan_smem(SV_MAX_PLAN_SEQUENCES)))
+    return SV_ERR_CUDA;
+  const int ctas = (long long)B * p.rows > sv::cache::kPlanFew ? sv::cache::kPlanCtas : 1;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  return launch(sv::cache::plan_round_kernel, dim3(ctas), sv::cache::kPlanThreads, sv::cache::plan_smem(B),
+                reinterpret_cast<cudaStream_t>(stream), p, attr);
+}
+
+extern "C" sv_status sv_append_kv4(int B, int gamma, int heads, int D, int page, int pages, const void* k,
+                                   const int64_t* k_strides, const void* v, const int64_t* v_strides, sv_dtype dtype,
+                                   const int32_t* slots, void* cache, sv_stream_t stream) {
+  if (!rows_ok(B, gamma) || !cache_ok(heads, D, page, pages) || !model_type(dtype) || !strides_ok(k_strides) ||
+      !strides_ok(v_strides))
+    return SV_ERR_INVALID_ARG;
+  if (B == 0 || pages == 0) return SV_OK;
+  if (!k || !v || !slots || !cache || !aligned16(k) || !aligned16(v) || !aligned16(cache)) return SV_ERR_INVALID_ARG;
+  sv::cache::StoreParams p = store_params(B * (gamma + 1), gamma + 1, heads, page, pages, slots);
+  p.k = k;
+  p.v = v;
+  for (int i = 0; i < 3; ++i) {
+    p.ks[i] = k_strides[i];
+    p.vs[i] = v_strides[i];
+  }
+  p.cache = static_cast<unsigned char*>(cache);
+  const unsigned grid = store_grid(p.R, heads, D);
+  if (grid == 0) return SV_ERR_UNSUPPORTED;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  using namespace sv::cache;
+  if (dtype == SV_DTYPE_BF16) {
+    if (D == 64) append_kv4_kernel<__nv_bfloat16, 64><<<grid, kStoreThreads, 0, s>>>(p);
+    else append_kv4_kernel<__nv_bfloat16, 128><<<grid, kStoreThreads, 0, s>>>(p);
+  } else {
+    if (D == 64) append_kv4_kernel<__half, 64><<<grid, kStoreThreads, 0, s>>>(p);
+    else append_kv4_kernel<__half, 128><<<grid, kStoreThreads, 0, s>>>(p);
+  }
+  return launched();
+}
+
+extern "C" sv_status sv_read_kv4(int R, int heads, int D, int page, int pages, const void* cache, sv_dtype dtype,
+                                 const int32_t* slots, void* k, void* v, sv_stream_t stream) {
+  if (R < 0 || R > SV_MAX_CACHE_ROWS || !cache_ok(heads, D, page, pages) || !model_type(dtype))
+    return SV_ERR_INVALID_ARG;
+  if (R == 0) return SV_OK;
+  if (!slots || !k || !v || !aligned16(k) || !aligned16(v) || (pages > 0 && (!cache || !aligned16(cache))))
+    return SV_ERR_INVALID_ARG;
+  sv::cache::StoreParams p = store_params(R, 1, heads, page, pages, slots);
+  p.cache = static_cast<unsigned char*>(const_cast<void*>(cache));
+  p.ko = k;
+  p.vo = v;
+  const unsigned grid = store_grid(R, heads, D);
+  if (grid == 0) return SV_ERR_UNSUPPORTED;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  using namespace sv::cache;
+  if (dtype == SV_DTYPE_BF16) {
+    if (D == 64) read_kv4_kernel<__nv_bfloat16, 64><<<grid, kStoreThreads, 0, s>>>(p);
+    else read_kv4_kernel<__nv_bfloat16, 128><<<grid, kStoreThreads, 0, s>>>(p);
+  } else {
+    if (D == 64) read_kv4_kernel<__half, 64><<<grid, kStoreThreads, 0, s>>>(p);
+    else read_kv4_kernel<__half, 128><<<grid, kStoreThreads, 0, s>>>(p);
+  }
+  return launched();
+}
+
+extern "C" size_t sv_attend_kv4_workspace_bytes(int gamma, int heads, int G, int D) {
+  if (!attend_sizes_ok(gamma, heads, G, D)) return 0;
+  const int MT = attend_row_tiles((gamma + 1) * G);
+  return attend_layout(MT, D, sm_count() * attend_ctas_per_sm(MT)).total;
+}
+
+extern "C" sv_status sv_attend_kv4(int B, int gamma, int heads, int G, int D, int page, int pages, int N, const void* q,
+                                   const int64_t* q_strides, sv_dtype dtype, const void* cache,
+                                   const int32_t* block_table, const int32_t* lengths, const int32_t* gamma_b,
+                                   float scale, void* out, float* lse, int fill, void* workspace,
+                                   size_t workspace_bytes, sv_stream_t stream) {
+  if (!rows_ok(B, gamma) || !attend_sizes_ok(gamma, heads, G, D) || !cache_ok(heads, D, page, pages) || N < 0 ||
+      (long long)B * N > SV_MAX_CACHE_SLOTS || (long long)N * page > SV_MAX_CACHE_SLOTS || !model_type(dtype) ||
+      !strides_ok(q_strides) || !(scale > 0.f) || !std::isfinite(scale * 1.44269504f))
+    return SV_ERR_INVALID_ARG;
+  if (B == 0) return SV_OK;
+  if (!q || !lengths || !out || !aligned16(q) || !aligned16(out) || (N > 0 && !block_table) ||
+      (pages > 0 && (!cache || !aligned16(cache))))
+    return SV_ERR_INVALID_ARG;
+  if (!workspace || !aligned16(workspace) || workspace_bytes < sv_attend_kv4_workspace_bytes(gamma, heads, G, D))
+    return SV_ERR_WORKSPACE;
+  sv::cache::AttendParams p{};
+  p.B = B;
+  p.rows = gamma + 1;
+  p.H = heads;
+  p.G = G;
+  p.page = page;
+  p.pages = pages;
+  p.N = N;
+  p.q = q;
+  for (int i = 0; i < 3; ++i) p.qs[i] = q_strides[i];
+  p.cache = static_cast<const unsigned char*>(cache);
+  p.table = block_table;
+  p.lengths = lengths;
+  p.gamma_b = gamma_b;
+  p.scale = scale * 1.44269504f;
+  p.out = out;
+  p.lse = lse;
+  p.fill = fill;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (dtype == SV_DTYPE_BF16)
+    return D == 64 ? launch_attend_rows<__nv_bfloat16, 64>(p, workspace, s)
+                   : launch_attend_rows<__nv_bfloat16, 128>(p, workspace, s);
+  return D == 64 ? launch_attend_rows<__half, 64>(p, workspace, s) : launch_attend_rows<__half, 128>(p, workspace, s);
+}
