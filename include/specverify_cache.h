@@ -67,7 +67,8 @@ extern "C" {
  * The bookkeeping between two rounds, in place on the state.
  *
  *   lengths      [B] int32, in and out: tokens whose keys and values are valid.
- *                lengths[b] += kept[b] (at least 0)
+ *                lengths[b] += kept[b] (at least 0, at most 2^31 - 1, as
+ *                positions are)
  *   kept         [B] int32 or NULL (none): tokens of the last round that stay,
  *                negative: tokens taken back
  *   gamma_b      [B] int32 or NULL (gamma): drafts of the next round, clamped to
