@@ -13,9 +13,14 @@
 // out of the sums at the end.  q is brought to float16 with a power of two per
 // row, p_t s'_t with one per warp; the sums are float32.
 //
-// Work: the (sequence, head, row tile)s' tokens in units of 64 are one line of
+// A tensor core cuts off what lies below its sum's last bits, so sums of codes
+// n >= 0 would lose more and more over a long sequence: every second group of
+// eight tokens is taken as n - 15 (the sign bit and the complement, in the same
+// AND and XOR), and its offset as o' + 15 s'.
+//
+// Work: the (sequence, head, row tile)s' tokens in units of 128 are one line of
 // units; CTA i of W takes an equal part of it, finds its place from lengths
-// and walks on.  Four warps of a CTA take 16 tokens of a unit each, with a
+// and walks on.  The warps of a CTA take 32 tokens at a time each, with a
 // softmax and sums of their own, and are joined at the end of the segment.  A
 // segment that a CTA does not hold in full goes to the workspace;
 // attend_join_kernel, which is launched right behind, joins these in order.
@@ -28,12 +33,11 @@
 namespace sv {
 namespace cache {
 
-constexpr int kAtWarps = 4;
-constexpr int kAtThreads = 32 * kAtWarps;
-constexpr int kAtUnit = 64;               // tokens of a unit: 16 a warp
-constexpr int kAtJoinThreads = 128;
+constexpr int kAtUnit = 128;              // tokens of a unit
+constexpr int kAtStages = 3;              // groups of 32 tokens in a warp's ring
+constexpr int kAtJoinThreads = 256;
 constexpr float kAtSlack = 8.f;           // a row's reference may be 2^8 below its largest term
-constexpr float kAtValueTop = 128.f;      // largest p s' 2^x / 2^slack: their product stays below float16's 65504
+constexpr float kAtValueTop = 128.f;      // largest s' 2^x: p s' 2^x stays below 2^(7 + 8), float16 ends at 65504
 
 struct AttendParams {
   int B, rows, H, G, page, pages, N;      // rows: gamma + 1
@@ -66,51 +70,178 @@ __device__ __forceinline__ uint32_t half2_bits(float a, float b) {
 struct Sequence {
   int rows, seen, tiles, chunks;          // row tiles; units a (head, row tile)
   int first;                              // tokens that row 0 sees, before the limit of the table
-  __device__ __forceinline__ Sequence(const AttendParams& p, int b, int TR) {
+  __device__ __forceinline__ Sequence(const AttendParams& p, int b, int TR, int unit) {
     rows = p.gamma_b ? min(max(p.gamma_b[b], -1), p.rows - 1) + 1 : p.rows;
     first = (int)min((long long)max(p.lengths[b], 0) + 1, 0x7fffff00ll);
     seen = (int)min((long long)first + rows - 1, (long long)p.N * p.page);
     tiles = (rows * p.G + TR - 1) / TR;
-    chunks = max(1, (seen + kAtUnit - 1) / kAtUnit);
+    chunks = max(1, (seen + unit - 1) / unit);
   }
   __device__ __forceinline__ long long units(int H) const { return (long long)H * tiles * chunks; }
 };
 
-// 16 tokens of one head as a lane holds them (g = lane / 4, c = lane % 4), for
-// the groups of eight tokens j = 0, 1: the key codes of token 8 j + g, quarter
-// c; the value codes of tokens 8 j + 2 c and + 1, eighth g; those two tokens'
-// numbers.
-template <int KW>
-struct Codes {
-  uint32_t k[2][KW], v[2][KW];
-  uint4 n[2];
-};
-template <int KW>
-__device__ __forceinline__ void load_words(uint32_t (&w)[KW], const unsigned char* at) {
-  if constexpr (KW == 4) {
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(at));
-  } else {
-    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(at));
+// Rows behind a sequence's last become 0.
+template <typename T, int D, int THREADS>
+__device__ __forceinline__ void fill_behind(const AttendParams& p) {
+  if (!p.fill || !p.gamma_b) return;
+  const int HG = p.H * p.G;
+  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+    const int from = min(max(p.gamma_b[b], -1), p.rows - 1) + 1;
+    const long long r0 = (long long)b * p.rows + from, r1 = (long long)(b + 1) * p.rows;
+    for (long long x = r0 * HG * (D / 8) + threadIdx.x; x < r1 * HG * (D / 8); x += THREADS)
+      static_cast<uint4*>(p.out)[x] = make_uint4(0, 0, 0, 0);
+    if (p.lse)
+      for (long long x = r0 * HG + threadIdx.x; x < r1 * HG; x += THREADS) p.lse[x] = 0.f;
   }
 }
-// block: the head's block of the page; t: the 16 tokens' first in the page
-template <int D>
-__device__ __forceinline__ void load_codes(Codes<D / 32>& x, const unsigned char* block, int t, int page, int g, int c) {
+
+// Four channels of a row: sums y and mass l, both relative to 2^top.
+template <typename T, int D>
+__device__ __forceinline__ void finish_row(const AttendParams& p, long long q_row, int dg, float4 y, float top, float l) {
+  const float over = l == 0.f ? 0.f : 1.f / l;
+  reinterpret_cast<uint2*>(p.out)[q_row * (D / 4) + dg] =
+      make_uint2(Kv<T>::pack(y.x * over, y.y * over), Kv<T>::pack(y.z * over, y.w * over));
+  if (p.lse && dg == 0) p.lse[q_row] = l == 0.f ? __int_as_float(0xff800000) : (top + log2f(l)) * 6.931471805599453e-01f;
+}
+
+// A CTA's part of the line of units: [u, end), u in sequence b, whose first
+// unit is `base`; U units in all, W CTAs have one at least.  Every warp finds
+// it on its own.
+struct Part {
+  long long U, W, u, end, base;
+  int b;
+  __device__ __forceinline__ bool some() const { return blockIdx.x < W; }
+  // the CTA that unit x belongs to
+  __device__ __forceinline__ int owner(long long x) const { return (int)(((x + 1) * W - 1) / U); }
+};
+__device__ __forceinline__ Part find_part(const AttendParams& p, int TR, int unit) {
+  const int lane = threadIdx.x & 31;
+  Part x;
+  // each lane takes a run of sequences
+  const int run = (p.B + 31) / 32;
+  const int b0 = min(lane * run, p.B), b1 = min(b0 + run, p.B);
+  long long mine = 0;
+  for (int b = b0; b < b1; ++b) mine += Sequence(p, b, TR, unit).units(p.H);
+  long long upto = mine;
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    load_words(x.k[j], block + (t + 8 * j + g) * (D / 2) + c * (D / 8));
-    load_words(x.v[j], block + page * (D / 2) + ((t >> 1) + 4 * j + c) * D + g * (D / 8));
-    uint32_t n[4];
-    load_words(n, block + page * D + (t + 8 * j + 2 * c) * 8);
-    x.n[j] = make_uint4(n[0], n[1], n[2], n[3]);
+  for (int m = 1; m < 32; m <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, upto, m);
+    if (lane >= m) upto += y;
   }
+  x.U = __shfl_sync(0xffffffffu, upto, 31);
+  x.W = min((long long)gridDim.x, x.U);
+  if (threadIdx.x == 0) p.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  if (!x.some()) return x;
+  x.u = x.U * blockIdx.x / x.W;
+  x.end = x.U * (blockIdx.x + 1) / x.W;
+  x.base = upto - mine;
+  x.b = b0;
+  const bool here = x.u >= upto - mine && x.u < upto;
+  if (here) {
+    for (; x.b < b1 - 1; ++x.b) {
+      const long long n = Sequence(p, x.b, TR, unit).units(p.H);
+      if (x.u < x.base + n) break;
+      x.base += n;
+    }
+  }
+  const int from = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+  x.b = __shfl_sync(0xffffffffu, x.b, from);
+  x.base = __shfl_sync(0xffffffffu, x.base, from);
+  return x;
+}
+
+// The segment that unit u is in: head, row tile, and its units from u on that
+// are this CTA's.
+struct Segment {
+  int h, rt, at, chunk0, chunks;
+  __device__ __forceinline__ Segment(const Sequence& s, long long u, long long base, long long end) {
+    if (u - base < 0x7fffffffll) {        // (a 64-bit division takes longer)
+      at = (int)(u - base) / s.chunks;
+      chunk0 = (int)(u - base) - at * s.chunks;
+    } else {
+      at = (int)((u - base) / s.chunks);
+      chunk0 = (int)(u - base - (long long)at * s.chunks);
+    }
+    h = at / s.tiles;
+    rt = at - h * s.tiles;
+    chunks = (int)min((long long)(s.chunks - chunk0), end - u);
+  }
+};
+
+// 32 tokens of one head in a warp's ring: two subs of 16, each its keys, then
+// its values, then (behind both) its numbers, as they lie in the cache.  As
+// operands, lane (g, c) = (lane / 4, lane % 4) takes the key codes of token
+// 8 j + g, quarter c; the value codes of tokens 8 j + 2 c and + 1, eighth g;
+// those two tokens' numbers (j = 0, 1).
+template <int D>
+struct Stage {
+  static constexpr int kCodes = 8 * D;                       // bytes of a sub's keys, and of its values
+  static constexpr int kNumbers = 4 * kCodes;                // where the numbers begin
+  static constexpr int kBytes = kNumbers + 2 * 128;
+};
+template <int BYTES>
+__device__ __forceinline__ void copy_ahead(uint32_t to, const unsigned char* from) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_end_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
+
+template <int WORDS>
+__device__ __forceinline__ void shared_words(uint32_t (&w)[WORDS], uint32_t at) {
+  if constexpr (WORDS == 4)
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at) : "memory");
+  else
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at) : "memory");
+}
+
+// Two float32 operations an instruction.
+struct Two {
+  unsigned long long v;
+};
+__device__ __forceinline__ Two two(float a, float b) {
+  Two p;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(p.v) : "f"(a), "f"(b));
+  return p;
+}
+__device__ __forceinline__ void split(Two p, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p.v)); }
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+  Two d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return d;
+}
+__device__ __forceinline__ Two mul2(Two a, Two b) {
+  Two d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+  return d;
+}
+__device__ __forceinline__ Two add2(Two a, Two b) {
+  Two d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+  return d;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 
 template <typename T, int D, int MT>
 struct AttendShape {
   static constexpr int TR = 16 * MT;      // rows of a tile
-  static constexpr int kSmem = kAtWarps * (TR * D + 2 * TR) * 4;
+  static constexpr int kCtas = MT == 1 ? 3 : 2;              // an SM
+  static constexpr int kWarps = 4, kThreads = 32 * kWarps;
+  static constexpr int kQ = MT * (D / 16) * 512;             // q as operands
+  // a warp's ring, which its sums take the place of at the end of a segment
+  static constexpr int kRing = kAtStages * Stage<D>::kBytes;
+  static constexpr int kSums = (TR * D + 2 * TR) * 4;
+  static constexpr int kWarp = kRing > kSums ? kRing : kSums;
+  static constexpr int kSmem = kQ + kWarps * kWarp;
+  static_assert(kCtas * (kSmem + 2048) <= 228 * 1024, "shared memory of an SM");
 };
 
 // Position of a group of four channels (dg) of row r in a warp's sums in
@@ -118,141 +249,178 @@ struct AttendShape {
 __device__ __forceinline__ int swizzled(int r, int dg) { return dg ^ ((dg >> 3) | (r & 1) << 2); }
 
 template <typename T, int D, int MT>
-__global__ void __launch_bounds__(kAtThreads, MT == 1 ? 3 : 2) attend_kernel(const __grid_constant__ AttendParams p) {
-  constexpr int KW = D / 32, TR = 16 * MT;
-  extern __shared__ float at_sm[];
-  __shared__ long long warp_units[kAtWarps];
-  __shared__ long long found_base;
-  __shared__ int found_b;
+__global__ void __launch_bounds__(AttendShape<T, D, MT>::kThreads, AttendShape<T, D, MT>::kCtas) attend_kernel(const __grid_constant__ AttendParams p) {
+  using S = AttendShape<T, D, MT>;
+  constexpr int KW = D / 32, TR = S::TR, kWarpFloats = S::kWarp / 4, LANES = D / 8;
+  constexpr int kWarps = S::kWarps, kThreads = S::kThreads;
+  constexpr bool kFine = std::is_same<T, __half>::value;     // the weights' rest is an operand too
+  extern __shared__ __align__(16) float at_sm[];
+  __shared__ float q_sums[TR], warp_top[kWarps];
+  __shared__ int limits[TR];
+  __shared__ long long out_rows[TR];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
+  float* const all_sums = at_sm + S::kQ / 4;
   pdl_launch_dependents();
 
-  // rows behind a sequence's last
-  if (p.fill && p.gamma_b) {
-    for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-      const int from = min(max(p.gamma_b[b], -1), p.rows - 1) + 1;
-      const long long r0 = (long long)b * p.rows + from, r1 = (long long)(b + 1) * p.rows;
-      const int HG = p.H * p.G;
-      for (long long x = r0 * HG * (D / 8) + tid; x < r1 * HG * (D / 8); x += kAtThreads)
-        static_cast<uint4*>(p.out)[x] = make_uint4(0, 0, 0, 0);
-      if (p.lse)
-        for (long long x = r0 * HG + tid; x < r1 * HG; x += kAtThreads) p.lse[x] = 0.f;
-    }
-  }
-
-  // all units, and those of the sequences before each thread's run
-  const int run = (p.B + kAtThreads - 1) / kAtThreads;
-  const int b0 = min(tid * run, p.B), b1 = min(b0 + run, p.B);
-  long long mine = 0;
-  for (int b = b0; b < b1; ++b) mine += Sequence(p, b, TR).units(p.H);
-  long long upto = mine;
-#pragma unroll
-  for (int m = 1; m < 32; m <<= 1) {
-    const long long x = __shfl_up_sync(0xffffffffu, upto, m);
-    if (lane >= m) upto += x;
-  }
-  if (lane == 31) warp_units[warp] = upto;
-  __syncthreads();
-  long long U = 0;
-#pragma unroll
-  for (int w = 0; w < kAtWarps; ++w) {
-    if (w < warp) upto += warp_units[w];
-    U += warp_units[w];
-  }
-  const long long W = min((long long)gridDim.x, U);
+  fill_behind<T, D, kThreads>(p);
+  const Part line = find_part(p, TR, kAtUnit);
+  if (!line.some()) return;
+  long long u = line.u, base = line.base;
+  int b = line.b;
   const int me = blockIdx.x;
-  if (me >= W) {
-    if (tid == 0) p.desc[me] = make_int4(-1, 0, 0, 0);
-    return;
-  }
-  long long u = U * me / W;
-  const long long end = U * (me + 1) / W;
-  if (u >= upto - mine && u < upto) {
-    long long base = upto - mine;
-    int b = b0;
-    for (; b < b1 - 1; ++b) {
-      const long long n = Sequence(p, b, TR).units(p.H);
-      if (u < base + n) break;
-      base += n;
-    }
-    found_b = b;
-    found_base = base;
-  }
-  __syncthreads();
-  int b = found_b;
-  long long base = found_base;
-  if (tid == 0) p.desc[me] = make_int4(-1, 0, 0, 0);
 
   const long long block_bytes = (long long)p.page * kTokenBytes<D>;
   const int page_tiles = p.page / 16;
-  while (u < end) {
-    const Sequence s(p, b, TR);
+  const uint32_t q_at = (uint32_t)__cvta_generic_to_shared(at_sm) + lane * 16;
+  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(all_sums + warp * kWarpFloats);
+  while (u < line.end) {
+    const Sequence s(p, b, TR, kAtUnit);
     const long long n_units = s.units(p.H);
     if (u >= base + n_units) {
       base += n_units;
       ++b;
       continue;
     }
-    const int at = (int)((u - base) / s.chunks), chunk0 = (int)(u - base - (long long)at * s.chunks);
-    const int h = at / s.tiles, rt = at - h * s.tiles;
-    const int chunks = (int)min((long long)(s.chunks - chunk0), end - u);
+    const Segment segment(s, u, base, line.end);
+    const int h = segment.h, rt = segment.rt, chunk0 = segment.chunk0, chunks = segment.chunks;
 
-    // ---- the rows: q as float16 fragments, a power of two per row apart
-    uint32_t qf[MT][2 * KW][4];
-    float row_scale[MT][2], q_sum[MT][2], ref[MT][2], mass[MT][2], shift[MT][2];
-    int limit[MT][2];                     // last position that the row sees
+    // ---- this warp's groups of 32 tokens, number `first` + 8 n
+    const int sub_end = (s.seen + 15) / 16;
+    const int first = chunk0 * (kAtUnit / 32) + warp;
+    const int groups = max(0, (min((chunk0 + chunks) * (kAtUnit / 32), (sub_end + 1) / 2) - first + kWarps - 1) / kWarps);
+    // A lane knows where sub lane % 2 of group lane / 2 of the next 16 begins
+    // in the cache, its number in the page in the low four bits; 0: hidden.
+    // The 16 behind them are asked for ahead of time.
+    int ask_id = -1, ask_sub = 0;
+    auto ask = [&](int n) {
+      const int mine = 2 * (first + kWarps * (n + (lane >> 1))) + (lane & 1);
+      ask_id = -1;
+      if (n + (lane >> 1) < groups && mine < sub_end) {
+        const int x = mine / page_tiles;
+        ask_id = __ldg(p.table + (long long)b * p.N + x);
+        ask_sub = mine - x * page_tiles;
+      }
+    };
+    unsigned long long ahead = 0;
+    auto learn = [&]() {
+      ahead = 0;
+      if (ask_id >= 0 && ask_id < p.pages)
+        ahead = reinterpret_cast<unsigned long long>(p.cache) +
+                (unsigned long long)(((long long)ask_id * p.H + h) * block_bytes + ask_sub * (8 * D) + ask_sub);
+    };
+    ask(0);
+    // q is on its way meanwhile: a thread's pieces of eight channels
+    constexpr int PIECES = (TR * LANES + kThreads - 1) / kThreads;
+    uint4 qv[PIECES];
+#pragma unroll
+    for (int k = 0; k < PIECES; ++k) {
+      const int x = tid + k * kThreads, rl = x / LANES, r = rt * TR + rl, i = r / p.G;
+      qv[k] = make_uint4(0, 0, 0, 0);
+      if (rl < TR && i < s.rows)
+        qv[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + b * p.qs[0] + i * p.qs[1] +
+                                                     (long long)(h * p.G + r - i * p.G) * p.qs[2]) + x % LANES);
+    }
+    uint32_t to = ring;                   // where the next group goes
+    uint32_t there = 0;                   // bits 2 (n % 8), + 1: which subs of group n are there
+    auto copy_group = [&](int n) {
+      if (n < groups) {
+        if ((n & 15) == 0) {
+          learn();
+          ask(n + 16);
+        }
+        const unsigned long long from0 = __shfl_sync(0xffffffffu, ahead, 2 * (n & 15));
+        const unsigned long long from1 = __shfl_sync(0xffffffffu, ahead, 2 * (n & 15) + 1);
+        const int bit = 2 * (n & 7);
+        there = (there & ~(3u << bit)) | (uint32_t)(from0 != 0) << bit | (uint32_t)(from1 != 0) << (bit + 1);
+        constexpr int C = Stage<D>::kCodes;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const unsigned long long from = i ? from1 : from0;
+          if (from == 0) continue;
+          const int sub = (int)(from & 15);
+          const unsigned char* codes = reinterpret_cast<const unsigned char*>(from - sub) + lane * 16;
+#pragma unroll
+          for (int j = 0; j < D / 64; ++j) {
+            copy_ahead<16>(to + lane * 16 + i * 2 * C + j * 512, codes + j * 512);
+            copy_ahead<16>(to + lane * 16 + i * 2 * C + C + j * 512, codes + p.page * (D / 2) + j * 512);
+          }
+          if (lane < 8)
+            copy_ahead<16>(to + lane * 16 + Stage<D>::kNumbers + i * 128, codes + p.page * D - sub * (8 * D - 128));
+        }
+        to = to == ring + (kAtStages - 1) * Stage<D>::kBytes ? ring : to + Stage<D>::kBytes;
+      }
+      copies_end_group();
+    };
+#pragma unroll
+    for (int n = 0; n < kAtStages - 1; ++n) copy_group(n);
+
+    // ---- q as operands: float16 with one power of two for the tile (a row
+    // whose largest element is 2^-20 of the tile's still has its scores to
+    // 2^-17 of their size)
+    float row_scale;
+    {
+      float top = 0.f;
+#pragma unroll
+      for (int k = 0; k < PIECES; ++k) {
+        const int x = tid + k * kThreads, rl = x / LANES;
+        const uint32_t w[4] = {qv[k].x, qv[k].y, qv[k].z, qv[k].w};
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float f0 = Kv<T>::lo(w[j]), f1 = Kv<T>::hi(w[j]);
+          top = max3(top, fabsf(f0), fabsf(f1));
+          sum += f0 + f1;
+        }
+#pragma unroll
+        for (int m = LANES / 2; m >= 1; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+        if (x % LANES == 0 && rl < TR) {
+          const int r = rt * TR + rl, i = r / p.G;
+          q_sums[rl] = sum;
+          limits[rl] = i < s.rows ? min(s.first - 1 + i, s.seen - 1) : -1;
+          out_rows[rl] = i < s.rows ? ((long long)b * p.rows + i) * p.H * p.G + (long long)h * p.G + (r - i * p.G) : -1;
+        }
+      }
+#pragma unroll
+      for (int m = 16; m >= 1; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
+      if (lane == 0) warp_top[warp] = top;
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < kWarps; ++j) top = fmaxf(top, warp_top[j]);
+      // 2^up * top in [2^13, 2^14)
+      const int up = top > 0.f ? min(140 - (int)(__float_as_uint(top) >> 23), 126) : 0;
+      const float raise = __uint_as_float((uint32_t)(up + 127) << 23);
+      row_scale = p.scale * 0x1p24f * __uint_as_float((uint32_t)(127 - up) << 23);
+      // the products' unit is 2^-24 of a code
+      if (tid < TR) q_sums[tid] *= raise * 0x1p-24f;
+#pragma unroll
+      for (int k = 0; k < PIECES; ++k) {
+        const int x = tid + k * kThreads, rl = x / LANES, word = x % LANES;
+        if (rl >= TR) break;
+        const uint32_t w[4] = {qv[k].x, qv[k].y, qv[k].z, qv[k].w};
+        // word j of quarter cc; channels 2 t, 2 t + 4 as they are, 2 t + 1,
+        // 2 t + 5 for codes of 16 times their size
+        const int cc = word / KW, j = word % KW, m = rl >> 4, e = rl >> 3 & 1;
+        uint32_t* to_q = reinterpret_cast<uint32_t*>(at_sm) + ((m * 2 * KW + 2 * j) * 32 + (rl & 7) * 4 + cc) * 4 + e;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          to_q[t * 128] = half2_bits(Kv<T>::lo(w[t]) * raise, Kv<T>::lo(w[t + 2]) * raise);
+          to_q[t * 128 + 2] = half2_bits(Kv<T>::hi(w[t]) * raise * 0.0625f, Kv<T>::hi(w[t + 2]) * raise * 0.0625f);
+        }
+      }
+      __syncthreads();
+    }
+
+    float ref[MT][2];
+    Two q_sum[MT][2], mass[MT][2], shift[MT][2];          // mass, shift: of the lane's even and odd tokens
     float o[MT][4 * KW][4];
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int r = rt * TR + m * 16 + e * 8 + g, i = r / p.G;
-        const bool there = i < s.rows;
-        uint4 x[KW];
-#pragma unroll
-        for (int j = 0; j < KW; ++j) x[j] = make_uint4(0, 0, 0, 0);
-        if (there) {
-          const T* row = static_cast<const T*>(p.q) + b * p.qs[0] + i * p.qs[1] + (long long)(h * p.G + r - i * p.G) * p.qs[2];
-#pragma unroll
-          for (int j = 0; j < KW; ++j) x[j] = __ldg(reinterpret_cast<const uint4*>(row) + c * KW + j);
-        }
-        float f[KW][8], top = 0.f;
-#pragma unroll
-        for (int j = 0; j < KW; ++j) {
-          const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
-#pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            f[j][2 * t] = Kv<T>::lo(w[t]);
-            f[j][2 * t + 1] = Kv<T>::hi(w[t]);
-            top = fmaxf(top, fmaxf(fabsf(f[j][2 * t]), fabsf(f[j][2 * t + 1])));
-          }
-        }
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // 2^up * top in [2^13, 2^14)
-        const int up = top > 0.f ? min(140 - (int)(__float_as_uint(top) >> 23), 126) : 0;
-        const float raise = __uint_as_float((uint32_t)(up + 127) << 23);
-        float sum = 0.f;
-#pragma unroll
-        for (int j = 0; j < KW; ++j) {
-#pragma unroll
-          for (int t = 0; t < 8; ++t) {
-            f[j][t] *= raise;
-            sum += f[j][t];
-          }
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            qf[m][2 * j + t][e] = half2_bits(f[j][2 * t], f[j][2 * t + 4]);
-            qf[m][2 * j + t][2 + e] = half2_bits(f[j][2 * t + 1] * 0.0625f, f[j][2 * t + 5] * 0.0625f);
-          }
-        }
-        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        q_sum[m][e] = sum * 0x1p-24f;       // in the units of the products with the codes
-        row_scale[m][e] = p.scale * 0x1p24f * __uint_as_float((uint32_t)(127 - up) << 23);
-        ref[m][e] = -FLT_MAX;
-        mass[m][e] = shift[m][e] = 0.f;
-        limit[m][e] = there ? min(s.first - 1 + i, s.seen - 1) : -1;
+        const float q = q_sums[m * 16 + e * 8 + g];
+        q_sum[m][e] = two(q, q);
+        ref[m][e] = 0.f;
+        mass[m][e] = shift[m][e] = two(0.f, 0.f);
       }
 #pragma unroll
       for (int t = 0; t < 4 * KW; ++t)
@@ -260,99 +428,77 @@ __global__ void __launch_bounds__(kAtThreads, MT == 1 ? 3 : 2) attend_kernel(con
         for (int x = 0; x < 4; ++x) o[m][t][x] = 0.f;
     }
     float value_scale = 0x1p126f;         // what p s' is multiplied by, a power of two
+    // The first group sets the references.  A row that sees none of it sees
+    // none of the later ones: its mass stays 0.
+    bool fresh = true;
 
-    // ---- this warp's groups of 16 tokens
-    const int last = min((chunk0 + chunks) * (kAtUnit / 16), (s.seen + 15) / 16);
-    const int first = chunk0 * (kAtUnit / 16) + warp;
-    const int every = s.first;            // positions below it are seen by every row of the sequence
-    int ahead = 0;                        // page of this lane's group of the next 32
-    auto look = [&](int t) {
-      const int mine_t = t + lane * kAtWarps;
-      ahead = mine_t < last ? __ldg(p.table + (long long)b * p.N + mine_t / page_tiles) : -1;
-      if (ahead >= p.pages) ahead = -1;
-    };
-    Codes<KW> next;
-    int next_page = -1;
-    if (first < last) {
-      look(first);
-      next_page = __shfl_sync(0xffffffffu, ahead, 0);
-      if (next_page >= 0)
-        load_codes<D>(next, p.cache + ((long long)next_page * p.H + h) * block_bytes, (first % page_tiles) * 16, p.page, g, c);
-    }
-    int turn = 0;
-    for (int t = first; t < last; t += kAtWarps) {
-      const Codes<KW> x = next;
-      const int page = next_page;
-      const int tn = t + kAtWarps;
-      if (tn < last) {
-        if (++turn == 32) {
-          turn = 0;
-          look(tn);
-        }
-        next_page = __shfl_sync(0xffffffffu, ahead, turn);
-        if (next_page >= 0)
-          load_codes<D>(next, p.cache + ((long long)next_page * p.H + h) * block_bytes, (tn % page_tiles) * 16, p.page, g, c);
-      }
-      if (page < 0) continue;
-
-      // scores: q . n for 16 tokens
-      float z[MT][2][4];
+    auto group = [&](auto masked_group, int token0, uint32_t subs, uint32_t from) {
+      constexpr bool kMasked = decltype(masked_group)::value;
+      // scores: q . n for 32 tokens, four groups of eight
+      float z[MT][4][4];
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < 4; ++j)
 #pragma unroll
           for (int e = 0; e < 4; ++e) z[m][j][e] = 0.f;
+      {
+        uint32_t kw[4][KW];
 #pragma unroll
-      for (int w = 0; w < KW; ++w)
+        for (int j = 0; j < 4; ++j)
+          shared_words(kw[j], from + (j >> 1) * 2 * Stage<D>::kCodes + (8 * (j & 1) + g) * (D / 2) + c * (D / 8));
 #pragma unroll
-        for (int half = 0; half < 2; ++half)
+        for (int w = 0; w < KW; ++w)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const uint32_t k = x.k[j][w] >> (8 * half);
+          for (int half = 0; half < 2; ++half) {
+            uint32_t qf[MT][4];
 #pragma unroll
-            for (int m = 0; m < MT; ++m) mma16816(z[m][j], qf[m][2 * w + half], k & 0x000f000fu, k & 0x00f000f0u);
+            for (int m = 0; m < MT; ++m) shared_words(qf[m], q_at + (m * 2 * KW + 2 * w + half) * 512);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t k = kw[j][w] >> (8 * half);
+#pragma unroll
+              for (int m = 0; m < MT; ++m) mma16816(z[m][j], qf[m], k & 0x000f000fu, k & 0x00f000f0u);
+            }
           }
-
-      // the four tokens' numbers: [j][which of the two]
-      float ks[2][2], ko[2][2], vs[2][2], vo[2][2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        ks[j][0] = Kv<T>::lo(x.n[j].x);
-        ko[j][0] = Kv<T>::hi(x.n[j].x);
-        vs[j][0] = Kv<T>::lo(x.n[j].y);
-        vo[j][0] = Kv<T>::hi(x.n[j].y);
-        ks[j][1] = Kv<T>::lo(x.n[j].z);
-        ko[j][1] = Kv<T>::hi(x.n[j].z);
-        vs[j][1] = Kv<T>::lo(x.n[j].w);
-        vo[j][1] = Kv<T>::hi(x.n[j].w);
       }
-      const bool masked = t * 16 + 16 > every;
-      if (masked) {
-        // numbers of tokens that nobody sees may be anything
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-            if (t * 16 + 8 * j + 2 * c + e >= s.seen) ks[j][e] = ko[j][e] = vs[j][e] = vo[j][e] = 0.f;
-      }
+      // the numbers of the two tokens of each group of eight
+      uint32_t nv[4][2];
       float most = -FLT_MAX, largest = 0.f;
+      const int t0 = token0 + 2 * c;
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int j = 0; j < 4; ++j) {
+        uint32_t nw[4];
+        shared_words(nw, from + Stage<D>::kNumbers + (8 * j + 2 * c) * 8);
+        if (kMasked) {
+          // those of tokens that nobody sees may be anything
+          const bool sub = subs >> (j >> 1) & 1;
+          if (!sub || t0 + 8 * j >= s.seen) nw[0] = nw[1] = 0;
+          if (!sub || t0 + 8 * j + 1 >= s.seen) nw[2] = nw[3] = 0;
+        }
+        const Two scale2 = two(row_scale, row_scale);
+        const Two ks = mul2(two(Kv<T>::lo(nw[0]), Kv<T>::lo(nw[2])), scale2);
+        const Two ko = mul2(two(Kv<T>::hi(nw[0]), Kv<T>::hi(nw[2])), scale2);
+        nv[j][0] = nw[1];
+        nv[j][1] = nw[3];
+        largest = max3(largest, Kv<T>::lo(nw[1]), Kv<T>::lo(nw[3]));
 #pragma unroll
-        for (int e = 0; e < 2; ++e) largest = fmaxf(largest, vs[j][e]);
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float y = fmaf(z[m][j][e], ks[j][e & 1], ko[j][e & 1] * q_sum[m][e >> 1]);
-            if (masked && t * 16 + 8 * j + 2 * c + (e & 1) > limit[m][e >> 1]) y = __int_as_float(0xff800000);
-            z[m][j][e] = y;
-            most = fmaxf(most, fmaf(y, row_scale[m][e >> 1], -ref[m][e >> 1]));
+          for (int r = 0; r < 2; ++r) {
+            float y0, y1;
+            split(fma2(two(z[m][j][2 * r], z[m][j][2 * r + 1]), ks, fma2(ko, q_sum[m][r], two(-ref[m][r], -ref[m][r]))), y0, y1);
+            if (kMasked) {
+              const int lim = subs >> (j >> 1) & 1 ? limits[m * 16 + 8 * r + g] : -1;
+              if (t0 + 8 * j > lim) y0 = __int_as_float(0xff800000);
+              if (t0 + 8 * j + 1 > lim) y1 = __int_as_float(0xff800000);
+            }
+            z[m][j][2 * r] = y0;
+            z[m][j][2 * r + 1] = y1;
+            most = max3(most, y0, y1);
           }
-      if (__any_sync(0xffffffffu, most > kAtSlack || largest * value_scale > kAtValueTop)) {
+      }
+      if (fresh || __any_sync(0xffffffffu, most > kAtSlack || largest * value_scale > kAtValueTop)) {
         // a row's terms outgrow its reference, or the values' scales theirs
         largest = fmaxf(largest, __shfl_xor_sync(0xffffffffu, largest, 1));
         largest = fmaxf(largest, __shfl_xor_sync(0xffffffffu, largest, 2));
@@ -360,101 +506,135 @@ __global__ void __launch_bounds__(kAtThreads, MT == 1 ? 3 : 2) attend_kernel(con
         if (largest * value_scale > kAtValueTop) {
           // largest < 2^(e - 126): 2^(133 - e) brings it below 2^7
           const int e = (int)(__float_as_uint(largest) >> 23);
-          const float to = __uint_as_float((uint32_t)min(max(133 - e + 127, 1), 253) << 23);
-          by = to / value_scale;
-          value_scale = to;
+          const float to_scale = __uint_as_float((uint32_t)min(max(133 - e + 127, 1), 253) << 23);
+          by = to_scale / value_scale;
+          value_scale = to_scale;
         }
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float top = fmaxf(fmaxf(z[m][0][2 * e], z[m][0][2 * e + 1]), fmaxf(z[m][1][2 * e], z[m][1][2 * e + 1]));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const float now = fmaxf(ref[m][e], top * row_scale[m][e]);
-            const float f = ex2_approx(ref[m][e] - now);
-            ref[m][e] = now;
-            mass[m][e] *= f;
-            shift[m][e] *= f;
-            const float fv = f * by;
+          for (int r = 0; r < 2; ++r) {
+            float up = __int_as_float(0xff800000);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) up = max3(up, z[m][j][2 * r], z[m][j][2 * r + 1]);
+            up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 1));
+            up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 2));
+            up = fresh ? (up == __int_as_float(0xff800000) ? 0.f : up) : fmaxf(up, 0.f);
+            ref[m][r] += up;
+            const float f = fresh ? 0.f : ex2_approx(-up), fv = f * by;
+            mass[m][r] = mul2(mass[m][r], two(f, f));
+            shift[m][r] = mul2(shift[m][r], two(f, f));
 #pragma unroll
             for (int n = 0; n < 4 * KW; ++n) {
-              o[m][n][2 * e] *= fv;
-              o[m][n][2 * e + 1] *= fv;
+              o[m][n][2 * r] *= fv;
+              o[m][n][2 * r + 1] *= fv;
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              z[m][j][2 * r] -= up;
+              z[m][j][2 * r + 1] -= up;
+            }
+          }
+        fresh = false;
+      }
+
+      // weights and sums, 16 tokens at a time: their first eight as codes n,
+      // the others as n - 15
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        uint32_t vw[2][KW];
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          shared_words(vw[j], from + (2 * i + 1) * Stage<D>::kCodes + (4 * j + c) * D + g * (D / 8));
+        uint32_t pf[MT][4];
+        [[maybe_unused]] uint32_t pl[MT][4];
+#pragma unroll
+        for (int jj = 0; jj < 2; ++jj) {
+          const int j = 2 * i + jj;
+          const Two vs = two(Kv<T>::lo(nv[j][0]), Kv<T>::lo(nv[j][1]));
+          Two vo = two(Kv<T>::hi(nv[j][0]), Kv<T>::hi(nv[j][1]));
+          if (jj) vo = fma2(vs, two(15.f, 15.f), vo);
+          const Two vn = mul2(vs, two(value_scale, value_scale));
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const Two w = two(ex2_approx(z[m][j][2 * r]), ex2_approx(z[m][j][2 * r + 1]));
+              mass[m][r] = add2(mass[m][r], w);
+              float a0, a1;
+              split(mul2(w, vn), a0, a1);
+              if (kMasked) {
+                // (a hidden token's numbers may be NaN)
+                const int lim = subs >> i & 1 ? limits[m * 16 + 8 * r + g] : -1;
+                float f0, f1;
+                split(mul2(w, vo), f0, f1);
+                if (t0 + 8 * j > lim) a0 = f0 = 0.f;
+                if (t0 + 8 * j + 1 > lim) a1 = f1 = 0.f;
+                shift[m][r] = add2(shift[m][r], two(f0, f1));
+              } else {
+                shift[m][r] = fma2(w, vo, shift[m][r]);
+              }
+              pf[m][2 * jj + r] = half2_bits(a0, a1);
+              if constexpr (kFine) {
+                // a float16 result wants more than float16 weights: their rest
+                const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&pf[m][2 * jj + r]));
+                pl[m][2 * jj + r] = half2_bits(a0 - back.x, a1 - back.y);
+              }
+            }
+        }
+#pragma unroll
+        for (int w = 0; w < KW; ++w)
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const uint32_t v0 = vw[0][w] >> (8 * half), v1 = vw[1][w] >> (8 * half);
+            const uint32_t b00 = v0 & 0x000f000fu, b01 = (v1 & 0x000f000fu) ^ 0x800f800fu;
+            const uint32_t b10 = v0 & 0x00f000f0u, b11 = (v1 & 0x00f000f0u) ^ 0x80f080f0u;
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+              mma16816(o[m][4 * w + 2 * half], pf[m], b00, b01);
+              mma16816(o[m][4 * w + 2 * half + 1], pf[m], b10, b11);
+              if constexpr (kFine) {
+                mma16816(o[m][4 * w + 2 * half], pl[m], b00, b01);
+                mma16816(o[m][4 * w + 2 * half + 1], pl[m], b10, b11);
+              }
             }
           }
       }
-      float vn[2][2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) vn[j][e] = vs[j][e] * value_scale;
+    };
 
-      // weights, as the second product's left operand
-      uint32_t pf[MT][4];
-      uint32_t pl[MT][4];
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            float a[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float y = z[m][j][2 * r + e];
-              const float w = ex2_approx(fmaf(y, row_scale[m][r], -ref[m][r]));
-              mass[m][r] += w;
-              if (masked) {
-                const bool sees = t * 16 + 8 * j + 2 * c + e <= limit[m][r];
-                shift[m][r] += sees ? w * vo[j][e] : 0.f;
-                a[e] = sees ? w * vn[j][e] : 0.f;
-              } else {
-                shift[m][r] = fmaf(w, vo[j][e], shift[m][r]);
-                a[e] = w * vn[j][e];
-              }
-            }
-            pf[m][2 * j + r] = half2_bits(a[0], a[1]);
-            if constexpr (std::is_same<T, __half>::value) {
-              // a float16 result wants more than float16 weights: their rest
-              const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&pf[m][2 * j + r]));
-              pl[m][2 * j + r] = half2_bits(a[0] - back.x, a[1] - back.y);
-            }
-          }
-
-      // sums over the 16 tokens, eight channels at a time
-#pragma unroll
-      for (int w = 0; w < KW; ++w)
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const uint32_t v0 = x.v[0][w] >> (8 * half), v1 = x.v[1][w] >> (8 * half);
-#pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            mma16816(o[m][4 * w + 2 * half], pf[m], v0 & 0x000f000fu, v1 & 0x000f000fu);
-            mma16816(o[m][4 * w + 2 * half + 1], pf[m], v0 & 0x00f000f0u, v1 & 0x00f000f0u);
-            if constexpr (std::is_same<T, __half>::value) {
-              mma16816(o[m][4 * w + 2 * half], pl[m], v0 & 0x000f000fu, v1 & 0x000f000fu);
-              mma16816(o[m][4 * w + 2 * half + 1], pl[m], v0 & 0x00f000f0u, v1 & 0x00f000f0u);
-            }
-          }
-        }
+    uint32_t from = ring;
+    for (int n = 0; n < groups; ++n) {
+      copies_wait<kAtStages - 2>();
+      __syncwarp();                       // every lane's copies are there, and everybody is done with the group before
+      const uint32_t subs = there >> (2 * (n & 7)) & 3u;
+      copy_group(n + kAtStages - 1);
+      const int token0 = 32 * (first + kWarps * n);
+      if (subs == 3u && token0 + 32 <= s.first) group(std::false_type{}, token0, subs, from);
+      else if (subs) group(std::true_type{}, token0, subs, from);
+      from = from == ring + (kAtStages - 1) * Stage<D>::kBytes ? ring : from + Stage<D>::kBytes;
     }
+    copies_wait<0>();
+    __syncwarp();
 
     // ---- the warps' sums side by side in shared memory
-    float* sums = at_sm + warp * (TR * D + 2 * TR);
+    float* sums = all_sums + warp * kWarpFloats;
     const float down = 1.f / value_scale;
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int r = m * 16 + e * 8 + g;
-        float l = mass[m][e], f = shift[m][e];
+        float l, f, l1, f1;
+        split(mass[m][e], l, l1);
+        split(shift[m][e], f, f1);
+        l += l1;
+        f += f1;
         l += __shfl_xor_sync(0xffffffffu, l, 1);
         f += __shfl_xor_sync(0xffffffffu, f, 1);
         l += __shfl_xor_sync(0xffffffffu, l, 2);
         f += __shfl_xor_sync(0xffffffffu, f, 2);
         if (c == 0) {
-          sums[TR * D + r] = ref[m][e];
+          sums[TR * D + r] = l == 0.f ? -FLT_MAX : ref[m][e];
           sums[TR * D + TR + r] = l;
         }
 #pragma unroll
@@ -472,19 +652,24 @@ __global__ void __launch_bounds__(kAtThreads, MT == 1 ? 3 : 2) attend_kernel(con
     __syncthreads();
     const bool whole = chunk0 == 0 && chunks == s.chunks;
     float* part = p.part + (size_t)(2 * me + (chunk0 == 0)) * part_floats(TR, D);
-    for (int x = tid; x < TR * (D / 4); x += kAtThreads) {
+#pragma unroll
+    for (int x0 = 0; x0 < TR * (D / 4); x0 += kThreads) {
+      const int x = x0 + tid;
+      if (TR * (D / 4) % kThreads != 0 && x >= TR * (D / 4)) break;
       const int r = x / (D / 4), dg = x % (D / 4), at_r = r * (D / 4) + swizzled(r, dg);
+      const long long q_row = out_rows[r];
+      if (q_row < 0) continue;
       float top = -FLT_MAX;
 #pragma unroll
-      for (int w = 0; w < kAtWarps; ++w) {
-        const float m = at_sm[w * (TR * D + 2 * TR) + TR * D + r];
+      for (int w = 0; w < kWarps; ++w) {
+        const float m = all_sums[w * kWarpFloats + TR * D + r];
         top = m > top || m != m ? m : top;
       }
       float l = 0.f;
       float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < kAtWarps; ++w) {
-        const float* sw = at_sm + w * (TR * D + 2 * TR);
+      for (int w = 0; w < kWarps; ++w) {
+        const float* sw = all_sums + w * kWarpFloats;
         const float f = ex2_approx(sw[TR * D + r] - top);
         const float4 a = reinterpret_cast<const float4*>(sw)[at_r];
         l = fmaf(f, sw[TR * D + TR + r], l);
@@ -499,61 +684,73 @@ __global__ void __launch_bounds__(kAtThreads, MT == 1 ? 3 : 2) attend_kernel(con
           part[TR * D + r] = top;
           part[TR * D + TR + r] = l;
         }
-        continue;
+      } else {
+        finish_row<T, D>(p, q_row, dg, y, top, l);
       }
-      const int rr = rt * TR + r, i = rr / p.G;
-      if (i >= s.rows) continue;
-      const long long q_row = ((long long)b * p.rows + i) * p.H * p.G + (long long)h * p.G + (rr - i * p.G);
-      const float over = l == 0.f ? 0.f : 1.f / l;
-      reinterpret_cast<uint2*>(p.out)[q_row * (D / 4) + dg] =
-          make_uint2(Kv<T>::pack(y.x * over, y.y * over), Kv<T>::pack(y.z * over, y.w * over));
-      if (p.lse && dg == 0) p.lse[q_row] = l == 0.f ? __int_as_float(0xff800000) : (top + log2f(l)) * 6.931471805599453e-01f;
     }
     __syncthreads();
-    if (!whole && chunk0 == 0 && tid == 0) {
-      // the segment's last unit is CTA ((x + 1) W - 1) / U's
-      const long long x = base + (long long)at * s.chunks + s.chunks - 1;
-      p.desc[me] = make_int4(b, h, rt, (int)(((x + 1) * W - 1) / U));
-    }
+    if (!whole && chunk0 == 0 && tid == 0)
+      p.desc[me] = make_int4(b, h, rt, line.owner(base + (long long)segment.at * s.chunks + s.chunks - 1));
     u += chunks;
   }
 }
 
 // Joins the parts of the segment that begins in CTA blockIdx.x's range and
 // ends behind it: its own second part, then the first parts of those behind.
-template <typename T, int D, int TR>
-__global__ void __launch_bounds__(kAtJoinThreads) attend_join_kernel(const __grid_constant__ AttendParams p) {
+// A warp has a row; a lane four channels, and the reference and the mass of
+// one of 32 parts at a time.
+template <typename T, int D>
+__global__ void __launch_bounds__(kAtJoinThreads) attend_join_kernel(const __grid_constant__ AttendParams p, const int TR) {
   pdl_wait();
-  const int4 d = p.desc[blockIdx.x];
+  const int own = blockIdx.x, lane = threadIdx.x & 31;
+  const int r = blockIdx.y * (kAtJoinThreads / 32) + (threadIdx.x >> 5);
+  const int4 d = p.desc[own];
   if (d.x < 0) return;
-  const int b = d.x, h = d.y, rt = d.z, last = d.w;
-  const Sequence s(p, b, TR);
-  for (int x = blockIdx.y * kAtJoinThreads + threadIdx.x; x < TR * (D / 4); x += gridDim.y * kAtJoinThreads) {
-    const int r = x / (D / 4), dg = x % (D / 4), rr = rt * TR + r, i = rr / p.G;
-    if (i >= s.rows) continue;
-    float top = -FLT_MAX;
-    for (int a = blockIdx.x; a <= last; ++a) {
-      const float m = p.part[(size_t)(2 * a + (a == (int)blockIdx.x)) * part_floats(TR, D) + TR * D + r];
-      top = m > top || m != m ? m : top;
+  const int b = d.x, h = d.y, rt = d.z, count = d.w - own + 1;
+  const int rows = p.gamma_b ? min(max(p.gamma_b[b], -1), p.rows - 1) + 1 : p.rows;
+  const int rr = rt * TR + r, i = rr / p.G;
+  if (i >= rows) return;
+  const int floats = part_floats(TR, D);
+  float top = -FLT_MAX, l = 0.f;
+  float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int a0 = 0; a0 < count; a0 += 32) {
+    const int a = a0 + lane, n = min(count - a0, 32);
+    float m = -FLT_MAX, mass = 0.f;
+    if (a < count) {
+      const float* part = p.part + (size_t)(2 * (own + a) + (a == 0)) * floats + TR * D + r;
+      m = part[0];
+      mass = part[TR];
     }
-    float l = 0.f;
-    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int a = blockIdx.x; a <= last; ++a) {
-      const float* part = p.part + (size_t)(2 * a + (a == (int)blockIdx.x)) * part_floats(TR, D);
-      const float f = ex2_approx(part[TR * D + r] - top);
-      const float4 v = reinterpret_cast<const float4*>(part)[x];
-      l = fmaf(f, part[TR * D + TR + r], l);
-      y.x = fmaf(f, v.x, y.x);
-      y.y = fmaf(f, v.y, y.y);
-      y.z = fmaf(f, v.z, y.z);
-      y.w = fmaf(f, v.w, y.w);
+    float now = m;
+    bool bad = m != m;
+#pragma unroll
+    for (int x = 16; x >= 1; x >>= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, x));
+    now = fmaxf(now, top);
+    if (__any_sync(0xffffffffu, bad)) now = __int_as_float(0x7fffffff);
+    const float f = ex2_approx(m - now), back = ex2_approx(top - now);
+    top = now;
+    float sum = f * mass;
+#pragma unroll
+    for (int x = 16; x >= 1; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+    l = fmaf(l, back, sum);
+    y.x *= back;
+    y.y *= back;
+    y.z *= back;
+    y.w *= back;
+#pragma unroll 8
+    for (int k = 0; k < n; ++k) {
+      const float g = __shfl_sync(0xffffffffu, f, k);
+      if (lane < D / 4) {
+        const float4 v = reinterpret_cast<const float4*>(p.part + (size_t)(2 * (own + a0 + k) + (a0 + k == 0)) * floats)[r * (D / 4) + lane];
+        y.x = fmaf(g, v.x, y.x);
+        y.y = fmaf(g, v.y, y.y);
+        y.z = fmaf(g, v.z, y.z);
+        y.w = fmaf(g, v.w, y.w);
+      }
     }
-    const long long q_row = ((long long)b * p.rows + i) * p.H * p.G + (long long)h * p.G + (rr - i * p.G);
-    const float over = l == 0.f ? 0.f : 1.f / l;
-    reinterpret_cast<uint2*>(p.out)[q_row * (D / 4) + dg] =
-        make_uint2(Kv<T>::pack(y.x * over, y.y * over), Kv<T>::pack(y.z * over, y.w * over));
-    if (p.lse && dg == 0) p.lse[q_row] = l == 0.f ? __int_as_float(0xff800000) : (top + log2f(l)) * 6.931471805599453e-01f;
   }
+  if (lane < D / 4)
+    finish_row<T, D>(p, ((long long)b * p.rows + i) * p.H * p.G + (long long)h * p.G + (rr - i * p.G), lane, y, top, l);
 }
 
 }  // namespace cache

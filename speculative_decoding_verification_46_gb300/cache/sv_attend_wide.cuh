@@ -1,0 +1,735 @@
+// Attention of many rows over the 4-bit cache: both contractions on the fifth
+// generation tensor cores, with the codes as the operand in tensor memory.
+//
+// With R rows of a sequence and head (gamma + 1 times the query heads of a
+// group), 128 tokens are one step:
+//   scores^T [128 tokens x R] = codes of the keys [128 x D] . q^T
+//   sums^T   [D x R]         += (codes of the values)^T [D x 128] . weights^T
+// The codes are the left operand, so the tensor cores' time grows with R (a
+// multiple of 16), not with a padded tile, and the codes go from registers to
+// tensor memory: shared memory could not take them in and give them out again
+// at this rate.  q and the weights, the small sides, are in shared memory.
+// The formulas are those of sv_attend.cuh.  A tensor core cuts off what lies
+// below its sum's last bits, so sums of n >= 0 would lose more and more over a
+// long sequence: half of the tokens are taken as n - 15 (the sign bit and the
+// complement, in the same AND and XOR), and their offset as o' + 15 s'.
+//
+// Eight warps do everything in turn, two CTAs per SM fill each other's waits.
+// A step: (1) key codes to tensor memory; barrier, first product; (2) value
+// codes to tensor memory meanwhile; (3) the scores' softmax against a
+// reference per row, weights to shared memory; barrier, second product, which
+// the next step's (1) does not wait for.  Where a term outgrows its row's
+// reference by 2^8 (a segment's first step, hardly ever later) the barrier
+// says so to all, and the step's weights are formed again.
+//
+// Tensor memory, 256 columns a CTA: key codes, value codes, scores, sums.  With
+// R = 80 and D = 128 the second half of the value codes takes the place of key
+// codes that the first product has read.
+#pragma once
+
+#include "sv_attend.cuh"
+
+namespace sv {
+namespace cache {
+
+constexpr int kWdThreads = 288;      // eight warps that form operands and weights, one that issues the products
+constexpr int kWdWorkers = 256;
+constexpr int kWdUnit = 128;         // tokens of a step
+constexpr int kWdColumns = 256;      // of tensor memory
+constexpr int kWdMostRows = 80;
+constexpr int kWdPatience = 1 << 14; // tries of a wait, of up to 0.1 ms each
+
+// ------------------------------------------------------------ tensor memory
+
+__device__ __forceinline__ void tm_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tm_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tm_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// 16 lanes: register 2 n + e of thread (g, c) goes to lane 8 e + g, column 4 n + c
+__device__ __forceinline__ void tm_store_16x128(uint32_t at, const uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+      "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(at),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
+      "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]),
+      "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]),
+      "r"(v[31])
+      : "memory");
+}
+__device__ __forceinline__ void tm_store_16x128(uint32_t at, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
+      "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+// 16 lanes, 8 columns: thread (g, c) gets columns 2 c, 2 c + 1 of lane g, then of lane 8 + g
+__device__ __forceinline__ void tm_load_16x256(float (&v)[4], uint32_t at) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]) : "r"(at));
+}
+// 32 lanes, 8 columns: a thread has its lane's
+__device__ __forceinline__ void tm_load_32x8(float (&v)[8], uint32_t at) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]) : "r"(at));
+}
+__device__ __forceinline__ void tm_store_32x8(uint32_t at, const float (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+               "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]) : "memory");
+}
+// d [128 x N] (+)= a [128 x 16] . b [N x 16]^T, float16 in, float32 sums
+__device__ __forceinline__ void tm_mma(uint32_t d, uint32_t a, uint64_t b, uint32_t kind, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(kind), "r"((uint32_t)add)
+      : "memory");
+}
+__device__ __forceinline__ void tm_commit(uint32_t barrier) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(barrier) : "memory");
+}
+// A K-major operand in shared memory: rows of 128 bytes, 16-byte pieces
+// exchanged by the row's number (the 128-byte swizzle), eight rows each 1 KB.
+__device__ __forceinline__ uint64_t smem_operand(uint32_t at) {
+  return (uint64_t)(at >> 4 & 0x3fff) | 1ull << 16 | 64ull << 32 | 1ull << 46 | 2ull << 61;
+}
+
+// A wait that ends: where the phase does not come, *gave_up is set for the
+// whole CTA, whose later waits are short and whose rows become NaN.
+__device__ __forceinline__ void wait_phase(uint32_t barrier, uint32_t parity, volatile int* gave_up) {
+  uint32_t done = 0;
+#pragma unroll 1
+  for (int i = 0; i < kWdPatience && !done; ++i) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done) : "r"(barrier), "r"(parity), "r"(100000u) : "memory");
+    if (!done && i >= 64 && *gave_up) break;
+  }
+  if (!done) *gave_up = 1;
+  __syncwarp();
+}
+
+// The transposes of four 8 x 8 matrices of 16-bit elements: matrix i's row j
+// goes to the address that lane 8 i + j gives.
+__device__ __forceinline__ void store_transposed(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+
+// The eight workers meet; with `any`, they learn whether one of them says so.
+__device__ __forceinline__ void workers_meet() { asm volatile("barrier.cta.sync 1, %0;" ::"n"(kWdWorkers) : "memory"); }
+__device__ __forceinline__ bool workers_any(bool any) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r) : "r"((uint32_t)any), "n"(kWdWorkers) : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void arrive(uint32_t barrier) {
+  asm volatile("mbarrier.arrive.shared.b64 _, [%0];" ::"r"(barrier) : "memory");
+}
+// NG: R / 16; each half of the warps (a warpgroup) has the softmax of NG
+// groups of eight rows.
+template <typename T, int D, int NG>
+struct WideShape {
+  static constexpr int R = 16 * NG;
+  static constexpr bool kFine = std::is_same<T, __half>::value;   // the weights' rest is an operand too
+  // a step in the ring: eight groups of 16 tokens (subs), their keys, their
+  // values and their numbers; the padding sends subs to different banks
+  static constexpr int kSubKeys = 8 * D, kSubValues = 8 * D + 16, kSubNumbers = 128 + 16;
+  static constexpr int oValues = 8 * kSubKeys, oNumbers = oValues + 8 * kSubValues, kStage = oNumbers + 8 * kSubNumbers;
+  static constexpr int kQ = R * D * 2, kP = R * kWdUnit * 2;
+  // steps in the ring: two CTAs have 227 KB of shared memory together
+  static constexpr int kStages = kFine && R == 80 && D == 128 ? 2 : 3;
+  static constexpr int oP = kQ, oRing = oP + (kFine ? 2 : 1) * kP, oSmall = oRing + kStages * kStage;
+  // floats: row pairs' sums of q and references [4 R / 2], factor, tops [4], masses [4], shifts [4]; ints: limits
+  static constexpr int kSmall = R * 16 * 4;
+  static constexpr int kSmem = oSmall + kSmall + 1024;            // (aligned to 1 KB in the kernel)
+  static constexpr bool kTight = D / 2 + 64 + 2 * R > kWdColumns;
+  static constexpr int cV = D / 2, cS = kTight ? D / 2 + 32 : D / 2 + 64, cO = cS + R;
+  static_assert(cO + R <= kWdColumns, "tensor memory");
+  static_assert(R <= kWdMostRows, "rows");
+  static_assert(2 * (kSmem + 2048) <= 228 * 1024, "two CTAs an SM");
+};
+
+template <typename T, int D, int NG>
+__global__ void __launch_bounds__(kWdThreads, 2) attend_wide_kernel(const __grid_constant__ AttendParams p) {
+  using S = WideShape<T, D, NG>;
+  constexpr int R = S::R, KW = D / 32, RH = 8 * NG;
+  extern __shared__ unsigned char wd_raw[];
+  __shared__ uint32_t tm_base;
+  __shared__ __align__(8) unsigned long long bars[4];
+  __shared__ int gave_up_flag;
+  __shared__ float warp_top[8];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, w = warp & 3, wg = warp >> 2, g = lane >> 2, c = lane & 3;
+  const uint32_t sm0 = (uint32_t)__cvta_generic_to_shared(wd_raw), sm = (sm0 + 1023u) & ~1023u;
+  unsigned char* const sp = wd_raw + (sm - sm0);
+  float4* const pairs = reinterpret_cast<float4*>(sp + S::oSmall);   // rows 2 i, 2 i + 1: sums of q, references below 0
+  float* const factor = reinterpret_cast<float*>(pairs) + 2 * R;
+  float* const tops = factor + R;
+  float* const masses = tops + 4 * R;
+  float* const shifts = masses + 4 * R;
+  int* const limits = reinterpret_cast<int*>(shifts + 4 * R);
+  volatile int* const gave_up = &gave_up_flag;
+  // scores there, sums there, key codes there, weights there
+  const uint32_t bar_s = (uint32_t)__cvta_generic_to_shared(&bars[0]), bar_o = bar_s + 8, bar_k = bar_s + 16, bar_p = bar_s + 24;
+  pdl_launch_dependents();
+
+  fill_behind<T, D, kWdThreads>(p);
+  const Part line = find_part(p, R, kWdUnit);
+  if (!line.some()) return;
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"((uint32_t)__cvta_generic_to_shared(&tm_base)),
+                 "n"(kWdColumns) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  if (tid == 0) {
+    gave_up_flag = 0;
+    for (int i = 0; i < 4; ++i)
+      asm volatile("mbarrier.init.shared.b64 [%0], %1;" ::"r"(bar_s + 8 * i), "r"(i == 2 ? 8 : 1) : "memory");
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  tm_fence_before();
+  __syncthreads();
+  tm_fence_after();
+  const uint32_t tm = tm_base, tm_w = tm + ((uint32_t)(32 * w) << 16);
+  const uint32_t kind = 1u << 4 | (uint32_t)(R >> 3) << 17 | (128u >> 4) << 24;
+  uint32_t phase_s = 0, phase_o = 0;     // of the next wait
+  int slot = 0, slot_to = 0;             // of the ring: the step's, the next to fill
+  const uint64_t q_operand = smem_operand(sm), p_operand = smem_operand(sm + S::oP);
+
+  if (warp == kWdWorkers / 32) {
+    // ---- this warp issues the products (an issue waits for those before it),
+    // step by step over the same segments
+    uint32_t phase = 0;
+    long long u = line.u, base = line.base;
+    int b = line.b;
+    while (u < line.end) {
+      const Sequence s(p, b, R, kWdUnit);
+      const long long n_units = s.units(p.H);
+      if (u >= base + n_units) {
+        base += n_units;
+        ++b;
+        continue;
+      }
+      const int chunks = Segment(s, u, base, line.end).chunks;
+      for (int n = 0; n < chunks; ++n, phase ^= 1) {
+        wait_phase(bar_k, phase, gave_up);
+        if (lane == 0) {
+          tm_fence_after();
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+            tm_mma(tm + S::cS, tm + 8 * k, q_operand + (uint64_t)((k >> 2) * (R * 8) + (k & 3) * 2), kind, k > 0);
+          tm_commit(bar_s);
+        }
+        __syncwarp();
+        wait_phase(bar_p, phase, gave_up);
+        if (lane == 0) {
+          tm_fence_after();
+#pragma unroll
+          for (int k = 0; k < kWdUnit / 16; ++k) {
+            const uint32_t a = tm + (S::kTight && k >= 4 ? 8 * (k - 4) : S::cV + 8 * k);
+            const uint64_t at_p = p_operand + (uint64_t)((k >> 2) * (R * 8) + (k & 3) * 2);
+            tm_mma(tm + S::cO, a, at_p, kind, n > 0 || k > 0);
+            if (S::kFine) tm_mma(tm + S::cO, a, at_p + S::kP / 16, kind, true);
+          }
+          tm_commit(bar_o);
+        }
+        __syncwarp();
+      }
+      u += chunks;
+    }
+    return;
+  }
+
+  const long long block_bytes = (long long)p.page * kTokenBytes<D>;
+  const int page_tiles = p.page / 16, me = blockIdx.x;
+  long long u = line.u, base = line.base;
+  int b = line.b;
+
+  while (u < line.end) {
+    const Sequence s(p, b, R, kWdUnit);
+    const long long n_units = s.units(p.H);
+    if (u >= base + n_units) {
+      base += n_units;
+      ++b;
+      continue;
+    }
+    const Segment segment(s, u, base, line.end);
+    const int h = segment.h, rt = segment.rt, chunk0 = segment.chunk0, chunks = segment.chunks;
+    const int sub_end = (s.seen + 15) / 16;
+
+    // ---- the ring: warp i copies sub i of a step.  A lane knows where one of
+    // the next 32 subs begins, its number in the page in the low four bits
+    // (0: hidden); the 32 behind them are looked up ahead of time.
+    auto look = [&](int sub0) {
+      const int mine = sub0 + lane;
+      unsigned long long r = 0;
+      if (mine < sub_end) {
+        const int n = mine / page_tiles, id = __ldg(p.table + (long long)b * p.N + n);
+        if (id >= 0 && id < p.pages) {
+          const int sub = mine - n * page_tiles;
+          r = reinterpret_cast<unsigned long long>(p.cache) + (unsigned long long)(((long long)id * p.H + h) * block_bytes + sub * (8 * D) + sub);
+        }
+      }
+      return r;
+    };
+    unsigned long long ahead = look(chunk0 * 8), later = look(chunk0 * 8 + 32);
+    uint32_t next_subs = 0;              // which of the 32 are there
+    uint32_t seen_subs = 0;              // byte n % 4: which subs of step n are there
+    auto copy_step = [&](int n) {
+      if (n < chunks) {
+        const int turn = (n & 3) * 8;
+        if (turn == 0) {
+          if (n > 0) {
+            ahead = later;
+            later = look((chunk0 + n) * 8 + 32);
+          }
+          next_subs = __ballot_sync(0xffffffffu, ahead != 0);
+        }
+        seen_subs = (seen_subs & ~(0xffu << turn)) | (next_subs & 0xffu << turn);
+        const unsigned long long from = __shfl_sync(0xffffffffu, ahead, turn + warp);
+        if (from != 0) {
+          const int sub = (int)(from & 15);
+          const unsigned char* codes = reinterpret_cast<const unsigned char*>(from - sub) + lane * 16;
+          const uint32_t to = sm + S::oRing + slot_to * S::kStage + lane * 16;
+#pragma unroll
+          for (int j = 0; j < D / 64; ++j) {
+            copy_ahead<16>(to + warp * S::kSubKeys + j * 512, codes + j * 512);
+            copy_ahead<16>(to + S::oValues + warp * S::kSubValues + j * 512, codes + p.page * (D / 2) + j * 512);
+          }
+          if (lane < 8) copy_ahead<16>(to + S::oNumbers + warp * S::kSubNumbers, codes + p.page * D - sub * (8 * D - 128));
+        }
+        slot_to = slot_to + 1 == S::kStages ? 0 : slot_to + 1;
+      }
+      copies_end_group();
+    };
+#pragma unroll
+    for (int n = 0; n < S::kStages; ++n) copy_step(n);
+
+    // ---- q: float16 with one power of two for the tile (a row whose largest
+    // element is 2^-20 of the tile's still has its scores to 2^-17 of their
+    // size), channels in the order in which the key codes come: element
+    // 2 (c + 4 (4 k + i)) + e is channel 8 (KW c + k) + i + 4 e, halves e of
+    // pair i of word k
+    float raise, row_scale;
+    {
+      constexpr int LANES = D / 8;
+      float top = 0.f;
+      for (int x = tid; x < R * LANES; x += kWdWorkers) {
+        const int r = rt * R + x / LANES, i = r / p.G;
+        if (i < s.rows) {
+          const T* row = static_cast<const T*>(p.q) + b * p.qs[0] + i * p.qs[1] + (long long)(h * p.G + r - i * p.G) * p.qs[2];
+          const uint4 v = __ldg(reinterpret_cast<const uint4*>(row) + x % LANES);
+          const uint32_t ww[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) top = fmaxf(top, fmaxf(fabsf(Kv<T>::lo(ww[j])), fabsf(Kv<T>::hi(ww[j]))));
+        }
+      }
+#pragma unroll
+      for (int m = 16; m >= 1; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
+      if (lane == 0) warp_top[warp] = top;
+      if (tid < R) {
+        const int i = (rt * R + tid) / p.G;
+        limits[tid] = i < s.rows ? min(s.first - 1 + i, s.seen - 1) : -1;
+      }
+      workers_meet();
+#pragma unroll
+      for (int j = 0; j < 8; ++j) top = fmaxf(top, warp_top[j]);
+      const int up = top > 0.f ? min(140 - (int)(__float_as_uint(top) >> 23), 126) : 0;
+      raise = __uint_as_float((uint32_t)(up + 127) << 23);
+      row_scale = p.scale * 0x1p24f * __uint_as_float((uint32_t)(127 - up) << 23);
+      for (int x = tid; x < R * LANES; x += kWdWorkers) {
+        const int rl = x / LANES, word = x % LANES, r = rt * R + rl, i = r / p.G;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (i < s.rows) {
+          const T* row = static_cast<const T*>(p.q) + b * p.qs[0] + i * p.qs[1] + (long long)(h * p.G + r - i * p.G) * p.qs[2];
+          v = __ldg(reinterpret_cast<const uint4*>(row) + word);
+        }
+        const uint32_t ww[4] = {v.x, v.y, v.z, v.w};
+        float f[8], sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          f[2 * j] = Kv<T>::lo(ww[j]) * raise;
+          f[2 * j + 1] = Kv<T>::hi(ww[j]) * raise;
+          sum += f[2 * j] + f[2 * j + 1];
+        }
+        const int cc = word / KW, k = word % KW;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float t = j & 1 ? 0.0625f : 1.f;
+          const int piece = 4 * k + j, half = piece >> 3;
+          *reinterpret_cast<uint32_t*>(sp + half * (R * 128) + rl * 128 + (((piece & 7) ^ (rl & 7)) << 4) + 4 * cc) =
+              half2_bits(f[j] * t, f[j + 4] * t);
+        }
+#pragma unroll
+        for (int m = LANES / 2; m >= 1; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+        if (word == 0) {
+          reinterpret_cast<float*>(pairs + (rl >> 1))[rl & 1] = sum * 0x1p-24f;
+          reinterpret_cast<float*>(pairs + (rl >> 1))[2 + (rl & 1)] = FLT_MAX;
+        }
+      }
+    }
+    copies_wait<S::kStages - 1>();
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    workers_meet();
+
+    // this thread's rows, two at a time: 8 k + 2 c, + 1 of its warpgroup's
+    Two mass[NG], shift[NG];
+#pragma unroll
+    for (int k = 0; k < NG; ++k) mass[k] = shift[k] = two(0.f, 0.f);
+    float4* const my_pairs = pairs + wg * (RH / 2) + c;      // (+ 4 k)
+    float value_scale = 0x1p126f;
+
+    for (int n = 0; n < chunks; ++n) {
+      const uint32_t stage = sm + S::oRing + slot * S::kStage;
+      const uint32_t subs = seen_subs >> ((n & 3) * 8) & 0xffu;
+      if (S::kTight && n > 0) {
+        wait_phase(bar_o, phase_o, gave_up);
+        phase_o ^= 1;
+        tm_fence_after();
+      }
+
+      // (1) key codes: the warpgroup's 16 lanes.  Lane 32 w + 16 bl + 8 e + g
+      // is token 2 (2 w + bl) + g % 2 of sub 2 (g / 2) + e: the four pairs of
+      // tokens of a piece of eight lanes are in four subs, in different banks
+      {
+        uint32_t v[8 * KW];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          uint32_t k[KW];
+          shared_words(k, stage + (2 * (g >> 1) + e) * S::kSubKeys + (2 * (2 * w + wg) + (g & 1)) * (D / 2) + c * (D / 8));
+#pragma unroll
+          for (int j = 0; j < KW; ++j) {
+            v[8 * j + e] = k[j] & 0x000f000fu;
+            v[8 * j + 2 + e] = k[j] & 0x00f000f0u;
+            v[8 * j + 4 + e] = k[j] >> 8 & 0x000f000fu;
+            v[8 * j + 6 + e] = k[j] >> 8 & 0x00f000f0u;
+          }
+        }
+        tm_store_16x128(tm_w + ((uint32_t)(16 * wg) << 16), v);
+      }
+      tm_wait_st();
+      tm_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive(bar_k);
+      if (!S::kTight && n > 0) {
+        wait_phase(bar_o, phase_o, gave_up);
+        phase_o ^= 1;
+        tm_fence_after();
+      }
+
+      // (2) value codes: the warpgroup's 64 tokens.  Unit 8 w + g of a pair is
+      // channels 4 (8 w + g) .., which go to lanes 16 (i / 2) + 8 (i % 2) + g
+      auto values = [&](uint32_t column) {
+        if (32 * w >= D) return;
+        const uint32_t flip = wg ? 0x800f800fu : 0u, flip16 = wg ? 0x80f080f0u : 0u;
+        uint32_t v0[16], v1[16];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          uint32_t x;
+          asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x)
+                       : "r"(stage + S::oValues + (2 * c + (i & 1)) * S::kSubValues + (4 * wg + (i >> 1)) * D + 4 * (8 * w + g)) : "memory");
+          v0[2 * i] = (x & 0x000f000fu) ^ flip;
+          v0[2 * i + 1] = (x & 0x00f000f0u) ^ flip16;
+          v1[2 * i] = (x >> 8 & 0x000f000fu) ^ flip;
+          v1[2 * i + 1] = (x >> 8 & 0x00f000f0u) ^ flip16;
+        }
+        tm_store_16x128(tm_w + column, v0);
+        tm_store_16x128(tm_w + (16u << 16) + column, v1);
+      };
+      if (!S::kTight || wg == 0) values(S::cV + 32 * wg);
+      wait_phase(bar_s, phase_s, gave_up);
+      phase_s ^= 1;
+      tm_fence_after();
+      if (S::kTight && wg == 1) values(0);
+
+      // (3) weights; the thread's tokens are those of lanes 16 bl + 8 e + g
+      const int token0 = (chunk0 + n) * kWdUnit + 32 * (g >> 1) + 4 * w + (g & 1);      // + 16 e + 2 bl
+      const uint32_t numbers_at = stage + S::oNumbers + 2 * (g >> 1) * S::kSubNumbers + (4 * w + (g & 1)) * 8;
+      auto softmax = [&](auto masked_step) {
+        constexpr bool kMasked = decltype(masked_step)::value;
+        // whether rows 8 k + 2 c and + 1 see token (bl, e)
+        auto sees = [&](int k, int bl, int e) {
+          const int2 lim = *reinterpret_cast<const int2*>(limits + wg * RH + 8 * k + 2 * c);
+          const int t = subs >> (2 * (g >> 1) + e) & 1 ? token0 + 16 * e + 2 * bl : 0x7fffffff;
+          return make_int2(t <= lim.x, t <= lim.y);
+        };
+        uint32_t nk[2][2], nv[2][2];       // the tokens' numbers: key's, value's
+#pragma unroll
+        for (int bl = 0; bl < 2; ++bl)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            uint32_t x[2];
+            shared_words(x, numbers_at + e * S::kSubNumbers + bl * 16);
+            // (those of tokens that nobody sees may be anything)
+            if (kMasked && (token0 + 16 * e + 2 * bl >= s.seen || !(subs >> (2 * (g >> 1) + e) & 1))) x[0] = x[1] = 0;
+            nk[bl][e] = x[0];
+            nv[bl][e] = x[1];
+          }
+        float z[2][NG][4];
+        auto exponents = [&](auto plain) {   // plain: without the references
+#pragma unroll
+          for (int bl = 0; bl < 2; ++bl)
+#pragma unroll
+            for (int k = 0; k < NG; ++k) tm_load_16x256(z[bl][k], tm_w + ((uint32_t)(16 * bl) << 16) + S::cS + wg * RH + 8 * k);
+          tm_wait_ld();
+          float most = -FLT_MAX;
+          Two ks[2][2], ko[2][2];
+#pragma unroll
+          for (int bl = 0; bl < 2; ++bl)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float a = Kv<T>::lo(nk[bl][e]) * row_scale, o = Kv<T>::hi(nk[bl][e]) * row_scale;
+              ks[bl][e] = two(a, a);
+              ko[bl][e] = two(o, o);
+            }
+#pragma unroll
+          for (int k = 0; k < NG; ++k) {
+            const float4 pair = my_pairs[4 * k];
+            const Two q = two(pair.x, pair.y), r = two(pair.z, pair.w);
+#pragma unroll
+            for (int bl = 0; bl < 2; ++bl)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const Two y = fma2(two(z[bl][k][2 * e], z[bl][k][2 * e + 1]), ks[bl][e],
+                                   decltype(plain)::value ? mul2(ko[bl][e], q) : fma2(ko[bl][e], q, r));
+                float y0, y1;
+                split(y, y0, y1);
+                if (kMasked) {
+                  const int2 see = sees(k, bl, e);
+                  if (!see.x) y0 = __int_as_float(0xff800000);
+                  if (!see.y) y1 = __int_as_float(0xff800000);
+                }
+                most = max3(most, y0, y1);
+                z[bl][k][2 * e] = y0;
+                z[bl][k][2 * e + 1] = y1;
+              }
+          }
+          return most;
+        };
+        auto weights = [&]() {
+          // the weights of row r: 128 bytes for tokens 0 .. 63, and for the others
+          const uint32_t to = sm + S::oP + (w >> 1) * (R * 128) + (wg * RH + (lane & 7)) * 128 +
+                              ((((w & 1) * 4 + (lane >> 3)) ^ (lane & 7)) << 4);
+          Two vn[2][2];
+#pragma unroll
+          for (int bl = 0; bl < 2; ++bl)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float x = Kv<T>::lo(nv[bl][e]) * value_scale;
+              vn[bl][e] = two(x, x);
+            }
+#pragma unroll
+          for (int k = 0; k < NG; ++k) {
+            uint32_t a[4], rest[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int bl = j >> 1, e = j & 1;
+              z[bl][k][2 * e] = ex2_approx(z[bl][k][2 * e]);
+              z[bl][k][2 * e + 1] = ex2_approx(z[bl][k][2 * e + 1]);
+              float a0, a1;
+              split(mul2(two(z[bl][k][2 * e], z[bl][k][2 * e + 1]), vn[bl][e]), a0, a1);
+              if (kMasked) {
+                // (a hidden token's numbers may be NaN)
+                const int2 see = sees(k, bl, e);
+                if (!see.x) a0 = 0.f;
+                if (!see.y) a1 = 0.f;
+              }
+              a[j] = half2_bits(a0, a1);
+              if (S::kFine) {
+                // a float16 result wants more than float16 weights: their rest
+                const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&a[j]));
+                rest[j] = half2_bits(a0 - back.x, a1 - back.y);
+              }
+            }
+            store_transposed(to + k * 1024, a[0], a[1], a[2], a[3]);
+            if (S::kFine) store_transposed(to + S::kP + k * 1024, rest[0], rest[1], rest[2], rest[3]);
+          }
+        };
+
+        int again = n == 0;
+        if (n > 0) {
+          float largest = fmaxf(fmaxf(Kv<T>::lo(nv[0][0]), Kv<T>::lo(nv[0][1])), fmaxf(Kv<T>::lo(nv[1][0]), Kv<T>::lo(nv[1][1])));
+          again = exponents(std::false_type{}) > kAtSlack || largest * value_scale > kAtValueTop;
+          weights();
+          tm_wait_st();
+          copies_wait<S::kStages - 2>();
+          tm_fence_before();
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          again = workers_any(again);
+        }
+        if (again) {
+          // rows' references and the values' scale move; so do the sums
+          exponents(std::true_type{});
+#pragma unroll
+          for (int k = 0; k < NG; ++k) {
+            float t0 = fmaxf(fmaxf(z[0][k][0], z[0][k][2]), fmaxf(z[1][k][0], z[1][k][2]));
+            float t1 = fmaxf(fmaxf(z[0][k][1], z[0][k][3]), fmaxf(z[1][k][1], z[1][k][3]));
+#pragma unroll
+            for (int m = 4; m <= 16; m <<= 1) {
+              t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, m));
+              t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, m));
+            }
+            if (g == 0) *reinterpret_cast<float2*>(tops + w * R + wg * RH + 8 * k + 2 * c) = make_float2(t0, t1);
+          }
+          float largest = fmaxf(fmaxf(Kv<T>::lo(nv[0][0]), Kv<T>::lo(nv[0][1])), fmaxf(Kv<T>::lo(nv[1][0]), Kv<T>::lo(nv[1][1])));
+          largest = fmaxf(largest, 0.f);
+#pragma unroll
+          for (int m = 16; m >= 1; m >>= 1) largest = fmaxf(largest, __shfl_xor_sync(0xffffffffu, largest, m));
+          if (lane == 0) warp_top[warp] = largest;
+          workers_meet();
+#pragma unroll
+          for (int j = 0; j < 8; ++j) largest = fmaxf(largest, warp_top[j]);
+          float by = 1.f;
+          if (largest * value_scale > kAtValueTop) {
+            const int e = (int)(__float_as_uint(largest) >> 23);
+            const float to = __uint_as_float((uint32_t)min(max(133 - e + 127, 1), 253) << 23);
+            by = to / value_scale;
+            value_scale = to;
+          }
+#pragma unroll
+          for (int k = 0; k < NG; ++k) {
+            const float r0 = my_pairs[4 * k].z, r1 = my_pairs[4 * k].w;
+            float n0 = -r0, n1 = -r1;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float2 t = *reinterpret_cast<const float2*>(tops + j * R + wg * RH + 8 * k + 2 * c);
+              n0 = fmaxf(n0, t.x);
+              n1 = fmaxf(n1, t.y);
+            }
+            const float f0 = ex2_approx(-r0 - n0), f1 = ex2_approx(-r1 - n1);
+            mass[k] = mul2(mass[k], two(f0, f1));
+            shift[k] = mul2(shift[k], two(f0, f1));
+            if (w == 0 && g == 0) {
+              *reinterpret_cast<float2*>(factor + wg * RH + 8 * k + 2 * c) = make_float2(f0 * by, f1 * by);
+              *reinterpret_cast<float2*>(tops + wg * RH + 8 * k + 2 * c) = make_float2(-n0, -n1);
+            }
+          }
+          workers_meet();
+          if (w == 0 && g == 0)
+            for (int k = 0; k < NG; ++k) {
+              const float2 r = *reinterpret_cast<const float2*>(tops + wg * RH + 8 * k + 2 * c);
+              my_pairs[4 * k].z = r.x;
+              my_pairs[4 * k].w = r.y;
+            }
+          workers_meet();
+          if (n > 0) {
+            for (int k = 0; k < NG; ++k) {
+              float o[8];
+              const uint32_t col = tm_w + S::cO + wg * RH + 8 * k;
+              tm_load_32x8(o, col);
+              tm_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 8; ++j) o[j] *= factor[wg * RH + 8 * k + j];
+              tm_store_32x8(col, o);
+            }
+          }
+          exponents(std::false_type{});
+          weights();
+          tm_wait_st();
+          if (n == 0) copies_wait<S::kStages - 2>();
+          tm_fence_before();
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          workers_meet();
+        }
+        if (tid == 0) arrive(bar_p);
+        copy_step(n + S::kStages);         // (everybody has read this step's)
+        // the masses, and what the values' offsets add
+#pragma unroll
+        for (int bl = 0; bl < 2; ++bl)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float mid = fmaf(w < 2 ? 0.f : 15.f, Kv<T>::lo(nv[bl][e]), Kv<T>::hi(nv[bl][e]));
+#pragma unroll
+            for (int k = 0; k < NG; ++k) {
+              const Two wt = two(z[bl][k][2 * e], z[bl][k][2 * e + 1]);
+              mass[k] = add2(mass[k], wt);
+              if (kMasked) {
+                float f0, f1;
+                split(mul2(wt, two(mid, mid)), f0, f1);
+                const int2 see = sees(k, bl, e);
+                if (!see.x) f0 = 0.f;
+                if (!see.y) f1 = 0.f;
+                shift[k] = add2(shift[k], two(f0, f1));
+              } else {
+                shift[k] = fma2(wt, two(mid, mid), shift[k]);
+              }
+            }
+          }
+      };
+      if (subs != 0xffu || (chunk0 + n) * kWdUnit + kWdUnit > s.first) softmax(std::true_type{});
+      else softmax(std::false_type{});
+      if (++slot == S::kStages) slot = 0;
+    }
+
+    // ---- the rows' totals over the warps
+#pragma unroll
+    for (int k = 0; k < NG; ++k) {
+      float m0, m1, f0, f1;
+      split(mass[k], m0, m1);
+      split(shift[k], f0, f1);
+#pragma unroll
+      for (int m = 4; m <= 16; m <<= 1) {
+        m0 += __shfl_xor_sync(0xffffffffu, m0, m);
+        m1 += __shfl_xor_sync(0xffffffffu, m1, m);
+        f0 += __shfl_xor_sync(0xffffffffu, f0, m);
+        f1 += __shfl_xor_sync(0xffffffffu, f1, m);
+      }
+      if (g == 0) {
+        const int r = wg * RH + 8 * k + 2 * c;
+        *reinterpret_cast<float2*>(masses + w * R + r) = make_float2(m0, m1);
+        *reinterpret_cast<float2*>(shifts + w * R + r) = make_float2(f0, f1);
+        if (w == 0) {
+          *reinterpret_cast<float2*>(tops + r) = make_float2(-my_pairs[4 * k].z, -my_pairs[4 * k].w);
+        }
+      }
+    }
+    wait_phase(bar_o, phase_o, gave_up);
+    phase_o ^= 1;
+    tm_fence_after();
+    workers_meet();
+    const bool failed = *gave_up;
+    const bool whole = chunk0 == 0 && chunks == s.chunks;
+    float* part = p.part + (size_t)(2 * me + (chunk0 == 0)) * part_floats(R, D);
+    if (!whole && tid < R) {
+      part[R * D + tid] = failed ? __int_as_float(0x7fffffff) : tops[tid];
+      part[R * D + R + tid] = masses[tid] + masses[R + tid] + masses[2 * R + tid] + masses[3 * R + tid];
+    }
+    const float down = (lane & 8 ? 0x1p20f : 0x1p24f), scale_down = 1.f / value_scale;
+    // lane 16 bl + 8 e + g of warp w is channel 4 (8 w + g) + 2 bl + e
+    const int channel = 32 * w + 4 * (lane & 7) + (lane >> 3);
+    for (int k = 0; k < NG; ++k) {
+      float o[8];
+      tm_load_32x8(o, tm_w + S::cO + wg * RH + 8 * k);
+      tm_wait_ld();
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int r = wg * RH + 8 * k + j, rr = rt * R + r, i = rr / p.G;
+        if (i >= s.rows || channel >= D) continue;
+        float y = fmaf(o[j] * down, scale_down, shifts[r] + shifts[R + r] + shifts[2 * R + r] + shifts[3 * R + r]);
+        if (!whole) {
+          part[r * D + channel] = y;
+          continue;
+        }
+        const float l = masses[r] + masses[R + r] + masses[2 * R + r] + masses[3 * R + r];
+        const long long q_row = ((long long)b * p.rows + i) * p.H * p.G + (long long)h * p.G + (rr - i * p.G);
+        y = failed ? __int_as_float(0x7fffffff) : l == 0.f ? 0.f : y / l;
+        static_cast<unsigned short*>(p.out)[q_row * D + channel] = (unsigned short)Kv<T>::bits(y);
+        if (p.lse && channel == 0)
+          p.lse[q_row] = failed ? y : l == 0.f ? __int_as_float(0xff800000) : (tops[r] + log2f(l)) * 6.931471805599453e-01f;
+      }
+    }
+    if (!whole && chunk0 == 0 && tid == 0)
+      p.desc[me] = make_int4(b, h, rt, line.owner(base + (long long)segment.at * s.chunks + s.chunks - 1));
+    tm_fence_before();
+    workers_meet();
+    tm_fence_after();
+    u += chunks;
+  }
+  if (warp == 0)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "n"(kWdColumns));
+}
+
+}  // namespace cache
+}  // namespace sv

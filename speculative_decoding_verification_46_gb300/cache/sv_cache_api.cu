@@ -10,6 +10,7 @@
 
 #include "specverify_cache.h"
 #include "sv_attend.cuh"
+#include "sv_attend_wide.cuh"
 #include "sv_kv4.cuh"
 #include "sv_plan.cuh"
 
@@ -104,44 +105,71 @@ unsigned store_grid(int R, int heads, int D) {
 
 // ---------------------------------------------------------------- attend
 
-int attend_ctas_per_sm(int MT) { return MT == 1 ? 3 : 2; }
-int attend_row_tiles(int rows) { return rows <= 16 ? 1 : 2; }
+// Rows of a tile: up to 32 go to attend_kernel; more to attend_wide_kernel, in
+// as few tiles as its 80 rows allow, of equal size.
+int attend_tile_rows(int rows) {
+  if (rows <= 32) return rows <= 16 ? 16 : 32;
+  const int tiles = (rows + sv::cache::kWdMostRows - 1) / sv::cache::kWdMostRows;
+  return ((rows + tiles - 1) / tiles + 15) / 16 * 16;
+}
+int attend_ctas(int TR) { return sm_count() * (TR == 16 ? 3 : 2); }
 
 struct AttendLayout {
   size_t desc, part, total;
 };
-AttendLayout attend_layout(int MT, int D, int ctas) {
+AttendLayout attend_layout(int TR, int D) {
   AttendLayout L;
+  const size_t ctas = attend_ctas(TR);
   L.desc = 0;
-  L.part = up((size_t)ctas * sizeof(int4));
-  L.total = L.part + up((size_t)2 * ctas * sv::cache::part_floats(16 * MT, D) * sizeof(float));
+  L.part = up(ctas * sizeof(int4));
+  L.total = L.part + up(2 * ctas * sv::cache::part_floats(TR, D) * sizeof(float));
   return L;
 }
 
-template <typename T, int D, int MT>
+template <typename T, int D, int TR>
 sv_status launch_attend(sv::cache::AttendParams p, void* workspace, cudaStream_t stream) {
-  using Shape = sv::cache::AttendShape<T, D, MT>;
-  auto kern = sv::cache::attend_kernel<T, D, MT>;
-  static std::atomic<bool> set[64];
-  if (!allow_smem(set, (const void*)kern, Shape::kSmem)) return SV_ERR_CUDA;
-  const int ctas = sm_count() * attend_ctas_per_sm(MT);
-  const AttendLayout L = attend_layout(MT, D, ctas);
+  using namespace sv::cache;
+  const int ctas = attend_ctas(TR);
+  const AttendLayout L = attend_layout(TR, D);
   p.desc = reinterpret_cast<int4*>(static_cast<unsigned char*>(workspace) + L.desc);
   p.part = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + L.part);
-  kern<<<ctas, sv::cache::kAtThreads, Shape::kSmem, stream>>>(p);
+  static std::atomic<bool> set[64];
+  if constexpr (TR <= 32) {
+    auto kern = attend_kernel<T, D, TR / 16>;
+    if (!allow_smem(set, (const void*)kern, AttendShape<T, D, TR / 16>::kSmem)) return SV_ERR_CUDA;
+    kern<<<ctas, AttendShape<T, D, TR / 16>::kThreads, AttendShape<T, D, TR / 16>::kSmem, stream>>>(p);
+  } else {
+    auto kern = attend_wide_kernel<T, D, TR / 16>;
+    if (!allow_smem(set, (const void*)kern, WideShape<T, D, TR / 16>::kSmem)) return SV_ERR_CUDA;
+    kern<<<ctas, kWdThreads, WideShape<T, D, TR / 16>::kSmem, stream>>>(p);
+  }
   const sv_status st = launched();
   if (st != SV_OK) return st;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas, TR * 32 / kAtJoinThreads);
+  cfg.blockDim = dim3(kAtJoinThreads);
+  cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  return launch(sv::cache::attend_join_kernel<T, D, Shape::TR>, dim3(ctas, 4), sv::cache::kAtJoinThreads, 0, stream, p,
-                attr);
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, attend_join_kernel<T, D>, p, TR) != cudaSuccess) {
+    cudaGetLastError();
+    return SV_ERR_CUDA;
+  }
+  return launched();
 }
 
 template <typename T, int D>
 sv_status launch_attend_rows(const sv::cache::AttendParams& p, void* workspace, cudaStream_t stream) {
-  return attend_row_tiles(p.rows * p.G) == 1 ? launch_attend<T, D, 1>(p, workspace, stream)
-                                             : launch_attend<T, D, 2>(p, workspace, stream);
+  switch (attend_tile_rows(p.rows * p.G)) {
+    case 16: return launch_attend<T, D, 16>(p, workspace, stream);
+    case 32: return launch_attend<T, D, 32>(p, workspace, stream);
+    case 48: return launch_attend<T, D, 48>(p, workspace, stream);
+    case 64: return launch_attend<T, D, 64>(p, workspace, stream);
+    default: return launch_attend<T, D, 80>(p, workspace, stream);
+  }
 }
 
 bool attend_sizes_ok(int gamma, int heads, int G, int D) {
@@ -249,8 +277,7 @@ extern "C" sv_status sv_read_kv4(int R, int heads, int D, int page, int pages, c
 
 extern "C" size_t sv_attend_kv4_workspace_bytes(int gamma, int heads, int G, int D) {
   if (!attend_sizes_ok(gamma, heads, G, D)) return 0;
-  const int MT = attend_row_tiles((gamma + 1) * G);
-  return attend_layout(MT, D, sm_count() * attend_ctas_per_sm(MT)).total;
+  return attend_layout(attend_tile_rows((gamma + 1) * G), D).total;
 }
 
 extern "C" sv_status sv_attend_kv4(int B, int gamma, int heads, int G, int D, int page, int pages, int N, const void* q,
