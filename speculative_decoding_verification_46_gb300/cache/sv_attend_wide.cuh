@@ -32,8 +32,8 @@
 namespace sv {
 namespace cache {
 
-constexpr int kWdThreads = 288;      // eight warps that form operands and weights, one that issues the products
-constexpr int kWdWorkers = 256;
+constexpr int kWdThreads = 256;
+constexpr int kWdScoreWarp = 1, kWdSumWarp = 6;   // warps that also issue the first and the second product
 constexpr int kWdUnit = 128;         // tokens of a step
 constexpr int kWdColumns = 256;      // of tensor memory
 constexpr int kWdMostRows = 80;
@@ -116,18 +116,6 @@ __device__ __forceinline__ void store_transposed(uint32_t at, uint32_t a, uint32
                : "memory");
 }
 
-// The eight workers meet; with `any`, they learn whether one of them says so.
-__device__ __forceinline__ void workers_meet() { asm volatile("barrier.cta.sync 1, %0;" ::"n"(kWdWorkers) : "memory"); }
-__device__ __forceinline__ bool workers_any(bool any) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r) : "r"((uint32_t)any), "n"(kWdWorkers) : "memory");
-  return r != 0;
-}
-__device__ __forceinline__ void arrive(uint32_t barrier) {
-  asm volatile("mbarrier.arrive.shared.b64 _, [%0];" ::"r"(barrier) : "memory");
-}
 // NG: R / 16; each half of the warps (a warpgroup) has the softmax of NG
 // groups of eight rows.
 template <typename T, int D, int NG>
@@ -139,14 +127,18 @@ struct WideShape {
   static constexpr int kSubKeys = 8 * D, kSubValues = 8 * D + 16, kSubNumbers = 128 + 16;
   static constexpr int oValues = 8 * kSubKeys, oNumbers = oValues + 8 * kSubValues, kStage = oNumbers + 8 * kSubNumbers;
   static constexpr int kQ = R * D * 2, kP = R * kWdUnit * 2;
-  // steps in the ring: two CTAs have 227 KB of shared memory together
-  static constexpr int kStages = kFine && R == 80 && D == 128 ? 2 : 3;
-  static constexpr int oP = kQ, oRing = oP + (kFine ? 2 : 1) * kP, oSmall = oRing + kStages * kStage;
-  // floats: row pairs' sums of q and references [4 R / 2], factor, tops [4], masses [4], shifts [4]; ints: limits
-  static constexpr int kSmall = R * 16 * 4;
+  // steps in the ring: as many as two CTAs have room for
+  static constexpr int oP = kQ, oRing = oP + (kFine ? 2 : 1) * kP;
+  static constexpr int kRoom = (112 * 1024 - 1024 - R * 18 * 4 - oRing) / kStage;
+  static constexpr int kStages = kRoom < 4 ? kRoom : 4;
+  static constexpr int oSmall = oRing + kStages * kStage;
+  // row pairs' sums of q and references [4 R / 2], factor, tops [4], masses
+  // [4], shifts [4]; limits; rows of the output
+  static constexpr int kSmall = R * 18 * 4;
   static constexpr int kSmem = oSmall + kSmall + 1024;            // (aligned to 1 KB in the kernel)
   static constexpr bool kTight = D / 2 + 64 + 2 * R > kWdColumns;
   static constexpr int cV = D / 2, cS = kTight ? D / 2 + 32 : D / 2 + 64, cO = cS + R;
+  static_assert(kStages >= (kTight ? 2 : 3), "a step's keys are read while the one before is at work");
   static_assert(cO + R <= kWdColumns, "tensor memory");
   static_assert(R <= kWdMostRows, "rows");
   static_assert(2 * (kSmem + 2048) <= 228 * 1024, "two CTAs an SM");
@@ -155,10 +147,10 @@ struct WideShape {
 template <typename T, int D, int NG>
 __global__ void __launch_bounds__(kWdThreads, 2) attend_wide_kernel(const __grid_constant__ AttendParams p) {
   using S = WideShape<T, D, NG>;
-  constexpr int R = S::R, KW = D / 32, RH = 8 * NG;
+  constexpr int R = S::R, KW = D / 32, RH = 8 * NG, LANES = D / 8;
   extern __shared__ unsigned char wd_raw[];
   __shared__ uint32_t tm_base;
-  __shared__ __align__(8) unsigned long long bars[4];
+  __shared__ __align__(8) unsigned long long bars[2];
   __shared__ int gave_up_flag;
   __shared__ float warp_top[8];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, w = warp & 3, wg = warp >> 2, g = lane >> 2, c = lane & 3;
@@ -170,9 +162,10 @@ __global__ void __launch_bounds__(kWdThreads, 2) attend_wide_kernel(const __grid
   float* const masses = tops + 4 * R;
   float* const shifts = masses + 4 * R;
   int* const limits = reinterpret_cast<int*>(shifts + 4 * R);
+  long long* const out_rows = reinterpret_cast<long long*>(limits + R);
   volatile int* const gave_up = &gave_up_flag;
-  // scores there, sums there, key codes there, weights there
-  const uint32_t bar_s = (uint32_t)__cvta_generic_to_shared(&bars[0]), bar_o = bar_s + 8, bar_k = bar_s + 16, bar_p = bar_s + 24;
+  // scores there, sums there
+  const uint32_t bar_s = (uint32_t)__cvta_generic_to_shared(&bars[0]), bar_o = bar_s + 8;
   pdl_launch_dependents();
 
   fill_behind<T, D, kWdThreads>(p);
@@ -185,8 +178,7 @@ __global__ void __launch_bounds__(kWdThreads, 2) attend_wide_kernel(const __grid
   }
   if (tid == 0) {
     gave_up_flag = 0;
-    for (int i = 0; i < 4; ++i)
-      asm volatile("mbarrier.init.shared.b64 [%0], %1;" ::"r"(bar_s + 8 * i), "r"(i == 2 ? 8 : 1) : "memory");
+    asm volatile("mbarrier.init.shared.b64 [%0], 1;\n\tmbarrier.init.shared.b64 [%1], 1;" ::"r"(bar_s), "r"(bar_o) : "memory");
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   tm_fence_before();
@@ -194,58 +186,47 @@ __global__ void __launch_bounds__(kWdThreads, 2) attend_wide_kernel(const __grid
   tm_fence_after();
   const uint32_t tm = tm_base, tm_w = tm + ((uint32_t)(32 * w) << 16);
   const uint32_t kind = 1u << 4 | (uint32_t)(R >> 3) << 17 | (128u >> 4) << 24;
+  const uint64_t q_operand = smem_operand(sm), p_operand = smem_operand(sm + S::oP);
   uint32_t phase_s = 0, phase_o = 0;     // of the next wait
   int slot = 0, slot_to = 0;             // of the ring: the step's, the next to fill
-  const uint64_t q_operand = smem_operand(sm), p_operand = smem_operand(sm + S::oP);
-
-  if (warp == kWdWorkers / 32) {
-    // ---- this warp issues the products (an issue waits for those before it),
-    // step by step over the same segments
-    uint32_t phase = 0;
-    long long u = line.u, base = line.base;
-    int b = line.b;
-    while (u < line.end) {
-      const Sequence s(p, b, R, kWdUnit);
-      const long long n_units = s.units(p.H);
-      if (u >= base + n_units) {
-        base += n_units;
-        ++b;
-        continue;
-      }
-      const int chunks = Segment(s, u, base, line.end).chunks;
-      for (int n = 0; n < chunks; ++n, phase ^= 1) {
-        wait_phase(bar_k, phase, gave_up);
-        if (lane == 0) {
-          tm_fence_after();
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k)
-            tm_mma(tm + S::cS, tm + 8 * k, q_operand + (uint64_t)((k >> 2) * (R * 8) + (k & 3) * 2), kind, k > 0);
-          tm_commit(bar_s);
-        }
-        __syncwarp();
-        wait_phase(bar_p, phase, gave_up);
-        if (lane == 0) {
-          tm_fence_after();
-#pragma unroll
-          for (int k = 0; k < kWdUnit / 16; ++k) {
-            const uint32_t a = tm + (S::kTight && k >= 4 ? 8 * (k - 4) : S::cV + 8 * k);
-            const uint64_t at_p = p_operand + (uint64_t)((k >> 2) * (R * 8) + (k & 3) * 2);
-            tm_mma(tm + S::cO, a, at_p, kind, n > 0 || k > 0);
-            if (S::kFine) tm_mma(tm + S::cO, a, at_p + S::kP / 16, kind, true);
-          }
-          tm_commit(bar_o);
-        }
-        __syncwarp();
-      }
-      u += chunks;
-    }
-    return;
-  }
 
   const long long block_bytes = (long long)p.page * kTokenBytes<D>;
   const int page_tiles = p.page / 16, me = blockIdx.x;
   long long u = line.u, base = line.base;
   int b = line.b;
+
+  auto first_product = [&]() {
+    if (warp == kWdScoreWarp) {
+      if (lane == 0) {
+        tm_fence_after();
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          tm_mma(tm + S::cS, tm + 8 * k, q_operand + (uint64_t)((k >> 2) * (R * 8) + (k & 3) * 2), kind, k > 0);
+        tm_commit(bar_s);
+      }
+      __syncwarp();
+    }
+  };
+  // key codes of a step: the warpgroup's 16 lanes.  Lane 32 w + 16 bl + 8 e + g
+  // is token 2 (2 w + bl) + g % 2 of sub 2 (g / 2) + e: the four pairs of tokens
+  // of a piece of eight lanes are in four subs, in different banks
+  auto keys = [&](int from_slot) {
+    const uint32_t stage = sm + S::oRing + from_slot * S::kStage;
+    uint32_t v[8 * KW];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      uint32_t k[KW];
+      shared_words(k, stage + (2 * (g >> 1) + e) * S::kSubKeys + (2 * (2 * w + wg) + (g & 1)) * (D / 2) + c * (D / 8));
+#pragma unroll
+      for (int j = 0; j < KW; ++j) {
+        v[8 * j + e] = k[j] & 0x000f000fu;
+        v[8 * j + 2 + e] = k[j] & 0x00f000f0u;
+        v[8 * j + 4 + e] = k[j] >> 8 & 0x000f000fu;
+        v[8 * j + 6 + e] = k[j] >> 8 & 0x00f000f0u;
+      }
+    }
+    tm_store_16x128(tm_w + ((uint32_t)(16 * wg) << 16), v);
+  };
 
   while (u < line.end) {
     const Sequence s(p, b, R, kWdUnit);
@@ -261,30 +242,41 @@ __global__ void __launch_bounds__(kWdThreads, 2) attend_wide_kernel(const __grid
 
     // ---- the ring: warp i copies sub i of a step.  A lane knows where one of
     // the next 32 subs begins, its number in the page in the low four bits
-    // (0: hidden); the 32 behind them are looked up ahead of time.
-    auto look = [&](int sub0) {
-      const int mine = sub0 + lane;
-      unsigned long long r = 0;
+    // (0: hidden); the 32 behind them are asked for ahead of time.
+    int ask_id = -1, ask_sub = 0;
+    auto ask = [&](int n) {
+      const int mine = (chunk0 + n) * 8 + lane;
+      ask_id = -1;
       if (mine < sub_end) {
-        const int n = mine / page_tiles, id = __ldg(p.table + (long long)b * p.N + n);
-        if (id >= 0 && id < p.pages) {
-          const int sub = mine - n * page_tiles;
-          r = reinterpret_cast<unsigned long long>(p.cache) + (unsigned long long)(((long long)id * p.H + h) * block_bytes + sub * (8 * D) + sub);
-        }
+        const int x = mine / page_tiles;
+        ask_id = __ldg(p.table + (long long)b * p.N + x);
+        ask_sub = mine - x * page_tiles;
       }
-      return r;
     };
-    unsigned long long ahead = look(chunk0 * 8), later = look(chunk0 * 8 + 32);
+    ask(0);
+    // q is on its way meanwhile: a thread's pieces of eight channels
+    constexpr int PIECES = (R * LANES + kWdThreads - 1) / kWdThreads;
+    uint4 qv[PIECES];
+#pragma unroll
+    for (int k = 0; k < PIECES; ++k) {
+      const int x = tid + k * kWdThreads, rl = x / LANES, r = rt * R + rl, i = r / p.G;
+      qv[k] = make_uint4(0, 0, 0, 0);
+      if (rl < R && i < s.rows)
+        qv[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + b * p.qs[0] + i * p.qs[1] +
+                                                     (long long)(h * p.G + r - i * p.G) * p.qs[2]) + x % LANES);
+    }
+    unsigned long long ahead = 0;
     uint32_t next_subs = 0;              // which of the 32 are there
     uint32_t seen_subs = 0;              // byte n % 4: which subs of step n are there
     auto copy_step = [&](int n) {
       if (n < chunks) {
         const int turn = (n & 3) * 8;
         if (turn == 0) {
-          if (n > 0) {
-            ahead = later;
-            later = look((chunk0 + n) * 8 + 32);
-          }
+          ahead = 0;
+          if (ask_id >= 0 && ask_id < p.pages)
+            ahead = reinterpret_cast<unsigned long long>(p.cache) +
+                    (unsigned long long)(((long long)ask_id * p.H + h) * block_bytes + ask_sub * (8 * D) + ask_sub);
+          ask(n + 4);
           next_subs = __ballot_sync(0xffffffffu, ahead != 0);
         }
         seen_subs = (seen_subs & ~(0xffu << turn)) | (next_subs & 0xffu << turn);
@@ -312,67 +304,72 @@ __global__ void __launch_bounds__(kWdThreads, 2) attend_wide_kernel(const __grid
     // size), channels in the order in which the key codes come: element
     // 2 (c + 4 (4 k + i)) + e is channel 8 (KW c + k) + i + 4 e, halves e of
     // pair i of word k
-    float raise, row_scale;
+    float row_scale;
     {
-      constexpr int LANES = D / 8;
       float top = 0.f;
-      for (int x = tid; x < R * LANES; x += kWdWorkers) {
-        const int r = rt * R + x / LANES, i = r / p.G;
-        if (i < s.rows) {
-          const T* row = static_cast<const T*>(p.q) + b * p.qs[0] + i * p.qs[1] + (long long)(h * p.G + r - i * p.G) * p.qs[2];
-          const uint4 v = __ldg(reinterpret_cast<const uint4*>(row) + x % LANES);
-          const uint32_t ww[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-          for (int j = 0; j < 4; ++j) top = fmaxf(top, fmaxf(fabsf(Kv<T>::lo(ww[j])), fabsf(Kv<T>::hi(ww[j]))));
+      for (int k = 0; k < PIECES; ++k) {
+        const int x = tid + k * kWdThreads, rl = x / LANES;
+        const uint32_t ww[4] = {qv[k].x, qv[k].y, qv[k].z, qv[k].w};
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float f0 = Kv<T>::lo(ww[j]), f1 = Kv<T>::hi(ww[j]);
+          top = max3(top, fabsf(f0), fabsf(f1));
+          sum += f0 + f1;
+        }
+#pragma unroll
+        for (int m = LANES / 2; m >= 1; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+        if (x % LANES == 0 && rl < R) {
+          const int r = rt * R + rl, i = r / p.G;
+          reinterpret_cast<float*>(pairs + (rl >> 1))[rl & 1] = sum;
+          reinterpret_cast<float*>(pairs + (rl >> 1))[2 + (rl & 1)] = 0.f;
+          limits[rl] = i < s.rows ? min(s.first - 1 + i, s.seen - 1) : -1;
+          out_rows[rl] = i < s.rows ? ((long long)b * p.rows + i) * p.H * p.G + (long long)h * p.G + (r - i * p.G) : -1;
         }
       }
 #pragma unroll
       for (int m = 16; m >= 1; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
       if (lane == 0) warp_top[warp] = top;
-      if (tid < R) {
-        const int i = (rt * R + tid) / p.G;
-        limits[tid] = i < s.rows ? min(s.first - 1 + i, s.seen - 1) : -1;
-      }
-      workers_meet();
+      __syncthreads();
 #pragma unroll
       for (int j = 0; j < 8; ++j) top = fmaxf(top, warp_top[j]);
       const int up = top > 0.f ? min(140 - (int)(__float_as_uint(top) >> 23), 126) : 0;
-      raise = __uint_as_float((uint32_t)(up + 127) << 23);
+      const float raise = __uint_as_float((uint32_t)(up + 127) << 23);
       row_scale = p.scale * 0x1p24f * __uint_as_float((uint32_t)(127 - up) << 23);
-      for (int x = tid; x < R * LANES; x += kWdWorkers) {
-        const int rl = x / LANES, word = x % LANES, r = rt * R + rl, i = r / p.G;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (i < s.rows) {
-          const T* row = static_cast<const T*>(p.q) + b * p.qs[0] + i * p.qs[1] + (long long)(h * p.G + r - i * p.G) * p.qs[2];
-          v = __ldg(reinterpret_cast<const uint4*>(row) + word);
-        }
-        const uint32_t ww[4] = {v.x, v.y, v.z, v.w};
-        float f[8], sum = 0.f;
+      if (tid < R) reinterpret_cast<float*>(pairs + (tid >> 1))[tid & 1] *= raise * 0x1p-24f;
+#pragma unroll
+      for (int k = 0; k < PIECES; ++k) {
+        const int x = tid + k * kWdThreads, rl = x / LANES, word = x % LANES;
+        if (rl >= R) break;
+        const uint32_t ww[4] = {qv[k].x, qv[k].y, qv[k].z, qv[k].w};
+        float f[8];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           f[2 * j] = Kv<T>::lo(ww[j]) * raise;
           f[2 * j + 1] = Kv<T>::hi(ww[j]) * raise;
-          sum += f[2 * j] + f[2 * j + 1];
         }
-        const int cc = word / KW, k = word % KW;
+        const int cc = word / KW, kk = word % KW;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float t = j & 1 ? 0.0625f : 1.f;
-          const int piece = 4 * k + j, half = piece >> 3;
-          *reinterpret_cast<uint32_t*>(sp + half * (R * 128) + rl * 128 + (((piece & 7) ^ (rl & 7)) << 4) + 4 * cc) =
+          const int piece = 4 * kk + j;
+          *reinterpret_cast<uint32_t*>(sp + (piece >> 3) * (R * 128) + rl * 128 + (((piece & 7) ^ (rl & 7)) << 4) + 4 * cc) =
               half2_bits(f[j] * t, f[j + 4] * t);
-        }
-#pragma unroll
-        for (int m = LANES / 2; m >= 1; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-        if (word == 0) {
-          reinterpret_cast<float*>(pairs + (rl >> 1))[rl & 1] = sum * 0x1p-24f;
-          reinterpret_cast<float*>(pairs + (rl >> 1))[2 + (rl & 1)] = FLT_MAX;
         }
       }
     }
     copies_wait<S::kStages - 1>();
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    workers_meet();
+    __syncthreads();
+    if (!S::kTight) {
+      keys(slot);
+      tm_wait_st();
+      copies_wait<(S::kStages > 1 ? S::kStages - 2 : 0)>();
+      tm_fence_before();
+      __syncthreads();
+      first_product();
+    }
 
     // this thread's rows, two at a time: 8 k + 2 c, + 1 of its warpgroup's
     Two mass[NG], shift[NG];
@@ -384,42 +381,21 @@ __global__ void __launch_bounds__(kWdThreads, 2) attend_wide_kernel(const __grid
     for (int n = 0; n < chunks; ++n) {
       const uint32_t stage = sm + S::oRing + slot * S::kStage;
       const uint32_t subs = seen_subs >> ((n & 3) * 8) & 0xffu;
-      if (S::kTight && n > 0) {
+      const int slot_next = slot + 1 == S::kStages ? 0 : slot + 1;
+      if (n > 0) {
         wait_phase(bar_o, phase_o, gave_up);
         phase_o ^= 1;
         tm_fence_after();
       }
-
-      // (1) key codes: the warpgroup's 16 lanes.  Lane 32 w + 16 bl + 8 e + g
-      // is token 2 (2 w + bl) + g % 2 of sub 2 (g / 2) + e: the four pairs of
-      // tokens of a piece of eight lanes are in four subs, in different banks
-      {
-        uint32_t v[8 * KW];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          uint32_t k[KW];
-          shared_words(k, stage + (2 * (g >> 1) + e) * S::kSubKeys + (2 * (2 * w + wg) + (g & 1)) * (D / 2) + c * (D / 8));
-#pragma unroll
-          for (int j = 0; j < KW; ++j) {
-            v[8 * j + e] = k[j] & 0x000f000fu;
-            v[8 * j + 2 + e] = k[j] & 0x00f000f0u;
-            v[8 * j + 4 + e] = k[j] >> 8 & 0x000f000fu;
-            v[8 * j + 6 + e] = k[j] >> 8 & 0x00f000f0u;
-          }
-        }
-        tm_store_16x128(tm_w + ((uint32_t)(16 * wg) << 16), v);
-      }
-      tm_wait_st();
-      tm_fence_before();
-      __syncwarp();
-      if (lane == 0) arrive(bar_k);
-      if (!S::kTight && n > 0) {
-        wait_phase(bar_o, phase_o, gave_up);
-        phase_o ^= 1;
-        tm_fence_after();
+      if (S::kTight) {
+        keys(slot);
+        tm_wait_st();
+        tm_fence_before();
+        __syncthreads();
+        first_product();
       }
 
-      // (2) value codes: the warpgroup's 64 tokens.  Unit 8 w + g of a pair is
+      // value codes: the warpgroup's 64 tokens.  Unit 8 w + g of a pair is
       // channels 4 (8 w + g) .., which go to lanes 16 (i / 2) + 8 (i % 2) + g
       auto values = [&](uint32_t column) {
         if (32 * w >= D) return;
@@ -468,7 +444,7 @@ __global__ void __launch_bounds__(kWdThreads, 2) attend_wide_kernel(const __grid
             nv[bl][e] = x[1];
           }
         float z[2][NG][4];
-        auto exponents = [&](auto plain) {   // plain: without the references
+        auto exponents = [&]() {
 #pragma unroll
           for (int bl = 0; bl < 2; ++bl)
 #pragma unroll
@@ -492,8 +468,7 @@ __global__ void __launch_bounds__(kWdThreads, 2) attend_wide_kernel(const __grid
             for (int bl = 0; bl < 2; ++bl)
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                const Two y = fma2(two(z[bl][k][2 * e], z[bl][k][2 * e + 1]), ks[bl][e],
-                                   decltype(plain)::value ? mul2(ko[bl][e], q) : fma2(ko[bl][e], q, r));
+                const Two y = fma2(two(z[bl][k][2 * e], z[bl][k][2 * e + 1]), ks[bl][e], fma2(ko[bl][e], q, r));
                 float y0, y1;
                 split(y, y0, y1);
                 if (kMasked) {
@@ -548,20 +523,27 @@ __global__ void __launch_bounds__(kWdThreads, 2) attend_wide_kernel(const __grid
           }
         };
 
-        int again = n == 0;
-        if (n > 0) {
-          float largest = fmaxf(fmaxf(Kv<T>::lo(nv[0][0]), Kv<T>::lo(nv[0][1])), fmaxf(Kv<T>::lo(nv[1][0]), Kv<T>::lo(nv[1][1])));
-          again = exponents(std::false_type{}) > kAtSlack || largest * value_scale > kAtValueTop;
-          weights();
+        // the next step's key codes, and all of it visible to the others
+        auto meet = [&](bool any) {
           tm_wait_st();
-          copies_wait<S::kStages - 2>();
+          copies_wait<S::kTight ? S::kStages - 2 : S::kStages - 3>();
           tm_fence_before();
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          again = workers_any(again);
+          return __syncthreads_or(any);
+        };
+        float largest = fmaxf(fmaxf(Kv<T>::lo(nv[0][0]), Kv<T>::lo(nv[0][1])), fmaxf(Kv<T>::lo(nv[1][0]), Kv<T>::lo(nv[1][1])));
+        bool again = n == 0;
+        if (n > 0) {
+          again = exponents() > kAtSlack || largest * value_scale > kAtValueTop;
+          weights();
+          if (!S::kTight && n + 1 < chunks) keys(slot_next);
+          again = meet(again);
         }
         if (again) {
-          // rows' references and the values' scale move; so do the sums
-          exponents(std::true_type{});
+          // rows' references and the values' scale move; so do the sums.  The
+          // first step sets the references (they were 0): a row that sees none
+          // of it sees none of the later ones, its mass stays 0.
+          exponents();
 #pragma unroll
           for (int k = 0; k < NG; ++k) {
             float t0 = fmaxf(fmaxf(z[0][k][0], z[0][k][2]), fmaxf(z[1][k][0], z[1][k][2]));
@@ -573,12 +555,11 @@ __global__ void __launch_bounds__(kWdThreads, 2) attend_wide_kernel(const __grid
             }
             if (g == 0) *reinterpret_cast<float2*>(tops + w * R + wg * RH + 8 * k + 2 * c) = make_float2(t0, t1);
           }
-          float largest = fmaxf(fmaxf(Kv<T>::lo(nv[0][0]), Kv<T>::lo(nv[0][1])), fmaxf(Kv<T>::lo(nv[1][0]), Kv<T>::lo(nv[1][1])));
           largest = fmaxf(largest, 0.f);
 #pragma unroll
           for (int m = 16; m >= 1; m >>= 1) largest = fmaxf(largest, __shfl_xor_sync(0xffffffffu, largest, m));
           if (lane == 0) warp_top[warp] = largest;
-          workers_meet();
+          __syncthreads();
 #pragma unroll
           for (int j = 0; j < 8; ++j) largest = fmaxf(largest, warp_top[j]);
           float by = 1.f;
@@ -588,32 +569,39 @@ __global__ void __launch_bounds__(kWdThreads, 2) attend_wide_kernel(const __grid
             by = to / value_scale;
             value_scale = to;
           }
+          // a row's terms move down by `up`
+          auto rise = [&](float t) {
+            return n > 0 ? fmaxf(t, 0.f) : t == __int_as_float(0xff800000) ? 0.f : t;
+          };
 #pragma unroll
           for (int k = 0; k < NG; ++k) {
-            const float r0 = my_pairs[4 * k].z, r1 = my_pairs[4 * k].w;
-            float n0 = -r0, n1 = -r1;
+            float up0 = __int_as_float(0xff800000), up1 = up0;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const float2 t = *reinterpret_cast<const float2*>(tops + j * R + wg * RH + 8 * k + 2 * c);
-              n0 = fmaxf(n0, t.x);
-              n1 = fmaxf(n1, t.y);
+              up0 = fmaxf(up0, t.x);
+              up1 = fmaxf(up1, t.y);
             }
-            const float f0 = ex2_approx(-r0 - n0), f1 = ex2_approx(-r1 - n1);
+            up0 = rise(up0);
+            up1 = rise(up1);
+            const float f0 = n > 0 ? ex2_approx(-up0) : 0.f, f1 = n > 0 ? ex2_approx(-up1) : 0.f;
             mass[k] = mul2(mass[k], two(f0, f1));
             shift[k] = mul2(shift[k], two(f0, f1));
+#pragma unroll
+            for (int bl = 0; bl < 2; ++bl)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                z[bl][k][2 * e] -= up0;
+                z[bl][k][2 * e + 1] -= up1;
+              }
             if (w == 0 && g == 0) {
+              // (a warp of its own reads and writes these two rows' references here)
               *reinterpret_cast<float2*>(factor + wg * RH + 8 * k + 2 * c) = make_float2(f0 * by, f1 * by);
-              *reinterpret_cast<float2*>(tops + wg * RH + 8 * k + 2 * c) = make_float2(-n0, -n1);
+              my_pairs[4 * k].z -= up0;
+              my_pairs[4 * k].w -= up1;
             }
           }
-          workers_meet();
-          if (w == 0 && g == 0)
-            for (int k = 0; k < NG; ++k) {
-              const float2 r = *reinterpret_cast<const float2*>(tops + wg * RH + 8 * k + 2 * c);
-              my_pairs[4 * k].z = r.x;
-              my_pairs[4 * k].w = r.y;
-            }
-          workers_meet();
+          __syncthreads();
           if (n > 0) {
             for (int k = 0; k < NG; ++k) {
               float o[8];
@@ -625,15 +613,25 @@ __global__ void __launch_bounds__(kWdThreads, 2) attend_wide_kernel(const __grid
               tm_store_32x8(col, o);
             }
           }
-          exponents(std::false_type{});
           weights();
-          tm_wait_st();
-          if (n == 0) copies_wait<S::kStages - 2>();
-          tm_fence_before();
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          workers_meet();
+          if (!S::kTight && n == 0 && n + 1 < chunks) keys(slot_next);
+          meet(false);
         }
-        if (tid == 0) arrive(bar_p);
+        if (warp == kWdSumWarp) {
+          if (lane == 0) {
+            tm_fence_after();
+#pragma unroll
+            for (int k = 0; k < kWdUnit / 16; ++k) {
+              const uint32_t a = tm + (S::kTight && k >= 4 ? 8 * (k - 4) : S::cV + 8 * k);
+              const uint64_t at_p = p_operand + (uint64_t)((k >> 2) * (R * 8) + (k & 3) * 2);
+              tm_mma(tm + S::cO, a, at_p, kind, n > 0 || k > 0);
+              if (S::kFine) tm_mma(tm + S::cO, a, at_p + S::kP / 16, kind, true);
+            }
+            tm_commit(bar_o);
+          }
+          __syncwarp();
+        }
+        if (!S::kTight && n + 1 < chunks) first_product();
         copy_step(n + S::kStages);         // (everybody has read this step's)
         // the masses, and what the values' offsets add
 #pragma unroll
@@ -660,7 +658,7 @@ __global__ void __launch_bounds__(kWdThreads, 2) attend_wide_kernel(const __grid
       };
       if (subs != 0xffu || (chunk0 + n) * kWdUnit + kWdUnit > s.first) softmax(std::true_type{});
       else softmax(std::false_type{});
-      if (++slot == S::kStages) slot = 0;
+      slot = slot_next;
     }
 
     // ---- the rows' totals over the warps
@@ -688,42 +686,50 @@ __global__ void __launch_bounds__(kWdThreads, 2) attend_wide_kernel(const __grid
     wait_phase(bar_o, phase_o, gave_up);
     phase_o ^= 1;
     tm_fence_after();
-    workers_meet();
+    __syncthreads();
     const bool failed = *gave_up;
     const bool whole = chunk0 == 0 && chunks == s.chunks;
     float* part = p.part + (size_t)(2 * me + (chunk0 == 0)) * part_floats(R, D);
-    if (!whole && tid < R) {
-      part[R * D + tid] = failed ? __int_as_float(0x7fffffff) : tops[tid];
-      part[R * D + R + tid] = masses[tid] + masses[R + tid] + masses[2 * R + tid] + masses[3 * R + tid];
+    if (tid < R) {
+      // (the first of the four keeps the sum)
+      const float l = masses[tid] + masses[R + tid] + masses[2 * R + tid] + masses[3 * R + tid];
+      const float f = shifts[tid] + shifts[R + tid] + shifts[2 * R + tid] + shifts[3 * R + tid];
+      const float top = failed ? __int_as_float(0x7fffffff) : l == 0.f ? -FLT_MAX : tops[tid];
+      if (!whole) {
+        part[R * D + tid] = top;
+        part[R * D + R + tid] = l;
+        factor[tid] = 1.f;
+      } else {
+        factor[tid] = failed ? top : l == 0.f ? 0.f : 1.f / l;
+        const long long row = out_rows[tid];
+        if (p.lse && row >= 0)
+          p.lse[row] = failed ? top : l == 0.f ? __int_as_float(0xff800000) : (top + log2f(l)) * 6.931471805599453e-01f;
+      }
+      shifts[tid] = f;
     }
+    __syncthreads();
     const float down = (lane & 8 ? 0x1p20f : 0x1p24f), scale_down = 1.f / value_scale;
     // lane 16 bl + 8 e + g of warp w is channel 4 (8 w + g) + 2 bl + e
     const int channel = 32 * w + 4 * (lane & 7) + (lane >> 3);
+#pragma unroll 1
     for (int k = 0; k < NG; ++k) {
       float o[8];
       tm_load_32x8(o, tm_w + S::cO + wg * RH + 8 * k);
       tm_wait_ld();
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const int r = wg * RH + 8 * k + j, rr = rt * R + r, i = rr / p.G;
-        if (i >= s.rows || channel >= D) continue;
-        float y = fmaf(o[j] * down, scale_down, shifts[r] + shifts[R + r] + shifts[2 * R + r] + shifts[3 * R + r]);
-        if (!whole) {
-          part[r * D + channel] = y;
-          continue;
-        }
-        const float l = masses[r] + masses[R + r] + masses[2 * R + r] + masses[3 * R + r];
-        const long long q_row = ((long long)b * p.rows + i) * p.H * p.G + (long long)h * p.G + (rr - i * p.G);
-        y = failed ? __int_as_float(0x7fffffff) : l == 0.f ? 0.f : y / l;
-        static_cast<unsigned short*>(p.out)[q_row * D + channel] = (unsigned short)Kv<T>::bits(y);
-        if (p.lse && channel == 0)
-          p.lse[q_row] = failed ? y : l == 0.f ? __int_as_float(0xff800000) : (tops[r] + log2f(l)) * 6.931471805599453e-01f;
+        const int r = wg * RH + 8 * k + j;
+        const long long row = out_rows[r];
+        if (row < 0 || channel >= D) continue;
+        const float y = fmaf(o[j] * down, scale_down, shifts[r]) * factor[r];
+        if (!whole) part[r * D + channel] = y;
+        else static_cast<unsigned short*>(p.out)[row * D + channel] = (unsigned short)Kv<T>::bits(y);
       }
     }
     if (!whole && chunk0 == 0 && tid == 0)
       p.desc[me] = make_int4(b, h, rt, line.owner(base + (long long)segment.at * s.chunks + s.chunks - 1));
     tm_fence_before();
-    workers_meet();
+    __syncthreads();
     tm_fence_after();
     u += chunks;
   }
