@@ -34,6 +34,7 @@ namespace sv {
 namespace cache {
 
 constexpr int kAtUnit = 128;              // tokens of a unit
+constexpr int kAtStart = 2;               // units that stand for a segment's start
 constexpr int kAtStages = 3;              // groups of 32 tokens in a warp's ring
 constexpr int kAtJoinThreads = 256;
 constexpr float kAtSlack = 8.f;           // a row's reference may be 2^8 below its largest term
@@ -77,7 +78,8 @@ struct Sequence {
     tiles = (rows * p.G + TR - 1) / TR;
     chunks = max(1, (seen + unit - 1) / unit);
   }
-  __device__ __forceinline__ long long units(int H) const { return (long long)H * tiles * chunks; }
+  // (a segment's start takes about as long as kAtStart of its units)
+  __device__ __forceinline__ long long units(int H) const { return (long long)H * tiles * (chunks + kAtStart); }
 };
 
 // Rows behind a sequence's last become 0.
@@ -150,21 +152,31 @@ __device__ __forceinline__ Part find_part(const AttendParams& p, int TR, int uni
   return x;
 }
 
-// The segment that unit u is in: head, row tile, and its units from u on that
-// are this CTA's.
+// The segment that unit u is in: head, row tile, and those of its units from u
+// on that are this CTA's; the line goes on `step` units behind u.  The first
+// kAtStart units of a segment are its start alone: who has no others of it
+// (chunks = 0) does nothing.
 struct Segment {
-  int h, rt, at, chunk0, chunks;
+  int h, rt, at, chunk0, chunks, step;
   __device__ __forceinline__ Segment(const Sequence& s, long long u, long long base, long long end) {
+    const int all = s.chunks + kAtStart;
+    int begin;
     if (u - base < 0x7fffffffll) {        // (a 64-bit division takes longer)
-      at = (int)(u - base) / s.chunks;
-      chunk0 = (int)(u - base) - at * s.chunks;
+      at = (int)(u - base) / all;
+      begin = (int)(u - base) - at * all;
     } else {
-      at = (int)((u - base) / s.chunks);
-      chunk0 = (int)(u - base - (long long)at * s.chunks);
+      at = (int)((u - base) / all);
+      begin = (int)(u - base - (long long)at * all);
     }
     h = at / s.tiles;
     rt = at - h * s.tiles;
-    chunks = (int)min((long long)(s.chunks - chunk0), end - u);
+    step = (int)min((long long)(all - begin), end - u);
+    chunk0 = max(begin - kAtStart, 0);
+    chunks = max(begin + step - kAtStart, 0) - chunk0;
+  }
+  // its last unit
+  __device__ __forceinline__ long long last(const Sequence& s, long long base) const {
+    return base + (long long)(at + 1) * (s.chunks + kAtStart) - 1;
   }
 };
 
@@ -283,6 +295,8 @@ __global__ void __launch_bounds__(AttendShape<T, D, MT>::kThreads, AttendShape<T
     }
     const Segment segment(s, u, base, line.end);
     const int h = segment.h, rt = segment.rt, chunk0 = segment.chunk0, chunks = segment.chunks;
+    u += segment.step;
+    if (chunks == 0) continue;
 
     // ---- this warp's groups of 32 tokens, number `first` + 8 n
     const int sub_end = (s.seen + 15) / 16;
@@ -690,8 +704,7 @@ __global__ void __launch_bounds__(AttendShape<T, D, MT>::kThreads, AttendShape<T
     }
     __syncthreads();
     if (!whole && chunk0 == 0 && tid == 0)
-      p.desc[me] = make_int4(b, h, rt, line.owner(base + (long long)segment.at * s.chunks + s.chunks - 1));
-    u += chunks;
+      p.desc[me] = make_int4(b, h, rt, line.owner(segment.last(s, base)));
   }
 }
 

@@ -96,17 +96,26 @@ __device__ __forceinline__ uint64_t smem_operand(uint32_t at) {
 
 // A wait that ends: where the phase does not come, *gave_up is set for the
 // whole CTA, whose later waits are short and whose rows become NaN.
-__device__ __forceinline__ void wait_phase(uint32_t barrier, uint32_t parity, volatile int* gave_up) {
-  uint32_t done = 0;
-#pragma unroll 1
+__device__ __forceinline__ bool phase_there(uint32_t barrier, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done) : "r"(barrier), "r"(parity), "r"(100000u) : "memory");
+  return done != 0;
+}
+__device__ __noinline__ void wait_longer(uint32_t barrier, uint32_t parity, volatile int* gave_up) {
+  bool done = false;
   for (int i = 0; i < kWdPatience && !done; ++i) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done) : "r"(barrier), "r"(parity), "r"(100000u) : "memory");
+    done = phase_there(barrier, parity);
     if (!done && i >= 64 && *gave_up) break;
   }
   if (!done) *gave_up = 1;
-  __syncwarp();
+}
+__device__ __forceinline__ void wait_phase(uint32_t barrier, uint32_t parity, volatile int* gave_up) {
+  if (!__all_sync(0xffffffffu, phase_there(barrier, parity))) {
+    wait_longer(barrier, parity, gave_up);
+    __syncwarp();
+  }
 }
 
 // The transposes of four 8 x 8 matrices of 16-bit elements: matrix i's row j
@@ -238,9 +247,11 @@ __global__ void __launch_bounds__(kWdThreads, 2) attend_wide_kernel(const __grid
     }
     const Segment segment(s, u, base, line.end);
     const int h = segment.h, rt = segment.rt, chunk0 = segment.chunk0, chunks = segment.chunks;
+    u += segment.step;
+    if (chunks == 0) continue;
     const int sub_end = (s.seen + 15) / 16;
 
-    // ---- the ring: warp i copies sub i of a step.  A lane knows where one of
+    // ---- the ring: a warp copies a sub of a step.  A lane knows where one of
     // the next 32 subs begins, its number in the page in the low four bits
     // (0: hidden); the 32 behind them are asked for ahead of time.
     int ask_id = -1, ask_sub = 0;
@@ -280,18 +291,23 @@ __global__ void __launch_bounds__(kWdThreads, 2) attend_wide_kernel(const __grid
           next_subs = __ballot_sync(0xffffffffu, ahead != 0);
         }
         seen_subs = (seen_subs & ~(0xffu << turn)) | (next_subs & 0xffu << turn);
-        const unsigned long long from = __shfl_sync(0xffffffffu, ahead, turn + warp);
-        if (from != 0) {
+        // (warps 1 and 6 are busy with the products; 2 and 5 take one sub more)
+        auto copy_sub = [&](int x) {
+          const unsigned long long from = __shfl_sync(0xffffffffu, ahead, turn + x);
+          if (from == 0) return;
           const int sub = (int)(from & 15);
           const unsigned char* codes = reinterpret_cast<const unsigned char*>(from - sub) + lane * 16;
           const uint32_t to = sm + S::oRing + slot_to * S::kStage + lane * 16;
 #pragma unroll
           for (int j = 0; j < D / 64; ++j) {
-            copy_ahead<16>(to + warp * S::kSubKeys + j * 512, codes + j * 512);
-            copy_ahead<16>(to + S::oValues + warp * S::kSubValues + j * 512, codes + p.page * (D / 2) + j * 512);
+            copy_ahead<16>(to + x * S::kSubKeys + j * 512, codes + j * 512);
+            copy_ahead<16>(to + S::oValues + x * S::kSubValues + j * 512, codes + p.page * (D / 2) + j * 512);
           }
-          if (lane < 8) copy_ahead<16>(to + S::oNumbers + warp * S::kSubNumbers, codes + p.page * D - sub * (8 * D - 128));
-        }
+          if (lane < 8) copy_ahead<16>(to + S::oNumbers + x * S::kSubNumbers, codes + p.page * D - sub * (8 * D - 128));
+        };
+        if (warp != kWdScoreWarp && warp != kWdSumWarp) copy_sub(warp);
+        if (warp == 2) copy_sub(kWdScoreWarp);
+        if (warp == 5) copy_sub(kWdSumWarp);
         slot_to = slot_to + 1 == S::kStages ? 0 : slot_to + 1;
       }
       copies_end_group();
@@ -483,17 +499,21 @@ __global__ void __launch_bounds__(kWdThreads, 2) attend_wide_kernel(const __grid
           }
           return most;
         };
-        auto weights = [&]() {
+        // (a warp whose terms have not outgrown their references has formed its
+        // part of the masses for good: a reference that moves scales it)
+        auto weights = [&](bool first) {
           // the weights of row r: 128 bytes for tokens 0 .. 63, and for the others
           const uint32_t to = sm + S::oP + (w >> 1) * (R * 128) + (wg * RH + (lane & 7)) * 128 +
                               ((((w & 1) * 4 + (lane >> 3)) ^ (lane & 7)) << 4);
-          Two vn[2][2];
+          Two vn[2][2], vo[2][2];
 #pragma unroll
           for (int bl = 0; bl < 2; ++bl)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const float x = Kv<T>::lo(nv[bl][e]) * value_scale;
-              vn[bl][e] = two(x, x);
+              const float x = Kv<T>::lo(nv[bl][e]), n_x = x * value_scale;
+              const float o_x = fmaf(w < 2 ? 0.f : 15.f, x, Kv<T>::hi(nv[bl][e]));
+              vn[bl][e] = two(n_x, n_x);
+              vo[bl][e] = two(o_x, o_x);
             }
 #pragma unroll
           for (int k = 0; k < NG; ++k) {
@@ -501,15 +521,25 @@ __global__ void __launch_bounds__(kWdThreads, 2) attend_wide_kernel(const __grid
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const int bl = j >> 1, e = j & 1;
-              z[bl][k][2 * e] = ex2_approx(z[bl][k][2 * e]);
-              z[bl][k][2 * e + 1] = ex2_approx(z[bl][k][2 * e + 1]);
+              const Two wt = two(ex2_approx(z[bl][k][2 * e]), ex2_approx(z[bl][k][2 * e + 1]));
               float a0, a1;
-              split(mul2(two(z[bl][k][2 * e], z[bl][k][2 * e + 1]), vn[bl][e]), a0, a1);
+              split(mul2(wt, vn[bl][e]), a0, a1);
               if (kMasked) {
                 // (a hidden token's numbers may be NaN)
                 const int2 see = sees(k, bl, e);
                 if (!see.x) a0 = 0.f;
                 if (!see.y) a1 = 0.f;
+                float f0, f1;
+                split(mul2(wt, vo[bl][e]), f0, f1);
+                if (!see.x) f0 = 0.f;
+                if (!see.y) f1 = 0.f;
+                if (first) {
+                  mass[k] = add2(mass[k], wt);
+                  shift[k] = add2(shift[k], two(f0, f1));
+                }
+              } else if (first) {
+                mass[k] = add2(mass[k], wt);
+                shift[k] = fma2(wt, vo[bl][e], shift[k]);
               }
               a[j] = half2_bits(a0, a1);
               if (S::kFine) {
@@ -532,12 +562,13 @@ __global__ void __launch_bounds__(kWdThreads, 2) attend_wide_kernel(const __grid
           return __syncthreads_or(any);
         };
         float largest = fmaxf(fmaxf(Kv<T>::lo(nv[0][0]), Kv<T>::lo(nv[0][1])), fmaxf(Kv<T>::lo(nv[1][0]), Kv<T>::lo(nv[1][1])));
-        bool again = n == 0;
+        bool again = true, outgrown = true;
         if (n > 0) {
-          again = exponents() > kAtSlack || largest * value_scale > kAtValueTop;
-          weights();
+          const float most = exponents();
+          outgrown = __any_sync(0xffffffffu, most > kAtSlack || largest * value_scale > kAtValueTop);
+          if (!outgrown) weights(true);
           if (!S::kTight && n + 1 < chunks) keys(slot_next);
-          again = meet(again);
+          again = meet(outgrown);
         }
         if (again) {
           // rows' references and the values' scale move; so do the sums.  The
@@ -613,7 +644,7 @@ __global__ void __launch_bounds__(kWdThreads, 2) attend_wide_kernel(const __grid
               tm_store_32x8(col, o);
             }
           }
-          weights();
+          weights(outgrown);
           if (!S::kTight && n == 0 && n + 1 < chunks) keys(slot_next);
           meet(false);
         }
@@ -633,28 +664,6 @@ __global__ void __launch_bounds__(kWdThreads, 2) attend_wide_kernel(const __grid
         }
         if (!S::kTight && n + 1 < chunks) first_product();
         copy_step(n + S::kStages);         // (everybody has read this step's)
-        // the masses, and what the values' offsets add
-#pragma unroll
-        for (int bl = 0; bl < 2; ++bl)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float mid = fmaf(w < 2 ? 0.f : 15.f, Kv<T>::lo(nv[bl][e]), Kv<T>::hi(nv[bl][e]));
-#pragma unroll
-            for (int k = 0; k < NG; ++k) {
-              const Two wt = two(z[bl][k][2 * e], z[bl][k][2 * e + 1]);
-              mass[k] = add2(mass[k], wt);
-              if (kMasked) {
-                float f0, f1;
-                split(mul2(wt, two(mid, mid)), f0, f1);
-                const int2 see = sees(k, bl, e);
-                if (!see.x) f0 = 0.f;
-                if (!see.y) f1 = 0.f;
-                shift[k] = add2(shift[k], two(f0, f1));
-              } else {
-                shift[k] = fma2(wt, two(mid, mid), shift[k]);
-              }
-            }
-          }
       };
       if (subs != 0xffu || (chunk0 + n) * kWdUnit + kWdUnit > s.first) softmax(std::true_type{});
       else softmax(std::false_type{});
@@ -727,11 +736,10 @@ __global__ void __launch_bounds__(kWdThreads, 2) attend_wide_kernel(const __grid
       }
     }
     if (!whole && chunk0 == 0 && tid == 0)
-      p.desc[me] = make_int4(b, h, rt, line.owner(base + (long long)segment.at * s.chunks + s.chunks - 1));
+      p.desc[me] = make_int4(b, h, rt, line.owner(segment.last(s, base)));
     tm_fence_before();
     __syncthreads();
     tm_fence_after();
-    u += chunks;
   }
   if (warp == 0)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "n"(kWdColumns));

@@ -105,10 +105,10 @@ unsigned store_grid(int R, int heads, int D) {
 
 // ---------------------------------------------------------------- attend
 
-// Rows of a tile: up to 32 go to attend_kernel; more to attend_wide_kernel, in
+// Rows of a tile: up to 16 go to attend_kernel; more to attend_wide_kernel, in
 // as few tiles as its 80 rows allow, of equal size.
 int attend_tile_rows(int rows) {
-  if (rows <= 32) return rows <= 16 ? 16 : 32;
+  if (rows <= 16) return 16;
   const int tiles = (rows + sv::cache::kWdMostRows - 1) / sv::cache::kWdMostRows;
   return ((rows + tiles - 1) / tiles + 15) / 16 * 16;
 }
@@ -134,7 +134,7 @@ sv_status launch_attend(sv::cache::AttendParams p, void* workspace, cudaStream_t
   p.desc = reinterpret_cast<int4*>(static_cast<unsigned char*>(workspace) + L.desc);
   p.part = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + L.part);
   static std::atomic<bool> set[64];
-  if constexpr (TR <= 32) {
+  if constexpr (TR <= 16) {
     auto kern = attend_kernel<T, D, TR / 16>;
     if (!allow_smem(set, (const void*)kern, AttendShape<T, D, TR / 16>::kSmem)) return SV_ERR_CUDA;
     kern<<<ctas, AttendShape<T, D, TR / 16>::kThreads, AttendShape<T, D, TR / 16>::kSmem, stream>>>(p);
