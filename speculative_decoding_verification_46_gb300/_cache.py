@@ -99,8 +99,16 @@ def _need_model_rows(name, t):
 
 
 def _strides_of(t):
-    """Strides of the first three dimensions (0 where there is one element)."""
-    return tuple(st if n > 1 else 0 for n, st in zip(t.shape[:3], t.stride()[:3]))
+    """Strides of the first three dimensions (0 where there is one element, which may have any)."""
+    b, i, h, _ = t.stride()
+    if b % 8 or i % 8 or h % 8:
+        return tuple(st if n > 1 else 0 for n, st in zip(t.shape[:3], (b, i, h)))
+    return b, i, h
+
+
+def _all_written(*tensors):
+    """The caller's tensors have been written (see _written)."""
+    torch.autograd.graph.increment_version([t for t in tensors if not t.is_inference()])
 
 
 def _page_of(cache, page, D, heads, device):
@@ -164,15 +172,15 @@ def plan_round(lengths, gamma, page, block_table, blocks, free_blocks, free_coun
         raise ValueError(f"gamma must be at least 0 and B * (gamma + 1) at most {SV_MAX_CACHE_ROWS}, got {gamma}")
     with _on(dev, stream):
         _read_on(stream, lengths, block_table, blocks, free_blocks, free_count, kept, gamma_b)
-        slots, positions = torch.empty(2, B, gamma + 1, dtype=_i32, device=dev).unbind(0)
+        slots = torch.empty((B, gamma + 1), dtype=_i32, device=dev)
+        positions = torch.empty((B, gamma + 1), dtype=_i32, device=dev)
         status = torch.empty(B, dtype=_i32, device=dev)
         st = sv_plan_round(B, gamma, page, N, pool, _addr(lengths), _addr(kept), _addr(gamma_b), _addr(block_table),
                            _addr(blocks), _addr(free_blocks), _addr(free_count), _addr(slots), _addr(positions),
                            _addr(status), _handle(dev))
     if st != SV_OK:
         raise SvError(st, "sv_plan_round")
-    for t in (lengths, block_table, blocks, free_blocks, free_count):
-        _written(t)
+    _all_written(lengths, block_table, blocks, free_blocks, free_count)
     return slots, positions, status
 
 
@@ -226,7 +234,8 @@ def read_kv4(cache, slots, page, dtype, *, stream=None):
     pages = _page_of(cache, page, D, None, dev)
     with _on(dev, stream):
         _read_on(stream, cache, slots)
-        k, v = torch.empty((2,) + tuple(slots.shape) + (heads, D), dtype=dtype, device=dev).unbind(0)
+        k = torch.empty((*slots.shape, heads, D), dtype=dtype, device=dev)
+        v = torch.empty((*slots.shape, heads, D), dtype=dtype, device=dev)
         st = sv_read_kv4(slots.numel(), heads, D, page, pages, _addr(cache), _TORCH_DTYPE[dtype], _addr(slots),
                          _addr(k), _addr(v), _handle(dev))
     if st != SV_OK:

@@ -97,9 +97,9 @@ sv::cache::StoreParams store_params(int R, int rows, int heads, int page, int pa
   return p;
 }
 
-// CTAs for a group of D / 8 lanes per (row, head); 0: too many
+// CTAs for a group of D / 8 lanes per (two rows, head); 0: too many
 unsigned store_grid(int R, int heads, int D) {
-  const long long ctas = ((long long)R * heads * (D / 8) + sv::cache::kStoreThreads - 1) / sv::cache::kStoreThreads;
+  const long long ctas = (((long long)R + 1) / 2 * heads * (D / 8) + sv::cache::kStoreThreads - 1) / sv::cache::kStoreThreads;
   return ctas > 0x7fffffffll ? 0u : (unsigned)ctas;
 }
 
@@ -197,6 +197,7 @@ extern "C" sv_status sv_plan_round(int B, int gamma, int page, int N, int pool, 
   p.page = page;
   p.N = N;
   p.pool = pool;
+  p.whole = aligned16(slots) && aligned16(positions);
   p.lengths = lengths;
   p.kept = kept;
   p.gamma_b = gamma_b;
@@ -210,14 +211,29 @@ extern "C" sv_status sv_plan_round(int B, int gamma, int page, int N, int pool, 
   static std::atomic<bool> set[64];
   if (!allow_smem(set, (const void*)sv::cache::plan_round_kernel, sv::cache::plan_smem(SV_MAX_PLAN_SEQUENCES)))
     return SV_ERR_CUDA;
-  const int ctas = (long long)B * p.rows > sv::cache::kPlanFew ? sv::cache::kPlanCtas : 1;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  p.ids = SV_MAX_CACHE_SLOTS / page;
+  p.slots_here = (long long)B * p.rows <= sv::cache::kPlanFew;
   cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = ctas;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  return launch(sv::cache::plan_round_kernel, dim3(ctas), sv::cache::kPlanThreads, sv::cache::plan_smem(B),
-                reinterpret_cast<cudaStream_t>(stream), p, attr);
+  sv_status st;
+  if ((long long)B * p.rows <= sv::cache::kPlanMany) {
+    sv::cache::plan_round_kernel<<<1, sv::cache::kPlanThreads, sv::cache::plan_smem(B), s>>>(p);
+    st = launched();
+  } else {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = sv::cache::kPlanCtas;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    st = launch(sv::cache::plan_round_kernel, dim3(sv::cache::kPlanCtas), sv::cache::kPlanThreads, sv::cache::plan_smem(B), s, p,
+                attr);
+  }
+  if (st != SV_OK || p.slots_here) return st;
+  const long long groups = (long long)B * ((p.rows + 3) / 4);
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  return launch(sv::cache::plan_slots_kernel,
+                dim3((unsigned)((groups + sv::cache::kPlanSlotThreads - 1) / sv::cache::kPlanSlotThreads)),
+                sv::cache::kPlanSlotThreads, 0, s, p, attr);
 }
 
 extern "C" sv_status sv_append_kv4(int B, int gamma, int heads, int D, int page, int pages, const void* k,

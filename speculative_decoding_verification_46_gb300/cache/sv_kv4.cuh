@@ -1,9 +1,11 @@
 // The 4-bit cache's format (include/specverify_cache.h) and the kernels that
 // write rows into it and read them back.
 //
-// A row of D elements is 8 elements a lane: D / 8 lanes (16 or 8) of a warp
-// take a row, so a warp has 2 or 4 of them.  Least and greatest element by
-// shuffles, then every lane forms its 8 codes: one word.
+// Both move every byte once and are bound by HBM as long as a row costs few
+// instructions.  D / 8 lanes (16 or 8) have eight channels each of two
+// neighbouring rows of a head, so that a lane has four loads of 16 bytes on
+// the way and, where the rows' slots are neighbours too, writes the two
+// tokens' interleaved value codes as whole words.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -53,47 +55,93 @@ struct StoreParams {
 
 constexpr int kStoreThreads = 256;
 
+// Elements two at a time.
+template <typename T> struct Kv2;
+template <> struct Kv2<__nv_bfloat16> {
+  using V = __nv_bfloat162;
+  // 128 + n for the codes n of 0x000f of both halves, less 128
+  static constexpr uint32_t kMagic = 0x43004300u, kBase = 0x43004300u;
+};
+template <> struct Kv2<__half> {
+  using V = __half2;
+  static constexpr uint32_t kMagic = 0x64006400u, kBase = 0x64006400u;   // 1024 + n
+};
+template <typename V>
+__device__ __forceinline__ V as_two(uint32_t x) { return *reinterpret_cast<const V*>(&x); }
+template <typename V>
+__device__ __forceinline__ uint32_t as_bits(V x) { return *reinterpret_cast<const uint32_t*>(&x); }
+
+struct F2x {                         // two float32
+  unsigned long long v;
+};
+__device__ __forceinline__ F2x f2x(float a, float b) {
+  F2x p;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(p.v) : "f"(a), "f"(b));
+  return p;
+}
+__device__ __forceinline__ void f2x_split(F2x p, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p.v)); }
+__device__ __forceinline__ F2x f2x_add(F2x a, F2x b) {
+  F2x d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+  return d;
+}
+__device__ __forceinline__ F2x f2x_fma(F2x a, F2x b, F2x c) {
+  F2x d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return d;
+}
+
 // One row's codes (8 of a lane's elements, 4 bits each from the low end) and
 // its scale and offset as bits; LANES lanes hold the row.
 template <typename T, int LANES>
 __device__ __forceinline__ uint32_t quantise(const uint4& x, uint32_t& numbers) {
-  float f[8];
+  using V = typename Kv2<T>::V;
+  // the least element and the least negative of one, side by side; NaN stays
+  const V lo2 = __hmin2_nan(__hmin2_nan(as_two<V>(x.x), as_two<V>(x.y)), __hmin2_nan(as_two<V>(x.z), as_two<V>(x.w)));
+  const V hi2 = __hmax2_nan(__hmax2_nan(as_two<V>(x.x), as_two<V>(x.y)), __hmax2_nan(as_two<V>(x.z), as_two<V>(x.w)));
+  const uint32_t a = as_bits(lo2), b = as_bits(hi2) ^ 0x80008000u;
+  V both = __hmin2_nan(as_two<V>(__byte_perm(a, b, 0x5410)), as_two<V>(__byte_perm(a, b, 0x7632)));
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint32_t w = j == 0 ? x.x : j == 1 ? x.y : j == 2 ? x.z : x.w;
-    f[2 * j] = Kv<T>::lo(w);
-    f[2 * j + 1] = Kv<T>::hi(w);
-  }
-  float least = f[0], most = f[0], bad = f[0] - f[0];   // 0, or NaN where an element is not finite
-#pragma unroll
-  for (int j = 1; j < 8; ++j) {
-    least = fminf(least, f[j]);
-    most = fmaxf(most, f[j]);
-    bad += f[j] - f[j];
-  }
-#pragma unroll
-  for (int m = LANES / 2; m >= 1; m >>= 1) {
-    least = fminf(least, __shfl_xor_sync(0xffffffffu, least, m));
-    most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, m));
-    bad += __shfl_xor_sync(0xffffffffu, bad, m);
-  }
+  for (int m = LANES / 2; m >= 1; m >>= 1) both = __hmin2_nan(both, as_two<V>(__shfl_xor_sync(0xffffffffu, as_bits(both), m)));
+  const uint32_t ends = as_bits(both);
+  const float least = Kv<T>::lo(ends), most = -Kv<T>::hi(ends);
   const uint32_t sb = Kv<T>::bits(__fdiv_rn(most - least, 15.f));
   const float scale = Kv<T>::lo(sb);
-  if (!(scale + bad < __int_as_float(0x7f800000))) {   // not finite, or a NaN
+  if (!(scale < __int_as_float(0x7f800000))) {   // an element is not finite, or the scale
     const uint32_t nan = Kv<T>::bits(__int_as_float(0x7fffffff));
     numbers = nan | nan << 16;
     return 0;
   }
-  numbers = sb | Kv<T>::bits(least) << 16;
+  numbers = sb | ends << 16;
   const float inverse = scale < 1.17549435e-38f ? 0.f : __frcp_rn(scale);
-  uint32_t codes = 0;
+  const F2x minus = f2x(-least, -least);
+  // added and taken away again, 3 2^22 rounds to whole numbers, ties to even
+  const F2x magic = f2x(12582912.f, 12582912.f), back = f2x(-12582912.f, -12582912.f);
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  F2x c[4];                                      // codes i and i + 4
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    // (the product is at least 0)
-    const uint32_t n = __float2uint_rn(__fmul_rn(__fadd_rn(f[j], -least), inverse));
-    codes |= min(n, 15u) << (4 * j);
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t p = w[i >> 1], q = w[2 + (i >> 1)];
+    const F2x f = i & 1 ? f2x(Kv<T>::hi(p), Kv<T>::hi(q)) : f2x(Kv<T>::lo(p), Kv<T>::lo(q));
+    float y0, y1;
+    f2x_split(f2x_add(f, minus), y0, y1);
+    // (single products: paired ones are fused with the addition behind them,
+    // which takes away their rounding)
+    y0 = __fmul_rn(y0, inverse);
+    y1 = __fmul_rn(y1, inverse);
+    if (std::is_same<T, __half>::value) {
+      // (a scale below the normal numbers may be rounded far down; others leave y below 15.5)
+      y0 = fminf(y0, 15.f);
+      y1 = fminf(y1, 15.f);
+    }
+    c[i] = f2x_add(f2x_add(f2x(y0, y1), magic), back);
   }
-  return codes;
+  const F2x k16 = f2x(16.f, 16.f);
+  // (the sum of four codes' places stays exact)
+  const F2x sum = f2x_add(f2x_fma(f2x_fma(f2x_fma(c[3], k16, c[2]), k16, c[1]), k16, c[0]), f2x(8388608.f, 8388608.f));
+  float s0, s1;
+  f2x_split(sum, s0, s1);
+  return __byte_perm(__float_as_uint(s0), __float_as_uint(s1), 0x5410);
 }
 
 // Bytes from a block's start to the 8 codes of channels 8 l .. of token t.
@@ -105,66 +153,115 @@ __device__ __forceinline__ int value_at(int page, int t, int l) { return page * 
 template <int D>
 __device__ __forceinline__ int numbers_at(int page, int t) { return page * D + 8 * t; }
 
-// A lane group of D / 8 lanes per (row, head): its key, then its value.
+// Where rows 2 i, 2 i + 1 of a lane group are.
+struct RowPair {
+  int r, h;                // first row, head
+  int slot[2];             // -1: none
+  bool next;               // the second slot is the first one's odd neighbour
+};
+__device__ __forceinline__ RowPair row_pair(const StoreParams& p, long long item) {
+  RowPair x;
+  const long long pairs = ((long long)p.R + 1) / 2;
+  const long long i = item / p.H;
+  x.h = (int)(item - i * p.H);
+  x.r = i < pairs ? 2 * (int)i : 0;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int slot = i < pairs && x.r + j < p.R ? __ldg(p.slots + x.r + j) : -1;
+    x.slot[j] = slot >= 0 && slot < p.slots_end ? slot : -1;
+  }
+  x.next = x.slot[0] >= 0 && (x.slot[0] & 1) == 0 && x.slot[1] == x.slot[0] + 1;
+  return x;
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kStoreThreads) append_kv4_kernel(const __grid_constant__ StoreParams p) {
   constexpr int LANES = D / 8;
-  const long long item = ((long long)blockIdx.x * kStoreThreads + threadIdx.x) / LANES;
   const int l = threadIdx.x % LANES;
-  const long long items = (long long)p.R * p.H;
-  const int r = item < items ? (int)(item / p.H) : 0, h = item < items ? (int)(item % p.H) : 0;
-  const int slot = item < items ? p.slots[r] : -1;
-  const bool there = slot >= 0 && slot < p.slots_end;
-  if (!__any_sync(0xffffffffu, there)) return;
-  uint4 xk = make_uint4(0, 0, 0, 0), xv = xk;
-  if (there) {
-    const int b = r / p.rows, i = r - b * p.rows;
-    xk = __ldcs(reinterpret_cast<const uint4*>(static_cast<const T*>(p.k) + b * p.ks[0] + i * p.ks[1] + h * p.ks[2]) + l);
-    xv = __ldcs(reinterpret_cast<const uint4*>(static_cast<const T*>(p.v) + b * p.vs[0] + i * p.vs[1] + h * p.vs[2]) + l);
+  const RowPair pair = row_pair(p, ((long long)blockIdx.x * kStoreThreads + threadIdx.x) / LANES);
+  if (!__any_sync(0xffffffffu, pair.slot[0] >= 0 || pair.slot[1] >= 0)) return;
+  uint4 xk[2], xv[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    xk[j] = xv[j] = make_uint4(0, 0, 0, 0);
+    if (pair.slot[j] >= 0) {
+      const int r = pair.r + j, b = r / p.rows, i = r - b * p.rows;
+      xk[j] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const T*>(p.k) + b * p.ks[0] + i * p.ks[1] + pair.h * p.ks[2]) + l);
+      xv[j] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const T*>(p.v) + b * p.vs[0] + i * p.vs[1] + pair.h * p.vs[2]) + l);
+    }
   }
-  uint32_t nk, nv;
-  const uint32_t ck = quantise<T, LANES>(xk, nk), cv = quantise<T, LANES>(xv, nv);
-  if (!there) return;
-  const int page = slot / p.page, t = slot - page * p.page;
-  unsigned char* block = p.cache + ((long long)page * p.H + h) * ((long long)p.page * kTokenBytes<D>);
-  *reinterpret_cast<uint32_t*>(block + key_at<D>(t, l)) = ck;
-  unsigned char* at = block + value_at<D>(p.page, t, l);
-  *reinterpret_cast<unsigned short*>(at) = (unsigned short)cv;
-  *reinterpret_cast<unsigned short*>(at + 4) = (unsigned short)(cv >> 16);
-  if (l == 0) *reinterpret_cast<uint2*>(block + numbers_at<D>(p.page, t)) = make_uint2(nk, nv);
+  uint32_t ck[2], cv[2], nk[2], nv[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    ck[j] = quantise<T, LANES>(xk[j], nk[j]);
+    cv[j] = quantise<T, LANES>(xv[j], nv[j]);
+  }
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    if (pair.slot[j] < 0) continue;
+    const int page = pair.slot[j] / p.page, t = pair.slot[j] - page * p.page;
+    unsigned char* block = p.cache + ((long long)page * p.H + pair.h) * ((long long)p.page * kTokenBytes<D>);
+    *reinterpret_cast<uint32_t*>(block + key_at<D>(t, l)) = ck[j];
+    if (!pair.next) {
+      unsigned char* at = block + value_at<D>(p.page, t, l);
+      *reinterpret_cast<unsigned short*>(at) = (unsigned short)cv[j];
+      *reinterpret_cast<unsigned short*>(at + 4) = (unsigned short)(cv[j] >> 16);
+    } else if (j == 0) {
+      *reinterpret_cast<uint2*>(block + value_at<D>(p.page, t, l)) =
+          make_uint2(__byte_perm(cv[0], cv[1], 0x5410), __byte_perm(cv[0], cv[1], 0x7632));
+    }
+    if (l == 0) *reinterpret_cast<uint2*>(block + numbers_at<D>(p.page, t)) = make_uint2(nk[j], nv[j]);
+  }
 }
 
+// Eight elements from their codes; scale * code + offset rounds once.
 template <typename T>
 __device__ __forceinline__ uint4 held(uint32_t codes, uint32_t numbers) {
-  const float scale = Kv<T>::lo(numbers), offset = Kv<T>::hi(numbers);
-  float f[8];
+  using V = typename Kv2<T>::V;
+  const V scale = as_two<V>(__byte_perm(numbers, numbers, 0x1010)), offset = as_two<V>(__byte_perm(numbers, numbers, 0x3232));
+  uint32_t y[4];                                 // elements i and i + 4
 #pragma unroll
-  for (int j = 0; j < 8; ++j) f[j] = __fmaf_rn((float)(codes >> (4 * j) & 15u), scale, offset);
-  return make_uint4(Kv<T>::pack(f[0], f[1]), Kv<T>::pack(f[2], f[3]), Kv<T>::pack(f[4], f[5]), Kv<T>::pack(f[6], f[7]));
+  for (int i = 0; i < 4; ++i) {
+    const V n = __hsub2(as_two<V>((codes >> (4 * i) & 0x000f000fu) | Kv2<T>::kMagic), as_two<V>(Kv2<T>::kBase));
+    y[i] = as_bits(__hfma2(n, scale, offset));
+  }
+  return make_uint4(__byte_perm(y[0], y[1], 0x5410), __byte_perm(y[2], y[3], 0x5410), __byte_perm(y[0], y[1], 0x7632),
+                    __byte_perm(y[2], y[3], 0x7632));
 }
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kStoreThreads) read_kv4_kernel(const __grid_constant__ StoreParams p) {
   constexpr int LANES = D / 8;
-  const long long item = ((long long)blockIdx.x * kStoreThreads + threadIdx.x) / LANES;
   const int l = threadIdx.x % LANES;
-  if (item >= (long long)p.R * p.H) return;
-  const int r = (int)(item / p.H), h = (int)(item % p.H);
-  const int slot = p.slots[r];
-  uint4 xk = make_uint4(0, 0, 0, 0), xv = xk;
-  if (slot >= 0 && slot < p.slots_end) {
-    const int page = slot / p.page, t = slot - page * p.page;
-    const unsigned char* block = p.cache + ((long long)page * p.H + h) * ((long long)p.page * kTokenBytes<D>);
-    const uint32_t ck = *reinterpret_cast<const uint32_t*>(block + key_at<D>(t, l));
-    const unsigned char* at = block + value_at<D>(p.page, t, l);
-    const uint32_t cv = *reinterpret_cast<const unsigned short*>(at) |
-                        (uint32_t) * reinterpret_cast<const unsigned short*>(at + 4) << 16;
-    const uint2 n = *reinterpret_cast<const uint2*>(block + numbers_at<D>(p.page, t));
-    xk = held<T>(ck, n.x);
-    xv = held<T>(cv, n.y);
+  const long long item = ((long long)blockIdx.x * kStoreThreads + threadIdx.x) / LANES;
+  if (item >= ((long long)p.R + 1) / 2 * p.H) return;
+  const RowPair pair = row_pair(p, item);
+  uint32_t ck[2] = {0, 0}, cv[2] = {0, 0};
+  uint2 n[2] = {make_uint2(0, 0), make_uint2(0, 0)};
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    if (pair.slot[j] < 0) continue;
+    const int page = pair.slot[j] / p.page, t = pair.slot[j] - page * p.page;
+    const unsigned char* block = p.cache + ((long long)page * p.H + pair.h) * ((long long)p.page * kTokenBytes<D>);
+    ck[j] = *reinterpret_cast<const uint32_t*>(block + key_at<D>(t, l));
+    if (!pair.next) {
+      const unsigned char* at = block + value_at<D>(p.page, t, l);
+      cv[j] = *reinterpret_cast<const unsigned short*>(at) | (uint32_t) * reinterpret_cast<const unsigned short*>(at + 4) << 16;
+    } else if (j == 0) {
+      const uint2 x = *reinterpret_cast<const uint2*>(block + value_at<D>(p.page, t, l));
+      cv[0] = __byte_perm(x.x, x.y, 0x5410);
+      cv[1] = __byte_perm(x.x, x.y, 0x7632);
+    }
+    n[j] = *reinterpret_cast<const uint2*>(block + numbers_at<D>(p.page, t));
   }
-  __stcs(static_cast<uint4*>(p.ko) + item * LANES + l, xk);
-  __stcs(static_cast<uint4*>(p.vo) + item * LANES + l, xv);
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    if (pair.r + j >= p.R) continue;
+    // (without a slot: codes, scale and offset 0)
+    const long long at = ((long long)(pair.r + j) * p.H + pair.h) * LANES + l;
+    __stcs(static_cast<uint4*>(p.ko) + at, held<T>(ck[j], n[j].x));
+    __stcs(static_cast<uint4*>(p.vo) + at, held<T>(cv[j], n[j].y));
+  }
 }
 
 }  // namespace cache

@@ -11,16 +11,23 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "../csrc/sv_device.cuh"
+
 namespace sv {
 namespace cache {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanCtas = 8;        // of a cluster with many rows
-constexpr int kPlanFew = 8192;      // rows that one CTA takes
+constexpr int kPlanFew = 4096;      // rows whose slots the first kernel forms; those of more are a kernel of their own
+constexpr int kPlanMany = 65536;    // rows whose pages are moved by more CTAs than one
+constexpr int kPlanSlotThreads = 256;
 constexpr int kNoPages = 1, kTooLong = 2;
 
 struct PlanParams {
   int B, rows, page, N, pool;       // rows: gamma + 1
+  int ids;                          // page ids below it give slots below 2^30
+  bool slots_here;                  // plan_round_kernel forms the slots too
+  bool whole;                       // slots and positions are 16-byte aligned
   int32_t* lengths;
   const int32_t *kept, *gamma_b;
   int32_t *table, *blocks, *free_blocks, *free_count, *slots, *positions, *status;
@@ -60,6 +67,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_round_kernel(const __grid_c
   int* length = held + p.B;        // its new length
   int* part = length + p.B;        // its rows, and its status << 28
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_launch_dependents();
   const unsigned rank = cluster_rank();
   unsigned ctas;
   asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(ctas));
@@ -158,24 +166,65 @@ __global__ void __launch_bounds__(kPlanThreads) plan_round_kernel(const __grid_c
     const int b = sequence_of(takes, p.B, x);
     p.table[(long long)b * p.N + held[b] + (x - takes[b])] = __ldcg(p.free_blocks + (there - 1 - x));
   }
+  if (!p.slots_here) return;
   cluster_barrier();
 
   // (4)
   const int cells = p.B * p.rows;
+#pragma unroll 4
   for (int x = at; x < cells; x += NT) {
     const int b = x / p.rows, i = x - b * p.rows;
-    const int st = part[b] >> 28, n = part[b] & 0x0fffffff;
     int slot = -1, position = 0;
-    if (i < n) {
+    if (i < (part[b] & 0x0fffffff)) {
       position = (int)min((long long)length[b] + i, 0x7fffffffll);
-      if (st == 0) {
+      if (part[b] >> 28 == 0) {
         const int c = position / p.page;
         const int id = __ldcg(p.table + (long long)b * p.N + c);
-        if (id >= 0 && id < (1 << 30) / p.page) slot = id * p.page + (position - c * p.page);
+        if (id >= 0 && id < p.ids) slot = id * p.page + (position - c * p.page);
       }
     }
     p.slots[x] = slot;
     p.positions[x] = position;
+  }
+}
+
+// Slots and positions of many rows, behind the kernel above (which then leaves
+// them out): a thread has four neighbouring rows of one sequence, which lie in
+// two pages at most.
+__global__ void __launch_bounds__(kPlanSlotThreads) plan_slots_kernel(const __grid_constant__ PlanParams p) {
+  const int groups = (p.rows + 3) / 4;      // of a sequence
+  const long long x = (long long)blockIdx.x * kPlanSlotThreads + threadIdx.x;
+  const int b = (int)(x / groups), i = 4 * (int)(x - (long long)b * groups);
+  pdl_wait();
+  if (b >= p.B) return;
+  const int n = p.gamma_b ? min(max(p.gamma_b[b], -1), p.rows - 1) + 1 : p.rows;
+  const long long first = (long long)p.lengths[b] + i;
+  const bool fine = p.status[b] == 0 && i < n;
+  const int c = fine ? (int)(first / p.page) : 0, t = fine ? (int)first - c * p.page : 0;
+  int id[2] = {-1, -1};
+  if (fine) {
+    id[0] = p.table[(long long)b * p.N + c];
+    if (t + min(n - i, 4) > p.page) id[1] = p.table[(long long)b * p.N + c + 1];
+  }
+  int slot[4], position[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int over = t + j >= p.page;
+    const int page = id[over];
+    slot[j] = fine && i + j < n && page >= 0 && page < p.ids ? page * p.page + t + j - over * p.page : -1;
+    position[j] = i + j < n ? (int)min(first + j, 0x7fffffffll) : 0;
+  }
+  const long long to = (long long)b * p.rows + i;
+  if (p.rows % 4 == 0 && p.whole) {
+    *reinterpret_cast<int4*>(p.slots + to) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+    *reinterpret_cast<int4*>(p.positions + to) = make_int4(position[0], position[1], position[2], position[3]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (i + j < p.rows) {
+        p.slots[to + j] = slot[j];
+        p.positions[to + j] = position[j];
+      }
   }
 }
 
