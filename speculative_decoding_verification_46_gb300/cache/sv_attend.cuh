@@ -18,6 +18,11 @@
 // eight tokens is taken as n - 15 (the sign bit and the complement, in the same
 // AND and XOR), and its offset as o' + 15 s'.
 //
+// Tokens and channels are the products' left side and the rows their right one,
+// so that eight rows cost half of what sixteen do: scores^T [16 tokens x 8 rows]
+// = codes . q^T, sums^T [16 channels x 8 rows] += (value codes)^T . weights^T.  A
+// lane then has two rows of every 16 tokens' two, and their numbers once.
+//
 // Work: the (sequence, head, row tile)s' tokens in units of 128 are one line of
 // units; CTA i of W takes an equal part of it, finds its place from lengths
 // and walks on.  The warps of a CTA take 32 tokens at a time each, with a
@@ -57,10 +62,23 @@ struct AttendParams {
 // Floats of a part of TR rows.
 __host__ __device__ constexpr int part_floats(int TR, int D) { return TR * (D + 2); }
 
-__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+// c [16 x 8] += a [16 x 16] . b [16 x 8]
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// an 8 x 8 matrix of 16-bit elements, two of a row a lane, transposed
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+// (a & b) ^ c
+__device__ __forceinline__ uint32_t and_xor(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
 }
 __device__ __forceinline__ uint32_t half2_bits(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
@@ -182,9 +200,9 @@ struct Segment {
 
 // 32 tokens of one head in a warp's ring: two subs of 16, each its keys, then
 // its values, then (behind both) its numbers, as they lie in the cache.  As
-// operands, lane (g, c) = (lane / 4, lane % 4) takes the key codes of token
-// 8 j + g, quarter c; the value codes of tokens 8 j + 2 c and + 1, eighth g;
-// those two tokens' numbers (j = 0, 1).
+// operands, lane (g, c) = (lane / 4, lane % 4) takes the key codes of tokens g
+// and 8 + g of a sub, quarter c; the value codes of its tokens 2 c, 2 c + 1 and 8
+// more, eighth g; the numbers of tokens g and 8 + g.
 template <int D>
 struct Stage {
   static constexpr int kCodes = 8 * D;                       // bytes of a sub's keys, and of its values
@@ -242,12 +260,13 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
-template <typename T, int D, int MT>
+// NT: groups of eight rows
+template <typename T, int D, int NT>
 struct AttendShape {
-  static constexpr int TR = 16 * MT;      // rows of a tile
-  static constexpr int kCtas = MT == 1 ? 3 : 2;              // an SM
+  static constexpr int TR = 8 * NT;       // rows of a tile
+  static constexpr int kCtas = NT == 1 ? 4 : NT == 2 ? 3 : 2;   // an SM
   static constexpr int kWarps = 4, kThreads = 32 * kWarps;
-  static constexpr int kQ = MT * (D / 16) * 512;             // q as operands
+  static constexpr int kQ = NT * (D / 32) * 512;             // q as operands
   // a warp's ring, which its sums take the place of at the end of a segment
   static constexpr int kRing = kAtStages * Stage<D>::kBytes;
   static constexpr int kSums = (TR * D + 2 * TR) * 4;
@@ -258,11 +277,12 @@ struct AttendShape {
 
 // Position of a group of four channels (dg) of row r in a warp's sums in
 // shared memory: lanes that write at once go to different banks.
-__device__ __forceinline__ int swizzled(int r, int dg) { return dg ^ ((dg >> 3) | (r & 1) << 2); }
+template <int D>
+__device__ __forceinline__ int swizzled(int r, int dg) { return dg ^ ((r >> 1 & 3) << (D == 128 ? 0 : 2)); }
 
-template <typename T, int D, int MT>
-__global__ void __launch_bounds__(AttendShape<T, D, MT>::kThreads, AttendShape<T, D, MT>::kCtas) attend_kernel(const __grid_constant__ AttendParams p) {
-  using S = AttendShape<T, D, MT>;
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(AttendShape<T, D, NT>::kThreads, AttendShape<T, D, NT>::kCtas) attend_kernel(const __grid_constant__ AttendParams p) {
+  using S = AttendShape<T, D, NT>;
   constexpr int KW = D / 32, TR = S::TR, kWarpFloats = S::kWarp / 4, LANES = D / 8;
   constexpr int kWarps = S::kWarps, kThreads = S::kThreads;
   constexpr bool kFine = std::is_same<T, __half>::value;     // the weights' rest is an operand too
@@ -283,6 +303,7 @@ __global__ void __launch_bounds__(AttendShape<T, D, MT>::kThreads, AttendShape<T
 
   const long long block_bytes = (long long)p.page * kTokenBytes<D>;
   const int page_tiles = p.page / 16;
+  const uint32_t zero = (uint32_t)p.page >> 16;              // which the compiler does not know
   const uint32_t q_at = (uint32_t)__cvta_generic_to_shared(at_sm) + lane * 16;
   const uint32_t ring = (uint32_t)__cvta_generic_to_shared(all_sums + warp * kWarpFloats);
   while (u < line.end) {
@@ -411,33 +432,30 @@ __global__ void __launch_bounds__(AttendShape<T, D, MT>::kThreads, AttendShape<T
         const int x = tid + k * kThreads, rl = x / LANES, word = x % LANES;
         if (rl >= TR) break;
         const uint32_t w[4] = {qv[k].x, qv[k].y, qv[k].z, qv[k].w};
-        // word j of quarter cc; channels 2 t, 2 t + 4 as they are, 2 t + 1,
-        // 2 t + 5 for codes of 16 times their size
-        const int cc = word / KW, j = word % KW, m = rl >> 4, e = rl >> 3 & 1;
-        uint32_t* to_q = reinterpret_cast<uint32_t*>(at_sm) + ((m * 2 * KW + 2 * j) * 32 + (rl & 7) * 4 + cc) * 4 + e;
+        // word j of quarter cc: halves t; channels 2 t, 2 t + 4 as they are,
+        // 2 t + 1, 2 t + 5 for codes of 16 times their size
+        const int cc = word / KW, j = word % KW;
+        uint32_t y[4];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          to_q[t * 128] = half2_bits(Kv<T>::lo(w[t]) * raise, Kv<T>::lo(w[t + 2]) * raise);
-          to_q[t * 128 + 2] = half2_bits(Kv<T>::hi(w[t]) * raise * 0.0625f, Kv<T>::hi(w[t + 2]) * raise * 0.0625f);
+          y[2 * t] = half2_bits(Kv<T>::lo(w[t]) * raise, Kv<T>::lo(w[t + 2]) * raise);
+          y[2 * t + 1] = half2_bits(Kv<T>::hi(w[t]) * raise * 0.0625f, Kv<T>::hi(w[t + 2]) * raise * 0.0625f);
         }
+        reinterpret_cast<uint4*>(at_sm)[((rl >> 3) * KW + j) * 32 + (rl & 7) * 4 + cc] = make_uint4(y[0], y[1], y[2], y[3]);
       }
       __syncthreads();
     }
 
-    float ref[MT][2];
-    Two q_sum[MT][2], mass[MT][2], shift[MT][2];          // mass, shift: of the lane's even and odd tokens
-    float o[MT][4 * KW][4];
+    // rows 8 m + 2 c and + 1
+    Two q_sum[NT], minus_ref[NT], mass[NT], shift[NT];
+    float o[NT][2 * KW][4];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
+    for (int m = 0; m < NT; ++m) {
+      const float2 q = *reinterpret_cast<const float2*>(q_sums + 8 * m + 2 * c);
+      q_sum[m] = two(q.x, q.y);
+      minus_ref[m] = mass[m] = shift[m] = two(0.f, 0.f);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float q = q_sums[m * 16 + e * 8 + g];
-        q_sum[m][e] = two(q, q);
-        ref[m][e] = 0.f;
-        mass[m][e] = shift[m][e] = two(0.f, 0.f);
-      }
-#pragma unroll
-      for (int t = 0; t < 4 * KW; ++t)
+      for (int t = 0; t < 2 * KW; ++t)
 #pragma unroll
         for (int x = 0; x < 4; ++x) o[m][t][x] = 0.f;
     }
@@ -445,77 +463,79 @@ __global__ void __launch_bounds__(AttendShape<T, D, MT>::kThreads, AttendShape<T
     // The first group sets the references.  A row that sees none of it sees
     // none of the later ones: its mass stays 0.
     bool fresh = true;
+    const uint32_t flip = 0x800f800fu + zero, flip16 = 0x80f080f0u + zero;   // (registers: an instruction takes one constant)
 
     auto group = [&](auto masked_group, int token0, uint32_t subs, uint32_t from) {
       constexpr bool kMasked = decltype(masked_group)::value;
-      // scores: q . n for 32 tokens, four groups of eight
-      float z[MT][4][4];
+      // scores: q . n for 32 tokens; z[i][m]: tokens g, 8 + g of sub i, two rows each
+      float z[2][NT][4];
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int m = 0; m < NT; ++m)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) z[m][j][e] = 0.f;
+          for (int e = 0; e < 4; ++e) z[i][m][e] = 0.f;
       {
-        uint32_t kw[4][KW];
+        uint32_t kw[2][2][KW];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          shared_words(kw[j], from + (j >> 1) * 2 * Stage<D>::kCodes + (8 * (j & 1) + g) * (D / 2) + c * (D / 8));
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int w = 0; w < KW; ++w)
+          for (int e = 0; e < 2; ++e)
+            shared_words(kw[i][e], from + i * 2 * Stage<D>::kCodes + (8 * e + g) * (D / 2) + c * (D / 8));
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            uint32_t qf[MT][4];
+        for (int w = 0; w < KW; ++w) {
+          uint32_t qf[NT][4];
 #pragma unroll
-            for (int m = 0; m < MT; ++m) shared_words(qf[m], q_at + (m * 2 * KW + 2 * w + half) * 512);
+          for (int m = 0; m < NT; ++m) shared_words(qf[m], q_at + (m * KW + w) * 512);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const uint32_t k = kw[j][w] >> (8 * half);
+          for (int half = 0; half < 2; ++half)
 #pragma unroll
-              for (int m = 0; m < MT; ++m) mma16816(z[m][j], qf[m], k & 0x000f000fu, k & 0x00f000f0u);
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t x = kw[i][0][w] >> (8 * half), y = kw[i][1][w] >> (8 * half);
+              const uint32_t a0 = x & 0x000f000fu, a1 = y & 0x000f000fu, a2 = x & 0x00f000f0u, a3 = y & 0x00f000f0u;
+#pragma unroll
+              for (int m = 0; m < NT; ++m) mma16816(z[i][m], a0, a1, a2, a3, qf[m][2 * half], qf[m][2 * half + 1]);
             }
-          }
-      }
-      // the numbers of the two tokens of each group of eight
-      uint32_t nv[4][2];
-      float most = -FLT_MAX, largest = 0.f;
-      const int t0 = token0 + 2 * c;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint32_t nw[4];
-        shared_words(nw, from + Stage<D>::kNumbers + (8 * j + 2 * c) * 8);
-        if (kMasked) {
-          // those of tokens that nobody sees may be anything
-          const bool sub = subs >> (j >> 1) & 1;
-          if (!sub || t0 + 8 * j >= s.seen) nw[0] = nw[1] = 0;
-          if (!sub || t0 + 8 * j + 1 >= s.seen) nw[2] = nw[3] = 0;
         }
-        const Two scale2 = two(row_scale, row_scale);
-        const Two ks = mul2(two(Kv<T>::lo(nw[0]), Kv<T>::lo(nw[2])), scale2);
-        const Two ko = mul2(two(Kv<T>::hi(nw[0]), Kv<T>::hi(nw[2])), scale2);
-        nv[j][0] = nw[1];
-        nv[j][1] = nw[3];
-        largest = max3(largest, Kv<T>::lo(nw[1]), Kv<T>::lo(nw[3]));
+      }
+      // whether rows 8 m + 2 c and + 1 see token 8 e + g of sub i
+      auto sees = [&](int m, int i, int e) {
+        const int2 lim = *reinterpret_cast<const int2*>(limits + 8 * m + 2 * c);
+        const int t = subs >> i & 1 ? token0 + 16 * i + 8 * e + g : 0x7fffffff;
+        return make_int2(t <= lim.x, t <= lim.y);
+      };
+      uint32_t nv[2][2];                  // the values' numbers
+      float most = -FLT_MAX, largest = 0.f;
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
+        for (int e = 0; e < 2; ++e) {
+          uint32_t x[2];
+          shared_words(x, from + Stage<D>::kNumbers + (16 * i + 8 * e + g) * 8);
+          // (those of tokens that nobody sees may be anything)
+          if (kMasked && (!(subs >> i & 1) || token0 + 16 * i + 8 * e + g >= s.seen)) x[0] = x[1] = 0;
+          nv[i][e] = x[1];
+          const float k_scale = Kv<T>::lo(x[0]) * row_scale, k_offset = Kv<T>::hi(x[0]) * row_scale;
+          const Two ks = two(k_scale, k_scale), ko = two(k_offset, k_offset);
+          largest = fmaxf(largest, Kv<T>::lo(x[1]));
+#pragma unroll
+          for (int m = 0; m < NT; ++m) {
             float y0, y1;
-            split(fma2(two(z[m][j][2 * r], z[m][j][2 * r + 1]), ks, fma2(ko, q_sum[m][r], two(-ref[m][r], -ref[m][r]))), y0, y1);
+            split(fma2(two(z[i][m][2 * e], z[i][m][2 * e + 1]), ks, fma2(ko, q_sum[m], minus_ref[m])), y0, y1);
             if (kMasked) {
-              const int lim = subs >> (j >> 1) & 1 ? limits[m * 16 + 8 * r + g] : -1;
-              if (t0 + 8 * j > lim) y0 = __int_as_float(0xff800000);
-              if (t0 + 8 * j + 1 > lim) y1 = __int_as_float(0xff800000);
+              const int2 see = sees(m, i, e);
+              if (!see.x) y0 = __int_as_float(0xff800000);
+              if (!see.y) y1 = __int_as_float(0xff800000);
             }
-            z[m][j][2 * r] = y0;
-            z[m][j][2 * r + 1] = y1;
+            z[i][m][2 * e] = y0;
+            z[i][m][2 * e + 1] = y1;
             most = max3(most, y0, y1);
           }
-      }
-      if (fresh || __any_sync(0xffffffffu, most > kAtSlack || largest * value_scale > kAtValueTop)) {
+        }
+      if (__any_sync(0xffffffffu, fresh || most > kAtSlack || largest * value_scale > kAtValueTop)) {
         // a row's terms outgrow its reference, or the values' scales theirs
-        largest = fmaxf(largest, __shfl_xor_sync(0xffffffffu, largest, 1));
-        largest = fmaxf(largest, __shfl_xor_sync(0xffffffffu, largest, 2));
+#pragma unroll
+        for (int x = 4; x <= 16; x <<= 1) largest = fmaxf(largest, __shfl_xor_sync(0xffffffffu, largest, x));
         float by = 1.f;
         if (largest * value_scale > kAtValueTop) {
           // largest < 2^(e - 126): 2^(133 - e) brings it below 2^7
@@ -524,31 +544,35 @@ __global__ void __launch_bounds__(AttendShape<T, D, MT>::kThreads, AttendShape<T
           by = to_scale / value_scale;
           value_scale = to_scale;
         }
+        // a row's terms move down by `up`
+        auto rise = [&](float up) {
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+          for (int x = 4; x <= 16; x <<= 1) up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, x));
+          return fresh ? (up == __int_as_float(0xff800000) ? 0.f : up) : fmaxf(up, 0.f);
+        };
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            float up = __int_as_float(0xff800000);
+        for (int m = 0; m < NT; ++m) {
+          const float up0 = rise(fmaxf(fmaxf(z[0][m][0], z[0][m][2]), fmaxf(z[1][m][0], z[1][m][2])));
+          const float up1 = rise(fmaxf(fmaxf(z[0][m][1], z[0][m][3]), fmaxf(z[1][m][1], z[1][m][3])));
+          minus_ref[m] = add2(minus_ref[m], two(-up0, -up1));
+          const float f0 = fresh ? 0.f : ex2_approx(-up0), f1 = fresh ? 0.f : ex2_approx(-up1);
+          mass[m] = mul2(mass[m], two(f0, f1));
+          shift[m] = mul2(shift[m], two(f0, f1));
 #pragma unroll
-            for (int j = 0; j < 4; ++j) up = max3(up, z[m][j][2 * r], z[m][j][2 * r + 1]);
-            up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 1));
-            up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 2));
-            up = fresh ? (up == __int_as_float(0xff800000) ? 0.f : up) : fmaxf(up, 0.f);
-            ref[m][r] += up;
-            const float f = fresh ? 0.f : ex2_approx(-up), fv = f * by;
-            mass[m][r] = mul2(mass[m][r], two(f, f));
-            shift[m][r] = mul2(shift[m][r], two(f, f));
-#pragma unroll
-            for (int n = 0; n < 4 * KW; ++n) {
-              o[m][n][2 * r] *= fv;
-              o[m][n][2 * r + 1] *= fv;
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              z[m][j][2 * r] -= up;
-              z[m][j][2 * r + 1] -= up;
-            }
+          for (int n = 0; n < 2 * KW; ++n) {
+            o[m][n][0] *= f0 * by;
+            o[m][n][1] *= f1 * by;
+            o[m][n][2] *= f0 * by;
+            o[m][n][3] *= f1 * by;
           }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            z[i][m][0] -= up0;
+            z[i][m][1] -= up1;
+            z[i][m][2] -= up0;
+            z[i][m][3] -= up1;
+          }
+        }
         fresh = false;
       }
 
@@ -556,61 +580,54 @@ __global__ void __launch_bounds__(AttendShape<T, D, MT>::kThreads, AttendShape<T
       // the others as n - 15
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
+        uint32_t pb[NT][2];
+        [[maybe_unused]] uint32_t pl[NT][2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float scale = Kv<T>::lo(nv[i][e]), n_scale = scale * value_scale;
+          const float offset = e ? fmaf(15.f, scale, Kv<T>::hi(nv[i][e])) : Kv<T>::hi(nv[i][e]);
+          const Two vn = two(n_scale, n_scale), vo = two(offset, offset);
+#pragma unroll
+          for (int m = 0; m < NT; ++m) {
+            const Two w = two(ex2_approx(z[i][m][2 * e]), ex2_approx(z[i][m][2 * e + 1]));
+            mass[m] = add2(mass[m], w);
+            float a0, a1;
+            split(mul2(w, vn), a0, a1);
+            if (kMasked) {
+              // (a hidden token's numbers may be NaN)
+              const int2 see = sees(m, i, e);
+              float f0, f1;
+              split(mul2(w, vo), f0, f1);
+              if (!see.x) a0 = f0 = 0.f;
+              if (!see.y) a1 = f1 = 0.f;
+              shift[m] = add2(shift[m], two(f0, f1));
+            } else {
+              shift[m] = fma2(w, vo, shift[m]);
+            }
+            const uint32_t x = half2_bits(a0, a1);
+            pb[m][e] = transposed(x);
+            if constexpr (kFine) {
+              // a float16 result wants more than float16 weights: their rest
+              const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&x));
+              pl[m][e] = transposed(half2_bits(a0 - back.x, a1 - back.y));
+            }
+          }
+        }
         uint32_t vw[2][KW];
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-          shared_words(vw[j], from + (2 * i + 1) * Stage<D>::kCodes + (4 * j + c) * D + g * (D / 8));
-        uint32_t pf[MT][4];
-        [[maybe_unused]] uint32_t pl[MT][4];
-#pragma unroll
-        for (int jj = 0; jj < 2; ++jj) {
-          const int j = 2 * i + jj;
-          const Two vs = two(Kv<T>::lo(nv[j][0]), Kv<T>::lo(nv[j][1]));
-          Two vo = two(Kv<T>::hi(nv[j][0]), Kv<T>::hi(nv[j][1]));
-          if (jj) vo = fma2(vs, two(15.f, 15.f), vo);
-          const Two vn = mul2(vs, two(value_scale, value_scale));
-#pragma unroll
-          for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              const Two w = two(ex2_approx(z[m][j][2 * r]), ex2_approx(z[m][j][2 * r + 1]));
-              mass[m][r] = add2(mass[m][r], w);
-              float a0, a1;
-              split(mul2(w, vn), a0, a1);
-              if (kMasked) {
-                // (a hidden token's numbers may be NaN)
-                const int lim = subs >> i & 1 ? limits[m * 16 + 8 * r + g] : -1;
-                float f0, f1;
-                split(mul2(w, vo), f0, f1);
-                if (t0 + 8 * j > lim) a0 = f0 = 0.f;
-                if (t0 + 8 * j + 1 > lim) a1 = f1 = 0.f;
-                shift[m][r] = add2(shift[m][r], two(f0, f1));
-              } else {
-                shift[m][r] = fma2(w, vo, shift[m][r]);
-              }
-              pf[m][2 * jj + r] = half2_bits(a0, a1);
-              if constexpr (kFine) {
-                // a float16 result wants more than float16 weights: their rest
-                const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&pf[m][2 * jj + r]));
-                pl[m][2 * jj + r] = half2_bits(a0 - back.x, a1 - back.y);
-              }
-            }
-        }
+        for (int e = 0; e < 2; ++e)
+          shared_words(vw[e], from + (2 * i + 1) * Stage<D>::kCodes + (4 * e + c) * D + g * (D / 8));
 #pragma unroll
         for (int w = 0; w < KW; ++w)
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
-            const uint32_t v0 = vw[0][w] >> (8 * half), v1 = vw[1][w] >> (8 * half);
-            const uint32_t b00 = v0 & 0x000f000fu, b01 = (v1 & 0x000f000fu) ^ 0x800f800fu;
-            const uint32_t b10 = v0 & 0x00f000f0u, b11 = (v1 & 0x00f000f0u) ^ 0x80f080f0u;
+            const uint32_t x = vw[0][w] >> (8 * half), y = vw[1][w] >> (8 * half);
+            const uint32_t a0 = x & 0x000f000fu, a1 = x & 0x00f000f0u;
+            const uint32_t a2 = and_xor(y, 0x000f000fu, flip), a3 = and_xor(y, 0x00f000f0u, flip16);
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-              mma16816(o[m][4 * w + 2 * half], pf[m], b00, b01);
-              mma16816(o[m][4 * w + 2 * half + 1], pf[m], b10, b11);
-              if constexpr (kFine) {
-                mma16816(o[m][4 * w + 2 * half], pl[m], b00, b01);
-                mma16816(o[m][4 * w + 2 * half + 1], pl[m], b10, b11);
-              }
+            for (int m = 0; m < NT; ++m) {
+              mma16816(o[m][2 * w + half], a0, a1, a2, a3, pb[m][0], pb[m][1]);
+              if constexpr (kFine) mma16816(o[m][2 * w + half], a0, a1, a2, a3, pl[m][0], pl[m][1]);
             }
           }
       }
@@ -634,35 +651,33 @@ __global__ void __launch_bounds__(AttendShape<T, D, MT>::kThreads, AttendShape<T
     float* sums = all_sums + warp * kWarpFloats;
     const float down = 1.f / value_scale;
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int m = 0; m < NT; ++m) {
+      float l[2], f[2], ref[2];
+      split(mass[m], l[0], l[1]);
+      split(shift[m], f[0], f[1]);
+      split(minus_ref[m], ref[0], ref[1]);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int r = m * 16 + e * 8 + g;
-        float l, f, l1, f1;
-        split(mass[m][e], l, l1);
-        split(shift[m][e], f, f1);
-        l += l1;
-        f += f1;
-        l += __shfl_xor_sync(0xffffffffu, l, 1);
-        f += __shfl_xor_sync(0xffffffffu, f, 1);
-        l += __shfl_xor_sync(0xffffffffu, l, 2);
-        f += __shfl_xor_sync(0xffffffffu, f, 2);
-        if (c == 0) {
-          sums[TR * D + r] = l == 0.f ? -FLT_MAX : ref[m][e];
-          sums[TR * D + TR + r] = l;
+        const int r = 8 * m + 2 * c + e;
+#pragma unroll
+        for (int x = 4; x <= 16; x <<= 1) {
+          l[e] += __shfl_xor_sync(0xffffffffu, l[e], x);
+          f[e] += __shfl_xor_sync(0xffffffffu, f[e], x);
+        }
+        if (g == 0) {
+          sums[TR * D + r] = l[e] == 0.f ? -FLT_MAX : -ref[e];
+          sums[TR * D + TR + r] = l[e];
         }
 #pragma unroll
-        for (int col = 0; col < 2; ++col)
+        for (int w = 0; w < KW; ++w) {     // channels 4 (KW g + w) ..
+          float y[4];
 #pragma unroll
-          for (int w = 0; w < KW; ++w) {
-            const int dg = (2 * c + col) * KW + w;   // channels 4 dg ..
-            float y[4];
-#pragma unroll
-            for (int n = 0; n < 4; ++n)
-              y[n] = fmaf(o[m][4 * w + n][2 * e + col] * (n & 1 ? 0x1p20f : 0x1p24f), down, f);
-            reinterpret_cast<float4*>(sums)[r * (D / 4) + swizzled(r, dg)] = make_float4(y[0], y[1], y[2], y[3]);
-          }
+          for (int n = 0; n < 4; ++n)
+            y[n] = fmaf(o[m][2 * w + (n >> 1)][2 * (n & 1) + e] * (n & 1 ? 0x1p20f : 0x1p24f), down, f[e]);
+          reinterpret_cast<float4*>(sums)[r * (D / 4) + swizzled<D>(r, g * KW + w)] = make_float4(y[0], y[1], y[2], y[3]);
+        }
       }
+    }
     __syncthreads();
     const bool whole = chunk0 == 0 && chunks == s.chunks;
     float* part = p.part + (size_t)(2 * me + (chunk0 == 0)) * part_floats(TR, D);
@@ -670,7 +685,7 @@ __global__ void __launch_bounds__(AttendShape<T, D, MT>::kThreads, AttendShape<T
     for (int x0 = 0; x0 < TR * (D / 4); x0 += kThreads) {
       const int x = x0 + tid;
       if (TR * (D / 4) % kThreads != 0 && x >= TR * (D / 4)) break;
-      const int r = x / (D / 4), dg = x % (D / 4), at_r = r * (D / 4) + swizzled(r, dg);
+      const int r = x / (D / 4), dg = x % (D / 4), at_r = r * (D / 4) + swizzled<D>(r, dg);
       const long long q_row = out_rows[r];
       if (q_row < 0) continue;
       float top = -FLT_MAX;

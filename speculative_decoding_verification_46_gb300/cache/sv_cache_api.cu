@@ -105,14 +105,14 @@ unsigned store_grid(int R, int heads, int D) {
 
 // ---------------------------------------------------------------- attend
 
-// Rows of a tile: up to 16 go to attend_kernel; more to attend_wide_kernel, in
+// Rows of a tile: up to 24 go to attend_kernel; more to attend_wide_kernel, in
 // as few tiles as its 80 rows allow, of equal size.
 int attend_tile_rows(int rows) {
-  if (rows <= 16) return 16;
+  if (rows <= 24) return (std::max(rows, 1) + 7) / 8 * 8;
   const int tiles = (rows + sv::cache::kWdMostRows - 1) / sv::cache::kWdMostRows;
   return ((rows + tiles - 1) / tiles + 15) / 16 * 16;
 }
-int attend_ctas(int TR) { return sm_count() * (TR == 16 ? 3 : 2); }
+int attend_ctas(int TR) { return sm_count() * (TR == 8 ? 4 : TR == 16 ? 3 : 2); }
 
 struct AttendLayout {
   size_t desc, part, total;
@@ -134,10 +134,11 @@ sv_status launch_attend(sv::cache::AttendParams p, void* workspace, cudaStream_t
   p.desc = reinterpret_cast<int4*>(static_cast<unsigned char*>(workspace) + L.desc);
   p.part = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + L.part);
   static std::atomic<bool> set[64];
-  if constexpr (TR <= 16) {
-    auto kern = attend_kernel<T, D, TR / 16>;
-    if (!allow_smem(set, (const void*)kern, AttendShape<T, D, TR / 16>::kSmem)) return SV_ERR_CUDA;
-    kern<<<ctas, AttendShape<T, D, TR / 16>::kThreads, AttendShape<T, D, TR / 16>::kSmem, stream>>>(p);
+  if constexpr (TR <= 24) {
+    using Shape = AttendShape<T, D, TR / 8>;
+    auto kern = attend_kernel<T, D, TR / 8>;
+    if (!allow_smem(set, (const void*)kern, Shape::kSmem)) return SV_ERR_CUDA;
+    kern<<<ctas, Shape::kThreads, Shape::kSmem, stream>>>(p);
   } else {
     auto kern = attend_wide_kernel<T, D, TR / 16>;
     if (!allow_smem(set, (const void*)kern, WideShape<T, D, TR / 16>::kSmem)) return SV_ERR_CUDA;
@@ -164,7 +165,9 @@ sv_status launch_attend(sv::cache::AttendParams p, void* workspace, cudaStream_t
 template <typename T, int D>
 sv_status launch_attend_rows(const sv::cache::AttendParams& p, void* workspace, cudaStream_t stream) {
   switch (attend_tile_rows(p.rows * p.G)) {
+    case 8: return launch_attend<T, D, 8>(p, workspace, stream);
     case 16: return launch_attend<T, D, 16>(p, workspace, stream);
+    case 24: return launch_attend<T, D, 24>(p, workspace, stream);
     case 32: return launch_attend<T, D, 32>(p, workspace, stream);
     case 48: return launch_attend<T, D, 48>(p, workspace, stream);
     case 64: return launch_attend<T, D, 64>(p, workspace, stream);
