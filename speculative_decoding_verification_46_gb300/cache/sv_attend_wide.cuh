@@ -23,8 +23,8 @@
 // says so to all, and the step's weights are formed again.
 //
 // Tensor memory, 256 columns a CTA: key codes, value codes, scores, sums.  With
-// R = 80 and D = 128 the second half of the value codes takes the place of key
-// codes that the first product has read.
+// R = 80 and D = 128 the value codes take the place of the scores: then (2)
+// follows (3)'s reading of them, at whose barrier the references are settled.
 #pragma once
 
 #include "sv_attend.cuh"
@@ -146,8 +146,9 @@ struct WideShape {
   static constexpr int kSmall = R * 18 * 4;
   static constexpr int kSmem = oSmall + kSmall + 1024;            // (aligned to 1 KB in the kernel)
   static constexpr bool kTight = D / 2 + 64 + 2 * R > kWdColumns;
-  static constexpr int cV = D / 2, cS = kTight ? D / 2 + 32 : D / 2 + 64, cO = cS + R;
+  static constexpr int cV = D / 2, cS = kTight ? cV : cV + 64, cO = cS + R;
   static_assert(kStages >= (kTight ? 2 : 3), "a step's keys are read while the one before is at work");
+  static_assert(!kTight || R >= 64, "value codes in the scores' place");
   static_assert(cO + R <= kWdColumns, "tensor memory");
   static_assert(R <= kWdMostRows, "rows");
   static_assert(2 * (kSmem + 2048) <= 228 * 1024, "two CTAs an SM");
@@ -204,14 +205,17 @@ __global__ void __launch_bounds__(kWdThreads, 2) attend_wide_kernel(const __grid
   long long u = line.u, base = line.base;
   int b = line.b;
 
+  auto score_products = [&]() {
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k)
+      tm_mma(tm + S::cS, tm + 8 * k, q_operand + (uint64_t)((k >> 2) * (R * 8) + (k & 3) * 2), kind, k > 0);
+    tm_commit(bar_s);
+  };
   auto first_product = [&]() {
     if (warp == kWdScoreWarp) {
       if (lane == 0) {
         tm_fence_after();
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          tm_mma(tm + S::cS, tm + 8 * k, q_operand + (uint64_t)((k >> 2) * (R * 8) + (k & 3) * 2), kind, k > 0);
-        tm_commit(bar_s);
+        score_products();
       }
       __syncwarp();
     }
@@ -378,14 +382,12 @@ __global__ void __launch_bounds__(kWdThreads, 2) attend_wide_kernel(const __grid
     copies_wait<S::kStages - 1>();
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncthreads();
-    if (!S::kTight) {
-      keys(slot);
-      tm_wait_st();
-      copies_wait<(S::kStages > 1 ? S::kStages - 2 : 0)>();
-      tm_fence_before();
-      __syncthreads();
-      first_product();
-    }
+    keys(slot);
+    tm_wait_st();
+    copies_wait<S::kStages - 2>();
+    tm_fence_before();
+    __syncthreads();
+    first_product();
 
     // this thread's rows, two at a time: 8 k + 2 c, + 1 of its warpgroup's
     Two mass[NG], shift[NG];
@@ -398,17 +400,10 @@ __global__ void __launch_bounds__(kWdThreads, 2) attend_wide_kernel(const __grid
       const uint32_t stage = sm + S::oRing + slot * S::kStage;
       const uint32_t subs = seen_subs >> ((n & 3) * 8) & 0xffu;
       const int slot_next = slot + 1 == S::kStages ? 0 : slot + 1;
-      if (n > 0) {
+      if (!S::kTight && n > 0) {
         wait_phase(bar_o, phase_o, gave_up);
         phase_o ^= 1;
         tm_fence_after();
-      }
-      if (S::kTight) {
-        keys(slot);
-        tm_wait_st();
-        tm_fence_before();
-        __syncthreads();
-        first_product();
       }
 
       // value codes: the warpgroup's 64 tokens.  Unit 8 w + g of a pair is
@@ -430,11 +425,10 @@ __global__ void __launch_bounds__(kWdThreads, 2) attend_wide_kernel(const __grid
         tm_store_16x128(tm_w + column, v0);
         tm_store_16x128(tm_w + (16u << 16) + column, v1);
       };
-      if (!S::kTight || wg == 0) values(S::cV + 32 * wg);
+      if (!S::kTight) values(S::cV + 32 * wg);
       wait_phase(bar_s, phase_s, gave_up);
       phase_s ^= 1;
       tm_fence_after();
-      if (S::kTight && wg == 1) values(0);
 
       // (3) weights; the thread's tokens are those of lanes 16 bl + 8 e + g
       const int token0 = (chunk0 + n) * kWdUnit + 32 * (g >> 1) + 4 * w + (g & 1);      // + 16 e + 2 bl
@@ -553,7 +547,7 @@ __global__ void __launch_bounds__(kWdThreads, 2) attend_wide_kernel(const __grid
           }
         };
 
-        // the next step's key codes, and all of it visible to the others
+        // everybody's operands are there, and the copies of a later step
         auto meet = [&](bool any) {
           tm_wait_st();
           copies_wait<S::kTight ? S::kStages - 2 : S::kStages - 3>();
@@ -563,18 +557,20 @@ __global__ void __launch_bounds__(kWdThreads, 2) attend_wide_kernel(const __grid
         };
         float largest = fmaxf(fmaxf(Kv<T>::lo(nv[0][0]), Kv<T>::lo(nv[0][1])), fmaxf(Kv<T>::lo(nv[1][0]), Kv<T>::lo(nv[1][1])));
         bool again = true, outgrown = true;
-        if (n > 0) {
+        if (n > 0 || S::kTight) {
           const float most = exponents();
-          outgrown = __any_sync(0xffffffffu, most > kAtSlack || largest * value_scale > kAtValueTop);
-          if (!outgrown) weights(true);
-          if (!S::kTight && n + 1 < chunks) keys(slot_next);
+          outgrown = n == 0 || __any_sync(0xffffffffu, most > kAtSlack || largest * value_scale > kAtValueTop);
+          if (!S::kTight) {
+            if (!outgrown) weights(true);
+            if (n + 1 < chunks) keys(slot_next);
+          }
           again = meet(outgrown);
         }
         if (again) {
           // rows' references and the values' scale move; so do the sums.  The
           // first step sets the references (they were 0): a row that sees none
           // of it sees none of the later ones, its mass stays 0.
-          exponents();
+          if (!S::kTight) exponents();
 #pragma unroll
           for (int k = 0; k < NG; ++k) {
             float t0 = fmaxf(fmaxf(z[0][k][0], z[0][k][2]), fmaxf(z[1][k][0], z[1][k][2]));
@@ -644,8 +640,16 @@ __global__ void __launch_bounds__(kWdThreads, 2) attend_wide_kernel(const __grid
               tm_store_32x8(col, o);
             }
           }
-          weights(outgrown);
-          if (!S::kTight && n == 0 && n + 1 < chunks) keys(slot_next);
+          if (!S::kTight) {
+            weights(outgrown);
+            if (n == 0 && n + 1 < chunks) keys(slot_next);
+            meet(false);
+          }
+        }
+        if (S::kTight) {
+          values(S::cV + 32 * wg);
+          weights(true);
+          if (n + 1 < chunks) keys(slot_next);
           meet(false);
         }
         if (warp == kWdSumWarp) {
@@ -653,14 +657,20 @@ __global__ void __launch_bounds__(kWdThreads, 2) attend_wide_kernel(const __grid
             tm_fence_after();
 #pragma unroll
             for (int k = 0; k < kWdUnit / 16; ++k) {
-              const uint32_t a = tm + (S::kTight && k >= 4 ? 8 * (k - 4) : S::cV + 8 * k);
               const uint64_t at_p = p_operand + (uint64_t)((k >> 2) * (R * 8) + (k & 3) * 2);
-              tm_mma(tm + S::cO, a, at_p, kind, n > 0 || k > 0);
-              if (S::kFine) tm_mma(tm + S::cO, a, at_p + S::kP / 16, kind, true);
+              tm_mma(tm + S::cO, tm + S::cV + 8 * k, at_p, kind, n > 0 || k > 0);
+              if (S::kFine) tm_mma(tm + S::cO, tm + S::cV + 8 * k, at_p + S::kP / 16, kind, true);
             }
-            tm_commit(bar_o);
+            tm_commit(S::kTight && n + 1 == chunks ? bar_s : bar_o);
           }
           __syncwarp();
+          if (S::kTight && n + 1 < chunks) {
+            // the next scores take the value codes' place, once these are read
+            wait_phase(bar_o, phase_o, gave_up);
+            phase_o ^= 1;
+            if (lane == 0) score_products();
+            __syncwarp();
+          }
         }
         if (!S::kTight && n + 1 < chunks) first_product();
         copy_step(n + S::kStages);         // (everybody has read this step's)
@@ -692,8 +702,13 @@ __global__ void __launch_bounds__(kWdThreads, 2) attend_wide_kernel(const __grid
         }
       }
     }
-    wait_phase(bar_o, phase_o, gave_up);
-    phase_o ^= 1;
+    if (S::kTight) {
+      wait_phase(bar_s, phase_s, gave_up);
+      phase_s ^= 1;
+    } else {
+      wait_phase(bar_o, phase_o, gave_up);
+      phase_o ^= 1;
+    }
     tm_fence_after();
     __syncthreads();
     const bool failed = *gave_up;
