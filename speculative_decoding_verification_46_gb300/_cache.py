@@ -11,6 +11,7 @@ and pass their addresses.  There is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 
 import torch
@@ -29,6 +30,12 @@ SV_PLAN_NO_PAGES = 1
 SV_PLAN_TOO_LONG = 2
 
 _Strides = ctypes.c_int64 * 3
+
+
+def _as_strides(s):
+    return s if s is None or isinstance(s, _Strides) else _Strides(*s)
+
+
 _declared = None   # the library object whose signatures are declared
 
 
@@ -61,8 +68,8 @@ def sv_plan_round(B, gamma, page, N, pool, lengths, kept, gamma_b, block_table, 
 
 
 def sv_append_kv4(B, gamma, heads, D, page, pages, k, k_strides, v, v_strides, dtype, slots, cache, stream) -> int:
-    return int(_lib().sv_append_kv4(B, gamma, heads, D, page, pages, k, k_strides and _Strides(*k_strides), v,
-                                    v_strides and _Strides(*v_strides), dtype, slots, cache, stream))
+    return int(_lib().sv_append_kv4(B, gamma, heads, D, page, pages, k, _as_strides(k_strides), v,
+                                    _as_strides(v_strides), dtype, slots, cache, stream))
 
 
 def sv_read_kv4(R, heads, D, page, pages, cache, dtype, slots, k, v, stream) -> int:
@@ -75,7 +82,7 @@ def sv_attend_kv4_workspace_bytes(gamma: int, heads: int, G: int, D: int) -> int
 
 def sv_attend_kv4(B, gamma, heads, G, D, page, pages, N, q, q_strides, dtype, cache, block_table, lengths, gamma_b,
                   scale, out, lse, fill, workspace, workspace_bytes, stream) -> int:
-    return int(_lib().sv_attend_kv4(B, gamma, heads, G, D, page, pages, N, q, q_strides and _Strides(*q_strides), dtype,
+    return int(_lib().sv_attend_kv4(B, gamma, heads, G, D, page, pages, N, q, _as_strides(q_strides), dtype,
                                     cache, block_table, lengths, gamma_b, scale, out, lse, fill, workspace,
                                     workspace_bytes, stream))
 
@@ -101,14 +108,18 @@ def _need_model_rows(name, t):
 def _strides_of(t):
     """Strides of the first three dimensions (0 where there is one element, which may have any)."""
     b, i, h, _ = t.stride()
-    if b % 8 or i % 8 or h % 8:
-        return tuple(st if n > 1 else 0 for n, st in zip(t.shape[:3], (b, i, h)))
-    return b, i, h
+    if (b | i | h) & 7:
+        return _Strides(*(st if n > 1 else 0 for n, st in zip(t.shape, (b, i, h))))
+    return _Strides(b, i, h)
 
 
 def _all_written(*tensors):
     """The caller's tensors have been written (see _written)."""
-    torch.autograd.graph.increment_version([t for t in tensors if not t.is_inference()])
+    try:
+        torch.autograd.graph.increment_version(tensors)
+    except RuntimeError:                     # some were made in inference mode and have no version
+        for t in tensors:
+            _written(t)
 
 
 def _page_of(cache, page, D, heads, device):
@@ -171,13 +182,15 @@ def plan_round(lengths, gamma, page, block_table, blocks, free_blocks, free_coun
     if gamma < 0 or B * (gamma + 1) > SV_MAX_CACHE_ROWS:
         raise ValueError(f"gamma must be at least 0 and B * (gamma + 1) at most {SV_MAX_CACHE_ROWS}, got {gamma}")
     with _on(dev, stream):
-        _read_on(stream, lengths, block_table, blocks, free_blocks, free_count, kept, gamma_b)
+        if stream is not None:
+            _read_on(stream, lengths, block_table, blocks, free_blocks, free_count, kept, gamma_b)
         slots = torch.empty((B, gamma + 1), dtype=_i32, device=dev)
         positions = torch.empty((B, gamma + 1), dtype=_i32, device=dev)
         status = torch.empty(B, dtype=_i32, device=dev)
-        st = sv_plan_round(B, gamma, page, N, pool, _addr(lengths), _addr(kept), _addr(gamma_b), _addr(block_table),
-                           _addr(blocks), _addr(free_blocks), _addr(free_count), _addr(slots), _addr(positions),
-                           _addr(status), _handle(dev))
+        st = _lib().sv_plan_round(B, gamma, page, N, pool, lengths.data_ptr(), _addr(kept), _addr(gamma_b),
+                                  block_table.data_ptr(), blocks.data_ptr(), free_blocks.data_ptr(),
+                                  free_count.data_ptr(), slots.data_ptr(), positions.data_ptr(), status.data_ptr(),
+                                  _handle(dev))
     if st != SV_OK:
         raise SvError(st, "sv_plan_round")
     _all_written(lengths, block_table, blocks, free_blocks, free_count)
@@ -208,9 +221,11 @@ def append_kv4(k, v, slots, cache, *, stream=None):
     if G1 < 1:
         raise ValueError("k has no rows: [B, gamma+1, heads, D] with gamma >= 0")
     with _on(dev, stream):
-        _read_on(stream, k, v, slots, cache)
-        st = sv_append_kv4(B, G1 - 1, heads, D, page, pages, _addr(k), _strides_of(k), _addr(v), _strides_of(v),
-                           _TORCH_DTYPE[k.dtype], _addr(slots), _addr(cache), _handle(dev))
+        if stream is not None:
+            _read_on(stream, k, v, slots, cache)
+        st = _lib().sv_append_kv4(B, G1 - 1, heads, D, page, pages, k.data_ptr(), _strides_of(k), v.data_ptr(),
+                                  _strides_of(v), _TORCH_DTYPE[k.dtype], slots.data_ptr(), cache.data_ptr(),
+                                  _handle(dev))
     if st != SV_OK:
         raise SvError(st, "sv_append_kv4")
     _written(cache)
@@ -226,18 +241,18 @@ def read_kv4(cache, slots, page, dtype, *, stream=None):
     if dtype not in _MODEL_TYPES:
         raise ValueError(f"unsupported dtype {dtype}: bfloat16 or float16")
     _need("slots", slots, _i32, slots.shape, dev)
-    _need_cuda("cache", cache, torch.uint8)
     if cache.dim() != 3 or page < 1:
         raise ValueError(f"cache must be [pages, heads, page * (D + 8)], got {tuple(cache.shape)} and page {page}")
     D = cache.shape[2] // page - 8
     heads = cache.shape[1]
     pages = _page_of(cache, page, D, None, dev)
     with _on(dev, stream):
-        _read_on(stream, cache, slots)
+        if stream is not None:
+            _read_on(stream, cache, slots)
         k = torch.empty((*slots.shape, heads, D), dtype=dtype, device=dev)
         v = torch.empty((*slots.shape, heads, D), dtype=dtype, device=dev)
-        st = sv_read_kv4(slots.numel(), heads, D, page, pages, _addr(cache), _TORCH_DTYPE[dtype], _addr(slots),
-                         _addr(k), _addr(v), _handle(dev))
+        st = _lib().sv_read_kv4(slots.numel(), heads, D, page, pages, cache.data_ptr(), _TORCH_DTYPE[dtype],
+                                slots.data_ptr(), k.data_ptr(), v.data_ptr(), _handle(dev))
     if st != SV_OK:
         raise SvError(st, "sv_read_kv4")
     return k, v
@@ -253,6 +268,12 @@ def alloc_attend_workspace(gamma: int, heads: int, group: int, D: int, device=No
             raise SvError(SV_ERR_INVALID_ARG, "sv_attend_kv4_workspace_bytes")
         n = max(sv_attend_kv4_workspace_bytes(g, heads, group, D) for g in range(gamma + 1))
     return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+@functools.lru_cache(maxsize=256)
+def _attend_workspace_bytes(gamma, heads, group, D, device_index):
+    """(of the current device, whose index is passed: its SMs count)"""
+    return sv_attend_kv4_workspace_bytes(gamma, heads, group, D)
 
 
 def attend_kv4(q, cache, block_table, lengths, page, *, gamma_b=None, scale=None, out=None, return_lse=False,
@@ -298,7 +319,8 @@ def attend_kv4(q, cache, block_table, lengths, page, *, gamma_b=None, scale=None
     scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
     given = out
     with _on(dev, stream):
-        _read_on(stream, q, cache, block_table, lengths, gamma_b, out, workspace)
+        if stream is not None:
+            _read_on(stream, q, cache, block_table, lengths, gamma_b, out, workspace)
         if out is None:
             out = torch.empty((B, G1, HQ, D), dtype=q.dtype, device=dev)
         lse = None
@@ -307,14 +329,14 @@ def attend_kv4(q, cache, block_table, lengths, page, *, gamma_b=None, scale=None
             make = torch.zeros if given is not None and gamma_b is not None else torch.empty
             lse = make((B, G1, HQ), dtype=torch.float32, device=dev)
         if workspace is None:
-            n = sv_attend_kv4_workspace_bytes(G1 - 1, heads, HQ // heads, D)
+            n = _attend_workspace_bytes(G1 - 1, heads, HQ // heads, D, dev.index)
             if n == 0:
                 raise SvError(SV_ERR_INVALID_ARG, "sv_attend_kv4")
             workspace = torch.empty(n, dtype=torch.uint8, device=dev)
-        st = sv_attend_kv4(B, G1 - 1, heads, HQ // heads, D, page, pages, N, _addr(q), _strides_of(q),
-                           _TORCH_DTYPE[q.dtype], _addr(cache), _addr(block_table), _addr(lengths), _addr(gamma_b),
-                           scale, _addr(out), _addr(lse), given is None, _addr(workspace), workspace.numel(),
-                           _handle(dev))
+        st = _lib().sv_attend_kv4(B, G1 - 1, heads, HQ // heads, D, page, pages, N, q.data_ptr(), _strides_of(q),
+                                  _TORCH_DTYPE[q.dtype], cache.data_ptr(), block_table.data_ptr(), lengths.data_ptr(),
+                                  _addr(gamma_b), scale, out.data_ptr(), _addr(lse), given is None,
+                                  workspace.data_ptr(), workspace.numel(), _handle(dev))
     if st != SV_OK:
         raise SvError(st, "sv_attend_kv4")
     if given is not None:
