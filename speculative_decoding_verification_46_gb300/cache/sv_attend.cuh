@@ -209,12 +209,10 @@ struct Stage {
   static constexpr int kNumbers = 4 * kCodes;                // where the numbers begin
   static constexpr int kBytes = kNumbers + 2 * 128;
 };
-template <int BYTES>
-__device__ __forceinline__ void copy_ahead(uint32_t to, const unsigned char* from) {
-  if constexpr (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(from) : "memory");
+// 16 bytes, where `here`
+__device__ __forceinline__ void copy_ahead_if(bool here, uint32_t to, const unsigned char* from) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t@p cp.async.cg.shared.global [%0], [%1], 16;\n\t}" ::"r"(to), "l"(from),
+               "r"((uint32_t)here) : "memory");
 }
 __device__ __forceinline__ void copies_end_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int LEFT>
@@ -371,16 +369,16 @@ __global__ void __launch_bounds__(AttendShape<T, D, NT>::kThreads, AttendShape<T
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const unsigned long long from = i ? from1 : from0;
-          if (from == 0) continue;
+          const bool here = from != 0;
           const int sub = (int)(from & 15);
           const unsigned char* codes = reinterpret_cast<const unsigned char*>(from - sub) + lane * 16;
 #pragma unroll
           for (int j = 0; j < D / 64; ++j) {
-            copy_ahead<16>(to + lane * 16 + i * 2 * C + j * 512, codes + j * 512);
-            copy_ahead<16>(to + lane * 16 + i * 2 * C + C + j * 512, codes + p.page * (D / 2) + j * 512);
+            copy_ahead_if(here, to + lane * 16 + i * 2 * C + j * 512, codes + j * 512);
+            copy_ahead_if(here, to + lane * 16 + i * 2 * C + C + j * 512, codes + p.page * (D / 2) + j * 512);
           }
-          if (lane < 8)
-            copy_ahead<16>(to + lane * 16 + Stage<D>::kNumbers + i * 128, codes + p.page * D - sub * (8 * D - 128));
+          copy_ahead_if(here && lane < 8, to + lane * 16 + Stage<D>::kNumbers + i * 128,
+                        codes + p.page * D - sub * (8 * D - 128));
         }
         to = to == ring + (kAtStages - 1) * Stage<D>::kBytes ? ring : to + Stage<D>::kBytes;
       }

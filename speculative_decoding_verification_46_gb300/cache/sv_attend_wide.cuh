@@ -34,6 +34,7 @@ namespace cache {
 
 constexpr int kWdThreads = 256;
 constexpr int kWdScoreWarp = 1, kWdSumWarp = 6;   // warps that also issue the first and the second product
+constexpr int kWdAskWarp = 3;        // looks pages up
 constexpr int kWdUnit = 128;         // tokens of a step
 constexpr int kWdColumns = 256;      // of tensor memory
 constexpr int kWdMostRows = 80;
@@ -161,6 +162,8 @@ __global__ void __launch_bounds__(kWdThreads, 2) attend_wide_kernel(const __grid
   extern __shared__ unsigned char wd_raw[];
   __shared__ uint32_t tm_base;
   __shared__ __align__(8) unsigned long long bars[2];
+  __shared__ unsigned long long places[2][32];
+  __shared__ uint32_t place_subs[4];
   __shared__ int gave_up_flag;
   __shared__ float warp_top[8];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, w = warp & 3, wg = warp >> 2, g = lane >> 2, c = lane & 3;
@@ -220,6 +223,9 @@ __global__ void __launch_bounds__(kWdThreads, 2) attend_wide_kernel(const __grid
       __syncwarp();
     }
   };
+  // this thread's places in a step's keys and values
+  const uint32_t keys_at = 2 * (g >> 1) * S::kSubKeys + (2 * (2 * w + wg) + (g & 1)) * (D / 2) + c * (D / 8);
+  const uint32_t values_at = S::oValues + 2 * c * S::kSubValues + 4 * wg * D + 4 * (8 * w + g);
   // key codes of a step: the warpgroup's 16 lanes.  Lane 32 w + 16 bl + 8 e + g
   // is token 2 (2 w + bl) + g % 2 of sub 2 (g / 2) + e: the four pairs of tokens
   // of a piece of eight lanes are in four subs, in different banks
@@ -229,7 +235,7 @@ __global__ void __launch_bounds__(kWdThreads, 2) attend_wide_kernel(const __grid
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       uint32_t k[KW];
-      shared_words(k, stage + (2 * (g >> 1) + e) * S::kSubKeys + (2 * (2 * w + wg) + (g & 1)) * (D / 2) + c * (D / 8));
+      shared_words(k, stage + keys_at + e * S::kSubKeys);
 #pragma unroll
       for (int j = 0; j < KW; ++j) {
         v[8 * j + e] = k[j] & 0x000f000fu;
@@ -255,20 +261,30 @@ __global__ void __launch_bounds__(kWdThreads, 2) attend_wide_kernel(const __grid
     if (chunks == 0) continue;
     const int sub_end = (s.seen + 15) / 16;
 
-    // ---- the ring: a warp copies a sub of a step.  A lane knows where one of
-    // the next 32 subs begins, its number in the page in the low four bits
-    // (0: hidden); the 32 behind them are asked for ahead of time.
-    int ask_id = -1, ask_sub = 0;
-    auto ask = [&](int n) {
-      const int mine = (chunk0 + n) * 8 + lane;
-      ask_id = -1;
-      if (mine < sub_end) {
-        const int x = mine / page_tiles;
-        ask_id = __ldg(p.table + (long long)b * p.N + x);
-        ask_sub = mine - x * page_tiles;
-      }
+    // ---- the ring: a warp copies a sub of a step.  Where a sub begins, its
+    // number in the page in the low four bits (0: hidden), is looked up for
+    // four steps (32 subs) at a time, by every warp for the first four, later by
+    // one of them for all, two times four steps ahead.
+    auto ask = [&](int q, int& sub) {
+      const int mine = (chunk0 + 4 * q) * 8 + lane;
+      if (mine >= sub_end) return -1;
+      const int x = mine / page_tiles;
+      sub = mine - x * page_tiles;
+      return __ldg(p.table + (long long)b * p.N + x);
     };
-    ask(0);
+    auto place_of = [&](int id, int sub) {
+      return (uint32_t)id < (uint32_t)p.pages
+                 ? reinterpret_cast<unsigned long long>(p.cache) +
+                       (unsigned long long)(((long long)id * p.H + h) * block_bytes + sub * (8 * D + 1)) : 0ull;
+    };
+    auto tell = [&](int q, unsigned long long place) {
+      places[q & 1][lane] = place;
+      const uint32_t bits = __ballot_sync(0xffffffffu, place != 0);
+      if (lane == 0) place_subs[q & 3] = bits;
+    };
+    int sub0 = 0, sub1 = 0, asked = -1, asked_sub = 0;
+    const int id0 = ask(0, sub0);
+    const int id1 = warp == kWdAskWarp ? ask(1, sub1) : -1;
     // q is on its way meanwhile: a thread's pieces of eight channels
     constexpr int PIECES = (R * LANES + kWdThreads - 1) / kWdThreads;
     uint4 qv[PIECES];
@@ -280,44 +296,45 @@ __global__ void __launch_bounds__(kWdThreads, 2) attend_wide_kernel(const __grid
         qv[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + b * p.qs[0] + i * p.qs[1] +
                                                      (long long)(h * p.G + r - i * p.G) * p.qs[2]) + x % LANES);
     }
-    unsigned long long ahead = 0;
-    uint32_t next_subs = 0;              // which of the 32 are there
-    uint32_t seen_subs = 0;              // byte n % 4: which subs of step n are there
+    auto copy_sub = [&](int x, unsigned long long from) {
+      const bool here = from != 0;
+      const int sub = (int)(from & 15);
+      const unsigned char* codes = reinterpret_cast<const unsigned char*>(from - sub) + lane * 16;
+      const uint32_t to = sm + S::oRing + slot_to * S::kStage + lane * 16;
+#pragma unroll
+      for (int j = 0; j < D / 64; ++j) {
+        copy_ahead_if(here, to + x * S::kSubKeys + j * 512, codes + j * 512);
+        copy_ahead_if(here, to + S::oValues + x * S::kSubValues + j * 512, codes + p.page * (D / 2) + j * 512);
+      }
+      copy_ahead_if(here && lane < 8, to + S::oNumbers + x * S::kSubNumbers, codes + p.page * D - sub * (8 * D - 128));
+    };
+    {
+      const unsigned long long place = place_of(id0, sub0);
+#pragma unroll
+      for (int n = 0; n < S::kStages; ++n) {
+        const unsigned long long from = __shfl_sync(0xffffffffu, place, 8 * n + warp);
+        if (n < chunks) {
+          copy_sub(warp, from);
+          slot_to = slot_to + 1 == S::kStages ? 0 : slot_to + 1;
+        }
+        copies_end_group();
+      }
+      if (warp == kWdAskWarp) {
+        tell(0, place);
+        tell(1, place_of(id1, sub1));
+      }
+    }
+    // (warps 1 and 6 are busy with the products; 2 and 5 take one sub more)
     auto copy_step = [&](int n) {
       if (n < chunks) {
-        const int turn = (n & 3) * 8;
-        if (turn == 0) {
-          ahead = 0;
-          if (ask_id >= 0 && ask_id < p.pages)
-            ahead = reinterpret_cast<unsigned long long>(p.cache) +
-                    (unsigned long long)(((long long)ask_id * p.H + h) * block_bytes + ask_sub * (8 * D) + ask_sub);
-          ask(n + 4);
-          next_subs = __ballot_sync(0xffffffffu, ahead != 0);
-        }
-        seen_subs = (seen_subs & ~(0xffu << turn)) | (next_subs & 0xffu << turn);
-        // (warps 1 and 6 are busy with the products; 2 and 5 take one sub more)
-        auto copy_sub = [&](int x) {
-          const unsigned long long from = __shfl_sync(0xffffffffu, ahead, turn + x);
-          if (from == 0) return;
-          const int sub = (int)(from & 15);
-          const unsigned char* codes = reinterpret_cast<const unsigned char*>(from - sub) + lane * 16;
-          const uint32_t to = sm + S::oRing + slot_to * S::kStage + lane * 16;
-#pragma unroll
-          for (int j = 0; j < D / 64; ++j) {
-            copy_ahead<16>(to + x * S::kSubKeys + j * 512, codes + j * 512);
-            copy_ahead<16>(to + S::oValues + x * S::kSubValues + j * 512, codes + p.page * (D / 2) + j * 512);
-          }
-          if (lane < 8) copy_ahead<16>(to + S::oNumbers + x * S::kSubNumbers, codes + p.page * D - sub * (8 * D - 128));
-        };
-        if (warp != kWdScoreWarp && warp != kWdSumWarp) copy_sub(warp);
-        if (warp == 2) copy_sub(kWdScoreWarp);
-        if (warp == 5) copy_sub(kWdSumWarp);
+        const unsigned long long* place = places[n >> 2 & 1] + (n & 3) * 8;
+        if (warp != kWdScoreWarp && warp != kWdSumWarp) copy_sub(warp, place[warp]);
+        if (warp == 2) copy_sub(kWdScoreWarp, place[kWdScoreWarp]);
+        if (warp == 5) copy_sub(kWdSumWarp, place[kWdSumWarp]);
         slot_to = slot_to + 1 == S::kStages ? 0 : slot_to + 1;
       }
       copies_end_group();
     };
-#pragma unroll
-    for (int n = 0; n < S::kStages; ++n) copy_step(n);
 
     // ---- q: float16 with one power of two for the tile (a row whose largest
     // element is 2^-20 of the tile's still has its scores to 2^-17 of their
@@ -398,7 +415,7 @@ __global__ void __launch_bounds__(kWdThreads, 2) attend_wide_kernel(const __grid
 
     for (int n = 0; n < chunks; ++n) {
       const uint32_t stage = sm + S::oRing + slot * S::kStage;
-      const uint32_t subs = seen_subs >> ((n & 3) * 8) & 0xffu;
+      const uint32_t subs = place_subs[n >> 2 & 3] >> ((n & 3) * 8) & 0xffu;
       const int slot_next = slot + 1 == S::kStages ? 0 : slot + 1;
       if (!S::kTight && n > 0) {
         wait_phase(bar_o, phase_o, gave_up);
@@ -416,7 +433,7 @@ __global__ void __launch_bounds__(kWdThreads, 2) attend_wide_kernel(const __grid
         for (int i = 0; i < 8; ++i) {
           uint32_t x;
           asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x)
-                       : "r"(stage + S::oValues + (2 * c + (i & 1)) * S::kSubValues + (4 * wg + (i >> 1)) * D + 4 * (8 * w + g)) : "memory");
+                       : "r"(stage + values_at + (i & 1) * S::kSubValues + (i >> 1) * D) : "memory");
           v0[2 * i] = (x & 0x000f000fu) ^ flip;
           v0[2 * i + 1] = (x & 0x00f000f0u) ^ flip16;
           v1[2 * i] = (x >> 8 & 0x000f000fu) ^ flip;
@@ -674,6 +691,11 @@ __global__ void __launch_bounds__(kWdThreads, 2) attend_wide_kernel(const __grid
         }
         if (!S::kTight && n + 1 < chunks) first_product();
         copy_step(n + S::kStages);         // (everybody has read this step's)
+        if (warp == kWdAskWarp) {
+          // (what was told for these four steps has been read when this is told)
+          if ((n & 3) == 0) asked = ask((n >> 2) + 2, asked_sub);
+          if ((n & 3) == 2) tell((n >> 2) + 2, place_of(asked, asked_sub));
+        }
       };
       if (subs != 0xffu || (chunk0 + n) * kWdUnit + kWdUnit > s.first) softmax(std::true_type{});
       else softmax(std::false_type{});
