@@ -288,7 +288,8 @@ __global__ void __launch_bounds__(AttendShape<T, D, NT>::kThreads, AttendShape<T
   __shared__ float q_sums[TR], warp_top[kWarps];
   __shared__ int limits[TR];
   __shared__ long long out_rows[TR];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
+  const int tid = threadIdx.x, lane = tid & 31, g = lane >> 2, c = lane & 3;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);    // (the compiler sees that a warp shares it)
   float* const all_sums = at_sm + S::kQ / 4;
   pdl_launch_dependents();
 

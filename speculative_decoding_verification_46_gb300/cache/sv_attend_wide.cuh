@@ -166,7 +166,8 @@ __global__ void __launch_bounds__(kWdThreads, 2) attend_wide_kernel(const __grid
   __shared__ uint32_t place_subs[4];
   __shared__ int gave_up_flag;
   __shared__ float warp_top[8];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, w = warp & 3, wg = warp >> 2, g = lane >> 2, c = lane & 3;
+  const int tid = threadIdx.x, lane = tid & 31, g = lane >> 2, c = lane & 3;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0), w = warp & 3, wg = warp >> 2;   // (the compiler sees that a warp shares it)
   const uint32_t sm0 = (uint32_t)__cvta_generic_to_shared(wd_raw), sm = (sm0 + 1023u) & ~1023u;
   unsigned char* const sp = wd_raw + (sm - sm0);
   float4* const pairs = reinterpret_cast<float4*>(sp + S::oSmall);   // rows 2 i, 2 i + 1: sums of q, references below 0
