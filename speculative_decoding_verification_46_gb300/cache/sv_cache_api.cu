@@ -97,10 +97,12 @@ sv::cache::StoreParams store_params(int R, int rows, int heads, int page, int pa
   return p;
 }
 
-// CTAs for a group of D / 8 lanes per (two rows, head); 0: too many
+// CTAs for a group of D / 8 lanes per (two rows, head); 0: more groups than an
+// int counts (whose rows no card holds)
 unsigned store_grid(int R, int heads, int D) {
-  const long long ctas = (((long long)R + 1) / 2 * heads * (D / 8) + sv::cache::kStoreThreads - 1) / sv::cache::kStoreThreads;
-  return ctas > 0x7fffffffll ? 0u : (unsigned)ctas;
+  const long long groups = ((long long)R + 1) / 2 * heads;
+  const int per_cta = sv::cache::kStoreThreads / (D / 8);
+  return groups > 0x7fffffffll ? 0u : (unsigned)((groups + per_cta - 1) / per_cta);
 }
 
 // ---------------------------------------------------------------- attend

@@ -91,29 +91,38 @@ __device__ __forceinline__ F2x f2x_fma(F2x a, F2x b, F2x c) {
   return d;
 }
 
-// One row's codes (8 of a lane's elements, 4 bits each from the low end) and
-// its scale and offset as bits; LANES lanes hold the row.
+// The least element of a row and the least negative of one, side by side, in
+// all of its LANES lanes; NaN stays.
 template <typename T, int LANES>
-__device__ __forceinline__ uint32_t quantise(const uint4& x, uint32_t& numbers) {
+__device__ __forceinline__ uint32_t ends_of(const uint4& x) {
   using V = typename Kv2<T>::V;
-  // the least element and the least negative of one, side by side; NaN stays
   const V lo2 = __hmin2_nan(__hmin2_nan(as_two<V>(x.x), as_two<V>(x.y)), __hmin2_nan(as_two<V>(x.z), as_two<V>(x.w)));
   const V hi2 = __hmax2_nan(__hmax2_nan(as_two<V>(x.x), as_two<V>(x.y)), __hmax2_nan(as_two<V>(x.z), as_two<V>(x.w)));
   const uint32_t a = as_bits(lo2), b = as_bits(hi2) ^ 0x80008000u;
   V both = __hmin2_nan(as_two<V>(__byte_perm(a, b, 0x5410)), as_two<V>(__byte_perm(a, b, 0x7632)));
 #pragma unroll
   for (int m = LANES / 2; m >= 1; m >>= 1) both = __hmin2_nan(both, as_two<V>(__shfl_xor_sync(0xffffffffu, as_bits(both), m)));
-  const uint32_t ends = as_bits(both);
+  return as_bits(both);
+}
+// A row's scale and offset as bits, and what its elements are multiplied by;
+// for a row that is held as NaN (an element is not finite, or the scale) NaN.
+template <typename T>
+__device__ __forceinline__ uint32_t numbers_of(uint32_t ends, float& inverse) {
   const float least = Kv<T>::lo(ends), most = -Kv<T>::hi(ends);
   const uint32_t sb = Kv<T>::bits(__fdiv_rn(most - least, 15.f));
   const float scale = Kv<T>::lo(sb);
-  if (!(scale < __int_as_float(0x7f800000))) {   // an element is not finite, or the scale
+  if (!(scale < __int_as_float(0x7f800000))) {
     const uint32_t nan = Kv<T>::bits(__int_as_float(0x7fffffff));
-    numbers = nan | nan << 16;
-    return 0;
+    inverse = 0.f;
+    return nan | nan << 16;
   }
-  numbers = sb | ends << 16;
-  const float inverse = scale < 1.17549435e-38f ? 0.f : __frcp_rn(scale);
+  inverse = scale < 1.17549435e-38f ? 0.f : __frcp_rn(scale);
+  return sb | ends << 16;
+}
+// Codes of a lane's 8 elements, 4 bits each from the low end.
+template <typename T>
+__device__ __forceinline__ uint32_t codes_of(const uint4& x, uint32_t numbers, float inverse) {
+  const float least = Kv<T>::hi(numbers);
   const F2x minus = f2x(-least, -least);
   // added and taken away again, 3 2^22 rounds to whole numbers, ties to even
   const F2x magic = f2x(12582912.f, 12582912.f), back = f2x(-12582912.f, -12582912.f);
@@ -141,7 +150,7 @@ __device__ __forceinline__ uint32_t quantise(const uint4& x, uint32_t& numbers) 
   const F2x sum = f2x_add(f2x_fma(f2x_fma(f2x_fma(c[3], k16, c[2]), k16, c[1]), k16, c[0]), f2x(8388608.f, 8388608.f));
   float s0, s1;
   f2x_split(sum, s0, s1);
-  return __byte_perm(__float_as_uint(s0), __float_as_uint(s1), 0x5410);
+  return inverse > 0.f ? __byte_perm(__float_as_uint(s0), __float_as_uint(s1), 0x5410) : 0u;   // (0: NaN or constant rows)
 }
 
 // Bytes from a block's start to the 8 codes of channels 8 l .. of token t.
@@ -157,60 +166,82 @@ __device__ __forceinline__ int numbers_at(int page, int t) { return page * D + 8
 struct RowPair {
   int r, h;                // first row, head
   int slot[2];             // -1: none
+  int page[2], t[2];       // of the slots
   bool next;               // the second slot is the first one's odd neighbour
 };
-__device__ __forceinline__ RowPair row_pair(const StoreParams& p, long long item) {
+__device__ __forceinline__ RowPair row_pair(const StoreParams& p, uint32_t item) {
   RowPair x;
-  const long long pairs = ((long long)p.R + 1) / 2;
-  const long long i = item / p.H;
-  x.h = (int)(item - i * p.H);
-  x.r = i < pairs ? 2 * (int)i : 0;
+  const uint32_t i = item / (uint32_t)p.H;
+  x.h = (int)(item - i * (uint32_t)p.H);
+  x.r = 2 * (int)i;
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
-    const int slot = i < pairs && x.r + j < p.R ? __ldg(p.slots + x.r + j) : -1;
+    const int slot = x.r + j < p.R ? __ldg(p.slots + x.r + j) : -1;
     x.slot[j] = slot >= 0 && slot < p.slots_end ? slot : -1;
   }
   x.next = x.slot[0] >= 0 && (x.slot[0] & 1) == 0 && x.slot[1] == x.slot[0] + 1;
+  x.page[0] = (int)((uint32_t)max(x.slot[0], 0) / (uint32_t)p.page);
+  x.t[0] = x.slot[0] - x.page[0] * p.page;
+  x.page[1] = x.page[0];
+  x.t[1] = x.t[0] + 1;
+  if (!x.next) {
+    x.page[1] = (int)((uint32_t)max(x.slot[1], 0) / (uint32_t)p.page);
+    x.t[1] = x.slot[1] - x.page[1] * p.page;
+  }
   return x;
 }
+// (of a call's groups of D / 8 lanes, at most 2^31)
+__device__ __forceinline__ uint32_t pair_items(const StoreParams& p) { return ((uint32_t)p.R + 1) / 2 * (uint32_t)p.H; }
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kStoreThreads) append_kv4_kernel(const __grid_constant__ StoreParams p) {
   constexpr int LANES = D / 8;
-  const int l = threadIdx.x % LANES;
-  const RowPair pair = row_pair(p, ((long long)blockIdx.x * kStoreThreads + threadIdx.x) / LANES);
+  const int lane = threadIdx.x & 31, l = threadIdx.x % LANES;
+  const uint32_t item = blockIdx.x * (kStoreThreads / LANES) + threadIdx.x / LANES;
+  RowPair pair = row_pair(p, min(item, pair_items(p) - 1));
+  if (item >= pair_items(p)) pair.slot[0] = pair.slot[1] = -1;
   if (!__any_sync(0xffffffffu, pair.slot[0] >= 0 || pair.slot[1] >= 0)) return;
-  uint4 xk[2], xv[2];
+  uint4 x[4];                            // key, value of the first row, of the second
+  int b = pair.r / p.rows, i = pair.r - b * p.rows;
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
-    xk[j] = xv[j] = make_uint4(0, 0, 0, 0);
+    x[2 * j] = x[2 * j + 1] = make_uint4(0, 0, 0, 0);
     if (pair.slot[j] >= 0) {
-      const int r = pair.r + j, b = r / p.rows, i = r - b * p.rows;
-      xk[j] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const T*>(p.k) + b * p.ks[0] + i * p.ks[1] + pair.h * p.ks[2]) + l);
-      xv[j] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const T*>(p.v) + b * p.vs[0] + i * p.vs[1] + pair.h * p.vs[2]) + l);
+      x[2 * j] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const T*>(p.k) + b * p.ks[0] + i * p.ks[1] + pair.h * p.ks[2]) + l);
+      x[2 * j + 1] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const T*>(p.v) + b * p.vs[0] + i * p.vs[1] + pair.h * p.vs[2]) + l);
+    }
+    if (++i == p.rows) {
+      i = 0;
+      ++b;
     }
   }
-  uint32_t ck[2], cv[2], nk[2], nv[2];
+  uint32_t ends[4];
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    ck[j] = quantise<T, LANES>(xk[j], nk[j]);
-    cv[j] = quantise<T, LANES>(xv[j], nv[j]);
+  for (int j = 0; j < 4; ++j) ends[j] = ends_of<T, LANES>(x[j]);
+  // the division and the reciprocal of row j in lanes j, j + 4 .. alone
+  float inverse;
+  const uint32_t numbers = numbers_of<T>((lane & 2) ? (lane & 1) ? ends[3] : ends[2] : (lane & 1) ? ends[1] : ends[0], inverse);
+  uint32_t n[4], codes[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    n[j] = __shfl_sync(0xffffffffu, numbers, (lane & ~3) | j);
+    codes[j] = codes_of<T>(x[j], n[j], __shfl_sync(0xffffffffu, inverse, (lane & ~3) | j));
   }
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     if (pair.slot[j] < 0) continue;
-    const int page = pair.slot[j] / p.page, t = pair.slot[j] - page * p.page;
-    unsigned char* block = p.cache + ((long long)page * p.H + pair.h) * ((long long)p.page * kTokenBytes<D>);
-    *reinterpret_cast<uint32_t*>(block + key_at<D>(t, l)) = ck[j];
+    const int t = pair.t[j];
+    unsigned char* block = p.cache + ((long long)pair.page[j] * p.H + pair.h) * ((long long)p.page * kTokenBytes<D>);
+    *reinterpret_cast<uint32_t*>(block + key_at<D>(t, l)) = codes[2 * j];
     if (!pair.next) {
       unsigned char* at = block + value_at<D>(p.page, t, l);
-      *reinterpret_cast<unsigned short*>(at) = (unsigned short)cv[j];
-      *reinterpret_cast<unsigned short*>(at + 4) = (unsigned short)(cv[j] >> 16);
+      *reinterpret_cast<unsigned short*>(at) = (unsigned short)codes[2 * j + 1];
+      *reinterpret_cast<unsigned short*>(at + 4) = (unsigned short)(codes[2 * j + 1] >> 16);
     } else if (j == 0) {
       *reinterpret_cast<uint2*>(block + value_at<D>(p.page, t, l)) =
-          make_uint2(__byte_perm(cv[0], cv[1], 0x5410), __byte_perm(cv[0], cv[1], 0x7632));
+          make_uint2(__byte_perm(codes[1], codes[3], 0x5410), __byte_perm(codes[1], codes[3], 0x7632));
     }
-    if (l == 0) *reinterpret_cast<uint2*>(block + numbers_at<D>(p.page, t)) = make_uint2(nk[j], nv[j]);
+    if (l == 0) *reinterpret_cast<uint2*>(block + numbers_at<D>(p.page, t)) = make_uint2(n[2 * j], n[2 * j + 1]);
   }
 }
 
@@ -233,16 +264,16 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kStoreThreads) read_kv4_kernel(const __grid_constant__ StoreParams p) {
   constexpr int LANES = D / 8;
   const int l = threadIdx.x % LANES;
-  const long long item = ((long long)blockIdx.x * kStoreThreads + threadIdx.x) / LANES;
-  if (item >= ((long long)p.R + 1) / 2 * p.H) return;
+  const uint32_t item = blockIdx.x * (kStoreThreads / LANES) + threadIdx.x / LANES;
+  if (item >= pair_items(p)) return;
   const RowPair pair = row_pair(p, item);
   uint32_t ck[2] = {0, 0}, cv[2] = {0, 0};
   uint2 n[2] = {make_uint2(0, 0), make_uint2(0, 0)};
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     if (pair.slot[j] < 0) continue;
-    const int page = pair.slot[j] / p.page, t = pair.slot[j] - page * p.page;
-    const unsigned char* block = p.cache + ((long long)page * p.H + pair.h) * ((long long)p.page * kTokenBytes<D>);
+    const int t = pair.t[j];
+    const unsigned char* block = p.cache + ((long long)pair.page[j] * p.H + pair.h) * ((long long)p.page * kTokenBytes<D>);
     ck[j] = *reinterpret_cast<const uint32_t*>(block + key_at<D>(t, l));
     if (!pair.next) {
       const unsigned char* at = block + value_at<D>(p.page, t, l);
