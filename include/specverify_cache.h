@@ -110,6 +110,7 @@ sv_status sv_plan_round(int B, int gamma, int page, int N, int pool, int32_t* le
  *   dtype      SV_DTYPE_BF16 or SV_DTYPE_F16
  *   slots      [B][gamma+1] int32: a row whose slot is outside
  *              [0, pages * page) is not written.  No slot is given twice
+ *   cache      overlaps neither k nor v (SV_ERR_INVALID_ARG)
  */
 sv_status sv_append_kv4(int B, int gamma, int heads, int D, int page, int pages, const void* k,
                         const int64_t* k_strides, const void* v, const int64_t* v_strides, sv_dtype dtype,
@@ -117,8 +118,8 @@ sv_status sv_append_kv4(int B, int gamma, int heads, int D, int page, int pages,
 
 /*
  * What R slots hold: k, v [R][heads][D] of the model's type, contiguous and
- * 16-byte aligned, scale * code + offset rounded to it; 0 where the slot is
- * outside [0, pages * page).
+ * 16-byte aligned, apart from each other and from cache: scale * code + offset
+ * rounded to it; 0 where the slot is outside [0, pages * page).
  */
 sv_status sv_read_kv4(int R, int heads, int D, int page, int pages, const void* cache, sv_dtype dtype,
                       const int32_t* slots, void* k, void* v, sv_stream_t stream);
@@ -141,7 +142,8 @@ sv_status sv_read_kv4(int R, int heads, int D, int page, int pages, const void* 
  *                -1: none
  *   scale        positive and finite
  *   out          [B][gamma+1][heads * G][D] of q's type, contiguous, 16-byte
- *                aligned.  A row that sees no token is 0
+ *                aligned, overlapping neither q nor cache.  A row that sees no
+ *                token is 0
  *   lse          [B][gamma+1][heads * G] float32 or NULL; -inf where a row
  *                sees no token
  *   fill         nonzero: rows behind gamma_b become 0 in out and lse; 0: they

@@ -35,6 +35,17 @@ bool strides_ok(const int64_t* s) {
   return true;
 }
 
+// The bytes from x on of [B][rows][heads][D] 16-bit elements through strides.
+size_t extent(const int64_t* strides, int B, int rows, int heads, int D) {
+  return 2 * ((size_t)(B - 1) * strides[0] + (size_t)(rows - 1) * strides[1] + (size_t)(heads - 1) * strides[2] + D);
+}
+// a's na bytes and b's nb have nothing in common
+bool apart(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x + na <= y || y + nb <= x;
+}
+size_t cache_bytes(int pages, int heads, int page, int D) { return (size_t)pages * heads * page * (D + 8); }
+
 int device_index() {
   int dev = 0;
   return cudaGetDevice(&dev) == cudaSuccess ? dev : -1;
@@ -249,6 +260,9 @@ extern "C" sv_status sv_append_kv4(int B, int gamma, int heads, int D, int page,
     return SV_ERR_INVALID_ARG;
   if (B == 0 || pages == 0) return SV_OK;
   if (!k || !v || !slots || !cache || !aligned16(k) || !aligned16(v) || !aligned16(cache)) return SV_ERR_INVALID_ARG;
+  if (!apart(k, extent(k_strides, B, gamma + 1, heads, D), cache, cache_bytes(pages, heads, page, D)) ||
+      !apart(v, extent(v_strides, B, gamma + 1, heads, D), cache, cache_bytes(pages, heads, page, D)))
+    return SV_ERR_INVALID_ARG;
   sv::cache::StoreParams p = store_params(B * (gamma + 1), gamma + 1, heads, page, pages, slots);
   p.k = k;
   p.v = v;
@@ -277,6 +291,10 @@ extern "C" sv_status sv_read_kv4(int R, int heads, int D, int page, int pages, c
     return SV_ERR_INVALID_ARG;
   if (R == 0) return SV_OK;
   if (!slots || !k || !v || !aligned16(k) || !aligned16(v) || (pages > 0 && (!cache || !aligned16(cache))))
+    return SV_ERR_INVALID_ARG;
+  const size_t bytes = (size_t)R * heads * D * 2;
+  if (!apart(k, bytes, v, bytes) || !apart(k, bytes, cache, cache_bytes(pages, heads, page, D)) ||
+      !apart(v, bytes, cache, cache_bytes(pages, heads, page, D)))
     return SV_ERR_INVALID_ARG;
   sv::cache::StoreParams p = store_params(R, 1, heads, page, pages, slots);
   p.cache = static_cast<unsigned char*>(const_cast<void*>(cache));
@@ -313,6 +331,11 @@ extern "C" sv_status sv_attend_kv4(int B, int gamma, int heads, int G, int D, in
   if (B == 0) return SV_OK;
   if (!q || !lengths || !out || !aligned16(q) || !aligned16(out) || (N > 0 && !block_table) ||
       (pages > 0 && (!cache || !aligned16(cache))))
+    return SV_ERR_INVALID_ARG;
+  // (a CTA may write a row while another still reads q)
+  const size_t out_bytes = (size_t)B * (gamma + 1) * heads * G * D * 2;
+  if (!apart(out, out_bytes, q, extent(q_strides, B, gamma + 1, heads * G, D)) ||
+      !apart(out, out_bytes, cache, cache_bytes(pages, heads, page, D)))
     return SV_ERR_INVALID_ARG;
   if (!workspace || !aligned16(workspace) || workspace_bytes < sv_attend_kv4_workspace_bytes(gamma, heads, G, D))
     return SV_ERR_WORKSPACE;

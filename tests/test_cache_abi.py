@@ -63,8 +63,8 @@ def test_empty_calls(sv):
 
 
 def _append(sv, **kw):
-    a = dict(B=4, gamma=3, heads=2, D=64, page=16, pages=8, k=A, k_strides=(512, 128, 64), v=A, v_strides=(512, 128, 64),
-             dtype=sv.SV_DTYPE_BF16, slots=A, cache=A, stream=None)
+    a = dict(B=4, gamma=3, heads=2, D=64, page=16, pages=8, k=A, k_strides=(512, 128, 64), v=A + 65536, v_strides=(512, 128, 64),
+             dtype=sv.SV_DTYPE_BF16, slots=A, cache=A + (1 << 20), stream=None)
     a.update(kw)
     return sv.sv_append_kv4(*a.values())
 
@@ -72,28 +72,29 @@ def _append(sv, **kw):
 @pytest.mark.parametrize("kw", [dict(B=-1), dict(gamma=-1), dict(B=1 << 20, gamma=16), dict(heads=0), dict(heads=1025), dict(D=96),
                                 dict(D=256), dict(page=15), dict(page=512), dict(pages=-1), dict(pages=(1 << 26) + 1),
                                 dict(k=None), dict(v=None), dict(slots=None), dict(cache=None), dict(k=A + 8), dict(v=A + 2),
-                                dict(cache=A + 8), dict(dtype=0), dict(dtype=7), dict(k_strides=None), dict(v_strides=None),
+                                dict(cache=A + (1 << 20) + 8), dict(cache=A), dict(cache=A + 65536 + 128), dict(cache=A - 16), dict(dtype=0), dict(dtype=7), dict(k_strides=None), dict(v_strides=None),
                                 dict(k_strides=(512, 132, 64)), dict(v_strides=(512, -128, 64))])
 def test_append_refuses(sv, kw):
     assert _append(sv, **kw) == sv.SV_ERR_INVALID_ARG
 
 
 def _read(sv, **kw):
-    a = dict(R=16, heads=2, D=64, page=16, pages=8, cache=A, dtype=sv.SV_DTYPE_F16, slots=A, k=A, v=A, stream=None)
+    a = dict(R=16, heads=2, D=64, page=16, pages=8, cache=A, dtype=sv.SV_DTYPE_F16, slots=A, k=A + (1 << 20), v=A + (1 << 21), stream=None)
     a.update(kw)
     return sv.sv_read_kv4(*a.values())
 
 
 @pytest.mark.parametrize("kw", [dict(R=-1), dict(R=(1 << 24) + 1), dict(heads=0), dict(D=32), dict(page=20), dict(pages=-1),
                                 dict(cache=None), dict(cache=A + 4), dict(dtype=0), dict(slots=None), dict(k=None),
-                                dict(v=None), dict(k=A + 2), dict(v=A + 8)])
+                                dict(v=None), dict(k=A + (1 << 20) + 2), dict(v=A + (1 << 21) + 8), dict(k=A),
+                                dict(v=A + 1024), dict(v=A + (1 << 20) + 4080)])
 def test_read_refuses(sv, kw):
     assert _read(sv, **kw) == sv.SV_ERR_INVALID_ARG
 
 
 def _attend(sv, **kw):
-    a = dict(B=4, gamma=3, heads=2, G=4, D=64, page=16, pages=8, N=4, q=A, q_strides=(2048, 512, 64), dtype=sv.SV_DTYPE_BF16, cache=A,
-             block_table=A, lengths=A, gamma_b=None, scale=0.125, out=A, lse=None, fill=0, workspace=A, nbytes=1 << 40, stream=None)
+    a = dict(B=4, gamma=3, heads=2, G=4, D=64, page=16, pages=8, N=4, q=A, q_strides=(2048, 512, 64), dtype=sv.SV_DTYPE_BF16, cache=A + (1 << 21),
+             block_table=A, lengths=A, gamma_b=None, scale=0.125, out=A + (1 << 20), lse=None, fill=0, workspace=A, nbytes=1 << 40, stream=None)
     a.update(kw)
     return sv.sv_attend_kv4(*a.values())
 
@@ -101,9 +102,10 @@ def _attend(sv, **kw):
 @pytest.mark.parametrize("kw", [dict(B=-1), dict(gamma=-1), dict(gamma=65), dict(heads=0), dict(G=0), dict(G=65), dict(D=72),
                                 dict(page=0), dict(pages=-1), dict(N=-1), dict(N=(1 << 26) + 1), dict(q=None), dict(q=A + 8),
                                 dict(q_strides=None), dict(q_strides=(2048, 516, 64)), dict(dtype=0), dict(cache=None),
-                                dict(cache=A + 1), dict(block_table=None), dict(lengths=None), dict(scale=0.0),
+                                dict(cache=A + (1 << 21) + 1), dict(block_table=None), dict(lengths=None), dict(scale=0.0),
                                 dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")), dict(scale=3e38),
-                                dict(out=None), dict(out=A + 4)])
+                                dict(out=None), dict(out=A + (1 << 20) + 4), dict(out=A), dict(out=A + 16320),
+                                dict(out=A + (1 << 21))])
 def test_attend_refuses(sv, kw):
     assert _attend(sv, **kw) == sv.SV_ERR_INVALID_ARG
 
