@@ -26,7 +26,8 @@ LIBNAME = "libspecverify.so"
 LIB_PATH = os.path.join(LIBDIR, LIBNAME)
 
 SOURCES = [os.path.join(CSRC, "sv_api.cu"), os.path.join(CSRC, "sv_noalloc.cu"), os.path.join(ROWS, "sv_rows_api.cu"),
-           os.path.join(CACHE, "sv_cache_api.cu")]
+           os.path.join(CACHE, "sv_cache_api.cu"), os.path.join(CACHE, "sv_attend_bf16.cu"),
+           os.path.join(CACHE, "sv_attend_f16.cu")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

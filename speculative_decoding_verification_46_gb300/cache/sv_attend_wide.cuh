@@ -104,7 +104,7 @@ __device__ __forceinline__ bool phase_there(uint32_t barrier, uint32_t parity) {
       : "=r"(done) : "r"(barrier), "r"(parity), "r"(100000u) : "memory");
   return done != 0;
 }
-__device__ __noinline__ void wait_longer(uint32_t barrier, uint32_t parity, volatile int* gave_up) {
+static __device__ __noinline__ void wait_longer(uint32_t barrier, uint32_t parity, volatile int* gave_up) {
   bool done = false;
   for (int i = 0; i < kWdPatience && !done; ++i) {
     done = phase_there(barrier, parity);

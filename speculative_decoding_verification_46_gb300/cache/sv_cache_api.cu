@@ -9,15 +9,12 @@
 #include <cstdint>
 
 #include "specverify_cache.h"
-#include "sv_attend.cuh"
-#include "sv_attend_wide.cuh"
+#include "sv_attend_plan.h"
 #include "sv_kv4.cuh"
 #include "sv_plan.cuh"
 
 namespace {
 
-constexpr size_t kAlign = 256;
-size_t up(size_t x) { return (x + kAlign - 1) & ~(kAlign - 1); }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool model_type(sv_dtype dt) { return dt == SV_DTYPE_BF16 || dt == SV_DTYPE_F16; }
 bool page_ok(int page) { return page >= 16 && page <= SV_MAX_CACHE_PAGE && page % 16 == 0; }
@@ -46,54 +43,8 @@ bool apart(const void* a, size_t na, const void* b, size_t nb) {
 }
 size_t cache_bytes(int pages, int heads, int page, int D) { return (size_t)pages * heads * page * (D + 8); }
 
-int device_index() {
-  int dev = 0;
-  return cudaGetDevice(&dev) == cudaSuccess ? dev : -1;
-}
-int sm_count() {
-  static std::atomic<int> cached[64];
-  const int dev = device_index();
-  if (dev < 0) return 152;
-  if (dev < 64 && cached[dev].load(std::memory_order_relaxed) > 0) return cached[dev].load(std::memory_order_relaxed);
-  int n = 0;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 152;
-  if (dev < 64) cached[dev].store(n, std::memory_order_relaxed);
-  return n;
-}
-
-// Opt in to `most` bytes of dynamic shared memory, the most that any launch of
-// the kernel asks for, once per kernel (`set`: a static of the launch site) and
-// device: threads that come here together set the same limit.
-bool allow_smem(std::atomic<bool> (&set)[64], const void* kern, size_t most) {
-  const int dev = device_index();
-  if (dev < 0 || dev >= 64) return false;
-  if (set[dev].load(std::memory_order_acquire)) return true;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) != cudaSuccess) {
-    cudaGetLastError();
-    return false;
-  }
-  set[dev].store(true, std::memory_order_release);
-  return true;
-}
-
-sv_status launched() { return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA; }
-
-template <typename K, typename P>
-sv_status launch(K kern, dim3 grid, unsigned block, size_t smem, cudaStream_t stream, const P& p,
-                 cudaLaunchAttribute* attr) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(block);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) {
-    cudaGetLastError();
-    return SV_ERR_CUDA;
-  }
-  return launched();
-}
+using sv::cache::allow_smem;
+using sv::cache::launched;
 
 // ---------------------------------------------------------------- store
 
@@ -114,78 +65,6 @@ unsigned store_grid(int R, int heads, int D) {
   const long long groups = ((long long)R + 1) / 2 * heads;
   const int per_cta = sv::cache::kStoreThreads / (D / 8);
   return groups > 0x7fffffffll ? 0u : (unsigned)((groups + per_cta - 1) / per_cta);
-}
-
-// ---------------------------------------------------------------- attend
-
-// Rows of a tile: up to 24 go to attend_kernel; more to attend_wide_kernel, in
-// as few tiles as its 80 rows allow, of equal size.
-int attend_tile_rows(int rows) {
-  if (rows <= 24) return (std::max(rows, 1) + 7) / 8 * 8;
-  const int tiles = (rows + sv::cache::kWdMostRows - 1) / sv::cache::kWdMostRows;
-  return ((rows + tiles - 1) / tiles + 15) / 16 * 16;
-}
-int attend_ctas(int TR) { return sm_count() * (TR == 8 ? 4 : TR == 16 ? 3 : 2); }
-
-struct AttendLayout {
-  size_t desc, part, total;
-};
-AttendLayout attend_layout(int TR, int D) {
-  AttendLayout L;
-  const size_t ctas = attend_ctas(TR);
-  L.desc = 0;
-  L.part = up(ctas * sizeof(int4));
-  L.total = L.part + up(2 * ctas * sv::cache::part_floats(TR, D) * sizeof(float));
-  return L;
-}
-
-template <typename T, int D, int TR>
-sv_status launch_attend(sv::cache::AttendParams p, void* workspace, cudaStream_t stream) {
-  using namespace sv::cache;
-  const int ctas = attend_ctas(TR);
-  const AttendLayout L = attend_layout(TR, D);
-  p.desc = reinterpret_cast<int4*>(static_cast<unsigned char*>(workspace) + L.desc);
-  p.part = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + L.part);
-  static std::atomic<bool> set[64];
-  if constexpr (TR <= 24) {
-    using Shape = AttendShape<T, D, TR / 8>;
-    auto kern = attend_kernel<T, D, TR / 8>;
-    if (!allow_smem(set, (const void*)kern, Shape::kSmem)) return SV_ERR_CUDA;
-    kern<<<ctas, Shape::kThreads, Shape::kSmem, stream>>>(p);
-  } else {
-    auto kern = attend_wide_kernel<T, D, TR / 16>;
-    if (!allow_smem(set, (const void*)kern, WideShape<T, D, TR / 16>::kSmem)) return SV_ERR_CUDA;
-    kern<<<ctas, kWdThreads, WideShape<T, D, TR / 16>::kSmem, stream>>>(p);
-  }
-  const sv_status st = launched();
-  if (st != SV_OK) return st;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas, TR * 32 / kAtJoinThreads);
-  cfg.blockDim = dim3(kAtJoinThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, attend_join_kernel<T, D>, p, TR) != cudaSuccess) {
-    cudaGetLastError();
-    return SV_ERR_CUDA;
-  }
-  return launched();
-}
-
-template <typename T, int D>
-sv_status launch_attend_rows(const sv::cache::AttendParams& p, void* workspace, cudaStream_t stream) {
-  switch (attend_tile_rows(p.rows * p.G)) {
-    case 8: return launch_attend<T, D, 8>(p, workspace, stream);
-    case 16: return launch_attend<T, D, 16>(p, workspace, stream);
-    case 24: return launch_attend<T, D, 24>(p, workspace, stream);
-    case 32: return launch_attend<T, D, 32>(p, workspace, stream);
-    case 48: return launch_attend<T, D, 48>(p, workspace, stream);
-    case 64: return launch_attend<T, D, 64>(p, workspace, stream);
-    default: return launch_attend<T, D, 80>(p, workspace, stream);
-  }
 }
 
 bool attend_sizes_ok(int gamma, int heads, int G, int D) {
@@ -316,7 +195,7 @@ extern "C" sv_status sv_read_kv4(int R, int heads, int D, int page, int pages, c
 
 extern "C" size_t sv_attend_kv4_workspace_bytes(int gamma, int heads, int G, int D) {
   if (!attend_sizes_ok(gamma, heads, G, D)) return 0;
-  return attend_layout(attend_tile_rows((gamma + 1) * G), D).total;
+  return sv::cache::attend_layout(sv::cache::attend_tile_rows((gamma + 1) * G), D).total;
 }
 
 extern "C" sv_status sv_attend_kv4(int B, int gamma, int heads, int G, int D, int page, int pages, int N, const void* q,
@@ -358,8 +237,6 @@ extern "C" sv_status sv_attend_kv4(int B, int gamma, int heads, int G, int D, in
   p.lse = lse;
   p.fill = fill;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (dtype == SV_DTYPE_BF16)
-    return D == 64 ? launch_attend_rows<__nv_bfloat16, 64>(p, workspace, s)
-                   : launch_attend_rows<__nv_bfloat16, 128>(p, workspace, s);
-  return D == 64 ? launch_attend_rows<__half, 64>(p, workspace, s) : launch_attend_rows<__half, 128>(p, workspace, s);
+  return dtype == SV_DTYPE_BF16 ? sv::cache::launch_attend_bf16(p, D, workspace, s)
+                                : sv::cache::launch_attend_f16(p, D, workspace, s);
 }
