@@ -39,8 +39,8 @@ namespace sv {
 namespace cache {
 
 constexpr int kAtUnit = 128;              // tokens of a unit
-constexpr int kAtStart = 2;               // units that stand for a segment's start
-constexpr int kAtStages = 3;              // groups of 32 tokens in a warp's ring
+constexpr int kAtStart = 3;               // units that stand for a segment's start
+constexpr int kAtStages = 2;              // groups of 32 tokens in a warp's ring
 constexpr int kAtJoinThreads = 256;
 constexpr float kAtSlack = 8.f;           // a row's reference may be 2^8 below its largest term
 constexpr float kAtValueTop = 128.f;      // largest s' 2^x: p s' 2^x stays below 2^(7 + 8), float16 ends at 65504

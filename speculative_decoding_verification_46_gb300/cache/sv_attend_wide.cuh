@@ -137,10 +137,11 @@ struct WideShape {
   static constexpr int kSubKeys = 8 * D, kSubValues = 8 * D + 16, kSubNumbers = 128 + 16;
   static constexpr int oValues = 8 * kSubKeys, oNumbers = oValues + 8 * kSubValues, kStage = oNumbers + 8 * kSubNumbers;
   static constexpr int kQ = R * D * 2, kP = R * kWdUnit * 2;
-  // steps in the ring: as many as two CTAs have room for
+  // steps in the ring: three (a fourth gained nothing: 97.5 against 96.2 us for 40
+  // rows), or the two that the CTAs have room for
   static constexpr int oP = kQ, oRing = oP + (kFine ? 2 : 1) * kP;
   static constexpr int kRoom = (112 * 1024 - 1024 - R * 18 * 4 - oRing) / kStage;
-  static constexpr int kStages = kRoom < 4 ? kRoom : 4;
+  static constexpr int kStages = kRoom < 3 ? kRoom : 3;
   static constexpr int oSmall = oRing + kStages * kStage;
   // row pairs' sums of q and references [4 R / 2], factor, tops [4], masses
   // [4], shifts [4]; limits; rows of the output
