@@ -258,6 +258,10 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
+// The power of two (its exponent) that brings a row's largest element to
+// [2^13, 2^14).
+__device__ __forceinline__ int raised_by(float top) { return top > 0.f ? min(140 - (int)(__float_as_uint(top) >> 23), 126) : 0; }
+
 // NT: groups of eight rows
 template <typename T, int D, int NT>
 struct AttendShape {
@@ -285,7 +289,7 @@ __global__ void __launch_bounds__(AttendShape<T, D, NT>::kThreads, AttendShape<T
   constexpr int kWarps = S::kWarps, kThreads = S::kThreads;
   constexpr bool kFine = std::is_same<T, __half>::value;     // the weights' rest is an operand too
   extern __shared__ __align__(16) float at_sm[];
-  __shared__ float q_sums[TR], warp_top[kWarps];
+  __shared__ float q_sums[TR], row_scales[TR];
   __shared__ int limits[TR];
   __shared__ long long out_rows[TR];
   const int tid = threadIdx.x, lane = tid & 31, g = lane >> 2, c = lane & 3;
@@ -388,17 +392,13 @@ __global__ void __launch_bounds__(AttendShape<T, D, NT>::kThreads, AttendShape<T
 #pragma unroll
     for (int n = 0; n < kAtStages - 1; ++n) copy_group(n);
 
-    // ---- q as operands: float16 with one power of two for the tile (a row
-    // whose largest element is 2^-20 of the tile's still has its scores to
-    // 2^-17 of their size)
-    float row_scale;
+    // ---- q as operands: float16 with a power of two per row
     {
-      float top = 0.f;
 #pragma unroll
       for (int k = 0; k < PIECES; ++k) {
-        const int x = tid + k * kThreads, rl = x / LANES;
+        const int x = tid + k * kThreads, rl = x / LANES, word = x % LANES;
         const uint32_t w[4] = {qv[k].x, qv[k].y, qv[k].z, qv[k].w};
-        float sum = 0.f;
+        float top = 0.f, sum = 0.f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float f0 = Kv<T>::lo(w[j]), f1 = Kv<T>::hi(w[j]);
@@ -406,31 +406,20 @@ __global__ void __launch_bounds__(AttendShape<T, D, NT>::kThreads, AttendShape<T
           sum += f0 + f1;
         }
 #pragma unroll
-        for (int m = LANES / 2; m >= 1; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-        if (x % LANES == 0 && rl < TR) {
+        for (int m = LANES / 2; m >= 1; m >>= 1) {
+          sum += __shfl_xor_sync(0xffffffffu, sum, m);
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
+        }
+        if (rl >= TR) continue;
+        const int up = raised_by(top);
+        const float raise = __uint_as_float((uint32_t)(up + 127) << 23);
+        if (word == 0) {
           const int r = rt * TR + rl, i = r / p.G;
-          q_sums[rl] = sum;
+          q_sums[rl] = sum * raise * 0x1p-24f;   // (the products' unit is 2^-24 of a code)
+          row_scales[rl] = p.scale * 0x1p24f * __uint_as_float((uint32_t)(127 - up) << 23);
           limits[rl] = i < s.rows ? min(s.first - 1 + i, s.seen - 1) : -1;
           out_rows[rl] = i < s.rows ? ((long long)b * p.rows + i) * p.H * p.G + (long long)h * p.G + (r - i * p.G) : -1;
         }
-      }
-#pragma unroll
-      for (int m = 16; m >= 1; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
-      if (lane == 0) warp_top[warp] = top;
-      __syncthreads();
-#pragma unroll
-      for (int j = 0; j < kWarps; ++j) top = fmaxf(top, warp_top[j]);
-      // 2^up * top in [2^13, 2^14)
-      const int up = top > 0.f ? min(140 - (int)(__float_as_uint(top) >> 23), 126) : 0;
-      const float raise = __uint_as_float((uint32_t)(up + 127) << 23);
-      row_scale = p.scale * 0x1p24f * __uint_as_float((uint32_t)(127 - up) << 23);
-      // the products' unit is 2^-24 of a code
-      if (tid < TR) q_sums[tid] *= raise * 0x1p-24f;
-#pragma unroll
-      for (int k = 0; k < PIECES; ++k) {
-        const int x = tid + k * kThreads, rl = x / LANES, word = x % LANES;
-        if (rl >= TR) break;
-        const uint32_t w[4] = {qv[k].x, qv[k].y, qv[k].z, qv[k].w};
         // word j of quarter cc: halves t; channels 2 t, 2 t + 4 as they are,
         // 2 t + 1, 2 t + 5 for codes of 16 times their size
         const int cc = word / KW, j = word % KW;
@@ -446,12 +435,14 @@ __global__ void __launch_bounds__(AttendShape<T, D, NT>::kThreads, AttendShape<T
     }
 
     // rows 8 m + 2 c and + 1
-    Two q_sum[NT], minus_ref[NT], mass[NT], shift[NT];
+    Two q_sum[NT], row_scale[NT], minus_ref[NT], mass[NT], shift[NT];
     float o[NT][2 * KW][4];
 #pragma unroll
     for (int m = 0; m < NT; ++m) {
       const float2 q = *reinterpret_cast<const float2*>(q_sums + 8 * m + 2 * c);
+      const float2 f = *reinterpret_cast<const float2*>(row_scales + 8 * m + 2 * c);
       q_sum[m] = two(q.x, q.y);
+      row_scale[m] = two(f.x, f.y);
       minus_ref[m] = mass[m] = shift[m] = two(0.f, 0.f);
 #pragma unroll
       for (int t = 0; t < 2 * KW; ++t)
@@ -514,13 +505,13 @@ __global__ void __launch_bounds__(AttendShape<T, D, NT>::kThreads, AttendShape<T
           // (those of tokens that nobody sees may be anything)
           if (kMasked && (!(subs >> i & 1) || token0 + 16 * i + 8 * e + g >= s.seen)) x[0] = x[1] = 0;
           nv[i][e] = x[1];
-          const float k_scale = Kv<T>::lo(x[0]) * row_scale, k_offset = Kv<T>::hi(x[0]) * row_scale;
+          const float k_scale = Kv<T>::lo(x[0]), k_offset = Kv<T>::hi(x[0]);
           const Two ks = two(k_scale, k_scale), ko = two(k_offset, k_offset);
           largest = fmaxf(largest, Kv<T>::lo(x[1]));
 #pragma unroll
           for (int m = 0; m < NT; ++m) {
             float y0, y1;
-            split(fma2(two(z[i][m][2 * e], z[i][m][2 * e + 1]), ks, fma2(ko, q_sum[m], minus_ref[m])), y0, y1);
+            split(fma2(fma2(two(z[i][m][2 * e], z[i][m][2 * e + 1]), ks, mul2(ko, q_sum[m])), row_scale[m], minus_ref[m]), y0, y1);
             if (kMasked) {
               const int2 see = sees(m, i, e);
               if (!see.x) y0 = __int_as_float(0xff800000);

@@ -140,12 +140,12 @@ struct WideShape {
   // steps in the ring: three (a fourth gained nothing: 97.5 against 96.2 us for 40
   // rows), or the two that the CTAs have room for
   static constexpr int oP = kQ, oRing = oP + (kFine ? 2 : 1) * kP;
-  static constexpr int kRoom = (112 * 1024 - 1024 - R * 18 * 4 - oRing) / kStage;
+  static constexpr int kRoom = (112 * 1024 - 1024 - R * 19 * 4 - 8 - oRing) / kStage;
   static constexpr int kStages = kRoom < 3 ? kRoom : 3;
   static constexpr int oSmall = oRing + kStages * kStage;
   // row pairs' sums of q and references [4 R / 2], factor, tops [4], masses
-  // [4], shifts [4]; limits; rows of the output
-  static constexpr int kSmall = R * 18 * 4;
+  // [4], shifts [4], scales; limits; rows of the output
+  static constexpr int kSmall = R * 19 * 4 + 8;
   static constexpr int kSmem = oSmall + kSmall + 1024;            // (aligned to 1 KB in the kernel)
   static constexpr bool kTight = D / 2 + 64 + 2 * R > kWdColumns;
   static constexpr int cV = D / 2, cS = kTight ? cV : cV + 64, cO = cS + R;
@@ -176,7 +176,8 @@ __global__ void __launch_bounds__(kWdThreads, 2) attend_wide_kernel(const __grid
   float* const tops = factor + R;
   float* const masses = tops + 4 * R;
   float* const shifts = masses + 4 * R;
-  int* const limits = reinterpret_cast<int*>(shifts + 4 * R);
+  float* const row_scales = shifts + 4 * R;
+  int* const limits = reinterpret_cast<int*>(row_scales + R);
   long long* const out_rows = reinterpret_cast<long long*>(limits + R);
   volatile int* const gave_up = &gave_up_flag;
   // scores there, sums there
@@ -338,60 +339,43 @@ __global__ void __launch_bounds__(kWdThreads, 2) attend_wide_kernel(const __grid
       copies_end_group();
     };
 
-    // ---- q: float16 with one power of two for the tile (a row whose largest
-    // element is 2^-20 of the tile's still has its scores to 2^-17 of their
-    // size), channels in the order in which the key codes come: element
-    // 2 (c + 4 (4 k + i)) + e is channel 8 (KW c + k) + i + 4 e, halves e of
-    // pair i of word k
-    float row_scale;
+    // ---- q: float16 with a power of two per row, channels in the order in
+    // which the key codes come: element 2 (c + 4 (4 k + i)) + e is channel 8 (KW
+    // c + k) + i + 4 e, halves e of pair i of word k
     {
-      float top = 0.f;
-#pragma unroll
-      for (int k = 0; k < PIECES; ++k) {
-        const int x = tid + k * kWdThreads, rl = x / LANES;
-        const uint32_t ww[4] = {qv[k].x, qv[k].y, qv[k].z, qv[k].w};
-        float sum = 0.f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float f0 = Kv<T>::lo(ww[j]), f1 = Kv<T>::hi(ww[j]);
-          top = max3(top, fabsf(f0), fabsf(f1));
-          sum += f0 + f1;
-        }
-#pragma unroll
-        for (int m = LANES / 2; m >= 1; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-        if (x % LANES == 0 && rl < R) {
-          const int r = rt * R + rl, i = r / p.G;
-          reinterpret_cast<float*>(pairs + (rl >> 1))[rl & 1] = sum;
-          reinterpret_cast<float*>(pairs + (rl >> 1))[2 + (rl & 1)] = 0.f;
-          limits[rl] = i < s.rows ? min(s.first - 1 + i, s.seen - 1) : -1;
-          out_rows[rl] = i < s.rows ? ((long long)b * p.rows + i) * p.H * p.G + (long long)h * p.G + (r - i * p.G) : -1;
-        }
-      }
-#pragma unroll
-      for (int m = 16; m >= 1; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
-      if (lane == 0) warp_top[warp] = top;
-      __syncthreads();
-#pragma unroll
-      for (int j = 0; j < 8; ++j) top = fmaxf(top, warp_top[j]);
-      const int up = top > 0.f ? min(140 - (int)(__float_as_uint(top) >> 23), 126) : 0;
-      const float raise = __uint_as_float((uint32_t)(up + 127) << 23);
-      row_scale = p.scale * 0x1p24f * __uint_as_float((uint32_t)(127 - up) << 23);
-      if (tid < R) reinterpret_cast<float*>(pairs + (tid >> 1))[tid & 1] *= raise * 0x1p-24f;
 #pragma unroll
       for (int k = 0; k < PIECES; ++k) {
         const int x = tid + k * kWdThreads, rl = x / LANES, word = x % LANES;
-        if (rl >= R) break;
         const uint32_t ww[4] = {qv[k].x, qv[k].y, qv[k].z, qv[k].w};
-        float f[8];
+        float f[8], top = 0.f, sum = 0.f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          f[2 * j] = Kv<T>::lo(ww[j]) * raise;
-          f[2 * j + 1] = Kv<T>::hi(ww[j]) * raise;
+          f[2 * j] = Kv<T>::lo(ww[j]);
+          f[2 * j + 1] = Kv<T>::hi(ww[j]);
+          top = max3(top, fabsf(f[2 * j]), fabsf(f[2 * j + 1]));
+          sum += f[2 * j] + f[2 * j + 1];
+        }
+#pragma unroll
+        for (int m = LANES / 2; m >= 1; m >>= 1) {
+          sum += __shfl_xor_sync(0xffffffffu, sum, m);
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
+        }
+        if (rl >= R) continue;
+        const int up = raised_by(top);
+        const float raise = __uint_as_float((uint32_t)(up + 127) << 23);
+        if (word == 0) {
+          const int r = rt * R + rl, i = r / p.G;
+          float* pair = reinterpret_cast<float*>(pairs + (rl >> 1)) + (rl & 1);
+          pair[0] = sum * raise * 0x1p-24f;      // (the products' unit is 2^-24 of a code)
+          pair[2] = 0.f;
+          row_scales[rl] = p.scale * 0x1p24f * __uint_as_float((uint32_t)(127 - up) << 23);
+          limits[rl] = i < s.rows ? min(s.first - 1 + i, s.seen - 1) : -1;
+          out_rows[rl] = i < s.rows ? ((long long)b * p.rows + i) * p.H * p.G + (long long)h * p.G + (r - i * p.G) : -1;
         }
         const int cc = word / KW, kk = word % KW;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float t = j & 1 ? 0.0625f : 1.f;
+          const float t = j & 1 ? raise * 0.0625f : raise;
           const int piece = 4 * kk + j;
           *reinterpret_cast<uint32_t*>(sp + (piece >> 3) * (R * 128) + rl * 128 + (((piece & 7) ^ (rl & 7)) << 4) + 4 * cc) =
               half2_bits(f[j] * t, f[j + 4] * t);
@@ -485,19 +469,20 @@ __global__ void __launch_bounds__(kWdThreads, 2) attend_wide_kernel(const __grid
           for (int bl = 0; bl < 2; ++bl)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const float a = Kv<T>::lo(nk[bl][e]) * row_scale, o = Kv<T>::hi(nk[bl][e]) * row_scale;
+              const float a = Kv<T>::lo(nk[bl][e]), o = Kv<T>::hi(nk[bl][e]);
               ks[bl][e] = two(a, a);
               ko[bl][e] = two(o, o);
             }
 #pragma unroll
           for (int k = 0; k < NG; ++k) {
             const float4 pair = my_pairs[4 * k];
-            const Two q = two(pair.x, pair.y), r = two(pair.z, pair.w);
+            const float2 scale = *reinterpret_cast<const float2*>(row_scales + wg * RH + 8 * k + 2 * c);
+            const Two q = two(pair.x, pair.y), r = two(pair.z, pair.w), f = two(scale.x, scale.y);
 #pragma unroll
             for (int bl = 0; bl < 2; ++bl)
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                const Two y = fma2(two(z[bl][k][2 * e], z[bl][k][2 * e + 1]), ks[bl][e], fma2(ko[bl][e], q, r));
+                const Two y = fma2(fma2(two(z[bl][k][2 * e], z[bl][k][2 * e + 1]), ks[bl][e], mul2(ko[bl][e], q)), f, r);
                 float y0, y1;
                 split(y, y0, y1);
                 if (kMasked) {

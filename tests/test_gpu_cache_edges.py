@@ -224,3 +224,37 @@ def test_plan_around_its_forms(sv, rows):
         s = _State(B, rows // 16 + 40, B * (rows // 16 + 40), 16, rows, 300)
         s.round(sv, rows // B)
         s.round(sv, rows // B, kept=np.full(B, rows // (2 * B)), gamma_b=np.full(B, rows // (3 * B)))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("gamma, group", [(0, 4), (3, 4), (4, 8)])
+def test_rows_do_not_touch_each_other(sv, dtype, gamma, group):
+    """A row of NaN, of infinities or of other sizes changes nothing in the rows beside it."""
+    lengths = [300]
+    c = _Cache(sv, [n + gamma + 1 for n in lengths], 1, 128, 16, dtype)
+    q = _q(1, gamma + 1, group, 128, dtype)
+    want, want_lse = sv.attend_kv4(q, c.cache, c.table, _i32(lengths), 16, return_lse=True)
+    _check(want, want_lse, q, c, lengths, dtype)
+    for i, bad in enumerate((float("nan"), float("inf"), -float("inf"), 2.0 ** 15, 2.0 ** -14)):
+        x = q.clone()
+        h = i % group
+        if abs(bad) < 1e9:
+            x[:, :, h] = x[:, :, h].sign() * bad
+        else:
+            x[:, :, h, i::7] = bad
+        out, lse = sv.attend_kv4(x, c.cache, c.table, _i32(lengths), 16, return_lse=True)
+        rest = [j for j in range(group) if j != h]
+        part = type("C", (), dict(k=c.k, v=c.v, D=128))
+        _check(out[:, :, rest].contiguous(), lse[:, :, rest], q[:, :, rest].contiguous(), part, lengths, dtype)
+        if bad != bad or abs(bad) == float("inf"):
+            assert out[:, :, h].isnan().all()
+
+
+@pytest.mark.parametrize("group", [4, 40])
+def test_rows_of_very_different_sizes(sv, group):
+    """Queries 2^60 apart in one tile, each with a scale of scores of its own."""
+    c = _Cache(sv, [200], 1, 64, 16, "bf16")
+    q = _q(1, 1, group, 64, "bf16")
+    q = q * torch.as_tensor(np.exp2(np.linspace(-60, 0, group)), device=DEV, dtype=torch.bfloat16)[:, None]
+    out, lse = sv.attend_kv4(q, c.cache, c.table, _i32([199]), 16, return_lse=True)
+    _check(out, lse, q, c, [199], "bf16")
