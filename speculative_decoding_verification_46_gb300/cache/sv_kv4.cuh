@@ -199,20 +199,28 @@ __global__ void __launch_bounds__(kStoreThreads) append_kv4_kernel(const __grid_
   const int lane = threadIdx.x & 31, l = threadIdx.x % LANES;
   const uint32_t item = blockIdx.x * (kStoreThreads / LANES) + threadIdx.x / LANES;
   RowPair pair = row_pair(p, min(item, pair_items(p) - 1));
-  if (item >= pair_items(p)) pair.slot[0] = pair.slot[1] = -1;
+  if (item >= pair_items(p)) {
+    pair.slot[0] = pair.slot[1] = -1;
+    pair.next = false;
+  }
   if (!__any_sync(0xffffffffu, pair.slot[0] >= 0 || pair.slot[1] >= 0)) return;
   uint4 x[4];                            // key, value of the first row, of the second
-  int b = pair.r / p.rows, i = pair.r - b * p.rows;
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    x[2 * j] = x[2 * j + 1] = make_uint4(0, 0, 0, 0);
-    if (pair.slot[j] >= 0) {
-      x[2 * j] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const T*>(p.k) + b * p.ks[0] + i * p.ks[1] + pair.h * p.ks[2]) + l);
-      x[2 * j + 1] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const T*>(p.v) + b * p.vs[0] + i * p.vs[1] + pair.h * p.vs[2]) + l);
+  for (int j = 0; j < 4; ++j) x[j] = make_uint4(0, 0, 0, 0);
+  {
+    const int b = pair.r / p.rows, i = pair.r - b * p.rows;
+    const long long ok = b * p.ks[0] + i * p.ks[1] + pair.h * p.ks[2], ov = b * p.vs[0] + i * p.vs[1] + pair.h * p.vs[2];
+    const T *k = static_cast<const T*>(p.k) + ok + 8 * l, *v = static_cast<const T*>(p.v) + ov + 8 * l;
+    if (pair.slot[0] >= 0) {
+      x[0] = __ldcs(reinterpret_cast<const uint4*>(k));
+      x[1] = __ldcs(reinterpret_cast<const uint4*>(v));
     }
-    if (++i == p.rows) {
-      i = 0;
-      ++b;
+    if (pair.slot[1] >= 0) {
+      const bool same = i + 1 < p.rows;    // the sequence goes on
+      k += same ? p.ks[1] : p.ks[0] - i * p.ks[1];
+      v += same ? p.vs[1] : p.vs[0] - i * p.vs[1];
+      x[2] = __ldcs(reinterpret_cast<const uint4*>(k));
+      x[3] = __ldcs(reinterpret_cast<const uint4*>(v));
     }
   }
   uint32_t ends[4];
@@ -227,20 +235,27 @@ __global__ void __launch_bounds__(kStoreThreads) append_kv4_kernel(const __grid_
     n[j] = __shfl_sync(0xffffffffu, numbers, (lane & ~3) | j);
     codes[j] = codes_of<T>(x[j], n[j], __shfl_sync(0xffffffffu, inverse, (lane & ~3) | j));
   }
+  const int block_bytes = p.page * kTokenBytes<D>;
+  if (pair.next) {
+    const int t = pair.t[0];
+    unsigned char* block = p.cache + (long long)((uint32_t)pair.page[0] * (uint32_t)p.H + pair.h) * block_bytes;
+    uint32_t* key = reinterpret_cast<uint32_t*>(block + key_at<D>(t, l));
+    key[0] = codes[0];
+    key[D / 8] = codes[2];
+    *reinterpret_cast<uint2*>(block + value_at<D>(p.page, t, l)) =
+        make_uint2(__byte_perm(codes[1], codes[3], 0x5410), __byte_perm(codes[1], codes[3], 0x7632));
+    if (l == 0) *reinterpret_cast<uint4*>(block + numbers_at<D>(p.page, t)) = make_uint4(n[0], n[1], n[2], n[3]);
+    return;
+  }
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     if (pair.slot[j] < 0) continue;
     const int t = pair.t[j];
-    unsigned char* block = p.cache + ((long long)pair.page[j] * p.H + pair.h) * ((long long)p.page * kTokenBytes<D>);
+    unsigned char* block = p.cache + (long long)((uint32_t)pair.page[j] * (uint32_t)p.H + pair.h) * block_bytes;
     *reinterpret_cast<uint32_t*>(block + key_at<D>(t, l)) = codes[2 * j];
-    if (!pair.next) {
-      unsigned char* at = block + value_at<D>(p.page, t, l);
-      *reinterpret_cast<unsigned short*>(at) = (unsigned short)codes[2 * j + 1];
-      *reinterpret_cast<unsigned short*>(at + 4) = (unsigned short)(codes[2 * j + 1] >> 16);
-    } else if (j == 0) {
-      *reinterpret_cast<uint2*>(block + value_at<D>(p.page, t, l)) =
-          make_uint2(__byte_perm(codes[1], codes[3], 0x5410), __byte_perm(codes[1], codes[3], 0x7632));
-    }
+    unsigned char* at = block + value_at<D>(p.page, t, l);
+    *reinterpret_cast<unsigned short*>(at) = (unsigned short)codes[2 * j + 1];
+    *reinterpret_cast<unsigned short*>(at + 4) = (unsigned short)(codes[2 * j + 1] >> 16);
     if (l == 0) *reinterpret_cast<uint2*>(block + numbers_at<D>(p.page, t)) = make_uint2(n[2 * j], n[2 * j + 1]);
   }
 }

@@ -258,3 +258,23 @@ def test_rows_of_very_different_sizes(sv, group):
     q = q * torch.as_tensor(np.exp2(np.linspace(-60, 0, group)), device=DEV, dtype=torch.bfloat16)[:, None]
     out, lse = sv.attend_kv4(q, c.cache, c.table, _i32([199]), 16, return_lse=True)
     _check(out, lse, q, c, [199], "bf16")
+
+
+@pytest.mark.parametrize("D, heads", [(64, 1), (128, 3), (64, 5)])
+@pytest.mark.parametrize("start", [0, 1, 15, 16, 31])
+def test_append_neighbouring_slots(sv, D, heads, start):
+    """Rows whose slots follow one another, from even and odd ones, over the
+    ends of pages and of sequences: what lies beside them stays as it is."""
+    for B, G1 in ((1, 1), (1, 2), (2, 1), (1, 3), (3, 2), (2, 5), (1, 17), (5, 3)):
+        k, v = (_model_rows((B, G1, heads, D), s, "bf16") for s in (1, 2))
+        slots = _i32(start + np.arange(B * G1).reshape(B, G1))
+        cache = sv.alloc_kv4_cache(4, heads, D, 16, DEV)
+        cache.fill_(0x5A)
+        before = sv.read_kv4(cache, _i32(np.arange(64)), 16, torch.bfloat16)
+        sv.append_kv4(k, v, slots, cache)
+        after = sv.read_kv4(cache, _i32(np.arange(64)), 16, torch.bfloat16)
+        for x, a, b in zip((k, v), before, after):
+            want = a.double().cpu().numpy()
+            rows = x.double().cpu().numpy().reshape(B * G1, heads, D)
+            want[start:start + B * G1] = cacheref.to_model(cacheref.held(rows, "bf16"), "bf16")
+            assert np.array_equal(b.double().cpu().numpy(), want)
