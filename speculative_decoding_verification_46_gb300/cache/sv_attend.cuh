@@ -21,14 +21,32 @@
 // Tokens and channels are the products' left side and the rows their right one,
 // so that eight rows cost half of what sixteen do: scores^T [16 tokens x 8 rows]
 // = codes . q^T, sums^T [16 channels x 8 rows] += (value codes)^T . weights^T.  A
-// lane then has two rows of every 16 tokens' two, and their numbers once.
+// lane then has two tokens of every 16 and two rows of every eight: it reads two
+// tokens' numbers and no others.  With the rows on the left (a lane has a row,
+// and numbers of four tokens) 8 rows took 60 us where they now take 50, 24 rows
+// 88 where 79, 128 sequences of 4096 tokens 116 where 87.
 //
-// Work: the (sequence, head, row tile)s' tokens in units of 128 are one line of
-// units; CTA i of W takes an equal part of it, finds its place from lengths
-// and walks on.  The warps of a CTA take 32 tokens at a time each, with a
-// softmax and sums of their own, and are joined at the end of the segment.  A
+// Two ways to share the work out.  attend_joined (sv_attend_plan.h) chooses.
+// Few segments, which are (sequence, head, row tile)s, over a short table: a
+// cluster of eight CTAs a segment deals its 32-token groups out to its warps, and
+// the CTAs read each other's sums from shared memory.  One launch: one request of
+// 700 tokens, 8 x 4 heads of 128, takes 4.5 us, and 9.0 us the other way.
+// Otherwise: the segments' tokens in units of 128 are one line of units; CTA i of
+// W takes an equal part of it, finds its place from lengths and walks on.  A
 // segment that a CTA does not hold in full goes to the workspace;
 // attend_join_kernel, which is launched right behind, joins these in order.
+// Either way the warps of a CTA take 32 tokens at a time each, with a softmax and
+// sums of their own, and are joined at the end of the segment, in order.
+//
+// What bounds it.  Few rows over long sequences: the cache's bytes (128 sequences
+// of 4096 tokens, 8 heads of 128, bf16: 83 us, 5.2 TB/s; 4 of 240,000: 173 us,
+// 4.5 TB/s at 16 rows).  More rows: instructions.  A group of 32 tokens costs a
+// warp about as much for masks, numbers, exponentials and the operands'
+// exchange as for its products: 32 sequences of up to 8192 tokens take 45, 58 and
+// 74 us at 8, 16 and 24 rows (32 us of bytes); at 16 rows the schedulers issue in
+// half of the cycles and the tensor pipe is busy in 40 %.  16 tokens at a time with
+// another CTA an SM was slower (206 us where 181), so were rings of three groups
+// (49 us where 47 at 8 rows).
 #pragma once
 
 #include <float.h>
@@ -42,6 +60,8 @@ constexpr int kAtUnit = 128;              // tokens of a unit
 constexpr int kAtStart = 3;               // units that stand for a segment's start
 constexpr int kAtStages = 2;              // groups of 32 tokens in a warp's ring
 constexpr int kAtJoinThreads = 256;
+constexpr int kAtCluster = 8;             // CTAs of a segment that is joined in one launch,
+constexpr int kAtShort = 8192;            // which it may be up to this many positions of a table
 constexpr float kAtSlack = 8.f;           // a row's reference may be 2^8 below its largest term
 constexpr float kAtValueTop = 128.f;      // largest s' 2^x: p s' 2^x stays below 2^(7 + 8), float16 ends at 65504
 
@@ -128,8 +148,8 @@ __device__ __forceinline__ void finish_row(const AttendParams& p, long long q_ro
 // unit is `base`; U units in all, W CTAs have one at least.  Every warp finds
 // it on its own.
 struct Part {
-  long long U, W, u, end, base;
-  int b;
+  long long U = 0, W = 0, u = 0, end = 0, base = 0;
+  int b = 0;
   __device__ __forceinline__ bool some() const { return blockIdx.x < W; }
   // the CTA that unit x belongs to
   __device__ __forceinline__ int owner(long long x) const { return (int)(((x + 1) * W - 1) / U); }
@@ -176,27 +196,29 @@ __device__ __forceinline__ Part find_part(const AttendParams& p, int TR, int uni
 // (chunks = 0) does nothing.
 struct Segment {
   int h, rt, at, chunk0, chunks, step;
-  __device__ __forceinline__ Segment(const Sequence& s, long long u, long long base, long long end) {
-    const int all = s.chunks + kAtStart;
-    int begin;
-    if (u - base < 0x7fffffffll) {        // (a 64-bit division takes longer)
-      at = (int)(u - base) / all;
-      begin = (int)(u - base) - at * all;
-    } else {
-      at = (int)((u - base) / all);
-      begin = (int)(u - base - (long long)at * all);
-    }
-    h = at / s.tiles;
-    rt = at - h * s.tiles;
-    step = (int)min((long long)(all - begin), end - u);
-    chunk0 = max(begin - kAtStart, 0);
-    chunks = max(begin + step - kAtStart, 0) - chunk0;
-  }
   // its last unit
   __device__ __forceinline__ long long last(const Sequence& s, long long base) const {
     return base + (long long)(at + 1) * (s.chunks + kAtStart) - 1;
   }
 };
+__device__ __forceinline__ Segment segment_at(const Sequence& s, long long u, long long base, long long end) {
+  Segment x;
+  const int all = s.chunks + kAtStart;
+  int begin;
+  if (u - base < 0x7fffffffll) {          // (a 64-bit division takes longer)
+    x.at = (int)(u - base) / all;
+    begin = (int)(u - base) - x.at * all;
+  } else {
+    x.at = (int)((u - base) / all);
+    begin = (int)(u - base - (long long)x.at * all);
+  }
+  x.h = x.at / s.tiles;
+  x.rt = x.at - x.h * s.tiles;
+  x.step = (int)min((long long)(all - begin), end - u);
+  x.chunk0 = max(begin - kAtStart, 0);
+  x.chunks = max(begin + x.step - kAtStart, 0) - x.chunk0;
+  return x;
+}
 
 // 32 tokens of one head in a warp's ring: two subs of 16, each its keys, then
 // its values, then (behind both) its numbers, as they lie in the cache.  As
@@ -258,6 +280,23 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
+// Shared memory of CTA k of the cluster.
+__device__ __forceinline__ uint32_t cluster_address(uint32_t at, int k) {
+  uint32_t y;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(y) : "r"(at), "r"(k));
+  return y;
+}
+__device__ __forceinline__ float cluster_load(uint32_t at) {
+  float y;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(y) : "r"(at) : "memory");
+  return y;
+}
+__device__ __forceinline__ float4 cluster_load4(uint32_t at) {
+  float4 y;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(y.x), "=f"(y.y), "=f"(y.z), "=f"(y.w) : "r"(at) : "memory");
+  return y;
+}
+
 // The power of two (its exponent) that brings a row's largest element to
 // [2^13, 2^14).
 __device__ __forceinline__ int raised_by(float top) { return top > 0.f ? min(140 - (int)(__float_as_uint(top) >> 23), 126) : 0; }
@@ -274,7 +313,8 @@ struct AttendShape {
   static constexpr int kSums = (TR * D + 2 * TR) * 4;
   static constexpr int kWarp = kRing > kSums ? kRing : kSums;
   static constexpr int kSmem = kQ + kWarps * kWarp;
-  static_assert(kCtas * (kSmem + 2048) <= 228 * 1024, "shared memory of an SM");
+  static constexpr int kJoinedSmem = kSmem + kSums;          // with the CTA's own sums, which others read
+  static_assert(kCtas * (kJoinedSmem + 2048) <= 228 * 1024, "shared memory of an SM");
 };
 
 // Position of a group of four channels (dg) of row r in a warp's sums in
@@ -282,7 +322,8 @@ struct AttendShape {
 template <int D>
 __device__ __forceinline__ int swizzled(int r, int dg) { return dg ^ ((r >> 1 & 3) << (D == 128 ? 0 : 2)); }
 
-template <typename T, int D, int NT>
+// kJoined: a cluster of kAtCluster CTAs per sequence and head
+template <typename T, int D, int NT, bool kJoined>
 __global__ void __launch_bounds__(AttendShape<T, D, NT>::kThreads, AttendShape<T, D, NT>::kCtas) attend_kernel(const __grid_constant__ AttendParams p) {
   using S = AttendShape<T, D, NT>;
   constexpr int KW = D / 32, TR = S::TR, kWarpFloats = S::kWarp / 4, LANES = D / 8;
@@ -298,10 +339,17 @@ __global__ void __launch_bounds__(AttendShape<T, D, NT>::kThreads, AttendShape<T
   pdl_launch_dependents();
 
   fill_behind<T, D, kThreads>(p);
-  const Part line = find_part(p, TR, kAtUnit);
-  if (!line.some()) return;
+  Part line;
+  int b, rank = 0;
+  if constexpr (kJoined) {
+    rank = (int)cluster_rank();
+    b = blockIdx.x / kAtCluster / p.H;
+  } else {
+    line = find_part(p, TR, kAtUnit);
+    if (!line.some()) return;
+    b = line.b;
+  }
   long long u = line.u, base = line.base;
-  int b = line.b;
   const int me = blockIdx.x;
 
   const long long block_bytes = (long long)p.page * kTokenBytes<D>;
@@ -309,29 +357,36 @@ __global__ void __launch_bounds__(AttendShape<T, D, NT>::kThreads, AttendShape<T
   const uint32_t zero = (uint32_t)p.page >> 16;              // which the compiler does not know
   const uint32_t q_at = (uint32_t)__cvta_generic_to_shared(at_sm) + lane * 16;
   const uint32_t ring = (uint32_t)__cvta_generic_to_shared(all_sums + warp * kWarpFloats);
-  while (u < line.end) {
+  while (kJoined || u < line.end) {
     const Sequence s(p, b, TR, kAtUnit);
-    const long long n_units = s.units(p.H);
-    if (u >= base + n_units) {
-      base += n_units;
-      ++b;
-      continue;
+    Segment segment;
+    if constexpr (kJoined) {
+      if (s.rows == 0) return;
+      segment = Segment{(int)(blockIdx.x / kAtCluster) - b * p.H, 0, 0, 0, s.chunks, 0};
+    } else {
+      const long long n_units = s.units(p.H);
+      if (u >= base + n_units) {
+        base += n_units;
+        ++b;
+        continue;
+      }
+      segment = segment_at(s, u, base, line.end);
+      u += segment.step;
+      if (segment.chunks == 0) continue;
     }
-    const Segment segment(s, u, base, line.end);
     const int h = segment.h, rt = segment.rt, chunk0 = segment.chunk0, chunks = segment.chunks;
-    u += segment.step;
-    if (chunks == 0) continue;
 
-    // ---- this warp's groups of 32 tokens, number `first` + 8 n
+    // ---- this warp's groups of 32 tokens, number `first` + kStep n
+    constexpr int kStep = kJoined ? kAtCluster * kWarps : kWarps;
     const int sub_end = (s.seen + 15) / 16;
-    const int first = chunk0 * (kAtUnit / 32) + warp;
-    const int groups = max(0, (min((chunk0 + chunks) * (kAtUnit / 32), (sub_end + 1) / 2) - first + kWarps - 1) / kWarps);
+    const int first = chunk0 * (kAtUnit / 32) + rank * kWarps + warp;
+    const int groups = max(0, (min((chunk0 + chunks) * (kAtUnit / 32), (sub_end + 1) / 2) - first + kStep - 1) / kStep);
     // A lane knows where sub lane % 2 of group lane / 2 of the next 16 begins
     // in the cache, its number in the page in the low four bits; 0: hidden.
     // The 16 behind them are asked for ahead of time.
     int ask_id = -1, ask_sub = 0;
     auto ask = [&](int n) {
-      const int mine = 2 * (first + kWarps * (n + (lane >> 1))) + (lane & 1);
+      const int mine = 2 * (first + kStep * (n + (lane >> 1))) + (lane & 1);
       ask_id = -1;
       if (n + (lane >> 1) < groups && mine < sub_end) {
         const int x = mine / page_tiles;
@@ -629,7 +684,7 @@ __global__ void __launch_bounds__(AttendShape<T, D, NT>::kThreads, AttendShape<T
       __syncwarp();                       // every lane's copies are there, and everybody is done with the group before
       const uint32_t subs = there >> (2 * (n & 7)) & 3u;
       copy_group(n + kAtStages - 1);
-      const int token0 = 32 * (first + kWarps * n);
+      const int token0 = 32 * (first + kStep * n);
       if (subs == 3u && token0 + 32 <= s.first) group(std::false_type{}, token0, subs, from);
       else if (subs) group(std::true_type{}, token0, subs, from);
       from = from == ring + (kAtStages - 1) * Stage<D>::kBytes ? ring : from + Stage<D>::kBytes;
@@ -669,8 +724,8 @@ __global__ void __launch_bounds__(AttendShape<T, D, NT>::kThreads, AttendShape<T
       }
     }
     __syncthreads();
-    const bool whole = chunk0 == 0 && chunks == s.chunks;
-    float* part = p.part + (size_t)(2 * me + (chunk0 == 0)) * part_floats(TR, D);
+    const bool whole = !kJoined && chunk0 == 0 && chunks == s.chunks;
+    float* part = kJoined ? at_sm + S::kSmem / 4 : p.part + (size_t)(2 * me + (chunk0 == 0)) * part_floats(TR, D);
 #pragma unroll
     for (int x0 = 0; x0 < TR * (D / 4); x0 += kThreads) {
       const int x = x0 + tid;
@@ -707,9 +762,44 @@ __global__ void __launch_bounds__(AttendShape<T, D, NT>::kThreads, AttendShape<T
         finish_row<T, D>(p, q_row, dg, y, top, l);
       }
     }
-    __syncthreads();
-    if (!whole && chunk0 == 0 && tid == 0)
-      p.desc[me] = make_int4(b, h, rt, line.owner(segment.last(s, base)));
+    if constexpr (kJoined) {
+      // each CTA finishes an eighth of the channels' fours from all CTAs' sums
+      cluster_barrier();
+      constexpr int kMine = TR * (D / 4) / kAtCluster;
+      const uint32_t sums_at = (uint32_t)__cvta_generic_to_shared(part);
+      for (int x = rank * kMine + tid; x < (rank + 1) * kMine; x += kThreads) {
+        const int r = x / (D / 4), dg = x % (D / 4);
+        const long long q_row = out_rows[r];
+        if (q_row < 0) continue;
+        float m[kAtCluster], mass_k[kAtCluster], top = -FLT_MAX, l = 0.f;
+        float4 y_k[kAtCluster], y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < kAtCluster; ++k) {
+          const uint32_t there_at = cluster_address(sums_at, k);
+          m[k] = cluster_load(there_at + (TR * D + r) * 4);
+          mass_k[k] = cluster_load(there_at + (TR * D + TR + r) * 4);
+          y_k[k] = cluster_load4(there_at + x * 16);
+        }
+#pragma unroll
+        for (int k = 0; k < kAtCluster; ++k) top = m[k] > top || m[k] != m[k] ? m[k] : top;
+#pragma unroll
+        for (int k = 0; k < kAtCluster; ++k) {
+          const float f = ex2_approx(m[k] - top);
+          l = fmaf(f, mass_k[k], l);
+          y.x = fmaf(f, y_k[k].x, y.x);
+          y.y = fmaf(f, y_k[k].y, y.y);
+          y.z = fmaf(f, y_k[k].z, y.z);
+          y.w = fmaf(f, y_k[k].w, y.w);
+        }
+        finish_row<T, D>(p, q_row, dg, y, top, l);
+      }
+      cluster_barrier();                  // (the others have read this CTA's sums)
+      return;
+    } else {
+      __syncthreads();
+      if (!whole && chunk0 == 0 && tid == 0)
+        p.desc[me] = make_int4(b, h, rt, line.owner(segment.last(s, base)));
+    }
   }
 }
 

@@ -15,7 +15,18 @@ sv_status launch_attend(AttendParams p, void* workspace, cudaStream_t stream) {
   static std::atomic<bool> set[64];
   if constexpr (TR <= 24) {
     using Shape = AttendShape<T, D, TR / 8>;
-    auto kern = attend_kernel<T, D, TR / 8>;
+    if (attend_joined(p, TR)) {
+      auto joined = attend_kernel<T, D, TR / 8, true>;
+      static std::atomic<bool> set_joined[64];
+      if (!allow_smem(set_joined, (const void*)joined, Shape::kJoinedSmem)) return SV_ERR_CUDA;
+      cudaLaunchAttribute cluster[1];
+      cluster[0].id = cudaLaunchAttributeClusterDimension;
+      cluster[0].val.clusterDim.x = kAtCluster;
+      cluster[0].val.clusterDim.y = 1;
+      cluster[0].val.clusterDim.z = 1;
+      return launch(joined, dim3(p.B * p.H * kAtCluster), Shape::kThreads, Shape::kJoinedSmem, stream, p, cluster);
+    }
+    auto kern = attend_kernel<T, D, TR / 8, false>;
     if (!allow_smem(set, (const void*)kern, Shape::kSmem)) return SV_ERR_CUDA;
     kern<<<ctas, Shape::kThreads, Shape::kSmem, stream>>>(p);
   } else {

@@ -21,6 +21,22 @@ inline int attend_tile_rows(int rows) {
 }
 inline int attend_ctas(int TR) { return sm_count() * (TR == 8 ? 4 : TR == 16 ? 3 : 2); }
 
+// Whether a call of few rows is joined in one launch, by a cluster of eight CTAs
+// a segment: the table is short enough for eight, and all clusters are on the
+// GPU at once (with 3 or 2 CTAs an SM some SMs' places do not make up a cluster:
+// 57 segments of 16 rows would take two turns).  us with the workspace -> joined,
+// head size 128, tables and up to all of their tokens:
+//   segments, rows    1024          8192          16384
+//         8,  1        8.8 ->  5.2  21.0 ->  9.6  23.8 -> 14.2
+//        72,  1       11.7 ->  6.9  20.8 -> 15.7  30.0 -> 24.6
+//        48, 16       13.0 ->  8.9  20.8 -> 17.1  29.9 -> 28.3
+//        56, 16       13.5 -> 12.9  21.3 -> 21.7  31.1 -> 34.7
+//        24, 24       13.2 ->  9.3  19.4 -> 17.3  25.4 -> 26.8
+inline bool attend_joined(const AttendParams& p, int TR) {
+  const int places = TR == 8 ? attend_ctas(TR) : attend_ctas(TR) / 8 * 7;
+  return (long long)p.B * p.H * kAtCluster <= places && (long long)p.N * p.page <= kAtShort;
+}
+
 struct AttendLayout {
   size_t desc, part, total;
 };

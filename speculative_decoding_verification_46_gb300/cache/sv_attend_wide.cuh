@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(kWdThreads, 2) attend_wide_kernel(const __grid
       ++b;
       continue;
     }
-    const Segment segment(s, u, base, line.end);
+    const Segment segment = segment_at(s, u, base, line.end);
     const int h = segment.h, rt = segment.rt, chunk0 = segment.chunk0, chunks = segment.chunks;
     u += segment.step;
     if (chunks == 0) continue;

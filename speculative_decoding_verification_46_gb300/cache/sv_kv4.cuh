@@ -43,6 +43,15 @@ template <> struct Kv<__half> {
   }
 };
 
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ unsigned cluster_rank() {
+  unsigned r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+
 struct StoreParams {
   int R, rows, H, page;          // rows: gamma + 1
   long long slots_end;           // pages * page

@@ -11,7 +11,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include "../csrc/sv_device.cuh"
+#include "sv_kv4.cuh"
 
 namespace sv {
 namespace cache {
@@ -35,15 +35,6 @@ struct PlanParams {
 
 // Shared memory of the kernel: five integers a sequence.
 constexpr size_t plan_smem(int B) { return (size_t)B * 5 * sizeof(int); }
-
-__device__ __forceinline__ void cluster_barrier() {
-  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-}
-__device__ __forceinline__ unsigned cluster_rank() {
-  unsigned r;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
 
 // The sequence that flat index x belongs to: the last one whose sum of those
 // before it is at most x.

@@ -10,6 +10,7 @@ import numpy as np
 import pytest
 import torch
 
+import test_gpu_cache
 from oracle import cacheref
 from test_gpu_cache import DEV, DTYPES, _Cache, _check, _i32, _model_rows, _q, _State, sv  # noqa: F401
 
@@ -278,3 +279,73 @@ def test_append_neighbouring_slots(sv, D, heads, start):
             rows = x.double().cpu().numpy().reshape(B * G1, heads, D)
             want[start:start + B * G1] = cacheref.to_model(cacheref.held(rows, "bf16"), "bf16")
             assert np.array_equal(b.double().cpu().numpy(), want)
+
+
+# ------------------------------------------------------------------ few segments are joined in one launch, or with the workspace
+
+class _LongTables:
+    """The package, with tables too long for the join in one launch."""
+
+    def __init__(self, sv):
+        self.sv = sv
+
+    def __getattr__(self, name):
+        return getattr(self.sv, name)
+
+    def attend_kv4(self, q, cache, table, lengths, page, **kw):
+        more = 8192 // page + 1 - table.shape[1]
+        if more > 0:
+            table = torch.cat([table, table.new_full((len(table), more), -1)], 1)
+        return self.sv.attend_kv4(q, cache, table, lengths, page, **kw)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("gamma, group, D", [(0, 1, 64), (0, 8, 128), (6, 1, 128), (7, 2, 64), (3, 4, 128), (8, 1, 128), (2, 8, 128), (22, 1, 64)])
+def test_long_tables(sv, dtype, gamma, group, D):
+    far = _LongTables(sv)
+    test_gpu_cache.test_attend(far, dtype, gamma, 2, group, D, 16, [150, 0, 63, 1, 700, 129])
+    test_references_rise_along_the_sequence(far, dtype, gamma, group, D)
+    if group > 1 and D == 128:
+        test_rows_do_not_touch_each_other(far, dtype, gamma, group)
+
+
+def test_long_tables_in_other_calls(sv):
+    far = _LongTables(sv)
+    for page in (16, 48, 64, 256):
+        test_hidden_pages_far_into_a_sequence(far, page, 0, 4)
+    test_first_pages_hidden(far, 0, 2)
+    test_rows_of_very_different_sizes(far, 4)
+    test_gpu_cache.test_attend_nan_reaches_only_rows_that_see_it(far, 5, 2)
+    test_gpu_cache.test_attend_ragged(far, 3, 2, True)
+    test_gpu_cache.test_attend_ragged(far, 3, 2, False)
+    test_gpu_cache.test_attend_length_below_zero(far)
+    test_gpu_cache.test_attend_one_token_takes_all(far)
+    test_gpu_cache.test_attend_results_do_not_depend_on_the_run_or_workspace(far, 0, 4)
+    test_gpu_cache.test_two_captured_rounds_on_one_workspace(far)
+    for dtype in ("bf16", "f16"):
+        test_gpu_cache.test_attend_wide_range(far, dtype, 0)
+
+
+# (segments that fill the GPU once, and one sequence more)
+@pytest.mark.parametrize("B, heads, gamma, group", [(76, 1, 0, 2), (77, 1, 0, 2), (38, 2, 7, 1), (49, 1, 3, 4), (50, 1, 3, 4), (33, 1, 2, 8), (34, 1, 2, 8),
+                                                    (7, 7, 1, 7), (1, 33, 23, 1)])
+@pytest.mark.parametrize("page, width", [(16, 512), (16, 513), (256, 32), (48, 170)])
+def test_around_the_join_in_one_launch(sv, B, heads, gamma, group, page, width):
+    g = np.random.default_rng(B + page)
+    lengths = list(g.integers(0, 400, B))
+    lengths[0] = 1100
+    c = _Cache(sv, [n + gamma + 1 for n in lengths], heads, 64, page, "bf16", seed=B, width=width)
+    q = _q(B, gamma + 1, heads * group, 64, "bf16")
+    out, lse = sv.attend_kv4(q, c.cache, c.table, _i32(lengths), page, return_lse=True)
+    _check(out, lse, q, c, lengths, "bf16")
+
+
+def test_whole_table_in_one_launch(sv):
+    """8192 tokens in a table of 8192 positions, and lengths beyond it."""
+    n, page = 8191, 64
+    c = _Cache(sv, [n + 1], 2, 128, page, "bf16")
+    q = _q(1, 1, 8, 128, "bf16")
+    out, lse = sv.attend_kv4(q, c.cache, c.table, _i32([n]), page, return_lse=True)
+    _check(out, lse, q, c, [n], "bf16")
+    beyond, lse_beyond = sv.attend_kv4(q, c.cache, c.table, _i32([2 ** 31 - 1]), page, return_lse=True)
+    assert torch.equal(beyond, out) and torch.equal(lse_beyond, lse)
