@@ -13,7 +13,10 @@ namespace cache {
 inline size_t align_up(size_t x) { return (x + 255) & ~size_t(255); }
 
 // Rows of a tile: up to 24 go to attend_kernel; more to attend_wide_kernel, in
-// as few tiles as its 80 rows allow, of equal size.
+// as few tiles as its 80 rows allow, of equal size.  At 32 sequences of up to
+// 8192 tokens, 8 heads of 128, attend_kernel takes 74 us for 24 rows, and took
+// 100 for 32; attend_wide_kernel takes 85
+// us for 32, and for fewer, which it pads, no less.
 inline int attend_tile_rows(int rows) {
   if (rows <= 24) return (std::max(rows, 1) + 7) / 8 * 8;
   const int tiles = (rows + kWdMostRows - 1) / kWdMostRows;

@@ -15,16 +15,28 @@
 // complement, in the same AND and XOR), and their offset as o' + 15 s'.
 //
 // Eight warps do everything in turn, two CTAs per SM fill each other's waits.
-// A step: (1) key codes to tensor memory; barrier, first product; (2) value
-// codes to tensor memory meanwhile; (3) the scores' softmax against a
-// reference per row, weights to shared memory; barrier, second product, which
-// the next step's (1) does not wait for.  Where a term outgrows its row's
-// reference by 2^8 (a segment's first step, hardly ever later) the barrier
-// says so to all, and the step's weights are formed again.
+// In a step (1) the step's value codes go to tensor memory; (2) the scores, whose
+// product was issued a step ahead, become weights in shared memory against a
+// reference per row; (3) the next step's key codes follow, then the one barrier,
+// behind which one warp issues the next scores' product and another the sums'.
+// Where a term outgrows its row's reference by 2^8 (a segment's first step,
+// hardly ever later) the barrier says so to all, and the step's weights are
+// formed again; a warp whose terms have not has formed its masses for good.
 //
 // Tensor memory, 256 columns a CTA: key codes, value codes, scores, sums.  With
-// R = 80 and D = 128 the value codes take the place of the scores: then (2)
-// follows (3)'s reading of them, at whose barrier the references are settled.
+// R = 80 and D = 128 the value codes take the place of the scores: then (1)
+// follows (2)'s reading of them, at a barrier more, where the references are
+// settled before the weights.  (For fewer rows settling first takes longer: 99,
+// 112 and 123 us where 87, 100 and 114 at 32, 40 and 56 rows.)
+//
+// What bounds it: instructions, not bytes.  32 sequences of up to 8192 tokens, 8
+// heads of 128 (32 us of bytes) take 85, 98, 113 and 139 us at 32, 40, 56 and 72
+// rows; the schedulers issue in 56 and 52 % of the cycles at 40 and 72, with two
+// warps each, which wait for one another at the barrier.  A product of N <= 80
+// columns takes its issuing warp about 42 cycles, whatever N.  What was slower:
+// copies in bulk (a warp's lanes issue one in 75 cycles: 138 us where 116 at 32
+// rows), a ninth warp for the products (96 registers a thread: 255 us where 222
+// at 72 rows), a fourth step in the ring (97.5 us where 96.2 at 40 rows).
 #pragma once
 
 #include "sv_attend.cuh"

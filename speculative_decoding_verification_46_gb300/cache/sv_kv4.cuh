@@ -6,6 +6,11 @@
 // neighbouring rows of a head, so that a lane has four loads of 16 bytes on
 // the way and, where the rows' slots are neighbours too, writes the two
 // tokens' interleaved value codes as whole words.
+//
+// 8 x 4096 rows of 8 heads of 128, bf16, stored and read back: 59.6 us, 340 MB at
+// 5.7 TB/s (85 % of a copy's rate); stored with a word for every two channels
+// instead, 61.5; with a row at a time, one division and one reciprocal in every
+// lane and float32 sums of codes, 90.
 #pragma once
 
 #include <cuda_bf16.h>
