@@ -27,13 +27,13 @@ namespace cache {
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanCtas = 8;        // of a cluster with many rows
 // Rows whose slots the first kernel forms; those of more are a kernel of their
-// own.  (1024 sequences of 9 rows, two rounds: 15.6 us in one kernel of eight
-// CTAs, 12.1 with the second one; 1 of 5 rows 5.8 us in one kernel, and another
-// launch costs 2 us a round.)
-constexpr int kPlanFew = 4096;
-// Rows whose pages are moved by more CTAs than one.  (64 prompts of 4096 tokens,
-// two rounds: 12.5 us; a cluster that formed their slots too took 44.6.)
-constexpr int kPlanMany = 65536;
+// own.  (Two rounds, one kernel against two: 8.1 and 9.3 us for 64 sequences of 9
+// rows, 8.6 and 9.0 for one of 2048, 11.2 and 9.9 for 256 of 9, 19 and 12 for 1024.)
+constexpr int kPlanFew = 2048;
+// Rows whose pages are moved by more CTAs than one.  (Two rounds, one CTA against
+// eight: 11.6 and 12.3 us for 1024 sequences of 9 rows, 9.1 and 10.1 for 4 prompts
+// of 4096, 12.5 and 10.3 for 16, 27.6 and 12.7 for 64.)
+constexpr int kPlanMany = 32768;
 constexpr int kPlanSlotThreads = 256;
 constexpr int kNoPages = 1, kTooLong = 2;
 

@@ -218,7 +218,7 @@ def test_plan_on_another_stream_and_in_inference_mode(sv):
     sv.plan_round(state[0], 2, 16, *state[1:])               # tensors without a version, outside
 
 
-@pytest.mark.parametrize("rows", [4096, 4097, 65536, 65537, 70001])
+@pytest.mark.parametrize("rows", [2048, 2049, 4096, 4097, 32768, 32769, 65536, 65537, 70001])
 def test_plan_around_its_forms(sv, rows):
     """Row counts around those at which the slots become a kernel of their own and the pages are moved by a cluster."""
     for B in (1, 3):
