@@ -135,6 +135,8 @@ def _page_of(cache, page, D, heads, device):
         raise ValueError(f"head size must be 64 or 128, got {D}")
     if cache.shape[2] != page * (D + 8):
         raise ValueError(f"a block of {page} tokens with {D} channels has {page * (D + 8)} bytes, cache's {cache.shape[2]}")
+    if cache.shape[1] < 1:
+        raise ValueError("cache has no heads")
     if heads is not None and cache.shape[1] != heads:
         raise ValueError(f"cache has {cache.shape[1]} heads, the rows {heads}")
     return cache.shape[0]
@@ -216,7 +218,7 @@ def append_kv4(k, v, slots, cache, *, stream=None):
     _need("slots", slots, _i32, (B, G1), dev)
     if D not in (64, 128):
         raise ValueError(f"head size must be 64 or 128, got {D}")
-    page = cache.shape[-1] // (D + 8)
+    page = cache.shape[-1] // (D + 8) if cache.dim() else 0
     pages = _page_of(cache, page, D, heads, dev)
     if G1 < 1:
         raise ValueError("k has no rows: [B, gamma+1, heads, D] with gamma >= 0")

@@ -349,3 +349,22 @@ def test_whole_table_in_one_launch(sv):
     _check(out, lse, q, c, [n], "bf16")
     beyond, lse_beyond = sv.attend_kv4(q, c.cache, c.table, _i32([2 ** 31 - 1]), page, return_lse=True)
     assert torch.equal(beyond, out) and torch.equal(lse_beyond, lse)
+
+
+def test_caches_that_are_none(sv):
+    q = _q(1, 1, 2, 64, "bf16")
+    i = _i32([[0]])
+    for cache in (torch.zeros(2, 0, 16 * 72, dtype=torch.uint8, device=DEV), torch.zeros((), dtype=torch.uint8, device=DEV)):
+        with pytest.raises(ValueError):
+            sv.append_kv4(q, q, i, cache)
+        with pytest.raises(ValueError):
+            sv.read_kv4(cache, i, 16, torch.bfloat16)
+        with pytest.raises(ValueError):
+            sv.attend_kv4(q, cache, i, _i32([0]), 16)
+    # one without pages holds nothing
+    none = sv.alloc_kv4_cache(0, 2, 64, 16, DEV)
+    sv.append_kv4(q, q, i, none)
+    k, v = sv.read_kv4(none, i, 16, torch.bfloat16)
+    assert not k.any() and not v.any()
+    out, lse = sv.attend_kv4(q, none, i, _i32([5]), 16, return_lse=True)
+    assert not out.any() and (lse == -float("inf")).all()
