@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kWdThreads, 2) attend_wide_kernel(const __grid
   __shared__ __align__(8) unsigned long long bars[2];
   __shared__ unsigned long long places[2][32];
   __shared__ uint32_t place_subs[4];
-  __shared__ int gave_up_flag;
+  __shared__ int gave_up_flag, settled_flag;
   __shared__ float warp_top[8];
   const int tid = threadIdx.x, lane = tid & 31, g = lane >> 2, c = lane & 3;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0), w = warp & 3, wg = warp >> 2;   // (the compiler sees that a warp shares it)
@@ -192,6 +192,7 @@ __global__ void __launch_bounds__(kWdThreads, 2) attend_wide_kernel(const __grid
   int* const limits = reinterpret_cast<int*>(row_scales + R);
   long long* const out_rows = reinterpret_cast<long long*>(limits + R);
   volatile int* const gave_up = &gave_up_flag;
+  volatile int* const settled = &settled_flag;   // the segment's rows have their references
   // scores there, sums there
   const uint32_t bar_s = (uint32_t)__cvta_generic_to_shared(&bars[0]), bar_o = bar_s + 8;
   pdl_launch_dependents();
@@ -351,6 +352,7 @@ __global__ void __launch_bounds__(kWdThreads, 2) attend_wide_kernel(const __grid
       copies_end_group();
     };
 
+    if (S::kTight && tid == 0) *settled = 0;
     // ---- q: float16 with a power of two per row, channels in the order in
     // which the key codes come: element 2 (c + 4 (4 k + i)) + e is channel 8 (KW
     // c + k) + i + 4 e, halves e of pair i of word k
@@ -410,11 +412,16 @@ __global__ void __launch_bounds__(kWdThreads, 2) attend_wide_kernel(const __grid
     for (int k = 0; k < NG; ++k) mass[k] = shift[k] = two(0.f, 0.f);
     float4* const my_pairs = pairs + wg * (RH / 2) + c;      // (+ 4 k)
     float value_scale = 0x1p126f;
+    // No step so far had a sub that is there.  (With R = 80 and D = 128, where
+    // registers are short, in shared memory: 141 us for 72 rows, and 149; for fewer
+    // rows that takes longer, 87, 101 and 117 us where 85, 98 and 114.)
+    bool none = true;
 
     for (int n = 0; n < chunks; ++n) {
       const uint32_t stage = sm + S::oRing + slot * S::kStage;
       const uint32_t subs = place_subs[n >> 2 & 3] >> ((n & 3) * 8) & 0xffu;
       const int slot_next = slot + 1 == S::kStages ? 0 : slot + 1;
+      const bool fresh = S::kTight ? n == 0 || *settled == 0 : none;
       if (!S::kTight && n > 0) {
         wait_phase(bar_o, phase_o, gave_up);
         phase_o ^= 1;
@@ -450,6 +457,7 @@ __global__ void __launch_bounds__(kWdThreads, 2) attend_wide_kernel(const __grid
       const uint32_t numbers_at = stage + S::oNumbers + 2 * (g >> 1) * S::kSubNumbers + (4 * w + (g & 1)) * 8;
       auto softmax = [&](auto masked_step) {
         constexpr bool kMasked = decltype(masked_step)::value;
+        const bool unsettled = (kMasked || !S::kTight) && fresh;
         // whether rows 8 k + 2 c and + 1 see token (bl, e)
         auto sees = [&](int k, int bl, int e) {
           const int2 lim = *reinterpret_cast<const int2*>(limits + wg * RH + 8 * k + 2 * c);
@@ -575,7 +583,7 @@ __global__ void __launch_bounds__(kWdThreads, 2) attend_wide_kernel(const __grid
         bool again = true, outgrown = true;
         if (n > 0 || S::kTight) {
           const float most = exponents();
-          outgrown = n == 0 || __any_sync(0xffffffffu, most > kAtSlack || largest * value_scale > kAtValueTop);
+          outgrown = unsettled || __any_sync(0xffffffffu, most > kAtSlack || largest * value_scale > kAtValueTop);
           if (!S::kTight) {
             if (!outgrown) weights(true);
             if (n + 1 < chunks) keys(slot_next);
@@ -584,8 +592,10 @@ __global__ void __launch_bounds__(kWdThreads, 2) attend_wide_kernel(const __grid
         }
         if (again) {
           // rows' references and the values' scale move; so do the sums.  The
-          // first step sets the references (they were 0): a row that sees none
-          // of it sees none of the later ones, its mass stays 0.
+          // first step with a sub that is there sets the references (they were
+          // 0): a row that sees none of it sees none of the later ones, its mass
+          // stays 0.
+          if (S::kTight && unsettled && subs != 0 && tid == 0) *settled = 1;
           if (!S::kTight) exponents();
 #pragma unroll
           for (int k = 0; k < NG; ++k) {
@@ -614,7 +624,7 @@ __global__ void __launch_bounds__(kWdThreads, 2) attend_wide_kernel(const __grid
           }
           // a row's terms move down by `up`
           auto rise = [&](float t) {
-            return n > 0 ? fmaxf(t, 0.f) : t == __int_as_float(0xff800000) ? 0.f : t;
+            return !unsettled ? fmaxf(t, 0.f) : t == __int_as_float(0xff800000) ? 0.f : t;
           };
 #pragma unroll
           for (int k = 0; k < NG; ++k) {
@@ -627,7 +637,7 @@ __global__ void __launch_bounds__(kWdThreads, 2) attend_wide_kernel(const __grid
             }
             up0 = rise(up0);
             up1 = rise(up1);
-            const float f0 = n > 0 ? ex2_approx(-up0) : 0.f, f1 = n > 0 ? ex2_approx(-up1) : 0.f;
+            const float f0 = !unsettled ? ex2_approx(-up0) : 0.f, f1 = !unsettled ? ex2_approx(-up1) : 0.f;
             mass[k] = mul2(mass[k], two(f0, f1));
             shift[k] = mul2(shift[k], two(f0, f1));
 #pragma unroll
@@ -696,8 +706,9 @@ __global__ void __launch_bounds__(kWdThreads, 2) attend_wide_kernel(const __grid
           if ((n & 3) == 2) tell((n >> 2) + 2, place_of(asked, asked_sub));
         }
       };
-      if (subs != 0xffu || (chunk0 + n) * kWdUnit + kWdUnit > s.first) softmax(std::true_type{});
+      if ((S::kTight && fresh) || subs != 0xffu || (chunk0 + n) * kWdUnit + kWdUnit > s.first) softmax(std::true_type{});
       else softmax(std::false_type{});
+      none = none && subs == 0;
       slot = slot_next;
     }
 

@@ -283,6 +283,9 @@ def test_append_neighbouring_slots(sv, D, heads, start):
 
 # ------------------------------------------------------------------ few segments are joined in one launch, or with the workspace
 
+_SHORT = 16640     # positions of a table up to which calls are joined in one launch
+
+
 class _LongTables:
     """The package, with tables too long for the join in one launch."""
 
@@ -293,14 +296,22 @@ class _LongTables:
         return getattr(self.sv, name)
 
     def attend_kv4(self, q, cache, table, lengths, page, **kw):
-        more = 8192 // page + 1 - table.shape[1]
+        more = _SHORT // page + 1 - table.shape[1]
         if more > 0:
             table = torch.cat([table, table.new_full((len(table), more), -1)], 1)
         return self.sv.attend_kv4(q, cache, table, lengths, page, **kw)
 
 
+@pytest.mark.parametrize("dtype, D", [("bf16", 128), ("f16", 128), ("bf16", 64), ("f16", 64)])
+@pytest.mark.parametrize("gamma, group", [(6, 1), (7, 1), (8, 1), (15, 1), (16, 1), (23, 1), (24, 1), (7, 4), (32, 1), (5, 8), (48, 1), (12, 4),
+                                          (63, 1), (64, 1), (9, 8), (26, 3), (39, 4), (40, 4), (64, 5)])
+def test_every_tile_of_rows_with_long_tables(sv, dtype, D, gamma, group):
+    test_every_tile_of_rows(_LongTables(sv), dtype, D, gamma, group)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
-@pytest.mark.parametrize("gamma, group, D", [(0, 1, 64), (0, 8, 128), (6, 1, 128), (7, 2, 64), (3, 4, 128), (8, 1, 128), (2, 8, 128), (22, 1, 64)])
+@pytest.mark.parametrize("gamma, group, D", [(0, 1, 64), (0, 8, 128), (6, 1, 128), (7, 2, 64), (3, 4, 128), (8, 1, 128), (2, 8, 128), (22, 1, 64),
+                                             (4, 8, 128), (6, 8, 128), (8, 8, 128), (8, 8, 64), (16, 3, 128)])
 def test_long_tables(sv, dtype, gamma, group, D):
     far = _LongTables(sv)
     test_gpu_cache.test_attend(far, dtype, gamma, 2, group, D, 16, [150, 0, 63, 1, 700, 129])
@@ -313,23 +324,31 @@ def test_long_tables_in_other_calls(sv):
     far = _LongTables(sv)
     for page in (16, 48, 64, 256):
         test_hidden_pages_far_into_a_sequence(far, page, 0, 4)
-    test_first_pages_hidden(far, 0, 2)
-    test_rows_of_very_different_sizes(far, 4)
-    test_gpu_cache.test_attend_nan_reaches_only_rows_that_see_it(far, 5, 2)
-    test_gpu_cache.test_attend_ragged(far, 3, 2, True)
-    test_gpu_cache.test_attend_ragged(far, 3, 2, False)
+        test_hidden_pages_far_into_a_sequence(far, page, 4, 8)
+    for gamma, group in ((0, 2), (5, 8)):
+        test_first_pages_hidden(far, gamma, group)
+    for group in (4, 40):
+        test_rows_of_very_different_sizes(far, group)
+    for group in (2, 8):
+        test_gpu_cache.test_attend_nan_reaches_only_rows_that_see_it(far, 5, group)
+    for gamma, group in ((3, 2), (8, 8)):
+        test_gpu_cache.test_attend_ragged(far, gamma, group, True)
+        test_gpu_cache.test_attend_ragged(far, gamma, group, False)
     test_gpu_cache.test_attend_length_below_zero(far)
     test_gpu_cache.test_attend_one_token_takes_all(far)
-    test_gpu_cache.test_attend_results_do_not_depend_on_the_run_or_workspace(far, 0, 4)
+    for gamma, group in ((0, 4), (8, 8)):
+        test_gpu_cache.test_attend_results_do_not_depend_on_the_run_or_workspace(far, gamma, group)
     test_gpu_cache.test_two_captured_rounds_on_one_workspace(far)
+    test_gpu_cache.test_attend_strided_queries(far)
     for dtype in ("bf16", "f16"):
-        test_gpu_cache.test_attend_wide_range(far, dtype, 0)
+        for gamma in (0, 8):
+            test_gpu_cache.test_attend_wide_range(far, dtype, gamma)
 
 
 # (segments that fill the GPU once, and one sequence more)
 @pytest.mark.parametrize("B, heads, gamma, group", [(76, 1, 0, 2), (77, 1, 0, 2), (38, 2, 7, 1), (49, 1, 3, 4), (50, 1, 3, 4), (33, 1, 2, 8), (34, 1, 2, 8),
-                                                    (7, 7, 1, 7), (1, 33, 23, 1)])
-@pytest.mark.parametrize("page, width", [(16, 512), (16, 513), (256, 32), (48, 170)])
+                                                    (7, 7, 1, 7), (1, 33, 23, 1), (11, 1, 8, 8), (12, 1, 8, 8), (24, 1, 3, 8), (25, 1, 3, 8), (1, 3, 64, 4)])
+@pytest.mark.parametrize("page, width", [(16, 1040), (16, 1041), (256, 65), (48, 346), (48, 347)])
 def test_around_the_join_in_one_launch(sv, B, heads, gamma, group, page, width):
     g = np.random.default_rng(B + page)
     lengths = list(g.integers(0, 400, B))
@@ -341,14 +360,55 @@ def test_around_the_join_in_one_launch(sv, B, heads, gamma, group, page, width):
 
 
 def test_whole_table_in_one_launch(sv):
-    """8192 tokens in a table of 8192 positions, and lengths beyond it."""
-    n, page = 8191, 64
+    """As many tokens as a table of 16640 positions has, and lengths beyond it."""
+    n, page = _SHORT - 1, 64
     c = _Cache(sv, [n + 1], 2, 128, page, "bf16")
     q = _q(1, 1, 8, 128, "bf16")
     out, lse = sv.attend_kv4(q, c.cache, c.table, _i32([n]), page, return_lse=True)
     _check(out, lse, q, c, [n], "bf16")
     beyond, lse_beyond = sv.attend_kv4(q, c.cache, c.table, _i32([2 ** 31 - 1]), page, return_lse=True)
     assert torch.equal(beyond, out) and torch.equal(lse_beyond, lse)
+
+
+@pytest.mark.parametrize("gamma, group, D, dtype", [(8, 8, 128, "bf16"), (15, 5, 64, "f16"), (4, 8, 128, "f16"), (6, 5, 128, "bf16")])
+def test_ragged_tiles_in_one_launch(sv, gamma, group, D, dtype):
+    """Sequences with fewer row tiles than others, down to none."""
+    for gamma_b in ([gamma, -1], [0, gamma], [1, 2], [-1, -1], [gamma // 2, -9]):
+        rows = np.clip(gamma_b, -1, gamma) + 1
+        lengths = [333, 70]
+        c = _Cache(sv, [n + max(int(r), 1) for n, r in zip(lengths, rows)], 2, D, 16, dtype)
+        q = _q(2, gamma + 1, 2 * group, D, dtype)
+        behind = torch.as_tensor(np.arange(gamma + 1) >= rows[:, None], device=DEV)
+        for out in (None, torch.full_like(q, 3.0)):
+            got, lse = sv.attend_kv4(q, c.cache, c.table, _i32(lengths), 16, gamma_b=_i32(gamma_b), out=out, return_lse=True)
+            assert (got[behind] == (0.0 if out is None else 3.0)).all() and (lse[behind] == 0).all()
+            _check(torch.where(behind[..., None, None], 0.0, got), lse, q, c, lengths, dtype, gamma_b=gamma_b)
+
+
+@pytest.mark.parametrize("far", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("gamma, group, D", [(0, 2, 128), (3, 4, 128), (2, 8, 64), (3, 11, 128), (8, 8, 128), (8, 8, 64), (40, 4, 128)])
+def test_small_terms_behind_hidden_pages(sv, far, dtype, gamma, group, D):
+    """Scores far below 0 in the first tokens that are there, 0 to 3 steps in;
+    rows of which some see one token, some none.  With long tables there are so
+    many segments that a CTA has several steps of one."""
+    page, S, B, heads = (32, _LongTables(sv), 24, 16) if far else (32, sv, 2, 2)
+    for skip in (4, 8, 13):                                # (a step is 128 tokens)
+        lengths = [skip * page - 1 - gamma // 2, skip * page + 70] * (B // 2)
+        c = _Cache(sv, [n + gamma + 1 for n in lengths], heads, D, page, dtype, seed=skip)
+        q = _q(B, gamma + 1, heads * group, D, dtype, size=0.05) + 1.0
+        for b, n in enumerate(lengths):
+            t = n + gamma + 1
+            k = (torch.as_tensor(c.k[b], device=DEV)[None] * 0.05 - 32.0 / D ** 0.5).to(DTYPES[dtype])
+            v = torch.as_tensor(c.v[b], device=DEV)[None].to(DTYPES[dtype])
+            p = np.arange(t)
+            sv.append_kv4(k.contiguous(), v.contiguous(), _i32((c.table[b].cpu().numpy()[p // page] * page + p % page)[None]), c.cache)
+            c.k[b], c.v[b] = (cacheref.held(x[0].double().cpu().numpy(), dtype) for x in (k, v))
+        table = c.table.clone()
+        table[:, :skip] = -1
+        hidden = [np.arange(n + gamma + 1) < skip * page for n in lengths]
+        out, lse = S.attend_kv4(q, c.cache, table, _i32(lengths), page, return_lse=True)
+        _check(out, lse, q, c, lengths, dtype, hidden=hidden)
 
 
 def test_caches_that_are_none(sv):
