@@ -30,7 +30,9 @@
 // Few segments, which are (sequence, head, row tile)s, over a short table: a
 // cluster of eight CTAs a segment deals its 32-token groups out to its warps, and
 // the CTAs read each other's sums from shared memory.  One launch: one request of
-// 700 tokens, 8 x 4 heads of 128, takes 4.5 us, and 9.0 us the other way.
+// 700 tokens, 8 x 4 heads of 128, takes 4.5 us, and 9.0 us the other way; a round of
+// gamma 8 on 8 x 8 heads and up to 4096 tokens 14 us, and 25.5 in the kernel for
+// many rows.
 // Otherwise: the segments' tokens in units of 128 are one line of units; CTA i of
 // W takes an equal part of it, finds its place from lengths and walks on.  A
 // segment that a CTA does not hold in full goes to the workspace;
@@ -61,7 +63,7 @@ constexpr int kAtStart = 3;               // units that stand for a segment's st
 constexpr int kAtStages = 2;              // groups of 32 tokens in a warp's ring
 constexpr int kAtJoinThreads = 256;
 constexpr int kAtCluster = 8;             // CTAs of a segment that is joined in one launch,
-constexpr int kAtShort = 8192;            // which it may be up to this many positions of a table
+constexpr int kAtShort = 16640;           // which it may be up to this many positions of a table (16384 and a page)
 constexpr float kAtSlack = 8.f;           // a row's reference may be 2^8 below its largest term
 constexpr float kAtValueTop = 128.f;      // largest s' 2^x: p s' 2^x stays below 2^(7 + 8), float16 ends at 65504
 
@@ -322,7 +324,7 @@ struct AttendShape {
 template <int D>
 __device__ __forceinline__ int swizzled(int r, int dg) { return dg ^ ((r >> 1 & 3) << (D == 128 ? 0 : 2)); }
 
-// kJoined: a cluster of kAtCluster CTAs per sequence and head
+// kJoined: a cluster of kAtCluster CTAs per sequence, head and row tile
 template <typename T, int D, int NT, bool kJoined>
 __global__ void __launch_bounds__(AttendShape<T, D, NT>::kThreads, AttendShape<T, D, NT>::kCtas) attend_kernel(const __grid_constant__ AttendParams p) {
   using S = AttendShape<T, D, NT>;
@@ -340,10 +342,13 @@ __global__ void __launch_bounds__(AttendShape<T, D, NT>::kThreads, AttendShape<T
 
   fill_behind<T, D, kThreads>(p);
   Part line;
-  int b, rank = 0;
+  int b, rank = 0, head = 0, tile = 0;
   if constexpr (kJoined) {
     rank = (int)cluster_rank();
-    b = blockIdx.x / kAtCluster / p.H;
+    const int x = blockIdx.x / kAtCluster, tiles = (p.rows * p.G + TR - 1) / TR;
+    tile = x % tiles;
+    head = x / tiles % p.H;
+    b = x / tiles / p.H;
   } else {
     line = find_part(p, TR, kAtUnit);
     if (!line.some()) return;
@@ -361,8 +366,8 @@ __global__ void __launch_bounds__(AttendShape<T, D, NT>::kThreads, AttendShape<T
     const Sequence s(p, b, TR, kAtUnit);
     Segment segment;
     if constexpr (kJoined) {
-      if (s.rows == 0) return;
-      segment = Segment{(int)(blockIdx.x / kAtCluster) - b * p.H, 0, 0, 0, s.chunks, 0};
+      if (tile >= s.tiles) return;
+      segment = Segment{head, tile, 0, 0, s.chunks, 0};
     } else {
       const long long n_units = s.units(p.H);
       if (u >= base + n_units) {

@@ -15,17 +15,6 @@ sv_status launch_attend(AttendParams p, void* workspace, cudaStream_t stream) {
   static std::atomic<bool> set[64];
   if constexpr (TR <= 24) {
     using Shape = AttendShape<T, D, TR / 8>;
-    if (attend_joined(p, TR)) {
-      auto joined = attend_kernel<T, D, TR / 8, true>;
-      static std::atomic<bool> set_joined[64];
-      if (!allow_smem(set_joined, (const void*)joined, Shape::kJoinedSmem)) return SV_ERR_CUDA;
-      cudaLaunchAttribute cluster[1];
-      cluster[0].id = cudaLaunchAttributeClusterDimension;
-      cluster[0].val.clusterDim.x = kAtCluster;
-      cluster[0].val.clusterDim.y = 1;
-      cluster[0].val.clusterDim.z = 1;
-      return launch(joined, dim3(p.B * p.H * kAtCluster), Shape::kThreads, Shape::kJoinedSmem, stream, p, cluster);
-    }
     auto kern = attend_kernel<T, D, TR / 8, false>;
     if (!allow_smem(set, (const void*)kern, Shape::kSmem)) return SV_ERR_CUDA;
     kern<<<ctas, Shape::kThreads, Shape::kSmem, stream>>>(p);
@@ -52,8 +41,28 @@ sv_status launch_attend(AttendParams p, void* workspace, cudaStream_t stream) {
   return launched();
 }
 
+template <typename T, int D, int TR>
+sv_status launch_joined(const AttendParams& p, int segments, cudaStream_t stream) {
+  using Shape = AttendShape<T, D, TR / 8>;
+  auto kern = attend_kernel<T, D, TR / 8, true>;
+  static std::atomic<bool> set[64];
+  if (!allow_smem(set, (const void*)kern, Shape::kJoinedSmem)) return SV_ERR_CUDA;
+  cudaLaunchAttribute cluster[1];
+  cluster[0].id = cudaLaunchAttributeClusterDimension;
+  cluster[0].val.clusterDim.x = kAtCluster;
+  cluster[0].val.clusterDim.y = 1;
+  cluster[0].val.clusterDim.z = 1;
+  return launch(kern, dim3(segments * kAtCluster), Shape::kThreads, Shape::kJoinedSmem, stream, p, cluster);
+}
+
 template <typename T, int D>
 sv_status launch_attend_rows(const AttendParams& p, void* workspace, cudaStream_t stream) {
+  const AttendJoined joined = attend_joined(p);
+  if (joined.segments > 0) switch (joined.rows) {
+      case 8: return launch_joined<T, D, 8>(p, joined.segments, stream);
+      case 16: return launch_joined<T, D, 16>(p, joined.segments, stream);
+      default: return launch_joined<T, D, 24>(p, joined.segments, stream);
+    }
   switch (attend_tile_rows(p.rows * p.G)) {
     case 8: return launch_attend<T, D, 8>(p, workspace, stream);
     case 16: return launch_attend<T, D, 16>(p, workspace, stream);

@@ -12,7 +12,7 @@ namespace cache {
 
 inline size_t align_up(size_t x) { return (x + 255) & ~size_t(255); }
 
-// Rows of a tile: up to 24 go to attend_kernel; more to attend_wide_kernel, in
+// Rows of a tile where the call is not joined in one launch: up to 24 go to attend_kernel; more to attend_wide_kernel, in
 // as few tiles as its 80 rows allow, of equal size.  At 32 sequences of up to
 // 8192 tokens, 8 heads of 128, attend_kernel takes 74 us for 24 rows, and took
 // 100 for 32; attend_wide_kernel takes 85
@@ -24,20 +24,32 @@ inline int attend_tile_rows(int rows) {
 }
 inline int attend_ctas(int TR) { return sm_count() * (TR == 8 ? 4 : TR == 16 ? 3 : 2); }
 
-// Whether a call of few rows is joined in one launch, by a cluster of eight CTAs
-// a segment: the table is short enough for eight, and all clusters are on the
-// GPU at once (with 3 or 2 CTAs an SM some SMs' places do not make up a cluster:
-// 57 segments of 16 rows would take two turns).  us with the workspace -> joined,
-// head size 128, tables and up to all of their tokens:
-//   segments, rows    1024          8192          16384
-//         8,  1        8.8 ->  5.2  21.0 ->  9.6  23.8 -> 14.2
-//        72,  1       11.7 ->  6.9  20.8 -> 15.7  30.0 -> 24.6
-//        48, 16       13.0 ->  8.9  20.8 -> 17.1  29.9 -> 28.3
-//        56, 16       13.5 -> 12.9  21.3 -> 21.7  31.1 -> 34.7
-//        24, 24       13.2 ->  9.3  19.4 -> 17.3  25.4 -> 26.8
-inline bool attend_joined(const AttendParams& p, int TR) {
+// Whether a call is joined in one launch, by a cluster of eight CTAs a segment
+// (tiles of 8, 16 or 24 rows, as few as there can be, of equal size): the table
+// is short enough for eight, and all clusters are on the GPU at once (with 3 or 2
+// CTAs an SM some SMs' places do not make up a cluster: 57 segments of 16 rows
+// would take two turns).  Rows beyond 24 read the cache once a tile, from L2 for
+// the most part.  us with the workspace -> joined, 8 heads of 128 (2 in the last
+// line), tables and up to all of their tokens:
+//   sequences, rows   1024          8192          12200         16384
+//        1,   1        8.8 ->  5.2  20.8 ->  9.8  24.5 -> 11.4  24.9 -> 14.4
+//        9,   1       11.7 ->  6.9  20.7 -> 15.8  26.7 -> 22.1  29.9 -> 24.7
+//        6,  16       13.0 ->  8.9  20.9 -> 17.3  26.5 -> 24.7  29.9 -> 28.6
+//        7,  16       13.5 -> 12.9  21.3 -> 21.7                31.1 -> 34.7
+//        3,  24       13.2 ->  9.3  19.4 -> 17.6  23.8 -> 22.4  25.4 -> 26.9
+//        2,  40       14.8 ->  9.4  24.5 -> 18.5  27.3 -> 23.1  30.2 -> 29.3
+//        1,  72       17.1 ->  9.8  29.8 -> 19.3  32.6 -> 24.0  35.5 -> 30.0
+//        1, 256       15.0 ->  9.6  27.5 -> 19.2  29.9 -> 23.8  32.0 -> 30.1
+struct AttendJoined {
+  int rows, segments;                     // of a tile; 0 segments: not joined
+};
+inline AttendJoined attend_joined(const AttendParams& p) {
+  const int rows = p.rows * p.G, tiles = (rows + 23) / 24;
+  const int TR = ((rows + tiles - 1) / tiles + 7) / 8 * 8;
   const int places = TR == 8 ? attend_ctas(TR) : attend_ctas(TR) / 8 * 7;
-  return (long long)p.B * p.H * kAtCluster <= places && (long long)p.N * p.page <= kAtShort;
+  const long long segments = (long long)p.B * p.H * tiles;
+  const bool few = segments * kAtCluster <= places && (long long)p.N * p.page <= kAtShort;
+  return AttendJoined{TR, few ? (int)segments : 0};
 }
 
 struct AttendLayout {
