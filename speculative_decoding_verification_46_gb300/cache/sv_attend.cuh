@@ -11,7 +11,9 @@
 // are), so a word of eight codes becomes four operand registers with one shift
 // and four ANDs.  The factor 16 of every second register is taken out of q, or
 // out of the sums at the end.  q is brought to float16 with a power of two per
-// row, p_t s'_t with one per warp; the sums are float32.
+// row, p_t s'_t with one per warp; the sums are float32.  (The warp's power of two
+// brings the largest s' so far to [2^6, 2^7): what float16's last bit, 2^-24, cuts
+// off a weight is below 2^-25 15 s' / 2^6, about 2^-30 of the largest value.)
 //
 // A tensor core cuts off what lies below its sum's last bits, so sums of codes
 // n >= 0 would lose more and more over a long sequence: every second group of

@@ -30,7 +30,7 @@
 // 112 and 123 us where 87, 100 and 114 at 32, 40 and 56 rows.)
 //
 // What bounds it: instructions, not bytes.  32 sequences of up to 8192 tokens, 8
-// heads of 128 (32 us of bytes) take 85, 98, 113 and 139 us at 32, 40, 56 and 72
+// heads of 128 (32 us of bytes) take 85, 98, 112 and 140 us at 32, 40, 56 and 72
 // rows; the schedulers issue in 56 and 52 % of the cycles at 40 and 72, with two
 // warps each, which wait for one another at the barrier.  A product of N <= 80
 // columns takes its issuing warp about 42 cycles, whatever N.  What was slower:
