@@ -428,3 +428,28 @@ def test_caches_that_are_none(sv):
     assert not k.any() and not v.any()
     out, lse = sv.attend_kv4(q, none, i, _i32([5]), 16, return_lse=True)
     assert not out.any() and (lse == -float("inf")).all()
+
+
+class _Filled:
+    """The package, with caches that hold `byte` wherever nothing was written."""
+
+    def __init__(self, sv, byte):
+        self.sv, self.byte = sv, byte
+
+    def __getattr__(self, name):
+        return getattr(self.sv, name)
+
+    def alloc_kv4_cache(self, *args, **kw):
+        return self.sv.alloc_kv4_cache(*args, **kw).fill_(self.byte)
+
+
+@pytest.mark.parametrize("byte", [0x7B, 0x7F, 0xFB, 0x00])     # large numbers of either sign, NaN or the largest, nothing
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("gamma, group", [(0, 4), (3, 4), (4, 8), (8, 8)])
+def test_unwritten_slots_hold_anything(sv, byte, dtype, gamma, group):
+    lengths = [3, 150, 511]
+    c = _Cache(_Filled(sv, byte), [n + gamma + 1 for n in lengths], 2, 128, 64, dtype, garbage=False)
+    q = _q(3, gamma + 1, 2 * group, 128, dtype)
+    for S in (sv, _LongTables(sv)):
+        out, lse = S.attend_kv4(q, c.cache, c.table, _i32(lengths), 64, return_lse=True)
+        _check(out, lse, q, c, lengths, dtype)
