@@ -155,10 +155,11 @@ sv_status sv_read_kv4(int R, int heads, int D, int page, int pages, const void* 
  *                16-byte aligned, any contents; one per concurrent call
  *
  * Sums and softmax statistics are float32.  A token's weight times its value's
- * scale is rounded to float16 (bf16 results) or to two float16 parts (fp16
- * results), relative to the largest scale of a value that the sequence has in
- * that head: beside the relative error, 2^-30 of the largest value for each
- * token.  Results do not depend on the order in which CTAs run.
+ * scale is rounded to float16 (bf16 results, where the rounding counts for what
+ * an element is away from the middle of its row alone) or to two float16 parts
+ * (fp16 results), relative to the largest scale of a value that the sequence
+ * has in that head: beside the relative error, 2^-30 of the largest value for
+ * each token.  Results do not depend on the order in which CTAs run.
  */
 size_t sv_attend_kv4_workspace_bytes(int gamma, int heads, int G, int D);
 

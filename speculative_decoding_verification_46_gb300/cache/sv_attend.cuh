@@ -20,6 +20,16 @@
 // eight tokens is taken as n - 15 (the sign bit and the complement, in the same
 // AND and XOR), and its offset as o' + 15 s'.
 //
+// Rounding p s' to float16 would cost a bfloat16 result |n| or |n - 15| times
+// the rounding, about 8 s' p, were its offset's term p o' formed from p as it
+// is.  So the middle of the row, o' + 7.5 s', is taken with p, and the rest with
+// the rounded weight r: r n' +- 7.5 r (-7.5 for n, 7.5 for n - 15), which leaves
+// |n - 7.5|, about 3 (errors against 64 bits, 48 sequences of 6000 tokens:
+// 0.001673 where 0.001751; rounding the exact result gives 0.001660).  A second
+// operand for the weights' rest, as float16 results have it, would take out
+// that too (0.001660), in 81 us where 67 for 20 rows and 219 where 182 for 16
+// rows of 240,000 tokens; formed from p alone they took 63 and 174.
+//
 // Tokens and channels are the products' left side and the rows their right one,
 // so that eight rows cost half of what sixteen do: scores^T [16 tokens x 8 rows]
 // = codes . q^T, sums^T [16 channels x 8 rows] += (value codes)^T . weights^T.  A
@@ -107,6 +117,13 @@ __device__ __forceinline__ uint32_t and_xor(uint32_t a, uint32_t b, uint32_t c) 
 __device__ __forceinline__ uint32_t half2_bits(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+constexpr unsigned short kHalfRange = 0x4780, kMinusHalfRange = 0xc780;      // 7.5, -7.5 in float16
+// c0 += half 0 of a * m, c1 += half 1 of a * m, in float32; m is a float16's bits
+__device__ __forceinline__ void add_product(float& c0, float& c1, uint32_t a, unsigned short m) {
+  asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tfma.rn.f32.f16 %0, x, %3, %0;\n\tfma.rn.f32.f16 %1, y, %3, %1;\n\t}"
+      : "+f"(c0), "+f"(c1) : "r"(a), "h"(m));
 }
 
 // Tokens that rows of sequence b may see, its rows, and how they are cut.
@@ -630,6 +647,11 @@ __global__ void __launch_bounds__(AttendShape<T, D, NT>::kThreads, AttendShape<T
 
       // weights and sums, 16 tokens at a time: their first eight as codes n,
       // the others as n - 15
+      [[maybe_unused]] float centre[NT][2];
+      if constexpr (!kFine) {
+#pragma unroll
+        for (int m = 0; m < NT; ++m) centre[m][0] = centre[m][1] = 0.f;
+      }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         uint32_t pb[NT][2];
@@ -637,7 +659,8 @@ __global__ void __launch_bounds__(AttendShape<T, D, NT>::kThreads, AttendShape<T
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const float scale = Kv<T>::lo(nv[i][e]), n_scale = scale * value_scale;
-          const float offset = e ? fmaf(15.f, scale, Kv<T>::hi(nv[i][e])) : Kv<T>::hi(nv[i][e]);
+          // (not kFine: the middle of the row, and the rest with the rounded weights)
+          const float offset = fmaf(kFine ? e ? 15.f : 0.f : 7.5f, scale, Kv<T>::hi(nv[i][e]));
           const Two vn = two(n_scale, n_scale), vo = two(offset, offset);
 #pragma unroll
           for (int m = 0; m < NT; ++m) {
@@ -662,6 +685,8 @@ __global__ void __launch_bounds__(AttendShape<T, D, NT>::kThreads, AttendShape<T
               // a float16 result wants more than float16 weights: their rest
               const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&x));
               pl[m][e] = transposed(half2_bits(a0 - back.x, a1 - back.y));
+            } else {
+              add_product(centre[m][0], centre[m][1], x, e ? kHalfRange : kMinusHalfRange);
             }
           }
         }
@@ -682,6 +707,11 @@ __global__ void __launch_bounds__(AttendShape<T, D, NT>::kThreads, AttendShape<T
               if constexpr (kFine) mma16816(o[m][2 * w + half], a0, a1, a2, a3, pl[m][0], pl[m][1]);
             }
           }
+      }
+      if constexpr (!kFine) {
+        const float down = 1.f / value_scale;
+#pragma unroll
+        for (int m = 0; m < NT; ++m) shift[m] = fma2(two(centre[m][0], centre[m][1]), two(down, down), shift[m]);
       }
     };
 

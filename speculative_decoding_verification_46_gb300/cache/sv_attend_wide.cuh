@@ -416,6 +416,7 @@ __global__ void __launch_bounds__(kWdThreads, 2) attend_wide_kernel(const __grid
     // registers are short, in shared memory: 141 us for 72 rows, and 149; for fewer
     // rows that takes longer, 87, 101 and 117 us where 85, 98 and 114.)
     bool none = true;
+    const unsigned short half_range = w < 2 ? kMinusHalfRange : kHalfRange;
 
     for (int n = 0; n < chunks; ++n) {
       const uint32_t stage = sm + S::oRing + slot * S::kStage;
@@ -517,6 +518,28 @@ __global__ void __launch_bounds__(kWdThreads, 2) attend_wide_kernel(const __grid
           }
           return most;
         };
+        // `by` times what weights() adds to the shifts for the middles of the
+        // values' rows (not kFine): the weights of z as operands, times -+7.5
+        auto centre = [&](float by) {
+#pragma unroll
+          for (int k = 0; k < NG; ++k) {
+            float c0 = 0.f, c1 = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int bl = j >> 1, e = j & 1;
+              const float n_x = Kv<T>::lo(nv[bl][e]) * value_scale;
+              float a0, a1;
+              split(mul2(two(ex2_approx(z[bl][k][2 * e]), ex2_approx(z[bl][k][2 * e + 1])), two(n_x, n_x)), a0, a1);
+              if (kMasked) {
+                const int2 see = sees(k, bl, e);
+                if (!see.x) a0 = 0.f;
+                if (!see.y) a1 = 0.f;
+              }
+              add_product(c0, c1, half2_bits(a0, a1), half_range);
+            }
+            shift[k] = fma2(two(c0, c1), two(by, by), shift[k]);
+          }
+        };
         // (a warp whose terms have not outgrown their references has formed its
         // part of the masses for good: a reference that moves scales it)
         auto weights = [&](bool first) {
@@ -529,13 +552,15 @@ __global__ void __launch_bounds__(kWdThreads, 2) attend_wide_kernel(const __grid
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const float x = Kv<T>::lo(nv[bl][e]), n_x = x * value_scale;
-              const float o_x = fmaf(w < 2 ? 0.f : 15.f, x, Kv<T>::hi(nv[bl][e]));
+              const float o_x = fmaf(S::kFine ? w < 2 ? 0.f : 15.f : 7.5f, x, Kv<T>::hi(nv[bl][e]));
               vn[bl][e] = two(n_x, n_x);
               vo[bl][e] = two(o_x, o_x);
             }
+          const float down = 1.f / value_scale;
 #pragma unroll
           for (int k = 0; k < NG; ++k) {
             uint32_t a[4], rest[4];
+            float c0 = 0.f, c1 = 0.f;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const int bl = j >> 1, e = j & 1;
@@ -564,8 +589,11 @@ __global__ void __launch_bounds__(kWdThreads, 2) attend_wide_kernel(const __grid
                 // a float16 result wants more than float16 weights: their rest
                 const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&a[j]));
                 rest[j] = half2_bits(a0 - back.x, a1 - back.y);
+              } else {
+                add_product(c0, c1, a[j], half_range);
               }
             }
+            if (!S::kFine) shift[k] = fma2(two(c0, c1), two(down, down), shift[k]);
             store_transposed(to + k * 1024, a[0], a[1], a[2], a[3]);
             if (S::kFine) store_transposed(to + S::kP + k * 1024, rest[0], rest[1], rest[2], rest[3]);
           }
@@ -596,7 +624,10 @@ __global__ void __launch_bounds__(kWdThreads, 2) attend_wide_kernel(const __grid
           // 0): a row that sees none of it sees none of the later ones, its mass
           // stays 0.
           if (S::kTight && unsettled && subs != 0 && tid == 0) *settled = 1;
-          if (!S::kTight) exponents();
+          if (!S::kTight) {
+            exponents();
+            if (!S::kFine && !outgrown) centre(-1.f / value_scale);   // (they come with the weights formed again)
+          }
 #pragma unroll
           for (int k = 0; k < NG; ++k) {
             float t0 = fmaxf(fmaxf(z[0][k][0], z[0][k][2]), fmaxf(z[1][k][0], z[1][k][2]));
