@@ -134,9 +134,9 @@ sv_status sv_read_kv4(int R, int heads, int D, int page, int pages, const void* 
  *                key/value head h
  *   gamma        at most SV_MAX_GAMMA
  *   q            [B][gamma+1][heads * G][D] through q_strides (batch, row,
- *                head), as k's in sv_append_kv4.  A row with an element beyond
- *                2^100, an infinity or a NaN may give NaN; the rows beside it
- *                are not touched by it
+ *                head), as k's in sv_append_kv4.  A row with an element that
+ *                is beyond 2^100 or is so times scale, an infinity or a NaN may
+ *                give NaN; the rows beside it are not touched by it
  *   block_table  [B][N] int32: an entry outside [0, pages) hides its tokens,
  *                as does a position at N * page and behind
  *   lengths      [B] int32: tokens cached before the round (negative: 0)

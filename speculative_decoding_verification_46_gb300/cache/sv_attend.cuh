@@ -319,8 +319,14 @@ __device__ __forceinline__ float4 cluster_load4(uint32_t at) {
 }
 
 // The power of two (its exponent) that brings a row's largest element to
-// [2^13, 2^14).
-__device__ __forceinline__ int raised_by(float top) { return top > 0.f ? min(140 - (int)(__float_as_uint(top) >> 23), 126) : 0; }
+// [2^13, 2^14), or as near as 2^126 does: a row of zeros, whose scores any scale
+// leaves at 0, then has a small one.
+__device__ __forceinline__ int raised_by(float top) { return top > 0.f ? min(140 - (int)(__float_as_uint(top) >> 23), 126) : 126; }
+// x 2^e, |e| <= 252, in two steps: neither leaves float32's range where the result does not.
+__device__ __forceinline__ float times_power(float x, int e) {
+  const int a = e >> 1, b = e - a;
+  return x * __uint_as_float((uint32_t)(a + 127) << 23) * __uint_as_float((uint32_t)(b + 127) << 23);
+}
 
 // NT: groups of eight rows
 template <typename T, int D, int NT>
@@ -495,7 +501,7 @@ __global__ void __launch_bounds__(AttendShape<T, D, NT>::kThreads, AttendShape<T
         if (word == 0) {
           const int r = rt * TR + rl, i = r / p.G;
           q_sums[rl] = sum * raise * 0x1p-24f;   // (the products' unit is 2^-24 of a code)
-          row_scales[rl] = p.scale * 0x1p24f * __uint_as_float((uint32_t)(127 - up) << 23);
+          row_scales[rl] = times_power(p.scale, 24 - up);
           limits[rl] = i < s.rows ? min(s.first - 1 + i, s.seen - 1) : -1;
           out_rows[rl] = i < s.rows ? ((long long)b * p.rows + i) * p.H * p.G + (long long)h * p.G + (r - i * p.G) : -1;
         }

@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(kWdThreads, 2) attend_wide_kernel(const __grid
           float* pair = reinterpret_cast<float*>(pairs + (rl >> 1)) + (rl & 1);
           pair[0] = sum * raise * 0x1p-24f;      // (the products' unit is 2^-24 of a code)
           pair[2] = 0.f;
-          row_scales[rl] = p.scale * 0x1p24f * __uint_as_float((uint32_t)(127 - up) << 23);
+          row_scales[rl] = times_power(p.scale, 24 - up);
           limits[rl] = i < s.rows ? min(s.first - 1 + i, s.seen - 1) : -1;
           out_rows[rl] = i < s.rows ? ((long long)b * p.rows + i) * p.H * p.G + (long long)h * p.G + (r - i * p.G) : -1;
         }

@@ -1,0 +1,35 @@
+"""Softmax scales and queries at the ends of their ranges (attend_kv4), against
+the float64 restatement with the tolerances of test_gpu_cache.py."""
+
+import numpy as np
+import pytest
+import torch
+
+from test_gpu_cache import DEV, _Cache, _check, _i32, _q, sv  # noqa: F401
+from test_gpu_cache_edges import _LongTables
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("far", [False, True])
+@pytest.mark.parametrize("group", [4, 20, 40])
+@pytest.mark.parametrize("power", [104, 108, 126])
+def test_large_scales_of_small_queries(sv, power, group, far):
+    """Scores of ordinary size from queries of 2^-126 to 2^-98 and scales to match, beside rows of zeros."""
+    lengths = [70, 20]
+    c = _Cache(sv, [n + 1 for n in lengths], 2, 128, 16, "bf16")
+    q = _q(2, 1, 2 * group, 128, "bf16", size=1.0) * 2.0 ** -(power + 2)
+    q = torch.where(q.abs() < 2.0 ** -126, 2.0 ** -126, q)        # (no subnormal ones)
+    q[:, :, 1::4] = 0.0
+    out, lse = (_LongTables(sv) if far else sv).attend_kv4(q, c.cache, c.table, _i32(lengths), 16, scale=2.0 ** power, return_lse=True)
+    _check(out, lse, q, c, lengths, "bf16", scale=2.0 ** power)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("group", [2, 40])
+def test_rows_of_zeros_at_any_scale(sv, dtype, group):
+    c = _Cache(sv, [50], 1, 64, 16, dtype)
+    q = torch.zeros_like(_q(1, 1, group, 64, dtype))
+    for scale in (2.0 ** -149, 2.0 ** -126, 1.0, 2.0 ** 100, 2.0 ** 127):
+        out, lse = sv.attend_kv4(q, c.cache, c.table, _i32([49]), 16, scale=scale, return_lse=True)
+        _check(out, lse, q, c, [49], dtype, scale=scale)
