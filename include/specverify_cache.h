@@ -41,6 +41,8 @@
  *            2^-126
  * A row with a NaN or an infinity, or whose scale is not finite, is held as
  * NaN: scale and offset NaN, codes 0.
+ * The bytes do not say which type they are of: a cache is read and attended with
+ * the type that was appended.
  */
 #ifndef SPECVERIFY_CACHE_H
 #define SPECVERIFY_CACHE_H
@@ -93,6 +95,11 @@ extern "C" {
  * reverse order, so that a round that is taken back leaves the free list as it
  * was.  A count outside its array is clamped to it; a page id outside
  * [0, 2^30 / page) gives slot -1.  Giving never writes behind `pool`.
+ *
+ * A sequence with a status has moved to lengths[b] all the same, but nothing of
+ * this round is stored for it, and what its last page holds behind lengths[b] are
+ * rejected drafts: give sv_attend_kv4 gamma_b = -1 for it, and the next
+ * sv_plan_round kept = 0 (as for every sequence without rows in a round).
  *
  * SV_ERR_INVALID_ARG for bad sizes (B * N and pool * page above
  * SV_MAX_CACHE_SLOTS among them) and NULL arrays.

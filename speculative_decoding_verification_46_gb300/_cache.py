@@ -164,8 +164,9 @@ def plan_round(lengths, gamma, page, block_table, blocks, free_blocks, free_coun
     drafts, or gamma_b [B] int32 of them (-1: the sequence takes no part).  All
     contiguous CUDA tensors on one device.  Returns (slots [B, gamma+1] int32,
     -1 behind a sequence's last row; positions [B, gamma+1] int32; status [B]
-    int32, SV_PLAN_ bits: such a sequence got no pages and no slots).  stream:
-    as in adjust_logits.
+    int32, SV_PLAN_ bits: such a sequence got no pages and no slots, but its
+    length has moved; give attend_kv4 gamma_b = -1 for it, and the next call
+    kept = 0).  stream: as in adjust_logits.
     """
     dev = lengths.device
     B = lengths.shape[0] if lengths.dim() == 1 else -1
