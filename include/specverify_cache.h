@@ -161,7 +161,8 @@ sv_status sv_read_kv4(int R, int heads, int D, int page, int pages, const void* 
  *                (0 for sizes that are not supported) on the current device,
  *                16-byte aligned, any contents; one per concurrent call
  *
- * Sums and softmax statistics are float32.  A token's weight times its value's
+ * Sums and softmax statistics are float32, of weights up to 2^8: held values
+ * beyond 2^100 may give infinities or NaN.  A token's weight times its value's
  * scale is rounded to float16 (bf16 results, where the rounding counts for what
  * an element is away from the middle of its row alone) or to two float16 parts
  * (fp16 results), relative to the largest scale of a value that the sequence

@@ -64,3 +64,22 @@ def test_queries_are_exact_over_2_to_26(sv, D, group, far):
     small = rows.clone()
     small[..., top] = 0.0                                          # (the same scores; their size is the small ones')
     _check(out, lse, small, c, [n], "bf16", scale=scale)
+
+
+@pytest.mark.parametrize("far", [False, True])
+@pytest.mark.parametrize("group", [4, 20, 40, 64])
+@pytest.mark.parametrize("keys, values", [(0, 100), (0, -100), (60, 98), (-60, -98)])
+def test_large_and_small_keys_and_values(sv, keys, values, group, far):
+    """Held values up to 2^100, with keys whose size the queries make up for."""
+    n, page = 500, 16
+    c = _Cache(sv, [n + 1], 1, 128, page, "bf16")
+    p = np.arange(n + 1)
+    slots = _i32((c.table[0].cpu().numpy()[p // page] * page + p % page)[None])
+    x, v = (torch.as_tensor(a).to(torch.bfloat16).to(DEV)[None] for a in (c.k[0], c.v[0]))
+    x, v = x * 2.0 ** keys, v / v.abs().max() * 2.0 ** values
+    sv.append_kv4(x, v, slots, c.cache)
+    c.k[0], c.v[0] = (cacheref.held(a[0].double().cpu().numpy(), "bf16") for a in (x, v))
+    q = _q(1, 1, group, 128, "bf16", size=0.5) * 2.0 ** -keys
+    out, lse = (_LongTables(sv) if far else sv).attend_kv4(q, c.cache, c.table, _i32([n]), page, return_lse=True)
+    c.v[0] *= 2.0 ** -values
+    _check(out.double() * 2.0 ** -values, lse, q, c, [n], "bf16")
