@@ -145,7 +145,11 @@ sv_status sv_read_kv4(int R, int heads, int D, int page, int pages, const void* 
  *                is beyond 2^100 or is so times scale, an infinity or a NaN may
  *                give NaN; the rows beside it are not touched by it
  *   block_table  [B][N] int32: an entry outside [0, pages) hides its tokens,
- *                as does a position at N * page and behind
+ *                as does a position at N * page and behind.  N * page bounds
+ *                the sequences' lengths: few sequences take one launch instead
+ *                of two, and about half of the time, where it is at most 16640,
+ *                so a table of no more columns than its longest sequence has
+ *                pages serves short sequences best
  *   lengths      [B] int32: tokens cached before the round (negative: 0)
  *   gamma_b      [B] int32 or NULL (gamma): rows i <= gamma_b[b] take part;
  *                -1: none

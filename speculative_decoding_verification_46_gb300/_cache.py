@@ -289,7 +289,9 @@ def attend_kv4(q, cache, block_table, lengths, page, *, gamma_b=None, scale=None
     groups of neighbours.  Row i of sequence b sees the positions 0 ..
     lengths[b] + i through block_table [B, N] int32: lengths [B] int32 counts
     the tokens before the round, whose own tokens have been appended; table
-    entries that are no page hide their tokens.  gamma_b [B] int32: a ragged
+    entries that are no page hide their tokens.  (Few short sequences are
+    served faster where the table has no more columns than they have pages: up
+    to 16640 positions are one launch.)  gamma_b [B] int32: a ragged
     round, rows behind a sequence's last are not computed (-1: none is).
     scale: 1 / sqrt(D) by default.  Returns out [B, gamma+1, query heads, D],
     with return_lse also the logarithm of each row's sum [B, gamma+1, query

@@ -34,16 +34,16 @@
 // so that eight rows cost half of what sixteen do: scores^T [16 tokens x 8 rows]
 // = codes . q^T, sums^T [16 channels x 8 rows] += (value codes)^T . weights^T.  A
 // lane then has two tokens of every 16 and two rows of every eight: it reads two
-// tokens' numbers and no others.  With the rows on the left (a lane has a row,
-// and numbers of four tokens) 8 rows took 60 us where they now take 50, 24 rows
-// 88 where 79, 128 sequences of 4096 tokens 116 where 87.
+// tokens' numbers and no others.  (When it was turned round: with the rows on the
+// left, a lane has a row and numbers of four tokens, 8 rows took 60 us and 50 this
+// way, 24 rows 88 and 79, 128 sequences of 4096 tokens 116 and 87.)
 //
 // Two ways to share the work out.  attend_joined (sv_attend_plan.h) chooses.
 // Few segments, which are (sequence, head, row tile)s, over a short table: a
 // cluster of eight CTAs a segment deals its 32-token groups out to its warps, and
 // the CTAs read each other's sums from shared memory.  One launch: one request of
-// 700 tokens, 8 x 4 heads of 128, takes 4.5 us, and 9.0 us the other way; a round of
-// gamma 8 on 8 x 8 heads and up to 4096 tokens 14 us, and 25.5 in the kernel for
+// 700 tokens, 8 heads of 128, takes 4.8 us, and 8.7 us the other way; a round of
+// gamma 8 on 8 x 8 heads and up to 4096 tokens 13 us, and 25 in the kernel for
 // many rows.
 // Otherwise: the segments' tokens in units of 128 are one line of units; CTA i of
 // W takes an equal part of it, finds its place from lengths and walks on.  A
@@ -53,14 +53,16 @@
 // sums of their own, and are joined at the end of the segment, in order.
 //
 // What bounds it.  Few rows over long sequences: the cache's bytes (128 sequences
-// of 4096 tokens, 8 heads of 128, bf16: 83 us, 5.2 TB/s; 4 of 240,000: 173 us,
-// 4.5 TB/s at 16 rows).  More rows: instructions.  A group of 32 tokens costs a
+// of 4096 tokens, 8 heads of 128, bf16: 84 us, 5.1 TB/s; 4 of 240,000: 182 us,
+// 4.3 TB/s at 16 rows).  More rows: instructions.  A group of 32 tokens costs a
 // warp about as much for masks, numbers, exponentials and the operands'
-// exchange as for its products: 32 sequences of up to 8192 tokens take 45, 58 and
-// 74 us at 8, 16 and 24 rows (32 us of bytes); at 16 rows the schedulers issue in
-// half of the cycles and the tensor pipe is busy in 40 %.  16 tokens at a time with
-// another CTA an SM was slower (206 us where 181), so were rings of three groups
-// (49 us where 47 at 8 rows).
+// exchange as for its products: 32 sequences of up to 8192 tokens take 46, 60 and
+// 78 us at 8, 16 and 24 rows (32 us of bytes); at 16 rows the schedulers issue in
+// half of the cycles and the tensor pipe is busy in 39 %, with 12 warps an SM and
+// some registers spilled (52 bytes a thread).  float16 results, which form each
+// value product twice, take 48, 70 and 93 us: the tensor pipe is busy in half of
+// the cycles at 16 rows.  When they were tried, 16 tokens at a time with another
+// CTA an SM took 206 us where 181, rings of three groups 49 us where 47 at 8 rows.
 #pragma once
 
 #include <float.h>

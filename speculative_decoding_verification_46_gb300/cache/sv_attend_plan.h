@@ -14,9 +14,9 @@ inline size_t align_up(size_t x) { return (x + 255) & ~size_t(255); }
 
 // Rows of a tile where the call is not joined in one launch: up to 24 go to attend_kernel; more to attend_wide_kernel, in
 // as few tiles as its 80 rows allow, of equal size.  At 32 sequences of up to
-// 8192 tokens, 8 heads of 128, attend_kernel takes 74 us for 24 rows, and took
-// 100 for 32; attend_wide_kernel takes 85
-// us for 32, and for fewer, which it pads, no less.
+// 8192 tokens, 8 heads of 128, attend_kernel takes 78 us for 24 rows, and took
+// 100 for 32; attend_wide_kernel takes 88 us for 32, and for fewer, which it pads,
+// no less.
 inline int attend_tile_rows(int rows) {
   if (rows <= 24) return (std::max(rows, 1) + 7) / 8 * 8;
   const int tiles = (rows + kWdMostRows - 1) / kWdMostRows;
@@ -29,17 +29,19 @@ inline int attend_ctas(int TR) { return sm_count() * (TR == 8 ? 4 : TR == 16 ? 3
 // is short enough for eight, and all clusters are on the GPU at once (with 3 or 2
 // CTAs an SM some SMs' places do not make up a cluster: 57 segments of 16 rows
 // would take two turns).  Rows beyond 24 read the cache once a tile, from L2 for
-// the most part.  us with the workspace -> joined, 8 heads of 128 (2 in the last
-// line), tables and up to all of their tokens:
-//   sequences, rows   1024          8192          12200         16384
-//        1,   1        8.8 ->  5.2  20.8 ->  9.8  24.5 -> 11.4  24.9 -> 14.4
-//        9,   1       11.7 ->  6.9  20.7 -> 15.8  26.7 -> 22.1  29.9 -> 24.7
-//        6,  16       13.0 ->  8.9  20.9 -> 17.3  26.5 -> 24.7  29.9 -> 28.6
-//        7,  16       13.5 -> 12.9  21.3 -> 21.7                31.1 -> 34.7
-//        3,  24       13.2 ->  9.3  19.4 -> 17.6  23.8 -> 22.4  25.4 -> 26.9
-//        2,  40       14.8 ->  9.4  24.5 -> 18.5  27.3 -> 23.1  30.2 -> 29.3
-//        1,  72       17.1 ->  9.8  29.8 -> 19.3  32.6 -> 24.0  35.5 -> 30.0
-//        1, 256       15.0 ->  9.6  27.5 -> 19.2  29.9 -> 23.8  32.0 -> 30.1
+// the most part.  us with the workspace -> joined, heads of 128, sequences of half
+// to all of the tokens above them (all of them for a single one), tables as wide:
+//   segments, rows            700          4096          8192         12200         16384
+//   8 (8 heads),  1    8.7 ->  4.8  13.1 ->  7.1  20.0 ->  9.8  23.6 -> 12.5  23.8 -> 15.2
+//  72 (8 heads),  1   10.6 ->  6.7  15.9 -> 11.2  20.7 -> 16.0  25.8 -> 20.9  29.7 -> 24.7
+//  48 (8 heads), 16   11.9 ->  8.4  17.1 -> 13.2  21.5 -> 18.8  25.0 -> 24.1  31.9 -> 31.8
+//  24 (8 heads), 24   12.7 ->  8.8  17.0 -> 13.2  20.4 -> 17.3  22.0 -> 21.6  28.1 -> 28.2
+//  33 (11 heads), 24  13.0 ->  9.0  17.8 -> 13.3  21.6 -> 17.4  26.0 -> 21.7  31.8 -> 28.3
+//  32 (8 heads), 40   13.5 ->  8.8  22.9 -> 12.7  26.0 -> 18.4  27.8 -> 23.9  31.7 -> 29.3
+//  24 (8 heads), 72   17.1 ->  8.9  25.0 -> 13.2  30.9 -> 18.8  34.2 -> 24.3  36.7 -> 29.8
+//  33 (3 heads), 256  15.6 ->  9.1  25.7 -> 13.3  27.9 -> 19.0  30.6 -> 24.5  34.4 -> 29.8
+// The lengths are on the device; a table that is wider than its sequences need is
+// taken for what it could hold.
 struct AttendJoined {
   int rows, segments;                     // of a tile; 0 segments: not joined
 };

@@ -26,14 +26,20 @@
 // Tensor memory, 256 columns a CTA: key codes, value codes, scores, sums.  With
 // R = 80 and D = 128 the value codes take the place of the scores: then (1)
 // follows (2)'s reading of them, at a barrier more, where the references are
-// settled before the weights.  (For fewer rows settling first takes longer: 99,
-// 112 and 123 us where 87, 100 and 114 at 32, 40 and 56 rows.)
+// settled before the weights, and the next scores wait for this step's sums:
+// scores, barrier, value codes and weights, barrier, sums follow one another.  (For
+// fewer rows settling first took longer: 99, 112 and 123 us where 87, 100 and 114 at
+// 32, 40 and 56 rows.)
 //
 // What bounds it: instructions, not bytes.  32 sequences of up to 8192 tokens, 8
-// heads of 128 (32 us of bytes) take 85, 98, 112 and 140 us at 32, 40, 56 and 72
-// rows; the schedulers issue in 56 and 52 % of the cycles at 40 and 72, with two
-// warps each, which wait for one another at the barrier.  A product of N <= 80
-// columns takes its issuing warp about 42 cycles, whatever N.  What was slower:
+// heads of 128 (32 us of bytes) take 88, 103, 121 and 145 us at 32, 40, 56 and 72
+// rows (float16 results, with each value product and each store of weights twice:
+// 93, 110, 129 and 169); the schedulers issue in 58 and 52 % of the cycles at 40
+// and 72, with two CTAs of eight warps an SM, which wait for one another at the
+// barrier, and no pipe is busy in more than 44 %.  Their 128 registers a thread do
+// not hold 56 rows and more (72 to 200 bytes a thread are spilled).  A product of
+// N <= 80 columns takes its issuing warp about 42 cycles, whatever N.  What was
+// slower when it was tried:
 // copies in bulk (a warp's lanes issue one in 75 cycles: 138 us where 116 at 32
 // rows), a ninth warp for the products (96 registers a thread: 255 us where 222
 // at 72 rows), a fourth step in the ring (97.5 us where 96.2 at 40 rows).
